@@ -12,7 +12,9 @@
  *                           decode row (one kernel for small launches);
  *   lnk_paged_step_attn     packed prompt chunks plus decode rows in one call
  *                           ("step_paged"; with no decode rows it is
- *                           "prefill_paged").
+ *                           "prefill_paged");
+ *   lnk_paged_read_tokens   the stored k/v of given tokens, as bf16 (the
+ *                           append's inverse).
  *
  * Sources: the model pages "Mistral 7B Instruct v0.3", "Qwen3-4B" and
  * "Llama 3.1 8B Instruct", Entries table (prefill_paged, decode_paged,
@@ -88,9 +90,12 @@ typedef struct lnk_attn_desc {
                              iff p - window < j <= p (itself and window - 1 before) */
   float scale;            /* softmax scale; 0 selects 1 / sqrt(head_dim) */
   int32_t kv_dtype;       /* element type of k_pool / v_pool: LNK_KV_BF16 (0, the
-                             pages' pools) or LNK_KV_E4M3 (8-bit pools, below) */
-  float k_scale;          /* LNK_KV_E4M3: a K code c stands for e4m3(c) * k_scale (> 0, finite) */
-  float v_scale;          /* LNK_KV_E4M3: a V code c stands for e4m3(c) * v_scale (> 0, finite) */
+                             pages' pools), LNK_KV_E4M3 (8-bit pools, below) or
+                             LNK_KV_E2M1 (4-bit pools, below) */
+  float k_scale;          /* LNK_KV_E4M3: a K code c stands for e4m3(c) * k_scale (> 0, finite);
+                             LNK_KV_E2M1: for e2m1(c) * its block's scale * k_scale */
+  float v_scale;          /* LNK_KV_E4M3: a V code c stands for e4m3(c) * v_scale (> 0, finite);
+                             LNK_KV_E2M1: for e2m1(c) * its block's scale * v_scale */
 } lnk_attn_desc;
 
 /* Pool element types (lnk_attn_desc.kv_dtype).
@@ -111,9 +116,34 @@ typedef struct lnk_attn_desc {
  *   rotated queries to f16 (exactly, for magnitudes in [2^-14, 65504]): a
  *   query element above 65504 in magnitude becomes infinite there, and one
  *   below 2^-14 loses precision or becomes zero, so the queries must stay
- *   within that range (unit-scale projections do by far). */
+ *   within that range (unit-scale projections do by far).
+ *
+ * LNK_KV_E2M1: 4-bit pools (not on the pages; 4.5 bits an element, 28% of a
+ *   bf16 pool).  Elements are OCP E2M1 codes (1 sign bit, 2 exponent bits with
+ *   bias 1, 1 mantissa bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives)
+ *   with one E4M3 scale code for each block of 16 consecutive dimensions of a
+ *   head's row.  A page of one kv head is 36 * D contiguous bytes: 64 rows of
+ *   D / 2 code bytes (row j = position j of the page; byte i holds dimension
+ *   2i in its low four bits and 2i + 1 in its high four bits), then 4 * D
+ *   bytes of scale codes, the scale of block b (dimensions 16b .. 16b + 15) of
+ *   position j at byte ((j % 4) * (D / 16) + b) * 16 + j / 4.  The pools are
+ *   [Hkv][num_pages][36 * D] bytes (lnk_paged_page_bytes), 16-byte aligned,
+ *   and the lnk_bf16* pool arguments of every entry point point to them.
+ *     The append stores, for a block of the bf16 values x that a bf16 pool
+ *   would hold and with every operation one IEEE float32 operation,
+ *     s = E4M3(max|x| / (6 * pool scale)),  d = e4m3(s) * pool scale,
+ *     code = E2M1(x / d),
+ *   E4M3 and E2M1 rounding to nearest even and saturating (448 and 6).  A
+ *   block whose d is zero stores zeros (s = 0); a block that holds a NaN gets
+ *   the NaN scale 0x7F, which makes its 16 values NaN.  (s may round down, so
+ *   that the block's largest element saturates: it is then off by at most
+ *   1/17 of its size.)
+ *     Attention uses the values e2m1(code) * e4m3(s) * pool scale; products of
+ *   a code and a scale are exact in f16 and bf16.  The append and
+ *   lnk_paged_read_tokens are supported; attention returns LNK_EUNSUPPORTED. */
 #define LNK_KV_BF16 0
 #define LNK_KV_E4M3 1
+#define LNK_KV_E2M1 4
 
 /* Rotary frequencies: inv_freq[i] = exp(-(f32(i) * 2 / f32(D)) * log(theta))
  * in float32 ("Phi-3 Mini 4K Instruct -- files", src/rope.linnet, tables),
@@ -137,6 +167,12 @@ const char* lnk_status_string(lnk_status status);
  * out[0 .. head_dim/2).  Same definition as lnk_rope_desc's comment; log and
  * exp are taken correctly rounded, the llama3 rescale in double rounded once. */
 lnk_status lnk_rope_inv_freq(const lnk_rope_desc* rope, int32_t head_dim, float* out);
+
+/* Host-only: bytes of one page of one kv head in one pool (128 * D for bf16,
+ * 64 * D for LNK_KV_E4M3, 36 * D for LNK_KV_E2M1).  A pool is num_kv_heads *
+ * num_pages of them, and page p of head h starts at (h * num_pages + p) times
+ * this.  Returns 0 on bad arguments. */
+size_t lnk_paged_page_bytes(const lnk_attn_desc* desc);
 
 /* Bytes of device workspace that decode_attn / step_attn need for up to
  * max_rows decode rows on the current device.  Returns 0 on bad arguments.
@@ -165,7 +201,8 @@ size_t lnk_paged_workspace_size(const lnk_attn_desc* desc, int32_t max_rows);
  *   q_norm_w, k_norm_w  device [D] QK-norm weights, or NULL for no QK-norm
  *   norm_eps QK-norm epsilon (1e-6 for Qwen3)
  *   k_pool, v_pool  device pools (written at the tokens' slots only; 8-bit
- *            codes for LNK_KV_E4M3, see lnk_attn_desc.kv_dtype)
+ *            codes for LNK_KV_E4M3, 4-bit codes and their scales for
+ *            LNK_KV_E2M1, see lnk_attn_desc.kv_dtype)
  *   q_out    device [T][Hq][D]   rotated queries (zero for inactive tokens)
  *   T        tokens (0 is allowed and enqueues nothing)
  *
@@ -193,6 +230,36 @@ lnk_status lnk_paged_append_rope(const lnk_attn_desc* desc, const lnk_rope_desc*
                                  lnk_stream stream);
 
 /*
+ * lnk_paged_read_tokens -- the stored keys and values of T tokens, as bf16.
+ *
+ * The inverse of the append, for every pool type (the pages have no
+ * counterpart): moving rows from one pool type to another, checking what a
+ * pool holds, or running a computation of one's own on cached tokens.
+ *
+ *   k_pool, v_pool  device pools
+ *   positions, rows, slots, table  name the tokens as in lnk_paged_append_rope:
+ *            token t is position positions[t] of table row rows[t] (NULL: row
+ *            t), or pool slot slots[t] when slots != NULL; a token may occur
+ *            more than once
+ *   k_out, v_out  device [T][Hkv][D] bf16, 16-byte aligned: the pool's bits for
+ *            LNK_KV_BF16, the float32 product e4m3(c) * scale, or (e2m1(c) *
+ *            e4m3(s)) * scale, rounded to bf16 (nearest even) otherwise.
+ *            Either may be NULL: that pool is not read then (and may be NULL
+ *            itself).
+ *   T        tokens (0 is allowed and enqueues nothing)
+ *
+ * Inactive tokens (negative position) and tokens whose slot cannot be found
+ * (LNK_DEV_BAD_* in *dev_status) give zeros.  The kernel is launched as a
+ * programmatic dependent launch and reads `positions`, `rows`, `slots` and
+ * `table` (and only those) before it waits for the kernel before it on the
+ * stream, as the append does.
+ */
+lnk_status lnk_paged_read_tokens(const lnk_attn_desc* desc, const lnk_bf16* k_pool, const lnk_bf16* v_pool,
+                                 const int32_t* positions, const int32_t* rows, const int32_t* slots,
+                                 const int32_t* table, lnk_bf16* k_out, lnk_bf16* v_out, int32_t T,
+                                 int32_t* dev_status, lnk_stream stream);
+
+/*
  * lnk_paged_decode_attn -- one query token per decode row over its pages.
  *
  * Defines: "Mistral 7B Instruct v0.3" Entries table, decode_paged ("decode_rows
@@ -204,7 +271,7 @@ lnk_status lnk_paged_append_rope(const lnk_attn_desc* desc, const lnk_rope_desc*
  *   q_roped  device [B][Hq][D]  rotated queries (q_out of append_rope), 16-byte aligned
  *   positions device int32 [B]  position of row b's token (< 0: inactive row)
  *   table    device int32 [num_rows][pages_per_row]; decode row b uses table row b
- *   k_pool, v_pool device pools (bf16, or 8-bit codes for LNK_KV_E4M3)
+ *   k_pool, v_pool device pools (bf16, 8-bit or 4-bit: lnk_attn_desc.kv_dtype)
  *   out      device [B][Hq][D]  attention output (bf16, nearest even), 8-byte aligned
  *   B        decode rows, 0 <= B <= min(num_rows, 4096)
  *   workspace device scratch of ws_bytes >= lnk_paged_workspace_size(desc, B)

@@ -8,6 +8,7 @@ from .binding import (  # noqa: F401
     DEV_TIMEOUT,
     EXPORTED,
     KV_BF16,
+    KV_E2M1,
     KV_E4M3,
     LIBRARY_PATH,
     AttnDesc,
@@ -21,6 +22,8 @@ from .binding import (  # noqa: F401
     lnk_paged_decode_step,
     lnk_paged_decode_step_launches,
     lnk_paged_decode_attn_static,
+    lnk_paged_page_bytes,
+    lnk_paged_read_tokens,
     lnk_paged_step_attn,
     lnk_paged_workspace_size,
     lnk_rope_inv_freq,

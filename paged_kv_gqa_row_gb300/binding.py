@@ -33,6 +33,7 @@ EXPORTED = ["lnk_status_string", "lnk_rope_inv_freq", "lnk_paged_workspace_size"
             "lnk_paged_decode_attn_static", "lnk_pager_create", "lnk_pager_destroy", "lnk_pager_reserve",
             "lnk_pager_fork", "lnk_pager_prepare_append", "lnk_pager_release", "lnk_pager_table",
             "lnk_pager_free_pages", "lnk_pager_refcount", "lnk_paged_copy_pages",
+            "lnk_paged_page_bytes", "lnk_paged_read_tokens",
             "lnk_selftest_wait_timeout"]
 
 
@@ -43,7 +44,7 @@ class LnkError(RuntimeError):
         super().__init__(f"{where}: {msg}")
 
 
-KV_BF16, KV_E4M3 = 0, 1
+KV_BF16, KV_E4M3, KV_E2M1 = 0, 1, 4
 
 
 class AttnDesc(ctypes.Structure):
@@ -65,6 +66,11 @@ _lib.lnk_rope_inv_freq.restype = ctypes.c_int
 _lib.lnk_rope_inv_freq.argtypes = [ctypes.POINTER(RopeDesc), c_i32, ctypes.POINTER(c_f32)]
 _lib.lnk_paged_workspace_size.restype = c_size
 _lib.lnk_paged_workspace_size.argtypes = [ctypes.POINTER(AttnDesc), c_i32]
+_lib.lnk_paged_page_bytes.restype = c_size
+_lib.lnk_paged_page_bytes.argtypes = [ctypes.POINTER(AttnDesc)]
+_lib.lnk_paged_read_tokens.restype = ctypes.c_int
+_lib.lnk_paged_read_tokens.argtypes = [ctypes.POINTER(AttnDesc), c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp,
+                                       c_i32, c_vp, c_vp]
 _lib.lnk_paged_append_rope.restype = ctypes.c_int
 _lib.lnk_paged_append_rope.argtypes = [ctypes.POINTER(AttnDesc), ctypes.POINTER(RopeDesc),
                                        c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_f32,
@@ -159,6 +165,11 @@ def lnk_paged_workspace_size(desc: AttnDesc, max_rows: int) -> int:
     return int(_lib.lnk_paged_workspace_size(ctypes.byref(desc), max_rows))
 
 
+def lnk_paged_page_bytes(desc: AttnDesc) -> int:
+    """Bytes of one page of one kv head in one pool (0 for a bad descriptor)."""
+    return int(_lib.lnk_paged_page_bytes(ctypes.byref(desc)))
+
+
 def lnk_paged_append_rope(desc, rope, q, k, v, positions, rows, slots, table, q_norm_w, k_norm_w,
                           norm_eps, k_pool, v_pool, q_out, T, dev_status=None, stream=None):
     st = _lib.lnk_paged_append_rope(ctypes.byref(desc), ctypes.byref(rope), _ptr(q), _ptr(k), _ptr(v),
@@ -166,6 +177,15 @@ def lnk_paged_append_rope(desc, rope, q, k, v, positions, rows, slots, table, q_
                                     _ptr(q_norm_w), _ptr(k_norm_w), norm_eps, _ptr(k_pool),
                                     _ptr(v_pool), _ptr(q_out), T, _ptr(dev_status), _stream(stream))
     _check(st, "lnk_paged_append_rope")
+
+
+def lnk_paged_read_tokens(desc, k_pool, v_pool, positions, rows, slots, table, k_out, v_out, T,
+                          dev_status=None, stream=None):
+    """The stored keys and values of T tokens as bf16 [T, Hkv, D] (either output may be None)."""
+    st = _lib.lnk_paged_read_tokens(ctypes.byref(desc), _ptr(k_pool), _ptr(v_pool), _ptr(positions), _ptr(rows),
+                                    _ptr(slots), _ptr(table), _ptr(k_out), _ptr(v_out), T, _ptr(dev_status),
+                                    _stream(stream))
+    _check(st, "lnk_paged_read_tokens")
 
 
 def lnk_paged_decode_attn(desc, q_roped, positions, table, k_pool, v_pool, out, B, workspace,

@@ -98,8 +98,8 @@ lnk_status check_desc(const lnk_attn_desc* d) {
   if (g != 1 && g != 2 && g != 4 && g != 8) return LNK_EUNSUPPORTED;
   if (d->num_pages <= 0 || d->num_rows <= 0 || d->pages_per_row <= 0) return LNK_EINVAL;
   if (d->window < 0 || !(d->scale >= 0.f)) return LNK_EINVAL;
-  if (d->kv_dtype != LNK_KV_BF16 && d->kv_dtype != LNK_KV_E4M3) return LNK_EUNSUPPORTED;
-  if (d->kv_dtype == LNK_KV_E4M3 && !(d->k_scale > 0.f && d->k_scale <= FLT_MAX && d->v_scale > 0.f &&
+  if (d->kv_dtype != LNK_KV_BF16 && d->kv_dtype != LNK_KV_E4M3 && d->kv_dtype != LNK_KV_E2M1) return LNK_EUNSUPPORTED;
+  if (d->kv_dtype != LNK_KV_BF16 && !(d->k_scale > 0.f && d->k_scale <= FLT_MAX && d->v_scale > 0.f &&
                                        d->v_scale <= FLT_MAX))
     return LNK_EINVAL;
   // TMA row coordinates and 32-bit position arithmetic must not overflow
@@ -109,11 +109,11 @@ lnk_status check_desc(const lnk_attn_desc* d) {
   return LNK_OK;
 }
 
-// Softmax scale in log2 units; for 8-bit pools the scores are computed on
-// codes, so the key scale joins it.
+// Softmax scale in log2 units; for 8-bit and 4-bit pools the scores are
+// computed without the pool's key scale, so it joins the softmax scale.
 float scale_log2(const lnk_attn_desc* d) {
   double s = d->scale > 0.f ? static_cast<double>(d->scale) : 1.0 / std::sqrt(static_cast<double>(d->head_dim));
-  if (d->kv_dtype == LNK_KV_E4M3) s *= static_cast<double>(d->k_scale);
+  if (d->kv_dtype != LNK_KV_BF16) s *= static_cast<double>(d->k_scale);
   return static_cast<float>(s * 1.4426950408889634);  // log2(e)
 }
 
@@ -241,6 +241,10 @@ lnk_status lnk_rope_inv_freq(const lnk_rope_desc* rope, int32_t head_dim, float*
   return inv_freq_table(rope, head_dim, out);
 }
 
+size_t lnk_paged_page_bytes(const lnk_attn_desc* desc) {
+  return check_desc(desc) == LNK_OK ? static_cast<size_t>(page_bytes(desc->kv_dtype, desc->head_dim)) : 0;
+}
+
 size_t lnk_paged_workspace_size(const lnk_attn_desc* desc, int32_t max_rows) {
   if (check_desc(desc) != LNK_OK || max_rows < 0 || max_rows > kMaxDecodeRows) return 0;
   // the largest grid a call can use (two CTAs per SM)
@@ -318,6 +322,7 @@ static lnk_status append_params(const lnk_attn_desc* desc, const lnk_rope_desc* 
   p.num_rows = desc->num_rows;
   p.pages_per_row = desc->pages_per_row;
   p.kv8 = desc->kv_dtype == LNK_KV_E4M3;
+  p.kv4 = desc->kv_dtype == LNK_KV_E2M1;
   p.k_scale = desc->k_scale;
   p.v_scale = desc->v_scale;
   p.splits = 1;
@@ -344,6 +349,40 @@ lnk_status lnk_paged_append_rope(const lnk_attn_desc* desc, const lnk_rope_desc*
   if (st != LNK_OK) return st;
   return launch_append(p, desc->head_dim, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? LNK_OK
                                                                                                 : LNK_ECUDA;
+}
+
+lnk_status lnk_paged_read_tokens(const lnk_attn_desc* desc, const lnk_bf16* k_pool, const lnk_bf16* v_pool,
+                                 const int32_t* positions, const int32_t* rows, const int32_t* slots,
+                                 const int32_t* table, lnk_bf16* k_out, lnk_bf16* v_out, int32_t T,
+                                 int32_t* dev_status, lnk_stream stream) {
+  const lnk_status st = check_desc(desc);
+  if (st != LNK_OK) return st;
+  if (T < 0) return LNK_EINVAL;
+  if (T == 0) return LNK_OK;
+  if (!positions || (!slots && !table) || (!k_out && !v_out) || (k_out && !k_pool) || (v_out && !v_pool))
+    return LNK_EINVAL;
+  if (!aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(k_out, 16) || !aligned(v_out, 16)) return LNK_EINVAL;
+  if (rows == nullptr && slots == nullptr && T > desc->num_rows) return LNK_EINVAL;
+  ReadParams p;
+  p.pool[0] = reinterpret_cast<const uint8_t*>(k_pool);
+  p.pool[1] = reinterpret_cast<const uint8_t*>(v_pool);
+  p.out[0] = k_out;
+  p.out[1] = v_out;
+  p.scale[0] = desc->k_scale;
+  p.scale[1] = desc->v_scale;
+  p.positions = positions;
+  p.rows = rows;
+  p.slots = slots;
+  p.table = table;
+  p.status = dev_status;
+  p.T = T;
+  p.hkv = desc->num_kv_heads;
+  p.num_pages = desc->num_pages;
+  p.num_rows = desc->num_rows;
+  p.pages_per_row = desc->pages_per_row;
+  return launch_read_tokens(p, desc->head_dim, desc->kv_dtype, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? LNK_OK
+             : LNK_ECUDA;
 }
 
 // The pools reach the kernel through their tensor maps (kmap, vmap).
@@ -408,6 +447,7 @@ lnk_status decode_entry(const lnk_attn_desc* desc, const lnk_bf16* q_roped, cons
   if (B < 0 || B > desc->num_rows) return LNK_EINVAL;
   if (B > kMaxDecodeRows) return LNK_ERANGE;
   if (B == 0) return LNK_OK;
+  if (desc->kv_dtype == LNK_KV_E2M1) return LNK_EUNSUPPORTED;
   if (!q_roped || !positions || !table || !k_pool || !v_pool || !out) return LNK_EINVAL;
   if (!aligned(q_roped, 16) || !aligned(out, 8) || !aligned(k_pool, 16) || !aligned(v_pool, 16)) return LNK_EINVAL;
   CUtensorMap kmap, vmap;
@@ -461,6 +501,7 @@ lnk_status lnk_paged_decode_step(const lnk_attn_desc* desc, const lnk_rope_desc*
   if (B < 0 || B > desc->num_rows) return LNK_EINVAL;
   if (B > kMaxDecodeRows) return LNK_ERANGE;
   if (B == 0) return LNK_OK;
+  if (desc->kv_dtype == LNK_KV_E2M1) return LNK_EUNSUPPORTED;
   if (!table || !out || !aligned(q_out, 16) || !aligned(out, 8)) return LNK_EINVAL;
   AppendParams ap;
   st = append_params(desc, rope, q, k, v, positions, nullptr, nullptr, table, q_norm_w, k_norm_w, norm_eps, k_pool,
@@ -501,6 +542,7 @@ lnk_status lnk_paged_step_attn(const lnk_attn_desc* desc, const lnk_bf16* q_rope
   if (P < 0 || B < 0 || M < 0 || B > desc->num_rows) return LNK_EINVAL;
   if (B > kMaxDecodeRows) return LNK_ERANGE;
   if (P == 0 && B == 0) return LNK_OK;
+  if (desc->kv_dtype == LNK_KV_E2M1) return LNK_EUNSUPPORTED;
   if (!q_roped || !table || !k_pool || !v_pool || !out) return LNK_EINVAL;
   if (P > 0 && (!rows || !positions)) return LNK_EINVAL;
   if (B > 0 && !step_positions) return LNK_EINVAL;

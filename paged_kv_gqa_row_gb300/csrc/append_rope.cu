@@ -37,7 +37,50 @@ constexpr int kSplitCtasPerSm = 2;   // split launches aim at this many CTAs per
 
 using namespace rope;
 
-template <int D, int kWarps, int kMaxHeadsPerWarp>
+// A key row of a 4-bit pool: lane l < D/4 holds elements (2l, 2l + 1) in lo and
+// (2l + D/2, 2l + 1 + D/2) in hi, so eight lanes in a row hold a block of each
+// half.  Every lane of the warp calls it; `has`: the lane holds data.
+template <int D>
+__device__ __forceinline__ void store_key_e2m1(uint8_t* page, int j, int lane, bool has, uint32_t lo, uint32_t hi,
+                                               float ps) {
+  constexpr int H = D / 2;
+  uint32_t mlo = bf16x2_absmax(lo), mhi = bf16x2_absmax(hi);
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) {
+    mlo = max(mlo, __shfl_xor_sync(0xffffffffu, mlo, o));
+    mhi = max(mhi, __shfl_xor_sync(0xffffffffu, mhi, o));
+  }
+  if (!has) return;
+  const float six_ps = __fmul_rn(6.f, ps);
+  float dlo, dhi;
+  const uint32_t slo = e2m1_scale(mlo, six_ps, ps, dlo), shi = e2m1_scale(mhi, six_ps, ps, dhi);
+  uint8_t* row = page + j * (D / 2);
+  row[lane] = static_cast<uint8_t>(e2m1_codes(lo, dlo));
+  row[H / 2 + lane] = static_cast<uint8_t>(e2m1_codes(hi, dhi));
+  if ((lane & 7) == 0) {
+    page[e2m1_scale_offset<D>(j, lane >> 3)] = static_cast<uint8_t>(slo);
+    page[e2m1_scale_offset<D>(j, H / 16 + (lane >> 3))] = static_cast<uint8_t>(shi);
+  }
+}
+
+// A value row of a 4-bit pool: lane l < D/8 holds elements 8l .. 8l + 7, so two
+// lanes hold a block.  Every lane of the warp calls it.
+template <int D>
+__device__ __forceinline__ void store_value_e2m1(uint8_t* page, int j, int lane, uint4 x, float ps) {
+  uint32_t m = max(max(bf16x2_absmax(x.x), bf16x2_absmax(x.y)), max(bf16x2_absmax(x.z), bf16x2_absmax(x.w)));
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  if (lane >= D / 8) return;
+  float d;
+  const uint32_t s = e2m1_scale(m, __fmul_rn(6.f, ps), ps, d);
+  const uint32_t codes = e2m1_codes(x.x, d) | (e2m1_codes(x.y, d) << 8) | (e2m1_codes(x.z, d) << 16) |
+                         (e2m1_codes(x.w, d) << 24);
+  *reinterpret_cast<uint32_t*>(page + j * (D / 2) + 4 * lane) = codes;
+  if ((lane & 1) == 0) page[e2m1_scale_offset<D>(j, lane >> 1)] = static_cast<uint8_t>(s);
+}
+
+// KV4: pools of E2M1 codes and block scales (a variant of its own, so that the
+// other pools' kernel keeps its registers).
+template <int D, int kWarps, int kMaxHeadsPerWarp, bool KV4>
 __global__ void __launch_bounds__(kWarps * 32) append_rope_kernel(const AppendParams p) {
   constexpr int H = D / 2;
   constexpr int kLanes = D / 4;  // lanes holding data: two elements of each half
@@ -157,14 +200,25 @@ __global__ void __launch_bounds__(kWarps * 32) append_rope_kernel(const AppendPa
     if (l >= nloc) break;
     const bool is_q = hh < p.hq;
     uint16_t* dst = nullptr;
-    uint8_t* dst8 = nullptr;  // 8-bit pools: the key row's codes
+    uint8_t* dst8 = nullptr;  // 8-bit pools: the key row's codes; 4-bit pools: the key's page
     if (is_q) {
       dst = p.q_out + (static_cast<size_t>(t) * p.hq + hh) * D;
     } else {
       if (slot < 0) continue;
       const size_t off = (hh - p.hq) * pool_head_stride + static_cast<size_t>(slot) * D;
-      if (p.kv8) dst8 = reinterpret_cast<uint8_t*>(p.k_pool) + off;
+      if constexpr (KV4)
+        dst8 = reinterpret_cast<uint8_t*>(p.k_pool) +
+               (static_cast<size_t>(hh - p.hq) * p.num_pages + static_cast<size_t>(slot / kPage)) * (36 * D);
+      else if (p.kv8) dst8 = reinterpret_cast<uint8_t*>(p.k_pool) + off;
       else dst = p.k_pool + off;
+    }
+    if constexpr (KV4) {
+      if (!is_q) {  // (a key head with a slot: the token is active)
+        uint32_t lo = 0u, hi = 0u;
+        if (has) rotate_pairs(xlo[j], xhi[j], s_coef[1], e, norm_k, norm_k ? s_r[l] : DF{1.f, 0.f}, lo, hi);
+        store_key_e2m1<D>(dst8, static_cast<int>(slot % kPage), lane, has, lo, hi, p.k_scale);
+        continue;
+      }
     }
     if (!has) continue;
     if (pos < 0) {  // inactive token: zero query output
@@ -189,6 +243,13 @@ __global__ void __launch_bounds__(kWarps * 32) append_rope_kernel(const AppendPa
   if (slot >= 0) {
     for (int vh = sp + S * warp; vh < p.hkv; vh += S * kWarps) {
       const uint4* src = reinterpret_cast<const uint4*>(p.v + (static_cast<size_t>(t) * p.hkv + vh) * D);
+      if constexpr (KV4) {
+        uint8_t* page = reinterpret_cast<uint8_t*>(p.v_pool) +
+                        (static_cast<size_t>(vh) * p.num_pages + static_cast<size_t>(slot / kPage)) * (36 * D);
+        store_value_e2m1<D>(page, static_cast<int>(slot % kPage), lane,
+                            lane < D / 8 ? src[lane] : make_uint4(0u, 0u, 0u, 0u), p.v_scale);
+        continue;
+      }
       const size_t off = vh * pool_head_stride + static_cast<size_t>(slot) * D;
       if (lane < D / 8) {
         const uint4 x = src[lane];
@@ -205,13 +266,13 @@ __global__ void __launch_bounds__(kWarps * 32) append_rope_kernel(const AppendPa
   }
 }
 
-template <int D, int kWarps, int kHeads>
+template <int D, int kWarps, int kHeads, bool KV4>
 cudaError_t launch_append_w(const AppendParams& p, cudaStream_t stream) {
   // Prefer the largest shared-memory carveout, like the attention kernels that
   // follow: their CTAs can then start on an SM next to this kernel's (the
   // attention kernel is launched as a programmatic dependent) without the SM
   // first switching its L1 / shared-memory split.
-  const cudaError_t carve = prefer_max_shared(reinterpret_cast<const void*>(append_rope_kernel<D, kWarps, kHeads>));
+  const cudaError_t carve = prefer_max_shared(reinterpret_cast<const void*>(append_rope_kernel<D, kWarps, kHeads, KV4>));
   if (carve != cudaSuccess) return carve;
   const long long ctas = static_cast<long long>(p.T) * p.splits;
   if (ctas > 0x7fffffffll) return cudaErrorInvalidValue;
@@ -225,10 +286,10 @@ cudaError_t launch_append_w(const AppendParams& p, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, append_rope_kernel<D, kWarps, kHeads>, p);
+  return cudaLaunchKernelEx(&cfg, append_rope_kernel<D, kWarps, kHeads, KV4>, p);
 }
 
-template <int D>
+template <int D, bool KV4>
 cudaError_t launch_append_t(const AppendParams& p_in, cudaStream_t stream) {
   AppendParams p = p_in;
   const long long sms = device_sm_count();
@@ -239,12 +300,12 @@ cudaError_t launch_append_t(const AppendParams& p_in, cudaStream_t stream) {
     const int need = (nrot + kWarpsSplit * kHeadsSplit - 1) / (kWarpsSplit * kHeadsSplit);
     const long long want = (kSplitCtasPerSm * sms + p.T - 1) / p.T;
     p.splits = static_cast<int>(std::max<long long>(need, std::min<long long>(nrot, want)));
-    return launch_append_w<D, kWarpsSplit, kHeadsSplit>(p, stream);
+    return launch_append_w<D, kWarpsSplit, kHeadsSplit, KV4>(p, stream);
   }
   p.splits = 1;
   if (static_cast<long long>(p.T) >= kWideTokensPerSm * sms)
-    return launch_append_w<D, kWarpsWide, kMaxRotated / kWarpsWide>(p, stream);
-  return launch_append_w<D, kWarpsSmall, kMaxRotated / kWarpsSmall>(p, stream);
+    return launch_append_w<D, kWarpsWide, kMaxRotated / kWarpsWide, KV4>(p, stream);
+  return launch_append_w<D, kWarpsSmall, kMaxRotated / kWarpsSmall, KV4>(p, stream);
 }
 
 }  // namespace
@@ -252,10 +313,13 @@ cudaError_t launch_append_t(const AppendParams& p_in, cudaStream_t stream) {
 cudaError_t launch_append(const AppendParams& p, int head_dim, cudaStream_t stream) {
   if (p.T == 0) return cudaSuccess;
   if (p.hq + p.hkv > kMaxRotated) return cudaErrorInvalidValue;
-  switch (head_dim) {
-    case 64: return launch_append_t<64>(p, stream);
-    case 96: return launch_append_t<96>(p, stream);
-    case 128: return launch_append_t<128>(p, stream);
+  switch (head_dim + (p.kv4 ? 1 : 0)) {
+    case 64: return launch_append_t<64, false>(p, stream);
+    case 96: return launch_append_t<96, false>(p, stream);
+    case 128: return launch_append_t<128, false>(p, stream);
+    case 65: return launch_append_t<64, true>(p, stream);
+    case 97: return launch_append_t<96, true>(p, stream);
+    case 129: return launch_append_t<128, true>(p, stream);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -16,6 +16,12 @@ constexpr int kBoxBytes = kPage * kBoxCols * 2;  // one 64 x 64 bf16 box: 8 KiB
 constexpr int kMaxDecodeRows = 4096;
 constexpr int kMaxGroup = 8;
 
+// Bytes of one page of one kv head (lnk_attn_desc.kv_dtype; 0 for another type).
+__host__ __device__ constexpr int page_bytes(int kv_dtype, int d) {
+  return kv_dtype == LNK_KV_BF16 ? 2 * kPage * d
+                                 : (kv_dtype == LNK_KV_E4M3 ? kPage * d : (kv_dtype == LNK_KV_E2M1 ? 36 * d : 0));
+}
+
 __host__ __device__ constexpr int boxes_for(int d) { return (d + kBoxCols - 1) / kBoxCols; }
 
 // ---------------------------------------------------------------- append --
@@ -36,12 +42,28 @@ struct AppendParams {
   double norm_eps;
   int T, hq, hkv, num_pages, num_rows, pages_per_row;
   int kv8;                    // pools hold E4M3 codes
-  float k_scale, v_scale;     // their scales (a code c stands for e4m3(c) * scale)
+  int kv4;                    // pools hold E2M1 codes and E4M3 block scales
+  float k_scale, v_scale;     // their scales (see lnk_attn_desc)
   int splits;                 // CTAs per token (set by launch_append)
   float inv_freq[64];
 };
 
 cudaError_t launch_append(const AppendParams& p, int head_dim, cudaStream_t stream);
+
+// ------------------------------------------------------------ read tokens --
+struct ReadParams {
+  const uint8_t* pool[2];     // K, V (null: not read)
+  uint16_t* out[2];           // [T][Hkv][D]
+  float scale[2];
+  const int32_t* positions;   // [T]
+  const int32_t* rows;
+  const int32_t* slots;
+  const int32_t* table;
+  int32_t* status;
+  int T, hkv, num_pages, num_rows, pages_per_row;
+};
+
+cudaError_t launch_read_tokens(const ReadParams& p, int head_dim, int kv_dtype, cudaStream_t stream);
 
 // ---------------------------------------------------------------- decode --
 struct DecodeParams {

@@ -185,6 +185,49 @@ __device__ __forceinline__ uint16_t e4m3_pair(uint32_t bits, float scale) {
   return static_cast<uint16_t>(__nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3));
 }
 
+// ------------------------------------------------------------ 4-bit blocks --
+// Two floats to a byte of E2M1 codes (nearest even, saturating to +-6), `lo`
+// in the low four bits.
+__device__ __forceinline__ uint32_t e2m1_pair(float lo, float hi) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 t, z;\n\tmov.b16 {t, z}, 0;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tmov.b32 %0, {t, z, z, z};\n\t}"
+      : "=r"(r)
+      : "f"(hi), "f"(lo));
+  return r;
+}
+
+// The larger magnitude of two bf16 values (as bits without the sign: integer
+// order is the order of magnitudes, with NaN above infinity).
+__device__ __forceinline__ uint32_t bf16x2_absmax(uint32_t w) { return max(w & 0x7FFFu, (w >> 16) & 0x7FFFu); }
+
+// A block of 16: its scale code, and the value `d` that its elements are
+// divided by (0: the block stores zero codes).  absmax: the block's largest
+// magnitude as bf16 bits; six_ps = fl32(6 * ps).
+__device__ __forceinline__ uint32_t e2m1_scale(uint32_t absmax, float six_ps, float ps, float& d) {
+  const float t = __fdiv_rn(__uint_as_float(absmax << 16), six_ps);
+  uint32_t s = __nv_cvt_float_to_fp8(t, __NV_SATFINITE, __NV_E4M3) & 0xFFu;
+  if (absmax > 0x7F80u) s = 0x7Fu;  // NaN
+  const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(s), __NV_E4M3);
+  d = __fmul_rn(__half2float(__half(h)), ps);
+  if (!(d > 0.f)) {
+    d = 0.f;
+    if (s != 0x7Fu) s = 0u;
+  }
+  return s;
+}
+
+// The byte of codes of two bf16 values (low half first) of a block with divisor d.
+__device__ __forceinline__ uint32_t e2m1_codes(uint32_t bits, float d) {
+  if (d == 0.f) return 0u;
+  return e2m1_pair(__fdiv_rn(__uint_as_float(bits << 16), d), __fdiv_rn(__uint_as_float(bits & 0xFFFF0000u), d));
+}
+
+// Byte offset of position j's scale of block b in a page of one head.
+template <int D>
+__device__ __forceinline__ int e2m1_scale_offset(int j, int b) {
+  return 32 * D + ((j & 3) * (D / 16) + b) * 16 + (j >> 2);
+}
+
 // Sine and cosine (float pairs) of the float32 angle f32(pos) * inv_freq.
 __device__ __forceinline__ void angle_sincos(int pos, float inv_freq, DF& sn, DF& cs) {
   const float a = __fmul_rn(static_cast<float>(pos), inv_freq);
