@@ -139,8 +139,10 @@ typedef struct lnk_attn_desc {
  *   that the block's largest element saturates: it is then off by at most
  *   1/17 of its size.)
  *     Attention uses the values e2m1(code) * e4m3(s) * pool scale; products of
- *   a code and a scale are exact in f16 and bf16.  The append and
- *   lnk_paged_read_tokens are supported; attention returns LNK_EUNSUPPORTED. */
+ *   a code and a scale are exact in f16 and bf16.  Append, reading
+ *   tokens and decode rows are supported; chunk attention returns
+ *   LNK_EUNSUPPORTED.  Decode converts the rotated queries to f16 as for
+ *   LNK_KV_E4M3, with the same range. */
 #define LNK_KV_BF16 0
 #define LNK_KV_E4M3 1
 #define LNK_KV_E2M1 4

@@ -385,22 +385,45 @@ lnk_status lnk_paged_read_tokens(const lnk_attn_desc* desc, const lnk_bf16* k_po
              : LNK_ECUDA;
 }
 
-// The pools reach the kernel through their tensor maps (kmap, vmap).
+// The launch that a decode call takes (fused: the one-kernel decode step).
+static bool decode_launch(const lnk_attn_desc* desc, int32_t B, DecodeLaunch* launch, bool fused = false) {
+  const cudaError_t err =
+      desc->kv_dtype == LNK_KV_E2M1
+          ? decode4_prepare(desc->head_dim, B, launch)
+          : decode_prepare(desc->head_dim, desc->kv_dtype == LNK_KV_E4M3, B, desc->num_kv_heads, launch, fused);
+  return err == cudaSuccess && launch->grid > 0;
+}
+
+// The pools as the attention kernels take them: tensor maps, or plain pointers
+// for 4-bit pools (whose maps stay zero).
+struct Pools {
+  CUtensorMap kmap, vmap;
+  const uint8_t *k4 = nullptr, *v4 = nullptr;
+};
+
+static bool make_pools(Pools* out, const lnk_bf16* k_pool, const lnk_bf16* v_pool, const lnk_attn_desc& d) {
+  if (d.kv_dtype == LNK_KV_E2M1) {
+    out->k4 = reinterpret_cast<const uint8_t*>(k_pool);
+    out->v4 = reinterpret_cast<const uint8_t*>(v_pool);
+    std::memset(&out->kmap, 0, sizeof(out->kmap));
+    std::memset(&out->vmap, 0, sizeof(out->vmap));
+    return true;
+  }
+  return pool_map(&out->kmap, k_pool, d) && pool_map(&out->vmap, v_pool, d);
+}
+
 // clear_counters: zero the workspace's counters on the stream right before the
 // launch (after every check has passed), for a workspace whose previous
 // contents are unknown.
 // fuse: the fused decode step's append parameters (null: attention only).
 static lnk_status decode_common(const lnk_attn_desc* desc, const lnk_bf16* q, const int32_t* positions,
                                 const int32_t* table, lnk_bf16* out, int32_t B, void* workspace, size_t ws_bytes,
-                                int32_t* dev_status, const CUtensorMap& kmap, const CUtensorMap& vmap,
-                                cudaStream_t stream, bool clear_counters = false,
+                                int32_t* dev_status, const Pools& pools, cudaStream_t stream,
+                                bool clear_counters = false,
                                 const AppendParams* fuse = nullptr) {
   if (B == 0) return LNK_OK;
   DecodeLaunch launch;
-  const bool kv8 = desc->kv_dtype == LNK_KV_E4M3;
-  if (decode_prepare(desc->head_dim, kv8, B, desc->num_kv_heads, &launch, fuse != nullptr) != cudaSuccess ||
-      launch.grid <= 0)
-    return LNK_ECUDA;
+  if (!decode_launch(desc, B, &launch, fuse != nullptr)) return LNK_ECUDA;
   const int group = desc->num_q_heads / desc->num_kv_heads;
   const DecodeWorkspace w = decode_workspace_layout(B, desc->num_kv_heads, group, desc->head_dim, launch.grid);
   if (workspace == nullptr || ws_bytes < w.total || !aligned(workspace, 256)) return LNK_EWORKSPACE;
@@ -423,7 +446,9 @@ static lnk_status decode_common(const lnk_attn_desc* desc, const lnk_bf16* q, co
   p.pages_per_row = desc->pages_per_row;
   p.window = desc->window;
   p.scale_log2 = scale_log2(desc);
-  p.out_scale = kv8 ? desc->v_scale : 1.f;
+  p.out_scale = desc->kv_dtype != LNK_KV_BF16 ? desc->v_scale : 1.f;
+  p.k_pool4 = pools.k4;
+  p.v_pool4 = pools.v4;
   std::memset(&p.ap, 0, sizeof(p.ap));
   p.fuse = 0;
   if (fuse != nullptr) {
@@ -431,7 +456,10 @@ static lnk_status decode_common(const lnk_attn_desc* desc, const lnk_bf16* q, co
     p.ap = *fuse;
   }
   if (clear_counters && cudaMemsetAsync(ws, 0, w.ml, stream) != cudaSuccess) return LNK_ECUDA;
-  return launch_decode(kmap, vmap, p, desc->head_dim, launch, stream) == cudaSuccess ? LNK_OK : LNK_ECUDA;
+  const cudaError_t err = desc->kv_dtype == LNK_KV_E2M1
+                              ? launch_decode4(p, desc->head_dim, launch, stream)
+                              : launch_decode(pools.kmap, pools.vmap, p, desc->head_dim, launch, stream);
+  return err == cudaSuccess ? LNK_OK : LNK_ECUDA;
 }
 
 }  // extern "C"
@@ -447,12 +475,11 @@ lnk_status decode_entry(const lnk_attn_desc* desc, const lnk_bf16* q_roped, cons
   if (B < 0 || B > desc->num_rows) return LNK_EINVAL;
   if (B > kMaxDecodeRows) return LNK_ERANGE;
   if (B == 0) return LNK_OK;
-  if (desc->kv_dtype == LNK_KV_E2M1) return LNK_EUNSUPPORTED;
   if (!q_roped || !positions || !table || !k_pool || !v_pool || !out) return LNK_EINVAL;
   if (!aligned(q_roped, 16) || !aligned(out, 8) || !aligned(k_pool, 16) || !aligned(v_pool, 16)) return LNK_EINVAL;
-  CUtensorMap kmap, vmap;
-  if (!pool_map(&kmap, k_pool, *desc) || !pool_map(&vmap, v_pool, *desc)) return LNK_ECUDA;
-  return decode_common(desc, q_roped, positions, table, out, B, workspace, ws_bytes, dev_status, kmap, vmap,
+  Pools pools;
+  if (!make_pools(&pools, k_pool, v_pool, *desc)) return LNK_ECUDA;
+  return decode_common(desc, q_roped, positions, table, out, B, workspace, ws_bytes, dev_status, pools,
                        reinterpret_cast<cudaStream_t>(stream), clear_counters);
 }
 
@@ -473,6 +500,7 @@ lnk_status lnk_paged_decode_attn(const lnk_attn_desc* desc, const lnk_bf16* q_ro
 // kFuseMaxPages pages a pair (so that one long pair cannot hold up the launch
 // for long).
 static bool decode_step_fuses(const lnk_attn_desc* desc, int32_t B, int grid) {
+  if (desc->kv_dtype == LNK_KV_E2M1) return false;  // (the 4-bit kernel has no one-kernel form)
   const long long pairs = static_cast<long long>(B) * desc->num_kv_heads;
   long long pair_pages = desc->pages_per_row;
   if (desc->window > 0) pair_pages = std::min<long long>(pair_pages, (desc->window - 1) / kPage + 2);
@@ -483,10 +511,7 @@ int32_t lnk_paged_decode_step_launches(const lnk_attn_desc* desc, int32_t B) {
   if (check_desc(desc) != LNK_OK || B < 0 || B > desc->num_rows || B > kMaxDecodeRows) return -1;
   if (B == 0) return 0;
   DecodeLaunch launch;
-  if (decode_prepare(desc->head_dim, desc->kv_dtype == LNK_KV_E4M3, B, desc->num_kv_heads, &launch, true) !=
-          cudaSuccess ||
-      launch.grid <= 0)
-    return -1;
+  if (!decode_launch(desc, B, &launch, true)) return -1;
   return decode_step_fuses(desc, B, launch.grid) ? 1 : 2;
 }
 
@@ -501,22 +526,17 @@ lnk_status lnk_paged_decode_step(const lnk_attn_desc* desc, const lnk_rope_desc*
   if (B < 0 || B > desc->num_rows) return LNK_EINVAL;
   if (B > kMaxDecodeRows) return LNK_ERANGE;
   if (B == 0) return LNK_OK;
-  if (desc->kv_dtype == LNK_KV_E2M1) return LNK_EUNSUPPORTED;
   if (!table || !out || !aligned(q_out, 16) || !aligned(out, 8)) return LNK_EINVAL;
   AppendParams ap;
   st = append_params(desc, rope, q, k, v, positions, nullptr, nullptr, table, q_norm_w, k_norm_w, norm_eps, k_pool,
                      v_pool, q_out, B, dev_status, &ap);
   if (st != LNK_OK) return st;
-  CUtensorMap kmap, vmap;
-  if (!pool_map(&kmap, k_pool, *desc) || !pool_map(&vmap, v_pool, *desc)) return LNK_ECUDA;
+  Pools pools;
+  if (!make_pools(&pools, k_pool, v_pool, *desc)) return LNK_ECUDA;
   // the launch of the one-kernel form, and the attention kernel's launch of
   // the two-kernel form
   DecodeLaunch fused_launch, launch;
-  const bool kv8 = desc->kv_dtype == LNK_KV_E4M3;
-  if (decode_prepare(desc->head_dim, kv8, B, desc->num_kv_heads, &fused_launch, true) != cudaSuccess ||
-      fused_launch.grid <= 0 ||
-      decode_prepare(desc->head_dim, kv8, B, desc->num_kv_heads, &launch) != cudaSuccess || launch.grid <= 0)
-    return LNK_ECUDA;
+  if (!decode_launch(desc, B, &fused_launch, true) || !decode_launch(desc, B, &launch)) return LNK_ECUDA;
   const int group = desc->num_q_heads / desc->num_kv_heads;
   const bool fuses = decode_step_fuses(desc, B, fused_launch.grid);
   const DecodeWorkspace w = decode_workspace_layout(B, desc->num_kv_heads, group, desc->head_dim,
@@ -524,11 +544,11 @@ lnk_status lnk_paged_decode_step(const lnk_attn_desc* desc, const lnk_rope_desc*
   if (workspace == nullptr || ws_bytes < w.total || !aligned(workspace, 256)) return LNK_EWORKSPACE;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (fuses)
-    return decode_common(desc, q_out, positions, table, out, B, workspace, ws_bytes, dev_status, kmap, vmap, s,
-                         false, &ap);
+    return decode_common(desc, q_out, positions, table, out, B, workspace, ws_bytes, dev_status, pools, s, false,
+                         &ap);
   // otherwise the append, then attention
   if (launch_append(ap, desc->head_dim, s) != cudaSuccess) return LNK_ECUDA;
-  return decode_common(desc, q_out, positions, table, out, B, workspace, ws_bytes, dev_status, kmap, vmap, s);
+  return decode_common(desc, q_out, positions, table, out, B, workspace, ws_bytes, dev_status, pools, s);
 }
 
 lnk_status lnk_paged_step_attn(const lnk_attn_desc* desc, const lnk_bf16* q_roped, const int32_t* rows,
@@ -542,7 +562,6 @@ lnk_status lnk_paged_step_attn(const lnk_attn_desc* desc, const lnk_bf16* q_rope
   if (P < 0 || B < 0 || M < 0 || B > desc->num_rows) return LNK_EINVAL;
   if (B > kMaxDecodeRows) return LNK_ERANGE;
   if (P == 0 && B == 0) return LNK_OK;
-  if (desc->kv_dtype == LNK_KV_E2M1) return LNK_EUNSUPPORTED;
   if (!q_roped || !table || !k_pool || !v_pool || !out) return LNK_EINVAL;
   if (P > 0 && (!rows || !positions)) return LNK_EINVAL;
   if (B > 0 && !step_positions) return LNK_EINVAL;
@@ -553,8 +572,8 @@ lnk_status lnk_paged_step_attn(const lnk_attn_desc* desc, const lnk_bf16* q_rope
     const size_t need = lnk_paged_workspace_size(desc, B);
     if (workspace == nullptr || need == 0 || ws_bytes < need) return LNK_EWORKSPACE;
   }
-  CUtensorMap kmap, vmap;
-  if (!pool_map(&kmap, k_pool, *desc) || !pool_map(&vmap, v_pool, *desc)) return LNK_ECUDA;
+  Pools pools;
+  if (!make_pools(&pools, k_pool, v_pool, *desc)) return LNK_ECUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int group = desc->num_q_heads / desc->num_kv_heads;
   const size_t row_elems = static_cast<size_t>(desc->num_q_heads) * desc->head_dim;
@@ -578,11 +597,11 @@ lnk_status lnk_paged_step_attn(const lnk_attn_desc* desc, const lnk_bf16* q_rope
     c.tile_tokens = 128 / group;
     c.num_tiles = (P + kChunkHalves * c.tile_tokens - 1) / (kChunkHalves * c.tile_tokens);
     c.scale_log2 = scale_log2(desc);
-    if (launch_chunk(kmap, vmap, c, desc->head_dim, s) != cudaSuccess) return LNK_ECUDA;
+    if (launch_chunk(pools.kmap, pools.vmap, c, desc->head_dim, s) != cudaSuccess) return LNK_ECUDA;
   }
   if (B > 0) {
     st = decode_common(desc, q_roped + static_cast<size_t>(P) * row_elems, step_positions, table,
-                       out + static_cast<size_t>(P) * row_elems, B, workspace, ws_bytes, dev_status, kmap, vmap, s);
+                       out + static_cast<size_t>(P) * row_elems, B, workspace, ws_bytes, dev_status, pools, s);
     if (st != LNK_OK) return st;
   }
   if (M > 0) {

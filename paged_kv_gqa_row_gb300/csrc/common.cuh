@@ -78,7 +78,9 @@ struct DecodeParams {
   float* ws_o;                // [segments][G][D]: unnormalised partial outputs
   int B, hq, hkv, group, num_pages, pages_per_row, window;
   float scale_log2;           // softmax scale * log2(e) (8-bit pools: times the key scale)
-  float out_scale;            // 1, or the value scale of an 8-bit pool
+  float out_scale;            // 1, or the value scale of an 8-bit or 4-bit pool
+  const uint8_t* k_pool4;     // 4-bit pools (the others are reached through tensor maps)
+  const uint8_t* v_pool4;
   // Fused decode step (fuse != 0): the CTA of pair (b, h) first rotates and
   // writes row b's token for kv head h (the append's work for that pair, with
   // `ap`: T = B, token b in table row b) and then attends.  Set only when every
@@ -113,6 +115,10 @@ lnk_status decode_entry(const lnk_attn_desc* desc, const lnk_bf16* q_roped, cons
                         bool clear_counters);
 cudaError_t launch_decode(const CUtensorMap& kmap, const CUtensorMap& vmap, const DecodeParams& p,
                           int head_dim, const DecodeLaunch& launch, cudaStream_t stream);
+
+// The same for 4-bit pools (p.k_pool4, p.v_pool4), in decode4.cu.
+cudaError_t decode4_prepare(int head_dim, int B, DecodeLaunch* launch);
+cudaError_t launch_decode4(const DecodeParams& p, int head_dim, const DecodeLaunch& launch, cudaStream_t stream);
 
 // ----------------------------------------------------------------- chunk --
 // A chunk-attention CTA holds this many halves of 128 query rows.
