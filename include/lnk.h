@@ -424,7 +424,10 @@ lnk_status lnk_paged_decode_attn_static(const lnk_attn_desc* desc, const lnk_bf1
  *     more than once onto a fresh private page (copy on write): the caller
  *     copies the old page into the new one with lnk_paged_copy_pages before
  *     the append;
- *   - release drops a row's pages; a page whose count reaches 0 is free.
+ *   - release drops a row's pages; a page whose count reaches 0 is free;
+ *   - compact moves the pages above a limit to free pages below it, so that the
+ *     upper part of the pools can be given back or the pools written out in
+ *     one piece: the caller copies the pages with lnk_paged_copy_pages_layers.
  * The pager holds host memory only (its table is exported into a caller
  * buffer for upload to the device) and is not thread-safe: serialise the
  * calls made on one pager.  Host pointers below are host memory.
@@ -467,6 +470,19 @@ lnk_status lnk_pager_prepare_append(lnk_pager* pager, const int32_t* rows, const
 /* Unmaps every page of `row`; pages whose count reaches 0 become free. */
 lnk_status lnk_pager_release(lnk_pager* pager, int32_t row);
 
+/* Moves every mapped page >= limit to a free page below limit: sources in
+ * ascending order, each to the lowest free page.  Every table entry that mapped
+ * the old page (of all rows that share it) maps the new one, which takes over
+ * its count, and the old page is free.  The moves are written as (old page, new
+ * page) to copy_src/copy_dst (host arrays of `capacity`; num_pages - limit
+ * always suffices) and *num_copies counts them; no page is both a source and a
+ * target.  Copy the pages in every layer's pools before anything reads the new
+ * table or writes the old pages.  LNK_EINVAL for a limit outside [0, num_pages]
+ * or a negative capacity, LNK_ERANGE if capacity does not suffice, LNK_ENOSPACE
+ * if the free pages below limit do not; on any error nothing changes. */
+lnk_status lnk_pager_compact(lnk_pager* pager, int32_t limit, int32_t* copy_src, int32_t* copy_dst,
+                             int32_t capacity, int32_t* num_copies);
+
 /* Writes the table, [num_rows][pages_per_row] int32 (-1 = unmapped), into the
  * host buffer `table`. */
 lnk_status lnk_pager_table(const lnk_pager* pager, int32_t* table);
@@ -486,6 +502,17 @@ int32_t lnk_pager_refcount(const lnk_pager* pager, int32_t page);
 lnk_status lnk_paged_copy_pages(const lnk_attn_desc* desc, lnk_bf16* k_pool, lnk_bf16* v_pool,
                                 const int32_t* src_pages, const int32_t* dst_pages, int32_t n,
                                 int32_t* dev_status, lnk_stream stream);
+
+/* The same in the pools of `layers` layers that share one table: k_pools and
+ * v_pools are host arrays of `layers` device pointers (read during the call;
+ * the addresses travel with the launch, so a captured call keeps them).  One
+ * launch for up to 128 layers and 65535 pairs.  desc's shape holds for every
+ * layer.  A bad pair is skipped in every layer.  layers = 0 or n = 0 enqueues
+ * nothing. */
+lnk_status lnk_paged_copy_pages_layers(const lnk_attn_desc* desc, lnk_bf16* const* k_pools,
+                                       lnk_bf16* const* v_pools, int32_t layers, const int32_t* src_pages,
+                                       const int32_t* dst_pages, int32_t n, int32_t* dev_status,
+                                       lnk_stream stream);
 
 /* ---------------------------------------------------------------------------
  * Self-test of the bounded waits.  Every wait inside the kernels above is

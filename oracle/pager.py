@@ -16,7 +16,10 @@ plainest allocator that lets rows share the pages of a common prefix:
     entry is unmapped, or, if the page is mapped by other entries too, maps a
     fresh page instead and records (old, new) for a copy of the contents;
   * release(row): the row's entries are unmapped; a page whose count reaches
-    zero is free again.
+    zero is free again;
+  * compact(limit): each mapped page >= limit, in ascending order, moves to the
+    lowest free page, which has to lie below limit; all entries that map it
+    follow, and (old, new) is recorded for a copy of the contents.
   * A call that fails (bad row, position past the table row, too few free
     pages) changes nothing.
 """
@@ -124,6 +127,20 @@ class Pager:
                 if self.count[page] == 0:
                     self.free.add(page)
                 self.rows[row][lp] = UNMAPPED
+
+    def compact(self, limit: int):
+        if not 0 <= limit <= self.num_pages:
+            raise PagerError("EINVAL")
+        old = [p for p in range(limit, self.num_pages) if self.count[p] > 0]
+        new = sorted(p for p in self.free if p < limit)[:len(old)]
+        if len(new) < len(old):
+            raise PagerError("ENOSPACE")
+        to = dict(zip(old, new))
+        self.rows = [[to.get(p, p) for p in row] for row in self.rows]
+        for a, b in to.items():
+            self.count[a], self.count[b] = 0, self.count[a]
+        self.free = (self.free - set(new)) | set(old)
+        return list(to.items())
 
     def table(self):
         return [list(r) for r in self.rows]

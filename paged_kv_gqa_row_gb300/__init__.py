@@ -18,6 +18,7 @@ from .binding import (  # noqa: F401
     attn_desc,
     lnk_paged_append_rope,
     lnk_paged_copy_pages,
+    lnk_paged_copy_pages_layers,
     lnk_paged_decode_attn,
     lnk_paged_decode_step,
     lnk_paged_decode_step_launches,

@@ -33,7 +33,7 @@ EXPORTED = ["lnk_status_string", "lnk_rope_inv_freq", "lnk_paged_workspace_size"
             "lnk_paged_decode_attn_static", "lnk_pager_create", "lnk_pager_destroy", "lnk_pager_reserve",
             "lnk_pager_fork", "lnk_pager_prepare_append", "lnk_pager_release", "lnk_pager_table",
             "lnk_pager_free_pages", "lnk_pager_refcount", "lnk_paged_copy_pages",
-            "lnk_paged_page_bytes", "lnk_paged_read_tokens",
+            "lnk_paged_page_bytes", "lnk_paged_read_tokens", "lnk_pager_compact", "lnk_paged_copy_pages_layers",
             "lnk_selftest_wait_timeout"]
 
 
@@ -110,6 +110,10 @@ _lib.lnk_pager_free_pages.restype = c_i32
 _lib.lnk_pager_free_pages.argtypes = [c_vp]
 _lib.lnk_pager_refcount.restype = c_i32
 _lib.lnk_pager_refcount.argtypes = [c_vp, c_i32]
+_lib.lnk_pager_compact.restype = ctypes.c_int
+_lib.lnk_pager_compact.argtypes = [c_vp, c_i32, _i32p, _i32p, c_i32, _i32p]
+_lib.lnk_paged_copy_pages_layers.restype = ctypes.c_int
+_lib.lnk_paged_copy_pages_layers.argtypes = [ctypes.POINTER(AttnDesc), c_vp, c_vp, c_i32, c_vp, c_vp, c_i32, c_vp, c_vp]
 _lib.lnk_paged_copy_pages.restype = ctypes.c_int
 _lib.lnk_paged_copy_pages.argtypes = [ctypes.POINTER(AttnDesc), c_vp, c_vp, c_vp, c_vp, c_i32, c_vp, c_vp]
 _lib.lnk_selftest_wait_timeout.restype = ctypes.c_int
@@ -235,6 +239,18 @@ def lnk_paged_copy_pages(desc, k_pool, v_pool, src_pages, dst_pages, n, dev_stat
     _check(st, "lnk_paged_copy_pages")
 
 
+def lnk_paged_copy_pages_layers(desc, k_pools, v_pools, src_pages, dst_pages, n, dev_status=None, stream=None):
+    """lnk_paged_copy_pages in every layer: k_pools and v_pools are sequences of the layers' pools."""
+    if len(k_pools) != len(v_pools):
+        raise ValueError("k_pools and v_pools differ in length")
+    layers = len(k_pools)
+    ptrs = (c_vp * (2 * layers))(*[_ptr(x) for x in k_pools], *[_ptr(x) for x in v_pools])
+    base = ctypes.addressof(ptrs)
+    st = _lib.lnk_paged_copy_pages_layers(ctypes.byref(desc), base, base + layers * ctypes.sizeof(c_vp), layers,
+                                          _ptr(src_pages), _ptr(dst_pages), n, _ptr(dev_status), _stream(stream))
+    _check(st, "lnk_paged_copy_pages_layers")
+
+
 def lnk_selftest_wait_timeout(dev_status, limit_ns, stream=None):
     st = _lib.lnk_selftest_wait_timeout(_ptr(dev_status), int(limit_ns), _stream(stream))
     _check(st, "lnk_selftest_wait_timeout")
@@ -282,6 +298,15 @@ class Pager:
         nc = c_i32(0)
         _check(_lib.lnk_pager_prepare_append(self._h, rp, qp, n, srcp, dstp, ctypes.byref(nc)),
                "lnk_pager_prepare_append")
+        return [(int(src[i]), int(dst[i])) for i in range(nc.value)]
+
+    def compact(self, limit: int):
+        """Moves the pages at or above `limit` below it; returns the (old, new) page copies, in order."""
+        cap = max(0, self.num_pages - limit)
+        src, srcp = _i32_array([0] * max(1, cap))
+        dst, dstp = _i32_array([0] * max(1, cap))
+        nc = c_i32(0)
+        _check(_lib.lnk_pager_compact(self._h, limit, srcp, dstp, cap, ctypes.byref(nc)), "lnk_pager_compact")
         return [(int(src[i]), int(dst[i])) for i in range(nc.value)]
 
     def release(self, row: int):

@@ -1,16 +1,18 @@
 // Host page allocator for the page pool (lnk_pager_*): a free set handed out
 // lowest page first, a reference count per page, rows that share the pages of
 // a common prefix (fork), copy on write when a row writes into a shared page,
-// and release.  It owns host memory only and exports its table for upload.
+// release, and compaction below a page limit.  It owns host memory only and exports its table for upload.
 //
 // Source: "Mistral 7B Instruct v0.3", Entries table (prefill_paged: each
 // token attends over its row's pages up to its position -- chunks, shared
 // prefixes).  The pages do not say how pages are handed out; this is the
 // plainest allocator that lets rows share prefix pages.
+#include <algorithm>
 #include <cstdint>
 #include <new>
 #include <set>
 #include <unordered_map>
+#include <utility>
 #include <vector>
 
 #include "../../include/lnk.h"
@@ -161,6 +163,40 @@ lnk_status lnk_pager_release(lnk_pager* pg, int32_t row) {
       e = kUnmapped;
     }
   }
+  return LNK_OK;
+}
+
+lnk_status lnk_pager_compact(lnk_pager* pg, int32_t limit, int32_t* copy_src, int32_t* copy_dst, int32_t capacity,
+                             int32_t* num_copies) {
+  if (pg == nullptr || num_copies == nullptr) return LNK_EINVAL;
+  *num_copies = 0;
+  if (limit < 0 || limit > pg->num_pages || capacity < 0) return LNK_EINVAL;
+  int32_t moves = 0, room = 0;
+  for (int32_t p = limit; p < pg->num_pages; ++p) moves += pg->refcount[p] > 0;
+  if (moves == 0) return LNK_OK;
+  if (copy_src == nullptr || copy_dst == nullptr) return LNK_EINVAL;
+  if (moves > capacity) return LNK_ERANGE;
+  for (auto it = pg->free_pages.begin(); it != pg->free_pages.end() && *it < limit && room < moves; ++it) ++room;
+  if (room < moves) return LNK_ENOSPACE;
+  // Sources ascend and the free pages are taken lowest first, so both lists do;
+  // the set's nodes change their page in place (nothing here allocates).
+  int32_t n = 0;
+  for (int32_t p = limit; p < pg->num_pages; ++p) {
+    if (pg->refcount[p] == 0) continue;
+    auto node = pg->free_pages.extract(pg->free_pages.begin());
+    const int32_t to = node.value();
+    pg->refcount[to] = pg->refcount[p];
+    pg->refcount[p] = 0;
+    node.value() = p;
+    pg->free_pages.insert(pg->free_pages.end(), std::move(node));
+    copy_src[n] = p;
+    copy_dst[n] = to;
+    ++n;
+  }
+  // every entry that maps a moved page, in whatever rows
+  for (int32_t& e : pg->table)
+    if (e >= limit) e = copy_dst[std::lower_bound(copy_src, copy_src + n, e) - copy_src];
+  *num_copies = n;
   return LNK_OK;
 }
 
