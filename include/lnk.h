@@ -139,10 +139,9 @@ typedef struct lnk_attn_desc {
  *   that the block's largest element saturates: it is then off by at most
  *   1/17 of its size.)
  *     Attention uses the values e2m1(code) * e4m3(s) * pool scale; products of
- *   a code and a scale are exact in f16 and bf16.  Append, reading
- *   tokens and decode rows are supported; chunk attention returns
- *   LNK_EUNSUPPORTED.  Decode converts the rotated queries to f16 as for
- *   LNK_KV_E4M3, with the same range. */
+ *   a code and a scale are exact in f16 and bf16.  Every entry
+ *   point takes these pools.  Attention converts the rotated queries to f16 as
+ *   decode does for LNK_KV_E4M3, with the same range. */
 #define LNK_KV_BF16 0
 #define LNK_KV_E4M3 1
 #define LNK_KV_E2M1 4
@@ -365,7 +364,8 @@ int32_t lnk_paged_decode_step_launches(const lnk_attn_desc* desc, int32_t B);
  *   last      device int32 [M] or NULL: chunk token whose output row is copied
  *             to last_out[m] (device [M][Hq][D]); M may be 0
  *   P, B      chunk tokens and decode rows (either may be 0); P > 0 with
- *             LNK_KV_E4M3 pools returns LNK_EUNSUPPORTED
+ *             LNK_KV_E4M3 pools returns LNK_EUNSUPPORTED (bf16 and 4-bit pools
+ *             are served)
  *   workspace as for decode_attn with max_rows >= B
  */
 lnk_status lnk_paged_step_attn(const lnk_attn_desc* desc, const lnk_bf16* q_roped,

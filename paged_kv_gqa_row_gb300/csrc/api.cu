@@ -566,7 +566,7 @@ lnk_status lnk_paged_step_attn(const lnk_attn_desc* desc, const lnk_bf16* q_rope
   if (P > 0 && (!rows || !positions)) return LNK_EINVAL;
   if (B > 0 && !step_positions) return LNK_EINVAL;
   if (M > 0 && (!last || !last_out)) return LNK_EINVAL;
-  if (P > 0 && desc->kv_dtype != LNK_KV_BF16) return LNK_EUNSUPPORTED;  // chunk kernel reads bf16 pools
+  if (P > 0 && desc->kv_dtype == LNK_KV_E4M3) return LNK_EUNSUPPORTED;  // the chunk kernel has no 8-bit form
   if (!aligned(q_roped, 16) || !aligned(out, 8) || !aligned(k_pool, 16) || !aligned(v_pool, 16)) return LNK_EINVAL;
   if (B > 0) {
     const size_t need = lnk_paged_workspace_size(desc, B);
@@ -594,6 +594,9 @@ lnk_status lnk_paged_step_attn(const lnk_attn_desc* desc, const lnk_bf16* q_rope
     c.num_rows = desc->num_rows;
     c.pages_per_row = desc->pages_per_row;
     c.window = desc->window;
+    c.k_pool4 = pools.k4;
+    c.v_pool4 = pools.v4;
+    c.out_scale = desc->v_scale;
     c.tile_tokens = 128 / group;
     c.num_tiles = (P + kChunkHalves * c.tile_tokens - 1) / (kChunkHalves * c.tile_tokens);
     c.scale_log2 = scale_log2(desc);

@@ -133,6 +133,9 @@ struct ChunkParams {
   uint16_t* out;              // [P][Hq][D]
   int32_t* status;
   int P, hq, hkv, group, num_pages, num_rows, pages_per_row, window;
+  const uint8_t* k_pool4;     // 4-bit pools; null for bf16 pools (reached through tensor maps)
+  const uint8_t* v_pool4;
+  float out_scale;            // the value scale of 4-bit pools
   int tile_tokens, num_tiles;  // tokens per half tile (128 / group); tiles of kChunkHalves halves
   float scale_log2;
 };

@@ -145,7 +145,7 @@ def test_a_serving_run_over_4_bit_pools_with_forks_and_compaction():
         for layer in range(layers):
             kv, vv = ofp4.pool_values(u8(k_pools[layer]), ks), ofp4.pool_values(u8(v_pools[layer]), vs)
             for b, p in enumerate(positions):
-                check_token(to_bits(outs[layer])[b], to_bits(queries[layer])[b], b, p, host, kv, vv, 0, 2.0 ** -11,
+                check_token(to_bits(outs[layer])[b], to_bits(queries[layer])[b], b, p, host, kv, vv, 0,
                             f"layer {layer} row {b}")
 
     write(1, [0] * 150, list(range(150)))
