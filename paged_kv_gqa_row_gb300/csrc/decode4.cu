@@ -50,8 +50,12 @@ constexpr int kProducerWarp = kWarps;
 constexpr int kEpilogueWarp = kWarps + 1;
 constexpr int kThreads = (kWarps + 2) * 32;
 constexpr int kCtasPerSm = 2;
-constexpr int kStages = 6;  // K + V pages in the ring
-constexpr int kSlots = 2;   // hand-off slots per consumer warp
+// K + V pages in the ring.  A multiple of the warps: page k goes to stage
+// k % kStages and warp k % kWarps, so that every stage belongs to one warp.  (A
+// stage shared by two warps would be waited on by parity from two places: a warp
+// that is ahead could take the phase before the last for the one it waits for.)
+constexpr int kStages = 8;
+static_assert(kStages % kWarps == 0, "a stage's phases are waited for by one warp, in order");
 constexpr int kPairWhole = 1;
 constexpr int kEnd = 2;
 constexpr int kFirst = 4;   // the warp's first page of the segment (the stage has its query rows)
@@ -63,6 +67,7 @@ struct Stage {
 
 template <int D>
 struct Smem {
+  static constexpr int kSlots = D == 128 ? 1 : 2;     // hand-off slots per consumer warp (what fits)
   static constexpr int kPageBytes = 36 * D;
   static constexpr int kStageBytes = 2 * kPageBytes;  // K, then V
   static constexpr int kQBytes = kMaxGroup * D * 2;
@@ -100,6 +105,7 @@ __device__ __forceinline__ uint32_t mix_odd(uint32_t a, uint32_t b) {
 template <int D>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode4_kernel(const DecodeParams p) {
   using L = Smem<D>;
+  constexpr int kSlots = L::kSlots;
   constexpr int KS = D / 16;  // k-steps of Q.K, d-tiles of P.V, blocks of a row
   constexpr int KW = D / 32;  // words of a key row per lane
   extern __shared__ uint8_t smem_raw[];
