@@ -4,17 +4,24 @@
 // decode.cu's (decode_plan.cuh).  What differs is the CTA's inside, because a
 // page of one head is only 36 D bytes of K and of V: at the rate HBM delivers
 // them, an SM has about 390 cycles for the 16384 elements of a page's K and V
-// (D = 128), so the instructions spent per page decide, and everything that is
-// paid per page and warp is paid by ONE warp per page:
-//  * warps 0 .. kWarps - 1, consumers: warp w takes whole pages (64 keys), those
-//    with index w modulo kWarps in the CTA's stream, with an online softmax of
-//    its own; one set of maxima, votes and barriers serves 64 keys;
-//  * producer warp: one lane walks the CTA's page-heads and loads each page's K
-//    and V (two contiguous blocks of 36 D bytes, 1-D bulk copies) into a ring of
-//    stages; a segment's query rows go with the first page that each warp
-//    gets of it;
-//  * epilogue warp: merges the states of the warps that had pages of a segment
-//    (at most min(kWarps, pages) of them) and writes the output or the partial.
+// (D = 128).  So the instructions spent per page decide, every scheduler needs
+// as many warps at work as registers allow, and whatever is paid per page is
+// paid by one warp per page:
+//  * warps 0 .. kWarps - 1, consumers: the CTA's chunk of the stream is cut into
+//    one run of pages per warp, and a warp works through its run alone, page
+//    after page (64 keys), with an online softmax of its own.  A pair that lies
+//    inside a run is finished there, in registers.  What a run has of a longer
+//    pair is a piece: its state waits in shared memory until all warps are done,
+//    and then the whole CTA merges the pieces of each pair, in their order.
+//    (Dealing the pages of a pair out to all warps instead took a merge of 11
+//    states per pair, by one warp, while the others waited: 121 us against 65 on
+//    64 rows of 512 .. 8192 keys.)
+//  * a producer warp, whose lane w feeds consumer w: the lanes walk their
+//    consumers' runs side by side (page table, masks) and load each page's K and
+//    V, two contiguous blocks of 36 D bytes, into the consumer's own ring of
+//    three blocks (K, V, K, V, ... in turn).  One lane for all consumers took
+//    about 1100 cycles a page and held the kernel at 4.2 TB/s.
+// One CTA per SM: its consumers and the producer take the whole register file.
 //
 // Arithmetic.  A code times its block's E4M3 scale has at most five significant
 // bits and lies in f16's range (2^-10 .. 2688), so the converted keys and values
@@ -45,48 +52,45 @@
 namespace lnk {
 namespace {
 
-constexpr int kWarps = 4;  // consumer warps
+constexpr int kWarps = 11;  // consumer warps; with the producer 12: 3 per scheduler at 168 registers
 constexpr int kProducerWarp = kWarps;
-constexpr int kEpilogueWarp = kWarps + 1;
-constexpr int kThreads = (kWarps + 2) * 32;
-constexpr int kCtasPerSm = 2;
-// K + V pages in the ring.  A multiple of the warps: page k goes to stage
-// k % kStages and warp k % kWarps, so that every stage belongs to one warp.  (A
-// stage shared by two warps would be waited on by parity from two places: a warp
-// that is ahead could take the phase before the last for the one it waits for.)
-constexpr int kStages = 8;
-static_assert(kStages % kWarps == 0, "a stage's phases are waited for by one warp, in order");
-constexpr int kPairWhole = 1;
-constexpr int kEnd = 2;
-constexpr int kFirst = 4;   // the warp's first page of the segment (the stage has its query rows)
-constexpr int kLast = 8;    // the warp's last page of the segment
+constexpr int kThreads = (kWarps + 1) * 32;
+constexpr int kRing = 3;    // blocks (a page's K, or its V) in a consumer's ring
+// Page records per consumer.  A page's record is read until its piece is dealt
+// with, after its blocks were freed; page ip + 4 is recorded only once page ip +
+// 2 has been used up.
+constexpr int kPages = 4;
+constexpr int kEnd = 1;
+constexpr int kFirst = 2;  // the piece's first page
+constexpr int kLast = 4;   // the piece's last page
+constexpr int kWhole = 8;  // the piece is its whole pair
+constexpr int kRunEnd = 16;  // the run's last page
+constexpr int kPieces = 2 * kWarps;  // a run's first and last piece
 
-struct Stage {
-  int b, h, klo, khi, flags, seg, nseg, c0, pages;  // pages: of the segment, in this chunk
+struct Page {
+  int b, h, klo, khi, flags;
 };
 
 template <int D>
 struct Smem {
-  static constexpr int kSlots = D == 128 ? 1 : 2;     // hand-off slots per consumer warp (what fits)
-  static constexpr int kPageBytes = 36 * D;
-  static constexpr int kStageBytes = 2 * kPageBytes;  // K, then V
-  static constexpr int kQBytes = kMaxGroup * D * 2;
-  static constexpr int kOStride = D + 4;              // padded staging row
-  static constexpr int kSlotFloats = kMaxGroup * kOStride;
-  static constexpr size_t stages = 0;
-  static constexpr size_t qbuf = stages + size_t(kStages) * kStageBytes;
-  static constexpr size_t ostage = qbuf + size_t(kStages) * kQBytes;          // [kWarps][kSlots][kMaxGroup][kOStride]
-  static constexpr size_t mstage = ostage + size_t(kWarps) * kSlots * kSlotFloats * 4;  // [kWarps][kSlots][kMaxGroup]
-  static constexpr size_t lstage = mstage + size_t(kWarps) * kSlots * kMaxGroup * 4;
-  static constexpr size_t epi = lstage + size_t(kWarps) * kSlots * kMaxGroup * 4;  // [2][kMaxGroup]: max, sum
-  // full[kStages], empty[kStages], slot_full[kWarps][kSlots], slot_empty[kWarps][kSlots]
-  static constexpr size_t bars = epi + 2 * kMaxGroup * 4;
-  static constexpr size_t info = bars + (2 * kStages + 2 * kWarps * kSlots) * sizeof(uint64_t);
-  static constexpr size_t slot_info = info + kStages * sizeof(Stage);
-  static constexpr size_t misc = slot_info + kWarps * kSlots * sizeof(Stage);  // abort, longest pair, warp sums
-  static constexpr size_t pref = misc + (2 + kWarps + 2) * 4;
-  static_assert(kStageBytes % 128 == 0 && kQBytes % 16 == 0 && bars % 8 == 0, "copies land on 16-byte boundaries");
+  static constexpr int kBlock = 36 * D;               // K or V of a page
+  static constexpr int kOStride = D + 4;              // padded row of a warp's state
+  static constexpr int kStateFloats = kMaxGroup * kOStride;
+  static constexpr size_t ring = 0;                                                  // [kWarps][kRing][kBlock]
+  // States of a run's first piece; that of its last piece goes into the warp's
+  // ring, which is free by then.
+  static constexpr size_t state = ring + size_t(kWarps) * kRing * kBlock;            // [kWarps][kMaxGroup][kOStride]
+  static constexpr size_t smax = state + size_t(kWarps) * kStateFloats * 4;          // [kPieces][kMaxGroup]
+  static constexpr size_t ssum = smax + size_t(kPieces) * kMaxGroup * 4;
+  static constexpr size_t bars = ssum + size_t(kPieces) * kMaxGroup * 4;             // full, empty: [kWarps][kRing]
+  static constexpr size_t info = bars + size_t(2 * kWarps * kRing) * sizeof(uint64_t);  // [kWarps][kPages]
+  static constexpr size_t pair = info + size_t(kPages * kWarps) * sizeof(Page);      // [kPieces]: b * Hkv + h, or -1
+  static constexpr size_t misc = pair + kPieces * 4;  // abort, longest pair, warp sums, last arrivals [2]
+  static constexpr size_t pref = misc + (2 + kWarps + 1 + 2) * 4;
+  static_assert(kStateFloats * 4 <= kRing * kBlock, "a state fits the ring");
+  static_assert(kBlock % 128 == 0 && state % 16 == 0 && bars % 8 == 0, "alignment of copies, states and barriers");
   static size_t bytes(int B) { return pref + size_t(B + 1) * 4 + 128; }  // + alignment slack
+  static_assert(pref + size_t(kMaxDecodeRows + 1) * 4 + 128 <= 227 * 1024, "one CTA's shared memory");
 };
 
 __device__ __forceinline__ uint32_t low2(uint32_t h) { return __byte_perm(h, h, 0x1010); }
@@ -103,23 +107,21 @@ __device__ __forceinline__ uint32_t mix_odd(uint32_t a, uint32_t b) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) decode4_kernel(const DecodeParams p) {
+__global__ void __launch_bounds__(kThreads, 1) decode4_kernel(const DecodeParams p) {
   using L = Smem<D>;
-  constexpr int kSlots = L::kSlots;
   constexpr int KS = D / 16;  // k-steps of Q.K, d-tiles of P.V, blocks of a row
   constexpr int KW = D / 32;  // words of a key row per lane
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
-  uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + L::bars);
-  uint64_t* empty_bar = full_bar + kStages;
-  uint64_t* slot_full = empty_bar + kStages;           // [kWarps][kSlots]
-  uint64_t* slot_empty = slot_full + kWarps * kSlots;  // [kWarps][kSlots]
-  Stage* info = reinterpret_cast<Stage*>(smem + L::info);
-  Stage* slot_info = reinterpret_cast<Stage*>(smem + L::slot_info);
-  float* ost = reinterpret_cast<float*>(smem + L::ostage);
-  float* mst = reinterpret_cast<float*>(smem + L::mstage);
-  float* lst = reinterpret_cast<float*>(smem + L::lstage);
-  int* misc = reinterpret_cast<int*>(smem + L::misc);  // [0] abort, [1] longest pair, [2..] warp sums of the scan
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + L::bars);  // [kWarps][kRing]
+  uint64_t* empty_bar = full_bar + kWarps * kRing;
+  Page* info = reinterpret_cast<Page*>(smem + L::info);
+  int* piece_pair = reinterpret_cast<int*>(smem + L::pair);
+  float* state = reinterpret_cast<float*>(smem + L::state);
+  float* smax = reinterpret_cast<float*>(smem + L::smax);
+  float* ssum = reinterpret_cast<float*>(smem + L::ssum);
+  int* misc = reinterpret_cast<int*>(smem + L::misc);  // [0] abort, [1] longest pair, [2..13] warp sums of the scan
+  int* arrived_last = misc + 2 + kWarps + 1;           // [2]: this CTA is the last of its first / last pair's
   volatile int* abort_flag = misc;
   int* pref = reinterpret_cast<int*>(smem + L::pref);
 
@@ -133,17 +135,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode4_kernel(const Dec
   const int B = p.B;
   const int G = p.group;
 
-  if (tid == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(smem_addr(full_bar + s), 1);
-      mbar_init(smem_addr(empty_bar + s), 1);
+  if (tid < kWarps * kRing) {
+    mbar_init(smem_addr(full_bar + tid), 1);
+    mbar_init(smem_addr(empty_bar + tid), 1);
+    if (tid < kPieces) piece_pair[tid] = -1;
+    if (tid == 0) {
+      misc[0] = 0;
+      misc[1] = 0;
     }
-    for (int i = 0; i < kWarps * kSlots; ++i) {
-      mbar_init(smem_addr(slot_full + i), 1);
-      mbar_init(smem_addr(slot_empty + i), 1);
-    }
-    misc[0] = 0;
-    misc[1] = 0;
     fence_mbarrier_init();
   }
 
@@ -184,276 +183,158 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode4_kernel(const Dec
   const long long nchunks = pair_chunks ? pairs : (per > 0 ? (total + per - 1) / per : 0);
   const long long chunk = blockIdx.x;
 
+  long long start, end;  // the chunk's page-heads
+  if (pair_chunks) {
+    const int b = static_cast<int>(chunk / p.hkv), h = static_cast<int>(chunk % p.hkv);
+    const int np = chunk < nchunks ? pref[b + 1] - pref[b] : 0;
+    start = chunk < nchunks ? static_cast<long long>(pref[b]) * p.hkv + static_cast<long long>(h) * np : 0;
+    end = start + np;
+  } else {
+    start = chunk * per;
+    end = min(total, start + per);
+  }
+
   // Wait for the previous kernel on the stream (it writes q and the pools).
   // The producer waits later, right before its first copy.
   if (warp != kProducerWarp) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     // rows with nothing to attend to get a zero output
-    const int zt = warp < kProducerWarp ? tid : tid - 32;
     for (int b = blockIdx.x; b < B; b += gridDim.x) {
       if (pref[b + 1] == pref[b]) {
         uint32_t* o = reinterpret_cast<uint32_t*>(p.out + static_cast<size_t>(b) * p.hq * D);
-        for (int i = zt; i < p.hq * D / 2; i += kThreads - 32) o[i] = 0u;
+        for (int i = tid; i < p.hq * D / 2; i += kWarps * 32) o[i] = 0u;
       }
     }
   }
-  if (chunk >= nchunks) return;
+  if (start >= end) return;
+  const long long n = end - start;
+  // warp w's run of page-heads
+  auto run_begin = [&](int w) { return start + n * w / kWarps; };
 
   if (warp == kProducerWarp) {
     // ============================== producer ==============================
-    if (lane != 0) return;
-    long long start, end;
-    if (pair_chunks) {
-      const int b = static_cast<int>(chunk / p.hkv), h = static_cast<int>(chunk % p.hkv);
-      const int np = pref[b + 1] - pref[b];
-      start = static_cast<long long>(pref[b]) * p.hkv + static_cast<long long>(h) * np;
-      end = start + np;
-    } else {
-      start = chunk * per;
-      end = min(total, start + per);
+    const int w = min(lane, kWarps - 1);
+    uint64_t* full = full_bar + w * kRing;
+    uint64_t* empty = empty_bar + w * kRing;
+    const long long rb = run_begin(w), re = run_begin(w + 1);
+    long long gi = rb;
+    Cursor cur;
+    int entry = 0;  // the page table's entry for page-head gi
+    if (gi < re) {
+      locate(cur, gi, pref, p, start, end, per, chunk);
+      entry = cur.trow[cur.first_page + cur.j];
     }
-    int k = 0;
-    bool stop = false, waited = false;
-    if (start < end) {
-      // ranges in order: the segment shared with the next chunk first, so that
-      // cut pairs finish early
-      Cursor cur;
-      locate(cur, end - 1, pref, p, start, end, per, chunk);
-      const long long last_seg = max(start, end - 1 - cur.j);
-      const bool last_cut = (end - 1 - cur.j) + cur.np > end;
-      const bool two = last_cut && last_seg > start;
-      for (int rg = 0; rg < (two ? 2 : 1) && !stop; ++rg) {
-        const long long rb = two && rg == 0 ? last_seg : start, re = two && rg == 1 ? last_seg : end;
-        locate(cur, rb, pref, p, start, end, per, chunk);
-        int seg_pages = 0, idx = 0;  // pages of the cursor's segment, and its page in it
-        for (long long gi = rb; gi < re; ++gi, ++k) {
-          if (gi == rb || cur.j == 0) {
-            seg_pages = static_cast<int>(min(static_cast<long long>(cur.np - cur.j), re - gi));
-            idx = 0;
+    // on to the next head or row (the lanes cross pairs one at a time, so this
+    // has to be short)
+    auto next_pair = [&]() {
+      cur.j = 0;
+      if (++cur.h < p.hkv) return;
+      cur.h = 0;
+      ++cur.b;
+      if (pref[cur.b + 1] == pref[cur.b]) {  // rows without pages: the first one that has some
+        int lo = cur.b + 1, hi = B - 1;
+        while (lo < hi) {
+          const int mid = (lo + hi) >> 1;
+          if (pref[mid + 1] > pref[cur.b]) hi = mid; else lo = mid + 1;
+        }
+        cur.b = lo;
+      }
+      cur.np = pref[cur.b + 1] - pref[cur.b];
+      cur.pos = p.positions[cur.b];
+      cur.lo = p.window > 0 ? max(0, cur.pos - p.window + 1) : 0;
+      cur.first_page = cur.lo / kPage;
+      cur.trow = p.table + static_cast<long long>(cur.b) * p.pages_per_row;
+    };
+    int blk = 0, round = 0, ip = 0;  // ring block and its use, page of this consumer
+    bool vnext = false;              // the page's V comes next
+    bool done = lane >= kWarps;
+    int page = 0;
+    bool valid = false;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    uint64_t last_ns = global_timer_ns();
+    bool moved_since = false;
+    for (uint32_t it = 1;; ++it) {
+      bool moved = false;
+      // (the lanes poll: none waits for another's consumer)
+      if (!done && (round == 0 || mbar_test_wait(smem_addr(empty + blk), (round - 1) & 1))) {
+        const uint32_t fb = smem_addr(full + blk);
+        const uint32_t dst = smem_addr(smem + L::ring + size_t(w * kRing + blk) * L::kBlock);
+        if (!vnext) {
+          Page& pi = info[w * kPages + ip % kPages];
+          if (gi >= re) {
+            pi.flags = kEnd;
+            mbar_arrive(fb);
+            done = true;
+          } else {
+            page = entry;
+            valid = page >= 0 && page < p.num_pages;
+            const int lp = cur.first_page + cur.j;
+            pi.b = cur.b;
+            pi.h = cur.h;
+            pi.klo = valid ? max(cur.lo - lp * kPage, 0) : 0;
+            pi.khi = valid ? min(cur.pos - lp * kPage + 1, kPage) : 0;
+            const bool first = gi == rb || cur.j == 0;
+            pi.flags = (first ? kFirst : 0) | (gi + 1 == re ? kRunEnd : 0) |
+                       (gi + 1 == re || cur.j + 1 == cur.np ? kLast : 0) |
+                       (gi - cur.j >= rb && gi - cur.j + cur.np <= re ? kWhole : 0);
+            if (!valid && p.status != nullptr) atomicOr(p.status, LNK_DEV_BAD_PAGE);
+            if (first) {  // the piece's query rows, into L1
+              const char* qsrc = reinterpret_cast<const char*>(
+                  p.q + (static_cast<size_t>(cur.b) * p.hq + static_cast<size_t>(cur.h) * G) * D);
+              for (int o = 0; o < G * D * 2; o += 128)
+                asm volatile("prefetch.global.L1 [%0];" ::"l"(reinterpret_cast<uint64_t>(qsrc + o)));
+            }
+            if (valid) {
+              mbar_arrive_expect_tx(fb, L::kBlock);
+              bulk_load(dst, p.k_pool4 + (static_cast<size_t>(cur.h) * p.num_pages + page) * L::kBlock, L::kBlock, fb);
+            } else {
+              mbar_arrive(fb);
+            }
+            vnext = true;
           }
-          const int lp = cur.first_page + cur.j;
-          const int page = cur.trow[lp];
-          const int s = k % kStages;
-          if (k >= kStages && !mbar_wait(smem_addr(empty_bar + s), ((k / kStages) - 1) & 1, abort_flag)) {
-            stop = true;
-            break;
-          }
-          const bool first = idx < kWarps;
-          const bool valid = page >= 0 && page < p.num_pages;
-          Stage si;
-          si.b = cur.b;
-          si.h = cur.h;
-          si.klo = max(cur.lo - lp * kPage, 0);
-          si.khi = min(cur.pos - lp * kPage + 1, kPage);
-          si.flags = (first ? kFirst : 0) | (seg_pages - 1 - idx < kWarps ? kLast : 0) | (cur.whole ? kPairWhole : 0);
-          si.seg = cur.seg;
-          si.nseg = cur.nseg;
-          si.c0 = cur.c0;
-          si.pages = seg_pages;
-          if (!valid) {
-            if (p.status != nullptr) atomicOr(p.status, LNK_DEV_BAD_PAGE);
-            si.klo = si.khi = 0;
-          }
-          info[s] = si;
-          const uint32_t fb = smem_addr(full_bar + s);
-          const uint32_t q_bytes = first ? static_cast<uint32_t>(G * D * 2) : 0u;
-          const uint32_t tx = (valid ? static_cast<uint32_t>(L::kStageBytes) : 0u) + q_bytes;
-          if (tx) mbar_arrive_expect_tx(fb, tx); else mbar_arrive(fb);
-          if (!waited) {  // (the previous kernel writes q and the pools)
-            asm volatile("griddepcontrol.wait;" ::: "memory");
-            waited = true;
-          }
-          if (q_bytes > 0) {
-            const uint16_t* qsrc = p.q + (static_cast<size_t>(cur.b) * p.hq + static_cast<size_t>(cur.h) * G) * D;
-            bulk_load(smem_addr(smem + L::qbuf + size_t(s) * L::kQBytes), qsrc, q_bytes, fb);
-          }
+        } else {
           if (valid) {
-            const uint32_t dst = smem_addr(smem + L::stages + size_t(s) * L::kStageBytes);
-            const size_t at = (static_cast<size_t>(cur.h) * p.num_pages + page) * L::kPageBytes;
-            bulk_load(dst, p.k_pool4 + at, L::kPageBytes, fb);
-            bulk_load(dst + L::kPageBytes, p.v_pool4 + at, L::kPageBytes, fb);
+            mbar_arrive_expect_tx(fb, L::kBlock);
+            bulk_load(dst, p.v_pool4 + (static_cast<size_t>(cur.h) * p.num_pages + page) * L::kBlock, L::kBlock, fb);
+          } else {
+            mbar_arrive(fb);
           }
-          ++idx;
-          if (++cur.j == cur.np && gi + 1 < re) locate(cur, gi + 1, pref, p, start, end, per, chunk);
+          vnext = false;
+          ++ip;
+          // this consumer's next page
+          if (++gi < re) {
+            if (++cur.j == cur.np) next_pair();
+            entry = cur.trow[cur.first_page + cur.j];
+          }
+        }
+        if (++blk == kRing) {
+          blk = 0;
+          ++round;
+        }
+        moved = true;
+      }
+      if (__all_sync(0xffffffffu, done)) break;
+      moved = __any_sync(0xffffffffu, moved);
+      moved_since = moved_since || moved;
+      if (!moved) __nanosleep(32);
+      // bounded: stop when nothing has moved for the waits' limit
+      if ((it & 255u) == 0) {
+        const uint64_t now = __shfl_sync(0xffffffffu, global_timer_ns(), 0);
+        if (moved_since) last_ns = now;
+        moved_since = false;
+        if (__any_sync(0xffffffffu, *abort_flag != 0) || now - last_ns > 2 * kWaitLimitNs) {
+          *abort_flag = 1;
+          break;
         }
       }
-    }
-    if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
-    // the end of the work: a stage without data for every consumer warp
-    for (int w = 0; w < kWarps && !stop; ++w, ++k) {
-      const int s = k % kStages;
-      if (k >= kStages && !mbar_wait(smem_addr(empty_bar + s), ((k / kStages) - 1) & 1, abort_flag)) {
-        stop = true;  // the consumers stop on the abort flag
-        break;
-      }
-      Stage si{};
-      si.flags = kEnd;
-      info[s] = si;
-      mbar_arrive(smem_addr(full_bar + s));
     }
     // Drain: do not leave the CTA while a copy may still land in its memory.
-    for (int kk = max(0, k - kStages); kk < k; ++kk) {
-      const uint32_t fb = smem_addr(full_bar + kk % kStages);
-      const uint64_t t0 = global_timer_ns();
-      while (!mbar_try_wait(fb, (kk / kStages) & 1) && global_timer_ns() - t0 < kWaitLimitNs) {
-      }
-    }
-    if (*abort_flag && p.status != nullptr) atomicOr(p.status, LNK_DEV_TIMEOUT);
-    return;
-  }
-
-  if (warp == kEpilogueWarp) {
-    // ============================== epilogue ==============================
-    float* eml = reinterpret_cast<float*>(smem + L::epi);  // [2][kMaxGroup]: max, sum per head
-    constexpr int D4 = D / 4;
-    int seq = 0;    // lane w: segments taken from consumer warp w
-    int first = 0;  // consumer warp with the next segment's first page
-    for (;;) {
-      const int n0 = __shfl_sync(0xffffffffu, seq, first);
-      if (!__all_sync(0xffffffffu, mbar_wait(smem_addr(slot_full + first * kSlots + n0 % kSlots), (n0 / kSlots) & 1,
-                                             abort_flag)))
-        break;
-      const Stage si = slot_info[first * kSlots + n0 % kSlots];
-      if (si.flags & kEnd) break;
-      const int nw = min(kWarps, si.pages);  // warps with pages of the segment: first, first + 1, ...
-      bool ok = true;
-      int slot_of[kWarps];  // their hand-off slots
-#pragma unroll
-      for (int i = 0; i < kWarps; ++i) {
-        const int w = (first + i) % kWarps;
-        const int n = __shfl_sync(0xffffffffu, seq, w);
-        slot_of[i] = w * kSlots + n % kSlots;
-        if (i > 0 && i < nw)
-          ok = ok && __all_sync(0xffffffffu, mbar_wait(smem_addr(slot_full + slot_of[i]), (n / kSlots) & 1, abort_flag));
-      }
-      if (!ok) break;
-      const bool whole = (si.flags & kPairWhole) != 0;
-      uint16_t* out_pair = p.out + (static_cast<size_t>(si.b) * p.hq + static_cast<size_t>(si.h) * G) * D;
-      const int q = si.b * p.hkv + si.h;
-      // per head: merged max and sum of the warps
-      if (lane < G) {
-        float M = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < kWarps; ++i)
-          if (i < nw) M = fmaxf(M, mst[slot_of[i] * kMaxGroup + lane]);
-        float Ls = 0.f;
-        if (M != -INFINITY) {
-#pragma unroll
-          for (int i = 0; i < kWarps; ++i) {
-            if (i >= nw) continue;
-            const float mw = mst[slot_of[i] * kMaxGroup + lane];
-            if (mw != -INFINITY) Ls += lst[slot_of[i] * kMaxGroup + lane] * exp2f(mw - M);
-          }
-        }
-        eml[lane] = M;
-        eml[kMaxGroup + lane] = Ls;
-      }
-      __syncwarp();
-      for (int it = lane; it < G * D4; it += 32) {
-        const int g = it / D4, d = (it % D4) * 4;
-        const float M = eml[g], Ls = eml[kMaxGroup + g];
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (M != -INFINITY) {
-#pragma unroll
-          for (int i = 0; i < kWarps; ++i) {
-            if (i >= nw) continue;
-            const float mw = mst[slot_of[i] * kMaxGroup + g];
-            const float f = mw == -INFINITY ? 0.f : exp2f(mw - M);
-            const float4 v = *reinterpret_cast<const float4*>(ost + size_t(slot_of[i]) * L::kSlotFloats + g * L::kOStride + d);
-            acc.x += v.x * f;
-            acc.y += v.y * f;
-            acc.z += v.z * f;
-            acc.w += v.w * f;
-          }
-        }
-        if (whole) {
-          const float inv = Ls > 0.f ? p.out_scale / Ls : 0.f;
-          uint2 pk;
-          pk.x = pack_bf16x2(acc.x * inv, acc.y * inv);
-          pk.y = pack_bf16x2(acc.z * inv, acc.w * inv);
-          *reinterpret_cast<uint2*>(out_pair + g * D + d) = pk;
-        } else {
-          *reinterpret_cast<float4*>(p.ws_o + (static_cast<size_t>(si.seg) * G + g) * D + d) = acc;
-          if (d == 0) {
-            p.ws_ml[(static_cast<size_t>(si.seg) * G + g) * 2 + 0] = M;
-            p.ws_ml[(static_cast<size_t>(si.seg) * G + g) * 2 + 1] = Ls;
-          }
-        }
-      }
-      __syncwarp();
-      // the warps' slots are consumed
-      {
-        const int i = (lane - first + kWarps) % kWarps;
-        if (lane < kWarps && i < nw) {
-          mbar_arrive(smem_addr(slot_empty + lane * kSlots + seq % kSlots));
-          ++seq;
-        }
-      }
-      first = (first + si.pages) % kWarps;
-      if (!whole) {
-        // publish the partial, then count the pair's finished segments
-        __threadfence();
-        __syncwarp();
-        int last = 0;
-        if (lane == 0) {
-          const int old = atomicAdd(p.ws_count + q, 1);
-          last = old == si.nseg - 1;
-          if (last) p.ws_count[q] = 0;  // ready for the next call
-        }
-        last = __shfl_sync(0xffffffffu, last, 0);
-        if (last) {
-          __threadfence();
-          const size_t seg0 = static_cast<size_t>(q + si.c0);
-          const int nsg = si.nseg;
-          // pass 1: per head, online max and sum over the pair's segments; lane
-          // handles head lane % G of segments lane / G, lane / G + 32 / G, ...
-          float rm = -INFINITY, rl = 0.f;
-          for (int i = lane; i < nsg * G; i += 32) {
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.ws_ml) + seg0 * G + i);
-            if (ml.x != -INFINITY) {
-              const float mn = fmaxf(rm, ml.x);
-              rl = rl * exp2f(rm - mn) + ml.y * exp2f(ml.x - mn);
-              rm = mn;
-            }
-          }
-          for (int off = G; off < 32; off <<= 1) {
-            const float om = __shfl_xor_sync(0xffffffffu, rm, off);
-            const float ol = __shfl_xor_sync(0xffffffffu, rl, off);
-            const float mn = fmaxf(rm, om);
-            if (mn != -INFINITY) {
-              rl = (rm == -INFINITY ? 0.f : rl * exp2f(rm - mn)) + (om == -INFINITY ? 0.f : ol * exp2f(om - mn));
-              rm = mn;
-            }
-          }
-          __syncwarp();
-          if (lane < G) {
-            eml[lane] = rm;
-            eml[kMaxGroup + lane] = rl;
-          }
-          __syncwarp();
-          // pass 2: weighted sum of the partial outputs (independent loads)
-          for (int it = lane; it < G * D4; it += 32) {
-            const int g = it / D4, d = (it % D4) * 4;
-            const float M = eml[g], Ls = eml[kMaxGroup + g];
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (M != -INFINITY) {
-              for (int sg = 0; sg < nsg; ++sg) {
-                const size_t row = (seg0 + sg) * G + g;
-                const float mseg = __ldcg(p.ws_ml + row * 2);
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(p.ws_o + row * D + d));
-                const float f = mseg == -INFINITY ? 0.f : exp2f(mseg - M);
-                acc.x += v.x * f;
-                acc.y += v.y * f;
-                acc.z += v.z * f;
-                acc.w += v.w * f;
-              }
-            }
-            const float inv = Ls > 0.f ? p.out_scale / Ls : 0.f;
-            uint2 pk;
-            pk.x = pack_bf16x2(acc.x * inv, acc.y * inv);
-            pk.y = pack_bf16x2(acc.z * inv, acc.w * inv);
-            *reinterpret_cast<uint2*>(out_pair + g * D + d) = pk;
-          }
+    if (lane < kWarps) {
+      for (int i = 0; i < kRing; ++i) {  // the last use of each block
+        const int uses = round + (i < blk ? 1 : 0);
+        if (uses == 0) continue;
+        const uint64_t t1 = global_timer_ns();
+        while (!mbar_try_wait(smem_addr(full + i), (uses - 1) & 1) && global_timer_ns() - t1 < kWaitLimitNs) {
         }
       }
     }
@@ -468,26 +349,26 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode4_kernel(const Dec
   // blocks of this lane's key dimensions, and of its value dimensions
   const int kb = (c * KW) / 2;
   const int vb = D == 128 ? r : r / 2;
+  // where a piece's state lies: the run's first in its slot, the last in the ring
+  auto piece_state = [&](int i) {
+    return i & 1 ? reinterpret_cast<const float*>(smem + L::ring + size_t(i >> 1) * kRing * L::kBlock)
+                 : state + size_t(i >> 1) * L::kStateFloats;
+  };
+  uint64_t* full = full_bar + warp * kRing;
+  uint64_t* empty = empty_bar + warp * kRing;
+  const uint8_t* ring = smem + L::ring + size_t(warp) * kRing * L::kBlock;
   uint32_t qf[KS][2];
   float o[KS][4];
   float m_a = -INFINITY, m_b = -INFINITY, l_a = 0.f, l_b = 0.f;  // heads 2c, 2c + 1
-  int nslot = 0;
+  int blk = 0, phase = 0;  // the next block of the ring, and its phase
 
-  for (int k = warp;; k += kWarps) {
-    const int s = k % kStages;
-    if (!__all_sync(0xffffffffu, mbar_wait(smem_addr(full_bar + s), (k / kStages) & 1, abort_flag))) break;
-    const Stage si = info[s];
-    const int slot = warp * kSlots + nslot % kSlots;
-    if (si.flags & kEnd) {  // pass the end on to the epilogue
-      if (!__all_sync(0xffffffffu, mbar_wait(smem_addr(slot_empty + slot), ((nslot / kSlots) & 1) ^ 1, abort_flag))) break;
-      if (lane == 0) {
-        slot_info[slot] = si;
-        mbar_arrive(smem_addr(slot_full + slot));
-      }
-      break;
-    }
-    if (si.flags & kFirst) {
-      const uint16_t* qs = reinterpret_cast<const uint16_t*>(smem + L::qbuf + size_t(s) * L::kQBytes) + r * D + c * (D / 4);
+  for (int ip = 0;; ++ip) {
+    if (!__all_sync(0xffffffffu, mbar_wait(smem_addr(full + blk), phase, abort_flag))) break;
+    const Page& pi = info[warp * kPages + ip % kPages];
+    const int flags = pi.flags, klo = pi.klo, khi = pi.khi;
+    if (flags & kEnd) break;
+    if (flags & kFirst) {
+      const uint16_t* qs = p.q + (static_cast<size_t>(pi.b) * p.hq + static_cast<size_t>(pi.h) * G + r) * D + c * (D / 4);
 #pragma unroll
       for (int kk = 0; kk < KS; ++kk) {  // dimensions c D/4 + 4 kk .. + 3 of head r
         const uint2 w = r < G ? *reinterpret_cast<const uint2*>(qs + 4 * kk) : make_uint2(0u, 0u);
@@ -499,11 +380,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode4_kernel(const Dec
       m_a = m_b = -INFINITY;
       l_a = l_b = 0.f;
     }
-    const bool work = si.khi > si.klo;
+    const bool work = khi > klo;
+    const bool partial = klo > 0 || khi < kPage;
+    const uint8_t* kp = ring + blk * L::kBlock;
+    const int kblk = blk;
+    if (++blk == kRing) {
+      blk = 0;
+      phase ^= 1;
+    }
+    const uint8_t* vp = ring + blk * L::kBlock;
+    uint32_t pb[4][2];  // P^T, keys in the order of the value pairs
     if (work) {
-      const uint8_t* kp = smem + L::stages + size_t(s) * L::kStageBytes;
-      const uint8_t* vp = kp + L::kPageBytes;
-      const bool partial = si.klo > 0 || si.khi < kPage;
       // ---- S^T = K Q^T ----
       float sc[4][4];
 #pragma unroll
@@ -534,6 +421,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode4_kernel(const Dec
             for (int x = 0; x < KW; ++x) kw[i][x] = reinterpret_cast<const uint32_t*>(src)[x];
           }
         }
+        // the keys are in registers: their block may be loaded again
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(empty + kblk));
 #pragma unroll
         for (int x = 0; x < KW; ++x) {
 #pragma unroll
@@ -563,21 +453,21 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode4_kernel(const Dec
       for (int t = 0; t < 4; ++t) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          sc[t][i] *= p.scale_log2;
           if (partial) {
             const int key = 16 * t + 8 * (i >> 1) + kperm;
-            if (key < si.klo || key >= si.khi) sc[t][i] = -INFINITY;
+            if (key < klo || key >= khi) sc[t][i] = -INFINITY;
           }
         }
-        mx_a = fmaxf(mx_a, fmaxf(sc[t][0], sc[t][2]));
-        mx_b = fmaxf(mx_b, fmaxf(sc[t][1], sc[t][3]));
+        mx_a = fmax3(mx_a, sc[t][0], sc[t][2]);
+        mx_b = fmax3(mx_b, sc[t][1], sc[t][3]);
       }
 #pragma unroll
       for (int off = 4; off < 32; off <<= 1) {
         mx_a = fmaxf(mx_a, __shfl_xor_sync(0xffffffffu, mx_a, off));
         mx_b = fmaxf(mx_b, __shfl_xor_sync(0xffffffffu, mx_b, off));
       }
-      const float mn_a = fmaxf(m_a, mx_a), mn_b = fmaxf(m_b, mx_b);
+      // (the scale is positive: the largest product is the largest score's)
+      const float mn_a = fmaxf(m_a, mx_a * p.scale_log2), mn_b = fmaxf(m_b, mx_b * p.scale_log2);
       const bool same_max = __all_sync(0xffffffffu, mn_a == m_a && mn_b == m_b);
       const float base_a = mn_a == -INFINITY ? 0.f : mn_a;
       const float base_b = mn_b == -INFINITY ? 0.f : mn_b;
@@ -595,16 +485,24 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode4_kernel(const Dec
       }
       m_a = mn_a;
       m_b = mn_b;
-      uint32_t pb[4][2];  // P^T, keys in the order of the value pairs
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        const float p0 = ex2_approx(sc[t][0] - base_a), p1 = ex2_approx(sc[t][1] - base_b);
-        const float p2 = ex2_approx(sc[t][2] - base_a), p3 = ex2_approx(sc[t][3] - base_b);
+        const float p0 = ex2_approx(fmaf(sc[t][0], p.scale_log2, -base_a));
+        const float p1 = ex2_approx(fmaf(sc[t][1], p.scale_log2, -base_b));
+        const float p2 = ex2_approx(fmaf(sc[t][2], p.scale_log2, -base_a));
+        const float p3 = ex2_approx(fmaf(sc[t][3], p.scale_log2, -base_b));
         l_a += p0 + p2;
         l_b += p1 + p3;
         pb[t][0] = movmatrix_trans(pack_f16x2(p0, p1));
         pb[t][1] = movmatrix_trans(pack_f16x2(p2, p3));
       }
+    }
+    if (!work) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(empty + kblk));
+    }
+    if (!__all_sync(0xffffffffu, mbar_wait(smem_addr(full + blk), phase, abort_flag))) break;
+    if (work) {
       // ---- O^T += V^T P^T ----
       // scales of keys c + 4 i in pairs (i, i + 1), for the lane's blocks; zero where masked
       constexpr int NVB = D == 96 ? 2 : 1;
@@ -618,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode4_kernel(const Dec
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const int key = c + 4 * i;
-            if (key < si.klo || key >= si.khi) ww[i >> 2] &= ~(0xFFu << (8 * (i & 3)));
+            if (key < klo || key >= khi) ww[i >> 2] &= ~(0xFFu << (8 * (i & 3)));
           }
         }
         e4m3x4_to_f16x2x2(w.x, vs[n][0], vs[n][1]);
@@ -669,38 +567,187 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode4_kernel(const Dec
       }
     }
     __syncwarp();
-    if (lane == 0) mbar_arrive(smem_addr(empty_bar + s));
+    if (lane == 0) mbar_arrive(smem_addr(empty + blk));
+    if (++blk == kRing) {
+      blk = 0;
+      phase ^= 1;
+    }
+    if (!(flags & kLast)) continue;
 
-    if (si.flags & kLast) {
-      // ---- hand this warp's state for the segment to the epilogue ----
-      float la = l_a, lb = l_b;
+    float la = l_a, lb = l_b;
 #pragma unroll
-      for (int off = 4; off < 32; off <<= 1) {
-        la += __shfl_xor_sync(0xffffffffu, la, off);
-        lb += __shfl_xor_sync(0xffffffffu, lb, off);
-      }
-      if (!__all_sync(0xffffffffu, mbar_wait(smem_addr(slot_empty + slot), ((nslot / kSlots) & 1) ^ 1, abort_flag))) break;
-      if (lane < 4) {
-        mst[slot * kMaxGroup + 2 * c] = m_a;
-        mst[slot * kMaxGroup + 2 * c + 1] = m_b;
-        lst[slot * kMaxGroup + 2 * c] = la;
-        lst[slot * kMaxGroup + 2 * c + 1] = lb;
-      }
-      if (lane == 0) slot_info[slot] = si;
-      float* oa = ost + size_t(slot) * L::kSlotFloats + (2 * c) * L::kOStride;
-      float* ob = oa + L::kOStride;
+    for (int off = 4; off < 32; off <<= 1) {
+      la += __shfl_xor_sync(0xffffffffu, la, off);
+      lb += __shfl_xor_sync(0xffffffffu, lb, off);
+    }
+    const int ob = pi.b, oh = pi.h;
+    if (flags & kWhole) {
+      // ---- a whole pair: this lane's dimensions of heads 2c and 2c + 1 ----
+      const float ia = la > 0.f ? p.out_scale / la : 0.f, ib = lb > 0.f ? p.out_scale / lb : 0.f;
+      uint16_t* oa = p.out + (static_cast<size_t>(ob) * p.hq + static_cast<size_t>(oh) * G + 2 * c) * D;
 #pragma unroll
       for (int dt = 0; dt < KS; dt += 2) {
-        // d-tiles dt, dt + 1: four consecutive dimensions
-        int d;
-        if constexpr (D == 128) d = 16 * r + 2 * dt;
-        else d = dt < 4 ? 8 * r + 2 * dt : 64 + 4 * r;
-        *reinterpret_cast<float4*>(oa + d) = make_float4(o[dt][0], o[dt][2], o[dt + 1][0], o[dt + 1][2]);
-        *reinterpret_cast<float4*>(ob + d) = make_float4(o[dt][1], o[dt][3], o[dt + 1][1], o[dt + 1][3]);
+        const int d = D == 128 ? 16 * r + 2 * dt : (dt < 4 ? 8 * r + 2 * dt : 64 + 4 * r);
+        if (2 * c < G)
+          *reinterpret_cast<uint2*>(oa + d) = make_uint2(pack_bf16x2(o[dt][0] * ia, o[dt][2] * ia),
+                                                         pack_bf16x2(o[dt + 1][0] * ia, o[dt + 1][2] * ia));
+        if (2 * c + 1 < G)
+          *reinterpret_cast<uint2*>(oa + D + d) = make_uint2(pack_bf16x2(o[dt][1] * ib, o[dt][3] * ib),
+                                                             pack_bf16x2(o[dt + 1][1] * ib, o[dt + 1][3] * ib));
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(slot_full + slot));
-      ++nslot;
+      continue;
+    }
+    // ---- a piece of a longer pair: its state into shared memory ----
+    const int piece = 2 * warp + (flags & kRunEnd ? 1 : 0);
+    if (lane < 4) {
+      smax[piece * kMaxGroup + 2 * c] = m_a;
+      smax[piece * kMaxGroup + 2 * c + 1] = m_b;
+      ssum[piece * kMaxGroup + 2 * c] = la;
+      ssum[piece * kMaxGroup + 2 * c + 1] = lb;
+    }
+    if (lane == 0) piece_pair[piece] = ob * p.hkv + oh;
+    float* oa = const_cast<float*>(piece_state(piece)) + (2 * c) * L::kOStride;
+#pragma unroll
+    for (int dt = 0; dt < KS; dt += 2) {
+      // d-tiles dt, dt + 1: four consecutive dimensions
+      const int d = D == 128 ? 16 * r + 2 * dt : (dt < 4 ? 8 * r + 2 * dt : 64 + 4 * r);
+      *reinterpret_cast<float4*>(oa + d) = make_float4(o[dt][0], o[dt][2], o[dt + 1][0], o[dt + 1][2]);
+      *reinterpret_cast<float4*>(oa + L::kOStride + d) = make_float4(o[dt][1], o[dt][3], o[dt + 1][1], o[dt + 1][3]);
+    }
+  }
+
+  // ================= all runs are done: merge the pieces ==================
+  // (every consumer warp comes here, whatever ended its loop)
+  constexpr int kAll = kWarps * 32;
+  named_barrier_sync(1, kAll);
+  // Pieces of one pair are neighbours.  Bit i: piece i is there / begins a pair.
+  const int mine = lane < kPieces ? piece_pair[lane] : -1;
+  const unsigned there = __ballot_sync(0xffffffffu, mine >= 0);
+  const unsigned before = there & ((1u << lane) - 1u);
+  const int prev = __shfl_sync(0xffffffffu, mine, before ? 31 - __clz(before) : 0);
+  const unsigned heads = __ballot_sync(0xffffffffu, mine >= 0 && (before == 0u || prev != mine));
+  const int npairs = __popc(heads);
+  constexpr int D4 = D / 4;
+  const int items = G * D4;
+  bool cut = false;  // some pair goes on in another CTA
+  {
+    unsigned rest = heads;
+    for (int gidx = 0; gidx < npairs; ++gidx) {
+      const int at = __ffs(rest) - 1;
+      rest &= rest - 1;
+      const unsigned mask = there & (rest ? (1u << (__ffs(rest) - 1)) - (1u << at) : ~0u << at);
+      const int q = piece_pair[at], b = q / p.hkv, h = q % p.hkv;
+      const int np = pref[b + 1] - pref[b];
+      const long long pair_start = static_cast<long long>(pref[b]) * p.hkv + static_cast<long long>(h) * np;
+      const bool whole = pair_start >= start && pair_start + np <= end;
+      cut = cut || !whole;
+      // the CTA's threads take the pair's outputs, four dimensions each, in turn
+      // with the other pairs'
+      for (int it = (tid + kAll - gidx * items % kAll) % kAll; it < items; it += kAll) {
+        const int g = it / D4, d = (it % D4) * 4;
+        float M = -INFINITY;
+        for (unsigned m = mask; m; m &= m - 1) M = fmaxf(M, smax[(__ffs(m) - 1) * kMaxGroup + g]);
+        float Ls = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (M != -INFINITY) {
+          for (unsigned m = mask; m; m &= m - 1) {
+            const int i = __ffs(m) - 1;
+            const float mw = smax[i * kMaxGroup + g];
+            const float f = mw == -INFINITY ? 0.f : exp2f(mw - M);
+            const float4 v = *reinterpret_cast<const float4*>(piece_state(i) + g * L::kOStride + d);
+            Ls += ssum[i * kMaxGroup + g] * f;
+            acc.x += v.x * f;
+            acc.y += v.y * f;
+            acc.z += v.z * f;
+            acc.w += v.w * f;
+          }
+        }
+        if (whole) {
+          const float inv = Ls > 0.f ? p.out_scale / Ls : 0.f;
+          uint16_t* out = p.out + (static_cast<size_t>(b) * p.hq + static_cast<size_t>(h) * G + g) * D + d;
+          *reinterpret_cast<uint2*>(out) =
+              make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+        } else {  // the partial's place in the workspace: pair + chunk
+          const size_t row = (static_cast<size_t>(q) + chunk) * G + g;
+          *reinterpret_cast<float4*>(p.ws_o + row * D + d) = acc;
+          if (d == 0) *reinterpret_cast<float2*>(p.ws_ml + row * 2) = make_float2(M, Ls);
+        }
+      }
+    }
+  }
+  if (cut) {
+    // ---- pairs shared with other CTAs (the chunk's first pair, its last pair):
+    // publish the partials, count the pair's finished chunks; the last CTA merges ----
+    __threadfence();
+    named_barrier_sync(1, kAll);
+    const int ends[2] = {piece_pair[__ffs(heads) - 1], piece_pair[31 - __clz(heads)]};
+    auto shared_pair = [&](int which, int& c0, int& nseg) {
+      if (which == 1 && npairs == 1) return false;
+      const int q = ends[which], b = q / p.hkv, h = q % p.hkv;
+      const int np = pref[b + 1] - pref[b];
+      const long long pair_start = static_cast<long long>(pref[b]) * p.hkv + static_cast<long long>(h) * np;
+      if (pair_start >= start && pair_start + np <= end) return false;
+      c0 = static_cast<int>(pair_start / per);  // the chunk with the pair's first page
+      nseg = static_cast<int>((pair_start + np - 1) / per) - c0 + 1;
+      return true;
+    };
+    if (tid < 2) {
+      int c0, nseg, last = 0;
+      if (shared_pair(tid, c0, nseg)) {
+        last = atomicAdd(p.ws_count + ends[tid], 1) == nseg - 1;
+        if (last) p.ws_count[ends[tid]] = 0;  // ready for the next call
+      }
+      arrived_last[tid] = last;
+    }
+    named_barrier_sync(1, kAll);
+    for (int which = 0; which < 2; ++which) {
+      if (!arrived_last[which]) continue;
+      int c0 = 0, nseg = 0;
+      shared_pair(which, c0, nseg);
+      __threadfence();
+      const int q = ends[which];
+      const size_t seg0 = static_cast<size_t>(q) + c0;
+      for (int it = tid; it < items; it += kAll) {
+        const int g = it / D4, d = (it % D4) * 4;
+        float M = -INFINITY, Ls = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        constexpr int kAtOnce = 8;
+        for (int s0 = 0; s0 < nseg; s0 += kAtOnce) {  // partials in their order, several loads in flight
+          float2 ml[kAtOnce];
+          float4 v[kAtOnce];
+#pragma unroll
+          for (int u = 0; u < kAtOnce; ++u) {
+            const size_t row = (seg0 + min(s0 + u, nseg - 1)) * G + g;
+            ml[u] = __ldcg(reinterpret_cast<const float2*>(p.ws_ml) + row);
+            v[u] = __ldcg(reinterpret_cast<const float4*>(p.ws_o + row * D + d));
+          }
+          float mn = M;
+#pragma unroll
+          for (int u = 0; u < kAtOnce; ++u)
+            if (s0 + u < nseg) mn = fmaxf(mn, ml[u].x);
+          if (mn == -INFINITY) continue;
+          const float f0 = M == -INFINITY ? 0.f : exp2f(M - mn);
+          Ls *= f0;
+          acc.x *= f0;
+          acc.y *= f0;
+          acc.z *= f0;
+          acc.w *= f0;
+#pragma unroll
+          for (int u = 0; u < kAtOnce; ++u) {
+            const float f = s0 + u < nseg && ml[u].x != -INFINITY ? exp2f(ml[u].x - mn) : 0.f;
+            Ls += ml[u].y * f;
+            acc.x += v[u].x * f;
+            acc.y += v[u].y * f;
+            acc.z += v[u].z * f;
+            acc.w += v[u].w * f;
+          }
+          M = mn;
+        }
+        const float inv = Ls > 0.f ? p.out_scale / Ls : 0.f;
+        uint16_t* out = p.out + (static_cast<size_t>(q / p.hkv) * p.hq + static_cast<size_t>(q % p.hkv) * G + g) * D + d;
+        *reinterpret_cast<uint2*>(out) =
+            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+      }
     }
   }
   if (*abort_flag && lane == 0 && p.status != nullptr) atomicOr(p.status, LNK_DEV_TIMEOUT);
@@ -728,10 +775,7 @@ cudaError_t prepare_t(int B, DecodeLaunch* launch) {
   cudaError_t err = set_max_dynamic_smem(fn, static_cast<int>(bytes));
   if (err != cudaSuccess) return err;
   launch->smem_bytes = static_cast<int>(bytes);
-  int per_sm = 1;  // two CTAs per SM when they fit (shared memory grows with B)
-  err = occupancy_blocks(&per_sm, fn, kThreads, bytes);
-  if (err != cudaSuccess) return err;
-  launch->grid = device_sm_count() * (per_sm >= kCtasPerSm ? kCtasPerSm : 1);
+  launch->grid = device_sm_count();
   launch->mode = 0;
   return cudaSuccess;
 }
