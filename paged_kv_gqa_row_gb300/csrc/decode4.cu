@@ -85,8 +85,8 @@ struct Smem {
   static constexpr size_t bars = ssum + size_t(kPieces) * kMaxGroup * 4;             // full, empty: [kWarps][kRing]
   static constexpr size_t info = bars + size_t(2 * kWarps * kRing) * sizeof(uint64_t);  // [kWarps][kPages]
   static constexpr size_t pair = info + size_t(kPages * kWarps) * sizeof(Page);      // [kPieces]: b * Hkv + h, or -1
-  static constexpr size_t misc = pair + kPieces * 4;  // abort, longest pair, warp sums, last arrivals [2]
-  static constexpr size_t pref = misc + (2 + kWarps + 1 + 2) * 4;
+  static constexpr size_t misc = pair + kPieces * 4;  // abort, longest pair, warp sums, last arrivals [2], shared pairs [2][3]
+  static constexpr size_t pref = misc + (2 + kWarps + 1 + 2 + 6) * 4;
   static_assert(kStateFloats * 4 <= kRing * kBlock, "a state fits the ring");
   static_assert(kBlock % 128 == 0 && state % 16 == 0 && bars % 8 == 0, "alignment of copies, states and barriers");
   static size_t bytes(int B) { return pref + size_t(B + 1) * 4 + 128; }  // + alignment slack
@@ -122,6 +122,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode4_kernel(const DecodeParams
   float* ssum = reinterpret_cast<float*>(smem + L::ssum);
   int* misc = reinterpret_cast<int*>(smem + L::misc);  // [0] abort, [1] longest pair, [2..13] warp sums of the scan
   int* arrived_last = misc + 2 + kWarps + 1;           // [2]: this CTA is the last of its first / last pair's
+  int* shared = arrived_last + 2;                      // [2][3]: the chunk's first and last pair (below)
   volatile int* abort_flag = misc;
   int* pref = reinterpret_cast<int*>(smem + L::pref);
 
@@ -194,22 +195,37 @@ __global__ void __launch_bounds__(kThreads, 1) decode4_kernel(const DecodeParams
     end = min(total, start + per);
   }
 
-  // Wait for the previous kernel on the stream (it writes q and the pools).
-  // The producer waits later, right before its first copy.
-  if (warp != kProducerWarp) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    // rows with nothing to attend to get a zero output
+  // rows with nothing to attend to get a zero output, once the previous kernel
+  // on the stream is done
+  auto zero_rows = [&]() {
     for (int b = blockIdx.x; b < B; b += gridDim.x) {
       if (pref[b + 1] == pref[b]) {
         uint32_t* o = reinterpret_cast<uint32_t*>(p.out + static_cast<size_t>(b) * p.hq * D);
         for (int i = tid; i < p.hq * D / 2; i += kWarps * 32) o[i] = 0u;
       }
     }
+  };
+  if (start >= end) {
+    if (warp != kProducerWarp) {
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      zero_rows();
+    }
+    return;
   }
-  if (start >= end) return;
   const long long n = end - start;
   // warp w's run of page-heads
   auto run_begin = [&](int w) { return start + n * w / kWarps; };
+
+  // The pairs of the chunk's first and last page-head, where other chunks have
+  // pages of them too: pair, first chunk, chunks (0: not shared).
+  if (tid < 2) {
+    Cursor e;
+    locate(e, tid == 0 ? start : end - 1, pref, p, start, end, per, chunk);
+    const int q = e.b * p.hkv + e.h;
+    shared[tid * 3] = q;
+    shared[tid * 3 + 1] = e.c0;
+    shared[tid * 3 + 2] = e.whole || (tid == 1 && end - 1 - e.j <= start) ? 0 : e.nseg;
+  }
 
   if (warp == kProducerWarp) {
     // ============================== producer ==============================
@@ -362,356 +378,353 @@ __global__ void __launch_bounds__(kThreads, 1) decode4_kernel(const DecodeParams
   float m_a = -INFINITY, m_b = -INFINITY, l_a = 0.f, l_b = 0.f;  // heads 2c, 2c + 1
   int blk = 0, phase = 0;  // the next block of the ring, and its phase
 
-  for (int ip = 0;; ++ip) {
-    if (!__all_sync(0xffffffffu, mbar_wait(smem_addr(full + blk), phase, abort_flag))) break;
-    const Page& pi = info[warp * kPages + ip % kPages];
-    const int flags = pi.flags, klo = pi.klo, khi = pi.khi;
-    if (flags & kEnd) break;
-    if (flags & kFirst) {
-      const uint16_t* qs = p.q + (static_cast<size_t>(pi.b) * p.hq + static_cast<size_t>(pi.h) * G + r) * D + c * (D / 4);
+  // four outputs of head g of pair q (pairs are in the order of the output's heads)
+  auto store_out = [&](int q, int g, int d, const float4& acc, float sum) {
+    const float inv = sum > 0.f ? p.out_scale / sum : 0.f;
+    *reinterpret_cast<uint2*>(p.out + (static_cast<size_t>(q) * G + g) * D + d) =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  };
+  constexpr int kAll = kWarps * 32;
+  constexpr int D4 = D / 4;
+
+  // Two passes: the real one, and before it, while the previous kernel on the
+  // stream still runs, a dry one of the final phase that stores nothing.  It
+  // brings that phase's code into the instruction cache: met for the first time
+  // at the end, it took 3.3 us for 2 us' less work.
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+    const bool dry = pass == 0;
+    if (!dry) {
+      // (the previous kernel writes q and the pools)
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      zero_rows();
+    for (int ip = 0;; ++ip) {
+      if (!__all_sync(0xffffffffu, mbar_wait(smem_addr(full + blk), phase, abort_flag))) break;
+      const Page& pi = info[warp * kPages + ip % kPages];
+      const int flags = pi.flags, klo = pi.klo, khi = pi.khi;
+      if (flags & kEnd) break;
+      if (flags & kFirst) {
+        const uint16_t* qs = p.q + (static_cast<size_t>(pi.b) * p.hq + static_cast<size_t>(pi.h) * G + r) * D + c * (D / 4);
 #pragma unroll
-      for (int kk = 0; kk < KS; ++kk) {  // dimensions c D/4 + 4 kk .. + 3 of head r
-        const uint2 w = r < G ? *reinterpret_cast<const uint2*>(qs + 4 * kk) : make_uint2(0u, 0u);
-        qf[kk][0] = bf16x2_to_f16x2(w.x);
-        qf[kk][1] = bf16x2_to_f16x2(w.y);
-      }
-#pragma unroll
-      for (int dt = 0; dt < KS; ++dt) o[dt][0] = o[dt][1] = o[dt][2] = o[dt][3] = 0.f;
-      m_a = m_b = -INFINITY;
-      l_a = l_b = 0.f;
-    }
-    const bool work = khi > klo;
-    const bool partial = klo > 0 || khi < kPage;
-    const uint8_t* kp = ring + blk * L::kBlock;
-    const int kblk = blk;
-    if (++blk == kRing) {
-      blk = 0;
-      phase ^= 1;
-    }
-    const uint8_t* vp = ring + blk * L::kBlock;
-    uint32_t pb[4][2];  // P^T, keys in the order of the value pairs
-    if (work) {
-      // ---- S^T = K Q^T ----
-      float sc[4][4];
-#pragma unroll
-      for (int t = 0; t < 4; ++t) sc[t][0] = sc[t][1] = sc[t][2] = sc[t][3] = 0.f;
-      {
-        // scales of keys kperm + 8 i, i = 0 .. 7, in pairs (i, i + 1), for the lane's blocks
-        constexpr int NBLK = D == 64 ? 1 : 2;
-        uint32_t ks[NBLK][4];
-#pragma unroll
-        for (int n = 0; n < NBLK; ++n) {
-          const uint4 w = *reinterpret_cast<const uint4*>(kp + 32 * D + ((r >> 1) * KS + kb + n) * 16);
-          const uint32_t sel = (r & 1) ? 0x7531u : 0x6420u;
-          e4m3x4_to_f16x2x2(__byte_perm(w.x, w.y, sel), ks[n][0], ks[n][1]);
-          e4m3x4_to_f16x2x2(__byte_perm(w.z, w.w, sel), ks[n][2], ks[n][3]);
+        for (int kk = 0; kk < KS; ++kk) {  // dimensions c D/4 + 4 kk .. + 3 of head r
+          const uint2 w = r < G ? *reinterpret_cast<const uint2*>(qs + 4 * kk) : make_uint2(0u, 0u);
+          qf[kk][0] = bf16x2_to_f16x2(w.x);
+          qf[kk][1] = bf16x2_to_f16x2(w.y);
         }
-        uint32_t kw[8][KW];  // code words of keys kperm + 8 i
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint8_t* src = kp + (kperm + 8 * i) * (D / 2) + c * (KW * 4);
-          if constexpr (D == 128) {
-            const uint4 w = *reinterpret_cast<const uint4*>(src);
-            kw[i][0] = w.x; kw[i][1] = w.y; kw[i][2] = w.z; kw[i][3] = w.w;
-          } else if constexpr (D == 64) {
-            const uint2 w = *reinterpret_cast<const uint2*>(src);
-            kw[i][0] = w.x; kw[i][1] = w.y;
-          } else {
+        for (int dt = 0; dt < KS; ++dt) o[dt][0] = o[dt][1] = o[dt][2] = o[dt][3] = 0.f;
+        m_a = m_b = -INFINITY;
+        l_a = l_b = 0.f;
+      }
+      const bool work = khi > klo;
+      const bool partial = klo > 0 || khi < kPage;
+      const uint8_t* kp = ring + blk * L::kBlock;
+      const int kblk = blk;
+      if (++blk == kRing) {
+        blk = 0;
+        phase ^= 1;
+      }
+      const uint8_t* vp = ring + blk * L::kBlock;
+      uint32_t pb[4][2];  // P^T, keys in the order of the value pairs
+      if (work) {
+        // ---- S^T = K Q^T ----
+        float sc[4][4];
 #pragma unroll
-            for (int x = 0; x < KW; ++x) kw[i][x] = reinterpret_cast<const uint32_t*>(src)[x];
+        for (int t = 0; t < 4; ++t) sc[t][0] = sc[t][1] = sc[t][2] = sc[t][3] = 0.f;
+        {
+          // scales of keys kperm + 8 i, i = 0 .. 7, in pairs (i, i + 1), for the lane's blocks
+          constexpr int NBLK = D == 64 ? 1 : 2;
+          uint32_t ks[NBLK][4];
+#pragma unroll
+          for (int n = 0; n < NBLK; ++n) {
+            const uint4 w = *reinterpret_cast<const uint4*>(kp + 32 * D + ((r >> 1) * KS + kb + n) * 16);
+            const uint32_t sel = (r & 1) ? 0x7531u : 0x6420u;
+            e4m3x4_to_f16x2x2(__byte_perm(w.x, w.y, sel), ks[n][0], ks[n][1]);
+            e4m3x4_to_f16x2x2(__byte_perm(w.z, w.w, sel), ks[n][2], ks[n][3]);
+          }
+          uint32_t kw[8][KW];  // code words of keys kperm + 8 i
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint8_t* src = kp + (kperm + 8 * i) * (D / 2) + c * (KW * 4);
+            if constexpr (D == 128) {
+              const uint4 w = *reinterpret_cast<const uint4*>(src);
+              kw[i][0] = w.x; kw[i][1] = w.y; kw[i][2] = w.z; kw[i][3] = w.w;
+            } else if constexpr (D == 64) {
+              const uint2 w = *reinterpret_cast<const uint2*>(src);
+              kw[i][0] = w.x; kw[i][1] = w.y;
+            } else {
+#pragma unroll
+              for (int x = 0; x < KW; ++x) kw[i][x] = reinterpret_cast<const uint32_t*>(src)[x];
+            }
+          }
+          // the keys are in registers: their block may be loaded again
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(empty + kblk));
+#pragma unroll
+          for (int x = 0; x < KW; ++x) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+              // word x lies in the lane's first or second block
+              uint32_t sp;
+              if constexpr (D == 64) sp = ks[0][t];
+              else if constexpr (D == 128) sp = ks[x >> 1][t];
+              else sp = x == 0 ? ks[0][t] : (x == 2 ? ks[1][t] : ((c & 1) ? ks[1][t] : ks[0][t]));
+              uint32_t ra[4], rb[4];  // rows r (key 2t) and r + 8 (key 2t + 1), two k-steps each
+              e2m1x8_to_f16x2x4(kw[2 * t][x], ra);
+              e2m1x8_to_f16x2x4(kw[2 * t + 1][x], rb);
+              const uint32_t sa = low2(sp), sb = high2(sp);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                ra[i] = mul_f16x2(ra[i], sa);
+                rb[i] = mul_f16x2(rb[i], sb);
+              }
+              mma_f16_16816(sc[t], ra[0], rb[0], ra[1], rb[1], qf[2 * x][0], qf[2 * x][1]);
+              mma_f16_16816(sc[t], ra[2], rb[2], ra[3], rb[3], qf[2 * x + 1][0], qf[2 * x + 1][1]);
+            }
           }
         }
-        // the keys are in registers: their block may be loaded again
+        // ---- mask, online softmax (log2 domain) ----
+        float mx_a = -INFINITY, mx_b = -INFINITY;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (partial) {
+              const int key = 16 * t + 8 * (i >> 1) + kperm;
+              if (key < klo || key >= khi) sc[t][i] = -INFINITY;
+            }
+          }
+          mx_a = fmax3(mx_a, sc[t][0], sc[t][2]);
+          mx_b = fmax3(mx_b, sc[t][1], sc[t][3]);
+        }
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) {
+          mx_a = fmaxf(mx_a, __shfl_xor_sync(0xffffffffu, mx_a, off));
+          mx_b = fmaxf(mx_b, __shfl_xor_sync(0xffffffffu, mx_b, off));
+        }
+        // (the scale is positive: the largest product is the largest score's)
+        const float mn_a = fmaxf(m_a, mx_a * p.scale_log2), mn_b = fmaxf(m_b, mx_b * p.scale_log2);
+        const bool same_max = __all_sync(0xffffffffu, mn_a == m_a && mn_b == m_b);
+        const float base_a = mn_a == -INFINITY ? 0.f : mn_a;
+        const float base_b = mn_b == -INFINITY ? 0.f : mn_b;
+        if (!same_max) {  // a running max moved: O and the sums follow
+          const float al_a = ex2_approx(m_a - base_a), al_b = ex2_approx(m_b - base_b);
+          l_a *= al_a;
+          l_b *= al_b;
+#pragma unroll
+          for (int dt = 0; dt < KS; ++dt) {
+            o[dt][0] *= al_a;
+            o[dt][1] *= al_b;
+            o[dt][2] *= al_a;
+            o[dt][3] *= al_b;
+          }
+        }
+        m_a = mn_a;
+        m_b = mn_b;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const float p0 = ex2_approx(fmaf(sc[t][0], p.scale_log2, -base_a));
+          const float p1 = ex2_approx(fmaf(sc[t][1], p.scale_log2, -base_b));
+          const float p2 = ex2_approx(fmaf(sc[t][2], p.scale_log2, -base_a));
+          const float p3 = ex2_approx(fmaf(sc[t][3], p.scale_log2, -base_b));
+          l_a += p0 + p2;
+          l_b += p1 + p3;
+          pb[t][0] = movmatrix_trans(pack_f16x2(p0, p1));
+          pb[t][1] = movmatrix_trans(pack_f16x2(p2, p3));
+        }
+      }
+      if (!work) {
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(empty + kblk));
-#pragma unroll
-        for (int x = 0; x < KW; ++x) {
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            // word x lies in the lane's first or second block
-            uint32_t sp;
-            if constexpr (D == 64) sp = ks[0][t];
-            else if constexpr (D == 128) sp = ks[x >> 1][t];
-            else sp = x == 0 ? ks[0][t] : (x == 2 ? ks[1][t] : ((c & 1) ? ks[1][t] : ks[0][t]));
-            uint32_t ra[4], rb[4];  // rows r (key 2t) and r + 8 (key 2t + 1), two k-steps each
-            e2m1x8_to_f16x2x4(kw[2 * t][x], ra);
-            e2m1x8_to_f16x2x4(kw[2 * t + 1][x], rb);
-            const uint32_t sa = low2(sp), sb = high2(sp);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              ra[i] = mul_f16x2(ra[i], sa);
-              rb[i] = mul_f16x2(rb[i], sb);
-            }
-            mma_f16_16816(sc[t], ra[0], rb[0], ra[1], rb[1], qf[2 * x][0], qf[2 * x][1]);
-            mma_f16_16816(sc[t], ra[2], rb[2], ra[3], rb[3], qf[2 * x + 1][0], qf[2 * x + 1][1]);
-          }
-        }
       }
-      // ---- mask, online softmax (log2 domain) ----
-      float mx_a = -INFINITY, mx_b = -INFINITY;
+      if (!__all_sync(0xffffffffu, mbar_wait(smem_addr(full + blk), phase, abort_flag))) break;
+      if (work) {
+        // ---- O^T += V^T P^T ----
+        // scales of keys c + 4 i in pairs (i, i + 1), for the lane's blocks; zero where masked
+        constexpr int NVB = D == 96 ? 2 : 1;
+        uint32_t vs[NVB][8];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int n = 0; n < NVB; ++n) {
+          const int b = n == 0 ? vb : 4 + r / 4;
+          uint4 w = *reinterpret_cast<const uint4*>(vp + 32 * D + (c * KS + b) * 16);
           if (partial) {
-            const int key = 16 * t + 8 * (i >> 1) + kperm;
-            if (key < klo || key >= khi) sc[t][i] = -INFINITY;
+            uint32_t* ww = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int key = c + 4 * i;
+              if (key < klo || key >= khi) ww[i >> 2] &= ~(0xFFu << (8 * (i & 3)));
+            }
+          }
+          e4m3x4_to_f16x2x2(w.x, vs[n][0], vs[n][1]);
+          e4m3x4_to_f16x2x2(w.y, vs[n][2], vs[n][3]);
+          e4m3x4_to_f16x2x2(w.z, vs[n][4], vs[n][5]);
+          e4m3x4_to_f16x2x2(w.w, vs[n][6], vs[n][7]);
+        }
+        constexpr int VW = D == 128 ? 2 : 1;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          uint32_t vw[4][VW];
+          uint32_t vh[4];  // D = 96: dimensions 64 + 4 r .. + 3
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint8_t* src = vp + (c + 4 * (4 * t + i)) * (D / 2);
+            if constexpr (D == 128) {
+              const uint2 w = *reinterpret_cast<const uint2*>(src + 8 * r);
+              vw[i][0] = w.x;
+              vw[i][1] = w.y;
+            } else {
+              vw[i][0] = *reinterpret_cast<const uint32_t*>(src + 4 * r);
+              if constexpr (D == 96) vh[i] = *reinterpret_cast<const uint16_t*>(src + 32 + 2 * r);
+            }
+          }
+#pragma unroll
+          for (int y = 0; y < VW; ++y) {
+            uint32_t e0[4], o0[4], e1[4], o1[4];
+            e2m1x8_to_f16x2x4(mix_even(vw[0][y], vw[1][y]), e0);
+            e2m1x8_to_f16x2x4(mix_odd(vw[0][y], vw[1][y]), o0);
+            e2m1x8_to_f16x2x4(mix_even(vw[2][y], vw[3][y]), e1);
+            e2m1x8_to_f16x2x4(mix_odd(vw[2][y], vw[3][y]), o1);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              mma_f16_16816(o[4 * y + i], mul_f16x2(e0[i], vs[0][2 * t]), mul_f16x2(o0[i], vs[0][2 * t]),
+                            mul_f16x2(e1[i], vs[0][2 * t + 1]), mul_f16x2(o1[i], vs[0][2 * t + 1]), pb[t][0], pb[t][1]);
+          }
+          if constexpr (D == 96) {
+            // the 16-bit words of two keys, side by side, convert as one word each
+            uint32_t e0[4], e1[4];
+            e2m1x8_to_f16x2x4(mix_even(vh[0], vh[1]) | (mix_odd(vh[0], vh[1]) << 16), e0);
+            e2m1x8_to_f16x2x4(mix_even(vh[2], vh[3]) | (mix_odd(vh[2], vh[3]) << 16), e1);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              mma_f16_16816(o[4 + i], mul_f16x2(e0[i], vs[NVB - 1][2 * t]), mul_f16x2(e0[2 + i], vs[NVB - 1][2 * t]),
+                            mul_f16x2(e1[i], vs[NVB - 1][2 * t + 1]), mul_f16x2(e1[2 + i], vs[NVB - 1][2 * t + 1]),
+                            pb[t][0], pb[t][1]);
           }
         }
-        mx_a = fmax3(mx_a, sc[t][0], sc[t][2]);
-        mx_b = fmax3(mx_b, sc[t][1], sc[t][3]);
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(empty + blk));
+      if (++blk == kRing) {
+        blk = 0;
+        phase ^= 1;
+      }
+      if (!(flags & kLast)) continue;
+
+      float la = l_a, lb = l_b;
 #pragma unroll
       for (int off = 4; off < 32; off <<= 1) {
-        mx_a = fmaxf(mx_a, __shfl_xor_sync(0xffffffffu, mx_a, off));
-        mx_b = fmaxf(mx_b, __shfl_xor_sync(0xffffffffu, mx_b, off));
+        la += __shfl_xor_sync(0xffffffffu, la, off);
+        lb += __shfl_xor_sync(0xffffffffu, lb, off);
       }
-      // (the scale is positive: the largest product is the largest score's)
-      const float mn_a = fmaxf(m_a, mx_a * p.scale_log2), mn_b = fmaxf(m_b, mx_b * p.scale_log2);
-      const bool same_max = __all_sync(0xffffffffu, mn_a == m_a && mn_b == m_b);
-      const float base_a = mn_a == -INFINITY ? 0.f : mn_a;
-      const float base_b = mn_b == -INFINITY ? 0.f : mn_b;
-      if (!same_max) {  // a running max moved: O and the sums follow
-        const float al_a = ex2_approx(m_a - base_a), al_b = ex2_approx(m_b - base_b);
-        l_a *= al_a;
-        l_b *= al_b;
+      const int ob = pi.b, oh = pi.h;
+      if (flags & kWhole) {
+        // ---- a whole pair: this lane's dimensions of heads 2c and 2c + 1 ----
+        const float ia = la > 0.f ? p.out_scale / la : 0.f, ib = lb > 0.f ? p.out_scale / lb : 0.f;
+        uint16_t* oa = p.out + (static_cast<size_t>(ob) * p.hq + static_cast<size_t>(oh) * G + 2 * c) * D;
 #pragma unroll
-        for (int dt = 0; dt < KS; ++dt) {
-          o[dt][0] *= al_a;
-          o[dt][1] *= al_b;
-          o[dt][2] *= al_a;
-          o[dt][3] *= al_b;
+        for (int dt = 0; dt < KS; dt += 2) {
+          const int d = D == 128 ? 16 * r + 2 * dt : (dt < 4 ? 8 * r + 2 * dt : 64 + 4 * r);
+          if (2 * c < G)
+            *reinterpret_cast<uint2*>(oa + d) = make_uint2(pack_bf16x2(o[dt][0] * ia, o[dt][2] * ia),
+                                                           pack_bf16x2(o[dt + 1][0] * ia, o[dt + 1][2] * ia));
+          if (2 * c + 1 < G)
+            *reinterpret_cast<uint2*>(oa + D + d) = make_uint2(pack_bf16x2(o[dt][1] * ib, o[dt][3] * ib),
+                                                               pack_bf16x2(o[dt + 1][1] * ib, o[dt + 1][3] * ib));
         }
+        continue;
       }
-      m_a = mn_a;
-      m_b = mn_b;
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const float p0 = ex2_approx(fmaf(sc[t][0], p.scale_log2, -base_a));
-        const float p1 = ex2_approx(fmaf(sc[t][1], p.scale_log2, -base_b));
-        const float p2 = ex2_approx(fmaf(sc[t][2], p.scale_log2, -base_a));
-        const float p3 = ex2_approx(fmaf(sc[t][3], p.scale_log2, -base_b));
-        l_a += p0 + p2;
-        l_b += p1 + p3;
-        pb[t][0] = movmatrix_trans(pack_f16x2(p0, p1));
-        pb[t][1] = movmatrix_trans(pack_f16x2(p2, p3));
+      // ---- a piece of a longer pair: its state into shared memory ----
+      const int piece = 2 * warp + (flags & kRunEnd ? 1 : 0);
+      if (lane < 4) {
+        smax[piece * kMaxGroup + 2 * c] = m_a;
+        smax[piece * kMaxGroup + 2 * c + 1] = m_b;
+        ssum[piece * kMaxGroup + 2 * c] = la;
+        ssum[piece * kMaxGroup + 2 * c + 1] = lb;
       }
-    }
-    if (!work) {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(empty + kblk));
-    }
-    if (!__all_sync(0xffffffffu, mbar_wait(smem_addr(full + blk), phase, abort_flag))) break;
-    if (work) {
-      // ---- O^T += V^T P^T ----
-      // scales of keys c + 4 i in pairs (i, i + 1), for the lane's blocks; zero where masked
-      constexpr int NVB = D == 96 ? 2 : 1;
-      uint32_t vs[NVB][8];
-#pragma unroll
-      for (int n = 0; n < NVB; ++n) {
-        const int b = n == 0 ? vb : 4 + r / 4;
-        uint4 w = *reinterpret_cast<const uint4*>(vp + 32 * D + (c * KS + b) * 16);
-        if (partial) {
-          uint32_t* ww = reinterpret_cast<uint32_t*>(&w);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int key = c + 4 * i;
-            if (key < klo || key >= khi) ww[i >> 2] &= ~(0xFFu << (8 * (i & 3)));
-          }
-        }
-        e4m3x4_to_f16x2x2(w.x, vs[n][0], vs[n][1]);
-        e4m3x4_to_f16x2x2(w.y, vs[n][2], vs[n][3]);
-        e4m3x4_to_f16x2x2(w.z, vs[n][4], vs[n][5]);
-        e4m3x4_to_f16x2x2(w.w, vs[n][6], vs[n][7]);
-      }
-      constexpr int VW = D == 128 ? 2 : 1;
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        uint32_t vw[4][VW];
-        uint32_t vh[4];  // D = 96: dimensions 64 + 4 r .. + 3
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint8_t* src = vp + (c + 4 * (4 * t + i)) * (D / 2);
-          if constexpr (D == 128) {
-            const uint2 w = *reinterpret_cast<const uint2*>(src + 8 * r);
-            vw[i][0] = w.x;
-            vw[i][1] = w.y;
-          } else {
-            vw[i][0] = *reinterpret_cast<const uint32_t*>(src + 4 * r);
-            if constexpr (D == 96) vh[i] = *reinterpret_cast<const uint16_t*>(src + 32 + 2 * r);
-          }
-        }
-#pragma unroll
-        for (int y = 0; y < VW; ++y) {
-          uint32_t e0[4], o0[4], e1[4], o1[4];
-          e2m1x8_to_f16x2x4(mix_even(vw[0][y], vw[1][y]), e0);
-          e2m1x8_to_f16x2x4(mix_odd(vw[0][y], vw[1][y]), o0);
-          e2m1x8_to_f16x2x4(mix_even(vw[2][y], vw[3][y]), e1);
-          e2m1x8_to_f16x2x4(mix_odd(vw[2][y], vw[3][y]), o1);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            mma_f16_16816(o[4 * y + i], mul_f16x2(e0[i], vs[0][2 * t]), mul_f16x2(o0[i], vs[0][2 * t]),
-                          mul_f16x2(e1[i], vs[0][2 * t + 1]), mul_f16x2(o1[i], vs[0][2 * t + 1]), pb[t][0], pb[t][1]);
-        }
-        if constexpr (D == 96) {
-          // the 16-bit words of two keys, side by side, convert as one word each
-          uint32_t e0[4], e1[4];
-          e2m1x8_to_f16x2x4(mix_even(vh[0], vh[1]) | (mix_odd(vh[0], vh[1]) << 16), e0);
-          e2m1x8_to_f16x2x4(mix_even(vh[2], vh[3]) | (mix_odd(vh[2], vh[3]) << 16), e1);
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            mma_f16_16816(o[4 + i], mul_f16x2(e0[i], vs[NVB - 1][2 * t]), mul_f16x2(e0[2 + i], vs[NVB - 1][2 * t]),
-                          mul_f16x2(e1[i], vs[NVB - 1][2 * t + 1]), mul_f16x2(e1[2 + i], vs[NVB - 1][2 * t + 1]),
-                          pb[t][0], pb[t][1]);
-        }
-      }
-    }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(smem_addr(empty + blk));
-    if (++blk == kRing) {
-      blk = 0;
-      phase ^= 1;
-    }
-    if (!(flags & kLast)) continue;
-
-    float la = l_a, lb = l_b;
-#pragma unroll
-    for (int off = 4; off < 32; off <<= 1) {
-      la += __shfl_xor_sync(0xffffffffu, la, off);
-      lb += __shfl_xor_sync(0xffffffffu, lb, off);
-    }
-    const int ob = pi.b, oh = pi.h;
-    if (flags & kWhole) {
-      // ---- a whole pair: this lane's dimensions of heads 2c and 2c + 1 ----
-      const float ia = la > 0.f ? p.out_scale / la : 0.f, ib = lb > 0.f ? p.out_scale / lb : 0.f;
-      uint16_t* oa = p.out + (static_cast<size_t>(ob) * p.hq + static_cast<size_t>(oh) * G + 2 * c) * D;
+      if (lane == 0) piece_pair[piece] = ob * p.hkv + oh;
+      float* oa = const_cast<float*>(piece_state(piece)) + (2 * c) * L::kOStride;
 #pragma unroll
       for (int dt = 0; dt < KS; dt += 2) {
+        // d-tiles dt, dt + 1: four consecutive dimensions
         const int d = D == 128 ? 16 * r + 2 * dt : (dt < 4 ? 8 * r + 2 * dt : 64 + 4 * r);
-        if (2 * c < G)
-          *reinterpret_cast<uint2*>(oa + d) = make_uint2(pack_bf16x2(o[dt][0] * ia, o[dt][2] * ia),
-                                                         pack_bf16x2(o[dt + 1][0] * ia, o[dt + 1][2] * ia));
-        if (2 * c + 1 < G)
-          *reinterpret_cast<uint2*>(oa + D + d) = make_uint2(pack_bf16x2(o[dt][1] * ib, o[dt][3] * ib),
-                                                             pack_bf16x2(o[dt + 1][1] * ib, o[dt + 1][3] * ib));
+        *reinterpret_cast<float4*>(oa + d) = make_float4(o[dt][0], o[dt][2], o[dt + 1][0], o[dt + 1][2]);
+        *reinterpret_cast<float4*>(oa + L::kOStride + d) = make_float4(o[dt][1], o[dt][3], o[dt + 1][1], o[dt + 1][3]);
       }
-      continue;
     }
-    // ---- a piece of a longer pair: its state into shared memory ----
-    const int piece = 2 * warp + (flags & kRunEnd ? 1 : 0);
-    if (lane < 4) {
-      smax[piece * kMaxGroup + 2 * c] = m_a;
-      smax[piece * kMaxGroup + 2 * c + 1] = m_b;
-      ssum[piece * kMaxGroup + 2 * c] = la;
-      ssum[piece * kMaxGroup + 2 * c + 1] = lb;
     }
-    if (lane == 0) piece_pair[piece] = ob * p.hkv + oh;
-    float* oa = const_cast<float*>(piece_state(piece)) + (2 * c) * L::kOStride;
-#pragma unroll
-    for (int dt = 0; dt < KS; dt += 2) {
-      // d-tiles dt, dt + 1: four consecutive dimensions
-      const int d = D == 128 ? 16 * r + 2 * dt : (dt < 4 ? 8 * r + 2 * dt : 64 + 4 * r);
-      *reinterpret_cast<float4*>(oa + d) = make_float4(o[dt][0], o[dt][2], o[dt + 1][0], o[dt + 1][2]);
-      *reinterpret_cast<float4*>(oa + L::kOStride + d) = make_float4(o[dt][1], o[dt][3], o[dt + 1][1], o[dt + 1][3]);
-    }
-  }
 
-  // ================= all runs are done: merge the pieces ==================
-  // (every consumer warp comes here, whatever ended its loop)
-  constexpr int kAll = kWarps * 32;
-  named_barrier_sync(1, kAll);
-  // Pieces of one pair are neighbours.  Bit i: piece i is there / begins a pair.
-  const int mine = lane < kPieces ? piece_pair[lane] : -1;
-  const unsigned there = __ballot_sync(0xffffffffu, mine >= 0);
-  const unsigned before = there & ((1u << lane) - 1u);
-  const int prev = __shfl_sync(0xffffffffu, mine, before ? 31 - __clz(before) : 0);
-  const unsigned heads = __ballot_sync(0xffffffffu, mine >= 0 && (before == 0u || prev != mine));
-  const int npairs = __popc(heads);
-  constexpr int D4 = D / 4;
-  const int items = G * D4;
-  bool cut = false;  // some pair goes on in another CTA
-  {
-    unsigned rest = heads;
-    for (int gidx = 0; gidx < npairs; ++gidx) {
+    // ================= all runs are done: merge the pieces ==================
+    // (every consumer warp comes here, whatever ended its loop)
+    named_barrier_sync(1, kAll);
+    // Pieces of one pair are neighbours.  Bit i: piece i is there / begins a pair.
+    const int mine = dry ? (lane == 0 ? 0 : -1) : (lane < kPieces ? piece_pair[lane] : -1);
+    const unsigned there = __ballot_sync(0xffffffffu, mine >= 0);
+    const unsigned before = there & ((1u << lane) - 1u);
+    const int prev = __shfl_sync(0xffffffffu, mine, before ? 31 - __clz(before) : 0);
+    const unsigned heads = __ballot_sync(0xffffffffu, mine >= 0 && (before == 0u || prev != mine));
+    const int items = G * D4;  // of a pair: four dimensions of a head each
+    const int total_items = __popc(heads) * items;
+    const bool cut0 = dry || shared[2] != 0, cut1 = !dry && shared[5] != 0;
+    for (int idx = tid; idx < total_items; idx += kAll) {
+      const int gidx = idx / items, it = idx - gidx * items;
+      const int g = it / D4, d = (it % D4) * 4;
+      unsigned rest = heads;
+      for (int i = 0; i < gidx; ++i) rest &= rest - 1;
       const int at = __ffs(rest) - 1;
       rest &= rest - 1;
       const unsigned mask = there & (rest ? (1u << (__ffs(rest) - 1)) - (1u << at) : ~0u << at);
-      const int q = piece_pair[at], b = q / p.hkv, h = q % p.hkv;
-      const int np = pref[b + 1] - pref[b];
-      const long long pair_start = static_cast<long long>(pref[b]) * p.hkv + static_cast<long long>(h) * np;
-      const bool whole = pair_start >= start && pair_start + np <= end;
-      cut = cut || !whole;
-      // the CTA's threads take the pair's outputs, four dimensions each, in turn
-      // with the other pairs'
-      for (int it = (tid + kAll - gidx * items % kAll) % kAll; it < items; it += kAll) {
-        const int g = it / D4, d = (it % D4) * 4;
-        float M = -INFINITY;
-        for (unsigned m = mask; m; m &= m - 1) M = fmaxf(M, smax[(__ffs(m) - 1) * kMaxGroup + g]);
-        float Ls = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (M != -INFINITY) {
-          for (unsigned m = mask; m; m &= m - 1) {
-            const int i = __ffs(m) - 1;
-            const float mw = smax[i * kMaxGroup + g];
-            const float f = mw == -INFINITY ? 0.f : exp2f(mw - M);
-            const float4 v = *reinterpret_cast<const float4*>(piece_state(i) + g * L::kOStride + d);
-            Ls += ssum[i * kMaxGroup + g] * f;
-            acc.x += v.x * f;
-            acc.y += v.y * f;
-            acc.z += v.z * f;
-            acc.w += v.w * f;
-          }
-        }
-        if (whole) {
-          const float inv = Ls > 0.f ? p.out_scale / Ls : 0.f;
-          uint16_t* out = p.out + (static_cast<size_t>(b) * p.hq + static_cast<size_t>(h) * G + g) * D + d;
-          *reinterpret_cast<uint2*>(out) =
-              make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-        } else {  // the partial's place in the workspace: pair + chunk
-          const size_t row = (static_cast<size_t>(q) + chunk) * G + g;
-          *reinterpret_cast<float4*>(p.ws_o + row * D + d) = acc;
-          if (d == 0) *reinterpret_cast<float2*>(p.ws_ml + row * 2) = make_float2(M, Ls);
-        }
+      const int q = dry ? 0 : piece_pair[at];
+      float M = -INFINITY;
+      for (unsigned m = mask; m; m &= m - 1) M = fmaxf(M, smax[(__ffs(m) - 1) * kMaxGroup + g]);
+      const float base = M == -INFINITY ? 0.f : M;  // (then every weight is 2^-inf = 0)
+      float Ls = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (unsigned m = mask; m; m &= m - 1) {
+        const int i = __ffs(m) - 1;
+        const float f = ex2_approx(smax[i * kMaxGroup + g] - base);
+        const float4 v = *reinterpret_cast<const float4*>(piece_state(i) + g * L::kOStride + d);
+        Ls += ssum[i * kMaxGroup + g] * f;
+        acc.x += v.x * f;
+        acc.y += v.y * f;
+        acc.z += v.z * f;
+        acc.w += v.w * f;
+      }
+      if (dry) continue;
+      if ((cut0 && q == shared[0]) || (cut1 && q == shared[3])) {  // the partial's place in the workspace: pair + chunk
+        const size_t row = (static_cast<size_t>(q) + chunk) * G + g;
+        *reinterpret_cast<float4*>(p.ws_o + row * D + d) = acc;
+        if (d == 0) *reinterpret_cast<float2*>(p.ws_ml + row * 2) = make_float2(M, Ls);
+      } else {
+        store_out(q, g, d, acc, Ls);
       }
     }
-  }
-  if (cut) {
-    // ---- pairs shared with other CTAs (the chunk's first pair, its last pair):
-    // publish the partials, count the pair's finished chunks; the last CTA merges ----
-    __threadfence();
+    if (!cut0 && !cut1) continue;
+    // ---- pairs shared with other CTAs: count the pair's finished chunks; the
+    // last CTA merges them (the barrier and the fence publish the partials) ----
     named_barrier_sync(1, kAll);
-    const int ends[2] = {piece_pair[__ffs(heads) - 1], piece_pair[31 - __clz(heads)]};
-    auto shared_pair = [&](int which, int& c0, int& nseg) {
-      if (which == 1 && npairs == 1) return false;
-      const int q = ends[which], b = q / p.hkv, h = q % p.hkv;
-      const int np = pref[b + 1] - pref[b];
-      const long long pair_start = static_cast<long long>(pref[b]) * p.hkv + static_cast<long long>(h) * np;
-      if (pair_start >= start && pair_start + np <= end) return false;
-      c0 = static_cast<int>(pair_start / per);  // the chunk with the pair's first page
-      nseg = static_cast<int>((pair_start + np - 1) / per) - c0 + 1;
-      return true;
-    };
     if (tid < 2) {
-      int c0, nseg, last = 0;
-      if (shared_pair(tid, c0, nseg)) {
-        last = atomicAdd(p.ws_count + ends[tid], 1) == nseg - 1;
-        if (last) p.ws_count[ends[tid]] = 0;  // ready for the next call
+      int last = dry;
+      if (!dry && shared[tid * 3 + 2] != 0) {
+        const int q = shared[tid * 3];
+        __threadfence();
+        last = atomicAdd(p.ws_count + q, 1) == shared[tid * 3 + 2] - 1;
+        __threadfence();
+        if (last) p.ws_count[q] = 0;  // ready for the next call
       }
       arrived_last[tid] = last;
     }
     named_barrier_sync(1, kAll);
+#pragma unroll 1
     for (int which = 0; which < 2; ++which) {
       if (!arrived_last[which]) continue;
-      int c0 = 0, nseg = 0;
-      shared_pair(which, c0, nseg);
-      __threadfence();
-      const int q = ends[which];
-      const size_t seg0 = static_cast<size_t>(q) + c0;
+      const int q = dry ? 0 : shared[which * 3], nseg = dry ? 1 : shared[which * 3 + 2];
+      const size_t seg0 = dry ? 0 : static_cast<size_t>(q) + shared[which * 3 + 1];
       for (int it = tid; it < items; it += kAll) {
         const int g = it / D4, d = (it % D4) * 4;
         float M = -INFINITY, Ls = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        constexpr int kAtOnce = 8;
+        constexpr int kAtOnce = 4;
+#pragma unroll 1
         for (int s0 = 0; s0 < nseg; s0 += kAtOnce) {  // partials in their order, several loads in flight
           float2 ml[kAtOnce];
           float4 v[kAtOnce];
@@ -720,13 +733,13 @@ __global__ void __launch_bounds__(kThreads, 1) decode4_kernel(const DecodeParams
             const size_t row = (seg0 + min(s0 + u, nseg - 1)) * G + g;
             ml[u] = __ldcg(reinterpret_cast<const float2*>(p.ws_ml) + row);
             v[u] = __ldcg(reinterpret_cast<const float4*>(p.ws_o + row * D + d));
+            if (s0 + u >= nseg) ml[u].x = -INFINITY;
           }
           float mn = M;
 #pragma unroll
-          for (int u = 0; u < kAtOnce; ++u)
-            if (s0 + u < nseg) mn = fmaxf(mn, ml[u].x);
-          if (mn == -INFINITY) continue;
-          const float f0 = M == -INFINITY ? 0.f : exp2f(M - mn);
+          for (int u = 0; u < kAtOnce; ++u) mn = fmaxf(mn, ml[u].x);
+          const float base = mn == -INFINITY ? 0.f : mn;
+          const float f0 = ex2_approx(M - base);
           Ls *= f0;
           acc.x *= f0;
           acc.y *= f0;
@@ -734,7 +747,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode4_kernel(const DecodeParams
           acc.w *= f0;
 #pragma unroll
           for (int u = 0; u < kAtOnce; ++u) {
-            const float f = s0 + u < nseg && ml[u].x != -INFINITY ? exp2f(ml[u].x - mn) : 0.f;
+            const float f = ex2_approx(ml[u].x - base);
             Ls += ml[u].y * f;
             acc.x += v[u].x * f;
             acc.y += v[u].y * f;
@@ -743,10 +756,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode4_kernel(const DecodeParams
           }
           M = mn;
         }
-        const float inv = Ls > 0.f ? p.out_scale / Ls : 0.f;
-        uint16_t* out = p.out + (static_cast<size_t>(q / p.hkv) * p.hq + static_cast<size_t>(q % p.hkv) * G + g) * D + d;
-        *reinterpret_cast<uint2*>(out) =
-            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+        if (!dry) store_out(q, g, d, acc, Ls);
       }
     }
   }
