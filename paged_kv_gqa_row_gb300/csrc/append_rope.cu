@@ -37,47 +37,6 @@ constexpr int kSplitCtasPerSm = 2;   // split launches aim at this many CTAs per
 
 using namespace rope;
 
-// A key row of a 4-bit pool: lane l < D/4 holds elements (2l, 2l + 1) in lo and
-// (2l + D/2, 2l + 1 + D/2) in hi, so eight lanes in a row hold a block of each
-// half.  Every lane of the warp calls it; `has`: the lane holds data.
-template <int D>
-__device__ __forceinline__ void store_key_e2m1(uint8_t* page, int j, int lane, bool has, uint32_t lo, uint32_t hi,
-                                               float ps) {
-  constexpr int H = D / 2;
-  uint32_t mlo = bf16x2_absmax(lo), mhi = bf16x2_absmax(hi);
-#pragma unroll
-  for (int o = 1; o < 8; o <<= 1) {
-    mlo = max(mlo, __shfl_xor_sync(0xffffffffu, mlo, o));
-    mhi = max(mhi, __shfl_xor_sync(0xffffffffu, mhi, o));
-  }
-  if (!has) return;
-  const float six_ps = __fmul_rn(6.f, ps);
-  float dlo, dhi;
-  const uint32_t slo = e2m1_scale(mlo, six_ps, ps, dlo), shi = e2m1_scale(mhi, six_ps, ps, dhi);
-  uint8_t* row = page + j * (D / 2);
-  row[lane] = static_cast<uint8_t>(e2m1_codes(lo, dlo));
-  row[H / 2 + lane] = static_cast<uint8_t>(e2m1_codes(hi, dhi));
-  if ((lane & 7) == 0) {
-    page[e2m1_scale_offset<D>(j, lane >> 3)] = static_cast<uint8_t>(slo);
-    page[e2m1_scale_offset<D>(j, H / 16 + (lane >> 3))] = static_cast<uint8_t>(shi);
-  }
-}
-
-// A value row of a 4-bit pool: lane l < D/8 holds elements 8l .. 8l + 7, so two
-// lanes hold a block.  Every lane of the warp calls it.
-template <int D>
-__device__ __forceinline__ void store_value_e2m1(uint8_t* page, int j, int lane, uint4 x, float ps) {
-  uint32_t m = max(max(bf16x2_absmax(x.x), bf16x2_absmax(x.y)), max(bf16x2_absmax(x.z), bf16x2_absmax(x.w)));
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  if (lane >= D / 8) return;
-  float d;
-  const uint32_t s = e2m1_scale(m, __fmul_rn(6.f, ps), ps, d);
-  const uint32_t codes = e2m1_codes(x.x, d) | (e2m1_codes(x.y, d) << 8) | (e2m1_codes(x.z, d) << 16) |
-                         (e2m1_codes(x.w, d) << 24);
-  *reinterpret_cast<uint32_t*>(page + j * (D / 2) + 4 * lane) = codes;
-  if ((lane & 1) == 0) page[e2m1_scale_offset<D>(j, lane >> 1)] = static_cast<uint8_t>(s);
-}
-
 // KV4: pools of E2M1 codes and block scales (a variant of its own, so that the
 // other pools' kernel keeps its registers).
 template <int D, int kWarps, int kMaxHeadsPerWarp, bool KV4>
@@ -246,7 +205,7 @@ __global__ void __launch_bounds__(kWarps * 32) append_rope_kernel(const AppendPa
       if constexpr (KV4) {
         uint8_t* page = reinterpret_cast<uint8_t*>(p.v_pool) +
                         (static_cast<size_t>(vh) * p.num_pages + static_cast<size_t>(slot / kPage)) * (36 * D);
-        store_value_e2m1<D>(page, static_cast<int>(slot % kPage), lane,
+        store_value_e2m1<D>(page, static_cast<int>(slot % kPage), lane, lane < D / 8,
                             lane < D / 8 ? src[lane] : make_uint4(0u, 0u, 0u, 0u), p.v_scale);
         continue;
       }
@@ -291,6 +250,7 @@ cudaError_t launch_append_w(const AppendParams& p, cudaStream_t stream) {
 
 template <int D, bool KV4>
 cudaError_t launch_append_t(const AppendParams& p_in, cudaStream_t stream) {
+  if (KV4 && append4_takes(p_in.T)) return launch_append4(p_in, D, stream);
   AppendParams p = p_in;
   const long long sms = device_sm_count();
   const int nrot = p.hq + p.hkv;

@@ -50,6 +50,10 @@ struct AppendParams {
 
 cudaError_t launch_append(const AppendParams& p, int head_dim, cudaStream_t stream);
 
+// 4-bit pools, launches of many tokens (append4.cu).
+bool append4_takes(int tokens);
+cudaError_t launch_append4(const AppendParams& p, int head_dim, cudaStream_t stream);
+
 // ------------------------------------------------------------ read tokens --
 struct ReadParams {
   const uint8_t* pool[2];     // K, V (null: not read)

@@ -228,6 +228,47 @@ __device__ __forceinline__ int e2m1_scale_offset(int j, int b) {
   return 32 * D + ((j & 3) * (D / 16) + b) * 16 + (j >> 2);
 }
 
+// A key row of a 4-bit pool: lane l < D/4 holds elements (2l, 2l + 1) in lo and
+// (2l + D/2, 2l + 1 + D/2) in hi, so eight lanes in a row hold a block of each
+// half.  Every lane of the warp calls it; `has`: the lane holds data.
+template <int D>
+__device__ __forceinline__ void store_key_e2m1(uint8_t* page, int j, int lane, bool has, uint32_t lo, uint32_t hi,
+                                               float ps) {
+  constexpr int H = D / 2;
+  uint32_t mlo = bf16x2_absmax(lo), mhi = bf16x2_absmax(hi);
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) {
+    mlo = max(mlo, __shfl_xor_sync(0xffffffffu, mlo, o));
+    mhi = max(mhi, __shfl_xor_sync(0xffffffffu, mhi, o));
+  }
+  if (!has) return;
+  const float six_ps = __fmul_rn(6.f, ps);
+  float dlo, dhi;
+  const uint32_t slo = e2m1_scale(mlo, six_ps, ps, dlo), shi = e2m1_scale(mhi, six_ps, ps, dhi);
+  uint8_t* row = page + j * (D / 2);
+  row[lane] = static_cast<uint8_t>(e2m1_codes(lo, dlo));
+  row[H / 2 + lane] = static_cast<uint8_t>(e2m1_codes(hi, dhi));
+  if ((lane & 7) == 0) {
+    page[e2m1_scale_offset<D>(j, lane >> 3)] = static_cast<uint8_t>(slo);
+    page[e2m1_scale_offset<D>(j, H / 16 + (lane >> 3))] = static_cast<uint8_t>(shi);
+  }
+}
+
+// A value row of a 4-bit pool: lane l of those with `has` holds elements 8l ..
+// 8l + 7, so two lanes (2i, 2i + 1) hold a block.  Every lane of the warp calls it.
+template <int D>
+__device__ __forceinline__ void store_value_e2m1(uint8_t* page, int j, int l, bool has, uint4 x, float ps) {
+  uint32_t m = max(max(bf16x2_absmax(x.x), bf16x2_absmax(x.y)), max(bf16x2_absmax(x.z), bf16x2_absmax(x.w)));
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  if (!has) return;
+  float d;
+  const uint32_t s = e2m1_scale(m, __fmul_rn(6.f, ps), ps, d);
+  const uint32_t codes = e2m1_codes(x.x, d) | (e2m1_codes(x.y, d) << 8) | (e2m1_codes(x.z, d) << 16) |
+                         (e2m1_codes(x.w, d) << 24);
+  *reinterpret_cast<uint32_t*>(page + j * (D / 2) + 4 * l) = codes;
+  if ((l & 1) == 0) page[e2m1_scale_offset<D>(j, l >> 1)] = static_cast<uint8_t>(s);
+}
+
 // Sine and cosine (float pairs) of the float32 angle f32(pos) * inv_freq.
 __device__ __forceinline__ void angle_sincos(int pos, float inv_freq, DF& sn, DF& cs) {
   const float a = __fmul_rn(static_cast<float>(pos), inv_freq);

@@ -123,6 +123,53 @@ def test_append_with_qk_norm_and_with_slots():
     assert torch.equal(again.k_pool, dev.k_pool) and torch.equal(again.v_pool, dev.v_pool)
 
 
+@pytest.mark.parametrize("hq,hkv,d,tokens,norm", [(8, 2, 128, 400, True), (6, 6, 96, 160, True), (5, 5, 64, 153, False),
+                                                  (16, 2, 128, 700, False), (32, 8, 128, 151, True), (3, 3, 96, 1300, True),
+                                                  (1, 1, 64, 2000, True)])
+def test_prompts_at_any_position_with_and_without_norm(hq, hkv, d, tokens, norm):
+    """Launches around and above the size where the many-token form takes over:
+    positions of every magnitude (far ones have angles beyond 2^20), inactive
+    tokens, bad slots, and heads of zeros, against the oracle's bytes."""
+    import paged_kv_gqa_row_gb300 as lnk
+    rng = np.random.RandomState(tokens + d)
+    pages = tokens // 64 + 2
+    q, k, v = (synth.tensor_bf16(tokens + d, i, (tokens, h, d)) for i, h in enumerate((hq, hkv, hkv)))
+    q[7, 0] = 0
+    positions = (2.0 ** rng.uniform(0, 30, tokens)).astype(np.int64)
+    positions[:40] = np.arange(40)
+    positions[[3, 50, tokens - 1]] = -1
+    slots = rng.permutation(pages * 64)[:tokens]
+    gq = gk = None
+    if norm:
+        gq, gk = (obf16.from_f64(1 + 0.1 * rng.standard_normal(d)) for _ in range(2))
+    inv = orope.inv_freq(5e5, d, (8.0, 1.0, 4.0, 8192))
+    blank = np.zeros((hkv, pages, 36 * d), dtype=np.uint8)
+    q_want, kp, vp = ofp4.append_rope(q, k, v, positions, None, None, blank, blank, inv, K_SCALE, V_SCALE, slots=slots,
+                                      gamma_q=gq, gamma_k=gk, eps=1e-6)
+    bad = slots.copy()
+    bad_tokens = [5, 60]
+    bad[bad_tokens] = [pages * 64, -3]
+    desc = lnk.attn_desc(hq, hkv, d, pages, 1, 1, kv_dtype=lnk.KV_E2M1, k_scale=K_SCALE, v_scale=V_SCALE)
+    rope = lnk.rope_desc(5e5, (8.0, 1.0, 4.0, 8192))
+    for use, want_status in ((slots, 0), (bad, 0x08)):
+        kd, vd = d8(blank), d8(blank)
+        q_out = torch.full((tokens, hq, d), 0x55, dtype=torch.int16, device="cuda")
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        lnk.lnk_paged_append_rope(desc, rope, d16(q), d16(k), d16(v), d32(positions), None, d32(use), None,
+                                  None if gq is None else d16(gq), None if gk is None else d16(gk), 1e-6, kd, vd, q_out,
+                                  tokens, status)
+        torch.cuda.synchronize()
+        assert int(status.item()) == want_status
+        assert_ulp_close(to_bits(q_out), q_want, "q_out")
+        if want_status:  # the bad tokens' slots stay as they were
+            for t in bad_tokens:
+                for pool in (kp, vp):
+                    for h in range(hkv):
+                        ofp4.write_row(pool[h, slots[t] // 64], slots[t] % 64, np.zeros(d, np.uint8), np.zeros(d // 16, np.uint8))
+        assert np.array_equal(u8(vd), vp), f"V bytes: {int(np.sum(u8(vd) != vp))} differ"
+        assert np.array_equal(u8(kd), kp), f"K bytes: {int(np.sum(u8(kd) != kp))} differ"
+
+
 def test_blocks_of_zeros_extremes_infinities_and_nan():
     """Value rows (stored without rotation) whose blocks are zero, below the least
     scale, saturating, infinite, NaN, and full of ties."""
