@@ -3,28 +3,26 @@
 //
 // The results are append_rope.cu's, bit for bit: the float-pair evaluation of
 // rope_math.cuh rounded once to bf16.  What it costs is avoided almost always:
-// a lane first evaluates its outputs in float32 with a bound E on the error,
-//     |u - exact| <= E,   E = 2^-21 S (2^-20 S r with QK-norm),
-//     S = |x1 c1| + |x2 s2|, the two terms of the rotation, r the RMS factor,
-// and where u - E and u + E round to the same bf16 value, that is the answer.
-// Otherwise (about one head in ten: some lane of the warp is near a border) the
-// warp evaluates the head by the float pairs.  The bound: each coefficient is
-// rounded once or twice (cosine or sine to float32, times the weight), each
-// product and the sum once: at most 4 S units of 2^-24.  With QK-norm the
-// float32 sum of the 128 exact squares adds at most 9 units to the mean's
-// relative error, half of that to r, the reciprocal root at most 4 and the last
-// product 1; u - E and u + E are rounded too: 5 units without, 15.5 with the norm,
-// against 8 and 16 in E.
+// a lane first evaluates an output in float32, with the coefficients' low parts,
+//     q = x2 s.hi + (x1 c.lo + x2 s.lo),  t = x1 c.hi + q   (fused products)
+// and with a bound E on its error; where t - E and t + E round to the same bf16
+// value, that is the answer, else (2 to 5 heads in a hundred have a lane near a
+// border) the warp evaluates the head by the float pairs.  The bound, in units of
+// 2^-24: q is rounded once (1 |q|), t once (1 |t|), the ends once (1 |t|), and
+// what is of second order is below a quarter of (|q| + |t|): 3.5 max(|q|, |t|).
+// With QK-norm the result is t r: the sum of D exact squares is rounded 7 times
+// (two in the lane, five in the tree), the mean and eps add 3, half of it counts
+// for r; r's own refinement 1.5, and the product 1: 8 more units of |t|, 11.5 in
+// all (12 taken).
 //
-// A warp works alone, without barriers: it takes one token (or one of S shares
-// of its heads), each lane evaluates the sine and cosine of its two frequencies
-// in registers, and the loads of four heads are in flight together.  What bounds
-// it: instructions (about 70 a head, 330 a frequency, 10 a division of the
-// quantizer).
+// A CTA takes one or two tokens, eight warps in all: its threads evaluate the
+// sines and cosines once (one frequency of one token each), and after the one
+// barrier every warp takes a share of one token's heads, the loads of the next
+// four heads in flight while it works on four.  What bounds it: instructions
+// (about 60 a head, 20 more with the norm, 100 more to quantize a key row, 10 of
+// them for each division; 400 a frequency).
 //
 // Sources: as append_rope.cu; the 4-bit format is this library's (lnk_attn_desc).
-#include <algorithm>
-
 #include "common.cuh"
 #include "ptx.cuh"
 #include "rope_math.cuh"
@@ -36,41 +34,100 @@ using namespace rope;
 
 constexpr int kWarps = 8;
 constexpr int kHeadsAtOnce = 4;
-constexpr int kWarpsPerSm = 24;  // what a launch aims at
+constexpr int kMaxTokens = 2;    // of a CTA
+constexpr int kCtasPerSm = 3;
+
+// The QK-norm factor 1 / sqrt(ss / D + eps) as a float pair (about 2^-44): one
+// step from the float32 root r0.  With d = 1 - v r0^2 (v r0^2 in float pairs, the
+// difference exact), 1 / sqrt(v) = r0 (1 + d / 2 + 3 d^2 / 8 + ...), |d| < 2^-20.
+// (Double precision, as rope_math.cuh takes it once per head, is slow here: with
+// it this kernel's FP64 pipe was a third of its time.)
+template <int D>
+__device__ __forceinline__ DF rms_factor_df(DF ss, float eps) {
+  constexpr double kInv = 1.0 / D;
+  constexpr float kHi = static_cast<float>(kInv), kLo = static_cast<float>(kInv - static_cast<double>(kHi));
+  const DF v = df_add(df_mul(ss, DF{kHi, kLo}), DF{eps, 0.f});
+  const float r0 = rsqrtf(v.hi);
+  const DF w = df_mul(v, two_prod(r0, r0));
+  const float d = __fsub_rn(__fsub_rn(1.f, w.hi), w.lo);
+  return fast_two_sum(r0, __fmul_rn(r0, __fmul_rn(d, __fmaf_rn(0.375f, d, 0.5f))));
+}
 
 // The float-pair evaluation of one head (a whole warp calls it).
 template <int D>
-__device__ __noinline__ uint2 rotate_exact(uint32_t xlo, uint32_t xhi, DF sn0, DF cs0, DF sn1, DF cs1, float4 g,
-                                           bool normed, double eps) {
-  const Coefs c[2] = {coefs_of(sn0, cs0, g.x, g.z), coefs_of(sn1, cs1, g.y, g.w)};
+__device__ __noinline__ uint2 rotate_exact(uint32_t xlo, uint32_t xhi, Coefs c0, Coefs c1, bool normed, float eps) {
+  const Coefs c[2] = {c0, c1};
   DF r{1.f, 0.f};
-  if (normed) r = rms_factor(head_sumsq(xlo, xhi), D, eps);
+  if (normed) r = rms_factor_df<D>(head_sumsq(xlo, xhi), eps);
   uint32_t lo, hi;
   rotate_pairs(xlo, xhi, c, 0, normed, r, lo, hi);
   return make_uint2(lo, hi);
 }
 
-// One output and whether it is certain.
-__device__ __forceinline__ uint32_t round_certain(float u, float e, bool& certain) {
-  const uint32_t w = pack_bf16x2(__fsub_rn(u, e), __fadd_rn(u, e));
-  // (zero, tiny, huge and NaN bounds go the other way)
-  certain = certain && (w >> 16) == (w & 0xFFFFu) && e > 1e-30f && e < 1e30f;
-  return w & 0xFFFFu;
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kWarps * 32) append4_kernel(const AppendParams p) {
+__device__ __forceinline__ float fmin3(float a, float b, float c) {
+  float d;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// A coefficient of two neighbouring elements, as packed floats: high and low parts.
+struct Pair {
+  uint64_t hi, lo;
+};
+
+// Two outputs x a + y b (neighbouring elements), times r: their bf16 values (low
+// half first).  `wrong` collects bits where the bounds round differently; emin,
+// emax: the bounds' range.
+__device__ __forceinline__ uint32_t round_pair(uint64_t x, const Pair& a, uint64_t y, const Pair& b, uint64_t r,
+                                               uint64_t unit, bool normed, uint32_t& wrong, float& emin, float& emax) {
+  const uint64_t q = fma_f32x2(y, b.hi, fma_f32x2(y, b.lo, mul_f32x2(x, a.lo)));
+  uint64_t t = fma_f32x2(x, a.hi, q);
+  float q0, q1, t0, t1, e0, e1;
+  f32x2_split(q, q0, q1);
+  f32x2_split(t, t0, t1);
+  const uint64_t e = mul_f32x2(f32x2(fmaxf(fabsf(q0), fabsf(t0)), fmaxf(fabsf(q1), fabsf(t1))), unit);
+  if (normed) t = mul_f32x2(t, r);
+  f32x2_split(e, e0, e1);
+  emin = fmin3(emin, e0, e1);
+  emax = fmax3(emax, e0, e1);
+  float l0, l1, h0, h1;
+  f32x2_split(fma_f32x2(e, f32x2(-1.f, -1.f), t), l0, l1);
+  f32x2_split(add_f32x2(t, e), h0, h1);
+  const uint32_t lo = pack_bf16x2(l0, l1), hi = pack_bf16x2(h0, h1);
+  wrong |= lo ^ hi;
+  return lo;
+}
+
+// POW2: both pool scales are powers of two (e2m1_pow2).
+template <int D, bool POW2>
+__global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) append4_kernel(const AppendParams p) {
   constexpr int H = D / 2;
+  __shared__ float4 s_angle[kMaxTokens][H];  // sine and cosine, as float pairs
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int S = p.splits;
-  const long long gw = static_cast<long long>(blockIdx.x) * kWarps + warp;
-  const int t = static_cast<int>(gw / S), sp = static_cast<int>(gw % S);  // token; heads sp, sp + S, ...
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int S = p.splits;           // warps of a token
+  const int tpc = kWarps / S;       // tokens of the CTA
+  const int t0 = blockIdx.x * tpc;
+  const int t = t0 + warp / S, sp = warp % S;  // this warp: heads sp, sp + S, ... of token t
   const bool live = t < p.T;
-  const bool has = lane < D / 4;  // lanes holding elements (e, e + 1) and (e + D/2, e + 1 + D/2)
+  const bool has = lane < D / 4;    // lanes holding elements (e, e + 1) and (e + D/2, e + 1 + D/2)
   const int e = 2 * lane;
 
-  // Before the wait: the slot and the angles (positions, rows, slots, table only).
+  // Before the wait: the angles and the slot (positions, rows, slots, table only).
+  for (int i = tid; i < tpc * H; i += kWarps * 32) {
+    const int ti = i / H, f = i % H;
+    const int pos = t0 + ti < p.T ? p.positions[t0 + ti] : -1;
+    if (pos < 0) continue;
+    DF sn, cs;
+    angle_sincos(pos, p.inv_freq[f], sn, cs);
+    s_angle[ti][f] = make_float4(sn.hi, sn.lo, cs.hi, cs.lo);
+  }
   const int pos = live ? p.positions[t] : -1;
   long long slot = -1;
   int bad = 0;
@@ -92,93 +149,121 @@ __global__ void __launch_bounds__(kWarps * 32) append4_kernel(const AppendParams
       }
     }
   }
-  DF sn[2] = {{0.f, 0.f}, {0.f, 0.f}}, cs[2] = {{1.f, 0.f}, {1.f, 0.f}};
-  if (has && pos >= 0) {
-#pragma unroll
-    for (int k = 0; k < 2; ++k) angle_sincos(pos, p.inv_freq[e + k], sn[k], cs[k]);
-  }
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  __syncthreads();
   if (!live) return;
   if (bad && sp == 0 && lane == 0 && p.status != nullptr) atomicOr(p.status, bad);
 
-  // QK-norm weights of elements e, e + 1, e + D/2, e + 1 + D/2: queries, keys
-  float4 gam[2] = {make_float4(1.f, 1.f, 1.f, 1.f), make_float4(1.f, 1.f, 1.f, 1.f)};
-#pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    const uint16_t* g = w == 0 ? p.q_norm_w : p.k_norm_w;
-    if (g != nullptr && has) {
-      const uint32_t a = *reinterpret_cast<const uint32_t*>(g + e), b = *reinterpret_cast<const uint32_t*>(g + H + e);
-      gam[w] = make_float4(bf16_lo(a), bf16_hi(a), bf16_lo(b), bf16_hi(b));
-    }
+  // sine and cosine of elements e, e + 1
+  float4 an[2] = {make_float4(0.f, 0.f, 1.f, 0.f), make_float4(0.f, 0.f, 1.f, 0.f)};
+  if (has && pos >= 0) {
+    an[0] = s_angle[warp / S][e];
+    an[1] = s_angle[warp / S][e + 1];
   }
+  // The coefficients with the QK-norm weights: the queries', then the keys'.
+  Coefs co[2];
+  Pair c1, s2, c2, s1;  // of x1 and x2 in the low half's outputs, of x2 and x1 in the high half's
+  auto set_weights = [&](const uint16_t* w) {
+    float4 g = make_float4(1.f, 1.f, 1.f, 1.f);  // of elements e, e + 1, e + D/2, e + 1 + D/2
+    if (w != nullptr && has) {
+      const uint32_t a = *reinterpret_cast<const uint32_t*>(w + e), b = *reinterpret_cast<const uint32_t*>(w + H + e);
+      g = make_float4(bf16_lo(a), bf16_hi(a), bf16_lo(b), bf16_hi(b));
+    }
+    co[0] = coefs_of(DF{an[0].x, an[0].y}, DF{an[0].z, an[0].w}, g.x, g.z);
+    co[1] = coefs_of(DF{an[1].x, an[1].y}, DF{an[1].z, an[1].w}, g.y, g.w);
+    c1 = {f32x2(co[0].gc1.hi, co[1].gc1.hi), f32x2(co[0].gc1.lo, co[1].gc1.lo)};
+    s2 = {f32x2(-co[0].gs2.hi, -co[1].gs2.hi), f32x2(-co[0].gs2.lo, -co[1].gs2.lo)};
+    c2 = {f32x2(co[0].gc2.hi, co[1].gc2.hi), f32x2(co[0].gc2.lo, co[1].gc2.lo)};
+    s1 = {f32x2(co[0].gs1.hi, co[1].gs1.hi), f32x2(co[0].gs1.lo, co[1].gs1.lo)};
+  };
   const float eps32 = static_cast<float>(p.norm_eps);
 
-  // ---- rotated heads: queries, then keys ----
-  const int nrot = p.hq + p.hkv;
   uint8_t* kpage = reinterpret_cast<uint8_t*>(p.k_pool) + static_cast<size_t>(slot >= 0 ? slot / kPage : 0) * (36 * D);
   const size_t head_stride = static_cast<size_t>(p.num_pages) * (36 * D);
   const int j = slot >= 0 ? static_cast<int>(slot % kPage) : 0;
-#pragma unroll 1
-  for (int h0 = sp; h0 < nrot; h0 += S * kHeadsAtOnce) {
-    uint32_t xlo[kHeadsAtOnce], xhi[kHeadsAtOnce];
+  const uint16_t* qrow = p.q + static_cast<size_t>(t) * p.hq * D + e;
+  const uint16_t* krow = p.k + static_cast<size_t>(t) * p.hkv * D + e;
+  uint16_t* orow = p.q_out + static_cast<size_t>(t) * p.hq * D + e;
+  const bool reads = has && pos >= 0;
+  // One head's rotated elements (zero for an inactive token).
+  auto rotate = [&](uint32_t xl, uint32_t xh, bool normed, uint32_t& lo, uint32_t& hi) {
+    lo = hi = 0u;
+    if (pos < 0) return;
+    const uint64_t x1 = f32x2(bf16_lo(xl), bf16_hi(xl)), x2 = f32x2(bf16_lo(xh), bf16_hi(xh));
+    uint64_t r = 0, unit = f32x2(3.5f * 0x1p-24f, 3.5f * 0x1p-24f);
+    if (normed) {
+      float q0, q1;
+      f32x2_split(fma_f32x2(x1, x1, mul_f32x2(x2, x2)), q0, q1);
+      float ss = q0 + q1;
 #pragma unroll
-    for (int u = 0; u < kHeadsAtOnce; ++u) {
-      const int hh = h0 + S * u;
-      xlo[u] = xhi[u] = 0u;
-      if (hh < nrot && has && pos >= 0) {
-        const uint16_t* src = hh < p.hq ? p.q + (static_cast<size_t>(t) * p.hq + hh) * D
-                                        : p.k + (static_cast<size_t>(t) * p.hkv + (hh - p.hq)) * D;
-        xlo[u] = *reinterpret_cast<const uint32_t*>(src + e);
-        xhi[u] = *reinterpret_cast<const uint32_t*>(src + H + e);
-      }
+      for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      const float v = __fadd_rn(__fmul_rn(ss, 1.f / D), eps32);
+      const float r0 = rsqrtf(v);
+      const float rr = __fmaf_rn(0.5f * r0, __fmaf_rn(-__fmul_rn(v, r0), r0, 1.f), r0);
+      r = f32x2(rr, rr);
+      unit = f32x2(12.f * 0x1p-24f * rr, 12.f * 0x1p-24f * rr);
     }
+    uint32_t wrong = 0u;
+    float emin = 1.f, emax = 0.f;
+    lo = round_pair(x1, c1, x2, s2, r, unit, normed, wrong, emin, emax);
+    hi = round_pair(x2, c2, x1, s1, r, unit, normed, wrong, emin, emax);
+    // (bounds that are zero, tiny, huge or NaN leave it to the float pairs)
+    const bool certain = wrong == 0u && emin > 1e-30f && emax < 1e30f;
+    if (__any_sync(0xffffffffu, has && !certain)) {
+      const uint2 x = rotate_exact<D>(xl, xh, co[0], co[1], normed, eps32);
+      lo = x.x;
+      hi = x.y;
+    }
+  };
+
+  // ---- query heads ----
+  uint32_t xlo[kHeadsAtOnce], xhi[kHeadsAtOnce];
+  auto load = [&](const uint16_t* base, int heads, int h0, int u) {
+    const int hh = h0 + S * u;
+    xlo[u] = xhi[u] = 0u;
+    if (hh < heads && reads) {
+      xlo[u] = *reinterpret_cast<const uint32_t*>(base + hh * D);
+      xhi[u] = *reinterpret_cast<const uint32_t*>(base + hh * D + H);
+    }
+  };
+#pragma unroll
+  for (int u = 0; u < kHeadsAtOnce; ++u) load(qrow, p.hq, sp, u);
+  set_weights(p.q_norm_w);
+#pragma unroll 1
+  for (int h0 = sp; h0 < p.hq; h0 += S * kHeadsAtOnce) {
 #pragma unroll
     for (int u = 0; u < kHeadsAtOnce; ++u) {
       const int hh = h0 + S * u;
-      if (hh >= nrot) break;
-      const bool is_q = hh < p.hq;
-      if (!is_q && slot < 0) continue;
-      uint32_t lo = 0u, hi = 0u;  // (an inactive token's queries are zero)
-      if (pos >= 0) {
-        const float4 g = gam[is_q ? 0 : 1];
-        const bool normed = (is_q ? p.q_norm_w : p.k_norm_w) != nullptr;
-        const float x1[2] = {bf16_lo(xlo[u]), bf16_hi(xlo[u])}, x2[2] = {bf16_lo(xhi[u]), bf16_hi(xhi[u])};
-        float r = 1.f, unit = 0x1p-21f;
-        if (normed) {
-          float ss = fmaf(x1[0], x1[0], x1[1] * x1[1]) + fmaf(x2[0], x2[0], x2[1] * x2[1]);
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-          r = rsqrtf(ss * (1.f / D) + eps32);
-          unit = 0x1p-20f * r;
-        }
-        bool certain = true;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const float g1 = k ? g.y : g.x, g2 = k ? g.w : g.z;
-          const float a = x1[k] * (g1 * cs[k].hi), b = x2[k] * (g2 * sn[k].hi);
-          const float c = x2[k] * (g2 * cs[k].hi), d = x1[k] * (g1 * sn[k].hi);
-          lo |= round_certain((a - b) * r, (fabsf(a) + fabsf(b)) * unit, certain) << (16 * k);
-          hi |= round_certain((c + d) * r, (fabsf(c) + fabsf(d)) * unit, certain) << (16 * k);
-        }
-        if (__any_sync(0xffffffffu, has && !certain)) {
-          const uint2 x = rotate_exact<D>(xlo[u], xhi[u], sn[0], cs[0], sn[1], cs[1], g, normed, p.norm_eps);
-          lo = x.x;
-          hi = x.y;
-        }
-        if (!has) lo = hi = 0u;
-      }
-      if (is_q) {
-        if (has) {
-          uint16_t* dst = p.q_out + (static_cast<size_t>(t) * p.hq + hh) * D;
-          *reinterpret_cast<uint32_t*>(dst + e) = lo;
-          *reinterpret_cast<uint32_t*>(dst + H + e) = hi;
-        }
-      } else {
-        store_key_e2m1<D>(kpage + static_cast<size_t>(hh - p.hq) * head_stride, j, lane, has, lo, hi, p.k_scale);
+      if (hh >= p.hq) break;
+      const uint32_t xl = xlo[u], xh = xhi[u];
+      load(qrow, p.hq, h0 + S * kHeadsAtOnce, u);
+      uint32_t lo, hi;
+      rotate(xl, xh, p.q_norm_w != nullptr, lo, hi);
+      if (has) {
+        *reinterpret_cast<uint32_t*>(orow + hh * D) = lo;
+        *reinterpret_cast<uint32_t*>(orow + hh * D + H) = hi;
       }
     }
   }
   if (slot < 0) return;
+  // ---- key heads ----
+#pragma unroll
+  for (int u = 0; u < kHeadsAtOnce; ++u) load(krow, p.hkv, sp, u);
+  set_weights(p.k_norm_w);
+#pragma unroll 1
+  for (int h0 = sp; h0 < p.hkv; h0 += S * kHeadsAtOnce) {
+#pragma unroll
+    for (int u = 0; u < kHeadsAtOnce; ++u) {
+      const int hh = h0 + S * u;
+      if (hh >= p.hkv) break;
+      const uint32_t xl = xlo[u], xh = xhi[u];
+      load(krow, p.hkv, h0 + S * kHeadsAtOnce, u);
+      uint32_t lo, hi;
+      rotate(xl, xh, p.k_norm_w != nullptr, lo, hi);
+      if (!has) lo = hi = 0u;
+      store_key_e2m1<D, POW2>(kpage + static_cast<size_t>(hh) * head_stride, j, lane, has, lo, hi, p.k_scale);
+    }
+  }
   // ---- value heads, two at a time: lanes 0 .. 15 and 16 .. 31 ----
   uint8_t* vpage = reinterpret_cast<uint8_t*>(p.v_pool) + static_cast<size_t>(slot / kPage) * (36 * D);
   const int l = lane & 15;
@@ -188,13 +273,14 @@ __global__ void __launch_bounds__(kWarps * 32) append4_kernel(const AppendParams
     const bool mine = l < D / 8 && vh < p.hkv;
     uint4 x = make_uint4(0u, 0u, 0u, 0u);
     if (mine) x = reinterpret_cast<const uint4*>(p.v + (static_cast<size_t>(t) * p.hkv + vh) * D)[l];
-    store_value_e2m1<D>(vpage + static_cast<size_t>(vh) * head_stride, j, l, mine, x, p.v_scale);
+    store_value_e2m1<D, POW2>(vpage + static_cast<size_t>(vh) * head_stride, j, l, mine, x, p.v_scale);
   }
 }
 
-template <int D>
+template <int D, bool POW2>
 cudaError_t launch_t(const AppendParams& p, cudaStream_t stream) {
-  const long long ctas = (static_cast<long long>(p.T) * p.splits + kWarps - 1) / kWarps;
+  const long long tpc = kWarps / p.splits;
+  const long long ctas = (p.T + tpc - 1) / tpc;
   if (ctas > 0x7fffffffll) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas));
@@ -205,7 +291,7 @@ cudaError_t launch_t(const AppendParams& p, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, append4_kernel<D>, p);
+  return cudaLaunchKernelEx(&cfg, append4_kernel<D, POW2>, p);
 }
 
 }  // namespace
@@ -214,14 +300,13 @@ bool append4_takes(int tokens) { return tokens >= device_sm_count(); }
 
 cudaError_t launch_append4(const AppendParams& p_in, int head_dim, cudaStream_t stream) {
   AppendParams p = p_in;
-  // enough warps for kWarpsPerSm on every SM, a batch of heads for each at least
-  const long long want = (static_cast<long long>(kWarpsPerSm) * device_sm_count() + p.T - 1) / p.T;
-  const int most = std::max(1, (p.hq + p.hkv) / kHeadsAtOnce);
-  p.splits = static_cast<int>(std::max<long long>(1, std::min<long long>(most, want)));
+  // one token per CTA, or two once there are more than a wave of CTAs
+  p.splits = kWarps / (p.T > static_cast<long long>(kCtasPerSm) * device_sm_count() ? 2 : 1);
+  const bool pow2 = rope::e2m1_pow2(p.k_scale) && rope::e2m1_pow2(p.v_scale);
   switch (head_dim) {
-    case 64: return launch_t<64>(p, stream);
-    case 96: return launch_t<96>(p, stream);
-    case 128: return launch_t<128>(p, stream);
+    case 64: return pow2 ? launch_t<64, true>(p, stream) : launch_t<64, false>(p, stream);
+    case 96: return pow2 ? launch_t<96, true>(p, stream) : launch_t<96, false>(p, stream);
+    case 128: return pow2 ? launch_t<128, true>(p, stream) : launch_t<128, false>(p, stream);
     default: return cudaErrorInvalidValue;
   }
 }

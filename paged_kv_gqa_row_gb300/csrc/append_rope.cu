@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(kWarps * 32) append_rope_kernel(const AppendPa
       if (!is_q) {  // (a key head with a slot: the token is active)
         uint32_t lo = 0u, hi = 0u;
         if (has) rotate_pairs(xlo[j], xhi[j], s_coef[1], e, norm_k, norm_k ? s_r[l] : DF{1.f, 0.f}, lo, hi);
-        store_key_e2m1<D>(dst8, static_cast<int>(slot % kPage), lane, has, lo, hi, p.k_scale);
+        store_key_e2m1<D, false>(dst8, static_cast<int>(slot % kPage), lane, has, lo, hi, p.k_scale);
         continue;
       }
     }
@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kWarps * 32) append_rope_kernel(const AppendPa
       if constexpr (KV4) {
         uint8_t* page = reinterpret_cast<uint8_t*>(p.v_pool) +
                         (static_cast<size_t>(vh) * p.num_pages + static_cast<size_t>(slot / kPage)) * (36 * D);
-        store_value_e2m1<D>(page, static_cast<int>(slot % kPage), lane, lane < D / 8,
+        store_value_e2m1<D, false>(page, static_cast<int>(slot % kPage), lane, lane < D / 8,
                             lane < D / 8 ? src[lane] : make_uint4(0u, 0u, 0u, 0u), p.v_scale);
         continue;
       }

@@ -24,6 +24,7 @@
 #include <cuda_fp8.h>
 
 #include <cstdint>
+#include <cstring>
 
 namespace lnk {
 namespace rope {
@@ -200,11 +201,45 @@ __device__ __forceinline__ uint32_t e2m1_pair(float lo, float hi) {
 // order is the order of magnitudes, with NaN above infinity).
 __device__ __forceinline__ uint32_t bf16x2_absmax(uint32_t w) { return max(w & 0x7FFFu, (w >> 16) & 0x7FFFu); }
 
-// A block of 16: its scale code, and the value `d` that its elements are
-// divided by (0: the block stores zero codes).  absmax: the block's largest
-// magnitude as bf16 bits; six_ps = fl32(6 * ps).
-__device__ __forceinline__ uint32_t e2m1_scale(uint32_t absmax, float six_ps, float ps, float& d) {
-  const float t = __fdiv_rn(__uint_as_float(absmax << 16), six_ps);
+// Whether a pool scale is a power of two (in a range that leaves its products
+// and reciprocals normal): the quantizer then needs no division, see below.
+__host__ __device__ __forceinline__ bool e2m1_pow2(float ps) {
+#ifdef __CUDA_ARCH__
+  const uint32_t u = __float_as_uint(ps);
+#else
+  uint32_t u;
+  memcpy(&u, &ps, 4);
+#endif
+  return (u & 0x007FFFFFu) == 0u && (u >> 23) >= 127u - 60u && (u >> 23) <= 127u + 60u;
+}
+
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// A block of 16: its scale code, and its divisor d (0: the block stores zero
+// codes) or, for POW2, the reciprocal of d.  absmax: the block's largest
+// magnitude as bf16 bits.
+//
+// POW2 (ps is a power of two): rounding a quotient to float32 and then to E4M3
+// or E2M1 is decided by which side of a border B (a midpoint of the format) the
+// exact quotient lies on.  The numerator has 8 significant bits and B times the
+// denominator at most 7, so a quotient that is not on the border is off it by at
+// least 2^-9 of it, and one that is on it must be met exactly.  A product with
+// the reciprocal (relative error below 2^-21), rounded to a grid that holds the
+// borders and is finer than 2^-11 of them, is on the same side: 16 significant
+// bits for the scale, multiples of 2^-16 for the elements (borders 0.25 .. 5).
+template <bool POW2>
+__device__ __forceinline__ uint32_t e2m1_scale(uint32_t absmax, float ps, float& d) {
+  const float a = __uint_as_float(absmax << 16);
+  float t;
+  if constexpr (POW2) {
+    t = __uint_as_float((__float_as_uint(__fmul_rn(a, rcp_approx(6.f * ps))) + 0x80u) & 0xFFFFFF00u);
+  } else {
+    t = __fdiv_rn(a, __fmul_rn(6.f, ps));
+  }
   uint32_t s = __nv_cvt_float_to_fp8(t, __NV_SATFINITE, __NV_E4M3) & 0xFFu;
   if (absmax > 0x7F80u) s = 0x7Fu;  // NaN
   const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(s), __NV_E4M3);
@@ -212,14 +247,27 @@ __device__ __forceinline__ uint32_t e2m1_scale(uint32_t absmax, float six_ps, fl
   if (!(d > 0.f)) {
     d = 0.f;
     if (s != 0x7Fu) s = 0u;
+  } else if (POW2) {
+    d = rcp_approx(d);
   }
   return s;
 }
 
-// The byte of codes of two bf16 values (low half first) of a block with divisor d.
+// The byte of codes of two bf16 values (low half first) of a block with d from e2m1_scale.
+template <bool POW2>
 __device__ __forceinline__ uint32_t e2m1_codes(uint32_t bits, float d) {
-  if (d == 0.f) return 0u;
-  return e2m1_pair(__fdiv_rn(__uint_as_float(bits << 16), d), __fdiv_rn(__uint_as_float(bits & 0xFFFF0000u), d));
+  const uint32_t x0 = bits << 16, x1 = bits & 0xFFFF0000u;
+  if constexpr (POW2) {
+    // to multiples of 2^-16 (magnitudes beyond 64 saturate anyway); the sign is the value's own
+    const float u0 = __fsub_rn(__fadd_rn(__fmul_rn(__uint_as_float(x0), d), 192.f), 192.f);
+    const float u1 = __fsub_rn(__fadd_rn(__fmul_rn(__uint_as_float(x1), d), 192.f), 192.f);
+    const uint32_t c = e2m1_pair(__uint_as_float((__float_as_uint(u0) & 0x7FFFFFFFu) | (x0 & 0x80000000u)),
+                                 __uint_as_float((__float_as_uint(u1) & 0x7FFFFFFFu) | (x1 & 0x80000000u)));
+    return d == 0.f ? 0u : c;
+  } else {
+    if (d == 0.f) return 0u;
+    return e2m1_pair(__fdiv_rn(__uint_as_float(x0), d), __fdiv_rn(__uint_as_float(x1), d));
+  }
 }
 
 // Byte offset of position j's scale of block b in a page of one head.
@@ -231,7 +279,7 @@ __device__ __forceinline__ int e2m1_scale_offset(int j, int b) {
 // A key row of a 4-bit pool: lane l < D/4 holds elements (2l, 2l + 1) in lo and
 // (2l + D/2, 2l + 1 + D/2) in hi, so eight lanes in a row hold a block of each
 // half.  Every lane of the warp calls it; `has`: the lane holds data.
-template <int D>
+template <int D, bool POW2>
 __device__ __forceinline__ void store_key_e2m1(uint8_t* page, int j, int lane, bool has, uint32_t lo, uint32_t hi,
                                                float ps) {
   constexpr int H = D / 2;
@@ -242,12 +290,11 @@ __device__ __forceinline__ void store_key_e2m1(uint8_t* page, int j, int lane, b
     mhi = max(mhi, __shfl_xor_sync(0xffffffffu, mhi, o));
   }
   if (!has) return;
-  const float six_ps = __fmul_rn(6.f, ps);
   float dlo, dhi;
-  const uint32_t slo = e2m1_scale(mlo, six_ps, ps, dlo), shi = e2m1_scale(mhi, six_ps, ps, dhi);
+  const uint32_t slo = e2m1_scale<POW2>(mlo, ps, dlo), shi = e2m1_scale<POW2>(mhi, ps, dhi);
   uint8_t* row = page + j * (D / 2);
-  row[lane] = static_cast<uint8_t>(e2m1_codes(lo, dlo));
-  row[H / 2 + lane] = static_cast<uint8_t>(e2m1_codes(hi, dhi));
+  row[lane] = static_cast<uint8_t>(e2m1_codes<POW2>(lo, dlo));
+  row[H / 2 + lane] = static_cast<uint8_t>(e2m1_codes<POW2>(hi, dhi));
   if ((lane & 7) == 0) {
     page[e2m1_scale_offset<D>(j, lane >> 3)] = static_cast<uint8_t>(slo);
     page[e2m1_scale_offset<D>(j, H / 16 + (lane >> 3))] = static_cast<uint8_t>(shi);
@@ -256,15 +303,15 @@ __device__ __forceinline__ void store_key_e2m1(uint8_t* page, int j, int lane, b
 
 // A value row of a 4-bit pool: lane l of those with `has` holds elements 8l ..
 // 8l + 7, so two lanes (2i, 2i + 1) hold a block.  Every lane of the warp calls it.
-template <int D>
+template <int D, bool POW2>
 __device__ __forceinline__ void store_value_e2m1(uint8_t* page, int j, int l, bool has, uint4 x, float ps) {
   uint32_t m = max(max(bf16x2_absmax(x.x), bf16x2_absmax(x.y)), max(bf16x2_absmax(x.z), bf16x2_absmax(x.w)));
   m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
   if (!has) return;
   float d;
-  const uint32_t s = e2m1_scale(m, __fmul_rn(6.f, ps), ps, d);
-  const uint32_t codes = e2m1_codes(x.x, d) | (e2m1_codes(x.y, d) << 8) | (e2m1_codes(x.z, d) << 16) |
-                         (e2m1_codes(x.w, d) << 24);
+  const uint32_t s = e2m1_scale<POW2>(m, ps, d);
+  const uint32_t codes = e2m1_codes<POW2>(x.x, d) | (e2m1_codes<POW2>(x.y, d) << 8) |
+                         (e2m1_codes<POW2>(x.z, d) << 16) | (e2m1_codes<POW2>(x.w, d) << 24);
   *reinterpret_cast<uint32_t*>(page + j * (D / 2) + 4 * l) = codes;
   if ((l & 1) == 0) page[e2m1_scale_offset<D>(j, l >> 1)] = static_cast<uint8_t>(s);
 }

@@ -272,3 +272,38 @@ def test_read_tokens_gives_the_stored_values(kind, hkv, d):
     for i, s in enumerate(slots):
         want = bits[0][:, s] if 0 <= s < n_pages * 64 else np.zeros((hkv, d), dtype=np.uint16)
         assert np.array_equal(got[i], want), i
+
+
+@pytest.mark.parametrize("ps", [1.0, 0.25, 2.0 ** -20, 2.0 ** 30, 2.0 ** -70, 0.37, 3.0])
+@pytest.mark.parametrize("tokens", [12, 300])
+def test_values_of_every_bit_pattern(tokens, ps):
+    """Value rows of arbitrary bf16 bits (subnormals, infinities and NaN among them),
+    of elements that lie on the formats' borders, and of wild ranges, in launches of
+    either form and with pool scales that are powers of two or not."""
+    import paged_kv_gqa_row_gb300 as lnk
+    d, hkv = 128, 3
+    rng = np.random.RandomState(tokens + int(abs(np.log2(ps)) * 10))
+    bits = rng.randint(0, 1 << 16, (tokens, hkv, d)).astype(np.uint16)
+    # blocks of exact borders: multiples of a scale value times the borders' halves
+    scale = ofp8.decode(rng.randint(8, 120, (tokens, d // 16)).astype(np.uint8)) * ps
+    grid = rng.choice([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0, 0.5, 3.0], (tokens, d)) * rng.choice([-1, 1], (tokens, d))
+    exact = np.repeat(scale, 16, axis=-1) * grid
+    exact[:, ::16] = scale * 6
+    small = (np.abs(exact) < 1e37) & (np.abs(exact) > 1e-37)
+    bits[:, 0] = obf16.from_f64(np.where(small, exact, 1.0))
+    bits[:, 1] = obf16.from_f64(rng.standard_normal((tokens, d)) * ps * 2.0 ** rng.uniform(-12, 14, (tokens, 1)))
+    codes, scales = ofp4.quantize(bits, ps)
+    pages = tokens // 64 + 1
+    want = np.full((hkv, pages, 36 * d), 0xEE, dtype=np.uint8)
+    for t in range(tokens):
+        for h in range(hkv):
+            ofp4.write_row(want[h, t // 64], t % 64, codes[t, h], scales[t, h])
+    desc = lnk.attn_desc(hkv, hkv, d, pages, 1, pages, kv_dtype=lnk.KV_E2M1, k_scale=ps, v_scale=ps)
+    kp = d8(np.zeros_like(want))
+    vp = d8(np.full_like(want, 0xEE))
+    q = torch.zeros((tokens, hkv, d), dtype=torch.int16, device="cuda")
+    lnk.lnk_paged_append_rope(desc, lnk.rope_desc(1e4), q, q, d16(bits), d32(np.arange(tokens)), d32(np.zeros(tokens)),
+                              None, d32([np.arange(pages)]), None, None, 0.0, kp, vp, torch.empty_like(q), tokens)
+    torch.cuda.synchronize()
+    got = u8(vp)
+    assert np.array_equal(got, want), f"{int(np.sum(got != want))} bytes differ"
