@@ -48,8 +48,10 @@
 //  * warps 12-15 convert: a thread takes 16 dimensions of one key (8 code bytes
 //    and their scale), converts, scales and stores them as two 16-byte pieces of
 //    the swizzled tile (code times scale is exact in f16), and zeroes the value
-//    rows outside the real keys; a warp then arrives on rank 0's K or V barrier,
-//    so the relay falls away;
+//    rows outside the real keys; then the warps arrive on their CTA's K or V
+//    barrier, and in rank 1 two relay threads pass that on (the arrival that
+//    publishes stores to the other CTA takes 600 to 900 cycles: made by the
+//    converting warps themselves, it doubled the time of a step);
 //  * queries and P are f16 too (both operands of a product have one type).
 // Sixteen warps share the SM's registers unevenly (setmaxnreg): the two softmax
 // warpgroups take 176 a thread, the other two 80.
@@ -146,34 +148,48 @@ __device__ __forceinline__ void step_entries(const ChunkParams& p, const int* ru
   if (lp + 1 <= (run_kmax[c.run] - 1) / kPage) eb = trow[lp + 1];
 }
 
-// Converts `units` blocks per thread of one 64-column box: key j, block b of the
-// packed page `src` (NB4 of its blocks, from b0) into row j of the swizzled f16
-// tile `dst`.  Keys outside [x, y) get zeros.
-template <int D, int NB4>
-__device__ __forceinline__ void convert_box(const uint8_t* src, uint8_t* dst, int b0, int t, int x, int y) {
-  constexpr int kRowsAtOnce = kConvertThreads / NB4;
-  static_assert(kPage % kRowsAtOnce == 0 || kRowsAtOnce % kPage == 0, "whole passes");
-  const int lb = t % NB4;
+// One 64-column box of a packed page for the converting warps: NBLK of the row's
+// blocks, from b0; thread t takes block b0 + t % NBLK of rows t / NBLK, + kAtOnce,
+// ...  Loads and stores are apart, so that the loads of several boxes are in
+// flight before the first store.
+template <int D, int NBLK>
+struct Box {
+  static constexpr int kAtOnce = kConvertThreads / NBLK;  // rows
+  static constexpr int kUnits = kAtOnce >= kPage ? 1 : kPage / kAtOnce;
+  static_assert(kPage % kAtOnce == 0, "whole passes");
+  uint2 w[kUnits];     // 16 codes
+  uint32_t s[kUnits];  // their scale
+
+  __device__ __forceinline__ void load(const uint8_t* src, int b0, int t) {
+    const int b = b0 + t % NBLK;
 #pragma unroll
-  for (int j0 = 0; j0 < kPage; j0 += kRowsAtOnce) {
-    const int j = j0 + t / NB4;
-    if (kRowsAtOnce > kPage && j >= kPage) break;
-    const uint2 w = *reinterpret_cast<const uint2*>(src + j * (D / 2) + (b0 + lb) * 8);
-    uint32_t s = src[32 * D + ((j & 3) * (D / 16) + b0 + lb) * 16 + (j >> 2)];
-    if (j < x || j >= y) s = 0u;  // (codes are finite: zero)
-    const uint32_t s2 = e4m3x2_to_f16x2(s | (s << 8));
-    uint32_t lo[4], hi[4];
-    e2m1x8_to_f16x2x4(w.x, lo);
-    e2m1x8_to_f16x2x4(w.y, hi);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      lo[i] = mul_f16x2(lo[i], s2);
-      hi[i] = mul_f16x2(hi[i], s2);
+    for (int u = 0; u < kUnits; ++u) {
+      const int j = u * kAtOnce + t / NBLK;
+      w[u] = *reinterpret_cast<const uint2*>(src + j * (D / 2) + b * 8);
+      s[u] = src[32 * D + ((j & 3) * (D / 16) + b) * 16 + (j >> 2)];
     }
-    *reinterpret_cast<uint4*>(dst + swz128(j, 2 * lb)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-    *reinterpret_cast<uint4*>(dst + swz128(j, 2 * lb + 1)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
   }
-}
+  // Into the swizzled f16 tile `dst`; rows outside [x, y) get zeros.
+  __device__ __forceinline__ void store(uint8_t* dst, int t, int x, int y) const {
+    const int lb = t % NBLK;
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+      const int j = u * kAtOnce + t / NBLK;
+      const uint32_t sc = j < x || j >= y ? 0u : s[u];  // (codes are finite: zero)
+      const uint32_t s2 = e4m3x2_to_f16x2(sc | (sc << 8));
+      uint32_t lo[4], hi[4];
+      e2m1x8_to_f16x2x4(w[u].x, lo);
+      e2m1x8_to_f16x2x4(w[u].y, hi);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        lo[i] = mul_f16x2(lo[i], s2);
+        hi[i] = mul_f16x2(hi[i], s2);
+      }
+      *reinterpret_cast<uint4*>(dst + swz128(j, 2 * lb)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      *reinterpret_cast<uint4*>(dst + swz128(j, 2 * lb + 1)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    }
+  }
+};
 
 template <int D, bool KV4>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<KV4>::kThreads, 1)
@@ -278,8 +294,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<KV4>::kThreads
 
   if (tid == 0) {
     // rank 0's full barriers also count the relay's arrival for rank 1's copy
-    // (4-bit pools: one arrival of each converting warp of both CTAs)
-    const int nfull = KV4 ? 8 : (rank == 0 ? 2 : 1);
+    // (4-bit pools: the converting warps arrive on their own CTA's barrier)
+    const int nfull = (KV4 ? kConvertThreads / 32 : 1) + (rank == 0 ? 1 : 0);
     for (int s = 0; s < kStagesK; ++s) {
       mbar_init(smem_addr(kfull + s), nfull);
       mbar_init(smem_addr(kempty + s), 1);
@@ -493,6 +509,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<KV4>::kThreads
     } else if (warp == 1) {
       if (rank != 0) {
         // ============================ relay (rank 1) ==========================
+        if (KV4 && lane == 0) {
+          // the keys' relay: publishes what this CTA's warps converted
+          const uint32_t kfull0 = mapa_shared(smem_addr(kfull), 0);
+          for (int j = 0; j < nsteps; ++j) {
+            const int sk = j % kStagesK;
+            if (!mbar_wait(smem_addr(kfull + sk), (j / kStagesK) & 1, abort_flag)) break;
+            mbar_arrive_cluster(kfull0 + sk * 8);
+          }
+        }
         if (!KV4 && lane == 0 && nsteps > 0) {
           const uint32_t kfull0 = mapa_shared(smem_addr(kfull), 0);
           const uint32_t vfull0 = mapa_shared(smem_addr(vfull), 0);
@@ -538,6 +563,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<KV4>::kThreads
         }
       }
     } else if (warp == R::kPvWarp) {
+      if (KV4 && rank != 0 && lane == 0) {
+        // the values' relay (rank 1)
+        const uint32_t vfull0 = mapa_shared(smem_addr(vfull), 0);
+        for (int j = 0; j < nsteps; ++j) {
+          const int sv = j % kStagesV;
+          if (!mbar_wait(smem_addr(vfull + sv), (j / kStagesV) & 1, abort_flag)) break;
+          mbar_arrive_cluster(vfull0 + sv * 8);
+        }
+      }
       if (rank == 0 && lane == 0 && nsteps > 0) {
         // ========================= P.V issuer (rank 0) ========================
         // One thread issues every P.V, in step order: O accumulates in order,
@@ -569,8 +603,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<KV4>::kThreads
     // ===================== conversion (4-bit pools) =======================
     setmaxnreg_dec<kRegsOther>();
     const int t = tid - R::kConvertWarp * 32;
-    const uint32_t kfull0 = mapa_shared(smem_addr(kfull), 0);
-    const uint32_t vfull0 = mapa_shared(smem_addr(vfull), 0);
     for (int j = 0; j < nsteps; ++j) {
       const int sp = j % kRing, sk = j % kStagesK, sv = j % kStagesV;
       bool ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(rawfull + sp), (j / kRing) & 1, abort_flag));
@@ -580,31 +612,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<KV4>::kThreads
       const int2 real = raw_keys[sp];
       const uint8_t* raw = smem + L::packed + size_t(sp) * 3 * L::kPageBytes;
       uint8_t* kt = smem + L::kring + size_t(sk) * L::kKStage;
-      // this CTA's K page (masked keys' scores are replaced, whatever they are)
-      convert_box<D, 4>(raw, kt, 0, t, 0, kPage);
-      if constexpr (D > 64) convert_box<D, D / 16 - 4>(raw, kt + kBoxBytes, 4, t, 0, kPage);
+      constexpr int kRest = D > 64 ? D / 16 - 4 : 4;  // blocks past column 64
+      const int tv = static_cast<int>(rank) * 4;      // this CTA's first value block
+      {
+        // this CTA's K page (masked keys' scores are replaced, whatever they are)
+        Box<D, 4> lo;
+        Box<D, kRest> hi;
+        lo.load(raw, 0, t);
+        if constexpr (D > 64) hi.load(raw, 4, t);
+        lo.store(kt, t, 0, kPage);
+        if constexpr (D > 64) hi.store(kt + kBoxBytes, t, 0, kPage);
+      }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(kfull0 + sk * 8);
-      if (j >= kStagesV)
-        ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(vempty + sv), ((j / kStagesV) - 1) & 1, abort_flag));
-      if (!ok) break;
+      if (lane == 0) mbar_arrive(smem_addr(kfull + sk));
       // this CTA's 64 value columns of both pages (columns past D hold whatever
       // they hold: the output's columns past D are not read)
       uint8_t* vt = smem + L::vring + size_t(sv) * L::kVStage;
-#pragma unroll
-      for (int pg = 0; pg < 2; ++pg) {
-        const uint8_t* src = raw + (1 + pg) * L::kPageBytes;
-        const int x = real.x - pg * kPage, y = real.y - pg * kPage;
-        if (rank == 0) convert_box<D, 4>(src, vt + pg * kBoxBytes, 0, t, x, y);
-        else if constexpr (D > 64) convert_box<D, D / 16 - 4>(src, vt + pg * kBoxBytes, 4, t, x, y);
-      }
+      auto values = [&](auto box, bool any) {
+        auto box2 = box;
+        if (any) {
+          box.load(raw + L::kPageBytes, tv, t);
+          box2.load(raw + 2 * L::kPageBytes, tv, t);
+        }
+        // (the packed stage is in registers)
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(rawempty + sp));
+        // every warp waits, whether it has values or not: no arrival for a later
+        // use of the stage may come before all those of this one
+        if (j >= kStagesV)
+          ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(vempty + sv), ((j / kStagesV) - 1) & 1, abort_flag));
+        if (!ok || !any) return;
+        box.store(vt, t, real.x, real.y);
+        box2.store(vt + kBoxBytes, t, real.x - kPage, real.y - kPage);
+      };
+      if (rank == 0) values(Box<D, 4>{}, true);
+      else values(Box<D, kRest>{}, D > 64);
+      if (!ok) break;
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive_cluster(vfull0 + sv * 8);
-        mbar_arrive(smem_addr(rawempty + sp));
-      }
+      if (lane == 0) mbar_arrive(smem_addr(vfull + sv));
     }
   } else {
     // ============================== softmax ===============================
