@@ -80,6 +80,11 @@ struct Roles {
   static constexpr int kStagesP = KV4 ? 4 : 0;       // packed stages (4-bit pools)
 };
 constexpr int kConvertThreads = 128;
+// Step records (4-bit pools) that the producer writes and the converting and the
+// softmax warps read.  The producer records step j + 8 at the earliest when the
+// keys of step j + 4 are converted, so after Q.K^T of step j + 1, for which the
+// softmax has read the scores, and the record, of step j - 1: 16 are enough.
+constexpr int kStepRecords = 16;
 constexpr int kRegsSoftmax = 176, kRegsOther = 80;  // 256 threads of each: 65536, what the block starts with
 constexpr int kRows = 128;                // query rows per CTA = tensor-memory lanes
 constexpr int kTileRows = 2 * kRows;      // rows of a tile (both CTAs)
@@ -114,8 +119,9 @@ struct TcSmem {
   // softmax groups' hand-off: max [2][128] and ok [2][128] per step parity;
   // at the end max, sum and ok [2][128] per group
   static constexpr size_t xchg = cost + kMaxOrderedTiles * 4;
-  static constexpr size_t keys = xchg + 10 * kRows * 4;     // [kStagesP] int2: the stage's real keys [x, y)
-  static constexpr size_t end = keys + size_t(kStagesP) * 8;
+  // 4-bit pools: [kStepRecords] int4, a step's real keys [x, y), first key z and run w
+  static constexpr size_t keys = (xchg + 10 * kRows * 4 + 15) / 16 * 16;
+  static constexpr size_t end = keys + (KV4 ? size_t(kStepRecords) * 16 : 0);
   static constexpr size_t bytes = end + 1024;
   static_assert(bytes <= 227 * 1024, "one CTA's shared memory");
 };
@@ -214,7 +220,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<KV4>::kThreads
   uint64_t* odone = pvdone + 2;          // the last P.V
   uint64_t* rawfull = odone + 1;         // [kStagesP] packed stages (4-bit pools)
   uint64_t* rawempty = rawfull + kStagesP;
-  int2* raw_keys = reinterpret_cast<int2*>(smem + L::keys);
+  int4* records = reinterpret_cast<int4*>(smem + L::keys);
   int* tok_lo = reinterpret_cast<int*>(smem + L::tok);
   int* tok_hi = tok_lo + kTileRows;
   int* tok_run = tok_hi + kTileRows;
@@ -430,8 +436,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<KV4>::kThreads
           const int pa = bad_a ? 0 : ea, pb = (bad_b || eb == kPastRun) ? 0 : eb;
           if (j >= kRing && !mbar_wait(smem_addr(rawempty + sp), ((j / kRing) - 1) & 1, abort_flag)) break;
           const int kb = (run_first[cur.run] + 2 * cur.s) * kPage;
-          raw_keys[sp] = make_int2(max(run_kmin[cur.run] - kb, bad_a ? kPage : 0),
-                                   min(run_kmax[cur.run] - kb, (bad_b || eb == kPastRun) ? kPage : kStepKeys));
+          records[j % kStepRecords] =
+              make_int4(max(run_kmin[cur.run] - kb, bad_a ? kPage : 0),
+                        min(run_kmax[cur.run] - kb, (bad_b || eb == kPastRun) ? kPage : kStepKeys), kb, cur.run);
           const uint32_t fb = smem_addr(rawfull + sp);
           mbar_arrive_expect_tx(fb, 3 * L::kPageBytes);
           const uint32_t dst = smem_addr(smem + L::packed + size_t(sp) * 3 * L::kPageBytes);
@@ -609,7 +616,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<KV4>::kThreads
       if (ok && j >= kStagesK)
         ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(kempty + sk), ((j / kStagesK) - 1) & 1, abort_flag));
       if (!ok) break;
-      const int2 real = raw_keys[sp];
+      const int4 real = records[j % kStepRecords];
       const uint8_t* raw = smem + L::packed + size_t(sp) * 3 * L::kPageBytes;
       uint8_t* kt = smem + L::kring + size_t(sk) * L::kKStage;
       constexpr int kRest = D > 64 ? D / 16 - 4 : 4;  // blocks past column 64
@@ -692,18 +699,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<KV4>::kThreads
     bool ok = true, stuck = false;
     StepCursor cur;
     int ea = kPastRun, eb = kPastRun;  // table entries of the step's two pages, read one step ahead
-    if (nsteps > 0) step_entries(p, run_row, run_first, run_kmax, misc[0], cur, ea, eb);
+    if (!KV4 && nsteps > 0) step_entries(p, run_row, run_first, run_kmax, misc[0], cur, ea, eb);
     const uint32_t sc = tmem + lanes + L::kColS + static_cast<uint32_t>(grp) * kStepKeys;  // S_grp
     const uint32_t pcol = tmem + lanes + L::kColP + static_cast<uint32_t>(grp) * (kStepKeys / 2);  // P_grp
     const uint32_t sfree0 = mapa_shared(smem_addr(sfree), 0);
-    for (int j = 0; j < nsteps; ++j, cur.next(run_steps)) {
-      const int kmin = run_kmin[cur.run], kmax = run_kmax[cur.run];
-      const int lpa = run_first[cur.run] + 2 * cur.s;
-      const int kb = lpa * kPage;         // logical key of the step's first slot
-      // pages of the step that hold data: in the run and with a valid table entry
-      const bool va = ea >= 0 && ea < p.num_pages;
-      const bool vb = eb >= 0 && eb < p.num_pages;
-      {
+    auto next_step = [&] {
+      if constexpr (!KV4) cur.next(run_steps);
+    };
+    for (int j = 0; j < nsteps; ++j, next_step()) {
+      int kmin = 0, kmax = 0, kb = 0;     // kb: logical key of the step's first slot
+      bool va = false, vb = false;        // pages of the step that hold data: in the run and with a valid table entry
+      if constexpr (!KV4) {
+        kmin = run_kmin[cur.run], kmax = run_kmax[cur.run];
+        const int lpa = run_first[cur.run] + 2 * cur.s;
+        kb = lpa * kPage;
+        va = ea >= 0 && ea < p.num_pages;
+        vb = eb >= 0 && eb < p.num_pages;
         StepCursor nc = cur;
         nc.next(run_steps);
         step_entries(p, run_row, run_first, run_kmax, misc[0], nc, ea, eb);
@@ -752,10 +763,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<KV4>::kThreads
         for (int i = 0; i < kStepKeys; ++i) x[i] = -INFINITY;
       }
       // visible keys of this step for this row: [a0, e0), minus a missing page
-      const bool in_run = live && cur.run == run_id;
+      int run = cur.run;
+      int ma = va ? 0 : kPage, me = vb ? kStepKeys : kPage;  // keys on valid pages: [ma, me)
+      if constexpr (KV4) {  // (from the producer's record, published with the step's scores)
+        const int4 rec = records[j % kStepRecords];
+        ma = rec.x;
+        me = rec.y;
+        kb = rec.z;
+        run = rec.w;
+      }
+      const bool in_run = live && run == run_id;
       const int ka = in_run ? max(lo - kb, 0) : kStepKeys;
       const int ke = in_run ? max(ka, min(hi - kb, kStepKeys)) : kStepKeys;
-      const int ma = va ? 0 : kPage, me = vb ? kStepKeys : kPage;  // keys on valid pages: [ma, me)
       const int a0 = max(ka, ma), e0 = min(ke, me);
       if (!__all_sync(0xffffffffu, a0 == 0 && e0 == kStepKeys)) {
 #pragma unroll
