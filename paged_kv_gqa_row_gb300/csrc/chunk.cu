@@ -54,7 +54,14 @@
 //    converting warps themselves, it doubled the time of a step);
 //  * queries and P are f16 too (both operands of a product have one type).
 // Sixteen warps share the SM's registers unevenly (setmaxnreg): the two softmax
-// warpgroups take 176 a thread, the other two 80.
+// warpgroups take 192 a thread, the other two 64 (176 and 80: 3% slower, 200 and
+// 56: 4%).  Tile rings of four stages and three packed stages: rings of three
+// and four packed stages took 6% longer.
+// What bounds it: the converting warps and the softmax share the schedulers, and
+// a tile's start and end are not hidden (one CTA fills an SM).  Four prompts of
+// 2048 tokens, 32 query heads on 8, D = 128: 211 us, 389 TFLOP/s (bf16 pools 181
+// us); four prompts of 512 tokens over 16384 stored keys, with 32 decode rows of
+// 8192 keys: 232 us (bf16 pools 255 us), 640 TFLOP/s.
 //
 // Sources: "Mistral 7B Instruct v0.3", Entries table (prefill_paged: prompts
 // packed end to end, each token written at its place in the pool and attending
@@ -75,17 +82,17 @@ struct Roles {
   static constexpr int kSoftmaxWarp = KV4 ? 4 : 2;   // the first of eight
   static constexpr int kPvWarp = KV4 ? 2 : 10;
   static constexpr int kConvertWarp = 12;            // the first of four (4-bit pools)
-  static constexpr int kStagesK = KV4 ? 3 : 4;       // K ring (this CTA's page of a step)
-  static constexpr int kStagesV = KV4 ? 3 : 4;       // V ring (this CTA's columns of both pages)
-  static constexpr int kStagesP = KV4 ? 4 : 0;       // packed stages (4-bit pools)
+  static constexpr int kStagesK = 4;                 // K ring (this CTA's page of a step)
+  static constexpr int kStagesV = 4;                 // V ring (this CTA's columns of both pages)
+  static constexpr int kStagesP = KV4 ? 3 : 0;       // packed stages (4-bit pools)
 };
 constexpr int kConvertThreads = 128;
 // Step records (4-bit pools) that the producer writes and the converting and the
 // softmax warps read.  The producer records step j + 8 at the earliest when the
-// keys of step j + 4 are converted, so after Q.K^T of step j + 1, for which the
+// keys of step j + 5 are converted, so after Q.K^T of step j + 1, for which the
 // softmax has read the scores, and the record, of step j - 1: 16 are enough.
 constexpr int kStepRecords = 16;
-constexpr int kRegsSoftmax = 176, kRegsOther = 80;  // 256 threads of each: 65536, what the block starts with
+constexpr int kRegsSoftmax = 192, kRegsOther = 64;  // 256 threads of each: 65536, what the block starts with
 constexpr int kRows = 128;                // query rows per CTA = tensor-memory lanes
 constexpr int kTileRows = 2 * kRows;      // rows of a tile (both CTAs)
 constexpr int kStepKeys = 2 * kPage;      // keys per step
