@@ -600,7 +600,9 @@ lnk_status lnk_paged_step_attn(const lnk_attn_desc* desc, const lnk_bf16* q_rope
     c.tile_tokens = 128 / group;
     c.num_tiles = (P + kChunkHalves * c.tile_tokens - 1) / (kChunkHalves * c.tile_tokens);
     c.scale_log2 = scale_log2(desc);
-    if (launch_chunk(pools.kmap, pools.vmap, c, desc->head_dim, s) != cudaSuccess) return LNK_ECUDA;
+    const cudaError_t err = pools.k4 != nullptr ? launch_chunk4(c, desc->head_dim, s)
+                                                : launch_chunk(pools.kmap, pools.vmap, c, desc->head_dim, s);
+    if (err != cudaSuccess) return LNK_ECUDA;
   }
   if (B > 0) {
     st = decode_common(desc, q_roped + static_cast<size_t>(P) * row_elems, step_positions, table,

@@ -40,29 +40,6 @@
 // Barriers that the other CTA arrives on live in rank 0 (the P and relay
 // barriers); the 2-SM commits arrive in both CTAs at once.
 //
-// 4-bit pools (KV4, LNK_KV_E2M1): the tensor cores read f16 tiles of the same
-// layout, which four more warps make from the packed pages:
-//  * the producer loads this CTA's K page and both V pages of a step as they
-//    are (36 D bytes each, 1-D bulk copies) into a ring of packed stages, with
-//    the range of the step's keys that are real;
-//  * warps 12-15 convert: a thread takes 16 dimensions of one key (8 code bytes
-//    and their scale), converts, scales and stores them as two 16-byte pieces of
-//    the swizzled tile (code times scale is exact in f16), and zeroes the value
-//    rows outside the real keys; then the warps arrive on their CTA's K or V
-//    barrier, and in rank 1 two relay threads pass that on (the arrival that
-//    publishes stores to the other CTA takes 600 to 900 cycles: made by the
-//    converting warps themselves, it doubled the time of a step);
-//  * queries and P are f16 too (both operands of a product have one type).
-// Sixteen warps share the SM's registers unevenly (setmaxnreg): the two softmax
-// warpgroups take 192 a thread, the other two 64 (176 and 80: 3% slower, 200 and
-// 56: 4%).  Tile rings of four stages and three packed stages: rings of three
-// and four packed stages took 6% longer.
-// What bounds it: the converting warps and the softmax share the schedulers, and
-// a tile's start and end are not hidden (one CTA fills an SM).  Four prompts of
-// 2048 tokens, 32 query heads on 8, D = 128: 211 us, 389 TFLOP/s (bf16 pools 181
-// us); four prompts of 512 tokens over 16384 stored keys, with 32 decode rows of
-// 8192 keys: 232 us (bf16 pools 255 us), 640 TFLOP/s.
-//
 // Sources: "Mistral 7B Instruct v0.3", Entries table (prefill_paged: prompts
 // packed end to end, each token written at its place in the pool and attending
 // over its row's pages up to its position; step_paged); "Phi-3 Mini 4K
@@ -74,36 +51,17 @@
 namespace lnk {
 namespace {
 
-// Warp roles (see the top): with bf16 pools 11 warps, the softmax in 2-9; with
-// 4-bit pools 16 warps in whole warpgroups, as setmaxnreg asks.
-template <bool KV4>
-struct Roles {
-  static constexpr int kThreads = KV4 ? 16 * 32 : 11 * 32;
-  static constexpr int kSoftmaxWarp = KV4 ? 4 : 2;   // the first of eight
-  static constexpr int kPvWarp = KV4 ? 2 : 10;
-  static constexpr int kConvertWarp = 12;            // the first of four (4-bit pools)
-  static constexpr int kStagesK = 4;                 // K ring (this CTA's page of a step)
-  static constexpr int kStagesV = 4;                 // V ring (this CTA's columns of both pages)
-  static constexpr int kStagesP = KV4 ? 3 : 0;       // packed stages (4-bit pools)
-};
-constexpr int kConvertThreads = 128;
-// Step records (4-bit pools) that the producer writes and the converting and the
-// softmax warps read.  The producer records step j + 8 at the earliest when the
-// keys of step j + 5 are converted, so after Q.K^T of step j + 1, for which the
-// softmax has read the scores, and the record, of step j - 1: 16 are enough.
-constexpr int kStepRecords = 16;
-constexpr int kRegsSoftmax = 192, kRegsOther = 64;  // 256 threads of each: 65536, what the block starts with
+constexpr int kThreads = 11 * 32;
+constexpr int kStagesK = 4;               // K ring (this CTA's page of a step)
+constexpr int kStagesV = 4;               // V ring (this CTA's columns of both pages)
 constexpr int kRows = 128;                // query rows per CTA = tensor-memory lanes
 constexpr int kTileRows = 2 * kRows;      // rows of a tile (both CTAs)
 constexpr int kStepKeys = 2 * kPage;      // keys per step
 constexpr float kRescaleLog2 = 8.f;       // rescale O when the max grows by more than 2^8
 constexpr int kMaxOrderedTiles = 512;     // tiles ordered by cost (larger launches keep token order)
 
-template <int D, bool KV4>
+template <int D>
 struct TcSmem {
-  using R = Roles<KV4>;
-  static constexpr int kStagesK = R::kStagesK, kStagesV = R::kStagesV, kStagesP = R::kStagesP;
-  static constexpr int kPageBytes = 36 * D;                 // a packed page (4-bit pools)
   static constexpr int NB = boxes_for(D);
   static constexpr int kKStage = NB * kBoxBytes;            // one page of K, all head-dim columns
   static constexpr int kVStage = 2 * kBoxBytes;             // both pages of V, 64 head-dim columns
@@ -115,10 +73,9 @@ struct TcSmem {
   static constexpr size_t kring = 0;
   static constexpr size_t vring = kring + size_t(kStagesK) * kKStage;
   static constexpr size_t qsm = vring + size_t(kStagesV) * kVStage;  // this CTA's query rows, K-major
-  static constexpr size_t packed = qsm + size_t(NB) * kQBox;  // [kStagesP]: K page, V page a, V page b
-  static constexpr size_t bars = packed + size_t(kStagesP) * 3 * kPageBytes;
-  // kfull[K], kempty[K], vfull[V], vempty[V], sfull[2], sfree[2], pfull[2], pvdone[2], odone, rawfull[P], rawempty[P]
-  static constexpr int kNumBars = 2 * kStagesK + 2 * kStagesV + 9 + 2 * kStagesP;
+  static constexpr size_t bars = qsm + size_t(NB) * kQBox;
+  // kfull[K], kempty[K], vfull[V], vempty[V], sfull[2], sfree[2], pfull[2], pvdone[2], odone
+  static constexpr int kNumBars = 2 * kStagesK + 2 * kStagesV + 9;
   static constexpr size_t tok = bars + kNumBars * sizeof(uint64_t);
   static constexpr size_t runs = tok + 4 * kTileRows * 4;
   static constexpr size_t misc = runs + 5 * kTileRows * 4;  // [0] runs, [1] steps, [2] abort, [3] tmem, [4] tile
@@ -126,11 +83,8 @@ struct TcSmem {
   // softmax groups' hand-off: max [2][128] and ok [2][128] per step parity;
   // at the end max, sum and ok [2][128] per group
   static constexpr size_t xchg = cost + kMaxOrderedTiles * 4;
-  // 4-bit pools: [kStepRecords] int4, a step's real keys [x, y), first key z and run w
-  static constexpr size_t keys = (xchg + 10 * kRows * 4 + 15) / 16 * 16;
-  static constexpr size_t end = keys + (KV4 ? size_t(kStepRecords) * 16 : 0);
+  static constexpr size_t end = xchg + 10 * kRows * 4;
   static constexpr size_t bytes = end + 1024;
-  static_assert(bytes <= 227 * 1024, "one CTA's shared memory");
 };
 
 // Walks the steps of a tile in order: run r, step s of the run (pages
@@ -161,57 +115,11 @@ __device__ __forceinline__ void step_entries(const ChunkParams& p, const int* ru
   if (lp + 1 <= (run_kmax[c.run] - 1) / kPage) eb = trow[lp + 1];
 }
 
-// One 64-column box of a packed page for the converting warps: NBLK of the row's
-// blocks, from b0; thread t takes block b0 + t % NBLK of rows t / NBLK, + kAtOnce,
-// ...  Loads and stores are apart, so that the loads of several boxes are in
-// flight before the first store.
-template <int D, int NBLK>
-struct Box {
-  static constexpr int kAtOnce = kConvertThreads / NBLK;  // rows
-  static constexpr int kUnits = kAtOnce >= kPage ? 1 : kPage / kAtOnce;
-  static_assert(kPage % kAtOnce == 0, "whole passes");
-  uint2 w[kUnits];     // 16 codes
-  uint32_t s[kUnits];  // their scale
-
-  __device__ __forceinline__ void load(const uint8_t* src, int b0, int t) {
-    const int b = b0 + t % NBLK;
-#pragma unroll
-    for (int u = 0; u < kUnits; ++u) {
-      const int j = u * kAtOnce + t / NBLK;
-      w[u] = *reinterpret_cast<const uint2*>(src + j * (D / 2) + b * 8);
-      s[u] = src[32 * D + ((j & 3) * (D / 16) + b) * 16 + (j >> 2)];
-    }
-  }
-  // Into the swizzled f16 tile `dst`; rows outside [x, y) get zeros.
-  __device__ __forceinline__ void store(uint8_t* dst, int t, int x, int y) const {
-    const int lb = t % NBLK;
-#pragma unroll
-    for (int u = 0; u < kUnits; ++u) {
-      const int j = u * kAtOnce + t / NBLK;
-      const uint32_t sc = j < x || j >= y ? 0u : s[u];  // (codes are finite: zero)
-      const uint32_t s2 = e4m3x2_to_f16x2(sc | (sc << 8));
-      uint32_t lo[4], hi[4];
-      e2m1x8_to_f16x2x4(w[u].x, lo);
-      e2m1x8_to_f16x2x4(w[u].y, hi);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        lo[i] = mul_f16x2(lo[i], s2);
-        hi[i] = mul_f16x2(hi[i], s2);
-      }
-      *reinterpret_cast<uint4*>(dst + swz128(j, 2 * lb)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-      *reinterpret_cast<uint4*>(dst + swz128(j, 2 * lb + 1)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    }
-  }
-};
-
-template <int D, bool KV4>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<KV4>::kThreads, 1)
+template <int D>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                  const ChunkParams p) {
-  using L = TcSmem<D, KV4>;
-  using R = Roles<KV4>;
-  constexpr int kThreads = R::kThreads, kStagesK = R::kStagesK, kStagesV = R::kStagesV, kStagesP = R::kStagesP;
-  constexpr int kRing = KV4 ? kStagesP : 1;
+  using L = TcSmem<D>;
   constexpr int NB = L::NB;
   constexpr int DK = D / 16;
   extern __shared__ uint8_t smem_raw[];
@@ -225,9 +133,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<KV4>::kThreads
   uint64_t* pfull = sfree + 2;           // [2] P_b written (rank 0 only)
   uint64_t* pvdone = pfull + 2;          // [2] P.V from P_b finished (all but the last)
   uint64_t* odone = pvdone + 2;          // the last P.V
-  uint64_t* rawfull = odone + 1;         // [kStagesP] packed stages (4-bit pools)
-  uint64_t* rawempty = rawfull + kStagesP;
-  int4* records = reinterpret_cast<int4*>(smem + L::keys);
   int* tok_lo = reinterpret_cast<int*>(smem + L::tok);
   int* tok_hi = tok_lo + kTileRows;
   int* tok_run = tok_hi + kTileRows;
@@ -285,7 +190,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<KV4>::kThreads
   // loaded before any is stored.  The cluster barrier below publishes them to
   // the pair's tensor cores (each thread orders its stores before the async
   // proxy first). ----
-  if (warp >= R::kSoftmaxWarp && warp < R::kSoftmaxWarp + 4) {
+  if (warp >= 2 && warp < 6) {
     const int rl = (warp & 3) * 32 + lane;
     const int row = static_cast<int>(rank) * kRows + rl;  // token * G + head
     const int tl = row / G, g = row % G;
@@ -294,11 +199,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<KV4>::kThreads
     uint4 a[D / 8];
 #pragma unroll
     for (int c = 0; c < D / 8; ++c) a[c] = tl < nt ? src[c] : make_uint4(0u, 0u, 0u, 0u);
-    if constexpr (KV4) {
-#pragma unroll
-      for (int c = 0; c < D / 8; ++c)
-        a[c] = make_uint4(bf16x2_to_f16x2(a[c].x), bf16x2_to_f16x2(a[c].y), bf16x2_to_f16x2(a[c].z), bf16x2_to_f16x2(a[c].w));
-    }
 #pragma unroll
     for (int c = 0; c < D / 8; ++c)
       *reinterpret_cast<uint4*>(smem + L::qsm + (c >> 3) * L::kQBox + swz128(rl, c & 7)) = a[c];
@@ -307,19 +207,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<KV4>::kThreads
 
   if (tid == 0) {
     // rank 0's full barriers also count the relay's arrival for rank 1's copy
-    // (4-bit pools: the converting warps arrive on their own CTA's barrier)
-    const int nfull = (KV4 ? kConvertThreads / 32 : 1) + (rank == 0 ? 1 : 0);
     for (int s = 0; s < kStagesK; ++s) {
-      mbar_init(smem_addr(kfull + s), nfull);
+      mbar_init(smem_addr(kfull + s), rank == 0 ? 2 : 1);
       mbar_init(smem_addr(kempty + s), 1);
     }
     for (int s = 0; s < kStagesV; ++s) {
-      mbar_init(smem_addr(vfull + s), nfull);
+      mbar_init(smem_addr(vfull + s), rank == 0 ? 2 : 1);
       mbar_init(smem_addr(vempty + s), 1);
-    }
-    for (int s = 0; s < kStagesP; ++s) {
-      mbar_init(smem_addr(rawfull + s), 1);
-      mbar_init(smem_addr(rawempty + s), kConvertThreads / 32);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_addr(sfull + b), 1);
@@ -416,260 +310,134 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<KV4>::kThreads
   const int nsteps = misc[1];
   const uint32_t tmem = static_cast<uint32_t>(misc[3]);
 
-  // setmaxnreg is for whole warpgroups: each of these three branches is one (or
-  // two) of them with 4-bit pools.
-  if (KV4 ? warp < R::kSoftmaxWarp : (warp < R::kSoftmaxWarp || warp == R::kPvWarp)) {
-    if constexpr (KV4) setmaxnreg_dec<kRegsOther>();
-    if (KV4 && warp == 0) {
-      // ======================= producer of packed pages =====================
-      if (lane == 0 && nsteps > 0) {
-        StepCursor cur;
-        int ea, eb;  // table entries of the step's two pages, read one step ahead
-        step_entries(p, run_row, run_first, run_kmax, misc[0], cur, ea, eb);
-        int j = 0;
-        for (; j < nsteps; ++j, cur.next(run_steps)) {
-          const int sp = j % kRing;
-          int na, nb;
-          {
-            StepCursor nc = cur;
-            nc.next(run_steps);
-            step_entries(p, run_row, run_first, run_kmax, misc[0], nc, na, nb);
-          }
-          // a page past the run or a bad table entry loads page 0 instead (its
-          // keys are masked and its values zeroed)
-          const bool bad_a = ea >= p.num_pages || ea < 0;
-          const bool bad_b = eb != kPastRun && (eb >= p.num_pages || eb < 0);
-          if (rank == 0 && (bad_a || bad_b) && p.status != nullptr) atomicOr(p.status, LNK_DEV_BAD_PAGE);
-          const int pa = bad_a ? 0 : ea, pb = (bad_b || eb == kPastRun) ? 0 : eb;
-          if (j >= kRing && !mbar_wait(smem_addr(rawempty + sp), ((j / kRing) - 1) & 1, abort_flag)) break;
-          const int kb = (run_first[cur.run] + 2 * cur.s) * kPage;
-          records[j % kStepRecords] =
-              make_int4(max(run_kmin[cur.run] - kb, bad_a ? kPage : 0),
-                        min(run_kmax[cur.run] - kb, (bad_b || eb == kPastRun) ? kPage : kStepKeys), kb, cur.run);
-          const uint32_t fb = smem_addr(rawfull + sp);
-          mbar_arrive_expect_tx(fb, 3 * L::kPageBytes);
-          const uint32_t dst = smem_addr(smem + L::packed + size_t(sp) * 3 * L::kPageBytes);
-          const size_t head = static_cast<size_t>(h) * p.num_pages;
-          bulk_load(dst, p.k_pool4 + (head + (rank == 0 ? pa : pb)) * L::kPageBytes, L::kPageBytes, fb);
-          bulk_load(dst + L::kPageBytes, p.v_pool4 + (head + pa) * L::kPageBytes, L::kPageBytes, fb);
-          bulk_load(dst + 2 * L::kPageBytes, p.v_pool4 + (head + pb) * L::kPageBytes, L::kPageBytes, fb);
-          ea = na;
-          eb = nb;
+  if (warp == 0) {
+    // ============================== producer ==============================
+    if (lane == 0 && nsteps > 0) {
+      StepCursor cur;
+      int ea, eb;  // table entries of the step's two pages, read one step ahead
+      step_entries(p, run_row, run_first, run_kmax, misc[0], cur, ea, eb);
+      int j = 0;
+      for (; j < nsteps; ++j, cur.next(run_steps)) {
+        const int sk = j % kStagesK, sv = j % kStagesV;
+        int na, nb;
+        {
+          StepCursor nc = cur;
+          nc.next(run_steps);
+          step_entries(p, run_row, run_first, run_kmax, misc[0], nc, na, nb);
         }
-        // do not leave while a copy may still land in this CTA's memory
-        for (int kk = max(0, j - kRing); kk < j; ++kk) {
-          const uint32_t fb = smem_addr(rawfull + kk % kRing);
-          const uint64_t t_0 = global_timer_ns();
-          while (!mbar_try_wait(fb, (kk / kRing) & 1) && global_timer_ns() - t_0 < kWaitLimitNs) {
-          }
-        }
-      }
-    } else if (!KV4 && warp == 0) {
-      // ============================== producer ==============================
-      if (lane == 0 && nsteps > 0) {
-        StepCursor cur;
-        int ea, eb;  // table entries of the step's two pages, read one step ahead
-        step_entries(p, run_row, run_first, run_kmax, misc[0], cur, ea, eb);
-        int j = 0;
-        for (; j < nsteps; ++j, cur.next(run_steps)) {
-          const int sk = j % kStagesK, sv = j % kStagesV;
-          int na, nb;
-          {
-            StepCursor nc = cur;
-            nc.next(run_steps);
-            step_entries(p, run_row, run_first, run_kmax, misc[0], nc, na, nb);
-          }
-          // a page past the run or a bad table entry loads page 0 instead (its
-          // keys are masked and its values zeroed)
-          const bool bad_a = ea >= p.num_pages || ea < 0;
-          const bool bad_b = eb != kPastRun && (eb >= p.num_pages || eb < 0);
-          if (rank == 0 && (bad_a || bad_b) && p.status != nullptr) atomicOr(p.status, LNK_DEV_BAD_PAGE);
-          const int pa = bad_a ? 0 : ea, pb = (bad_b || eb == kPastRun) ? 0 : eb;
-          if (j >= kStagesK && !mbar_wait(smem_addr(kempty + sk), ((j / kStagesK) - 1) & 1, abort_flag)) break;
-          uint32_t fb = smem_addr(kfull + sk);
-          mbar_arrive_expect_tx(fb, L::kKStage);
-          const uint32_t kdst = smem_addr(smem + L::kring + size_t(sk) * L::kKStage);
-          const int yk = (h * p.num_pages + (rank == 0 ? pa : pb)) * kPage;  // this CTA's K page
+        // a page past the run or a bad table entry loads page 0 instead (its
+        // keys are masked and its values zeroed)
+        const bool bad_a = ea >= p.num_pages || ea < 0;
+        const bool bad_b = eb != kPastRun && (eb >= p.num_pages || eb < 0);
+        if (rank == 0 && (bad_a || bad_b) && p.status != nullptr) atomicOr(p.status, LNK_DEV_BAD_PAGE);
+        const int pa = bad_a ? 0 : ea, pb = (bad_b || eb == kPastRun) ? 0 : eb;
+        if (j >= kStagesK && !mbar_wait(smem_addr(kempty + sk), ((j / kStagesK) - 1) & 1, abort_flag)) break;
+        uint32_t fb = smem_addr(kfull + sk);
+        mbar_arrive_expect_tx(fb, L::kKStage);
+        const uint32_t kdst = smem_addr(smem + L::kring + size_t(sk) * L::kKStage);
+        const int yk = (h * p.num_pages + (rank == 0 ? pa : pb)) * kPage;  // this CTA's K page
 #pragma unroll
-          for (int nb2 = 0; nb2 < NB; ++nb2) tma_load_2d(kdst + nb2 * kBoxBytes, &kmap, nb2 * kBoxCols, yk, fb);
-          if (j >= kStagesV && !mbar_wait(smem_addr(vempty + sv), ((j / kStagesV) - 1) & 1, abort_flag)) {
-            ++j;  // this step's K load was issued
-            break;
-          }
-          fb = smem_addr(vfull + sv);
-          mbar_arrive_expect_tx(fb, L::kVStage);
-          const uint32_t vdst = smem_addr(smem + L::vring + size_t(sv) * L::kVStage);
-          const int xv = static_cast<int>(rank) * kBoxCols;
-          tma_load_2d(vdst, &vmap, xv, (h * p.num_pages + pa) * kPage, fb);
-          tma_load_2d(vdst + kBoxBytes, &vmap, xv, (h * p.num_pages + pb) * kPage, fb);
-          ea = na;
-          eb = nb;
+        for (int nb2 = 0; nb2 < NB; ++nb2) tma_load_2d(kdst + nb2 * kBoxBytes, &kmap, nb2 * kBoxCols, yk, fb);
+        if (j >= kStagesV && !mbar_wait(smem_addr(vempty + sv), ((j / kStagesV) - 1) & 1, abort_flag)) {
+          ++j;  // this step's K load was issued
+          break;
         }
-        // do not leave while a copy may still land in this CTA's memory
-        const int issued = j;
-        for (int kk = max(0, issued - kStagesK); kk < issued; ++kk) {
-          const uint32_t fb = smem_addr(kfull + kk % kStagesK);
-          const uint64_t t_0 = global_timer_ns();
-          while (!mbar_try_wait(fb, (kk / kStagesK) & 1) && global_timer_ns() - t_0 < kWaitLimitNs) {
-          }
-        }
-        for (int kk = max(0, issued - kStagesV); kk < issued; ++kk) {
-          const uint32_t fb = smem_addr(vfull + kk % kStagesV);
-          const uint64_t t_0 = global_timer_ns();
-          while (!mbar_try_wait(fb, (kk / kStagesV) & 1) && global_timer_ns() - t_0 < kWaitLimitNs) {
-          }
+        fb = smem_addr(vfull + sv);
+        mbar_arrive_expect_tx(fb, L::kVStage);
+        const uint32_t vdst = smem_addr(smem + L::vring + size_t(sv) * L::kVStage);
+        const int xv = static_cast<int>(rank) * kBoxCols;
+        tma_load_2d(vdst, &vmap, xv, (h * p.num_pages + pa) * kPage, fb);
+        tma_load_2d(vdst + kBoxBytes, &vmap, xv, (h * p.num_pages + pb) * kPage, fb);
+        ea = na;
+        eb = nb;
+      }
+      // do not leave while a copy may still land in this CTA's memory
+      const int issued = j;
+      for (int kk = max(0, issued - kStagesK); kk < issued; ++kk) {
+        const uint32_t fb = smem_addr(kfull + kk % kStagesK);
+        const uint64_t t_0 = global_timer_ns();
+        while (!mbar_try_wait(fb, (kk / kStagesK) & 1) && global_timer_ns() - t_0 < kWaitLimitNs) {
         }
       }
-    } else if (warp == 1) {
-      if (rank != 0) {
-        // ============================ relay (rank 1) ==========================
-        if (KV4 && lane == 0) {
-          // the keys' relay: publishes what this CTA's warps converted
-          const uint32_t kfull0 = mapa_shared(smem_addr(kfull), 0);
-          for (int j = 0; j < nsteps; ++j) {
-            const int sk = j % kStagesK;
-            if (!mbar_wait(smem_addr(kfull + sk), (j / kStagesK) & 1, abort_flag)) break;
-            mbar_arrive_cluster(kfull0 + sk * 8);
-          }
-        }
-        if (!KV4 && lane == 0 && nsteps > 0) {
-          const uint32_t kfull0 = mapa_shared(smem_addr(kfull), 0);
-          const uint32_t vfull0 = mapa_shared(smem_addr(vfull), 0);
-          for (int j = 0; j < nsteps; ++j) {
-            const int sk = j % kStagesK, sv = j % kStagesV;
-            if (!mbar_wait(smem_addr(kfull + sk), (j / kStagesK) & 1, abort_flag)) break;
-            mbar_arrive_remote(kfull0 + sk * 8);
-            if (!mbar_wait(smem_addr(vfull + sv), (j / kStagesV) & 1, abort_flag)) break;
-            mbar_arrive_remote(vfull0 + sv * 8);
-          }
-        }
-      } else if (lane == 0 && nsteps > 0) {
-        // ======================= Q.K^T issuer (rank 0) ========================
-        constexpr uint32_t kIdS =
-            KV4 ? umma_idesc_f16(kTileRows, kStepKeys, 0, 0) : umma_idesc_bf16(kTileRows, kStepKeys, 0, 0);
-        // Descriptors of stage 0's K tile and of the query rows (K-major); another
-        // stage or K step adds its byte offset / 16 to the 14-bit address field,
-        // which cannot carry (shared addresses stay below 256 KiB).
-        const uint64_t kdesc0 = umma_desc_sw128(smem_addr(smem + L::kring), 0, 1024);
-        const uint64_t qdesc0 = umma_desc_sw128(smem_addr(smem + L::qsm), 0, 1024);
-        // S_b = Q K^T of step j, once the softmax has read S_b of step j - 2
-        // (sfree is at most one phase past that: the softmax reads S_b of step
-        // j only after this product) and both CTAs' K pages have landed.  (Both
-        // CTAs' query rows were stored before the cluster barrier.)
-        bool ok = true;
-        for (int j = 0; ok && j < nsteps; ++j) {
-          const int b = j & 1, sk = j % kStagesK;
-          ok = (j < 2 || mbar_wait(smem_addr(sfree + b), ((j - 2) >> 1) & 1, abort_flag)) &&
-               (KV4 ? mbar_wait_cluster(smem_addr(kfull + sk), (j / kStagesK) & 1, abort_flag)
-                    : mbar_wait(smem_addr(kfull + sk), (j / kStagesK) & 1, abort_flag));
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t sc = tmem + L::kColS + static_cast<uint32_t>(b) * kStepKeys;
-          const uint64_t kd = kdesc0 + static_cast<uint64_t>((sk * L::kKStage) >> 4);
-#pragma unroll
-          for (int kk = 0; kk < DK; ++kk) {
-            const uint32_t koff = ((kk >> 2) * kBoxBytes + (kk & 3) * 32) >> 4;
-            const uint32_t qoff = ((kk >> 2) * L::kQBox + (kk & 3) * 32) >> 4;
-            umma2_ss(sc, qdesc0 + qoff, kd + koff, kIdS, kk > 0);
-          }
-          umma2_commit_both(smem_addr(sfull + b));
-          umma2_commit_both(smem_addr(kempty + sk));
-        }
-      }
-    } else if (warp == R::kPvWarp) {
-      if (KV4 && rank != 0 && lane == 0) {
-        // the values' relay (rank 1)
-        const uint32_t vfull0 = mapa_shared(smem_addr(vfull), 0);
-        for (int j = 0; j < nsteps; ++j) {
-          const int sv = j % kStagesV;
-          if (!mbar_wait(smem_addr(vfull + sv), (j / kStagesV) & 1, abort_flag)) break;
-          mbar_arrive_cluster(vfull0 + sv * 8);
-        }
-      }
-      if (rank == 0 && lane == 0 && nsteps > 0) {
-        // ========================= P.V issuer (rank 0) ========================
-        // One thread issues every P.V, in step order: O accumulates in order,
-        // and a finished P.V implies that every earlier one has finished.
-        constexpr uint32_t kIdPV =
-            KV4 ? umma_idesc_f16(kTileRows, L::kPvN, 0, 1) : umma_idesc_bf16(kTileRows, L::kPvN, 0, 1);
-        const uint64_t vdesc0 = umma_desc_sw128(smem_addr(smem + L::vring), 0, 1024);
-        bool ok = true;
-        for (int j = 0; ok && j < nsteps; ++j) {
-          const int b = j & 1, sv = j % kStagesV;
-          ok = mbar_wait(smem_addr(pfull + b), (j >> 1) & 1, abort_flag) &&
-               (KV4 ? mbar_wait_cluster(smem_addr(vfull + sv), (j / kStagesV) & 1, abort_flag)
-                    : mbar_wait(smem_addr(vfull + sv), (j / kStagesV) & 1, abort_flag));
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t pc = tmem + L::kColP + static_cast<uint32_t>(b) * (kStepKeys / 2);
-          const uint64_t vd = vdesc0 + static_cast<uint64_t>((sv * L::kVStage) >> 4);
-#pragma unroll
-          for (int kk = 0; kk < kStepKeys / 16; ++kk) {  // 16 keys per product
-            const uint64_t bd = vd + ((kk * 16 * 128) >> 4);
-            umma2_ts(tmem + L::kColO, pc + kk * 8, bd, kIdPV, (j > 0 || kk > 0));
-          }
-          umma2_commit_both(smem_addr(vempty + sv));
-          umma2_commit_both(smem_addr(j + 1 < nsteps ? pvdone + b : odone));
+      for (int kk = max(0, issued - kStagesV); kk < issued; ++kk) {
+        const uint32_t fb = smem_addr(vfull + kk % kStagesV);
+        const uint64_t t_0 = global_timer_ns();
+        while (!mbar_try_wait(fb, (kk / kStagesV) & 1) && global_timer_ns() - t_0 < kWaitLimitNs) {
         }
       }
     }
-  } else if (KV4 && warp >= R::kConvertWarp) {
-    // ===================== conversion (4-bit pools) =======================
-    setmaxnreg_dec<kRegsOther>();
-    const int t = tid - R::kConvertWarp * 32;
-    for (int j = 0; j < nsteps; ++j) {
-      const int sp = j % kRing, sk = j % kStagesK, sv = j % kStagesV;
-      bool ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(rawfull + sp), (j / kRing) & 1, abort_flag));
-      if (ok && j >= kStagesK)
-        ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(kempty + sk), ((j / kStagesK) - 1) & 1, abort_flag));
-      if (!ok) break;
-      const int4 real = records[j % kStepRecords];
-      const uint8_t* raw = smem + L::packed + size_t(sp) * 3 * L::kPageBytes;
-      uint8_t* kt = smem + L::kring + size_t(sk) * L::kKStage;
-      constexpr int kRest = D > 64 ? D / 16 - 4 : 4;  // blocks past column 64
-      const int tv = static_cast<int>(rank) * 4;      // this CTA's first value block
-      {
-        // this CTA's K page (masked keys' scores are replaced, whatever they are)
-        Box<D, 4> lo;
-        Box<D, kRest> hi;
-        lo.load(raw, 0, t);
-        if constexpr (D > 64) hi.load(raw, 4, t);
-        lo.store(kt, t, 0, kPage);
-        if constexpr (D > 64) hi.store(kt + kBoxBytes, t, 0, kPage);
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(kfull + sk));
-      // this CTA's 64 value columns of both pages (columns past D hold whatever
-      // they hold: the output's columns past D are not read)
-      uint8_t* vt = smem + L::vring + size_t(sv) * L::kVStage;
-      auto values = [&](auto box, bool any) {
-        auto box2 = box;
-        if (any) {
-          box.load(raw + L::kPageBytes, tv, t);
-          box2.load(raw + 2 * L::kPageBytes, tv, t);
+  } else if (warp == 1) {
+    if (rank != 0) {
+      // ============================ relay (rank 1) ==========================
+      if (lane == 0 && nsteps > 0) {
+        const uint32_t kfull0 = mapa_shared(smem_addr(kfull), 0);
+        const uint32_t vfull0 = mapa_shared(smem_addr(vfull), 0);
+        for (int j = 0; j < nsteps; ++j) {
+          const int sk = j % kStagesK, sv = j % kStagesV;
+          if (!mbar_wait(smem_addr(kfull + sk), (j / kStagesK) & 1, abort_flag)) break;
+          mbar_arrive_remote(kfull0 + sk * 8);
+          if (!mbar_wait(smem_addr(vfull + sv), (j / kStagesV) & 1, abort_flag)) break;
+          mbar_arrive_remote(vfull0 + sv * 8);
         }
-        // (the packed stage is in registers)
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(rawempty + sp));
-        // every warp waits, whether it has values or not: no arrival for a later
-        // use of the stage may come before all those of this one
-        if (j >= kStagesV)
-          ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(vempty + sv), ((j / kStagesV) - 1) & 1, abort_flag));
-        if (!ok || !any) return;
-        box.store(vt, t, real.x, real.y);
-        box2.store(vt + kBoxBytes, t, real.x - kPage, real.y - kPage);
-      };
-      if (rank == 0) values(Box<D, 4>{}, true);
-      else values(Box<D, kRest>{}, D > 64);
-      if (!ok) break;
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(vfull + sv));
+      }
+    } else if (lane == 0 && nsteps > 0) {
+      // ======================= Q.K^T issuer (rank 0) ========================
+      constexpr uint32_t kIdS = umma_idesc_bf16(kTileRows, kStepKeys, 0, 0);
+      // Descriptors of stage 0's K tile and of the query rows (K-major); another
+      // stage or K step adds its byte offset / 16 to the 14-bit address field,
+      // which cannot carry (shared addresses stay below 256 KiB).
+      const uint64_t kdesc0 = umma_desc_sw128(smem_addr(smem + L::kring), 0, 1024);
+      const uint64_t qdesc0 = umma_desc_sw128(smem_addr(smem + L::qsm), 0, 1024);
+      // S_b = Q K^T of step j, once the softmax has read S_b of step j - 2
+      // (sfree is at most one phase past that: the softmax reads S_b of step
+      // j only after this product) and both CTAs' K pages have landed.  (Both
+      // CTAs' query rows were stored before the cluster barrier.)
+      bool ok = true;
+      for (int j = 0; ok && j < nsteps; ++j) {
+        const int b = j & 1, sk = j % kStagesK;
+        ok = (j < 2 || mbar_wait(smem_addr(sfree + b), ((j - 2) >> 1) & 1, abort_flag)) &&
+             mbar_wait(smem_addr(kfull + sk), (j / kStagesK) & 1, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t sc = tmem + L::kColS + static_cast<uint32_t>(b) * kStepKeys;
+        const uint64_t kd = kdesc0 + static_cast<uint64_t>((sk * L::kKStage) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < DK; ++kk) {
+          const uint32_t koff = ((kk >> 2) * kBoxBytes + (kk & 3) * 32) >> 4;
+          const uint32_t qoff = ((kk >> 2) * L::kQBox + (kk & 3) * 32) >> 4;
+          umma2_ss(sc, qdesc0 + qoff, kd + koff, kIdS, kk > 0);
+        }
+        umma2_commit_both(smem_addr(sfull + b));
+        umma2_commit_both(smem_addr(kempty + sk));
+      }
+    }
+  } else if (warp == 10) {
+    if (rank == 0 && lane == 0 && nsteps > 0) {
+      // ========================= P.V issuer (rank 0) ========================
+      // One thread issues every P.V, in step order: O accumulates in order,
+      // and a finished P.V implies that every earlier one has finished.
+      constexpr uint32_t kIdPV = umma_idesc_bf16(kTileRows, L::kPvN, 0, 1);
+      const uint64_t vdesc0 = umma_desc_sw128(smem_addr(smem + L::vring), 0, 1024);
+      bool ok = true;
+      for (int j = 0; ok && j < nsteps; ++j) {
+        const int b = j & 1, sv = j % kStagesV;
+        ok = mbar_wait(smem_addr(pfull + b), (j >> 1) & 1, abort_flag) &&
+             mbar_wait(smem_addr(vfull + sv), (j / kStagesV) & 1, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t pc = tmem + L::kColP + static_cast<uint32_t>(b) * (kStepKeys / 2);
+        const uint64_t vd = vdesc0 + static_cast<uint64_t>((sv * L::kVStage) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < kStepKeys / 16; ++kk) {  // 16 keys per product
+          const uint64_t bd = vd + ((kk * 16 * 128) >> 4);
+          umma2_ts(tmem + L::kColO, pc + kk * 8, bd, kIdPV, (j > 0 || kk > 0));
+        }
+        umma2_commit_both(smem_addr(vempty + sv));
+        umma2_commit_both(smem_addr(j + 1 < nsteps ? pvdone + b : odone));
+      }
     }
   } else {
     // ============================== softmax ===============================
-    if constexpr (KV4) setmaxnreg_inc<kRegsSoftmax>();
     // Two groups of four warps take the steps in turn: group 0 (warps 2-5)
     // the even steps, group 1 (warps 6-9) the odd ones, so that one group's
     // loads and maxima overlap the other's exponentials.  Step j uses S_(j mod
@@ -680,7 +448,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<KV4>::kThreads
     // the publisher arrives on and the receiver waits on), together with the
     // decision to go on, so a stop reaches both groups and neither waits for
     // the other in vain.
-    const int grp = (warp - R::kSoftmaxWarp) >> 2;
+    const int grp = (warp - 2) >> 2;
     const int qt = warp & 3;              // tensor-memory lane quarter of this warp
     const int rl = qt * 32 + lane;        // row of this CTA = tensor-memory lane
     const int row = static_cast<int>(rank) * kRows + rl;  // row of the tile = token * G + head
@@ -706,22 +474,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<KV4>::kThreads
     bool ok = true, stuck = false;
     StepCursor cur;
     int ea = kPastRun, eb = kPastRun;  // table entries of the step's two pages, read one step ahead
-    if (!KV4 && nsteps > 0) step_entries(p, run_row, run_first, run_kmax, misc[0], cur, ea, eb);
+    if (nsteps > 0) step_entries(p, run_row, run_first, run_kmax, misc[0], cur, ea, eb);
     const uint32_t sc = tmem + lanes + L::kColS + static_cast<uint32_t>(grp) * kStepKeys;  // S_grp
     const uint32_t pcol = tmem + lanes + L::kColP + static_cast<uint32_t>(grp) * (kStepKeys / 2);  // P_grp
     const uint32_t sfree0 = mapa_shared(smem_addr(sfree), 0);
-    auto next_step = [&] {
-      if constexpr (!KV4) cur.next(run_steps);
-    };
-    for (int j = 0; j < nsteps; ++j, next_step()) {
-      int kmin = 0, kmax = 0, kb = 0;     // kb: logical key of the step's first slot
-      bool va = false, vb = false;        // pages of the step that hold data: in the run and with a valid table entry
-      if constexpr (!KV4) {
-        kmin = run_kmin[cur.run], kmax = run_kmax[cur.run];
-        const int lpa = run_first[cur.run] + 2 * cur.s;
-        kb = lpa * kPage;
-        va = ea >= 0 && ea < p.num_pages;
-        vb = eb >= 0 && eb < p.num_pages;
+    for (int j = 0; j < nsteps; ++j, cur.next(run_steps)) {
+      const int kmin = run_kmin[cur.run], kmax = run_kmax[cur.run];
+      const int lpa = run_first[cur.run] + 2 * cur.s;
+      const int kb = lpa * kPage;         // logical key of the step's first slot
+      // pages of the step that hold data: in the run and with a valid table entry
+      const bool va = ea >= 0 && ea < p.num_pages;
+      const bool vb = eb >= 0 && eb < p.num_pages;
+      {
         StepCursor nc = cur;
         nc.next(run_steps);
         step_entries(p, run_row, run_first, run_kmax, misc[0], nc, ea, eb);
@@ -729,8 +493,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<KV4>::kThreads
       if ((j & 1) != grp) continue;
       const int sv = j % kStagesV;
       bool okw = !stuck && __all_sync(0xffffffffu, mbar_wait(smem_addr(sfull + grp), (j >> 1) & 1, abort_flag));
-      // (4-bit pools: the converting warps zero the value rows)
-      const bool partial = !KV4 && !(va && vb && kb >= kmin && kb + kStepKeys <= kmax);
+      const bool partial = !(va && vb && kb >= kmin && kb + kStepKeys <= kmax);
       if (okw && partial) {
         // Keys of the step outside the run's range or on a missing page may
         // hold stale or uninitialised data: zero their value rows (this CTA's
@@ -770,18 +533,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<KV4>::kThreads
         for (int i = 0; i < kStepKeys; ++i) x[i] = -INFINITY;
       }
       // visible keys of this step for this row: [a0, e0), minus a missing page
-      int run = cur.run;
-      int ma = va ? 0 : kPage, me = vb ? kStepKeys : kPage;  // keys on valid pages: [ma, me)
-      if constexpr (KV4) {  // (from the producer's record, published with the step's scores)
-        const int4 rec = records[j % kStepRecords];
-        ma = rec.x;
-        me = rec.y;
-        kb = rec.z;
-        run = rec.w;
-      }
-      const bool in_run = live && run == run_id;
+      const bool in_run = live && cur.run == run_id;
       const int ka = in_run ? max(lo - kb, 0) : kStepKeys;
       const int ke = in_run ? max(ka, min(hi - kb, kStepKeys)) : kStepKeys;
+      const int ma = va ? 0 : kPage, me = vb ? kStepKeys : kPage;  // keys on valid pages: [ma, me)
       const int a0 = max(ka, ma), e0 = min(ke, me);
       if (!__all_sync(0xffffffffu, a0 == 0 && e0 == kStepKeys)) {
 #pragma unroll
@@ -850,7 +605,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<KV4>::kThreads
           f32x2_split(fma_f32x2(f32x2(x[hh * 32 + 2 * i], x[hh * 32 + 2 * i + 1]), c2, n2), a0v, a1v);
           const float e0v = ex2_approx(a0v), e1v = ex2_approx(a1v);
           s2[i & 3] = add_f32x2(s2[i & 3], f32x2(e0v, e1v));
-          pk[i] = KV4 ? pack_f16x2(e0v, e1v) : pack_bf16x2(e0v, e1v);
+          pk[i] = pack_bf16x2(e0v, e1v);
         }
         tmem_st16(pcol + hh * 16, pk);
       }
@@ -909,7 +664,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<KV4>::kThreads
     // this group's half of the row: all of its columns read from tensor
     // memory at once, then stored 16 bytes at a time
     uint16_t* dst = p.out + qrow + grp * (D / 2);
-    const float inv = l_part > 0.f ? (KV4 ? p.out_scale : 1.f) / l_part : 0.f;
+    const float inv = l_part > 0.f ? 1.f / l_part : 0.f;
     uint32_t r[D / 2];
     if (ok && nsteps > 0) {
 #pragma unroll
@@ -943,15 +698,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<KV4>::kThreads
   if (warp == 1) tmem2_dealloc(tmem, L::kTmemCols);
 }
 
-template <int D, bool KV4>
+template <int D>
 cudaError_t launch_chunk_t(const CUtensorMap& kmap, const CUtensorMap& vmap, const ChunkParams& p,
                            cudaStream_t stream) {
-  const int bytes = static_cast<int>(TcSmem<D, KV4>::bytes);
-  cudaError_t err = set_max_dynamic_smem(reinterpret_cast<const void*>(chunk_kernel<D, KV4>), bytes);
+  const int bytes = static_cast<int>(TcSmem<D>::bytes);
+  cudaError_t err = set_max_dynamic_smem(reinterpret_cast<const void*>(chunk_kernel<D>), bytes);
   if (err != cudaSuccess) return err;
   const long long grid = 2ll * p.num_tiles * p.hkv;  // a cluster of two CTAs per (tile, kv head)
   if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
-  chunk_kernel<D, KV4><<<static_cast<unsigned>(grid), Roles<KV4>::kThreads, bytes, stream>>>(kmap, vmap, p);
+  chunk_kernel<D><<<static_cast<unsigned>(grid), kThreads, bytes, stream>>>(kmap, vmap, p);
   return cudaGetLastError();
 }
 
@@ -970,13 +725,10 @@ __global__ void gather_last_kernel(const uint16_t* out, const int32_t* last, uin
 cudaError_t launch_chunk(const CUtensorMap& kmap, const CUtensorMap& vmap, const ChunkParams& p, int head_dim,
                          cudaStream_t stream) {
   if (p.P == 0) return cudaSuccess;
-  switch (head_dim + (p.k_pool4 != nullptr ? 1 : 0)) {
-    case 64: return launch_chunk_t<64, false>(kmap, vmap, p, stream);
-    case 96: return launch_chunk_t<96, false>(kmap, vmap, p, stream);
-    case 128: return launch_chunk_t<128, false>(kmap, vmap, p, stream);
-    case 65: return launch_chunk_t<64, true>(kmap, vmap, p, stream);
-    case 97: return launch_chunk_t<96, true>(kmap, vmap, p, stream);
-    case 129: return launch_chunk_t<128, true>(kmap, vmap, p, stream);
+  switch (head_dim) {
+    case 64: return launch_chunk_t<64>(kmap, vmap, p, stream);
+    case 96: return launch_chunk_t<96>(kmap, vmap, p, stream);
+    case 128: return launch_chunk_t<128>(kmap, vmap, p, stream);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -137,7 +137,7 @@ struct ChunkParams {
   uint16_t* out;              // [P][Hq][D]
   int32_t* status;
   int P, hq, hkv, group, num_pages, num_rows, pages_per_row, window;
-  const uint8_t* k_pool4;     // 4-bit pools; null for bf16 pools (reached through tensor maps)
+  const uint8_t* k_pool4;     // 4-bit pools (bf16 pools are reached through tensor maps)
   const uint8_t* v_pool4;
   float out_scale;            // the value scale of 4-bit pools
   int tile_tokens, num_tiles;  // tokens per half tile (128 / group); tiles of kChunkHalves halves
@@ -146,6 +146,9 @@ struct ChunkParams {
 
 cudaError_t launch_chunk(const CUtensorMap& kmap, const CUtensorMap& vmap, const ChunkParams& p, int head_dim,
                          cudaStream_t stream);
+
+// The same over 4-bit pools.
+cudaError_t launch_chunk4(const ChunkParams& p, int head_dim, cudaStream_t stream);
 
 // ------------------------------------------------------------ gather last --
 cudaError_t launch_gather_last(const uint16_t* out, const int32_t* last, uint16_t* last_out, int M,

@@ -478,19 +478,6 @@ __device__ __forceinline__ void tmem2_dealloc(uint32_t taddr, uint32_t ncols) {
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 
-// ------------------------------------------------------- register shares --
-// All four warps of a warpgroup: take (inc) or give back (dec) registers, to N
-// per thread.  The shares of all warpgroups add up to at most what the block
-// was launched with, or an inc waits for ever.
-template <int N>
-__device__ __forceinline__ void setmaxnreg_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void setmaxnreg_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-
 // ---------------------------------------------------- paired fp32 (sm_100+) --
 // Two floats in one 64-bit register (`lo` in the low half) and the paired
 // fp32 instructions that work on both at once.
