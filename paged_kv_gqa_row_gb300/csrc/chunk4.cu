@@ -56,9 +56,10 @@ namespace {
 constexpr int kThreads = 16 * 32;
 constexpr int kPvWarp = 2, kSetupWarp = 3, kSoftmaxWarp = 4, kConvertWarp = 12;
 constexpr int kConvertThreads = 128;
-constexpr int kStagesK = 4;               // K ring (this CTA's page of a step)
-constexpr int kStagesV = 4;               // V ring (this CTA's columns of both pages)
+constexpr int kStagesK = 3;               // K ring (this CTA's page of a step)
+constexpr int kStagesV = 3;               // V ring (this CTA's columns of both pages)
 constexpr int kStagesP = 3;               // packed stages
+constexpr int kScores = 3;                // score buffers in tensor memory
 constexpr int kRows = 128;                // query rows per CTA = tensor-memory lanes
 constexpr int kTileRows = 2 * kRows;      // rows of a tile (both CTAs)
 constexpr int kStepKeys = 2 * kPage;      // keys per step
@@ -66,8 +67,7 @@ constexpr float kRescaleLog2 = 8.f;       // rescale O when the max grows by mor
 constexpr int kMaxOrderedTiles = 512;     // tiles ordered by cost (larger launches keep token order)
 // Step records that the producer writes and the converting and the softmax warps
 // read.  Step J is recorded once the keys of step J - 3 are converted, so after
-// Q.K^T of step J - 7, for which the softmax has read the scores of step J - 9 and,
-// before those, all of step J - 11: 16 are enough.
+// Q.K^T of step J - 6, for which P of step J - 9 was written and read: 16 are enough.
 constexpr int kStepRecords = 16;
 
 // A tile of the cluster's, as the set-up warp leaves it for the others.
@@ -86,17 +86,20 @@ struct Smem {
   static constexpr int kVStage = 2 * kBoxBytes;             // both pages of V, 64 head-dim columns
   static constexpr int kPvN = 128;                          // N of P.V (head_dim padded; 64 per CTA)
   static constexpr uint32_t kTmemCols = 512;
-  // tensor-memory columns: S_0, S_1 (f32 scores), P_0, P_1 (f16 pairs), O
-  static constexpr uint32_t kColS = 0, kColP = 256, kColO = 384;
+  // tensor-memory columns: S_0, S_1, S_2 (f32 scores; P_b, f16 pairs, takes the
+  // first half of S_b as the softmax reads it), O
+  static constexpr uint32_t kColS = 0, kColO = kScores * kStepKeys;
+  static_assert(kColO + kPvN <= kTmemCols, "tensor memory");
   static constexpr int kQBox = kRows * 128;                 // 128 query rows x 64 head-dim columns
   static constexpr size_t kring = 0;
   static constexpr size_t vring = kring + size_t(kStagesK) * kKStage;
   static constexpr size_t qsm = vring + size_t(kStagesV) * kVStage;  // this CTA's query rows, K-major
-  static constexpr size_t packed = qsm + size_t(NB) * kQBox;  // [kStagesP]: K page, V page a, V page b
+  static constexpr int kQTile = NB * kQBox;                 // two of them, for two tiles in turn
+  static constexpr size_t packed = qsm + size_t(2) * kQTile;  // [kStagesP]: K page, V page a, V page b
   static constexpr size_t bars = packed + size_t(kStagesP) * 3 * kPageBytes;
-  // kfull[K], kempty[K], vfull[V], vempty[V], rawfull[P], rawempty[P], sfull[2], sfree[2], pfull[2], pvdone[2],
-  // tfull[2], tempty[2], odone, ofree, qfull, qempty
-  static constexpr int kNumBars = 2 * (kStagesK + kStagesV + kStagesP) + 16;
+  // kfull[K], kempty[K], vfull[V], vempty[V], rawfull[P], rawempty[P], sfull[3], pfull[3], pvdone[3], tfull[2],
+  // tempty[2], odone, ofree, qfull[2], qempty[2]
+  static constexpr int kNumBars = 2 * (kStagesK + kStagesV + kStagesP) + 3 * kScores + 10;
   static constexpr size_t records = (bars + kNumBars * sizeof(uint64_t) + 15) / 16 * 16;  // [kStepRecords] int4
   static constexpr size_t tiles = records + size_t(kStepRecords) * 16;  // [2] Tile
   static constexpr size_t misc = tiles + 2 * sizeof(Tile);              // abort, tensor-memory address
@@ -321,16 +324,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk4_
   uint64_t* vempty = vfull + kStagesV;
   uint64_t* rawfull = vempty + kStagesV;  // packed stages
   uint64_t* rawempty = rawfull + kStagesP;
-  uint64_t* sfull = rawempty + kStagesP;  // [2] Q.K^T into S_b finished
-  uint64_t* sfree = sfull + 2;            // [2] the softmax has read S_b (rank 0 only)
-  uint64_t* pfull = sfree + 2;            // [2] P_b written (rank 0 only)
-  uint64_t* pvdone = pfull + 2;           // [2] P.V from P_b finished
-  uint64_t* tfull = pvdone + 2;           // [2] a slot's tile is set up
+  uint64_t* sfull = rawempty + kStagesP;  // [kScores] Q.K^T into S_b finished
+  uint64_t* pfull = sfull + kScores;      // [kScores] P_b written (rank 0 only)
+  uint64_t* pvdone = pfull + kScores;     // [kScores] P.V from P_b finished
+  uint64_t* tfull = pvdone + kScores;     // [2] a slot's tile is set up
   uint64_t* tempty = tfull + 2;           // [2] all have read it
   uint64_t* odone = tempty + 2;           // the last P.V of a tile finished
   uint64_t* ofree = odone + 1;            // the softmax has read O (rank 0 only)
-  uint64_t* qfull = ofree + 1;            // queries of a tile after the first stored, in both CTAs (rank 0 only)
-  uint64_t* qempty = qfull + 1;           // the last Q.K^T of a tile finished
+  uint64_t* qfull = ofree + 1;            // [2] a tile's queries stored in both CTAs (rank 0 only)
+  uint64_t* qempty = qfull + 2;           // [2] the tile's last Q.K^T finished
   int4* records = reinterpret_cast<int4*>(smem + L::records);
   Tile* tiles = reinterpret_cast<Tile*>(smem + L::tiles);
   int* misc = reinterpret_cast<int*>(smem + L::misc);
@@ -382,18 +384,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk4_
       mbar_init(smem_addr(rawfull + s), 1);
       mbar_init(smem_addr(rawempty + s), kConvertThreads / 32);
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < kScores; ++b) {
       mbar_init(smem_addr(sfull + b), 1);
-      mbar_init(smem_addr(sfree + b), 8);   // one softmax group (four warps) in each CTA
-      mbar_init(smem_addr(pfull + b), 8);
+      mbar_init(smem_addr(pfull + b), 8);   // one softmax group (four warps) in each CTA
       mbar_init(smem_addr(pvdone + b), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
       mbar_init(smem_addr(tfull + b), 1);
       mbar_init(smem_addr(tempty + b), kTileReaders);
+      mbar_init(smem_addr(qfull + b), 2 * (kConvertThreads / 32));
+      mbar_init(smem_addr(qempty + b), 1);
     }
     mbar_init(smem_addr(odone), 1);
     mbar_init(smem_addr(ofree), 16);  // both groups in both CTAs
-    mbar_init(smem_addr(qfull), 2 * (kConvertThreads / 32));
-    mbar_init(smem_addr(qempty), 1);
     misc[0] = 0;
     fence_mbarrier_init();
   }
@@ -505,25 +508,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk4_
         // which cannot carry (shared addresses stay below 256 KiB).
         const uint64_t kdesc0 = umma_desc_sw128(smem_addr(smem + L::kring), 0, 1024);
         const uint64_t qdesc0 = umma_desc_sw128(smem_addr(smem + L::qsm), 0, 1024);
-        // S_b = Q K^T of step J, once the softmax has read S_b of step J - 2
-        // (sfree is at most one phase past that: the softmax reads S_b of step J
-        // only after this product), both CTAs' K pages are converted and, for the
-        // first step of a tile, its queries stored in both CTAs (the first tile's:
-        // before the cluster barrier).
-        int J = 0, nq = 0;  // nq: tiles whose queries came through qfull
+        // S_b = Q K^T of step J (b = J mod 3), once P.V of step J - 3 has read P_b,
+        // both CTAs' K pages are converted and, for the first step of a tile, its
+        // queries stored in both CTAs.
+        int J = 0, n = 0;
         bool ok = true;
         for (int k = 0; ok && item_of(k, clusters, cluster) < items; ++k) {
           if (!tile_ready(k)) break;
           const int nsteps = tiles[k & 1].steps;
           mbar_arrive(smem_addr(tempty + (k & 1)));
           if (nsteps == 0) continue;
-          if (k > 0) {
-            ok = mbar_wait_cluster(smem_addr(qfull), nq & 1, abort_flag);
-            ++nq;
-          }
+          ok = mbar_wait_cluster(smem_addr(qfull + (n & 1)), (n >> 1) & 1, abort_flag);
+          const uint64_t qd = qdesc0 + static_cast<uint64_t>(((n & 1) * L::kQTile) >> 4);
           for (int j = 0; ok && j < nsteps; ++j, ++J) {
-            const int b = J & 1, sk = J % kStagesK;
-            ok = (J < 2 || mbar_wait(smem_addr(sfree + b), ((J - 2) >> 1) & 1, abort_flag)) &&
+            const int b = J % kScores, sk = J % kStagesK;
+            ok = (J < kScores || mbar_wait(smem_addr(pvdone + b), (J / kScores - 1) & 1, abort_flag)) &&
                  mbar_wait_cluster(smem_addr(kfull + sk), (J / kStagesK) & 1, abort_flag);
             if (!ok) break;
             tc_fence_after();
@@ -533,12 +532,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk4_
             for (int kk = 0; kk < DK; ++kk) {
               const uint32_t koff = ((kk >> 2) * kBoxBytes + (kk & 3) * 32) >> 4;
               const uint32_t qoff = ((kk >> 2) * L::kQBox + (kk & 3) * 32) >> 4;
-              umma2_ss(sc, qdesc0 + qoff, kd + koff, kIdS, kk > 0);
+              umma2_ss(sc, qd + qoff, kd + koff, kIdS, kk > 0);
             }
             umma2_commit_both(smem_addr(sfull + b));
             umma2_commit_both(smem_addr(kempty + sk));
-            if (j + 1 == nsteps) umma2_commit_both(smem_addr(qempty));
+            if (j + 1 == nsteps) umma2_commit_both(smem_addr(qempty + (n & 1)));
           }
+          ++n;
         }
       } else if (lane == 0) {
         // ========================= P.V issuer (rank 0) ========================
@@ -557,12 +557,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk4_
           if (n > 0) ok = mbar_wait(smem_addr(ofree), (n - 1) & 1, abort_flag);
           ++n;
           for (int j = 0; ok && j < nsteps; ++j, ++J) {
-            const int b = J & 1, sv = J % kStagesV;
-            ok = mbar_wait(smem_addr(pfull + b), (J >> 1) & 1, abort_flag) &&
+            const int b = J % kScores, sv = J % kStagesV;
+            ok = mbar_wait(smem_addr(pfull + b), (J / kScores) & 1, abort_flag) &&
                  mbar_wait_cluster(smem_addr(vfull + sv), (J / kStagesV) & 1, abort_flag);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t pc = tmem + L::kColP + static_cast<uint32_t>(b) * (kStepKeys / 2);
+            const uint32_t pc = tmem + L::kColS + static_cast<uint32_t>(b) * kStepKeys;
             const uint64_t vd = vdesc0 + static_cast<uint64_t>((sv * L::kVStage) >> 4);
 #pragma unroll
             for (int kk = 0; kk < kStepKeys / 16; ++kk) {  // 16 keys per product
@@ -596,24 +596,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk4_
     for (int k = 0; ok && item_of(k, clusters, cluster) < items; ++k) {
       if (!__all_sync(0xffffffffu, tile_ready(k))) break;
       const int nsteps = tiles[k & 1].steps, t0 = tiles[k & 1].t0, h = tiles[k & 1].h;
-      // the step before which the tile's queries are loaded: as many steps are
-      // converted while the last products with the old ones run
-      const int q_step = k > 0 ? min(kStagesK, nsteps) - 1 : -1;
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_addr(tempty + (k & 1)));
+      if (nsteps > 0) {
+        // the tile's queries, beside those of the tile before
+        if (n >= 2) ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(qempty + (n & 1)), ((n >> 1) - 1) & 1, abort_flag));
+        if (!ok) break;
+        if (k > 0) load_queries<D>(p, smem + L::qsm + (n & 1) * L::kQTile, t0, h, rank, t);
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(qfull0 + (n & 1) * 8);
+      }
       for (int step = 0; step < nsteps; ++step, ++J) {
         const int j = J, sp = j % kStagesP, sk = j % kStagesK, sv = j % kStagesV;
         ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(rawfull + sp), (j / kStagesP) & 1, abort_flag));
         if (ok && j >= kStagesK)
           ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(kempty + sk), ((j / kStagesK) - 1) & 1, abort_flag));
         if (!ok) break;
-        if (step == q_step) {
-          if (n > 0) ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(qempty), (n - 1) & 1, abort_flag));
-          if (!ok) break;
-          load_queries<D>(p, smem + L::qsm, t0, h, rank, t);
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(qfull0);
-        }
         const int4 real = records[j % kStepRecords];
         const uint8_t* raw = smem + L::packed + size_t(sp) * 3 * L::kPageBytes;
         uint8_t* kt = smem + L::kring + size_t(sk) * L::kKStage;
@@ -664,10 +662,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk4_
   } else {
     // =============================== softmax ==============================
     // Two groups of four warps take the steps in turn, J mod 2, so that one group's
-    // loads and maxima overlap the other's exponentials.  Step J uses S_(J mod 2),
-    // so group g always reads and writes S_g.  Warps w and w + 4 share the
-    // tensor-memory lanes of quarter w % 4: thread r of each group owns query row r
-    // of this CTA.  Within a tile the row's running max passes from the group of
+    // loads and maxima overlap the other's exponentials.  Warps w and w + 4 share
+    // the tensor-memory lanes of quarter w % 4: thread r of each group owns query
+    // row r of this CTA.  Within a tile the row's running max passes from the group of
     // one step to the group of the next through shared memory (a named barrier that
     // the publisher arrives on and the receiver waits on), together with the
     // decision to go on, so a stop reaches both groups and neither waits for the
@@ -686,10 +683,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk4_
     int* hand_ok = reinterpret_cast<int*>(smem + L::xchg) + 2 * kRows;  // [2][128]
     float* fin = reinterpret_cast<float*>(smem + L::xchg) + 4 * kRows;  // [2 tile parities]: max, sum, ok [2 groups][128]
     const uint32_t pfull0 = mapa_shared(smem_addr(pfull), 0);
-    const uint32_t sfree0 = mapa_shared(smem_addr(sfree), 0);
     const uint32_t ofree0 = mapa_shared(smem_addr(ofree), 0);
-    const uint32_t sc = tmem + lanes + L::kColS + static_cast<uint32_t>(grp) * kStepKeys;  // S_grp
-    const uint32_t pcol = tmem + lanes + L::kColP + static_cast<uint32_t>(grp) * (kStepKeys / 2);  // P_grp
     // Every wait's outcome is made warp-uniform: the tensor-memory loads and
     // stores that follow are warp-collective.
     bool ok = true, stuck = false;
@@ -708,8 +702,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk4_
       float m_part = -INFINITY;  // reference of this group's partial sum
       float l_part = 0.f;        // sum of this group's probabilities, relative to m_part
       for (int j = (J0 & 1) ^ grp; j < nsteps; j += 2) {  // this group's steps of the tile
-        const int J = J0 + j;
-        bool okw = !stuck && __all_sync(0xffffffffu, mbar_wait(smem_addr(sfull + grp), (J >> 1) & 1, abort_flag));
+        const int J = J0 + j, b = J % kScores;
+        const uint32_t sc = tmem + lanes + L::kColS + static_cast<uint32_t>(b) * kStepKeys;  // S_b, and P_b
+        bool okw = !stuck && __all_sync(0xffffffffu, mbar_wait(smem_addr(sfull + b), (J / kScores) & 1, abort_flag));
         tc_fence_after();
         // visible keys of this step for this row: its own [ka, ke) where they are
         // real (the producer's record, published with the step's scores)
@@ -777,22 +772,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk4_
         // one fma and one add per two keys)
         const float nbase = m_ref == -INFINITY ? 0.f : -m_ref;
         const uint64_t c2 = f32x2(p.scale_log2, p.scale_log2), n2 = f32x2(nbase, nbase);
-        // P_grp is free once P.V of step J - 2 has read it.  (This group waited
-        // for P.V of step J - 4 before it wrote P at step J - 2, so pvdone[grp]
-        // is at most one phase behind step J - 2 here, never two.)
-        if (J >= 2) stuck = stuck || !__all_sync(0xffffffffu, mbar_wait(smem_addr(pvdone + grp), ((J - 2) >> 1) & 1, abort_flag));
-        tc_fence_after();
         uint64_t s2[4] = {0ull, 0ull, 0ull, 0ull};  // running sums, two keys per register
 #pragma unroll 1
         for (int c = 0; c < kStepKeys; c += kPass) {
           float x[kPass];
           load_scores(sc + c, x);
-          if (c + kPass == kStepKeys) {
-            // S_grp may take the next scores
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_remote(sfree0 + grp * 8);
-          }
           if (masked) mask_scores(x, a0 - c, e0 - c);
 #pragma unroll
           for (int hh = 0; hh < kPass / 32; ++hh) {
@@ -805,19 +789,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk4_
               s2[i & 3] = add_f32x2(s2[i & 3], f32x2(e0v, e1v));
               pk[i] = pack_f16x2(e0v, e1v);
             }
-            tmem_st16(pcol + c / 2 + hh * 16, pk);
+            tmem_st16(sc + c / 2 + hh * 16, pk);  // (over scores that were read)
           }
         }
         if (__any_sync(0xffffffffu, alpha != 1.f) && j >= 1) {
           // the running max grew: rescale this row of O once P.V of step J - 1
-          // (written by the other group) has finished, before P.V of step J.
-          // (P.V runs in step order and the wait above saw step J - 2 finish,
-          // so step J - 3 has finished too: that barrier is at most one phase
-          // behind step J - 1.)
-          // (this group's hand-off for step J + 1 has gone out already: if the
-          // wait gives up, the failure travels with its next hand-off instead)
-          stuck = stuck || !__all_sync(0xffffffffu, mbar_wait(smem_addr(pvdone + ((J - 1) & 1)), ((J - 1) >> 1) & 1,
-                                                               abort_flag));
+          // (written by the other group) has finished, before P.V of step J.  (Its
+          // parity tells that step from J - 4 only if J - 4 has finished.  P.V runs
+          // in step order, so the wait for J - 3, which Q.K^T of step J waited for
+          // too, tells that.)
+          // (this group's hand-off for step J + 1 has gone out already: if a wait
+          // gives up, the failure travels with its next hand-off instead)
+          if (J >= kScores)
+            stuck = stuck || !__all_sync(0xffffffffu, mbar_wait(smem_addr(pvdone + b), (J / kScores - 1) & 1, abort_flag));
+          const int bp = (J - 1) % kScores;
+          stuck = stuck || !__all_sync(0xffffffffu, mbar_wait(smem_addr(pvdone + bp), ((J - 1) / kScores) & 1, abort_flag));
           tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < (stuck ? 0 : L::kPvN / 32); ++c) {
@@ -832,7 +818,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk4_
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_remote(pfull0 + grp * 8);
+        if (lane == 0) mbar_arrive_remote(pfull0 + b * 8);
         {
           float u0, u1;
           f32x2_split(add_f32x2(add_f32x2(s2[0], s2[1]), add_f32x2(s2[2], s2[3])), u0, u1);
