@@ -3,7 +3,7 @@
 //
 // The tiles, their runs of steps and the two products of a step are chunk.cu's
 // (256 query rows of one kv head per cluster of two CTAs, 128 keys a step, S and P
-// double-buffered in tensor memory).  Three things differ.
+// in tensor memory).  Three things differ.
 //
 // The operands.  The tensor cores read f16 tiles that this kernel makes from the
 // packed pages: a code times its block's scale is exact in f16 (at most five
@@ -19,10 +19,21 @@
 // And the code is short.  Softmax and converting warps share the schedulers, and
 // with a softmax written out for the 128 scores of a step (as chunk.cu has it, where
 // nothing else runs beside it) warps waited for instructions more than for anything
-// else.  So the scores stay in tensor memory and are read twice, 32 at a time, in
-// loops: four prompts of 1024 to 2047 tokens, 32 query heads on 8, D = 128, took
-// 223 us with the written-out softmax, 177 us with 64 scores at a time, 164 us with
-// 32 (and 211 us with a cluster for each item).
+// else.  So the scores stay in tensor memory and are read twice, in loops of 64 (for
+// the maximum) and 32 (for P): the example below took 223 us with the written-out
+// softmax, 177 us with 64 scores at a time throughout, 164 us with 32.
+//
+// Tensor memory holds three score buffers and O.  P takes the place of the scores it
+// is made from, in two halves, so that P.V starts on the first while the softmax
+// writes the second.
+//
+// What bounds it: the chain of one step, products of 500 cycles each behind one
+// another, a softmax of 2500 cycles, three steps in flight; the tensor cores are busy
+// half of the time.  Four prompts of 1024 to 2047 tokens, 32 query heads on 8,
+// D = 128: 136 us, 600 TFLOP/s (chunk.cu on bf16 pools 181 us).  Four prompts of 512
+// tokens after 1024 to 7168 others, with 32 decode rows: 190 us (bf16 pools 255 us).
+// Eight converting warps instead of four (fewer registers for all) took 10% longer,
+// deeper rings of tiles and shallower ones of packed pages as long.
 //
 // CTA structure (512 threads in both ranks):
 //  * warp 0, producer: this CTA's K page and both V pages of a step as they are
@@ -35,9 +46,8 @@
 //    thread r of a group owns query row r of its CTA (tensor-memory lane r);
 //  * warps 12-15 convert: a thread takes 16 dimensions of one key (8 code bytes
 //    and their scale) and stores them as two 16-byte pieces of the swizzled tile,
-//    zeros for the value rows outside the real keys.  They also load a tile's
-//    queries, once the last Q.K^T of the tile before has read the old ones (one
-//    warp took 20000 cycles for it).  They arrive on barriers of
+//    zeros for the value rows outside the real keys.  They also load the queries
+//    of the next tile beside those of the tile before.  They arrive on barriers of
 //    their own CTA, and the relays pass that on to rank 0: the arrival that
 //    publishes stores to the other CTA takes 600 to 900 cycles, and made by the
 //    converting warps themselves it doubled the time of a step.
@@ -66,7 +76,7 @@ constexpr int kStepKeys = 2 * kPage;      // keys per step
 constexpr float kRescaleLog2 = 8.f;       // rescale O when the max grows by more than 2^8
 constexpr int kMaxOrderedTiles = 512;     // tiles ordered by cost (larger launches keep token order)
 // Step records that the producer writes and the converting and the softmax warps
-// read.  Step J is recorded once the keys of step J - 3 are converted, so after
+// read.  Step J is recorded once step J - 3 is converted, so after
 // Q.K^T of step J - 6, for which P of step J - 9 was written and read: 16 are enough.
 constexpr int kStepRecords = 16;
 
@@ -97,9 +107,9 @@ struct Smem {
   static constexpr int kQTile = NB * kQBox;                 // two of them, for two tiles in turn
   static constexpr size_t packed = qsm + size_t(2) * kQTile;  // [kStagesP]: K page, V page a, V page b
   static constexpr size_t bars = packed + size_t(kStagesP) * 3 * kPageBytes;
-  // kfull[K], kempty[K], vfull[V], vempty[V], rawfull[P], rawempty[P], sfull[3], pfull[3], pvdone[3], tfull[2],
+  // kfull[K], kempty[K], vfull[V], vempty[V], rawfull[P], rawempty[P], sfull[3], pfull[6], pvdone[3], tfull[2],
   // tempty[2], odone, ofree, qfull[2], qempty[2]
-  static constexpr int kNumBars = 2 * (kStagesK + kStagesV + kStagesP) + 3 * kScores + 10;
+  static constexpr int kNumBars = 2 * (kStagesK + kStagesV + kStagesP) + 4 * kScores + 10;
   static constexpr size_t records = (bars + kNumBars * sizeof(uint64_t) + 15) / 16 * 16;  // [kStepRecords] int4
   static constexpr size_t tiles = records + size_t(kStepRecords) * 16;  // [2] Tile
   static constexpr size_t misc = tiles + 2 * sizeof(Tile);              // abort, tensor-memory address
@@ -290,11 +300,12 @@ struct Box {
   }
 };
 
-constexpr int kPass = 32;  // scores that a softmax thread holds at once
+constexpr int kPass = 32;  // scores of a row that P is made of at once (the maximum: twice as many)
 
-__device__ __forceinline__ void load_scores(uint32_t col, float (&x)[kPass]) {
+template <int N>
+__device__ __forceinline__ void load_scores(uint32_t col, float (&x)[N]) {
 #pragma unroll
-  for (int h = 0; h < kPass / 32; ++h) {
+  for (int h = 0; h < N / 32; ++h) {
     uint32_t (&r)[32] = *reinterpret_cast<uint32_t(*)[32]>(x + 32 * h);
     tmem_ld32(col + 32 * h, r);
   }
@@ -302,9 +313,10 @@ __device__ __forceinline__ void load_scores(uint32_t col, float (&x)[kPass]) {
 }
 
 // Scores outside [a, e) become -inf.
-__device__ __forceinline__ void mask_scores(float (&x)[kPass], int a, int e) {
+template <int N>
+__device__ __forceinline__ void mask_scores(float (&x)[N], int a, int e) {
 #pragma unroll
-  for (int h = 0; h < kPass / 32; ++h) {
+  for (int h = 0; h < N / 32; ++h) {
     const int first = min(max(a - 32 * h, 0), 32), end = min(max(e - 32 * h, 0), 32);
     const uint32_t in = end <= first ? 0u : (0xffffffffu >> (32 - (end - first))) << first;
 #pragma unroll
@@ -325,8 +337,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk4_
   uint64_t* rawfull = vempty + kStagesV;  // packed stages
   uint64_t* rawempty = rawfull + kStagesP;
   uint64_t* sfull = rawempty + kStagesP;  // [kScores] Q.K^T into S_b finished
-  uint64_t* pfull = sfull + kScores;      // [kScores] P_b written (rank 0 only)
-  uint64_t* pvdone = pfull + kScores;     // [kScores] P.V from P_b finished
+  uint64_t* pfull = sfull + kScores;      // [kScores][2] a half of P_b written (rank 0 only)
+  uint64_t* pvdone = pfull + 2 * kScores;  // [kScores] P.V from P_b finished
   uint64_t* tfull = pvdone + kScores;     // [2] a slot's tile is set up
   uint64_t* tempty = tfull + 2;           // [2] all have read it
   uint64_t* odone = tempty + 2;           // the last P.V of a tile finished
@@ -386,7 +398,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk4_
     }
     for (int b = 0; b < kScores; ++b) {
       mbar_init(smem_addr(sfull + b), 1);
-      mbar_init(smem_addr(pfull + b), 8);   // one softmax group (four warps) in each CTA
+      mbar_init(smem_addr(pfull + 2 * b), 8);  // one softmax group (four warps) in each CTA
+      mbar_init(smem_addr(pfull + 2 * b + 1), 8);
       mbar_init(smem_addr(pvdone + b), 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -558,17 +571,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk4_
           ++n;
           for (int j = 0; ok && j < nsteps; ++j, ++J) {
             const int b = J % kScores, sv = J % kStagesV;
-            ok = mbar_wait(smem_addr(pfull + b), (J / kScores) & 1, abort_flag) &&
-                 mbar_wait_cluster(smem_addr(vfull + sv), (J / kStagesV) & 1, abort_flag);
-            if (!ok) break;
-            tc_fence_after();
+            ok = mbar_wait_cluster(smem_addr(vfull + sv), (J / kStagesV) & 1, abort_flag);
             const uint32_t pc = tmem + L::kColS + static_cast<uint32_t>(b) * kStepKeys;
             const uint64_t vd = vdesc0 + static_cast<uint64_t>((sv * L::kVStage) >> 4);
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+              ok = ok && mbar_wait(smem_addr(pfull + 2 * b + half), (J / kScores) & 1, abort_flag);
+              if (!ok) break;
+              tc_fence_after();
 #pragma unroll
-            for (int kk = 0; kk < kStepKeys / 16; ++kk) {  // 16 keys per product
-              const uint64_t bd = vd + ((kk * 16 * 128) >> 4);
-              umma2_ts(tmem + L::kColO, pc + kk * 8, bd, kIdPV, (j > 0 || kk > 0));
+              for (int kk = 0; kk < kPage / 16; ++kk) {  // 16 keys per product
+                const uint64_t bd = vd + (((half * kPage + kk * 16) * 128) >> 4);
+                umma2_ts(tmem + L::kColO, pc + half * (kPage / 2) + kk * 8, bd, kIdPV, (j > 0 || half > 0 || kk > 0));
+              }
             }
+            if (!ok) break;
             umma2_commit_both(smem_addr(vempty + sv));
             umma2_commit_both(smem_addr(pvdone + b));
             if (j + 1 == nsteps) umma2_commit_both(smem_addr(odone));
@@ -719,8 +736,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk4_
         float mraw = -INFINITY;
         if (okw) {
 #pragma unroll 1
-          for (int c = 0; c < kStepKeys; c += kPass) {
-            float x[kPass];
+          for (int c = 0; c < kStepKeys; c += 2 * kPass) {
+            float x[2 * kPass];
             load_scores(sc + c, x);
             if (masked) mask_scores(x, a0 - c, e0 - c);
             // a tree of independent three-input maxima
@@ -729,8 +746,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk4_
             for (int i = 0; i < 8; ++i) {
               m[i] = x[i];
 #pragma unroll
-              for (int e = 8; e + 8 < kPass; e += 16) m[i] = fmax3(m[i], x[e + i], x[e + 8 + i]);
-              if (kPass % 16 == 0) m[i] = fmaxf(m[i], x[kPass - 8 + i]);
+              for (int e = 8; e + 8 < 2 * kPass; e += 16) m[i] = fmax3(m[i], x[e + i], x[e + 8 + i]);
+              m[i] = fmaxf(m[i], x[2 * kPass - 8 + i]);
             }
             mraw = fmax3(mraw, fmax3(m[0], m[1], m[2]), fmax3(fmaxf(m[3], m[4]), m[5], fmaxf(m[6], m[7])));
           }
@@ -768,30 +785,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk4_
           if (m_part != -INFINITY) l_part *= exp2f(m_part - m_ref);
           m_part = m_ref;
         }
-        // probabilities 2^(s * scale * log2(e) - m_ref), packed to f16 (paired fp32:
-        // one fma and one add per two keys)
-        const float nbase = m_ref == -INFINITY ? 0.f : -m_ref;
-        const uint64_t c2 = f32x2(p.scale_log2, p.scale_log2), n2 = f32x2(nbase, nbase);
-        uint64_t s2[4] = {0ull, 0ull, 0ull, 0ull};  // running sums, two keys per register
-#pragma unroll 1
-        for (int c = 0; c < kStepKeys; c += kPass) {
-          float x[kPass];
-          load_scores(sc + c, x);
-          if (masked) mask_scores(x, a0 - c, e0 - c);
-#pragma unroll
-          for (int hh = 0; hh < kPass / 32; ++hh) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              float a0v, a1v;
-              f32x2_split(fma_f32x2(f32x2(x[hh * 32 + 2 * i], x[hh * 32 + 2 * i + 1]), c2, n2), a0v, a1v);
-              const float e0v = ex2_approx(a0v), e1v = ex2_approx(a1v);
-              s2[i & 3] = add_f32x2(s2[i & 3], f32x2(e0v, e1v));
-              pk[i] = pack_f16x2(e0v, e1v);
-            }
-            tmem_st16(sc + c / 2 + hh * 16, pk);  // (over scores that were read)
-          }
-        }
         if (__any_sync(0xffffffffu, alpha != 1.f) && j >= 1) {
           // the running max grew: rescale this row of O once P.V of step J - 1
           // (written by the other group) has finished, before P.V of step J.  (Its
@@ -815,10 +808,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk4_
             tmem_st32(tmem + lanes + L::kColO + c * 32, r);
           }
         }
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_remote(pfull0 + b * 8);
+        // probabilities 2^(s * scale * log2(e) - m_ref), packed to f16 (paired fp32:
+        // one fma and one add per two keys)
+        const float nbase = m_ref == -INFINITY ? 0.f : -m_ref;
+        const uint64_t c2 = f32x2(p.scale_log2, p.scale_log2), n2 = f32x2(nbase, nbase);
+        uint64_t s2[4] = {0ull, 0ull, 0ull, 0ull};  // running sums, two keys per register
+#pragma unroll 1
+        for (int c = 0; c < kStepKeys; c += kPass) {
+          float x[kPass];
+          load_scores(sc + c, x);
+          if (masked) mask_scores(x, a0 - c, e0 - c);
+#pragma unroll
+          for (int hh = 0; hh < kPass / 32; ++hh) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float a0v, a1v;
+              f32x2_split(fma_f32x2(f32x2(x[hh * 32 + 2 * i], x[hh * 32 + 2 * i + 1]), c2, n2), a0v, a1v);
+              const float e0v = ex2_approx(a0v), e1v = ex2_approx(a1v);
+              s2[i & 3] = add_f32x2(s2[i & 3], f32x2(e0v, e1v));
+              pk[i] = pack_f16x2(e0v, e1v);
+            }
+            tmem_st16(sc + c / 2 + hh * 16, pk);  // (over scores that were read)
+          }
+          if ((c + kPass) % kPage == 0) {
+            // a half of P is written (and O rescaled): P.V may start on it
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(pfull0 + (2 * b + c / kPage) * 8);
+          }
+        }
         {
           float u0, u1;
           f32x2_split(add_f32x2(add_f32x2(s2[0], s2[1]), add_f32x2(s2[2], s2[3])), u0, u1);
