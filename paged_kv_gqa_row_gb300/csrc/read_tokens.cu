@@ -1,8 +1,8 @@
 // lnk_paged_read_tokens: the stored keys and values of given tokens as bf16,
 // for every pool type (the append's inverse).
 //
-// One thread per 8 elements of one (token, kv head, pool): it reads 16 bytes of
-// a bf16 pool, 8 of an 8-bit pool, or 4 code bytes and one scale byte of a
+// One thread per 8 elements of one (token, kv head), in both pools: it reads 16
+// bytes of a bf16 pool, 8 of an 8-bit pool, or 4 code bytes and one scale byte of a
 // 4-bit pool, and stores 16 bytes.  The elements of a token's heads are
 // consecutive threads, so the stores are whole lines; the loads of one head are
 // one contiguous row of its page.
@@ -51,8 +51,8 @@ __global__ void __launch_bounds__(kThreads) read_tokens_kernel(const ReadParams 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
   const int per = p.hkv * E8;
-  const long long t = i / per;
-  const int which = blockIdx.y;
+  // (a 64-bit division only where the index needs it)
+  const long long t = i <= 0xffffffffll ? static_cast<uint32_t>(i) / static_cast<uint32_t>(per) : i / per;
   const bool live = t < p.T;
   long long slot = -1;
   int bad = 0;
@@ -80,17 +80,21 @@ __global__ void __launch_bounds__(kThreads) read_tokens_kernel(const ReadParams 
   // (the previous kernel on the stream may still write the pools or the status,
   // or read the outputs)
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (!live || p.out[which] == nullptr) return;
+  if (!live) return;
   const int rest = static_cast<int>(i - t * per);
   const int h = rest / E8, e8 = rest % E8;
   if (bad && rest == 0 && p.status != nullptr) atomicOr(p.status, bad);
-  uint4 v = make_uint4(0u, 0u, 0u, 0u);
-  if (slot >= 0) {
-    const uint8_t* page = p.pool[which] +
-                          (static_cast<size_t>(h) * p.num_pages + static_cast<size_t>(slot / kPage)) * page_bytes(KV, D);
-    v = read8<D, KV>(page, static_cast<int>(slot % kPage), e8, p.scale[which]);
+  const size_t page = (static_cast<size_t>(h) * p.num_pages + static_cast<size_t>(slot / kPage)) * page_bytes(KV, D);
+  uint4 v[2];
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    v[which] = make_uint4(0u, 0u, 0u, 0u);
+    if (slot >= 0 && p.out[which] != nullptr)
+      v[which] = read8<D, KV>(p.pool[which] + page, static_cast<int>(slot % kPage), e8, p.scale[which]);
   }
-  reinterpret_cast<uint4*>(p.out[which])[i] = v;
+#pragma unroll
+  for (int which = 0; which < 2; ++which)
+    if (p.out[which] != nullptr) reinterpret_cast<uint4*>(p.out[which])[i] = v[which];
 }
 
 template <int D, int KV>
@@ -99,7 +103,7 @@ cudaError_t launch_read_t(const ReadParams& p, cudaStream_t stream) {
   const long long blocks = (n + kThreads - 1) / kThreads;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks), 2);
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = 0;
   cfg.stream = stream;
