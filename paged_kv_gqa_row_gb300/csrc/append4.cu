@@ -17,10 +17,12 @@
 //
 // A CTA takes one or two tokens, eight warps in all: its threads evaluate the
 // sines and cosines once (one frequency of one token each), and after the one
-// barrier every warp takes a share of one token's heads, the loads of the next
-// four heads in flight while it works on four.  What bounds it: instructions
-// (about 60 a head, 20 more with the norm, 100 more to quantize a key row, 10 of
-// them for each division; 400 a frequency).
+// barrier every warp takes a share of one token's heads, the loads of the next two
+// heads in flight while it works on two.  What bounds it: instructions, 10000 a
+// token at 2.4 a cycle of an SM (about 60 a head, 20 more with the norm, 100 more to
+// quantize a key row, 10 of them for each division; 400 a frequency).  2048 tokens
+// with QK-norm, 32 query heads on 8, D = 128: 27 us (1.6 TB/s of what it reads and
+// writes; 31 us with three CTAs an SM and four heads at once).
 //
 // Sources: as append_rope.cu; the 4-bit format is this library's (lnk_attn_desc).
 #include "common.cuh"
@@ -33,9 +35,9 @@ namespace {
 using namespace rope;
 
 constexpr int kWarps = 8;
-constexpr int kHeadsAtOnce = 4;
+constexpr int kHeadsAtOnce = 2;
 constexpr int kMaxTokens = 2;    // of a CTA
-constexpr int kCtasPerSm = 3;
+constexpr int kCtasPerSm = 4;
 
 // The QK-norm factor 1 / sqrt(ss / D + eps) as a float pair (about 2^-44): one
 // step from the float32 root r0.  With d = 1 - v r0^2 (v r0^2 in float pairs, the
@@ -296,11 +298,15 @@ cudaError_t launch_t(const AppendParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-bool append4_takes(int tokens) { return tokens >= device_sm_count(); }
+// From half as many tokens as SMs on: below that append_rope.cu, which splits a
+// token's heads over several CTAs (32 tokens, 32 query heads on 8, D = 128: 4.4 us
+// against 5.5 here; 64 tokens: 5.5 and 5.4; 100 tokens: 7.3 and 6.0).
+bool append4_takes(int tokens) { return 2 * static_cast<long long>(tokens) >= device_sm_count(); }
 
 cudaError_t launch_append4(const AppendParams& p_in, int head_dim, cudaStream_t stream) {
   AppendParams p = p_in;
-  // one token per CTA, or two once there are more than a wave of CTAs
+  // one token per CTA, or two once there are more than a wave of CTAs (2048 tokens:
+  // 27 us with two, 33 us with one, 29 us with four)
   p.splits = kWarps / (p.T > static_cast<long long>(kCtasPerSm) * device_sm_count() ? 2 : 1);
   const bool pow2 = rope::e2m1_pow2(p.k_scale) && rope::e2m1_pow2(p.v_scale);
   switch (head_dim) {
