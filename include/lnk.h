@@ -33,7 +33,7 @@
  *     bf16 (the caches' [Batch = 1, KvHeads, MaxSeq, D] with MaxSeq =
  *     num_pages * 64).  Logical position j of table row r lives in pool slot
  *     table[r * pages_per_row + j / 64] * 64 + j % 64.  Pool pointers must be
- *     16-byte aligned.
+ *     16-byte aligned.  (8-bit and 4-bit pools: lnk_attn_desc.)
  *   - Host-detectable argument errors return a status synchronously and
  *     enqueue nothing.  Data-dependent errors found on the device (a table
  *     entry outside [0, num_pages), a position past the table row, a bad row
@@ -322,7 +322,8 @@ lnk_status lnk_paged_decode_attn(const lnk_attn_desc* desc, const lnk_bf16* q_ro
  * pages), it is one kernel: the
  * CTA that attends for pair (b, h) first rotates that pair's query heads and
  * key head and writes its k/v row into the pool, then loads the row's pages
- * (the last one after that write).  Otherwise it is the two kernels above.
+ * (the last one after that write).  Otherwise, and on 4-bit pools always, it
+ * is the two kernels above.
  * In the one-kernel form a token's pool slot must not be visible to another
  * decode row of the same call (rows share only pages below their positions,
  * as copy on write keeps them), and `positions` and `table` must not be

@@ -19,7 +19,7 @@
 // sines and cosines once (one frequency of one token each), and after the one
 // barrier every warp takes a share of one token's heads, the loads of the next two
 // heads in flight while it works on two.  What bounds it: instructions, 10000 a
-// token at 2.4 a cycle of an SM (about 60 a head, 20 more with the norm, 100 more to
+// token at 2.6 a cycle of an SM (about 60 a head, 20 more with the norm, 100 more to
 // quantize a key row, 10 of them for each division; 400 a frequency).  2048 tokens
 // with QK-norm, 32 query heads on 8, D = 128: 27 us (1.6 TB/s of what it reads and
 // writes; 31 us with three CTAs an SM and four heads at once).

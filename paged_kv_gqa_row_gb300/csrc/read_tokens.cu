@@ -5,7 +5,10 @@
 // bytes of a bf16 pool, 8 of an 8-bit pool, or 4 code bytes and one scale byte of a
 // 4-bit pool, and stores 16 bytes.  The elements of a token's heads are
 // consecutive threads, so the stores are whole lines; the loads of one head are
-// one contiguous row of its page.
+// one contiguous row of its page.  Bound by latency (position, table, page): 2048
+// tokens of 8 heads, D = 128, 4-bit pools, 2.9 us in a row of calls, 3.6 TB/s of what
+// it reads and writes, most of it in L2 (8.6 us with a thread per pool and 64-bit
+// division throughout).
 #include <cuda_fp8.h>
 
 #include "common.cuh"
