@@ -361,7 +361,7 @@ int32_t lnk_paged_decode_step_launches(const lnk_attn_desc* desc, int32_t B);
  *             must share a row (LNK_DEV_SEGMENT otherwise).
  *   step_positions device int32 [B]  decode row b's position; row b uses table row b
  *   table, k_pool, v_pool  as above
- *   out       device [P + B][Hq][D]
+ *   out       device [P + B][Hq][D], 8-byte aligned, 16-byte if P > 0
  *   last      device int32 [M] or NULL: chunk token whose output row is copied
  *             to last_out[m] (device [M][Hq][D]); M may be 0
  *   P, B      chunk tokens and decode rows (either may be 0); P > 0 with

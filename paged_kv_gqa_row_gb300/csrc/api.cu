@@ -567,7 +567,8 @@ lnk_status lnk_paged_step_attn(const lnk_attn_desc* desc, const lnk_bf16* q_rope
   if (B > 0 && !step_positions) return LNK_EINVAL;
   if (M > 0 && (!last || !last_out)) return LNK_EINVAL;
   if (P > 0 && desc->kv_dtype == LNK_KV_E4M3) return LNK_EUNSUPPORTED;  // the chunk kernel has no 8-bit form
-  if (!aligned(q_roped, 16) || !aligned(out, 8) || !aligned(k_pool, 16) || !aligned(v_pool, 16)) return LNK_EINVAL;
+  if (!aligned(q_roped, 16) || !aligned(out, P > 0 ? 16 : 8) || !aligned(k_pool, 16) || !aligned(v_pool, 16))
+    return LNK_EINVAL;
   if (B > 0) {
     const size_t need = lnk_paged_workspace_size(desc, B);
     if (workspace == nullptr || need == 0 || ws_bytes < need) return LNK_EWORKSPACE;

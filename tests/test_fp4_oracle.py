@@ -114,3 +114,26 @@ def test_read_tokens_refuses_bad_arguments_without_a_launch():
         assert status(*changed(**kw)) == einval, kw
     bad = lnk.attn_desc(4, 2, 80, 6, 3, 6, kv_dtype=lnk.KV_E2M1)
     assert status(*changed(desc=bad)) == eunsupported
+
+
+def test_a_step_with_chunks_refuses_outputs_off_16_bytes_without_a_launch():
+    lnk = pytest.importorskip("paged_kv_gqa_row_gb300")
+    einval, eworkspace = 1, 5
+    for kind in (lnk.KV_BF16, lnk.KV_E2M1):
+        d = lnk.attn_desc(4, 2, 96, 6, 3, 6, kv_dtype=kind)
+
+        def status(out, P, B, **kw):
+            args = dict(q=16, k_pool=16, v_pool=16)
+            args.update(kw)
+            try:
+                lnk.lnk_paged_step_attn(d, args["q"], 16, 16, None, 16, 16, args["k_pool"], args["v_pool"], out, None, None,
+                                        P, B, 0, None, 0, None, 0)
+            except lnk.LnkError as e:
+                return e.status
+            return 0
+
+        assert status(24, 1, 0) == einval  # the chunks' rows are stored 16 bytes at a time
+        assert status(24, 0, 1) == eworkspace  # decode rows alone: 8 bytes are enough, the workspace is missing
+        assert status(20, 0, 1) == einval
+        assert status(16, 1, 1) == eworkspace
+        assert status(16, 1, 0, q=24) == einval and status(16, 1, 0, v_pool=8) == einval
