@@ -344,7 +344,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk4_
   uint64_t* odone = tempty + 2;           // the last P.V of a tile finished
   uint64_t* ofree = odone + 1;            // the softmax has read O (rank 0 only)
   uint64_t* qfull = ofree + 1;            // [2] a tile's queries stored in both CTAs (rank 0 only)
-  uint64_t* qempty = qfull + 2;           // [2] the tile's last Q.K^T finished
+  uint64_t* qempty = qfull + 2;           // [2] the tile's last Q.K^T finished, and its outputs left the buffer
   int4* records = reinterpret_cast<int4*>(smem + L::records);
   Tile* tiles = reinterpret_cast<Tile*>(smem + L::tiles);
   int* misc = reinterpret_cast<int*>(smem + L::misc);
@@ -406,7 +406,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk4_
       mbar_init(smem_addr(tfull + b), 1);
       mbar_init(smem_addr(tempty + b), kTileReaders);
       mbar_init(smem_addr(qfull + b), 2 * (kConvertThreads / 32));
-      mbar_init(smem_addr(qempty + b), 1);
+      mbar_init(smem_addr(qempty + b), 1 + 8);  // the last Q.K^T, and the softmax warps at the tile's end
     }
     mbar_init(smem_addr(odone), 1);
     mbar_init(smem_addr(ofree), 16);  // both groups in both CTAs
@@ -691,7 +691,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk4_
     const int qt = warp & 3;              // tensor-memory lane quarter of this warp
     const int rl = qt * 32 + lane;        // row of this CTA = tensor-memory lane
     const int row = static_cast<int>(rank) * kRows + rl;  // row of the tile = token * G + head
-    const int tl = row / G, g = row % G;
+    const int gshift = 31 - __clz(G);     // (a group is 1, 2, 4 or 8 heads)
+    const int tl = row >> gshift;
     const uint32_t lanes = static_cast<uint32_t>(qt * 32) << 16;
     const int bar_pub = 1 + qt + 4 * grp;        // this group's hand-off to the other group
     const int bar_sub = 1 + qt + 4 * (grp ^ 1);  // the other group's hand-off to this one
@@ -705,16 +706,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk4_
     // stores that follow are warp-collective.
     bool ok = true, stuck = false;
     int J0 = 0, n = 0;  // steps and tiles with steps before this tile
-    for (int k = 0; item_of(k, clusters, cluster) < items; ++k) {
-      // (the tile is ready: the first one is, and the others are waited for below)
+    // A tile as this thread sees it.  Entering one frees its slot.
+    int nsteps, t0, nt, h, lo, hi, run_id;
+    auto enter = [&](int k) {
       const Tile& t = tiles[k & 1];
-      const int nsteps = t.steps;
-      const bool inside = tl < t.nt;
-      const int lo = inside ? t.lo[tl] : 0, hi = inside ? t.hi[tl] : 0, run_id = inside ? t.run[tl] : -1;
-      const bool live = run_id >= 0;
-      const size_t qrow = (static_cast<size_t>(t.t0 + tl) * p.hq + static_cast<size_t>(t.h) * G + g) * D;
+      nsteps = t.steps, t0 = t.t0, nt = t.nt, h = t.h;
+      lo = hi = 0, run_id = -1;
+      if (tl < nt) lo = t.lo[tl], hi = t.hi[tl], run_id = t.run[tl];
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_addr(tempty + (k & 1)));
+    };
+    enter(0);
+    for (int k = 0;; ++k) {
+      const bool live = run_id >= 0;
       float m_ref = -INFINITY;   // the row's running max (log2 units) after this group's last step
       float m_part = -INFINITY;  // reference of this group's partial sum
       float l_part = 0.f;        // sum of this group's probabilities, relative to m_part
@@ -850,7 +854,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk4_
       bool okw = ok && !stuck;
       if (okw && nsteps > 0) okw = __all_sync(0xffffffffu, mbar_wait(smem_addr(odone), n & 1, abort_flag));
       tc_fence_after();
-      if (okw && item_of(k + 1, clusters, cluster) < items) okw = __all_sync(0xffffffffu, tile_ready(k + 1));
+      const bool more = item_of(k + 1, clusters, cluster) < items;
+      if (okw && more) okw = __all_sync(0xffffffffu, tile_ready(k + 1));
       float* fin_m = fin + (k & 1) * 6 * kRows;
       float* fin_l = fin_m + 2 * kRows;
       float* fin_ok = fin_l + 2 * kRows;
@@ -865,11 +870,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk4_
       const float la = m_part == -INFINITY ? 0.f : l_part * exp2f(m_part - mf);
       const float lb = mo == -INFINITY ? 0.f : lo_ * exp2f(mo - mf);
       l_part = grp == 0 ? la + lb : lb + la;
-      // this group's half of the row: all of its columns read from tensor memory at
-      // once, then stored 16 bytes at a time
-      const float inv = l_part > 0.f ? p.out_scale / l_part : 0.f;
-      uint32_t r[D / 2];
-      if (ok && nsteps > 0) {
+      // This group's half of the rows: from tensor memory to the tile's query buffer,
+      // which nobody reads any more (a thread has a row), and from there to memory
+      // (neighbouring threads have neighbouring 16 bytes; rows stored by a thread
+      // each made a third of the stores' lines).
+      constexpr int kPieces = D / 16;  // 16-byte pieces of half a row
+      uint8_t* stage = smem + L::qsm + (n & 1) * L::kQTile + (grp * 4 + qt) * (32 * D);
+      auto place = [&](int rr, int c) {  // (spread over the banks)
+        return rr * D + (kPieces == 6 ? c : c ^ ((rr * kPieces / 8) & (kPieces - 1))) * 16;
+      };
+      const bool any = ok && nsteps > 0;
+      if (any) {
+        const float inv = live && l_part > 0.f ? p.out_scale / l_part : 0.f;
+        uint32_t r[D / 2];
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           uint32_t (&rc)[16] = *reinterpret_cast<uint32_t(*)[16]>(r + c * 16);
@@ -880,24 +893,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk4_
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_remote(ofree0);
-      } else {
 #pragma unroll
-        for (int i = 0; i < D / 2; ++i) r[i] = 0u;
-      }
-      if (inside) {
-        uint4* o = reinterpret_cast<uint4*>(p.out + qrow + grp * (D / 2));
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
+        for (int c = 0; c < kPieces; ++c) {
           float v[8];
 #pragma unroll
-          for (int c = 0; c < 8; ++c) v[c] = live ? __uint_as_float(r[8 * i + c]) * inv : 0.f;
-          o[i] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                            pack_bf16x2(v[6], v[7]));
+          for (int i = 0; i < 8; ++i) v[i] = live ? __uint_as_float(r[8 * c + i]) * inv : 0.f;
+          *reinterpret_cast<uint4*>(stage + place(lane, c)) = make_uint4(
+              pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
         }
+        __syncwarp();
       }
-      if (!ok) break;
+      uint4 piece[kPieces];
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i)
+        piece[i] = any ? *reinterpret_cast<const uint4*>(stage + place((i * 32 + lane) / kPieces, (i * 32 + lane) % kPieces))
+                       : make_uint4(0u, 0u, 0u, 0u);
+      // On to the next tile; the stores come last, because an arrival right after
+      // them would wait for them.
+      uint16_t* dst = p.out + (static_cast<size_t>(t0) * p.hq + static_cast<size_t>(h) * G) * D + grp * (D / 2);
+      const int tokens = nt;
+      if (nsteps > 0) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(qempty + (n & 1)));
+      }
       J0 += nsteps;
       n += nsteps > 0;
+      if (ok && more) enter(k + 1);
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        const int orow = static_cast<int>(rank) * kRows + qt * 32 + (i * 32 + lane) / kPieces, ot = orow >> gshift;
+        if (ot < tokens)
+          *reinterpret_cast<uint4*>(dst + (static_cast<size_t>(ot) * p.hq + (orow & (G - 1))) * D +
+                                    (i * 32 + lane) % kPieces * 8) = piece[i];
+      }
+      if (!ok || !more) break;
     }
   }
   if (*abort_flag && lane == 0 && p.status != nullptr) atomicOr(p.status, LNK_DEV_TIMEOUT);
