@@ -882,36 +882,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk4_
       const bool any = ok && nsteps > 0;
       if (any) {
         const float inv = live && l_part > 0.f ? p.out_scale / l_part : 0.f;
-        uint32_t r[D / 2];
+        const uint32_t oc = tmem + lanes + L::kColO + grp * (D / 2);
+#pragma unroll 1
+        for (int c = 0; c < kPieces; c += 2) {
+          uint32_t r[16];
+          tmem_ld16(oc + c * 8, r);
+          tmem_ld_wait();
+          uint32_t w[8];
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t (&rc)[16] = *reinterpret_cast<uint32_t(*)[16]>(r + c * 16);
-          tmem_ld16(tmem + lanes + L::kColO + grp * (D / 2) + c * 16, rc);
+          for (int i = 0; i < 8; ++i)
+            w[i] = live ? pack_bf16x2(__uint_as_float(r[2 * i]) * inv, __uint_as_float(r[2 * i + 1]) * inv) : 0u;
+          *reinterpret_cast<uint4*>(stage + place(lane, c)) = make_uint4(w[0], w[1], w[2], w[3]);
+          *reinterpret_cast<uint4*>(stage + place(lane, c + 1)) = make_uint4(w[4], w[5], w[6], w[7]);
         }
-        tmem_ld_wait();
         // O may take the next tile's values
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_remote(ofree0);
-#pragma unroll
-        for (int c = 0; c < kPieces; ++c) {
-          float v[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = live ? __uint_as_float(r[8 * c + i]) * inv : 0.f;
-          *reinterpret_cast<uint4*>(stage + place(lane, c)) = make_uint4(
-              pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-        }
-        __syncwarp();
       }
-      uint4 piece[kPieces];
-#pragma unroll
-      for (int i = 0; i < kPieces; ++i)
-        piece[i] = any ? *reinterpret_cast<const uint4*>(stage + place((i * 32 + lane) / kPieces, (i * 32 + lane) % kPieces))
-                       : make_uint4(0u, 0u, 0u, 0u);
-      // On to the next tile; the stores come last, because an arrival right after
-      // them would wait for them.
       uint16_t* dst = p.out + (static_cast<size_t>(t0) * p.hq + static_cast<size_t>(h) * G) * D + grp * (D / 2);
-      const int tokens = nt;
+#pragma unroll 1
+      for (int i = lane; i < kPieces * 32; i += 32) {
+        const int rr = i / kPieces, c = i % kPieces;
+        const int orow = static_cast<int>(rank) * kRows + qt * 32 + rr, ot = orow >> gshift;
+        if (ot < nt)
+          *reinterpret_cast<uint4*>(dst + (static_cast<size_t>(ot) * p.hq + (orow & (G - 1))) * D + c * 8) =
+              any ? *reinterpret_cast<const uint4*>(stage + place(rr, c)) : make_uint4(0u, 0u, 0u, 0u);
+      }
       if (nsteps > 0) {
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(qempty + (n & 1)));
@@ -919,13 +916,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk4_
       J0 += nsteps;
       n += nsteps > 0;
       if (ok && more) enter(k + 1);
-#pragma unroll
-      for (int i = 0; i < kPieces; ++i) {
-        const int orow = static_cast<int>(rank) * kRows + qt * 32 + (i * 32 + lane) / kPieces, ot = orow >> gshift;
-        if (ot < tokens)
-          *reinterpret_cast<uint4*>(dst + (static_cast<size_t>(ot) * p.hq + (orow & (G - 1))) * D +
-                                    (i * 32 + lane) % kPieces * 8) = piece[i];
-      }
       if (!ok || !more) break;
     }
   }
