@@ -30,10 +30,12 @@
 // What bounds it: the chain of one step, products of 500 cycles each behind one
 // another, a softmax of 2500 cycles, three steps in flight; the tensor cores are busy a
 // third of the time.  Four prompts of 1024 to 2047 tokens, 32 query heads on 8,
-// D = 128: 136 us, 600 TFLOP/s (chunk.cu on bf16 pools 181 us).  Four prompts of 512
-// tokens after 1024 to 7168 others, with 32 decode rows: 190 us (bf16 pools 255 us).
+// D = 128: 130 us, 630 TFLOP/s (chunk.cu on bf16 pools 181 us).  Four prompts of 512
+// tokens after 1024 to 7168 others, with 32 decode rows: 187 us (bf16 pools 255 us).
 // Eight converting warps instead of four (fewer registers for all) took 10% longer,
-// deeper rings of tiles and shallower ones of packed pages as long.
+// deeper rings of tiles and shallower ones of packed pages as long; the next tile's
+// first step before a tile's end, or one loop for the keys' and the values'
+// conversion, 4 to 10% longer.
 //
 // CTA structure (512 threads in both ranks):
 //  * warp 0, producer: this CTA's K page and both V pages of a step as they are
