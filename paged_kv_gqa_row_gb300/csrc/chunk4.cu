@@ -363,26 +363,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk4_
   const long long items = static_cast<long long>(p.num_tiles) * p.hkv;
   const bool ordered = p.num_tiles <= kMaxOrderedTiles;
 
-  // ---- the tiles by estimated cost (pages that its last position sees), longest
-  // first; every CTA computes the same order ----
-  if (ordered) {
-    int* cost = reinterpret_cast<int*>(smem + L::xchg);
-    for (int i = tid; i < p.num_tiles; i += kThreads) {
-      const int pm = max(p.positions[i * TQ], p.positions[min(p.P, (i + 1) * TQ) - 1]);
-      const int pages = pm >= 0 ? pm / kPage + 1 : 0;
-      cost[i] = p.window > 0 ? min(pages, (p.window + TQ) / kPage + 2) : pages;
-    }
-    __syncthreads();
-    for (int i = tid; i < p.num_tiles; i += kThreads) {
-      const int ci = cost[i];
-      int rk = 0;
-      for (int k = 0; k < p.num_tiles; ++k) {
-        const int ck = cost[k];
-        rk += (ck > ci) || (ck == ci && k > i);  // ties: later tokens first
-      }
-      order[rk] = static_cast<uint16_t>(i);
-    }
-  }
+  // (the next kernel on the stream may start; this one reads and writes nothing of
+  // the caller's before the kernel before it has finished)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid == 0) {
     // rank 0's full barriers also count the relay's arrival for rank 1's tile
     const int nfull = kConvertThreads / 32 + (rank == 0 ? 1 : 0);
@@ -416,6 +399,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk4_
     fence_mbarrier_init();
   }
   if (warp == 1) tmem2_alloc(smem_addr(misc + 1), L::kTmemCols);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // ---- the tiles by estimated cost (pages that its last position sees), longest
+  // first; every CTA computes the same order ----
+  if (ordered) {
+    int* cost = reinterpret_cast<int*>(smem + L::xchg);
+    for (int i = tid; i < p.num_tiles; i += kThreads) {
+      const int pm = max(p.positions[i * TQ], p.positions[min(p.P, (i + 1) * TQ) - 1]);
+      const int pages = pm >= 0 ? pm / kPage + 1 : 0;
+      cost[i] = p.window > 0 ? min(pages, (p.window + TQ) / kPage + 2) : pages;
+    }
+    __syncthreads();
+    for (int i = tid; i < p.num_tiles; i += kThreads) {
+      const int ci = cost[i];
+      int rk = 0;
+      for (int k = 0; k < p.num_tiles; ++k) {
+        const int ck = cost[k];
+        rk += (ck > ci) || (ck == ci && k > i);  // ties: later tokens first
+      }
+      order[rk] = static_cast<uint16_t>(i);
+    }
+  }
   __syncthreads();
   auto tile_of = [&](long long item) {
     const int r = static_cast<int>(item / p.hkv);
@@ -971,8 +975,17 @@ cudaError_t launch_chunk4_t(const ChunkParams& p, cudaStream_t stream) {
   if (err != cudaSuccess) return err;
   const long long items = static_cast<long long>(p.num_tiles) * p.hkv;
   if (items < clusters) clusters = static_cast<int>(items);
-  chunk4_kernel<D><<<2 * clusters, kThreads, bytes, stream>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * clusters));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(bytes);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, chunk4_kernel<D>, p);
 }
 
 }  // namespace
