@@ -361,7 +361,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk4_
   const int G = p.group;
   const int TQ = 2 * p.tile_tokens;  // tokens of a tile
   const long long items = static_cast<long long>(p.num_tiles) * p.hkv;
-  const bool ordered = p.num_tiles <= kMaxOrderedTiles;
+  const bool ordered = items > clusters && p.num_tiles <= kMaxOrderedTiles;  // (one round needs no order)
 
   // (the next kernel on the stream may start; this one reads and writes nothing of
   // the caller's before the kernel before it has finished)
