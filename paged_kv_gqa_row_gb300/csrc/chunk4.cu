@@ -363,9 +363,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk4_
   const long long items = static_cast<long long>(p.num_tiles) * p.hkv;
   const bool ordered = items > clusters && p.num_tiles <= kMaxOrderedTiles;  // (one round needs no order)
 
-  // (the next kernel on the stream may start; this one reads and writes nothing of
-  // the caller's before the kernel before it has finished)
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid == 0) {
     // rank 0's full barriers also count the relay's arrival for rank 1's tile
     const int nfull = kConvertThreads / 32 + (rank == 0 ? 1 : 0);
@@ -399,6 +396,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk4_
     fence_mbarrier_init();
   }
   if (warp == 1) tmem2_alloc(smem_addr(misc + 1), L::kTmemCols);
+  // (nothing of the caller's is read or written before the previous kernel's end)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // ---- the tiles by estimated cost (pages that its last position sees), longest
   // first; every CTA computes the same order ----
@@ -925,6 +923,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk4_
       if (!ok || !more) break;
     }
   }
+  // The next kernel on the stream may start when all clusters are here.  (Allowed at
+  // the start, the CTAs of a decode kernel that waits took 1% from the last clusters.)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (*abort_flag && lane == 0 && p.status != nullptr) atomicOr(p.status, LNK_DEV_TIMEOUT);
   // neither CTA frees its tensor memory or leaves while the pair's products,
   // copies or remote arrivals may still touch it
