@@ -283,3 +283,35 @@ def test_pools_past_32_bit_offsets():
     for small, large in zip(*results):
         assert torch.equal(small.view(torch.uint8) if small.dtype == torch.uint8 else small.view(torch.int16),
                            large.view(torch.uint8) if large.dtype == torch.uint8 else large.view(torch.int16))
+
+
+FIRST_CALL = """
+import sys
+sys.path[:0] = ["tests", "."]
+import torch
+from test_gpu_fp4_large import Case
+rng = __import__("numpy").random.default_rng(1)
+rows, positions = [0] * 100 + [1] * 30, list(range(100)) + list(range(30))
+chk = Case(8, 2, 128, 4, 2, positions, rows)
+dec = Case(8, 2, 128, 4, 6, [5, 100, 255, 0, 64, -1])
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    chk.chunks()
+    dec.decode()
+    chk.lnk.lnk_paged_read_tokens(chk.desc, chk.k_pool, chk.v_pool, chk.positions, chk.rows, None, chk.table,
+                                  torch.empty((130, 2, 128), dtype=torch.bfloat16, device="cuda"), None, 130, chk.status)
+graph.replay()
+chk.check()
+dec.check()
+print("captured")
+"""
+
+
+def test_the_first_calls_of_a_process_may_be_captured():
+    """What a kernel's launch sets up once per device is allowed inside a capture."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stdout[-2000:] + r.stderr[-2000:]
