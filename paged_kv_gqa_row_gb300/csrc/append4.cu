@@ -15,7 +15,7 @@
 // for r; r's own refinement 1.5, and the product 1: 8 more units of |t|, 11.5 in
 // all (12 taken).
 //
-// A CTA takes one or two tokens, eight warps in all: its threads evaluate the
+// A CTA takes one or two tokens, or half of one, with eight warps: its threads evaluate the
 // sines and cosines once (one frequency of one token each), and after the one
 // barrier every warp takes a share of one token's heads, the loads of the next two
 // heads in flight while it works on two.  What bounds it: instructions, 10000 a
@@ -114,9 +114,11 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) append4_kernel(const 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int S = p.splits;           // warps of a token
-  const int tpc = kWarps / S;       // tokens of the CTA
-  const int t0 = blockIdx.x * tpc;
-  const int t = t0 + warp / S, sp = warp % S;  // this warp: heads sp, sp + S, ... of token t
+  const int parts = max(S / kWarps, 1);  // CTAs of a token
+  const int tpc = max(kWarps / S, 1);    // tokens of the CTA
+  const int t0 = static_cast<int>(blockIdx.x) / parts * tpc;
+  // this warp: heads sp, sp + S, ... of token t
+  const int t = t0 + warp / S, sp = static_cast<int>(blockIdx.x) % parts * kWarps + warp % S;
   const bool live = t < p.T;
   const bool has = lane < D / 4;    // lanes holding elements (e, e + 1) and (e + D/2, e + 1 + D/2)
   const int e = 2 * lane;
@@ -281,8 +283,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) append4_kernel(const 
 
 template <int D, bool POW2>
 cudaError_t launch_t(const AppendParams& p, cudaStream_t stream) {
-  const long long tpc = kWarps / p.splits;
-  const long long ctas = (p.T + tpc - 1) / tpc;
+  const long long ctas = (static_cast<long long>(p.T) * p.splits + kWarps - 1) / kWarps;
   if (ctas > 0x7fffffffll) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas));
@@ -300,14 +301,18 @@ cudaError_t launch_t(const AppendParams& p, cudaStream_t stream) {
 
 // From half as many tokens as SMs on: below that append_rope.cu, which splits a
 // token's heads over several CTAs (32 tokens, 32 query heads on 8, D = 128: 4.4 us
-// against 5.5 here; 64 tokens: 5.5 and 5.4; 100 tokens: 7.3 and 6.0).
+// against 5.5 here; 64 tokens: 5.5 and 5.4; 100 tokens: 7.3 and 5.0).
 bool append4_takes(int tokens) { return 2 * static_cast<long long>(tokens) >= device_sm_count(); }
 
 cudaError_t launch_append4(const AppendParams& p_in, int head_dim, cudaStream_t stream) {
   AppendParams p = p_in;
-  // one token per CTA, or two once there are more than a wave of CTAs (2048 tokens:
-  // 27 us with two, 33 us with one, 29 us with four)
-  p.splits = kWarps / (p.T > static_cast<long long>(kCtasPerSm) * device_sm_count() ? 2 : 1);
+  // Warps of a token: two CTAs' as long as there are SMs for all tokens, then one CTA's,
+  // then half of one.  With 16, 8 and 4 (us; 32 query heads on 8, D = 128 with QK-norm, and
+  // 32 on 32, D = 96): 152 tokens 5.1, 5.6, 8.0 and 5.0, 5.8, 9.4; 304 tokens 7.6, 6.7, 8.4
+  // and 8.2, 7.7, 9.6; 900 tokens 18.7, 15.0, 15.3 and 23.0, 19.5, 23.6; 1200 tokens 24.4,
+  // 18.5, 16.4 and 30.5, 25.8, 24.6; 2048 tokens (the former) 33 with 8, 27 with 4.
+  const int sms = device_sm_count();
+  p.splits = p.T <= sms ? 2 * kWarps : p.T <= 7ll * sms ? kWarps : kWarps / 2;
   const bool pow2 = rope::e2m1_pow2(p.k_scale) && rope::e2m1_pow2(p.v_scale);
   switch (head_dim) {
     case 64: return pow2 ? launch_t<64, true>(p, stream) : launch_t<64, false>(p, stream);

@@ -307,3 +307,9 @@ def test_values_of_every_bit_pattern(tokens, ps):
     torch.cuda.synchronize()
     got = u8(vp)
     assert np.array_equal(got, want), f"{int(np.sum(got != want))} bytes differ"
+
+
+@pytest.mark.parametrize("hq,hkv,d,tokens,norm", [(1, 1, 64, 80, True), (64, 8, 128, 90, False), (20, 20, 96, 77, True)])
+def test_few_prompt_tokens_whose_heads_are_split(hq, hkv, d, tokens, norm):
+    """Fewer tokens than SMs: a token's heads, fewer or more than 16, go to two CTAs."""
+    test_prompts_at_any_position_with_and_without_norm(hq, hkv, d, tokens, norm)
