@@ -30,7 +30,7 @@
 // What bounds it: the chain of one step, products of 500 cycles each behind one
 // another, a softmax of 2500 cycles, three steps in flight; the tensor cores are busy a
 // third of the time.  Four prompts of 1024 to 2047 tokens, 32 query heads on 8,
-// D = 128: 130 us, 630 TFLOP/s (chunk.cu on bf16 pools 181 us).  Four prompts of 512
+// D = 128: 127 us, 645 TFLOP/s (chunk.cu on bf16 pools 181 us).  Four prompts of 512
 // tokens after 1024 to 7168 others, with 32 decode rows: 187 us (bf16 pools 255 us).
 // Eight converting warps instead of four (fewer registers for all) took 10% longer,
 // deeper rings of tiles and shallower ones of packed pages as long; the next tile's
@@ -57,6 +57,7 @@
 // Sources: as chunk.cu; the 4-bit format is this library's (lnk_attn_desc).
 #include <map>
 #include <mutex>
+#include <type_traits>
 #include <utility>
 
 #include "common.cuh"
@@ -821,32 +822,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk4_
         const float nbase = m_ref == -INFINITY ? 0.f : -m_ref;
         const uint64_t c2 = f32x2(p.scale_log2, p.scale_log2), n2 = f32x2(nbase, nbase);
         uint64_t s2[4] = {0ull, 0ull, 0ull, 0ull};  // running sums, two keys per register
+        // (a loop of its own for the steps without masked keys: 2% of the call)
+        auto probabilities = [&](auto with_mask) {
 #pragma unroll 1
-        for (int c = 0; c < kStepKeys; c += kPass) {
-          float x[kPass];
-          load_scores(sc + c, x);
-          if (masked) mask_scores(x, a0 - c, e0 - c);
+          for (int c = 0; c < kStepKeys; c += kPass) {
+            float x[kPass];
+            load_scores(sc + c, x);
+            if constexpr (decltype(with_mask)::value) mask_scores(x, a0 - c, e0 - c);
 #pragma unroll
-          for (int hh = 0; hh < kPass / 32; ++hh) {
-            uint32_t pk[16];
+            for (int hh = 0; hh < kPass / 32; ++hh) {
+              uint32_t pk[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              float a0v, a1v;
-              f32x2_split(fma_f32x2(f32x2(x[hh * 32 + 2 * i], x[hh * 32 + 2 * i + 1]), c2, n2), a0v, a1v);
-              const float e0v = ex2_approx(a0v), e1v = ex2_approx(a1v);
-              s2[i & 3] = add_f32x2(s2[i & 3], f32x2(e0v, e1v));
-              pk[i] = pack_f16x2(e0v, e1v);
+              for (int i = 0; i < 16; ++i) {
+                float a0v, a1v;
+                f32x2_split(fma_f32x2(f32x2(x[hh * 32 + 2 * i], x[hh * 32 + 2 * i + 1]), c2, n2), a0v, a1v);
+                const float e0v = ex2_approx(a0v), e1v = ex2_approx(a1v);
+                s2[i & 3] = add_f32x2(s2[i & 3], f32x2(e0v, e1v));
+                pk[i] = pack_f16x2(e0v, e1v);
+              }
+              tmem_st16(sc + c / 2 + hh * 16, pk);  // (over scores that were read)
             }
-            tmem_st16(sc + c / 2 + hh * 16, pk);  // (over scores that were read)
+            if ((c + kPass) % kPage == 0) {
+              // a half of P is written (and O rescaled): P.V may start on it
+              tmem_st_wait();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive_remote(pfull0 + (2 * b + c / kPage) * 8);
+            }
           }
-          if ((c + kPass) % kPage == 0) {
-            // a half of P is written (and O rescaled): P.V may start on it
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_remote(pfull0 + (2 * b + c / kPage) * 8);
-          }
-        }
+        };
+        if (masked) probabilities(std::true_type{});
+        else probabilities(std::false_type{});
         {
           float u0, u1;
           f32x2_split(add_f32x2(add_f32x2(s2[0], s2[1]), add_f32x2(s2[2], s2[3])), u0, u1);
