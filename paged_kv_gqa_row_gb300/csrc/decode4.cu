@@ -22,7 +22,7 @@
 //    three blocks (K, V, K, V, ... in turn).  One lane for all consumers took
 //    about 1100 cycles a page and held the kernel at 4.2 TB/s.
 // One CTA per SM: its consumers and the producer take the whole register file.
-// 64 rows of 512 to 8192 keys, 32 query heads on 8, D = 128: 63 us, 5.1 TB/s (169 us
+// 64 rows of 512 to 8192 keys, 32 query heads on 8, D = 128: 62 us, 5.2 TB/s (169 us
 // on bf16 pools).  A stream of the same blocks without arithmetic takes 53 us; the
 // rest is the start, and at the end the merges of pieces and of cut pairs (6 to 9
 // us).  Fifteen consumers with two blocks each, the next page's values loaded ahead,
@@ -101,14 +101,21 @@ struct Smem {
 __device__ __forceinline__ uint32_t low2(uint32_t h) { return __byte_perm(h, h, 0x1010); }
 __device__ __forceinline__ uint32_t high2(uint32_t h) { return __byte_perm(h, h, 0x3232); }
 
+// The bits of a where m has ones, of b elsewhere (one operation).
+__device__ __forceinline__ uint32_t select_bits(uint32_t a, uint32_t b, uint32_t m) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xE4;" : "=r"(d) : "r"(a), "r"(b), "r"(m));
+  return d;
+}
+
 // Byte order of eight codes of two keys, one dimension of both per byte: the
 // even dimensions' codes (low four bits of a and of b) ...
 __device__ __forceinline__ uint32_t mix_even(uint32_t a, uint32_t b) {
-  return (a & 0x0F0F0F0Fu) | ((b << 4) & 0xF0F0F0F0u);
+  return select_bits(a, b << 4, 0x0F0F0F0Fu);
 }
 // ... and the odd ones'.
 __device__ __forceinline__ uint32_t mix_odd(uint32_t a, uint32_t b) {
-  return ((a >> 4) & 0x0F0F0F0Fu) | (b & 0xF0F0F0F0u);
+  return select_bits(a >> 4, b, 0x0F0F0F0Fu);
 }
 
 template <int D>
