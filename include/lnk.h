@@ -135,7 +135,8 @@ typedef struct lnk_attn_desc {
  *     code = E2M1(x / d),
  *   E4M3 and E2M1 rounding to nearest even and saturating (448 and 6).  A
  *   block whose d is zero stores zeros (s = 0); a block that holds a NaN gets
- *   the NaN scale 0x7F, which makes its 16 values NaN.  (s may round down, so
+ *   the NaN scale 0x7F, which makes its 16 values NaN (an infinity saturates
+ *   like any large value).  (s may round down, so
  *   that the block's largest element saturates: it is then off by at most
  *   1/17 of its size.)
  *     Attention uses the values e2m1(code) * e4m3(s) * pool scale; products of
@@ -210,7 +211,11 @@ size_t lnk_paged_workspace_size(const lnk_attn_desc* desc, int32_t max_rows);
  * Numerics: QK-norm, cos/sin of the float32 angle and the rotation are
  * evaluated to about 2^-46 relative (float pairs; double precision for
  * angles of 2^20 and more and for the QK-norm factor) and rounded once to
- * bf16 (nearest even); v is copied bit for bit.  Two tokens writing one slot
+ * bf16 (nearest even); v is copied bit for bit.  An element that is infinite
+ * or NaN, and one whose result is beyond float32's range, follows the same
+ * expression in float32 (so an infinity times a zero sine is NaN); with
+ * QK-norm, a head that holds an infinity or a NaN, or whose sum of squares is
+ * beyond float32's range, is NaN throughout.  Two tokens writing one slot
  * race (the engine's padding tokens write a shared dump slot nobody reads).
  *
  * Ordering with the preceding kernel: the append kernel is launched as a

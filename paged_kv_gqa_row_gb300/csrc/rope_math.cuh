@@ -15,7 +15,8 @@
 // looking at the low part only to break an exact tie of the high part.  The
 // result is the correctly rounded value of the exact expression except in
 // cases far rarer than one in 10^10, without per-element double-precision
-// arithmetic (which is slow on this GPU).
+// arithmetic (which is slow on this GPU).  Elements that are not finite follow the
+// same expression in float32.
 //
 // Sources: "Phi-3 Mini 4K Instruct -- files", src/rope.linnet (tables);
 // "Qwen3-4B", QK-norm paragraph.
@@ -164,8 +165,11 @@ __device__ __forceinline__ void sincos_df(float a, DF& sn, DF& cs) {
 }
 
 // Round hi + lo (|lo| <= half an ulp of hi, hi = RN(hi + lo)) to bf16, nearest even.
+// A NaN stays one (0x7FFF, as the hardware's conversion gives it): the integer
+// addition below would carry out of its exponent.
 __device__ __forceinline__ uint32_t df_to_bf16(DF v) {
   const uint32_t u = __float_as_uint(v.hi);
+  if ((u & 0x7FFFFFFFu) > 0x7F800000u) return 0x7FFFu;
   if ((u & 0xFFFFu) == 0x8000u && v.lo != 0.f) {
     // hi sits exactly between two bf16 values: the low part decides
     const bool away = (v.lo > 0.f) == (v.hi > 0.f);
@@ -383,6 +387,10 @@ __device__ __forceinline__ void rotate_pairs(uint32_t xlo, uint32_t xhi, const C
       o1 = mul_df(o1, r);
       o2 = mul_df(o2, r);
     }
+    // An infinite or NaN input, or a result beyond float32's range, leaves NaN in a
+    // pair (its error terms are inf - inf): the float32 expression is the answer then.
+    if (o1.hi != o1.hi) o1 = DF{__fmul_rn(r.hi, __fsub_rn(__fmul_rn(x1, ci.gc1.hi), __fmul_rn(x2, ci.gs2.hi))), 0.f};
+    if (o2.hi != o2.hi) o2 = DF{__fmul_rn(r.hi, __fadd_rn(__fmul_rn(x2, ci.gc2.hi), __fmul_rn(x1, ci.gs1.hi))), 0.f};
     lo_bits |= df_to_bf16(o1) << (16 * k);
     hi_bits |= df_to_bf16(o2) << (16 * k);
   }
