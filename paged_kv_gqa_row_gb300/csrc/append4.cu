@@ -72,9 +72,20 @@ __device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
   return d;
 }
 
-__device__ __forceinline__ float fmin3(float a, float b, float c) {
+// Minima and maxima that a NaN among the operands makes NaN.
+__device__ __forceinline__ float min3_nan(float a, float b, float c) {
   float d;
-  asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
   return d;
 }
 
@@ -85,7 +96,7 @@ struct Pair {
 
 // Two outputs x a + y b (neighbouring elements), times r: their bf16 values (low
 // half first).  `wrong` collects bits where the bounds round differently; emin,
-// emax: the bounds' range.
+// emax: the bounds' range (NaN if one of them is).
 __device__ __forceinline__ uint32_t round_pair(uint64_t x, const Pair& a, uint64_t y, const Pair& b, uint64_t r,
                                                uint64_t unit, bool normed, uint32_t& wrong, float& emin, float& emax) {
   const uint64_t q = fma_f32x2(y, b.hi, fma_f32x2(y, b.lo, mul_f32x2(x, a.lo)));
@@ -93,11 +104,11 @@ __device__ __forceinline__ uint32_t round_pair(uint64_t x, const Pair& a, uint64
   float q0, q1, t0, t1, e0, e1;
   f32x2_split(q, q0, q1);
   f32x2_split(t, t0, t1);
-  const uint64_t e = mul_f32x2(f32x2(fmaxf(fabsf(q0), fabsf(t0)), fmaxf(fabsf(q1), fabsf(t1))), unit);
+  const uint64_t e = mul_f32x2(f32x2(max_nan(fabsf(q0), fabsf(t0)), max_nan(fabsf(q1), fabsf(t1))), unit);
   if (normed) t = mul_f32x2(t, r);
   f32x2_split(e, e0, e1);
-  emin = fmin3(emin, e0, e1);
-  emax = fmax3(emax, e0, e1);
+  emin = min3_nan(emin, e0, e1);
+  emax = max3_nan(emax, e0, e1);
   float l0, l1, h0, h1;
   f32x2_split(fma_f32x2(e, f32x2(-1.f, -1.f), t), l0, l1);
   f32x2_split(add_f32x2(t, e), h0, h1);

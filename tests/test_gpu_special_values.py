@@ -73,6 +73,8 @@ def inputs(seed, tokens, hq, hkv, d, specials, every, first_position=1):
     poison(k, rng, specials, where)
     positions = rng.randint(first_position, 5000, tokens)
     positions[0] = first_position
+    if first_position == 0:  # every other poisoned token: sines of zero
+        positions[::2 * every] = 0
     return q, k, v, positions, rng
 
 
@@ -173,3 +175,30 @@ def test_the_one_kernel_decode_step_keeps_special_values(kv, norm):
         assert torch.equal(one, two)
     gamma = None if gq is None else obf16.to_f64(to_bits(gq))
     check_bits(to_bits(results[0][0]), rotated(q, positions, orope.inv_freq(THETA, d), gamma), "q_out")
+
+
+@pytest.mark.parametrize("scales", [(0.25, 0.5), (0.37, 1.9)])
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("tokens,hq,hkv,d", [(80, 6, 6, 96), (400, 8, 2, 64), (1500, 4, 1, 128)])
+def test_infinities_in_large_launches_over_4_bit_pools(tokens, hq, hkv, d, norm, scales):
+    """Position 0 among them, where an infinity meets coefficients that are exactly zero."""
+    check_append("e2m1", tokens, hq, hkv, d, norm, SPECIALS, 3, 6000 + tokens + d, scales, first_position=0)
+
+
+@pytest.mark.parametrize("norm", [False, True])
+def test_large_and_small_launches_store_the_same_special_heads(norm):
+    """Special values among heads of which a few in a hundred are near a rounding
+    border: the same bytes whichever form the launch takes."""
+    tokens, hq, hkv, d = 600, 8, 4, 128
+    q, k, v, positions, rng = inputs(91, tokens, hq, hkv, d, SPECIALS, 1, first_position=0)
+    gamma = [obf16.from_f64(1 + 0.1 * rng.standard_normal(d)) for _ in range(2)] if norm else None
+    pages = 10
+    slots = rng.permutation(pages * 64)[:tokens]
+    results = []
+    for size in (tokens, 40):
+        pools = [d8(np.zeros((hkv, pages, 36 * d))) for _ in range(2)]
+        got = [append("e2m1", q[a:a + size], k[a:a + size], v[a:a + size], positions[a:a + size], slots[a:a + size], pages,
+                      gamma, pools, (0.25, 0.5)) for a in range(0, tokens, size)]
+        results.append((np.concatenate(got), u8(pools[0]), u8(pools[1])))
+    for large, small in zip(*results):
+        assert np.array_equal(large, small)
