@@ -210,13 +210,17 @@ size_t lnk_paged_workspace_size(const lnk_attn_desc* desc, int32_t max_rows);
  *
  * Numerics: QK-norm, cos/sin of the float32 angle and the rotation are
  * evaluated to about 2^-46 relative (float pairs; double precision for
- * angles of 2^20 and more and for the QK-norm factor) and rounded once to
- * bf16 (nearest even); v is copied bit for bit.  An element that is infinite
+ * angles of 2^20 and more and for the QK-norm factor, which launches of many
+ * tokens into 4-bit pools evaluate in float pairs, to 2^-44) and rounded once
+ * to bf16 (nearest even); v is copied bit for bit.  An element that is infinite
  * or NaN, and one whose result is beyond float32's range, follows the same
  * expression in float32 (so an infinity times a zero sine is NaN); with
  * QK-norm, a head that holds an infinity or a NaN, or whose sum of squares is
- * beyond float32's range, is NaN throughout.  Two tokens writing one slot
- * race (the engine's padding tokens write a shared dump slot nobody reads).
+ * beyond float32's range, is NaN throughout.  (The squares are float32: a mean
+ * square plus norm_eps below 2^-96, which needs norm_eps = 0 or nearly so,
+ * makes the factor less accurate, and one of zero makes it infinite.)  Two
+ * tokens writing one slot race (the engine's padding tokens write a shared
+ * dump slot nobody reads).
  *
  * Ordering with the preceding kernel: the append kernel is launched as a
  * programmatic dependent launch and reads `positions`, `rows`, `slots` and

@@ -43,12 +43,17 @@ constexpr int kCtasPerSm = 4;
 // step from the float32 root r0.  With d = 1 - v r0^2 (v r0^2 in float pairs, the
 // difference exact), 1 / sqrt(v) = r0 (1 + d / 2 + 3 d^2 / 8 + ...), |d| < 2^-20.
 // (Double precision, as rope_math.cuh takes it once per head, is slow here: with
-// it this kernel's FP64 pipe was a third of its time.)
+// it this kernel's FP64 pipe was a third of its time.)  It holds while none of the
+// low parts underflows, v in [2^-90, 2^100] with room on both sides; what lies
+// outside (norm_eps = 0 and tiny heads, or huge ones) takes the double precision.
+__device__ __forceinline__ bool rms_in_range(float v) { return v > 0x1p-90f && v < 0x1p100f; }
+
 template <int D>
 __device__ __forceinline__ DF rms_factor_df(DF ss, float eps) {
   constexpr double kInv = 1.0 / D;
   constexpr float kHi = static_cast<float>(kInv), kLo = static_cast<float>(kInv - static_cast<double>(kHi));
   const DF v = df_add(df_mul(ss, DF{kHi, kLo}), DF{eps, 0.f});
+  if (!rms_in_range(v.hi)) return rms_factor(ss, D, static_cast<double>(eps));
   const float r0 = rsqrtf(v.hi);
   const DF w = df_mul(v, two_prod(r0, r0));
   const float d = __fsub_rn(__fsub_rn(1.f, w.hi), w.lo);
@@ -205,6 +210,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) append4_kernel(const 
     lo = hi = 0u;
     if (pos < 0) return;
     const uint64_t x1 = f32x2(bf16_lo(xl), bf16_hi(xl)), x2 = f32x2(bf16_lo(xh), bf16_hi(xh));
+    uint32_t wrong = 0u;
+    float emin = 1.f, emax = 0.f;
     uint64_t r = 0, unit = f32x2(3.5f * 0x1p-24f, 3.5f * 0x1p-24f);
     if (normed) {
       float q0, q1;
@@ -213,13 +220,12 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) append4_kernel(const 
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
       const float v = __fadd_rn(__fmul_rn(ss, 1.f / D), eps32);
+      if (!rms_in_range(v)) wrong = 1u;  // (the bound counts no underflow)
       const float r0 = rsqrtf(v);
       const float rr = __fmaf_rn(0.5f * r0, __fmaf_rn(-__fmul_rn(v, r0), r0, 1.f), r0);
       r = f32x2(rr, rr);
       unit = f32x2(12.f * 0x1p-24f * rr, 12.f * 0x1p-24f * rr);
     }
-    uint32_t wrong = 0u;
-    float emin = 1.f, emax = 0.f;
     lo = round_pair(x1, c1, x2, s2, r, unit, normed, wrong, emin, emax);
     hi = round_pair(x2, c2, x1, s1, r, unit, normed, wrong, emin, emax);
     // (bounds that are zero, tiny, huge or NaN leave it to the float pairs)
