@@ -140,7 +140,9 @@ typedef struct lnk_attn_desc {
  *   that the block's largest element saturates: it is then off by at most
  *   1/17 of its size.)
  *     Attention uses the values e2m1(code) * e4m3(s) * pool scale; products of
- *   a code and a scale are exact in f16 and bf16.  Every entry
+ *   a code and a scale are exact in f16 and bf16.  A key that a query does not
+ *   see adds nothing to its output, whatever its blocks hold; a NaN value block
+ *   that it sees makes its 16 dimensions of the output NaN.  Every entry
  *   point takes these pools.  Attention converts the rotated queries to f16 as
  *   decode does for LNK_KV_E4M3, with the same range. */
 #define LNK_KV_BF16 0

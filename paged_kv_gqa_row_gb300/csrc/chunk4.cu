@@ -54,6 +54,13 @@
 //    publishes stores to the other CTA takes 600 to 900 cycles, and made by the
 //    converting warps themselves it doubled the time of a step.
 //
+// NaN.  A product multiplies every value row of a step into all 256 query rows, and
+// P = 0 does not keep a NaN out.  So value blocks with a NaN scale are converted as
+// finite numbers, and a converting thread that meets one notes the tile in both CTAs.
+// At the end of such a tile each softmax thread looks through the scales of the keys
+// that its row sees, and the 16 dimensions of a NaN block become NaN in its output.
+// (Keys need nothing: the scores that a row does not see are replaced.)
+//
 // Sources: as chunk.cu; the 4-bit format is this library's (lnk_attn_desc).
 #include <map>
 #include <mutex>
@@ -89,6 +96,11 @@ struct Tile {
   int lo[kTileRows], hi[kTileRows], run[kTileRows];       // per token: visible keys [lo, hi), its run (-1: none)
   int row[kTileRows], kmin[kTileRows], kmax[kTileRows];  // per run: table row, keys [kmin, kmax)
 };
+// Notes of NaN value blocks, of tile n in place n mod kNanNotes.  A converting warp at
+// tile n + 4 has found the queries of n + 2 done with in its own CTA, whose softmax
+// came after P.V of n + 2, so after O of n + 1 was read in both CTAs: none of them
+// still asks for tile n.
+constexpr int kNanNotes = 4;
 constexpr int kTileReaders = 15;  // producer, warps 1 and 2, eight softmax and four converting warps
 
 template <int D>
@@ -116,7 +128,8 @@ struct Smem {
   static constexpr size_t records = (bars + kNumBars * sizeof(uint64_t) + 15) / 16 * 16;  // [kStepRecords] int4
   static constexpr size_t tiles = records + size_t(kStepRecords) * 16;  // [2] Tile
   static constexpr size_t misc = tiles + 2 * sizeof(Tile);              // abort, tensor-memory address
-  static constexpr size_t order = misc + 16;                            // [kMaxOrderedTiles]: uint16 tiles by cost
+  static constexpr size_t nans = misc + 16;                             // [kNanNotes]: last tile noted, plus one
+  static constexpr size_t order = nans + kNanNotes * 4;                            // [kMaxOrderedTiles]: uint16 tiles by cost
   // softmax groups' hand-off: max [2][128] and ok [2][128] per step parity; at a
   // tile's end max, sum and ok [2][128] per group and tile parity.  Before the
   // first tile: the tiles' costs.
@@ -260,6 +273,17 @@ __device__ __forceinline__ void set_up(const ChunkParams& p, Tile& t, int tile, 
   __syncwarp();
 }
 
+// A word of shared memory of this CTA or the peer (mapa_shared).
+__device__ __forceinline__ void store_cluster(uint32_t cluster_addr, int value) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(value) : "memory");
+}
+
+__device__ __forceinline__ uint32_t max_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
 // One 64-column box of a packed page for the converting warps: NBLK of the row's
 // blocks, from b0; thread t takes block b0 + t % NBLK of rows t / NBLK, + kAtOnce,
 // ...  Loads and stores are apart, so that the loads of several boxes are in
@@ -281,14 +305,23 @@ struct Box {
       s[u] = src[32 * D + ((j & 3) * (D / 16) + b) * 16 + (j >> 2)];
     }
   }
-  // Into the swizzled f16 tile `dst`; rows outside [x, y) get zeros.
-  __device__ __forceinline__ void store(uint8_t* dst, int t, int x, int y) const {
+  // Into the swizzled f16 tile `dst`; rows outside [x, y) get zeros.  FINITE: a NaN
+  // scale becomes the least finite one (a maximum drops the NaN), and the result is
+  // not zero if there was one.
+  template <bool FINITE>
+  __device__ __forceinline__ uint32_t store(uint8_t* dst, int t, int x, int y) const {
     const int lb = t % NBLK;
+    uint32_t dropped = 0u;
 #pragma unroll
     for (int u = 0; u < kUnits; ++u) {
       const int j = u * kAtOnce + t / NBLK;
       const uint32_t sc = j < x || j >= y ? 0u : s[u];  // (codes are finite: zero)
-      const uint32_t s2 = e4m3x2_to_f16x2(sc | (sc << 8));
+      uint32_t s2 = e4m3x2_to_f16x2(sc | (sc << 8));
+      if constexpr (FINITE) {
+        const uint32_t f2 = max_f16x2(s2, 0xDF00DF00u);  // (-448, twice)
+        dropped |= s2 ^ f2;
+        s2 = f2;
+      }
       uint32_t lo[4], hi[4];
       e2m1x8_to_f16x2x4(w[u].x, lo);
       e2m1x8_to_f16x2x4(w[u].y, hi);
@@ -300,8 +333,34 @@ struct Box {
       *reinterpret_cast<uint4*>(dst + swz128(j, 2 * lb)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       *reinterpret_cast<uint4*>(dst + swz128(j, 2 * lb + 1)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
     }
+    return dropped;
   }
 };
+
+// The blocks b0 .. b0 + D/32 - 1 (as bits from 0) with a NaN scale in any of the values
+// at positions [lo, hi) of a table row, one kv head's pages at `pool`.
+template <int D>
+__device__ __noinline__ uint32_t nan_blocks(const uint8_t* pool, const int32_t* trow, int num_pages, int lo, int hi, int b0) {
+  uint32_t blocks = 0u;
+#pragma unroll 1
+  for (int lp = lo / kPage; lp <= (hi - 1) / kPage; ++lp) {
+    const int page = trow[lp];
+    if (page < 0 || page >= num_pages) continue;
+    const uint8_t* scales = pool + static_cast<size_t>(page) * (36 * D) + 32 * D;
+#pragma unroll 1
+    for (int i = 0; i < 4 * (D / 32); ++i) {  // positions q, q + 4, ... of a page, one block
+      const int q = i & 3, b = i >> 2;
+      const uint4 x = *reinterpret_cast<const uint4*>(scales + (q * (D / 16) + b0 + b) * 16);
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int y = 0; y < 16; ++y) {
+        const int j = lp * kPage + q + 4 * y;
+        if (((w[y >> 2] >> (8 * (y & 3))) & 0x7Fu) == 0x7Fu && j >= lo && j < hi) blocks |= 1u << b;
+      }
+    }
+  }
+  return blocks;
+}
 
 constexpr int kPass = 32;  // scores of a row that P is made of at once (the maximum: twice as many)
 
@@ -351,6 +410,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk4_
   int4* records = reinterpret_cast<int4*>(smem + L::records);
   Tile* tiles = reinterpret_cast<Tile*>(smem + L::tiles);
   int* misc = reinterpret_cast<int*>(smem + L::misc);
+  volatile int* nan_notes = reinterpret_cast<volatile int*>(smem + L::nans);
   uint16_t* order = reinterpret_cast<uint16_t*>(smem + L::order);
   volatile int* abort_flag = misc;
 
@@ -394,6 +454,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk4_
     mbar_init(smem_addr(odone), 1);
     mbar_init(smem_addr(ofree), 16);  // both groups in both CTAs
     misc[0] = 0;
+    for (int i = 0; i < kNanNotes; ++i) nan_notes[i] = 0;
     fence_mbarrier_init();
   }
   if (warp == 1) tmem2_alloc(smem_addr(misc + 1), L::kTmemCols);
@@ -645,8 +706,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk4_
           Box<D, kRest> hi;
           lo.load(raw, 0, t);
           if constexpr (D > 64) hi.load(raw, 4, t);
-          lo.store(kt, t, 0, kPage);
-          if constexpr (D > 64) hi.store(kt + kBoxBytes, t, 0, kPage);
+          lo.template store<false>(kt, t, 0, kPage);
+          if constexpr (D > 64) hi.template store<false>(kt + kBoxBytes, t, 0, kPage);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -668,8 +729,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk4_
           if (j >= kStagesV)
             ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(vempty + sv), ((j / kStagesV) - 1) & 1, abort_flag));
           if (!ok || !any) return;
-          box.store(vt, t, real.x, real.y);
-          box2.store(vt + kBoxBytes, t, real.x - kPage, real.y - kPage);
+          const uint32_t dropped = box.template store<true>(vt, t, real.x, real.y) |
+                                   box2.template store<true>(vt + kBoxBytes, t, real.x - kPage, real.y - kPage);
+          if (dropped != 0u) {  // (published with the values)
+            const uint32_t note = smem_addr(smem + L::nans) + static_cast<uint32_t>(n % kNanNotes) * 4;
+            store_cluster(mapa_shared(note, 0), n + 1);
+            store_cluster(mapa_shared(note, 1), n + 1);
+            __threadfence();
+          }
         };
         if (kRest == 4 && D > 64) values(Box<D, 4>{}, true);  // (both CTAs' columns are whole)
         else if (rank == 0) values(Box<D, 4>{}, true);
@@ -891,6 +958,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk4_
       };
       const bool any = ok && nsteps > 0;
       if (any) {
+        uint32_t nans = 0u;
+        if (nan_notes[n % kNanNotes] == n + 1) {
+          if (live)
+            nans = nan_blocks<D>(p.v_pool4 + static_cast<size_t>(h) * p.num_pages * L::kPageBytes,
+                                 p.table + static_cast<size_t>(p.rows[t0 + tl]) * p.pages_per_row, p.num_pages, lo, hi,
+                                 grp * (D / 32));
+          __syncwarp();
+        }
         const float inv = live && l_part > 0.f ? p.out_scale / l_part : 0.f;
         const uint32_t oc = tmem + lanes + L::kColO + grp * (D / 2);
 #pragma unroll 1
@@ -902,6 +977,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk4_
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             w[i] = live ? pack_bf16x2(__uint_as_float(r[2 * i]) * inv, __uint_as_float(r[2 * i + 1]) * inv) : 0u;
+          if ((nans >> (c / 2)) & 1u) {  // (two pieces are a block)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = 0x7FFF7FFFu;
+          }
           *reinterpret_cast<uint4*>(stage + place(lane, c)) = make_uint4(w[0], w[1], w[2], w[3]);
           *reinterpret_cast<uint4*>(stage + place(lane, c + 1)) = make_uint4(w[4], w[5], w[6], w[7]);
         }
