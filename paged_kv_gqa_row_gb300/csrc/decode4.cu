@@ -31,8 +31,10 @@
 // Arithmetic.  A code times its block's E4M3 scale has at most five significant
 // bits and lies in f16's range (2^-10 .. 2688), so the converted keys and values
 // are exact; the query is rounded to f16 (exact in the range the header states),
-// the probabilities to f16 (relative 2^-11, on values that sum to the
-// denominator kept in float32), and all sums are float32.
+// the probabilities to f16, and all sums are float32.  Probabilities are relative to
+// 2^-14 of the largest, so that the largest is 2^14 in f16: those down to 2^-28 of it
+// are rounded to 2^-11 relative, and what smaller ones lose is below 2^-39 of it each.
+// (The factor is in the denominator too.)
 //
 // Fragments (mma m16n8k16, lane = 4 r + c).  The order of the contraction index
 // and of the output rows is free as long as both operands agree, so that every
@@ -71,6 +73,7 @@ constexpr int kLast = 4;   // the piece's last page
 constexpr int kWhole = 8;  // the piece is its whole pair
 constexpr int kRunEnd = 16;  // the run's last page
 constexpr int kPieces = 2 * kWarps;  // a run's first and last piece
+constexpr float kHeadroomLog2 = 14.f;  // the largest probability is 2^14 (f16 ends at 65504)
 
 struct Page {
   int b, h, klo, khi, flags;
@@ -515,7 +518,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode4_kernel(const DecodeParams
           mx_b = fmaxf(mx_b, __shfl_xor_sync(0xffffffffu, mx_b, off));
         }
         // (the scale is positive: the largest product is the largest score's)
-        const float mn_a = fmaxf(m_a, mx_a * p.scale_log2), mn_b = fmaxf(m_b, mx_b * p.scale_log2);
+        const float mn_a = fmaxf(m_a, fmaf(mx_a, p.scale_log2, -kHeadroomLog2));
+        const float mn_b = fmaxf(m_b, fmaf(mx_b, p.scale_log2, -kHeadroomLog2));
         const bool same_max = __all_sync(0xffffffffu, mn_a == m_a && mn_b == m_b);
         const float base_a = mn_a == -INFINITY ? 0.f : mn_a;
         const float base_b = mn_b == -INFINITY ? 0.f : mn_b;
