@@ -8,7 +8,11 @@
 // The operands.  The tensor cores read f16 tiles that this kernel makes from the
 // packed pages: a code times its block's scale is exact in f16 (at most five
 // significant bits, 2^-10 .. 2688); queries (exact in the range the header states)
-// and P (relative 2^-11) are f16 too, as both operands of a product have one type.
+// and P are f16 too, as both operands of a product have one type.  P is relative to
+// 2^-7 of the row's reference, which the largest score may exceed by 2^8 before the
+// reference follows: at most 2^15 in f16, rounded to 2^-11 relative down to 2^-21 of
+// the reference, and what smaller ones lose is below 2^-32 of it each.  (The factor
+// is in the sums too.)
 //
 // The tiles follow one another without a pause.  One cluster per pair of SMs takes
 // its share of the (tile, kv head) items in turn, and every ring and barrier runs
@@ -84,6 +88,7 @@ constexpr int kRows = 128;                // query rows per CTA = tensor-memory 
 constexpr int kTileRows = 2 * kRows;      // rows of a tile (both CTAs)
 constexpr int kStepKeys = 2 * kPage;      // keys per step
 constexpr float kRescaleLog2 = 8.f;       // rescale O when the max grows by more than 2^8
+constexpr float kHeadroomLog2 = 7.f;      // a score at the reference has P = 2^7 (f16 ends at 65504)
 constexpr int kMaxOrderedTiles = 512;     // tiles ordered by cost (larger launches keep token order)
 // Step records that the producer writes and the converting and the softmax warps
 // read.  Step J is recorded once step J - 3 is converted, so after
@@ -828,7 +833,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk4_
             mraw = fmax3(mraw, fmax3(m[0], m[1], m[2]), fmax3(fmaxf(m[3], m[4]), m[5], fmaxf(m[6], m[7])));
           }
         }
-        const float mx = mraw == -INFINITY ? -INFINITY : mraw * p.scale_log2;  // log2 units
+        // in log2 units, less the headroom (all references are: it cancels)
+        const float mx = mraw == -INFINITY ? -INFINITY : fmaf(mraw, p.scale_log2, -kHeadroomLog2);
         // the row's running max before this step, from the group of the step before
         if (j > 0) {
           named_barrier_sync(bar_sub, 64);

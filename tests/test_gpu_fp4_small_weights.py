@@ -64,3 +64,20 @@ def test_decode_adds_up_small_weights(d, n, heavy, level):
     torch.cuda.synchronize()
     assert int(status.item()) == 0
     check(to_bits(out), want, f"{n} keys at 2^-{level}")
+
+
+@pytest.mark.parametrize("d", [64, 96, 128])
+@pytest.mark.parametrize("n,heavy,level", [(64, 0, 20.6), (200, 3, 19.7), (1000, 130, 20.6), (1000, 900, 18.4),
+                                           (300, 290, 7.95)])
+def test_chunks_add_up_small_weights(d, n, heavy, level):
+    import paged_kv_gqa_row_gb300 as lnk
+    pages, keys, values, q, scale, want = problem(n, d, level, heavy)
+    kp, vp = (d8(pool_of(x, d)) for x in (keys, values))
+    desc = lnk.attn_desc(1, 1, d, pages, 1, pages, scale=scale, kv_dtype=lnk.KV_E2M1)
+    out = torch.zeros((3, 1, d), dtype=torch.int16, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    lnk.lnk_paged_step_attn(desc, d16(np.repeat(q[None], 3, 0)), d32([0] * 3), d32([n - 1] * 3), None, None,
+                            d32([np.arange(pages)]), kp, vp, out, None, None, 3, 0, 0, None, 0, status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    check(to_bits(out), want, f"{n} keys at 2^-{level}")
