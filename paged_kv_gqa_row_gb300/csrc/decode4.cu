@@ -282,7 +282,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode4_kernel(const DecodeParams
     int page = 0;
     bool valid = false;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    uint64_t last_ns = global_timer_ns();
+    // (lane 0's clock, here and below: the lanes give up in the same turn, as the votes need)
+    uint64_t last_ns = __shfl_sync(0xffffffffu, global_timer_ns(), 0);
     bool moved_since = false;
     for (uint32_t it = 1;; ++it) {
       bool moved = false;
