@@ -404,8 +404,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode4_kernel(const DecodeParams
   constexpr int D4 = D / 4;
 
   // Two passes: the real one, and before it, while the previous kernel on the
-  // stream still runs, a dry one of the final phase that stores nothing.  It
-  // brings that phase's code into the instruction cache before the end, when every
+  // stream still runs, a dry one of the final phase that touches no global memory.
+  // It brings that phase's code into the instruction cache before the end, when every
   // warp waits for it.
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
@@ -748,8 +748,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode4_kernel(const DecodeParams
 #pragma unroll
           for (int u = 0; u < kAtOnce; ++u) {
             const size_t row = (seg0 + min(s0 + u, nseg - 1)) * G + g;
-            ml[u] = __ldcg(reinterpret_cast<const float2*>(p.ws_ml) + row);
-            v[u] = __ldcg(reinterpret_cast<const float4*>(p.ws_o + row * D + d));
+            ml[u] = make_float2(-INFINITY, 0.f);
+            v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (!dry) {  // (the previous kernel may still write the workspace then)
+              ml[u] = __ldcg(reinterpret_cast<const float2*>(p.ws_ml) + row);
+              v[u] = __ldcg(reinterpret_cast<const float4*>(p.ws_o + row * D + d));
+            }
             if (s0 + u >= nseg) ml[u].x = -INFINITY;
           }
           float mn = M;
