@@ -571,7 +571,7 @@ lnk_status lnk_paged_step_attn(const lnk_attn_desc* desc, const lnk_bf16* q_rope
     return LNK_EINVAL;
   if (B > 0) {
     const size_t need = lnk_paged_workspace_size(desc, B);
-    if (workspace == nullptr || need == 0 || ws_bytes < need) return LNK_EWORKSPACE;
+    if (workspace == nullptr || need == 0 || ws_bytes < need || !aligned(workspace, 256)) return LNK_EWORKSPACE;
   }
   Pools pools;
   if (!make_pools(&pools, k_pool, v_pool, *desc)) return LNK_ECUDA;
