@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sys
 from array import array
 from typing import Optional
 
@@ -164,11 +165,13 @@ def _stream(stream) -> Optional[int]:
 
 def _addresses(tensors):
     """The addresses of a sequence of tensors (or integers) as a C array."""
+    torch = sys.modules.get("torch")  # (without it there are no tensors)
     try:
-        import torch
-        return array("Q", map(torch.Tensor.data_ptr, tensors))
+        if torch is not None:
+            return array("Q", map(torch.Tensor.data_ptr, tensors))
     except TypeError:  # integers among them
-        return array("Q", (_ptr(x) or 0 for x in tensors))
+        pass
+    return array("Q", (_ptr(x) or 0 for x in tensors))
 
 
 def _check(status: int, where: str):
