@@ -29,6 +29,7 @@ import argparse
 import hashlib
 import json
 import os
+import re
 import statistics
 import subprocess
 import sys
@@ -147,17 +148,35 @@ def read_tensor_peak():
         return FALLBACK_BF16_TFLOPS, "fallback (sustained)"
 
 
-def recorded_traffic(kernel_file: str, config: str):
-    """DRAM bytes per launch from a committed ncu summary, if it was taken on the
-    current source of the kernel; else None."""
-    path = os.path.join(ROOT, "profiles", "traffic.json")
-    try:
+def kernel_source_hash(kernel_file: str, root: str = ROOT) -> str:
+    """Hash of a kernel's code: its file and, in their order, the headers that it
+    includes by relative path (theirs too), without comments and white space."""
+    csrc = os.path.join(root, "paged_kv_gqa_row_gb300", "csrc")
+    done, parts = set(), []
+
+    def take(path):
+        path = os.path.normpath(path)
+        if path in done:
+            return
+        done.add(path)
         with open(path) as f:
-            rec = json.load(f)
-        with open(os.path.join(ROOT, "paged_kv_gqa_row_gb300", "csrc", kernel_file), "rb") as f:
             src = f.read()
-        entry = rec.get(config)
-        if entry and entry.get("source_sha256") == hashlib.sha256(src).hexdigest():
+        for name in re.findall(r'^\s*#include "([^"]+)"', src, re.M):
+            take(os.path.join(os.path.dirname(path), name))
+        code = re.sub(r"/\*.*?\*/|//[^\n]*", " ", src, flags=re.S)
+        parts.append(os.path.basename(path) + "\n" + " ".join(code.split()))
+
+    take(os.path.join(csrc, kernel_file))
+    return hashlib.sha256("\n".join(parts).encode()).hexdigest()
+
+
+def recorded_traffic(kernel_file: str, config: str, root: str = ROOT):
+    """DRAM bytes per launch from a committed ncu summary, if it was taken on the
+    current source of the kernel (kernel_source_hash); else None."""
+    try:
+        with open(os.path.join(root, "profiles", "traffic.json")) as f:
+            entry = json.load(f).get(config)
+        if entry and entry.get("source_sha256") == kernel_source_hash(kernel_file, root):
             return float(entry["dram_bytes_per_launch"])
     except Exception:
         pass
