@@ -39,25 +39,34 @@ constexpr int kHeadsAtOnce = 2;
 constexpr int kMaxTokens = 2;    // of a CTA
 constexpr int kCtasPerSm = 4;
 
+// v in a range where none of the low parts below underflows, and no square of a
+// head's larger elements (with room on both sides).
+__device__ __forceinline__ bool rms_in_range(float v) { return v > 0x1p-90f && v < 0x1p100f; }
+
 // The QK-norm factor 1 / sqrt(ss / D + eps) as a float pair (about 2^-44): one
 // step from the float32 root r0.  With d = 1 - v r0^2 (v r0^2 in float pairs, the
 // difference exact), 1 / sqrt(v) = r0 (1 + d / 2 + 3 d^2 / 8 + ...), |d| < 2^-20.
 // (Double precision, as rope_math.cuh takes it once per head, is slow here: with
-// it this kernel's FP64 pipe was a third of its time.)  It holds while none of the
-// low parts underflows, v in [2^-90, 2^100] with room on both sides; what lies
-// outside (norm_eps = 0 and tiny heads, or huge ones) takes the double precision.
-__device__ __forceinline__ bool rms_in_range(float v) { return v > 0x1p-90f && v < 0x1p100f; }
-
+// it this kernel's FP64 pipe was a third of its time.)  A v out of range (norm_eps = 0 and tiny heads, or huge
+// ones) is brought into it by a power of four.
 template <int D>
 __device__ __forceinline__ DF rms_factor_df(DF ss, float eps) {
   constexpr double kInv = 1.0 / D;
   constexpr float kHi = static_cast<float>(kInv), kLo = static_cast<float>(kInv - static_cast<double>(kHi));
-  const DF v = df_add(df_mul(ss, DF{kHi, kLo}), DF{eps, 0.f});
-  if (!rms_in_range(v.hi)) return rms_factor(ss, D, static_cast<double>(eps));
-  const float r0 = rsqrtf(v.hi);
-  const DF w = df_mul(v, two_prod(r0, r0));
-  const float d = __fsub_rn(__fsub_rn(1.f, w.hi), w.lo);
-  return fast_two_sum(r0, __fmul_rn(r0, __fmul_rn(d, __fmaf_rn(0.375f, d, 0.5f))));
+  auto factor = [](DF sum, float e) {
+    const DF v = df_add(df_mul(sum, DF{kHi, kLo}), DF{e, 0.f});
+    const float r0 = rsqrtf(v.hi);
+    const DF w = df_mul(v, two_prod(r0, r0));
+    const float d = __fsub_rn(__fsub_rn(1.f, w.hi), w.lo);
+    return fast_two_sum(r0, __fmul_rn(r0, __fmul_rn(d, __fmaf_rn(0.375f, d, 0.5f))));
+  };
+  const float size = __fmaf_rn(ss.hi, kHi, eps);
+  if (!rms_in_range(size)) {
+    const float four = size < 1.f ? 0x1p80f : 0x1p-60f, two = size < 1.f ? 0x1p40f : 0x1p-30f;
+    const DF r = factor(DF{__fmul_rn(ss.hi, four), __fmul_rn(ss.lo, four)}, __fmul_rn(eps, four));
+    return DF{ss.hi == 0.f && eps == 0.f ? INFINITY : __fmul_rn(r.hi, two), __fmul_rn(r.lo, two)};
+  }
+  return factor(ss, eps);
 }
 
 // The float-pair evaluation of one head (a whole warp calls it).
@@ -77,20 +86,9 @@ __device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
   return d;
 }
 
-// Minima and maxima that a NaN among the operands makes NaN.
-__device__ __forceinline__ float min3_nan(float a, float b, float c) {
+__device__ __forceinline__ float fmin3(float a, float b, float c) {
   float d;
-  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-__device__ __forceinline__ float max3_nan(float a, float b, float c) {
-  float d;
-  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float d;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
 
@@ -100,20 +98,21 @@ struct Pair {
 };
 
 // Two outputs x a + y b (neighbouring elements), times r: their bf16 values (low
-// half first).  `wrong` collects bits where the bounds round differently; emin,
-// emax: the bounds' range (NaN if one of them is).
+// half first).  `wrong` collects bits where the bounds round differently; emin: the
+// least bound; esum: the bounds' sum (not finite if one of them is not, which it is
+// where an output is not: q and t are NaN together, whatever x, y and r hold).
 __device__ __forceinline__ uint32_t round_pair(uint64_t x, const Pair& a, uint64_t y, const Pair& b, uint64_t r,
-                                               uint64_t unit, bool normed, uint32_t& wrong, float& emin, float& emax) {
+                                               uint64_t unit, bool normed, uint32_t& wrong, float& emin, uint64_t& esum) {
   const uint64_t q = fma_f32x2(y, b.hi, fma_f32x2(y, b.lo, mul_f32x2(x, a.lo)));
   uint64_t t = fma_f32x2(x, a.hi, q);
   float q0, q1, t0, t1, e0, e1;
   f32x2_split(q, q0, q1);
   f32x2_split(t, t0, t1);
-  const uint64_t e = mul_f32x2(f32x2(max_nan(fabsf(q0), fabsf(t0)), max_nan(fabsf(q1), fabsf(t1))), unit);
+  const uint64_t e = mul_f32x2(f32x2(fmaxf(fabsf(q0), fabsf(t0)), fmaxf(fabsf(q1), fabsf(t1))), unit);
   if (normed) t = mul_f32x2(t, r);
   f32x2_split(e, e0, e1);
-  emin = min3_nan(emin, e0, e1);
-  emax = max3_nan(emax, e0, e1);
+  emin = fmin3(emin, e0, e1);
+  esum = add_f32x2(esum, e);
   float l0, l1, h0, h1;
   f32x2_split(fma_f32x2(e, f32x2(-1.f, -1.f), t), l0, l1);
   f32x2_split(add_f32x2(t, e), h0, h1);
@@ -210,8 +209,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) append4_kernel(const 
     lo = hi = 0u;
     if (pos < 0) return;
     const uint64_t x1 = f32x2(bf16_lo(xl), bf16_hi(xl)), x2 = f32x2(bf16_lo(xh), bf16_hi(xh));
-    uint32_t wrong = 0u;
-    float emin = 1.f, emax = 0.f;
+    bool in_range = true;
     uint64_t r = 0, unit = f32x2(3.5f * 0x1p-24f, 3.5f * 0x1p-24f);
     if (normed) {
       float q0, q1;
@@ -220,16 +218,20 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) append4_kernel(const 
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
       const float v = __fadd_rn(__fmul_rn(ss, 1.f / D), eps32);
-      if (!rms_in_range(v)) wrong = 1u;  // (the bound counts no underflow)
       const float r0 = rsqrtf(v);
       const float rr = __fmaf_rn(0.5f * r0, __fmaf_rn(-__fmul_rn(v, r0), r0, 1.f), r0);
       r = f32x2(rr, rr);
       unit = f32x2(12.f * 0x1p-24f * rr, 12.f * 0x1p-24f * rr);
+      in_range = rms_in_range(v);  // (the bound counts no underflow)
     }
-    lo = round_pair(x1, c1, x2, s2, r, unit, normed, wrong, emin, emax);
-    hi = round_pair(x2, c2, x1, s1, r, unit, normed, wrong, emin, emax);
+    uint32_t wrong = 0u;
+    float emin = 1.f, es0, es1;
+    uint64_t esum = 0;
+    lo = round_pair(x1, c1, x2, s2, r, unit, normed, wrong, emin, esum);
+    hi = round_pair(x2, c2, x1, s1, r, unit, normed, wrong, emin, esum);
+    f32x2_split(esum, es0, es1);
     // (bounds that are zero, tiny, huge or NaN leave it to the float pairs)
-    const bool certain = wrong == 0u && emin > 1e-30f && emax < 1e30f;
+    const bool certain = in_range && wrong == 0u && emin > 1e-30f && es0 + es1 < 1e30f;
     if (__any_sync(0xffffffffu, has && !certain)) {
       const uint2 x = rotate_exact<D>(xl, xh, co[0], co[1], normed, eps32);
       lo = x.x;

@@ -22,6 +22,7 @@
 // "Qwen3-4B", QK-norm paragraph.
 #pragma once
 
+#include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
 #include <cstdint>
@@ -165,11 +166,9 @@ __device__ __forceinline__ void sincos_df(float a, DF& sn, DF& cs) {
 }
 
 // Round hi + lo (|lo| <= half an ulp of hi, hi = RN(hi + lo)) to bf16, nearest even.
-// A NaN stays one (0x7FFF, as the hardware's conversion gives it): the integer
-// addition below would carry out of its exponent.
+// Not for NaN: the integer addition would carry out of its exponent.
 __device__ __forceinline__ uint32_t df_to_bf16(DF v) {
   const uint32_t u = __float_as_uint(v.hi);
-  if ((u & 0x7FFFFFFFu) > 0x7F800000u) return 0x7FFFu;
   if ((u & 0xFFFFu) == 0x8000u && v.lo != 0.f) {
     // hi sits exactly between two bf16 values: the low part decides
     const bool away = (v.lo > 0.f) == (v.hi > 0.f);
@@ -177,6 +176,8 @@ __device__ __forceinline__ uint32_t df_to_bf16(DF v) {
   }
   return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
 }
+
+__device__ __forceinline__ uint32_t float_to_bf16(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
@@ -376,6 +377,7 @@ __device__ __forceinline__ DF rms_factor(DF ss, int d, double eps) {
 __device__ __forceinline__ void rotate_pairs(uint32_t xlo, uint32_t xhi, const Coefs* c, int e, bool normed, DF r,
                                              uint32_t& lo_bits, uint32_t& hi_bits) {
   lo_bits = hi_bits = 0u;
+  bool nan_lo[2], nan_hi[2];
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const Coefs ci = c[e + k];
@@ -387,12 +389,25 @@ __device__ __forceinline__ void rotate_pairs(uint32_t xlo, uint32_t xhi, const C
       o1 = mul_df(o1, r);
       o2 = mul_df(o2, r);
     }
-    // An infinite or NaN input, or a result beyond float32's range, leaves NaN in a
-    // pair (its error terms are inf - inf): the float32 expression is the answer then.
-    if (o1.hi != o1.hi) o1 = DF{__fmul_rn(r.hi, __fsub_rn(__fmul_rn(x1, ci.gc1.hi), __fmul_rn(x2, ci.gs2.hi))), 0.f};
-    if (o2.hi != o2.hi) o2 = DF{__fmul_rn(r.hi, __fadd_rn(__fmul_rn(x2, ci.gc2.hi), __fmul_rn(x1, ci.gs1.hi))), 0.f};
     lo_bits |= df_to_bf16(o1) << (16 * k);
     hi_bits |= df_to_bf16(o2) << (16 * k);
+    nan_lo[k] = o1.hi != o1.hi;
+    nan_hi[k] = o2.hi != o2.hi;
+  }
+  // An infinite or NaN input, or a result beyond float32's range, leaves NaN in a
+  // pair (its error terms are inf - inf): the float32 expression is the answer then.
+  if (nan_lo[0] || nan_lo[1] || nan_hi[0] || nan_hi[1]) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const Coefs ci = c[e + k];
+      const float x1 = k ? bf16_hi(xlo) : bf16_lo(xlo);
+      const float x2 = k ? bf16_hi(xhi) : bf16_lo(xhi);
+      const uint32_t keep = 0xFFFFu << (16 - 16 * k);  // the other element
+      const float o1 = __fmul_rn(r.hi, __fsub_rn(__fmul_rn(x1, ci.gc1.hi), __fmul_rn(x2, ci.gs2.hi)));
+      const float o2 = __fmul_rn(r.hi, __fadd_rn(__fmul_rn(x2, ci.gc2.hi), __fmul_rn(x1, ci.gs1.hi)));
+      if (nan_lo[k]) lo_bits = (lo_bits & keep) | (float_to_bf16(o1) << (16 * k));
+      if (nan_hi[k]) hi_bits = (hi_bits & keep) | (float_to_bf16(o2) << (16 * k));
+    }
   }
 }
 
