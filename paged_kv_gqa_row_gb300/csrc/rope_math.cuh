@@ -22,7 +22,6 @@
 // "Qwen3-4B", QK-norm paragraph.
 #pragma once
 
-#include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
 #include <cstdint>
@@ -165,19 +164,24 @@ __device__ __forceinline__ void sincos_df(float a, DF& sn, DF& cs) {
   }
 }
 
-// Round hi + lo (|lo| <= half an ulp of hi, hi = RN(hi + lo)) to bf16, nearest even.
-// Not for NaN: the integer addition would carry out of its exponent.
-__device__ __forceinline__ uint32_t df_to_bf16(DF v) {
+// hi + lo (|lo| <= half an ulp of hi, hi = RN(hi + lo)) as a float that rounds to the
+// same bf16 value: hi, unless it sits exactly between two bf16 values and the low
+// part decides; then the next float on that side.
+__device__ __forceinline__ float df_off_tie(DF v) {
   const uint32_t u = __float_as_uint(v.hi);
   if ((u & 0xFFFFu) == 0x8000u && v.lo != 0.f) {
-    // hi sits exactly between two bf16 values: the low part decides
     const bool away = (v.lo > 0.f) == (v.hi > 0.f);
-    return (u >> 16) + (away ? 1u : 0u);
+    return __uint_as_float(away ? u + 1u : u - 1u);
   }
-  return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
+  return v.hi;
 }
 
-__device__ __forceinline__ uint32_t float_to_bf16(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
+// Two floats to bf16 (nearest even), `lo` in the low half; NaN becomes 0x7FFF.
+__device__ __forceinline__ uint32_t floats_to_bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
@@ -376,39 +380,35 @@ __device__ __forceinline__ DF rms_factor(DF ss, int d, double eps) {
 // factor when normed.
 __device__ __forceinline__ void rotate_pairs(uint32_t xlo, uint32_t xhi, const Coefs* c, int e, bool normed, DF r,
                                              uint32_t& lo_bits, uint32_t& hi_bits) {
-  lo_bits = hi_bits = 0u;
-  bool nan_lo[2], nan_hi[2];
+  float o1[2], o2[2];
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const Coefs ci = c[e + k];
     const float x1 = k ? bf16_hi(xlo) : bf16_lo(xlo);
     const float x2 = k ? bf16_hi(xhi) : bf16_lo(xhi);
-    DF o1 = dot2(x1, ci.gc1, x2, ci.gs2);
-    DF o2 = dot2(x2, ci.gc2, x1, DF{-ci.gs1.hi, -ci.gs1.lo});
+    DF a = dot2(x1, ci.gc1, x2, ci.gs2);
+    DF b = dot2(x2, ci.gc2, x1, DF{-ci.gs1.hi, -ci.gs1.lo});
     if (normed) {
-      o1 = mul_df(o1, r);
-      o2 = mul_df(o2, r);
+      a = mul_df(a, r);
+      b = mul_df(b, r);
     }
-    lo_bits |= df_to_bf16(o1) << (16 * k);
-    hi_bits |= df_to_bf16(o2) << (16 * k);
-    nan_lo[k] = o1.hi != o1.hi;
-    nan_hi[k] = o2.hi != o2.hi;
+    o1[k] = df_off_tie(a);
+    o2[k] = df_off_tie(b);
   }
   // An infinite or NaN input, or a result beyond float32's range, leaves NaN in a
   // pair (its error terms are inf - inf): the float32 expression is the answer then.
-  if (nan_lo[0] || nan_lo[1] || nan_hi[0] || nan_hi[1]) {
+  if (o1[0] != o1[0] || o1[1] != o1[1] || o2[0] != o2[0] || o2[1] != o2[1]) {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const Coefs ci = c[e + k];
       const float x1 = k ? bf16_hi(xlo) : bf16_lo(xlo);
       const float x2 = k ? bf16_hi(xhi) : bf16_lo(xhi);
-      const uint32_t keep = 0xFFFFu << (16 - 16 * k);  // the other element
-      const float o1 = __fmul_rn(r.hi, __fsub_rn(__fmul_rn(x1, ci.gc1.hi), __fmul_rn(x2, ci.gs2.hi)));
-      const float o2 = __fmul_rn(r.hi, __fadd_rn(__fmul_rn(x2, ci.gc2.hi), __fmul_rn(x1, ci.gs1.hi)));
-      if (nan_lo[k]) lo_bits = (lo_bits & keep) | (float_to_bf16(o1) << (16 * k));
-      if (nan_hi[k]) hi_bits = (hi_bits & keep) | (float_to_bf16(o2) << (16 * k));
+      if (o1[k] != o1[k]) o1[k] = __fmul_rn(r.hi, __fsub_rn(__fmul_rn(x1, ci.gc1.hi), __fmul_rn(x2, ci.gs2.hi)));
+      if (o2[k] != o2[k]) o2[k] = __fmul_rn(r.hi, __fadd_rn(__fmul_rn(x2, ci.gc2.hi), __fmul_rn(x1, ci.gs1.hi)));
     }
   }
+  lo_bits = floats_to_bf16x2(o1[0], o1[1]);
+  hi_bits = floats_to_bf16x2(o2[0], o2[1]);
 }
 
 }  // namespace rope
