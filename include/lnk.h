@@ -42,6 +42,9 @@
  *     not report).  No kernel traps or faults on bad data.
  *   - A negative position marks an inactive token or row: nothing is written
  *     for it and its outputs are zero.  This is not an error.
+ *   - A key that a query does not see adds nothing to its output, whatever the
+ *     pools hold there (NaN and infinities among it); those that it sees follow
+ *     the arithmetic's rules for them.
  *   - Ordering: attention reads the slots append_rope writes, so call
  *     append_rope first on the same stream.
  */
@@ -140,9 +143,8 @@ typedef struct lnk_attn_desc {
  *   that the block's largest element saturates: it is then off by at most
  *   1/17 of its size.)
  *     Attention uses the values e2m1(code) * e4m3(s) * pool scale; products of
- *   a code and a scale are exact in f16 and bf16.  A key that a query does not
- *   see adds nothing to its output, whatever its blocks hold; a NaN value block
- *   that it sees makes its 16 dimensions of the output NaN.  Every entry
+ *   a code and a scale are exact in f16 and bf16.  A NaN value block that a
+ *   query sees makes its 16 dimensions of the output NaN.  Every entry
  *   point takes these pools.  Attention converts the rotated queries to f16 as
  *   decode does for LNK_KV_E4M3, with the same range. */
 #define LNK_KV_BF16 0

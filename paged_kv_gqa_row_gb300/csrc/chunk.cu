@@ -37,6 +37,12 @@
 //    of O only when the running max grows by more than 2^8 (until then P stays
 //    below 256, exact enough in bf16); at the end the groups combine their
 //    sums and each normalises and stores half of the row of O.
+//
+// NaN and infinities.  A product multiplies every value row of a step into all 256
+// rows, and P = 0 does not keep out a value that is not finite.  A row whose output
+// has an element that is not finite computes those elements again at the end, from
+// its own keys alone (attend_row).
+//
 // Barriers that the other CTA arrives on live in rank 0 (the P and relay
 // barriers); the 2-SM commits arrive in both CTAs at once.
 //
@@ -113,6 +119,78 @@ __device__ __forceinline__ void step_entries(const ChunkParams& p, const int* ru
   const int lp = run_first[c.run] + 2 * c.s;
   ea = trow[lp];
   if (lp + 1 <= (run_kmax[c.run] - 1) / kPage) eb = trow[lp + 1];
+}
+
+// Half a row's attention key by key in float32, for the elements of `out` (D / 2 of
+// them, stored already) that are not finite.  q: the row's query; trow: its table row;
+// k, v: one kv head's pages, v from the half's first column; keys [lo, hi).
+template <int D>
+__device__ __noinline__ void attend_row(const uint16_t* q, const int32_t* trow, const uint16_t* k, const uint16_t* v,
+                                        uint16_t* out, int num_pages, int lo, int hi, float scale_log2) {
+  auto unpack = [](uint32_t w, float& a, float& b) {
+    a = __uint_as_float(w << 16);
+    b = __uint_as_float(w & 0xFFFF0000u);
+  };
+  auto score = [&](size_t slot) {
+    const uint4* kr = reinterpret_cast<const uint4*>(k + slot * D);
+    float s = 0.f;
+#pragma unroll 1
+    for (int c = 0; c < D / 8; ++c) {
+      const uint4 x = kr[c], y = reinterpret_cast<const uint4*>(q)[c];
+      const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float x0, x1, y0, y1;
+        unpack(xs[i], x0, x1);
+        unpack(ys[i], y0, y1);
+        s = fmaf(x0, y0, s);
+        s = fmaf(x1, y1, s);
+      }
+    }
+    return s * scale_log2;
+  };
+  float m = -INFINITY, l = 0.f;
+  float acc[D / 2];
+#pragma unroll
+  for (int i = 0; i < D / 2; ++i) acc[i] = 0.f;
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {  // the maximum, then the sums
+#pragma unroll 1
+    for (int key = lo; key < hi; ++key) {
+      const int page = trow[key / kPage];
+      if (page < 0 || page >= num_pages) continue;
+      const size_t slot = static_cast<size_t>(page) * kPage + key % kPage;
+      const float s = score(slot);
+      if (pass == 0) {
+        m = fmaxf(m, s);
+        continue;
+      }
+      const float w = exp2f(s - (m == -INFINITY ? 0.f : m));
+      l += w;
+      const uint4* vr = reinterpret_cast<const uint4*>(v + slot * D);
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {
+        const uint4 x = vr[c];
+        const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float x0, x1;
+          unpack(xs[i], x0, x1);
+          acc[8 * c + 2 * i] = fmaf(w, x0, acc[8 * c + 2 * i]);
+          acc[8 * c + 2 * i + 1] = fmaf(w, x1, acc[8 * c + 2 * i + 1]);
+        }
+      }
+    }
+  }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+  for (int i = 0; i < D / 4; ++i) {
+    uint32_t* o = reinterpret_cast<uint32_t*>(out) + i;
+    const uint32_t old = *o, now = pack_bf16x2(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+    uint32_t mask = (old & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u;
+    if ((old & 0x7F800000u) == 0x7F800000u) mask |= 0xFFFF0000u;
+    *o = (old & ~mask) | (now & mask);
+  }
 }
 
 template <int D>
@@ -679,15 +757,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     if (tl < nt) {
       uint4* o = reinterpret_cast<uint4*>(dst);
+      uint32_t odd = 0u;  // bits 15 and 31: an element is not finite
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
         float v[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[k] = live ? __uint_as_float(r[8 * i + k]) * inv : 0.f;
-        o[i] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                          pack_bf16x2(v[6], v[7]));
+        const uint4 w = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                                   pack_bf16x2(v[6], v[7]));
+        o[i] = w;
+        odd |= ((w.x & 0x7F807F80u) + 0x00800080u) | ((w.y & 0x7F807F80u) + 0x00800080u) |
+               ((w.z & 0x7F807F80u) + 0x00800080u) | ((w.w & 0x7F807F80u) + 0x00800080u);
+      }
+      if ((odd & 0x80008000u) != 0u) {
+        uint32_t cta;  // (the kv head again, so that it takes no register until here)
+        asm volatile("mov.u32 %0, %%ctaid.x;" : "=r"(cta));
+        const size_t pool = static_cast<size_t>((cta >> 1) % static_cast<uint32_t>(p.hkv)) * p.num_pages * kPage * D;
+        attend_row<D>(p.q + qrow, p.table + static_cast<size_t>(tok_row[tl]) * p.pages_per_row, p.k_pool + pool,
+                      p.v_pool + pool + grp * (D / 2), dst, p.num_pages, tok_lo[tl], tok_hi[tl], p.scale_log2);
       }
     }
+    __syncwarp();
   }
   if (*abort_flag && lane == 0 && p.status != nullptr) atomicOr(p.status, LNK_DEV_TIMEOUT);
   // neither CTA frees its tensor memory or leaves while the pair's products,
