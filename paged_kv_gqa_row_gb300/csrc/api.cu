@@ -595,10 +595,8 @@ lnk_status lnk_paged_step_attn(const lnk_attn_desc* desc, const lnk_bf16* q_rope
     c.num_rows = desc->num_rows;
     c.pages_per_row = desc->pages_per_row;
     c.window = desc->window;
-    c.k_pool = k_pool;
-    c.v_pool = v_pool;
-    c.k_pool4 = pools.k4;
-    c.v_pool4 = pools.v4;
+    c.k_pool = reinterpret_cast<const uint8_t*>(k_pool);
+    c.v_pool = reinterpret_cast<const uint8_t*>(v_pool);
     c.out_scale = desc->v_scale;
     c.tile_tokens = 128 / group;
     c.num_tiles = (P + kChunkHalves * c.tile_tokens - 1) / (kChunkHalves * c.tile_tokens);

@@ -40,8 +40,8 @@
 //
 // NaN and infinities.  A product multiplies every value row of a step into all 256
 // rows, and P = 0 does not keep out a value that is not finite.  A row whose output
-// has an element that is not finite computes those elements again at the end, from
-// its own keys alone (attend_row).
+// has elements that are not finite finds those again at the end, from its own keys
+// alone (attend_row).
 //
 // Barriers that the other CTA arrives on live in rank 0 (the P and relay
 // barriers); the 2-SM commits arrive in both CTAs at once.
@@ -121,33 +121,62 @@ __device__ __forceinline__ void step_entries(const ChunkParams& p, const int* ru
   if (lp + 1 <= (run_kmax[c.run] - 1) / kPage) eb = trow[lp + 1];
 }
 
-// Half a row's attention key by key in float32, for the elements of `out` (D / 2 of
-// them, stored already) that are not finite.  q: the row's query; trow: its table row;
-// k, v: one kv head's pages, v from the half's first column; keys [lo, hi).
+// Half a row's output again (D / 2 elements at `out`, stored already) where it is not
+// finite.  An element whose column holds a NaN or an infinity among the row's own keys
+// is what the sum of positive weights times them gives; one that has none took it from
+// keys that the row does not see, and is computed in float32, key by key.
+// q: the row's query; trow: its table row; k, v: one kv head's pages, v from the half's
+// first column; keys [lo, hi).
+// (What it costs: four prompts of 1024 tokens after 8192 others, 32 query heads on 8,
+// D = 128, take 0.55 ms; with a NaN value in one of them at position 0, which its tokens
+// find at once, 0.61 ms; at position 8192, 6.9 ms; at 9000, where the 40 tokens before it
+// in its tile compute again, 48 ms.)
 template <int D>
 __device__ __noinline__ void attend_row(const uint16_t* q, const int32_t* trow, const uint16_t* k, const uint16_t* v,
                                         uint16_t* out, int num_pages, int lo, int hi, float scale_log2) {
+  constexpr int kWords = D / 4;  // pairs of elements
+  // bits 15 and 31: the half of a pair that is not finite
+  auto odd_halves = [](uint32_t w) { return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u; };
+  uint64_t todo = 0;  // a bit per element
+#pragma unroll 1
+  for (int i = 0; i < kWords; ++i) {
+    const uint32_t m = odd_halves(reinterpret_cast<const uint32_t*>(out)[i]);
+    todo |= static_cast<uint64_t>((m >> 15 & 1u) | (m >> 30 & 2u)) << (2 * i);
+  }
+  uint64_t nan = 0, pos = 0, neg = 0;  // of the visible values in these columns
+#pragma unroll 1
+  for (int key = lo; key < hi; ++key) {
+    const int page = trow[key / kPage];
+    if (page < 0 || page >= num_pages) continue;
+    const uint32_t* vr = reinterpret_cast<const uint32_t*>(v + (static_cast<size_t>(page) * kPage + key % kPage) * D);
+    uint32_t any = 0u;
+#pragma unroll
+    for (int c = 0; c < kWords / 4; ++c) {
+      const uint4 x = reinterpret_cast<const uint4*>(vr)[c];
+      any |= odd_halves(x.x) | odd_halves(x.y) | odd_halves(x.z) | odd_halves(x.w);
+    }
+    if (any == 0u) continue;
+#pragma unroll 1
+    for (int e = 0; e < 2 * kWords; ++e) {
+      const uint32_t x = reinterpret_cast<const uint16_t*>(vr)[e];
+      if ((x & 0x7F80u) != 0x7F80u) continue;
+      const uint64_t bit = 1ull << e;
+      if ((x & 0x7Fu) != 0u) nan |= bit;
+      else if (x & 0x8000u) neg |= bit;
+      else pos |= bit;
+    }
+    if ((todo & ~(nan | (pos & neg))) == 0) break;
+  }
+  nan |= pos & neg;
+  const uint64_t rest = todo & ~(nan | pos | neg);
+#pragma unroll 1
+  for (int e = 0; e < 2 * kWords; ++e)
+    if (todo >> e & 1) out[e] = nan >> e & 1 ? 0x7FFF : (pos >> e & 1 ? 0x7F80 : 0xFF80);
+  if (rest == 0) return;
+
   auto unpack = [](uint32_t w, float& a, float& b) {
     a = __uint_as_float(w << 16);
     b = __uint_as_float(w & 0xFFFF0000u);
-  };
-  auto score = [&](size_t slot) {
-    const uint4* kr = reinterpret_cast<const uint4*>(k + slot * D);
-    float s = 0.f;
-#pragma unroll 1
-    for (int c = 0; c < D / 8; ++c) {
-      const uint4 x = kr[c], y = reinterpret_cast<const uint4*>(q)[c];
-      const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float x0, x1, y0, y1;
-        unpack(xs[i], x0, x1);
-        unpack(ys[i], y0, y1);
-        s = fmaf(x0, y0, s);
-        s = fmaf(x1, y1, s);
-      }
-    }
-    return s * scale_log2;
   };
   float m = -INFINITY, l = 0.f;
   float acc[D / 2];
@@ -160,7 +189,22 @@ __device__ __noinline__ void attend_row(const uint16_t* q, const int32_t* trow, 
       const int page = trow[key / kPage];
       if (page < 0 || page >= num_pages) continue;
       const size_t slot = static_cast<size_t>(page) * kPage + key % kPage;
-      const float s = score(slot);
+      const uint4* kr = reinterpret_cast<const uint4*>(k + slot * D);
+      float s = 0.f;
+#pragma unroll 1
+      for (int c = 0; c < D / 8; ++c) {
+        const uint4 x = kr[c], y = reinterpret_cast<const uint4*>(q)[c];
+        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float x0, x1, y0, y1;
+          unpack(xs[i], x0, x1);
+          unpack(ys[i], y0, y1);
+          s = fmaf(x0, y0, s);
+          s = fmaf(x1, y1, s);
+        }
+      }
+      s *= scale_log2;
       if (pass == 0) {
         m = fmaxf(m, s);
         continue;
@@ -184,13 +228,8 @@ __device__ __noinline__ void attend_row(const uint16_t* q, const int32_t* trow, 
   }
   const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll
-  for (int i = 0; i < D / 4; ++i) {
-    uint32_t* o = reinterpret_cast<uint32_t*>(out) + i;
-    const uint32_t old = *o, now = pack_bf16x2(acc[2 * i] * inv, acc[2 * i + 1] * inv);
-    uint32_t mask = (old & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u;
-    if ((old & 0x7F800000u) == 0x7F800000u) mask |= 0xFFFF0000u;
-    *o = (old & ~mask) | (now & mask);
-  }
+  for (int e = 0; e < D / 2; ++e)
+    if (rest >> e & 1) out[e] = static_cast<uint16_t>(pack_bf16x2(acc[e] * inv, 0.f));
 }
 
 template <int D>
@@ -769,12 +808,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         odd |= ((w.x & 0x7F807F80u) + 0x00800080u) | ((w.y & 0x7F807F80u) + 0x00800080u) |
                ((w.z & 0x7F807F80u) + 0x00800080u) | ((w.w & 0x7F807F80u) + 0x00800080u);
       }
-      if ((odd & 0x80008000u) != 0u) {
+      if ((odd & 0x80008000u) != 0u && l_part == l_part) {  // (a NaN score is the row's own: all of it is NaN)
         uint32_t cta;  // (the kv head again, so that it takes no register until here)
         asm volatile("mov.u32 %0, %%ctaid.x;" : "=r"(cta));
         const size_t pool = static_cast<size_t>((cta >> 1) % static_cast<uint32_t>(p.hkv)) * p.num_pages * kPage * D;
-        attend_row<D>(p.q + qrow, p.table + static_cast<size_t>(tok_row[tl]) * p.pages_per_row, p.k_pool + pool,
-                      p.v_pool + pool + grp * (D / 2), dst, p.num_pages, tok_lo[tl], tok_hi[tl], p.scale_log2);
+        attend_row<D>(p.q + qrow, p.table + static_cast<size_t>(tok_row[tl]) * p.pages_per_row,
+                      reinterpret_cast<const uint16_t*>(p.k_pool) + pool,
+                      reinterpret_cast<const uint16_t*>(p.v_pool) + pool + grp * (D / 2), dst, p.num_pages, tok_lo[tl], tok_hi[tl], p.scale_log2);
       }
     }
     __syncwarp();

@@ -548,9 +548,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk4_
             const uint32_t fb = smem_addr(rawfull + sp);
             mbar_arrive_expect_tx(fb, 3 * L::kPageBytes);
             const uint32_t dst = smem_addr(smem + L::packed + size_t(sp) * 3 * L::kPageBytes);
-            bulk_load(dst, p.k_pool4 + (head + (rank == 0 ? pa : pb)) * L::kPageBytes, L::kPageBytes, fb);
-            bulk_load(dst + L::kPageBytes, p.v_pool4 + (head + pa) * L::kPageBytes, L::kPageBytes, fb);
-            bulk_load(dst + 2 * L::kPageBytes, p.v_pool4 + (head + pb) * L::kPageBytes, L::kPageBytes, fb);
+            bulk_load(dst, p.k_pool + (head + (rank == 0 ? pa : pb)) * L::kPageBytes, L::kPageBytes, fb);
+            bulk_load(dst + L::kPageBytes, p.v_pool + (head + pa) * L::kPageBytes, L::kPageBytes, fb);
+            bulk_load(dst + 2 * L::kPageBytes, p.v_pool + (head + pb) * L::kPageBytes, L::kPageBytes, fb);
             cur = nxt;
             ea = na;
             eb = nb;
@@ -967,7 +967,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk4_
         uint32_t nans = 0u;
         if (nan_notes[n % kNanNotes] == n + 1) {
           if (live)
-            nans = nan_blocks<D>(p.v_pool4 + static_cast<size_t>(h) * p.num_pages * L::kPageBytes,
+            nans = nan_blocks<D>(p.v_pool + static_cast<size_t>(h) * p.num_pages * L::kPageBytes,
                                  p.table + static_cast<size_t>(p.rows[t0 + tl]) * p.pages_per_row, p.num_pages, lo, hi,
                                  grp * (D / 32));
           __syncwarp();

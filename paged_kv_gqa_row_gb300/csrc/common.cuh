@@ -137,10 +137,8 @@ struct ChunkParams {
   uint16_t* out;              // [P][Hq][D]
   int32_t* status;
   int P, hq, hkv, group, num_pages, num_rows, pages_per_row, window;
-  const uint16_t* k_pool;     // bf16 pools (their tiles come through tensor maps)
-  const uint16_t* v_pool;
-  const uint8_t* k_pool4;     // 4-bit pools
-  const uint8_t* v_pool4;
+  const uint8_t* k_pool;      // (the tiles of bf16 pools come through tensor maps)
+  const uint8_t* v_pool;
   float out_scale;            // the value scale of 4-bit pools
   int tile_tokens, num_tiles;  // tokens per half tile (128 / group); tiles of kChunkHalves halves
   float scale_log2;
