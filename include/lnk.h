@@ -91,7 +91,8 @@ typedef struct lnk_attn_desc {
   int32_t pages_per_row;  /* columns of table (its row stride, in entries) */
   int32_t window;         /* 0: none; else key j is visible to a query at p
                              iff p - window < j <= p (itself and window - 1 before) */
-  float scale;            /* softmax scale; 0 selects 1 / sqrt(head_dim) */
+  float scale;            /* softmax scale; 0 selects 1 / sqrt(head_dim).  The scale (times
+                             k_scale, below) must lie in float32's range in log2 units */
   int32_t kv_dtype;       /* element type of k_pool / v_pool: LNK_KV_BF16 (0, the
                              pages' pools), LNK_KV_E4M3 (8-bit pools, below) or
                              LNK_KV_E2M1 (4-bit pools, below) */

@@ -88,6 +88,14 @@ bool pool_map(CUtensorMap* map, const void* pool, const lnk_attn_desc& d) {
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// Softmax scale in log2 units; for 8-bit and 4-bit pools the scores are
+// computed without the pool's key scale, so it joins the softmax scale.
+float scale_log2(const lnk_attn_desc* d) {
+  double s = d->scale > 0.f ? static_cast<double>(d->scale) : 1.0 / std::sqrt(static_cast<double>(d->head_dim));
+  if (d->kv_dtype != LNK_KV_BF16) s *= static_cast<double>(d->k_scale);
+  return static_cast<float>(s * 1.4426950408889634);  // log2(e)
+}
+
 // Shape checks shared by every entry point.
 lnk_status check_desc(const lnk_attn_desc* d) {
   if (d == nullptr) return LNK_EINVAL;
@@ -102,19 +110,13 @@ lnk_status check_desc(const lnk_attn_desc* d) {
   if (d->kv_dtype != LNK_KV_BF16 && !(d->k_scale > 0.f && d->k_scale <= FLT_MAX && d->v_scale > 0.f &&
                                        d->v_scale <= FLT_MAX))
     return LNK_EINVAL;
+  // (a zero or infinite factor would make NaN of masked scores and of zero ones)
+  if (!(scale_log2(d) > 0.f && scale_log2(d) <= FLT_MAX)) return LNK_ERANGE;
   // TMA row coordinates and 32-bit position arithmetic must not overflow
   if (static_cast<long long>(d->num_kv_heads) * d->num_pages * kPage >= (1ll << 31)) return LNK_ERANGE;
   if (static_cast<long long>(d->pages_per_row) * kPage >= (1ll << 31)) return LNK_ERANGE;
   if (static_cast<long long>(d->num_rows) * d->pages_per_row >= (1ll << 31)) return LNK_ERANGE;
   return LNK_OK;
-}
-
-// Softmax scale in log2 units; for 8-bit and 4-bit pools the scores are
-// computed without the pool's key scale, so it joins the softmax scale.
-float scale_log2(const lnk_attn_desc* d) {
-  double s = d->scale > 0.f ? static_cast<double>(d->scale) : 1.0 / std::sqrt(static_cast<double>(d->head_dim));
-  if (d->kv_dtype != LNK_KV_BF16) s *= static_cast<double>(d->k_scale);
-  return static_cast<float>(s * 1.4426950408889634);  // log2(e)
 }
 
 }  // namespace
