@@ -18,11 +18,14 @@
 // A CTA takes one or two tokens, or half of one, with eight warps: its threads evaluate the
 // sines and cosines once (one frequency of one token each), and after the one
 // barrier every warp takes a share of one token's heads, the loads of the next two
-// heads in flight while it works on two.  What bounds it: instructions, 10000 a
-// token at 2.6 a cycle of an SM (about 60 a head, 20 more with the norm, 100 more to
-// quantize a key row, 10 of them for each division; 400 a frequency).  2048 tokens
-// with QK-norm, 32 query heads on 8, D = 128: 27 us (1.6 TB/s of what it reads and
-// writes; 31 us with three CTAs an SM and four heads at once).
+// heads in flight while it works on two.  What bounds it: instructions, at 2.6 a cycle
+// of an SM.  2048 tokens with QK-norm, 32 query heads on 8, D = 128: 10100 warp
+// instructions a token, which launches of other shapes divide into 153 a query head
+// (97 without the norm), 327 a key and value head (77 more where a pool scale is no
+// power of two and the quantizer divides) and 2590 that a token costs whatever its heads
+// (sines and cosines, and the coefficients, which each of its four warps sets up twice);
+// 27 us (1.6 TB/s of what it reads and writes; 31 us with three CTAs an SM and four
+// heads at once).
 //
 // Sources: as append_rope.cu; the 4-bit format is this library's (lnk_attn_desc).
 #include "common.cuh"

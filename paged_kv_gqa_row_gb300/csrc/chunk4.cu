@@ -34,8 +34,8 @@
 // What bounds it: the chain of one step, products of 500 cycles each behind one
 // another, a softmax of 2500 cycles, three steps in flight; the tensor cores are busy a
 // third of the time.  Four prompts of 1024 to 2047 tokens, 32 query heads on 8,
-// D = 128: 127 us, 645 TFLOP/s (chunk.cu on bf16 pools 181 us).  Four prompts of 512
-// tokens after 1024 to 7168 others, with 32 decode rows: 187 us (bf16 pools 255 us).
+// D = 128: 129 us, 637 TFLOP/s (chunk.cu on bf16 pools 181 us).  Four prompts of 512
+// tokens after 1024 to 7168 others, with 32 decode rows: 190 us (bf16 pools 255 us).
 // Eight converting warps instead of four (fewer registers for all) took 10% longer,
 // deeper rings of tiles and shallower ones of packed pages as long; the next tile's
 // first step before a tile's end, or one loop for the keys' and the values'
@@ -1014,8 +1014,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk4_
       if (!ok || !more) break;
     }
   }
-  // The next kernel on the stream may start when all clusters are here.  (Allowed at
-  // the start, the CTAs of a decode kernel that waits took 1% from the last clusters.)
+  // The next kernel on the stream may start when every CTA has a thread here, at the
+  // latest when its set-up warp has set up the cluster's last tile.  (Allowed at the
+  // start, the CTAs of a decode kernel that waits took 1% from the last clusters.)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (*abort_flag && lane == 0 && p.status != nullptr) atomicOr(p.status, LNK_DEV_TIMEOUT);
   // neither CTA frees its tensor memory or leaves while the pair's products,

@@ -7,7 +7,7 @@
 // a CTA moves its unit with 16-byte loads and stores, four of each in flight
 // per thread.  The layers' pool addresses travel in the launch parameters, so
 // a copy in every layer of a model is one launch and can be captured.  Bound by HBM:
-// 160 pages of 8 heads in 32 layers, 4-bit pools, D = 128, 2.7 GB read and written:
+// 160 pages of 8 heads in 32 layers, bf16 pools, D = 128, 2.7 GB read and written:
 // 403 us, 6.6 TB/s; three pages: 8.9 us.
 #include "common.cuh"
 
