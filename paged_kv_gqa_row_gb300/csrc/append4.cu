@@ -50,8 +50,8 @@ __device__ __forceinline__ bool rms_in_range(float v) { return v > 0x1p-90f && v
 // step from the float32 root r0.  With d = 1 - v r0^2 (v r0^2 in float pairs, the
 // difference exact), 1 / sqrt(v) = r0 (1 + d / 2 + 3 d^2 / 8 + ...), |d| < 2^-20.
 // (Double precision, as rope_math.cuh takes it once per head, is slow here: with
-// it this kernel's FP64 pipe was a third of its time.)  A v out of range (norm_eps = 0 and tiny heads, or huge
-// ones) is brought into it by a power of four.
+// it this kernel's FP64 pipe was a third of its time.)  A v out of range (norm_eps =
+// 0 and tiny heads, or huge ones) is brought into it by a power of four.
 template <int D>
 __device__ __forceinline__ DF rms_factor_df(DF ss, float eps) {
   constexpr double kInv = 1.0 / D;
