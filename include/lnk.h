@@ -530,6 +530,118 @@ lnk_status lnk_paged_copy_pages_layers(const lnk_attn_desc* desc, lnk_bf16* cons
                                        lnk_stream stream);
 
 /* ---------------------------------------------------------------------------
+ * Latent cache
+ *
+ * For models whose keys and values come from one latent vector a token that all
+ * query heads share (latent attention; not on the pages): a pool holds, a token,
+ * the normalised latent c (C numbers) and the key's rotated part k (R numbers),
+ * and nothing a head.  The pager and its tables serve these pools unchanged.
+ *
+ * Head h has weights U_h [N][C] and V_h [N][C]; its keys are [U_h c, k] and its
+ * values V_h c.  Two forms of the same attention:
+ *   absorbed  the caller multiplies the query's first N numbers by U_h before the
+ *             call (q = [q_h U_h, rotated part], C + R numbers) and the output by
+ *             V_h after it; the keys are then the pool's rows, the values their
+ *             first C numbers.  lnk_latent_decode_attn, lnk_latent_step_attn.
+ *   expanded  the caller computes every head's keys and values from the latents;
+ *             fewer operations for whole prompts.  lnk_latent_prompt_attn.
+ *
+ * The conventions at the top hold.  A pool is [num_pages * 64][C + R] bf16, 16-byte
+ * aligned; position j of table row r is pool row table[r][j / 64] * 64 + j % 64.
+ * ------------------------------------------------------------------------- */
+typedef struct lnk_latent_desc {
+  int32_t num_heads;      /* query heads, 1 .. 1024 */
+  int32_t latent_dim;     /* C in {128, 256, 384, 512} */
+  int32_t rope_dim;       /* R in {32, 64} */
+  int32_t page_size;      /* positions per page; must be 64 */
+  int32_t num_pages;      /* pages of the pool */
+  int32_t num_rows;       /* rows of table */
+  int32_t pages_per_row;  /* columns of table (its row stride, in entries) */
+  int32_t window;         /* as in lnk_attn_desc */
+  float scale;            /* softmax scale, > 0 (that of the expanded heads: the absorbed
+                             query's length does not tell it), in float32's range in
+                             log2 units */
+} lnk_latent_desc;
+
+/* Bytes of device workspace that decode_attn / step_attn over a latent pool need on
+ * the current device (0 on bad arguments).  It needs no initialisation.  Calls that
+ * share a workspace must not run concurrently. */
+size_t lnk_latent_workspace_size(const lnk_latent_desc* desc);
+
+/*
+ * lnk_latent_append -- per token: the latent's RMS norm, the rotation, the write.
+ *
+ *   q        device: the query heads' parts to rotate, R numbers each; head h of token
+ *            t starts at q + (t * num_heads + h) * q_stride (elements; even, >= R), so
+ *            that projected queries are read where they lie.  4-byte aligned
+ *   kv       device [T][C + R]: projected latent and key part (16-byte aligned)
+ *   positions, rows, slots, table  as in lnk_paged_append_rope
+ *   norm_w   device [C] weights of the latent's RMS norm (16-byte aligned), or NULL: c
+ *            is the projected latent, bit for bit
+ *   norm_eps its epsilon
+ *   pool     device pool (written at the tokens' places only)
+ *   q_out    device: rotated parts, at q_out + (t * num_heads + h) * q_out_stride (zero
+ *            for inactive tokens); the numbers between them are left as they are.  With
+ *            q_out_stride = C + R and q_out C numbers into the absorbed queries they
+ *            land where lnk_latent_decode_attn reads them.  q_out = q with the same
+ *            stride rotates in place; otherwise the two must not overlap.
+ *   kv_out   device [T][C + R] or NULL: what the pool receives, packed (zero for
+ *            inactive tokens): the input of the expanded form's products
+ *   T        tokens (0 is allowed and enqueues nothing)
+ *
+ * Element i of a rotated part turns with element i + R / 2.  Numerics, the order of
+ * reads before the kernel before this one has ended, and what infinities and NaN do:
+ * as in lnk_paged_append_rope, the norm being that of its QK-norm over C numbers.
+ */
+lnk_status lnk_latent_append(const lnk_latent_desc* desc, const lnk_rope_desc* rope, const lnk_bf16* q,
+                             int64_t q_stride, const lnk_bf16* kv, const int32_t* positions,
+                             const int32_t* rows, const int32_t* slots, const int32_t* table,
+                             const lnk_bf16* norm_w, float norm_eps, lnk_bf16* pool, lnk_bf16* q_out,
+                             int64_t q_out_stride, lnk_bf16* kv_out, int32_t T, int32_t* dev_status,
+                             lnk_stream stream);
+
+/*
+ * lnk_latent_decode_attn -- absorbed attention, one query token per decode row.
+ *
+ *   q        device [B][num_heads][C + R] (16-byte aligned)
+ *   positions, table  as in lnk_paged_decode_attn: row b uses table row b
+ *   pool     device pool
+ *   out      device [B][num_heads][C] (16-byte aligned)
+ *   B        decode rows, 0 <= B <= min(num_rows, 4096)
+ *   workspace device scratch of ws_bytes >= lnk_latent_workspace_size(desc), 256-byte
+ *            aligned
+ *
+ * positions and table are read before the kernel before this one on the stream has
+ * ended, as in lnk_paged_decode_attn.
+ */
+lnk_status lnk_latent_decode_attn(const lnk_latent_desc* desc, const lnk_bf16* q, const int32_t* positions,
+                                  const int32_t* table, const lnk_bf16* pool, lnk_bf16* out, int32_t B,
+                                  void* workspace, size_t ws_bytes, int32_t* dev_status, lnk_stream stream);
+
+/*
+ * lnk_latent_step_attn -- absorbed attention of packed prompt pieces and decode rows.
+ *
+ *   q        device [P + B][num_heads][C + R]: P piece tokens, then B decode rows
+ *   rows, positions  device int32 [P]: table row and position of each piece token (pieces
+ *            of prompts, proposed tokens to check: a token sees its row's keys up to its
+ *            position, whichever call wrote them)
+ *   step_positions  device int32 [B]: decode row b's position; row b uses table row b
+ *   out      device [P + B][num_heads][C]
+ *   (P + B) * num_heads < 2^31.  The rest as in lnk_latent_decode_attn; rows and
+ *   step_positions are read as early as positions.
+ */
+lnk_status lnk_latent_step_attn(const lnk_latent_desc* desc, const lnk_bf16* q, const int32_t* rows,
+                                const int32_t* positions, const int32_t* step_positions, const int32_t* table,
+                                const lnk_bf16* pool, lnk_bf16* out, int32_t P, int32_t B, void* workspace,
+                                size_t ws_bytes, int32_t* dev_status, lnk_stream stream);
+
+/* lnk_paged_copy_pages_layers for latent pools: `pools` is a host array of `layers`
+ * device pointers.  One launch for up to 256 layers and 65535 pairs. */
+lnk_status lnk_latent_copy_pages(const lnk_latent_desc* desc, lnk_bf16* const* pools, int32_t layers,
+                                 const int32_t* src_pages, const int32_t* dst_pages, int32_t n,
+                                 int32_t* dev_status, lnk_stream stream);
+
+/* ---------------------------------------------------------------------------
  * Self-test of the bounded waits.  Every wait inside the kernels above is
  * bounded: after about two seconds it gives up, the CTA's other roles stop,
  * the kernel ORs LNK_DEV_TIMEOUT into *dev_status and returns (no trap, no

@@ -12,10 +12,17 @@ from .binding import (  # noqa: F401
     KV_E4M3,
     LIBRARY_PATH,
     AttnDesc,
+    LatentDesc,
     LnkError,
     Pager,
     RopeDesc,
     attn_desc,
+    latent_desc,
+    lnk_latent_append,
+    lnk_latent_copy_pages,
+    lnk_latent_decode_attn,
+    lnk_latent_step_attn,
+    lnk_latent_workspace_size,
     lnk_paged_append_rope,
     lnk_paged_copy_pages,
     lnk_paged_copy_pages_layers,

@@ -21,7 +21,7 @@ if not os.path.exists(LIBRARY_PATH):
     raise ImportError(f"liblnk.so is not built ({LIBRARY_PATH}); run paged_kv_gqa_row_gb300/build.py")
 _lib = ctypes.CDLL(LIBRARY_PATH)
 
-c_i32, c_f32, c_f64, c_size, c_vp = ctypes.c_int32, ctypes.c_float, ctypes.c_double, ctypes.c_size_t, ctypes.c_void_p
+c_i32, c_i64, c_f32, c_f64, c_size, c_vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_double, ctypes.c_size_t, ctypes.c_void_p
 
 LNK_OK = 0
 STATUS_NAMES = {0: "LNK_OK", 1: "LNK_EINVAL", 2: "LNK_ERANGE", 3: "LNK_ECUDA",
@@ -36,6 +36,8 @@ EXPORTED = ["lnk_status_string", "lnk_rope_inv_freq", "lnk_paged_workspace_size"
             "lnk_pager_fork", "lnk_pager_prepare_append", "lnk_pager_release", "lnk_pager_table",
             "lnk_pager_free_pages", "lnk_pager_refcount", "lnk_paged_copy_pages",
             "lnk_paged_page_bytes", "lnk_paged_read_tokens", "lnk_pager_compact", "lnk_paged_copy_pages_layers",
+            "lnk_latent_workspace_size", "lnk_latent_append", "lnk_latent_decode_attn", "lnk_latent_step_attn",
+            "lnk_latent_copy_pages",
             "lnk_selftest_wait_timeout"]
 
 
@@ -60,6 +62,12 @@ class RopeDesc(ctypes.Structure):
     _fields_ = [("theta", c_f64), ("llama3", c_i32), ("factor", c_f64),
                 ("low_freq_factor", c_f64), ("high_freq_factor", c_f64),
                 ("original_max_position", c_f64)]
+
+
+class LatentDesc(ctypes.Structure):
+    _fields_ = [("num_heads", c_i32), ("latent_dim", c_i32), ("rope_dim", c_i32), ("page_size", c_i32),
+                ("num_pages", c_i32), ("num_rows", c_i32), ("pages_per_row", c_i32), ("window", c_i32),
+                ("scale", c_f32)]
 
 
 _lib.lnk_status_string.restype = ctypes.c_char_p
@@ -118,6 +126,19 @@ _lib.lnk_paged_copy_pages_layers.restype = ctypes.c_int
 _lib.lnk_paged_copy_pages_layers.argtypes = [ctypes.POINTER(AttnDesc), c_vp, c_vp, c_i32, c_vp, c_vp, c_i32, c_vp, c_vp]
 _lib.lnk_paged_copy_pages.restype = ctypes.c_int
 _lib.lnk_paged_copy_pages.argtypes = [ctypes.POINTER(AttnDesc), c_vp, c_vp, c_vp, c_vp, c_i32, c_vp, c_vp]
+_lib.lnk_latent_workspace_size.restype = c_size
+_lib.lnk_latent_workspace_size.argtypes = [ctypes.POINTER(LatentDesc)]
+_lib.lnk_latent_append.restype = ctypes.c_int
+_lib.lnk_latent_append.argtypes = [ctypes.POINTER(LatentDesc), ctypes.POINTER(RopeDesc), c_vp, c_i64, c_vp, c_vp, c_vp,
+                                   c_vp, c_vp, c_vp, c_f32, c_vp, c_vp, c_i64, c_vp, c_i32, c_vp, c_vp]
+_lib.lnk_latent_decode_attn.restype = ctypes.c_int
+_lib.lnk_latent_decode_attn.argtypes = [ctypes.POINTER(LatentDesc), c_vp, c_vp, c_vp, c_vp, c_vp, c_i32, c_vp, c_size,
+                                        c_vp, c_vp]
+_lib.lnk_latent_step_attn.restype = ctypes.c_int
+_lib.lnk_latent_step_attn.argtypes = [ctypes.POINTER(LatentDesc), c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_i32, c_i32,
+                                      c_vp, c_size, c_vp, c_vp]
+_lib.lnk_latent_copy_pages.restype = ctypes.c_int
+_lib.lnk_latent_copy_pages.argtypes = [ctypes.POINTER(LatentDesc), c_vp, c_i32, c_vp, c_vp, c_i32, c_vp, c_vp]
 _lib.lnk_selftest_wait_timeout.restype = ctypes.c_int
 _lib.lnk_selftest_wait_timeout.argtypes = [c_vp, ctypes.c_uint64, c_vp]
 
@@ -133,6 +154,11 @@ def rope_desc(theta, llama3=None) -> RopeDesc:
         return RopeDesc(theta, 0, 0.0, 0.0, 0.0, 0.0)
     factor, low, high, orig = llama3
     return RopeDesc(theta, 1, factor, low, high, orig)
+
+
+def latent_desc(num_heads, latent_dim, rope_dim, num_pages, num_rows, pages_per_row, scale, window=0,
+                page_size=64) -> LatentDesc:
+    return LatentDesc(num_heads, latent_dim, rope_dim, page_size, num_pages, num_rows, pages_per_row, window, scale)
 
 
 def _ptr(x) -> Optional[int]:
@@ -271,6 +297,41 @@ def lnk_paged_copy_pages_layers(desc, k_pools, v_pools, src_pages, dst_pages, n,
     st = _lib.lnk_paged_copy_pages_layers(ctypes.byref(desc), k.buffer_info()[0], v.buffer_info()[0], len(k),
                                           _ptr(src_pages), _ptr(dst_pages), n, _ptr(dev_status), _stream(stream))
     _check(st, "lnk_paged_copy_pages_layers")
+
+
+def lnk_latent_workspace_size(desc: LatentDesc) -> int:
+    return int(_lib.lnk_latent_workspace_size(ctypes.byref(desc)))
+
+
+def lnk_latent_append(desc, rope, q, q_stride, kv, positions, rows, slots, table, norm_w, norm_eps, pool, q_out,
+                      q_out_stride, kv_out, T, dev_status=None, stream=None):
+    """q and q_out may be views: their addresses are the first head's rotated part, the strides go from head to head."""
+    st = _lib.lnk_latent_append(ctypes.byref(desc), ctypes.byref(rope), _ptr(q), q_stride, _ptr(kv), _ptr(positions),
+                                _ptr(rows), _ptr(slots), _ptr(table), _ptr(norm_w), norm_eps, _ptr(pool), _ptr(q_out),
+                                q_out_stride, _ptr(kv_out), T, _ptr(dev_status), _stream(stream))
+    _check(st, "lnk_latent_append")
+
+
+def lnk_latent_decode_attn(desc, q, positions, table, pool, out, B, workspace, ws_bytes, dev_status=None, stream=None):
+    st = _lib.lnk_latent_decode_attn(ctypes.byref(desc), _ptr(q), _ptr(positions), _ptr(table), _ptr(pool), _ptr(out), B,
+                                     _ptr(workspace), ws_bytes, _ptr(dev_status), _stream(stream))
+    _check(st, "lnk_latent_decode_attn")
+
+
+def lnk_latent_step_attn(desc, q, rows, positions, step_positions, table, pool, out, P, B, workspace, ws_bytes,
+                         dev_status=None, stream=None):
+    st = _lib.lnk_latent_step_attn(ctypes.byref(desc), _ptr(q), _ptr(rows), _ptr(positions), _ptr(step_positions),
+                                   _ptr(table), _ptr(pool), _ptr(out), P, B, _ptr(workspace), ws_bytes, _ptr(dev_status),
+                                   _stream(stream))
+    _check(st, "lnk_latent_step_attn")
+
+
+def lnk_latent_copy_pages(desc, pools, src_pages, dst_pages, n, dev_status=None, stream=None):
+    """Page copies in every layer's latent pool: pools is a sequence of them."""
+    a = _addresses(pools)
+    st = _lib.lnk_latent_copy_pages(ctypes.byref(desc), a.buffer_info()[0], len(a), _ptr(src_pages), _ptr(dst_pages), n,
+                                    _ptr(dev_status), _stream(stream))
+    _check(st, "lnk_latent_copy_pages")
 
 
 def lnk_selftest_wait_timeout(dev_status, limit_ns, stream=None):

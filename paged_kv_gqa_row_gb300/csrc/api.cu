@@ -10,6 +10,7 @@
 #include <tuple>
 
 #include "common.cuh"
+#include "latent.cuh"
 
 namespace lnk {
 
@@ -219,6 +220,25 @@ static lnk_status inv_freq_table(const lnk_rope_desc* rope, int head_dim, float*
   }
   return LNK_OK;
 }
+
+bool bf16_tensor_map(CUtensorMap* map, const void* base, int rank, const long long* dims, const long long* strides,
+                     const int* box) {
+  EncodeTiledFn enc = encode_fn();
+  if (enc == nullptr) return false;
+  cuuint64_t d[3], s[2];
+  cuuint32_t b[3];
+  const cuuint32_t ones[3] = {1, 1, 1};
+  for (int i = 0; i < rank; ++i) {
+    d[i] = static_cast<cuuint64_t>(dims[i]);
+    b[i] = static_cast<cuuint32_t>(box[i]);
+    if (i > 0) s[i - 1] = static_cast<cuuint64_t>(strides[i]) * 2;
+  }
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank), const_cast<void*>(base), d, s, b, ones,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+lnk_status rope_frequencies(const lnk_rope_desc* rope, int dim, float* out) { return inv_freq_table(rope, dim, out); }
 
 }  // namespace lnk
 

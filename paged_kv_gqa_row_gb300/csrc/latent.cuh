@@ -1,0 +1,74 @@
+// Parameter blocks and launchers of the latent-cache kernels.
+#pragma once
+
+#include "common.cuh"
+
+namespace lnk {
+
+constexpr int kLatentRows = 64;  // query rows of an attention tile at most
+
+// A row of a tile (a unit of the stream of pages) that the teams' shares cut: what
+// the joining kernel needs to know, written by the team whose share starts inside it.
+struct LatentCut {
+  int32_t t0, nt;     // the unit's first token and its tokens
+  int32_t j0;         // pages of the unit before the share (0: the share starts with a unit)
+  int32_t np;         // pages of the unit
+  long long per;      // pages of a share
+  long long pad;
+};
+
+struct LatentParams {
+  const uint16_t* q;               // [T][H][C + R]
+  const uint16_t* pool;            // [num_pages * 64][C + R]
+  const int32_t* rows;             // [P]
+  const int32_t* positions;        // [P]
+  const int32_t* step_positions;   // [T - P]
+  const int32_t* table;
+  uint16_t* out;                   // [T][H][C]
+  int32_t* status;
+  LatentCut* cuts;                 // [teams]
+  float* ml;                       // [2 * CTAs][kLatentRows][2]: reference (log2 units), sum
+  float* o;                        // [2 * CTAs][kLatentRows][C]: unnormalised partial outputs
+  int P, T, heads, latent_dim, rope_dim, num_pages, num_rows, pages_per_row, window;
+  int tile_rows;                   // query rows a tile (64, 32 or 16)
+  int tile_tokens;                 // prompt tokens a tile at most
+  int head_blocks;                 // tiles a token (heads > tile_rows)
+  int teams;                       // groups of head_blocks CTAs that share the stream
+  int min_pages;                   // of a share
+  float scale_log2;
+};
+
+cudaError_t launch_latent_attn(const CUtensorMap& qmap, const CUtensorMap& pmap, const LatentParams& p,
+                               cudaStream_t stream);
+
+struct LatentAppendParams {
+  const uint16_t* q;        // [T][H] rotated parts, q_stride elements from head to head
+  const uint16_t* kv;       // [T][C + R]
+  const int32_t* positions;
+  const int32_t* rows;
+  const int32_t* slots;
+  const int32_t* table;
+  const uint16_t* norm_w;   // [C] or null
+  uint16_t* pool;
+  uint16_t* q_out;
+  uint16_t* kv_out;         // or null
+  int32_t* status;
+  double norm_eps;
+  long long q_stride, q_out_stride;
+  int T, heads, latent_dim, rope_dim, num_pages, num_rows, pages_per_row;
+  float inv_freq[32];
+};
+
+cudaError_t launch_latent_append(const LatentAppendParams& p, cudaStream_t stream);
+
+lnk_status check_latent_desc(const lnk_latent_desc* desc);
+
+// A tensor map over bf16 data of 2 or 3 dimensions (sizes and, from the second on,
+// strides in elements), boxes of `box` elements, 128-byte swizzle.
+bool bf16_tensor_map(CUtensorMap* map, const void* base, int rank, const long long* dims, const long long* strides,
+                     const int* box);
+
+// The float32 frequencies of a rotation of `dim` elements (lnk_rope_inv_freq).
+lnk_status rope_frequencies(const lnk_rope_desc* rope, int dim, float* out);
+
+}  // namespace lnk

@@ -1,0 +1,190 @@
+// C entry points of the latent cache: argument checks and launches.
+#include <algorithm>
+#include <cfloat>
+#include <cstring>
+
+#include "latent.cuh"
+
+namespace lnk {
+namespace {
+
+constexpr int kMaxLatentHeads = 1024;
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+float latent_scale_log2(const lnk_latent_desc* d) {
+  return static_cast<float>(static_cast<double>(d->scale) * 1.4426950408889634);  // log2(e)
+}
+
+lnk_status check_desc(const lnk_latent_desc* d) {
+  if (d == nullptr) return LNK_EINVAL;
+  if (d->page_size != kPage) return LNK_EUNSUPPORTED;
+  if (d->latent_dim != 128 && d->latent_dim != 256 && d->latent_dim != 384 && d->latent_dim != 512)
+    return LNK_EUNSUPPORTED;
+  if (d->rope_dim != 32 && d->rope_dim != 64) return LNK_EUNSUPPORTED;
+  if (d->num_heads <= 0) return LNK_EINVAL;
+  if (d->num_heads > kMaxLatentHeads) return LNK_ERANGE;
+  if (d->num_pages <= 0 || d->num_rows <= 0 || d->pages_per_row <= 0) return LNK_EINVAL;
+  if (d->window < 0 || !(d->scale > 0.f)) return LNK_EINVAL;
+  // (a zero or infinite factor would make NaN of masked scores and of zero ones)
+  if (!(latent_scale_log2(d) > 0.f && latent_scale_log2(d) <= FLT_MAX)) return LNK_ERANGE;
+  // TMA row coordinates and 32-bit position arithmetic must not overflow
+  if (static_cast<long long>(d->num_pages) * kPage >= (1ll << 31)) return LNK_ERANGE;
+  if (static_cast<long long>(d->pages_per_row) * kPage >= (1ll << 31)) return LNK_ERANGE;
+  if (static_cast<long long>(d->num_rows) * d->pages_per_row >= (1ll << 31)) return LNK_ERANGE;
+  return LNK_OK;
+}
+
+struct Workspace {
+  size_t cuts, ml, o, total;
+};
+
+// The partial sums of two cut units a CTA, each of kLatentRows rows at most.
+Workspace workspace_layout(int ctas, int latent_dim) {
+  auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+  Workspace w;
+  w.cuts = 0;
+  w.ml = up(sizeof(LatentCut) * static_cast<size_t>(ctas));
+  w.o = w.ml + up(sizeof(float) * 2 * 2 * static_cast<size_t>(ctas) * kLatentRows);
+  w.total = w.o + sizeof(float) * 2 * static_cast<size_t>(ctas) * kLatentRows * static_cast<size_t>(latent_dim);
+  return w;
+}
+
+lnk_status attend(const lnk_latent_desc* desc, const lnk_bf16* q, const int32_t* rows, const int32_t* positions,
+                  const int32_t* step_positions, const int32_t* table, const lnk_bf16* pool, lnk_bf16* out, int32_t P,
+                  int32_t B, void* workspace, size_t ws_bytes, int32_t* dev_status, lnk_stream stream) {
+  const lnk_status st = check_desc(desc);
+  if (st != LNK_OK) return st;
+  if (P < 0 || B < 0 || B > desc->num_rows) return LNK_EINVAL;
+  if (B > kMaxDecodeRows) return LNK_ERANGE;
+  if ((static_cast<long long>(P) + B) * desc->num_heads >= (1ll << 31)) return LNK_ERANGE;
+  if (P == 0 && B == 0) return LNK_OK;
+  if (!q || !table || !pool || !out) return LNK_EINVAL;
+  if (P > 0 && (!rows || !positions)) return LNK_EINVAL;
+  if (B > 0 && !step_positions) return LNK_EINVAL;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(pool, 16)) return LNK_EINVAL;
+  const int sms = device_sm_count();
+  if (sms <= 0) return LNK_ECUDA;
+  const Workspace w = workspace_layout(sms, desc->latent_dim);
+  if (workspace == nullptr || ws_bytes < w.total || !aligned(workspace, 256)) return LNK_EWORKSPACE;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+
+  LatentParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.q = q;
+  p.pool = pool;
+  p.rows = rows;
+  p.positions = positions;
+  p.step_positions = step_positions;
+  p.table = table;
+  p.out = out;
+  p.status = dev_status;
+  p.cuts = reinterpret_cast<LatentCut*>(ws + w.cuts);
+  p.ml = reinterpret_cast<float*>(ws + w.ml);
+  p.o = reinterpret_cast<float*>(ws + w.o);
+  p.P = P;
+  p.T = P + B;
+  p.heads = desc->num_heads;
+  p.latent_dim = desc->latent_dim;
+  p.rope_dim = desc->rope_dim;
+  p.num_pages = desc->num_pages;
+  p.num_rows = desc->num_rows;
+  p.pages_per_row = desc->pages_per_row;
+  p.window = desc->window;
+  p.tile_rows = kLatentRows;
+  p.tile_tokens = std::max(1, p.tile_rows / p.heads);
+  p.head_blocks = (p.heads + p.tile_rows - 1) / p.tile_rows;
+  if (p.head_blocks > sms) return LNK_ERANGE;
+  p.teams = sms / p.head_blocks;
+  p.min_pages = 2;
+  p.scale_log2 = latent_scale_log2(desc);
+
+  const long long width = desc->latent_dim + desc->rope_dim;
+  const long long qdims[2] = {width, static_cast<long long>(p.T) * p.heads};
+  const long long pdims[2] = {width, static_cast<long long>(p.num_pages) * kPage};
+  const long long strides[2] = {1, width};
+  const int qbox[2] = {kBoxCols, p.tile_rows}, pbox[2] = {kBoxCols, kPage};
+  CUtensorMap qmap, pmap;
+  if (!bf16_tensor_map(&qmap, q, 2, qdims, strides, qbox) || !bf16_tensor_map(&pmap, pool, 2, pdims, strides, pbox))
+    return LNK_ECUDA;
+  return launch_latent_attn(qmap, pmap, p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? LNK_OK : LNK_ECUDA;
+}
+
+}  // namespace
+
+lnk_status check_latent_desc(const lnk_latent_desc* desc) { return check_desc(desc); }
+
+}  // namespace lnk
+
+using namespace lnk;
+
+extern "C" {
+
+size_t lnk_latent_workspace_size(const lnk_latent_desc* desc) {
+  if (check_desc(desc) != LNK_OK) return 0;
+  const int sms = device_sm_count();
+  return sms > 0 ? workspace_layout(sms, desc->latent_dim).total : 0;
+}
+
+lnk_status lnk_latent_append(const lnk_latent_desc* desc, const lnk_rope_desc* rope, const lnk_bf16* q,
+                             int64_t q_stride, const lnk_bf16* kv, const int32_t* positions, const int32_t* rows,
+                             const int32_t* slots, const int32_t* table, const lnk_bf16* norm_w, float norm_eps,
+                             lnk_bf16* pool, lnk_bf16* q_out, int64_t q_out_stride, lnk_bf16* kv_out, int32_t T,
+                             int32_t* dev_status, lnk_stream stream) {
+  lnk_status st = check_desc(desc);
+  if (st != LNK_OK) return st;
+  if (T < 0) return LNK_EINVAL;
+  if (T == 0) return LNK_OK;
+  if (!q || !kv || !positions || !pool || !q_out || (!slots && !table)) return LNK_EINVAL;
+  if (!aligned(q, 4) || !aligned(q_out, 4) || !aligned(kv, 16) || !aligned(pool, 16) || !aligned(kv_out, 16) ||
+      !aligned(norm_w, 16))
+    return LNK_EINVAL;
+  if (q_stride < desc->rope_dim || q_out_stride < desc->rope_dim || q_stride % 2 != 0 || q_out_stride % 2 != 0)
+    return LNK_EINVAL;
+  // (byte offsets of the last token must stay within 63 bits)
+  if (q_stride > (1ll << 30) || q_out_stride > (1ll << 30)) return LNK_ERANGE;
+  if (norm_w && !(norm_eps >= 0.f)) return LNK_EINVAL;
+  if (rows == nullptr && slots == nullptr && T > desc->num_rows) return LNK_EINVAL;
+  LatentAppendParams p;
+  std::memset(&p, 0, sizeof(p));
+  st = rope_frequencies(rope, desc->rope_dim, p.inv_freq);
+  if (st != LNK_OK) return st;
+  p.q = q;
+  p.kv = kv;
+  p.positions = positions;
+  p.rows = rows;
+  p.slots = slots;
+  p.table = table;
+  p.norm_w = norm_w;
+  p.pool = pool;
+  p.q_out = q_out;
+  p.kv_out = kv_out;
+  p.status = dev_status;
+  p.norm_eps = static_cast<double>(norm_eps);
+  p.q_stride = q_stride;
+  p.q_out_stride = q_out_stride;
+  p.T = T;
+  p.heads = desc->num_heads;
+  p.latent_dim = desc->latent_dim;
+  p.rope_dim = desc->rope_dim;
+  p.num_pages = desc->num_pages;
+  p.num_rows = desc->num_rows;
+  p.pages_per_row = desc->pages_per_row;
+  return launch_latent_append(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? LNK_OK : LNK_ECUDA;
+}
+
+lnk_status lnk_latent_decode_attn(const lnk_latent_desc* desc, const lnk_bf16* q, const int32_t* positions,
+                                  const int32_t* table, const lnk_bf16* pool, lnk_bf16* out, int32_t B, void* workspace,
+                                  size_t ws_bytes, int32_t* dev_status, lnk_stream stream) {
+  return attend(desc, q, nullptr, nullptr, positions, table, pool, out, 0, B, workspace, ws_bytes, dev_status, stream);
+}
+
+lnk_status lnk_latent_step_attn(const lnk_latent_desc* desc, const lnk_bf16* q, const int32_t* rows,
+                                const int32_t* positions, const int32_t* step_positions, const int32_t* table,
+                                const lnk_bf16* pool, lnk_bf16* out, int32_t P, int32_t B, void* workspace,
+                                size_t ws_bytes, int32_t* dev_status, lnk_stream stream) {
+  return attend(desc, q, rows, positions, step_positions, table, pool, out, P, B, workspace, ws_bytes, dev_status,
+                stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,733 @@
+// Attention over a paged latent cache, absorbed form: every query head scores the
+// whole row [c, k] of a token and sums the c,
+//     s_hj = scale q_h . [c_j, k_j],   o_h = sum_j softmax(s_h)_j c_j.
+// All heads (and all tokens of a prompt piece) share the keys, so a tile takes up to
+// N = 64 query rows of consecutive (token, head) pairs that see one table row, and
+// streams the row's pages (64 keys) once for all of them.
+//
+// The products are turned over, so that the accumulators' size follows the number of
+// query rows (C = 512 values of 64 rows are half of the tensor memory; with the rows
+// on the tensor-memory lanes 128 rows would fill all of it and leave no scores):
+//   S^T[64 keys x N]  = K Q^T    K: the page, K-major; Q: the rows, K-major;
+//   O^T[C x N]       += V^T P^T  V: the same page, read MN-major, 128 numbers of c a
+//                                product; P^T: bf16, one row of N a key.
+// A page therefore lies in shared memory once, as keys and as values.
+//
+// One persistent CTA an SM.  The pages of all tiles, laid end to end, are one stream
+// that the CTAs cut into equal shares (heads beyond 64: teams of CTAs, one for 64 heads
+// each, take the same share, so that the pages come from HBM once); a tile that is cut
+// leaves unnormalised sums in the workspace, which a second kernel joins.
+//
+// Softmax: P = 2^(s scale log2(e) - ref) with a reference a row that is the maximum of
+// the first page it sees and is raised only when a score exceeds it by 2^16: P is
+// rounded to bf16 and summed in float32, whose relative precision does not depend on
+// the reference.  So the usual page needs no maximum across threads, only a vote.
+//
+// Warps: 0 loads (TMA), 1 issues the products, 2-5 do the softmax: warp w holds keys
+// 16 (w % 4) .. + 15 of S^T and 32 lanes of each 128 numbers of O^T.
+//
+// A value that is not finite, at a key that some rows of a tile see and others do not,
+// would reach all of them through 0 * NaN.  Key rows that no token of the tile sees are
+// zeroed before they are values; a row whose output is not finite while its sum is
+// computes again from its own keys (attend_column).
+#include "latent.cuh"
+#include "ptx.cuh"
+
+namespace lnk {
+namespace {
+
+constexpr int kThreads = 192;
+constexpr float kRaiseLog2 = 16.f;
+constexpr int kSoftBar = 1;  // named barrier of the softmax warps
+
+template <int NB, int N>
+struct LatentSmem {
+  static constexpr int kChunks = 2 * NB + 1;                 // 64 numbers of a row each; the last: the rotated ones
+  static constexpr int kStage = kChunks * kBoxBytes;         // a page
+  static constexpr int kQ = kChunks * N * 128;
+  static constexpr int kP = kPage * 128;
+  static constexpr int kMisc = 2048;
+  static constexpr int kBudget = 232448 - 1024 - kMisc - kQ - kP;
+  static constexpr int kStages = kBudget / kStage < 4 ? kBudget / kStage : 4;
+  static constexpr int kGroups = NB + 1;                     // parts of a stage that are freed on their own
+  static constexpr size_t stage = 0;
+  static constexpr size_t q = size_t(kStages) * kStage;
+  static constexpr size_t p = q + kQ;
+  static constexpr size_t bars = p + kP;
+  // full[S][groups], empty[S][groups], sfull[2], pfull, pvdone, qfull, qempty, fin
+  static constexpr int kNumBars = 2 * kStages * kGroups + 7;
+  static constexpr size_t lo = bars + 8 * kNumBars;
+  static constexpr size_t hi = lo + 4 * kLatentRows;
+  static constexpr size_t alpha = hi + 4 * kLatentRows;      // factors of a raise; at the end 1 / sum
+  static constexpr size_t ref = alpha + 4 * kLatentRows;
+  static constexpr size_t misc = ref + 4 * kLatentRows;      // abort, tensor memory, share
+  static constexpr size_t end = misc + 256;
+  static_assert(end - bars <= kMisc, "barriers and row data");
+  static_assert(kStages >= 2, "stages");
+  static constexpr size_t bytes = bars + kMisc + 1024;
+  static constexpr uint32_t kColS = NB * N;                  // after O^T
+  static constexpr uint32_t kCols = NB * N + 2 * N <= 64 ? 64 : NB * N + 2 * N <= 128 ? 128
+                                  : NB * N + 2 * N <= 256 ? 256 : 512;
+};
+
+struct Share {
+  int t, j;           // first unit (its first token) and page in it
+  int left_hi, left_lo;
+};
+
+struct Unit {
+  int nt, row;        // tokens; table row (-1: nothing to see)
+  int kmin, kmax;     // keys that some token sees
+  int in_lo, in_hi;   // keys that every token sees
+  int first, np;      // first page; pages (one at least)
+};
+
+__device__ __forceinline__ int token_keys(const LatentParams& p, int t, int& row, int& lo, int& hi) {
+  int pos;
+  if (t < p.P) {
+    row = p.rows[t];
+    pos = p.positions[t];
+  } else {
+    row = t - p.P;
+    pos = p.step_positions[t - p.P];
+  }
+  lo = hi = 0;
+  if (pos < 0) return 0;
+  if (row < 0 || row >= p.num_rows) return LNK_DEV_BAD_ROW;
+  if (pos >= p.pages_per_row * kPage) return LNK_DEV_BAD_POSITION;
+  lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
+  hi = pos + 1;
+  return 0;
+}
+
+__device__ __forceinline__ bool unit_starts(const LatentParams& p, int t) {
+  return t >= p.P || p.tile_tokens == 1 || t % p.tile_tokens == 0 || p.rows[t] != p.rows[t - 1];
+}
+
+__device__ __forceinline__ Unit unit_at(const LatentParams& p, int t) {
+  Unit u;
+  u.nt = 0;
+  u.row = -1;
+  u.kmin = 0x7fffffff;
+  u.kmax = 0;
+  u.in_lo = 0;
+  u.in_hi = 0x7fffffff;
+  const int end = t < p.P ? min(p.P, (t / p.tile_tokens + 1) * p.tile_tokens) : t + 1;
+  int row0 = 0;
+  for (int s = t; s < end; ++s) {
+    int row, lo, hi;
+    token_keys(p, s, row, lo, hi);
+    if (s == t) row0 = row;
+    else if (row != row0) break;
+    ++u.nt;
+    u.in_lo = max(u.in_lo, lo);
+    u.in_hi = min(u.in_hi, hi);
+    if (hi > lo) {
+      u.row = row;
+      u.kmin = min(u.kmin, lo);
+      u.kmax = max(u.kmax, hi);
+    }
+  }
+  if (u.row < 0) u.kmin = 0;
+  u.first = u.kmin / kPage;
+  u.np = u.row < 0 ? 1 : (u.kmax - 1) / kPage - u.first + 1;
+  return u;
+}
+
+__device__ __forceinline__ float bf16_at(const uint16_t* x) {
+  return __uint_as_float(static_cast<uint32_t>(*x) << 16);
+}
+
+// One row's sums over its own visible keys [lo, hi), relative to the reference that the
+// tile's softmax used, key by key: element 128 mb + d of the row in acc[mb].  The whole warp.
+template <int NB>
+__device__ __noinline__ void attend_column(const LatentParams& p, const uint16_t* q, const int32_t* trow, int lo, int hi,
+                                           float nref, int d, float (&acc)[NB]) {
+  const int w = p.latent_dim + p.rope_dim, lane = threadIdx.x & 31;
+#pragma unroll
+  for (int mb = 0; mb < NB; ++mb) acc[mb] = 0.f;
+#pragma unroll 1
+  for (int key = lo; key < hi; ++key) {
+    const int page = trow[key / kPage];
+    if (page < 0 || page >= p.num_pages) continue;
+    const uint16_t* k = p.pool + (static_cast<size_t>(page) * kPage + key % kPage) * w;
+    float s = 0.f;
+#pragma unroll 1
+    for (int e = lane; e < w; e += 32) s = fmaf(bf16_at(q + e), bf16_at(k + e), s);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    const float e = exp2f(fmaf(s, p.scale_log2, nref));
+#pragma unroll
+    for (int mb = 0; mb < NB; ++mb) acc[mb] = fmaf(e, bf16_at(k + mb * 128 + d), acc[mb]);
+  }
+}
+
+template <int NB, int N>
+__global__ void __launch_bounds__(kThreads, 1)
+    latent_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap pmap,
+                  const __grid_constant__ LatentParams p) {
+  using L = LatentSmem<NB, N>;
+  constexpr int kStages = L::kStages, kGroups = L::kGroups;
+  constexpr int C = NB * 128;
+  constexpr int NX = N / 2;  // scores a softmax thread holds: N / 4 columns of two keys
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::bars);
+  const uint32_t full = smem_addr(bars);                     // [stage][group]
+  const uint32_t empty = full + 8 * kStages * kGroups;
+  const uint32_t sfull = empty + 8 * kStages * kGroups;      // [2]
+  const uint32_t pfull = sfull + 16, pvdone = pfull + 8, qfull = pvdone + 8, qempty = qfull + 8, fin = qempty + 8;
+  int* row_lo = reinterpret_cast<int*>(smem + L::lo);
+  int* row_hi = reinterpret_cast<int*>(smem + L::hi);
+  float* s_alpha = reinterpret_cast<float*>(smem + L::alpha);
+  float* s_ref = reinterpret_cast<float*>(smem + L::ref);
+  int* misc = reinterpret_cast<int*>(smem + L::misc);
+  volatile int* abort_flag = misc;
+  long long* scan = reinterpret_cast<long long*>(misc + 4);  // [7]: sums of the warps before, and the total
+  Share* share = reinterpret_cast<Share*>(misc + 20);
+
+  // the joining kernel may start: it waits for this grid's end
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int team = blockIdx.x / p.head_blocks, hb = blockIdx.x % p.head_blocks;
+
+  if (tid == 0) {
+    for (int i = 0; i < L::kNumBars; ++i) mbar_init(full + 8 * i, i == 2 * kStages * kGroups + 2 ? 4 : 1);
+    *abort_flag = 0;
+    share->t = 0;
+    share->j = 0;
+    share->left_hi = share->left_lo = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == 1) tmem_alloc(smem_addr(misc + 1), L::kCols);
+
+  // ---- this team's share of the stream: the units' pages counted by all threads, each
+  // thread a range of tokens (positions, rows and the table are read before the wait
+  // for the kernel before this one) ----
+  const int T = p.T;
+  const int span = (T + kThreads - 1) / kThreads;
+  const int ta = min(T, tid * span), tb = min(T, ta + span);
+  int bad = 0;
+  long long mine = 0;
+  for (int t = ta; t < tb; ++t) {
+    int row, lo, hi;
+    bad |= token_keys(p, t, row, lo, hi);
+    if (unit_starts(p, t)) mine += unit_at(p, t).np;
+  }
+  long long before = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += x;
+  }
+  if (lane == 31) scan[warp] = before;
+  __syncthreads();
+  long long total = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += scan[w];
+    total += scan[w];
+  }
+  before -= mine;
+  const long long per = max(static_cast<long long>(p.min_pages), (total + p.teams - 1) / p.teams);
+  const long long start = team * per;
+  if (start >= before && start < before + mine) {
+    long long at = before;
+    for (int t = ta; t < tb; ++t) {
+      if (!unit_starts(p, t)) continue;
+      const int np = unit_at(p, t).np;
+      if (start < at + np) {
+        const long long left = min(per, total - start);
+        share->t = t;
+        share->j = static_cast<int>(start - at);
+        share->left_hi = static_cast<int>(left >> 32);
+        share->left_lo = static_cast<int>(left);
+        break;
+      }
+      at += np;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = static_cast<uint32_t>(misc[1]);
+  int t = share->t, j0 = share->j;
+  long long left = (static_cast<long long>(share->left_hi) << 32) | static_cast<uint32_t>(share->left_lo);
+
+  // what the kernel before this one on the stream writes is touched from here on
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (bad && blockIdx.x == 0 && p.status != nullptr) atomicOr(p.status, bad);
+  if (tid == 0 && hb == 0) {
+    LatentCut cut;
+    cut.t0 = t;
+    cut.nt = cut.np = 0;
+    cut.j0 = left > 0 ? j0 : 0;
+    cut.per = per;
+    cut.pad = 0;
+    if (cut.j0 > 0) {
+      const Unit u = unit_at(p, t);
+      cut.nt = u.nt;
+      cut.np = u.np;
+    }
+    p.cuts[team] = cut;
+  }
+  // the tile's query rows: from row `t * heads + hb * N` of q on, as many as the unit has
+  if (warp == 0) {
+    // ============================== producer ==============================
+    if (lane == 0) {
+      int g = 0, issued = 0, units = 0;  // pages; parts of pages and query tiles whose copies were issued
+      bool ok = true;
+      for (int u = 0; ok && left > 0; ++u) {
+        const Unit un = unit_at(p, t);
+        const int n = static_cast<int>(min(left, static_cast<long long>(un.np - j0)));
+        const int32_t* trow = p.table + static_cast<long long>(max(un.row, 0)) * p.pages_per_row + un.first + j0;
+        for (int i = 0; ok && i < n; ++i, ++g) {
+          int page = un.row >= 0 ? trow[i] : 0;
+          if (page < 0 || page >= p.num_pages) {
+            if (hb == 0 && p.status != nullptr) atomicOr(p.status, LNK_DEV_BAD_PAGE);
+            page = 0;  // (its keys are masked and its values zeroed)
+          }
+          const int st = g % kStages;
+          const uint32_t dst = smem_addr(smem + L::stage) + st * L::kStage;
+          for (int gr = 0; ok && gr < kGroups; ++gr) {
+            const uint32_t fb = full + 8 * (st * kGroups + gr);
+            if (g >= kStages) ok = mbar_wait(empty + 8 * (st * kGroups + gr), ((g / kStages) - 1) & 1, abort_flag);
+            if (!ok) break;
+            const int c = 2 * gr;
+            mbar_arrive_expect_tx(fb, gr < NB ? 2 * kBoxBytes : kBoxBytes);
+            tma_load_2d(dst + c * kBoxBytes, &pmap, c * kBoxCols, page * kPage, fb);
+            if (gr < NB) tma_load_2d(dst + (c + 1) * kBoxBytes, &pmap, (c + 1) * kBoxCols, page * kPage, fb);
+            ++issued;
+          }
+          if (ok && i == 0) {
+            if (u > 0) ok = mbar_wait(qempty, (u - 1) & 1, abort_flag);
+            if (ok) {
+              mbar_arrive_expect_tx(qfull, L::kQ);
+              const int y = t * p.heads + hb * N;
+              for (int c = 0; c < L::kChunks; ++c)
+                tma_load_2d(smem_addr(smem + L::q) + c * (N * 128), &qmap, c * kBoxCols, y, qfull);
+              ++units;
+            }
+          }
+        }
+        left -= n;
+        t += un.nt;
+        j0 = 0;
+      }
+      // do not leave while a copy may still land in this CTA's memory
+      const int ring = kStages * kGroups;
+      for (int k = max(0, issued - ring); k < issued; ++k) {
+        const int pg = k / kGroups;
+        const uint32_t fb = full + 8 * ((pg % kStages) * kGroups + k % kGroups);
+        const uint64_t t_0 = global_timer_ns();
+        while (!mbar_try_wait(fb, (pg / kStages) & 1) && global_timer_ns() - t_0 < kWaitLimitNs) {
+        }
+      }
+      const uint64_t t_0 = global_timer_ns();
+      while (units > 0 && !mbar_try_wait(qfull, (units - 1) & 1) && global_timer_ns() - t_0 < kWaitLimitNs) {
+      }
+    }
+  } else if (warp == 1) {
+    // =========================== products' issuer ===========================
+    if (lane == 0) {
+      constexpr uint32_t kIdS = umma_idesc_bf16(kPage, N, 0, 0);
+      constexpr uint32_t kIdPV = umma_idesc_bf16(128, N, 1, 1);
+      const uint64_t kdesc = umma_desc_sw128(smem_addr(smem + L::stage), 0, 1024);
+      const uint64_t qdesc = umma_desc_sw128(smem_addr(smem + L::q), 0, 1024);
+      const uint64_t vdesc = umma_desc_sw128(smem_addr(smem + L::stage), kBoxBytes, 1024);
+      const uint64_t pdesc = umma_desc_sw128(smem_addr(smem + L::p), 0, 1024);
+      const int rope_steps = p.rope_dim / 16;
+      bool ok = true;
+      // S^T of page g of the stream
+      auto scores = [&](int g) {
+        const int st = g % kStages;
+        const uint32_t sc = tmem + L::kColS + (g & 1) * N;
+        const uint64_t kd = kdesc + ((st * L::kStage) >> 4);
+#pragma unroll
+        for (int gr = 0; gr < kGroups; ++gr) {
+          if (ok) ok = mbar_wait(full + 8 * (st * kGroups + gr), (g / kStages) & 1, abort_flag);
+          if (!ok) return;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            if (gr == NB && kk >= rope_steps) break;
+            const int c = 2 * gr + (kk >> 2);
+            umma_ss(sc, kd + ((c * kBoxBytes + (kk & 3) * 32) >> 4),
+                    qdesc + ((c * N * 128 + (kk & 3) * 32) >> 4), kIdS, gr > 0 || kk > 0);
+          }
+        }
+        umma_commit(sfull + 8 * (g & 1));
+        umma_commit(empty + 8 * (st * kGroups + NB));
+      };
+      int g = 0;
+      for (int u = 0; ok && left > 0; ++u) {
+        const Unit un = unit_at(p, t);
+        const int n = static_cast<int>(min(left, static_cast<long long>(un.np - j0)));
+        ok = mbar_wait(qfull, u & 1, abort_flag);
+        if (!ok) break;
+        scores(g);
+        if (n == 1) umma_commit(qempty);
+        for (int i = 0; ok && i < n; ++i, ++g) {
+          if (i + 1 < n) {
+            scores(g + 1);
+            if (i + 2 == n) umma_commit(qempty);
+          }
+          if (!ok) break;
+          ok = mbar_wait(pfull, g & 1, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          const int st = g % kStages;
+          const uint64_t vd = vdesc + ((st * L::kStage) >> 4);
+#pragma unroll
+          for (int mb = 0; mb < NB; ++mb) {
+#pragma unroll
+            for (int kk = 0; kk < kPage / 16; ++kk)
+              umma_ss(tmem + mb * N, vd + ((2 * mb * kBoxBytes + kk * 2048) >> 4), pdesc + ((kk * 2048) >> 4), kIdPV,
+                      i > 0 || kk > 0);
+            umma_commit(empty + 8 * (st * kGroups + mb));
+          }
+          umma_commit(pvdone);
+        }
+        left -= n;
+        t += un.nt;
+        j0 = 0;
+      }
+      // no product is in flight when the tensor memory goes
+      umma_commit(fin);
+      mbar_wait(fin, 0, abort_flag);
+    }
+  } else {
+    // ============================== softmax ===============================
+    const int qt = warp & 3;
+    const int sid = tid - 64;                 // 0 .. 127
+    const int ka = qt * 16 + (lane >> 2);     // this thread's keys of a page: ka, ka + 8
+    const int ca = 2 * (lane & 3);            // its columns: 8 i + ca, + 1
+    const uint32_t lanes = static_cast<uint32_t>(qt * 32) << 16;
+    float* scratch = reinterpret_cast<float*>(smem + L::p);  // [4][N], while no P is there
+    const uint64_t scale2 = f32x2(p.scale_log2, p.scale_log2);
+    bool ok = true;
+    int g = 0;
+    while (ok && left > 0) {
+      const Unit un = unit_at(p, t);
+      const int n = static_cast<int>(min(left, static_cast<long long>(un.np - j0)));
+      const int nrows = min(N, un.nt * p.heads - hb * N);
+      const int rowbase = t * p.heads + hb * N;
+      const bool direct = j0 == 0 && n == un.np;
+      named_barrier_sync(kSoftBar, 128);  // (the unit before is done with the rows' data)
+      // keys that each row sees (rows past the unit's: everything, nobody reads them)
+      if (sid < N) {
+        int lo = 0, hi = 0x7fffffff, row;
+        if (sid < nrows) token_keys(p, t + (hb * N + sid) / p.heads, row, lo, hi);
+        row_lo[sid] = lo;
+        row_hi[sid] = hi;
+      }
+      named_barrier_sync(kSoftBar, 128);
+      const int32_t* trow = p.table + static_cast<long long>(max(un.row, 0)) * p.pages_per_row;
+      float nref[N / 4], l[N / 4];  // minus the reference (0 while there is none), this thread's part of the sum
+      uint32_t unset = 0u;          // columns (bit) without a reference that see keys
+#pragma unroll
+      for (int i = 0; i < N / 4; ++i) {
+        nref[i] = l[i] = 0.f;
+        const int col = 8 * (i >> 1) + ca + (i & 1);
+        if (col < nrows && row_hi[col] > row_lo[col]) unset |= 1u << i;
+      }
+      bool force = true;            // some row has no reference yet (the same in every thread)
+      for (int i = 0; i < n; ++i, ++g) {
+        const int lp = un.first + j0 + i, kb = lp * kPage;
+        const int page = un.row >= 0 ? trow[lp] : -1;
+        const bool held = page >= 0 && page < p.num_pages;
+        ok = __all_sync(0xffffffffu, mbar_wait(sfull + 8 * (g & 1), (g >> 1) & 1, abort_flag));
+        tc_fence_after();
+        uint32_t r[NX];
+        if (ok) {
+          tmem_ld_16x256b(tmem + lanes + L::kColS + (g & 1) * N, r);
+          tmem_ld_wait();
+        }
+        if (!(held && kb >= un.in_lo && kb + kPage <= un.in_hi)) {
+#pragma unroll
+          for (int x = 0; x < NX; ++x) {
+            const int col = 8 * (x >> 2) + ca + (x & 1), key = kb + ka + (x & 2 ? 8 : 0);
+            if (!(held && key >= row_lo[col] && key < row_hi[col])) r[x] = 0xFF800000u;
+          }
+        }
+        float a[NX];
+        float mx = -INFINITY;
+        auto exponents = [&]() {
+#pragma unroll
+          for (int x = 0; x < NX; x += 2) {
+            const int i0 = (x >> 2) * 2;
+            f32x2_split(fma_f32x2(f32x2(__uint_as_float(r[x]), __uint_as_float(r[x + 1])), scale2,
+                                  f32x2(nref[i0], nref[i0 + 1])),
+                        a[x], a[x + 1]);
+            mx = fmax3(mx, a[x], a[x + 1]);
+          }
+        };
+        exponents();
+        if (named_barrier_or(kSoftBar, 128, mx > kRaiseLog2 || force || !ok)) {
+          // ---- references: set, or raised to the page's maximum ----
+          if (g > 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait(pvdone, (g - 1) & 1, abort_flag));
+          if (named_barrier_or(kSoftBar, 128, !ok)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int x = 0; x < N / 4; ++x) {
+            const int at = (x >> 1) * 4 + (x & 1);
+            float m = fmaxf(__uint_as_float(r[at]), __uint_as_float(r[at + 2]));
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            if (lane < 4) scratch[qt * N + 8 * (x >> 1) + ca + (x & 1)] = m;
+          }
+          named_barrier_sync(kSoftBar, 128);
+          bool moved = false;
+#pragma unroll
+          for (int x = 0; x < N / 4; ++x) {
+            const int col = 8 * (x >> 1) + ca + (x & 1);
+            float m = fmaxf(fmaxf(scratch[col], scratch[N + col]), fmaxf(scratch[2 * N + col], scratch[3 * N + col]));
+            float f = 1.f;
+            if (m != -INFINITY) {
+              m *= p.scale_log2;
+              if (unset >> x & 1) {
+                nref[x] = -m;
+                unset &= ~(1u << x);
+              } else if (m + nref[x] > kRaiseLog2) {
+                f = exp2f(-nref[x] - m);
+                l[x] *= f;
+                nref[x] = -m;
+                moved = true;
+              }
+            }
+            if (sid < 4) s_alpha[col] = f;
+          }
+          force = __any_sync(0xffffffffu, unset != 0u);
+          moved = __any_sync(0xffffffffu, moved);
+          named_barrier_sync(kSoftBar, 128);
+          if (moved && i > 0) {
+#pragma unroll 1
+            for (int c = 0; c < NB * N; c += 16) {
+              uint32_t v[16];
+              tmem_ld16(tmem + lanes + c, v);
+              tmem_ld_wait();
+#pragma unroll
+              for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * s_alpha[(c + k) % N]);
+              tmem_st16(tmem + lanes + c, v);
+            }
+            tmem_st_wait();
+          }
+          exponents();
+        }
+        // ---- P^T into shared memory, once the product before has read the last one ----
+        if (g > 0) ok = __all_sync(0xffffffffu, mbar_wait(pvdone, (g - 1) & 1, abort_flag));
+        uint8_t* prow = smem + L::p + ka * 128 + (lane & 3) * 4;
+#pragma unroll
+        for (int x = 0; x < NX; x += 4) {
+          const int i0 = x >> 1, chunk = x >> 2;
+          const float e0 = ex2_approx(a[x]), e1 = ex2_approx(a[x + 1]);
+          const float e2 = ex2_approx(a[x + 2]), e3 = ex2_approx(a[x + 3]);
+          l[i0] += e0 + e2;
+          l[i0 + 1] += e1 + e3;
+          const int at = (chunk ^ (ka & 7)) << 4;
+          *reinterpret_cast<uint32_t*>(prow + at) = pack_bf16x2(e0, e1);
+          *reinterpret_cast<uint32_t*>(prow + 8 * 128 + at) = pack_bf16x2(e2, e3);
+        }
+        // ---- value rows that no token of the unit sees may hold anything: zero ----
+        if (!(held && kb >= un.kmin && kb + kPage <= un.kmax)) {
+          uint8_t* v = smem + L::stage + (g % kStages) * L::kStage;
+          const int key = sid & 63;
+          if (!held || kb + key < un.kmin || kb + key >= un.kmax)
+            for (int c = sid >> 6; c < 2 * NB; c += 2)
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                *reinterpret_cast<uint4*>(v + c * kBoxBytes + key * 128 + k * 16) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(pfull);
+      }
+      // ---- the unit's end: sums joined, outputs or partial sums stored ----
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(pvdone, (g - 1) & 1, abort_flag));
+      if (named_barrier_or(kSoftBar, 128, !ok)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+#pragma unroll
+      for (int x = 0; x < N / 4; ++x) {
+        float s = l[x];
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (lane < 4) scratch[qt * N + 8 * (x >> 1) + ca + (x & 1)] = s;
+        if (sid < 4) s_ref[8 * (x >> 1) + ca + (x & 1)] = nref[x];
+      }
+      named_barrier_sync(kSoftBar, 128);
+      const size_t slot = direct ? 0 : (static_cast<size_t>(2 * team + (j0 == 0 ? 1 : 0)) * p.head_blocks + hb) * kLatentRows;
+      if (sid < N) {
+        const float s = (scratch[sid] + scratch[N + sid]) + (scratch[2 * N + sid] + scratch[3 * N + sid]);
+        s_alpha[sid] = direct ? (s > 0.f ? 1.f / s : s) : (s == s ? 1.f : s);
+        if (!direct) {
+          p.ml[(slot + sid) * 2] = s == 0.f ? -INFINITY : -s_ref[sid];
+          p.ml[(slot + sid) * 2 + 1] = s;
+        }
+      }
+      named_barrier_sync(kSoftBar, 128);
+      uint64_t odd = 0ull;  // columns with an element that is not finite
+#pragma unroll 1
+      for (int c = 0; c < NB * N; c += 16) {
+        uint32_t v[16];
+        tmem_ld16(tmem + lanes + c, v);
+        tmem_ld_wait();
+        const int mb = c / N, c0 = c % N, dim = mb * 128 + qt * 32 + lane;
+        if (direct) {
+#pragma unroll
+          for (int k = 0; k < 16; k += 2) {
+            // two rows of one number a lane -> one row of two numbers
+            const float f0 = s_alpha[c0 + k], f1 = s_alpha[c0 + k + 1];
+            const float x0 = f0 == 0.f ? 0.f : __uint_as_float(v[k]) * f0;
+            const float x1 = f1 == 0.f ? 0.f : __uint_as_float(v[k + 1]) * f1;
+            if ((__float_as_uint(x0) & 0x7F800000u) == 0x7F800000u && f0 == f0) odd |= 1ull << (c0 + k);
+            if ((__float_as_uint(x1) & 0x7F800000u) == 0x7F800000u && f1 == f1) odd |= 2ull << (c0 + k);
+            const float other = __shfl_xor_sync(0xffffffffu, lane & 1 ? x0 : x1, 1);
+            const int rr = c0 + k + (lane & 1);
+            if (rr < nrows)
+              *reinterpret_cast<uint32_t*>(p.out + static_cast<size_t>(rowbase + rr) * C + (dim & ~1)) =
+                  lane & 1 ? pack_bf16x2(other, x1) : pack_bf16x2(x0, other);
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            if ((v[k] & 0x7F800000u) == 0x7F800000u && s_alpha[c0 + k] == s_alpha[c0 + k]) odd |= 1ull << (c0 + k);
+            if (c0 + k < nrows) p.o[(slot + c0 + k) * C + dim] = __uint_as_float(v[k]);
+          }
+        }
+      }
+      if (__any_sync(0xffffffffu, odd != 0ull)) {
+        const int w = p.latent_dim + p.rope_dim;
+        const int seg_lo = (un.first + j0) * kPage, seg_hi = (un.first + j0 + n) * kPage;
+#pragma unroll 1
+        for (int rr = 0; rr < nrows; ++rr) {
+          if (!__any_sync(0xffffffffu, odd >> rr & 1)) continue;
+          float acc[NB];
+          attend_column<NB>(p, p.q + static_cast<size_t>(rowbase + rr) * w, trow, max(row_lo[rr], seg_lo),
+                            min(row_hi[rr], seg_hi), s_ref[rr], qt * 32 + lane, acc);
+#pragma unroll
+          for (int mb = 0; mb < NB; ++mb) {
+            const int dim = mb * 128 + qt * 32 + lane;
+            if (direct)
+              p.out[static_cast<size_t>(rowbase + rr) * C + dim] =
+                  static_cast<uint16_t>(pack_bf16x2(acc[mb] * s_alpha[rr], 0.f));
+            else
+              p.o[(slot + rr) * C + dim] = acc[mb];
+          }
+        }
+      }
+      tc_fence_before();
+      left -= n;
+      t += un.nt;
+      j0 = 0;
+    }
+    if (!ok) *abort_flag = 1;
+  }
+  __syncwarp();
+  if (*abort_flag && lane == 0 && p.status != nullptr) atomicOr(p.status, LNK_DEV_TIMEOUT);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, L::kCols);
+}
+
+// Joins the partial sums of the units that the shares cut: block (c, y) takes rows
+// 8 y .. 8 y + 7 of the unit in which share c starts, if c is the first share that
+// starts inside it.  One warp a row.
+constexpr int kJoinRows = 8;
+constexpr int kMaxTeams = 256;
+
+__global__ void __launch_bounds__(32 * kJoinRows) latent_join_kernel(const __grid_constant__ LatentParams p) {
+  __shared__ float s_w[kJoinRows][kMaxTeams];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const LatentCut cut = p.cuts[c];
+  if (cut.j0 == 0 || cut.j0 > cut.per) return;
+  const int r = blockIdx.y * kJoinRows + warp;
+  if (r >= cut.nt * p.heads) return;
+  const int hb = r / p.tile_rows, col = r % p.tile_rows, C = p.latent_dim;
+  const long long p0 = c * cut.per - cut.j0;
+  const int nseg = static_cast<int>((p0 + cut.np - 1) / cut.per) - c + 2;  // shares c - 1 .. the last
+  auto slot = [&](int k) {
+    return (static_cast<size_t>(2 * (c - 1 + k) + (k == 0 ? 1 : 0)) * p.head_blocks + hb) * kLatentRows + col;
+  };
+  float* w = s_w[warp];
+  float m = -INFINITY;
+  for (int k = lane; k < nseg; k += 32) m = fmaxf(m, p.ml[slot(k) * 2]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  float l = 0.f;
+  for (int k = lane; k < nseg; k += 32) {
+    const float mk = p.ml[slot(k) * 2];
+    const float f = mk == -INFINITY && m == -INFINITY ? 0.f : exp2f(mk - m);
+    w[k] = f;
+    const float lk = p.ml[slot(k) * 2 + 1];
+    l += f == 0.f && lk == lk ? 0.f : f * lk;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  __syncwarp();
+  const float inv = l > 0.f ? 1.f / l : l;
+  for (int d = lane * 4; d < C; d += 128) {
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < nseg; ++k) {
+      const float f = w[k];
+      const float4 x = *reinterpret_cast<const float4*>(p.o + slot(k) * C + d);
+      acc.x = fmaf(f, x.x, acc.x);
+      acc.y = fmaf(f, x.y, acc.y);
+      acc.z = fmaf(f, x.z, acc.z);
+      acc.w = fmaf(f, x.w, acc.w);
+    }
+    const size_t row = static_cast<size_t>(cut.t0) * p.heads + r;
+    *reinterpret_cast<uint2*>(p.out + row * C + d) =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  }
+}
+
+template <int NB, int N>
+cudaError_t launch_t(const CUtensorMap& qmap, const CUtensorMap& pmap, const LatentParams& p, cudaStream_t stream) {
+  const int bytes = static_cast<int>(LatentSmem<NB, N>::bytes);
+  cudaError_t err = set_max_dynamic_smem(reinterpret_cast<const void*>(latent_kernel<NB, N>), bytes);
+  if (err != cudaSuccess) return err;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.teams * p.head_blocks));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  err = cudaLaunchKernelEx(&cfg, latent_kernel<NB, N>, qmap, pmap, p);
+  if (err != cudaSuccess) return err;
+  const int rows = p.head_blocks > 1 ? p.heads : p.tile_tokens * p.heads;
+  cfg.gridDim = dim3(static_cast<unsigned>(p.teams), static_cast<unsigned>((rows + kJoinRows - 1) / kJoinRows));
+  cfg.blockDim = dim3(32 * kJoinRows);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, latent_join_kernel, p);
+}
+
+}  // namespace
+
+cudaError_t launch_latent_attn(const CUtensorMap& qmap, const CUtensorMap& pmap, const LatentParams& p,
+                               cudaStream_t stream) {
+  if (p.teams > kMaxTeams) return cudaErrorInvalidValue;
+  switch (p.latent_dim / 128 * 100 + p.tile_rows) {
+    case 164: return launch_t<1, 64>(qmap, pmap, p, stream);
+    case 264: return launch_t<2, 64>(qmap, pmap, p, stream);
+    case 364: return launch_t<3, 64>(qmap, pmap, p, stream);
+    case 464: return launch_t<4, 64>(qmap, pmap, p, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace lnk

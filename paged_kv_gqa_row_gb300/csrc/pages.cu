@@ -10,6 +10,7 @@
 // 160 pages of 8 heads in 32 layers, bf16 pools, D = 128, 2.7 GB read and written:
 // 403 us, 6.6 TB/s; three pages: 8.9 us.
 #include "common.cuh"
+#include "latent.cuh"
 
 namespace lnk {
 namespace {
@@ -24,6 +25,7 @@ struct CopyParams {
   const int32_t* dst;
   int32_t* status;
   int hkv, num_pages, units;  // units: 16-byte units per page of one head
+  size_t head_stride, page_stride;  // 16-byte units from head to head and from page to page
   int first;                  // of the launch's page pairs
 };
 
@@ -37,9 +39,8 @@ __global__ void __launch_bounds__(kThreads) copy_pages_kernel(const __grid_const
   }
   if (s == d) return;
   uint4* pool = reinterpret_cast<uint4*>(p.pool[which]);
-  const size_t head = static_cast<size_t>(h) * p.num_pages;
-  const uint4* from = pool + (head + s) * p.units;
-  uint4* to = pool + (head + d) * p.units;
+  const uint4* from = pool + h * p.head_stride + s * p.page_stride;
+  uint4* to = pool + h * p.head_stride + d * p.page_stride;
   for (int j = threadIdx.x; j < p.units; j += kUnroll * kThreads) {
     uint4 x[kUnroll];
 #pragma unroll
@@ -73,6 +74,8 @@ lnk_status copy_pages(const lnk_attn_desc* desc, lnk_bf16* const* k_pools, lnk_b
   p.hkv = desc->num_kv_heads;
   p.num_pages = desc->num_pages;
   p.units = bytes / 16;
+  p.page_stride = static_cast<size_t>(p.units);
+  p.head_stride = static_cast<size_t>(p.num_pages) * p.units;
   for (int32_t l0 = 0; l0 < layers; l0 += kLayersPerLaunch) {
     const int32_t nl = layers - l0 < kLayersPerLaunch ? layers - l0 : kLayersPerLaunch;
     for (int32_t l = 0; l < nl; ++l) {
@@ -107,4 +110,40 @@ extern "C" lnk_status lnk_paged_copy_pages_layers(const lnk_attn_desc* desc, lnk
   if (desc == nullptr || n < 0 || layers < 0) return LNK_EINVAL;
   if (layers > 0 && n > 0 && (k_pools == nullptr || v_pools == nullptr)) return LNK_EINVAL;
   return lnk::copy_pages(desc, k_pools, v_pools, layers, src_pages, dst_pages, n, dev_status, stream);
+}
+
+// A latent page is split into parts, a CTA each, so that a copy of few pages spreads
+// over the SMs.
+extern "C" lnk_status lnk_latent_copy_pages(const lnk_latent_desc* desc, lnk_bf16* const* pools, int32_t layers,
+                                            const int32_t* src_pages, const int32_t* dst_pages, int32_t n,
+                                            int32_t* dev_status, lnk_stream stream) {
+  using namespace lnk;
+  const lnk_status st = check_latent_desc(desc);
+  if (st != LNK_OK) return st;
+  if (layers < 0 || n < 0) return LNK_EINVAL;
+  if (layers == 0 || n == 0) return LNK_OK;
+  if (pools == nullptr || src_pages == nullptr || dst_pages == nullptr) return LNK_EINVAL;
+  for (int32_t l = 0; l < layers; ++l)
+    if (pools[l] == nullptr || reinterpret_cast<uintptr_t>(pools[l]) % 16 != 0) return LNK_EINVAL;
+  constexpr int kParts = 4;
+  CopyParams p;
+  p.src = src_pages;
+  p.dst = dst_pages;
+  p.status = dev_status;
+  p.hkv = kParts;
+  p.num_pages = desc->num_pages;
+  p.units = kPage * (desc->latent_dim + desc->rope_dim) * 2 / 16 / kParts;
+  p.head_stride = static_cast<size_t>(p.units);
+  p.page_stride = static_cast<size_t>(p.units) * kParts;
+  for (int32_t l0 = 0; l0 < layers; l0 += 2 * kLayersPerLaunch) {
+    const int32_t nl = layers - l0 < 2 * kLayersPerLaunch ? layers - l0 : 2 * kLayersPerLaunch;
+    for (int32_t l = 0; l < nl; ++l) p.pool[l] = reinterpret_cast<uint8_t*>(pools[l0 + l]);
+    for (int32_t i0 = 0; i0 < n; i0 += 65535) {
+      p.first = i0;
+      const dim3 grid(static_cast<unsigned>(kParts * nl), static_cast<unsigned>(n - i0 < 65535 ? n - i0 : 65535));
+      copy_pages_kernel<<<grid, kThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
+      if (cudaGetLastError() != cudaSuccess) return LNK_ECUDA;
+    }
+  }
+  return LNK_OK;
 }
