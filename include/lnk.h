@@ -635,6 +635,37 @@ lnk_status lnk_latent_step_attn(const lnk_latent_desc* desc, const lnk_bf16* q, 
                                 const lnk_bf16* pool, lnk_bf16* out, int32_t P, int32_t B, void* workspace,
                                 size_t ws_bytes, int32_t* dev_status, lnk_stream stream);
 
+/*
+ * lnk_latent_prompt_attn -- expanded attention of packed prompts.
+ *
+ * Prompt n has queries q_starts[n] .. q_starts[n + 1] - 1 and keys k_starts[n] ..
+ * k_starts[n + 1] - 1; its queries are the last of its keys, and a query sees the
+ * prompt's keys up to itself (with as many keys as queries: a prompt from its start;
+ * with more: behind a prefix whose keys the caller expanded too; a query before the
+ * prompt's first key sees none, and its output is zero).
+ *
+ *   num_heads  1 .. 1024; head_dim: D in {64, 128}; rope_dim: R in {32, 64}
+ *   scale    softmax scale, > 0, in float32's range in log2 units
+ *   q        device [Tq][num_heads][D + R]: the rotated part last
+ *   kv       device [Tk][num_heads][2 D]: a head's keys (first parts), then its values
+ *            (the product of the latents with [U_h, V_h])
+ *   k_rope   device: the rotated key part of token t, shared by the heads, at
+ *            k_rope + t * k_rope_stride (elements; a multiple of 8, >= R): lnk_latent_append's
+ *            kv_out + C with stride C + R, say
+ *   q_starts, k_starts  device int32 [N + 1], ascending, within [0, Tq] and [0, Tk].  A
+ *            prompt whose starts are not is skipped (its outputs stay as they were) and
+ *            sets LNK_DEV_SEGMENT; q_starts must ascend from a start that is not negative
+ *            for the prompts behind it to be found
+ *   out      device [Tq][num_heads][D] (queries that no prompt holds: left as they were)
+ *   Tq, Tk, N  may be 0; 2 (Tq / 256 + N) num_heads < 2^31
+ * q, kv, k_rope and out are 16-byte aligned.
+ */
+lnk_status lnk_latent_prompt_attn(int32_t num_heads, int32_t head_dim, int32_t rope_dim, float scale,
+                                  const lnk_bf16* q, const lnk_bf16* kv, const lnk_bf16* k_rope,
+                                  int64_t k_rope_stride, const int32_t* q_starts, const int32_t* k_starts,
+                                  lnk_bf16* out, int32_t Tq, int32_t Tk, int32_t N, int32_t* dev_status,
+                                  lnk_stream stream);
+
 /* lnk_paged_copy_pages_layers for latent pools: `pools` is a host array of `layers`
  * device pointers.  One launch for up to 256 layers and 65535 pairs. */
 lnk_status lnk_latent_copy_pages(const lnk_latent_desc* desc, lnk_bf16* const* pools, int32_t layers,

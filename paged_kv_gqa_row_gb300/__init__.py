@@ -21,6 +21,7 @@ from .binding import (  # noqa: F401
     lnk_latent_append,
     lnk_latent_copy_pages,
     lnk_latent_decode_attn,
+    lnk_latent_prompt_attn,
     lnk_latent_step_attn,
     lnk_latent_workspace_size,
     lnk_paged_append_rope,

@@ -37,7 +37,7 @@ EXPORTED = ["lnk_status_string", "lnk_rope_inv_freq", "lnk_paged_workspace_size"
             "lnk_pager_free_pages", "lnk_pager_refcount", "lnk_paged_copy_pages",
             "lnk_paged_page_bytes", "lnk_paged_read_tokens", "lnk_pager_compact", "lnk_paged_copy_pages_layers",
             "lnk_latent_workspace_size", "lnk_latent_append", "lnk_latent_decode_attn", "lnk_latent_step_attn",
-            "lnk_latent_copy_pages",
+            "lnk_latent_prompt_attn", "lnk_latent_copy_pages",
             "lnk_selftest_wait_timeout"]
 
 
@@ -137,6 +137,9 @@ _lib.lnk_latent_decode_attn.argtypes = [ctypes.POINTER(LatentDesc), c_vp, c_vp, 
 _lib.lnk_latent_step_attn.restype = ctypes.c_int
 _lib.lnk_latent_step_attn.argtypes = [ctypes.POINTER(LatentDesc), c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_i32, c_i32,
                                       c_vp, c_size, c_vp, c_vp]
+_lib.lnk_latent_prompt_attn.restype = ctypes.c_int
+_lib.lnk_latent_prompt_attn.argtypes = [c_i32, c_i32, c_i32, c_f32, c_vp, c_vp, c_vp, c_i64, c_vp, c_vp, c_vp, c_i32, c_i32,
+                                        c_i32, c_vp, c_vp]
 _lib.lnk_latent_copy_pages.restype = ctypes.c_int
 _lib.lnk_latent_copy_pages.argtypes = [ctypes.POINTER(LatentDesc), c_vp, c_i32, c_vp, c_vp, c_i32, c_vp, c_vp]
 _lib.lnk_selftest_wait_timeout.restype = ctypes.c_int
@@ -324,6 +327,14 @@ def lnk_latent_step_attn(desc, q, rows, positions, step_positions, table, pool, 
                                    _ptr(table), _ptr(pool), _ptr(out), P, B, _ptr(workspace), ws_bytes, _ptr(dev_status),
                                    _stream(stream))
     _check(st, "lnk_latent_step_attn")
+
+
+def lnk_latent_prompt_attn(num_heads, head_dim, rope_dim, scale, q, kv, k_rope, k_rope_stride, q_starts, k_starts, out, Tq,
+                           Tk, N, dev_status=None, stream=None):
+    st = _lib.lnk_latent_prompt_attn(num_heads, head_dim, rope_dim, scale, _ptr(q), _ptr(kv), _ptr(k_rope), k_rope_stride,
+                                     _ptr(q_starts), _ptr(k_starts), _ptr(out), Tq, Tk, N, _ptr(dev_status),
+                                     _stream(stream))
+    _check(st, "lnk_latent_prompt_attn")
 
 
 def lnk_latent_copy_pages(desc, pools, src_pages, dst_pages, n, dev_status=None, stream=None):

@@ -61,6 +61,24 @@ struct LatentAppendParams {
 
 cudaError_t launch_latent_append(const LatentAppendParams& p, cudaStream_t stream);
 
+struct LatentPromptParams {
+  const uint16_t* q;         // [Tq][H][D + R]
+  const uint16_t* kv;        // [Tk][H][2 D]
+  const uint16_t* k_rope;    // [Tk], rope_stride elements from token to token
+  const int32_t* q_starts;   // [prompts + 1]
+  const int32_t* k_starts;
+  uint16_t* out;             // [Tq][H][D]
+  int32_t* status;
+  long long rope_stride;
+  int heads, head_dim, rope_dim, Tq, Tk, prompts;
+  int tiles;                 // ids of tiles
+  float scale_log2;
+};
+
+int latent_prompt_tile_rows();
+cudaError_t launch_latent_prompt(const CUtensorMap& qmap, const CUtensorMap& kvmap, const CUtensorMap& rmap,
+                                 const LatentPromptParams& p, cudaStream_t stream);
+
 lnk_status check_latent_desc(const lnk_latent_desc* desc);
 
 // A tensor map over bf16 data of 2 or 3 dimensions (sizes and, from the second on,

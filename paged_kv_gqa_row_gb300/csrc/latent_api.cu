@@ -187,4 +187,56 @@ lnk_status lnk_latent_step_attn(const lnk_latent_desc* desc, const lnk_bf16* q, 
                 stream);
 }
 
+lnk_status lnk_latent_prompt_attn(int32_t num_heads, int32_t head_dim, int32_t rope_dim, float scale, const lnk_bf16* q,
+                                  const lnk_bf16* kv, const lnk_bf16* k_rope, int64_t k_rope_stride,
+                                  const int32_t* q_starts, const int32_t* k_starts, lnk_bf16* out, int32_t Tq, int32_t Tk,
+                                  int32_t N, int32_t* dev_status, lnk_stream stream) {
+  if (num_heads <= 0 || Tq < 0 || Tk < 0 || N < 0 || !(scale > 0.f)) return LNK_EINVAL;
+  if ((head_dim != 64 && head_dim != 128) || (rope_dim != 32 && rope_dim != 64)) return LNK_EUNSUPPORTED;
+  if (num_heads > kMaxLatentHeads) return LNK_ERANGE;
+  const float scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);  // log2(e)
+  if (!(scale_log2 > 0.f && scale_log2 <= FLT_MAX)) return LNK_ERANGE;
+  if (Tq == 0 || N == 0) return LNK_OK;
+  if (!q || !q_starts || !k_starts || !out) return LNK_EINVAL;
+  if (Tk > 0 && (!kv || !k_rope)) return LNK_EINVAL;
+  if (!aligned(q, 16) || !aligned(kv, 16) || !aligned(k_rope, 16) || !aligned(out, 16)) return LNK_EINVAL;
+  if (k_rope_stride < rope_dim || k_rope_stride % 8 != 0) return LNK_EINVAL;
+  if (k_rope_stride > (1ll << 30)) return LNK_ERANGE;
+  if (Tk == 0) {  // no prompt has a key: every query's output is zero (of the queries that a prompt holds)
+    kv = q;
+    k_rope = q;
+  }
+  const int rows = latent_prompt_tile_rows();
+  LatentPromptParams p;
+  p.q = q;
+  p.kv = kv;
+  p.k_rope = k_rope;
+  p.q_starts = q_starts;
+  p.k_starts = k_starts;
+  p.out = out;
+  p.status = dev_status;
+  p.rope_stride = k_rope_stride;
+  p.heads = num_heads;
+  p.head_dim = head_dim;
+  p.rope_dim = rope_dim;
+  p.Tq = Tq;
+  p.Tk = Tk;
+  p.prompts = N;
+  const long long tiles = static_cast<long long>(Tq) / rows + N;
+  if (2 * tiles * num_heads > 0x7fffffffll) return LNK_ERANGE;
+  p.tiles = static_cast<int>(tiles);
+  p.scale_log2 = scale_log2;
+  const long long h = num_heads, tk = std::max(1, Tk);
+  const long long qdims[3] = {head_dim + rope_dim, h, Tq}, qstr[3] = {1, head_dim + rope_dim, h * (head_dim + rope_dim)};
+  const long long kdims[3] = {2 * head_dim, h, tk}, kstr[3] = {1, 2 * head_dim, h * 2 * head_dim};
+  const long long rdims[2] = {rope_dim, tk}, rstr[2] = {1, k_rope_stride};
+  const int qbox[3] = {kBoxCols, 1, rows / 2}, kbox[3] = {kBoxCols, 1, 64}, rbox[2] = {kBoxCols, 64};
+  CUtensorMap qmap, kvmap, rmap;
+  if (!bf16_tensor_map(&qmap, q, 3, qdims, qstr, qbox) || !bf16_tensor_map(&kvmap, kv, 3, kdims, kstr, kbox) ||
+      !bf16_tensor_map(&rmap, k_rope, 2, rdims, rstr, rbox))
+    return LNK_ECUDA;
+  return launch_latent_prompt(qmap, kvmap, rmap, p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? LNK_OK
+                                                                                                          : LNK_ECUDA;
+}
+
 }  // extern "C"

@@ -109,3 +109,20 @@ def test_workspace_on_a_gpu_less_machine():
         pytest.skip("has a GPU")
     assert lnk.lnk_latent_workspace_size(desc()) == 0
     assert decode(desc()) == ECUDA
+
+
+def prompt(heads=4, d=128, r=64, scale=0.1, q=A, kv=A, kr=A, stride=64, qs=A, ks=A, out=A, Tq=10, Tk=10, N=2):
+    return raw("lnk_latent_prompt_attn", heads, d, r, ctypes.c_float(scale), q, kv, kr, ctypes.c_int64(stride), qs, ks, out,
+               Tq, Tk, N, None, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(heads=0), EINVAL), (dict(heads=1025), ERANGE), (dict(d=96), EUNSUPPORTED), (dict(r=48), EUNSUPPORTED),
+    (dict(scale=0.0), EINVAL), (dict(scale=float("nan")), EINVAL), (dict(scale=3e38), ERANGE), (dict(q=None), EINVAL),
+    (dict(kv=None), EINVAL), (dict(kr=None), EINVAL), (dict(qs=None), EINVAL), (dict(ks=None), EINVAL),
+    (dict(out=None), EINVAL), (dict(q=A + 8), EINVAL), (dict(kv=A + 8), EINVAL), (dict(kr=A + 8), EINVAL),
+    (dict(out=A + 8), EINVAL), (dict(stride=56), EINVAL), (dict(stride=68), EINVAL), (dict(stride=1 << 31), ERANGE),
+    (dict(Tq=-1), EINVAL), (dict(Tk=-1), EINVAL), (dict(N=-1), EINVAL), (dict(heads=1024, Tq=2 ** 31 - 1), ERANGE),
+    (dict(Tq=0, q=None, out=None), OK), (dict(N=0, q=None), OK)])
+def test_prompt_refusals(kw, status):
+    assert prompt(**kw) == status
