@@ -225,9 +225,9 @@ bool bf16_tensor_map(CUtensorMap* map, const void* base, int rank, const long lo
                      const int* box) {
   EncodeTiledFn enc = encode_fn();
   if (enc == nullptr) return false;
-  cuuint64_t d[3], s[2];
-  cuuint32_t b[3];
-  const cuuint32_t ones[3] = {1, 1, 1};
+  cuuint64_t d[4], s[3];
+  cuuint32_t b[4];
+  const cuuint32_t ones[4] = {1, 1, 1, 1};
   for (int i = 0; i < rank; ++i) {
     d[i] = static_cast<cuuint64_t>(dims[i]);
     b[i] = static_cast<cuuint32_t>(box[i]);

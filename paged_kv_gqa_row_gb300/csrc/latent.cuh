@@ -38,8 +38,10 @@ struct LatentParams {
   float scale_log2;
 };
 
-cudaError_t launch_latent_attn(const CUtensorMap& qmap, const CUtensorMap& pmap, const LatentParams& p,
-                               cudaStream_t stream);
+// qmap: query rows; pmap: the pool as [8 keys][64 numbers][row of 8][number of 64], boxes of 16
+// keys, or of 8 and without the rotated part where that has 32 numbers; rmap: that part.
+cudaError_t launch_latent_attn(const CUtensorMap& qmap, const CUtensorMap& pmap, const CUtensorMap& rmap,
+                               const LatentParams& p, cudaStream_t stream);
 
 struct LatentAppendParams {
   const uint16_t* q;        // [T][H] rotated parts, q_stride elements from head to head
@@ -81,7 +83,7 @@ cudaError_t launch_latent_prompt(const CUtensorMap& qmap, const CUtensorMap& kvm
 
 lnk_status check_latent_desc(const lnk_latent_desc* desc);
 
-// A tensor map over bf16 data of 2 or 3 dimensions (sizes and, from the second on,
+// A tensor map over bf16 data of 2 to 4 dimensions (sizes and, from the second on,
 // strides in elements), boxes of `box` elements, 128-byte swizzle.
 bool bf16_tensor_map(CUtensorMap* map, const void* base, int rank, const long long* dims, const long long* strides,
                      const int* box);

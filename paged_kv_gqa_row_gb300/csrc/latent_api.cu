@@ -91,7 +91,8 @@ lnk_status attend(const lnk_latent_desc* desc, const lnk_bf16* q, const int32_t*
   p.num_rows = desc->num_rows;
   p.pages_per_row = desc->pages_per_row;
   p.window = desc->window;
-  p.tile_rows = kLatentRows;
+  // decode rows alone never share a tile: no more rows than heads need; prompt tokens fill it
+  p.tile_rows = P > 0 || p.heads > 32 ? 64 : (p.heads > 16 ? 32 : 16);
   p.tile_tokens = std::max(1, p.tile_rows / p.heads);
   p.head_blocks = (p.heads + p.tile_rows - 1) / p.tile_rows;
   if (p.head_blocks > sms) return LNK_ERANGE;
@@ -101,13 +102,21 @@ lnk_status attend(const lnk_latent_desc* desc, const lnk_bf16* q, const int32_t*
 
   const long long width = desc->latent_dim + desc->rope_dim;
   const long long qdims[2] = {width, static_cast<long long>(p.T) * p.heads};
-  const long long pdims[2] = {width, static_cast<long long>(p.num_pages) * kPage};
-  const long long strides[2] = {1, width};
-  const int qbox[2] = {kBoxCols, p.tile_rows}, pbox[2] = {kBoxCols, kPage};
-  CUtensorMap qmap, pmap;
-  if (!bf16_tensor_map(&qmap, q, 2, qdims, strides, qbox) || !bf16_tensor_map(&pmap, pool, 2, pdims, strides, pbox))
+  const long long pdims[4] = {kBoxCols, 8, width / kBoxCols, static_cast<long long>(p.num_pages) * kPage / 8};
+  const long long rdims[2] = {width, static_cast<long long>(p.num_pages) * kPage};
+  const long long strides[2] = {1, width}, pstrides[4] = {1, width, kBoxCols, 8 * width};
+  const int qbox[2] = {kBoxCols, p.tile_rows}, rbox[2] = {kBoxCols, 8};
+  const int pbox[4] = {kBoxCols, 8, static_cast<int>(width / kBoxCols), p.rope_dim == 64 ? 2 : 1};
+  CUtensorMap qmap, pmap, rmap;
+  if (!bf16_tensor_map(&qmap, q, 2, qdims, strides, qbox) || !bf16_tensor_map(&pmap, pool, 4, pdims, pstrides, pbox))
     return LNK_ECUDA;
-  return launch_latent_attn(qmap, pmap, p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? LNK_OK : LNK_ECUDA;
+  if (p.rope_dim == 32) {
+    if (!bf16_tensor_map(&rmap, pool, 2, rdims, strides, rbox)) return LNK_ECUDA;
+  } else {
+    rmap = pmap;  // (not used)
+  }
+  return launch_latent_attn(qmap, pmap, rmap, p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? LNK_OK
+                                                                                                       : LNK_ECUDA;
 }
 
 }  // namespace

@@ -11,17 +11,19 @@
 //   S^T[64 keys x N]  = K Q^T    K: the page, K-major; Q: the rows, K-major;
 //   O^T[C x N]       += V^T P^T  V: the same page, read MN-major, 128 numbers of c a
 //                                product; P^T: bf16, one row of N a key.
-// A page therefore lies in shared memory once, as keys and as values.
+// A page therefore lies in shared memory once, as keys and as values: [8 keys][64 numbers]
+// of 1 KB each, so that what a copy of 16 keys reads is contiguous in the pool.
 //
 // One persistent CTA an SM.  The pages of all tiles, laid end to end, are one stream
 // that the CTAs cut into equal shares (heads beyond 64: teams of CTAs, one for 64 heads
 // each, take the same share, so that the pages come from HBM once); a tile that is cut
 // leaves unnormalised sums in the workspace, which a second kernel joins.
 //
-// Softmax: P = 2^(s scale log2(e) - ref) with a reference a row that is the maximum of
-// the first page it sees and is raised only when a score exceeds it by 2^16: P is
-// rounded to bf16 and summed in float32, whose relative precision does not depend on
-// the reference.  So the usual page needs no maximum across threads, only a vote.
+// Softmax: P = 2^(s scale log2(e) - ref).  P is rounded to bf16 and summed in float32,
+// whose relative precision does not depend on the reference, so that need not be the
+// maximum: it is the score of the row's first key, and is raised (to a page's maximum)
+// only when a score exceeds it by 2^32.  The usual page needs no maximum across threads,
+// only a vote.
 //
 // Warps: 0 loads (TMA), 1 issues the products, 2-5 do the softmax: warp w holds keys
 // 16 (w % 4) .. + 15 of S^T and 32 lanes of each 128 numbers of O^T.
@@ -37,25 +39,28 @@ namespace lnk {
 namespace {
 
 constexpr int kThreads = 192;
-constexpr float kRaiseLog2 = 16.f;
+constexpr float kRaiseLog2 = 32.f;
+constexpr int kAhead = 0;      // pages asked into L2 before they are loaded
 constexpr int kSoftBar = 1;  // named barrier of the softmax warps
 
 template <int NB, int N>
 struct LatentSmem {
   static constexpr int kChunks = 2 * NB + 1;                 // 64 numbers of a row each; the last: the rotated ones
-  static constexpr int kStage = kChunks * kBoxBytes;         // a page
+  static constexpr int kRg = kChunks * 1024;                 // eight keys: [chunk][8 rows of 128 bytes, swizzled]
+  static constexpr int kStage = 8 * kRg;                     // a page
   static constexpr int kQ = kChunks * N * 128;
   static constexpr int kP = kPage * 128;
   static constexpr int kMisc = 2048;
   static constexpr int kBudget = 232448 - 1024 - kMisc - kQ - kP;
   static constexpr int kStages = kBudget / kStage < 4 ? kBudget / kStage : 4;
-  static constexpr int kGroups = NB + 1;                     // parts of a stage that are freed on their own
+  static constexpr int kGroups = kPage / 16;                 // parts of a stage that are loaded and freed on their own
+  static constexpr int kGroup = 2 * kRg;                     // 16 keys
   static constexpr size_t stage = 0;
   static constexpr size_t q = size_t(kStages) * kStage;
   static constexpr size_t p = q + kQ;
   static constexpr size_t bars = p + kP;
-  // full[S][groups], empty[S][groups], sfull[2], pfull, pvdone, qfull, qempty, fin
-  static constexpr int kNumBars = 2 * kStages * kGroups + 7;
+  // full[S], empty[S][groups], sfull[2], pfull, pvdone, qfull, qempty, fin
+  static constexpr int kNumBars = kStages + kStages * kGroups + 7;
   static constexpr size_t lo = bars + 8 * kNumBars;
   static constexpr size_t hi = lo + 4 * kLatentRows;
   static constexpr size_t alpha = hi + 4 * kLatentRows;      // factors of a raise; at the end 1 / sum
@@ -165,16 +170,17 @@ __device__ __noinline__ void attend_column(const LatentParams& p, const uint16_t
 template <int NB, int N>
 __global__ void __launch_bounds__(kThreads, 1)
     latent_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap pmap,
-                  const __grid_constant__ LatentParams p) {
+                  const __grid_constant__ CUtensorMap rmap, const __grid_constant__ LatentParams p) {
   using L = LatentSmem<NB, N>;
   constexpr int kStages = L::kStages, kGroups = L::kGroups;
   constexpr int C = NB * 128;
+  constexpr int kEnd = N < 32 ? N : 32;  // rows of a step of the epilogue
   constexpr int NX = N / 2;  // scores a softmax thread holds: N / 4 columns of two keys
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::bars);
-  const uint32_t full = smem_addr(bars);                     // [stage][group]
-  const uint32_t empty = full + 8 * kStages * kGroups;
+  const uint32_t full = smem_addr(bars);                     // [stage]
+  const uint32_t empty = full + 8 * kStages;                 // [stage][group]
   const uint32_t sfull = empty + 8 * kStages * kGroups;      // [2]
   const uint32_t pfull = sfull + 16, pvdone = pfull + 8, qfull = pvdone + 8, qempty = qfull + 8, fin = qempty + 8;
   int* row_lo = reinterpret_cast<int*>(smem + L::lo);
@@ -189,11 +195,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   // the joining kernel may start: it waits for this grid's end
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int team = blockIdx.x / p.head_blocks, hb = blockIdx.x % p.head_blocks;
 
   if (tid == 0) {
-    for (int i = 0; i < L::kNumBars; ++i) mbar_init(full + 8 * i, i == 2 * kStages * kGroups + 2 ? 4 : 1);
+    for (int i = 0; i < L::kNumBars; ++i) mbar_init(full + 8 * i, 1);
+    for (int i = 0; i < kStages; ++i) mbar_init(full + 8 * i, kGroups);
+    mbar_init(pfull, 4);
     *abort_flag = 0;
     share->t = 0;
     share->j = 0;
@@ -251,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = static_cast<uint32_t>(misc[1]);
+  const uint32_t tmem = __shfl_sync(0xffffffffu, static_cast<uint32_t>(misc[1]), 0);
   int t = share->t, j0 = share->j;
   long long left = (static_cast<long long>(share->left_hi) << 32) | static_cast<uint32_t>(share->left_lo);
 
@@ -278,6 +286,38 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       int g = 0, issued = 0, units = 0;  // pages; parts of pages and query tiles whose copies were issued
       bool ok = true;
+      auto load_q = [&](int t) {
+        mbar_arrive_expect_tx(qfull, L::kQ);
+        for (int c = 0; c < L::kChunks; ++c)
+          tma_load_2d(smem_addr(smem + L::q) + c * (N * 128), &qmap, c * kBoxCols, t * p.heads + hb * N, qfull);
+        ++units;
+      };
+      // Pages are asked into L2 kAhead pages before they are loaded: shared memory holds two
+      // pages, which alone would not cover HBM's latency.
+      int at = t, aj = j0, an = 0, ant = 0, afirst = 0, ahead = 0;
+      long long aleft = left;
+      const int32_t* arow = nullptr;
+      auto prefetch = [&]() {
+        if (aleft <= 0 || hb != 0) return;
+        if (arow == nullptr) {
+          const Unit x = unit_at(p, at);
+          arow = p.table + static_cast<long long>(max(x.row, 0)) * p.pages_per_row + x.first;
+          an = x.row >= 0 ? x.np : 0;
+          ant = x.nt;
+          afirst = x.np;
+        }
+        const int page = aj < an ? arow[aj] : -1;
+        if (page >= 0 && page < p.num_pages)
+          bulk_prefetch_l2(p.pool + static_cast<size_t>(page) * kPage * (p.latent_dim + p.rope_dim),
+                           kPage * (p.latent_dim + p.rope_dim) * 2);
+        --aleft;
+        if (++aj >= afirst) {
+          at += ant;
+          aj = 0;
+          arow = nullptr;
+        }
+      };
+      if (left > 0) load_q(t);
       for (int u = 0; ok && left > 0; ++u) {
         const Unit un = unit_at(p, t);
         const int n = static_cast<int>(min(left, static_cast<long long>(un.np - j0)));
@@ -291,37 +331,36 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int st = g % kStages;
           const uint32_t dst = smem_addr(smem + L::stage) + st * L::kStage;
           for (int gr = 0; ok && gr < kGroups; ++gr) {
-            const uint32_t fb = full + 8 * (st * kGroups + gr);
+            const uint32_t fb = full + 8 * st;
             if (g >= kStages) ok = mbar_wait(empty + 8 * (st * kGroups + gr), ((g / kStages) - 1) & 1, abort_flag);
             if (!ok) break;
-            const int c = 2 * gr;
-            mbar_arrive_expect_tx(fb, gr < NB ? 2 * kBoxBytes : kBoxBytes);
-            tma_load_2d(dst + c * kBoxBytes, &pmap, c * kBoxCols, page * kPage, fb);
-            if (gr < NB) tma_load_2d(dst + (c + 1) * kBoxBytes, &pmap, (c + 1) * kBoxCols, page * kPage, fb);
+            mbar_arrive_expect_tx(fb, L::kGroup);
+            if (p.rope_dim == 64) {
+              tma_load_4d(dst + gr * L::kGroup, &pmap, 0, 0, 0, page * 8 + 2 * gr, fb);
+            } else {
+              for (int k = 2 * gr; k < 2 * gr + 2; ++k) {
+                tma_load_4d(dst + k * L::kRg, &pmap, 0, 0, 0, page * 8 + k, fb);
+                tma_load_2d(dst + k * L::kRg + 2 * NB * 1024, &rmap, C, page * kPage + k * 8, fb);
+              }
+            }
             ++issued;
           }
-          if (ok && i == 0) {
-            if (u > 0) ok = mbar_wait(qempty, (u - 1) & 1, abort_flag);
-            if (ok) {
-              mbar_arrive_expect_tx(qfull, L::kQ);
-              const int y = t * p.heads + hb * N;
-              for (int c = 0; c < L::kChunks; ++c)
-                tma_load_2d(smem_addr(smem + L::q) + c * (N * 128), &qmap, c * kBoxCols, y, qfull);
-              ++units;
-            }
+          for (; ahead < g + 1 + kAhead; ++ahead) prefetch();
+          if (ok && i == 0 && u > 0) {
+            ok = mbar_wait(qempty, (u - 1) & 1, abort_flag);
+            if (ok) load_q(t);
           }
         }
         left -= n;
         t += un.nt;
         j0 = 0;
       }
-      // do not leave while a copy may still land in this CTA's memory
-      const int ring = kStages * kGroups;
-      for (int k = max(0, issued - ring); k < issued; ++k) {
-        const int pg = k / kGroups;
-        const uint32_t fb = full + 8 * ((pg % kStages) * kGroups + k % kGroups);
+      // do not leave while a copy may still land in this CTA's memory (pages whose every part
+      // was asked for; a page that was given up halfway keeps its barrier to the limit)
+      const int asked = (issued + kGroups - 1) / kGroups;
+      for (int k = max(0, asked - kStages); k < asked; ++k) {
         const uint64_t t_0 = global_timer_ns();
-        while (!mbar_try_wait(fb, (pg / kStages) & 1) && global_timer_ns() - t_0 < kWaitLimitNs) {
+        while (!mbar_try_wait(full + 8 * (k % kStages), (k / kStages) & 1) && global_timer_ns() - t_0 < kWaitLimitNs) {
         }
       }
       const uint64_t t_0 = global_timer_ns();
@@ -330,73 +369,102 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     // =========================== products' issuer ===========================
-    if (lane == 0) {
-      constexpr uint32_t kIdS = umma_idesc_bf16(kPage, N, 0, 0);
-      constexpr uint32_t kIdPV = umma_idesc_bf16(128, N, 1, 1);
-      const uint64_t kdesc = umma_desc_sw128(smem_addr(smem + L::stage), 0, 1024);
-      const uint64_t qdesc = umma_desc_sw128(smem_addr(smem + L::q), 0, 1024);
-      const uint64_t vdesc = umma_desc_sw128(smem_addr(smem + L::stage), kBoxBytes, 1024);
-      const uint64_t pdesc = umma_desc_sw128(smem_addr(smem + L::p), 0, 1024);
-      const int rope_steps = p.rope_dim / 16;
-      bool ok = true;
-      // S^T of page g of the stream
-      auto scores = [&](int g) {
-        const int st = g % kStages;
-        const uint32_t sc = tmem + L::kColS + (g & 1) * N;
-        const uint64_t kd = kdesc + ((st * L::kStage) >> 4);
-#pragma unroll
-        for (int gr = 0; gr < kGroups; ++gr) {
-          if (ok) ok = mbar_wait(full + 8 * (st * kGroups + gr), (g / kStages) & 1, abort_flag);
-          if (!ok) return;
-          tc_fence_after();
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            if (gr == NB && kk >= rope_steps) break;
-            const int c = 2 * gr + (kk >> 2);
-            umma_ss(sc, kd + ((c * kBoxBytes + (kk & 3) * 32) >> 4),
-                    qdesc + ((c * N * 128 + (kk & 3) * 32) >> 4), kIdS, gr > 0 || kk > 0);
-          }
-        }
-        umma_commit(sfull + 8 * (g & 1));
-        umma_commit(empty + 8 * (st * kGroups + NB));
-      };
-      int g = 0;
-      for (int u = 0; ok && left > 0; ++u) {
-        const Unit un = unit_at(p, t);
-        const int n = static_cast<int>(min(left, static_cast<long long>(un.np - j0)));
-        ok = mbar_wait(qfull, u & 1, abort_flag);
-        if (!ok) break;
-        scores(g);
-        if (n == 1) umma_commit(qempty);
-        for (int i = 0; ok && i < n; ++i, ++g) {
-          if (i + 1 < n) {
-            scores(g + 1);
-            if (i + 2 == n) umma_commit(qempty);
-          }
-          if (!ok) break;
-          ok = mbar_wait(pfull, g & 1, abort_flag);
-          if (!ok) break;
-          tc_fence_after();
-          const int st = g % kStages;
-          const uint64_t vd = vdesc + ((st * L::kStage) >> 4);
-#pragma unroll
-          for (int mb = 0; mb < NB; ++mb) {
-#pragma unroll
-            for (int kk = 0; kk < kPage / 16; ++kk)
-              umma_ss(tmem + mb * N, vd + ((2 * mb * kBoxBytes + kk * 2048) >> 4), pdesc + ((kk * 2048) >> 4), kIdPV,
-                      i > 0 || kk > 0);
-            umma_commit(empty + 8 * (st * kGroups + mb));
-          }
-          umma_commit(pvdone);
-        }
-        left -= n;
-        t += un.nt;
-        j0 = 0;
-      }
-      // no product is in flight when the tensor memory goes
-      umma_commit(fin);
-      mbar_wait(fin, 0, abort_flag);
+    // The whole warp runs this, on values that are the same in all its threads.  The loops are
+    // not unrolled: a launch starts with cold instruction caches, and 36 products in a row
+    // took 14000 clocks the first time.
+    constexpr uint32_t kIdS = umma_idesc_bf16(kPage, N, 0, 0);
+    constexpr uint32_t kIdPV = umma_idesc_bf16(128, N, 1, 1);
+    const uint64_t kdesc = umma_desc_sw128(smem_addr(smem + L::stage), 0, L::kRg);
+    const uint64_t qdesc = umma_desc_sw128(smem_addr(smem + L::q), 0, 1024);
+    const uint64_t vdesc = umma_desc_sw128(smem_addr(smem + L::stage), 1024, L::kRg);
+    const uint64_t pdesc = umma_desc_sw128(smem_addr(smem + L::p), 0, 1024);
+    const uint32_t k_lo = static_cast<uint32_t>(kdesc), k_hi = static_cast<uint32_t>(kdesc >> 32);
+    const uint32_t q_lo = static_cast<uint32_t>(qdesc), q_hi = static_cast<uint32_t>(qdesc >> 32);
+    const uint32_t v_lo = static_cast<uint32_t>(vdesc), v_hi = static_cast<uint32_t>(vdesc >> 32);
+    const uint32_t p_lo = static_cast<uint32_t>(pdesc), p_hi = static_cast<uint32_t>(pdesc >> 32);
+    auto done = [](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test_wait(bar, parity)) != 0; };
+    // S^T of page s and the value product of page v <= s are issued in whatever order they
+    // become ready: neither waits for the other's data.
+    int s = 0, v = 0, u = 0;           // next score page; next value page; unit of page s
+    int ut = 0, un = 0, ui = 0;        // tokens and pages (of this share) of unit u, page s in it
+    uint32_t first = 0u;               // bit s & 1: page s is its unit's first here
+    bool more = left > 0;              // page s exists
+    if (more) {
+      const Unit x = unit_at(p, t);
+      ut = x.nt;
+      un = static_cast<int>(min(left, static_cast<long long>(x.np - j0)));
     }
+    uint64_t t0 = 0;
+    uint32_t idle = 0;
+    while (more || v < s) {
+      bool did = false;
+      if (v < s && done(pfull, v & 1)) {
+        tc_fence_after();
+        const int st = v % kStages;
+        const uint32_t vd = v_lo + ((st * L::kStage) >> 4);
+        const uint32_t keep = first >> (v & 1) & 1u ? 0u : 1u;
+#pragma unroll 1
+        for (int kk = 0; kk < L::kGroups; ++kk) {
+#pragma unroll
+          for (int mb = 0; mb < NB; ++mb)
+            umma_ss_warp(tmem + mb * N, vd + ((kk * L::kGroup + 2 * mb * 1024) >> 4), v_hi, p_lo + ((kk * 2048) >> 4), p_hi,
+                         kIdPV, kk > 0 ? 1u : keep);
+          umma_commit_warp(empty + 8 * (st * kGroups + kk));
+        }
+        umma_commit_warp(pvdone);
+        ++v;
+        did = true;
+      }
+      // (two score buffers: page s - 2 has been read once its value product was issued)
+      if (more && s <= v + 1 && done(full + 8 * (s % kStages), (s / kStages) & 1) && (ui > 0 || done(qfull, u & 1))) {
+        tc_fence_after();
+        const uint32_t sc = tmem + L::kColS + (s & 1) * N;
+        uint32_t kd = k_lo + (((s % kStages) * L::kStage) >> 4), qd = q_lo;
+#pragma unroll 1
+        for (int c = 0; c < 2 * NB; ++c, kd += 1024 >> 4, qd += (N * 128) >> 4) {
+          umma_ss_warp(sc, kd, k_hi, qd, q_hi, kIdS, c > 0 ? 1u : 0u);
+#pragma unroll
+          for (int kk = 1; kk < 4; ++kk) umma_ss_warp(sc, kd + ((kk * 32) >> 4), k_hi, qd + ((kk * 32) >> 4), q_hi, kIdS, 1u);
+        }
+        umma_ss_warp(sc, kd, k_hi, qd, q_hi, kIdS, 1u);
+        umma_ss_warp(sc, kd + (32 >> 4), k_hi, qd + (32 >> 4), q_hi, kIdS, 1u);
+        if (p.rope_dim == 64) {
+          umma_ss_warp(sc, kd + (64 >> 4), k_hi, qd + (64 >> 4), q_hi, kIdS, 1u);
+          umma_ss_warp(sc, kd + (96 >> 4), k_hi, qd + (96 >> 4), q_hi, kIdS, 1u);
+        }
+        umma_commit_warp(sfull + 8 * (s & 1));
+        first = (first & ~(1u << (s & 1))) | (ui == 0 ? 1u << (s & 1) : 0u);
+        ++s;
+        if (++ui == un) {  // the unit's last scores: its query rows may go
+          umma_commit_warp(qempty);
+          left -= un;
+          t += ut;
+          ui = 0;
+          ++u;
+          more = left > 0;
+          if (more) {
+            const Unit x = unit_at(p, t);
+            ut = x.nt;
+            un = static_cast<int>(min(left, static_cast<long long>(x.np)));
+          }
+        }
+        did = true;
+      }
+      if (did) {
+        idle = 0;
+      } else if ((++idle & 255u) == 0) {
+        if (idle == 256u) t0 = global_timer_ns();
+        const bool late = global_timer_ns() - t0 > kWaitLimitNs || idle >= kWaitLimitIters;
+        if (__any_sync(0xffffffffu, late || *abort_flag != 0)) {
+          *abort_flag = 1;
+          break;
+        }
+      }
+    }
+    // no product is in flight when the tensor memory goes
+    umma_commit_warp(fin);
+    mbar_wait(fin, 0, abort_flag);
+    __syncwarp();
   } else {
     // ============================== softmax ===============================
     const int qt = warp & 3;
@@ -421,6 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (sid < nrows) token_keys(p, t + (hb * N + sid) / p.heads, row, lo, hi);
         row_lo[sid] = lo;
         row_hi[sid] = hi;
+        s_ref[sid] = -INFINITY;  // the score of the row's first key, once it is known
       }
       named_barrier_sync(kSoftBar, 128);
       const int32_t* trow = p.table + static_cast<long long>(max(un.row, 0)) * p.pages_per_row;
@@ -451,6 +520,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!(held && key >= row_lo[col] && key < row_hi[col])) r[x] = 0xFF800000u;
           }
         }
+        if (force) {
+#pragma unroll
+          for (int x = 0; x < NX; ++x) {
+            const int col = 8 * (x >> 2) + ca + (x & 1), key = kb + ka + (x & 2 ? 8 : 0);
+            if (key == max(row_lo[col], kb)) s_ref[col] = fmaxf(s_ref[col], __uint_as_float(r[x]));
+          }
+          named_barrier_sync(kSoftBar, 128);
+#pragma unroll
+          for (int x = 0; x < N / 4; ++x) {
+            const float f = s_ref[8 * (x >> 1) + ca + (x & 1)];
+            if ((unset >> x & 1) && f != -INFINITY) {
+              nref[x] = -f * p.scale_log2;
+              unset &= ~(1u << x);
+            }
+          }
+        }
         float a[NX];
         float mx = -INFINITY;
         auto exponents = [&]() {
@@ -464,8 +549,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         };
         exponents();
-        if (named_barrier_or(kSoftBar, 128, mx > kRaiseLog2 || force || !ok)) {
-          // ---- references: set, or raised to the page's maximum ----
+        if (force) {
+          // a column without a reference that sees a score all the same (its first one is -inf)
+#pragma unroll
+          for (int x = 0; x < NX; ++x)
+            if ((unset >> ((x >> 2) * 2 + (x & 1)) & 1) && a[x] > -INFINITY) mx = INFINITY;
+          force = __any_sync(0xffffffffu, unset != 0u);
+        }
+        if (named_barrier_or(kSoftBar, 128, mx > kRaiseLog2 || !ok)) {
+          // ---- references raised (or set) to the page's maximum ----
           if (g > 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait(pvdone, (g - 1) & 1, abort_flag));
           if (named_barrier_or(kSoftBar, 128, !ok)) {
             ok = false;
@@ -493,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 nref[x] = -m;
                 unset &= ~(1u << x);
               } else if (m + nref[x] > kRaiseLog2) {
-                f = exp2f(-nref[x] - m);
+                f = ex2_approx(-nref[x] - m);
                 l[x] *= f;
                 nref[x] = -m;
                 moved = true;
@@ -540,7 +632,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = sid >> 6; c < 2 * NB; c += 2)
 #pragma unroll
               for (int k = 0; k < 8; ++k)
-                *reinterpret_cast<uint4*>(v + c * kBoxBytes + key * 128 + k * 16) = make_uint4(0u, 0u, 0u, 0u);
+                *reinterpret_cast<uint4*>(v + (key >> 3) * L::kRg + c * 1024 + (key & 7) * 128 + k * 16) =
+                    make_uint4(0u, 0u, 0u, 0u);
         }
         fence_proxy_async_smem();
         tc_fence_before();
@@ -573,42 +666,61 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       named_barrier_sync(kSoftBar, 128);
-      uint64_t odd = 0ull;  // columns with an element that is not finite
+      // a lane holds one number of every row: 64 bytes (or 128) of a row a store
+      uint32_t odd = 0u;  // bits 15 and 31: an element is not finite
 #pragma unroll 1
-      for (int c = 0; c < NB * N; c += 16) {
-        uint32_t v[16];
-        tmem_ld16(tmem + lanes + c, v);
-        tmem_ld_wait();
+      for (int c = 0; c < NB * N; c += kEnd) {
         const int mb = c / N, c0 = c % N, dim = mb * 128 + qt * 32 + lane;
+        if (c0 >= nrows) continue;
+        uint32_t v[kEnd];
+        if constexpr (kEnd == 32) tmem_ld32(tmem + lanes + c, v);
+        else tmem_ld16(tmem + lanes + c, v);
+        tmem_ld_wait();
+        const bool whole = c0 + kEnd <= nrows;
         if (direct) {
+          uint16_t* o = p.out + static_cast<size_t>(rowbase + c0) * C + dim;
 #pragma unroll
-          for (int k = 0; k < 16; k += 2) {
-            // two rows of one number a lane -> one row of two numbers
+          for (int k = 0; k < kEnd; k += 2) {
             const float f0 = s_alpha[c0 + k], f1 = s_alpha[c0 + k + 1];
-            const float x0 = f0 == 0.f ? 0.f : __uint_as_float(v[k]) * f0;
-            const float x1 = f1 == 0.f ? 0.f : __uint_as_float(v[k + 1]) * f1;
-            if ((__float_as_uint(x0) & 0x7F800000u) == 0x7F800000u && f0 == f0) odd |= 1ull << (c0 + k);
-            if ((__float_as_uint(x1) & 0x7F800000u) == 0x7F800000u && f1 == f1) odd |= 2ull << (c0 + k);
-            const float other = __shfl_xor_sync(0xffffffffu, lane & 1 ? x0 : x1, 1);
-            const int rr = c0 + k + (lane & 1);
-            if (rr < nrows)
-              *reinterpret_cast<uint32_t*>(p.out + static_cast<size_t>(rowbase + rr) * C + (dim & ~1)) =
-                  lane & 1 ? pack_bf16x2(other, x1) : pack_bf16x2(x0, other);
+            const uint32_t w = pack_bf16x2(f0 == 0.f ? 0.f : __uint_as_float(v[k]) * f0,
+                                           f1 == 0.f ? 0.f : __uint_as_float(v[k + 1]) * f1);
+            if (whole || c0 + k < nrows) {
+              o[k * C] = static_cast<uint16_t>(w);
+              odd |= (w & 0x7F80u) + 0x0080u;
+            }
+            if (whole || c0 + k + 1 < nrows) {
+              o[(k + 1) * C] = static_cast<uint16_t>(w >> 16);
+              odd |= (w & 0x7F800000u) + 0x00800000u;
+            }
           }
         } else {
+          float* o = p.o + (slot + c0) * C + dim;
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            if ((v[k] & 0x7F800000u) == 0x7F800000u && s_alpha[c0 + k] == s_alpha[c0 + k]) odd |= 1ull << (c0 + k);
-            if (c0 + k < nrows) p.o[(slot + c0 + k) * C + dim] = __uint_as_float(v[k]);
+          for (int k = 0; k < kEnd; ++k) {
+            if (whole || c0 + k < nrows) {
+              o[k * C] = __uint_as_float(v[k]);
+              odd |= ((v[k] >> 16 & 0x7F80u) + 0x0080u) & 0x8000u;
+            }
           }
         }
       }
-      if (__any_sync(0xffffffffu, odd != 0ull)) {
+      if (__any_sync(0xffffffffu, (odd & 0x80008000u) != 0u)) {
         const int w = p.latent_dim + p.rope_dim;
         const int seg_lo = (un.first + j0) * kPage, seg_hi = (un.first + j0 + n) * kPage;
 #pragma unroll 1
         for (int rr = 0; rr < nrows; ++rr) {
-          if (!__any_sync(0xffffffffu, odd >> rr & 1)) continue;
+          if (s_alpha[rr] != s_alpha[rr]) continue;  // (a sum that is NaN is the row's own: all of it is)
+          bool bad = false;
+#pragma unroll 1
+          for (int mb = 0; mb < NB; ++mb) {
+            uint32_t v[16];
+            tmem_ld16(tmem + lanes + mb * N + (rr & ~15), v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              if (k == (rr & 15)) bad |= (__float_as_uint(__uint_as_float(v[k]) * s_alpha[rr]) & 0x7F800000u) == 0x7F800000u;
+          }
+          if (!__any_sync(0xffffffffu, bad)) continue;
           float acc[NB];
           attend_column<NB>(p, p.q + static_cast<size_t>(rowbase + rr) * w, trow, max(row_lo[rr], seg_lo),
                             min(row_hi[rr], seg_hi), s_ref[rr], qt * 32 + lane, acc);
@@ -638,62 +750,142 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_dealloc(tmem, L::kCols);
 }
 
-// Joins the partial sums of the units that the shares cut: block (c, y) takes rows
-// 8 y .. 8 y + 7 of the unit in which share c starts, if c is the first share that
-// starts inside it.  One warp a row.
-constexpr int kJoinRows = 8;
+// Joins the partial sums of the units that the shares cut.  Every block lists the cut
+// units (one for each share that is the first to start inside one) and takes their rows
+// in turn: a warp a row where no unit has more than kFewParts parts, so that all of a
+// batch's rows are under way at once; else the whole block a row, which splits the parts
+// over groups of threads (a long row's parts are as many as the shares).
+constexpr int kJoinThreads = 256;
 constexpr int kMaxTeams = 256;
+constexpr int kFewParts = 4;
+constexpr int kJoinCtasPerSm = 4;
 
-__global__ void __launch_bounds__(32 * kJoinRows) latent_join_kernel(const __grid_constant__ LatentParams p) {
-  __shared__ float s_w[kJoinRows][kMaxTeams];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const LatentCut cut = p.cuts[c];
-  if (cut.j0 == 0 || cut.j0 > cut.per) return;
-  const int r = blockIdx.y * kJoinRows + warp;
-  if (r >= cut.nt * p.heads) return;
-  const int hb = r / p.tile_rows, col = r % p.tile_rows, C = p.latent_dim;
-  const long long p0 = c * cut.per - cut.j0;
-  const int nseg = static_cast<int>((p0 + cut.np - 1) / cut.per) - c + 2;  // shares c - 1 .. the last
-  auto slot = [&](int k) {
-    return (static_cast<size_t>(2 * (c - 1 + k) + (k == 0 ? 1 : 0)) * p.head_blocks + hb) * kLatentRows + col;
-  };
-  float* w = s_w[warp];
+// Weight 2^(m_k - m) of part k, and 1 / sum, from the parts' references and sums; a warp.
+template <class Slot>
+__device__ __forceinline__ float join_weights(const LatentParams& p, int parts, Slot slot, float* w) {
+  const int lane = threadIdx.x & 31;
   float m = -INFINITY;
-  for (int k = lane; k < nseg; k += 32) m = fmaxf(m, p.ml[slot(k) * 2]);
+  for (int k = lane; k < parts; k += 32) m = fmaxf(m, p.ml[slot(k) * 2]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   float l = 0.f;
-  for (int k = lane; k < nseg; k += 32) {
-    const float mk = p.ml[slot(k) * 2];
+  for (int k = lane; k < parts; k += 32) {
+    const float mk = p.ml[slot(k) * 2], lk = p.ml[slot(k) * 2 + 1];
     const float f = mk == -INFINITY && m == -INFINITY ? 0.f : exp2f(mk - m);
     w[k] = f;
-    const float lk = p.ml[slot(k) * 2 + 1];
     l += f == 0.f && lk == lk ? 0.f : f * lk;
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
   __syncwarp();
-  const float inv = l > 0.f ? 1.f / l : l;
-  for (int d = lane * 4; d < C; d += 128) {
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = 0; k < nseg; ++k) {
-      const float f = w[k];
-      const float4 x = *reinterpret_cast<const float4*>(p.o + slot(k) * C + d);
-      acc.x = fmaf(f, x.x, acc.x);
-      acc.y = fmaf(f, x.y, acc.y);
-      acc.z = fmaf(f, x.z, acc.z);
-      acc.w = fmaf(f, x.w, acc.w);
+  return l > 0.f ? 1.f / l : l;
+}
+
+__device__ __forceinline__ void add_part(float4& acc, float f, const float4& x) {
+  acc.x = fmaf(f, x.x, acc.x);
+  acc.y = fmaf(f, x.y, acc.y);
+  acc.z = fmaf(f, x.z, acc.z);
+  acc.w = fmaf(f, x.w, acc.w);
+}
+
+__global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const __grid_constant__ LatentParams p) {
+  __shared__ int s_unit[kMaxTeams], s_end[kMaxTeams];  // share that cuts first; rows up to and with its unit
+  __shared__ int s_rows[kMaxTeams], s_parts[kMaxTeams];
+  __shared__ int s_units, s_most;
+  __shared__ float s_w[kMaxTeams + 8 * kFewParts];
+  __shared__ float s_inv;
+  __shared__ float4 s_acc[kJoinThreads];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, C = p.latent_dim;
+  if (tid < p.teams) {
+    const LatentCut cut = p.cuts[tid];
+    const bool first = cut.j0 > 0 && cut.j0 <= cut.per;
+    // parts: shares tid - 1 .. the one that the unit's last page is in
+    s_rows[tid] = first ? cut.nt * p.heads : 0;
+    s_parts[tid] = first ? static_cast<int>((tid * cut.per - cut.j0 + cut.np - 1) / cut.per) - tid + 2 : 0;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    int n = 0, rows = 0, most = 0;
+    for (int base = 0; base < p.teams; base += 32) {
+      const int c = base + lane, r = c < p.teams ? s_rows[c] : 0;
+      int sum = r;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += x;
+      }
+      const unsigned has = __ballot_sync(0xffffffffu, r > 0);
+      if (r > 0) {
+        const int at = n + __popc(has & ((1u << lane) - 1u));
+        s_unit[at] = c;
+        s_end[at] = rows + sum;
+        most = max(most, s_parts[c]);
+      }
+      n += __popc(has);
+      rows += __shfl_sync(0xffffffffu, sum, 31);
     }
-    const size_t row = static_cast<size_t>(cut.t0) * p.heads + r;
-    *reinterpret_cast<uint2*>(p.out + row * C + d) =
-        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+    if (lane == 0) {
+      s_units = n;
+      s_most = most;
+    }
+  }
+  __syncthreads();
+  if (s_units == 0) return;
+  const int total = s_end[s_units - 1];
+  const bool few = s_most <= kFewParts;
+  const int step = few ? kJoinThreads / 32 : 1;
+  int at = 0;
+  for (int i = blockIdx.x * step + (few ? warp : 0); i < total; i += gridDim.x * step) {
+    while (i >= s_end[at]) ++at;
+    const int c = s_unit[at], r = i - (s_end[at] - s_rows[c]), parts = s_parts[c];
+    const int hb = r / p.tile_rows, col = r % p.tile_rows;
+    auto slot = [&](int k) {
+      return (static_cast<size_t>(2 * (c - 1 + k) + (k == 0 ? 1 : 0)) * p.head_blocks + hb) * kLatentRows + col;
+    };
+    uint16_t* out = p.out + (static_cast<size_t>(p.cuts[c].t0) * p.heads + r) * C;
+    if (few) {
+      float* w = s_w + warp * kFewParts;
+      const float inv = join_weights(p, parts, slot, w);
+      for (int d = lane * 4; d < C; d += 128) {
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < kFewParts; ++k)
+          if (k < parts) add_part(acc, w[k], *reinterpret_cast<const float4*>(p.o + slot(k) * C + d));
+        *reinterpret_cast<uint2*>(out + d) =
+            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+      }
+      __syncwarp();
+    } else {
+      if (warp == 0) {
+        const float inv = join_weights(p, parts, slot, s_w);
+        if (lane == 0) s_inv = inv;
+      }
+      __syncthreads();
+      const int quads = C / 4, groups = kJoinThreads / quads, g = tid / quads, d = tid % quads * 4;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (g < groups) {
+#pragma unroll 8
+        for (int k = g; k < parts; k += groups) add_part(acc, s_w[k], *reinterpret_cast<const float4*>(p.o + slot(k) * C + d));
+      }
+      s_acc[tid] = acc;
+      __syncthreads();
+      if (g == 0) {
+        for (int k = 1; k < groups; ++k) add_part(acc, 1.f, s_acc[tid + k * quads]);
+        const float inv = s_inv;
+        *reinterpret_cast<uint2*>(out + d) =
+            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+      }
+      __syncthreads();
+    }
   }
 }
 
 template <int NB, int N>
-cudaError_t launch_t(const CUtensorMap& qmap, const CUtensorMap& pmap, const LatentParams& p, cudaStream_t stream) {
+cudaError_t launch_t(const CUtensorMap& qmap, const CUtensorMap& pmap, const CUtensorMap& rmap, const LatentParams& p, cudaStream_t stream) {
   const int bytes = static_cast<int>(LatentSmem<NB, N>::bytes);
   cudaError_t err = set_max_dynamic_smem(reinterpret_cast<const void*>(latent_kernel<NB, N>), bytes);
   if (err != cudaSuccess) return err;
@@ -707,25 +899,32 @@ cudaError_t launch_t(const CUtensorMap& qmap, const CUtensorMap& pmap, const Lat
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  err = cudaLaunchKernelEx(&cfg, latent_kernel<NB, N>, qmap, pmap, p);
+  err = cudaLaunchKernelEx(&cfg, latent_kernel<NB, N>, qmap, pmap, rmap, p);
   if (err != cudaSuccess) return err;
-  const int rows = p.head_blocks > 1 ? p.heads : p.tile_tokens * p.heads;
-  cfg.gridDim = dim3(static_cast<unsigned>(p.teams), static_cast<unsigned>((rows + kJoinRows - 1) / kJoinRows));
-  cfg.blockDim = dim3(32 * kJoinRows);
+  cfg.gridDim = dim3(static_cast<unsigned>(kJoinCtasPerSm * device_sm_count()));
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, latent_join_kernel, p);
 }
 
 }  // namespace
 
-cudaError_t launch_latent_attn(const CUtensorMap& qmap, const CUtensorMap& pmap, const LatentParams& p,
+cudaError_t launch_latent_attn(const CUtensorMap& qmap, const CUtensorMap& pmap, const CUtensorMap& rmap, const LatentParams& p,
                                cudaStream_t stream) {
   if (p.teams > kMaxTeams) return cudaErrorInvalidValue;
   switch (p.latent_dim / 128 * 100 + p.tile_rows) {
-    case 164: return launch_t<1, 64>(qmap, pmap, p, stream);
-    case 264: return launch_t<2, 64>(qmap, pmap, p, stream);
-    case 364: return launch_t<3, 64>(qmap, pmap, p, stream);
-    case 464: return launch_t<4, 64>(qmap, pmap, p, stream);
+    case 116: return launch_t<1, 16>(qmap, pmap, rmap, p, stream);
+    case 132: return launch_t<1, 32>(qmap, pmap, rmap, p, stream);
+    case 164: return launch_t<1, 64>(qmap, pmap, rmap, p, stream);
+    case 216: return launch_t<2, 16>(qmap, pmap, rmap, p, stream);
+    case 232: return launch_t<2, 32>(qmap, pmap, rmap, p, stream);
+    case 264: return launch_t<2, 64>(qmap, pmap, rmap, p, stream);
+    case 316: return launch_t<3, 16>(qmap, pmap, rmap, p, stream);
+    case 332: return launch_t<3, 32>(qmap, pmap, rmap, p, stream);
+    case 364: return launch_t<3, 64>(qmap, pmap, rmap, p, stream);
+    case 416: return launch_t<4, 16>(qmap, pmap, rmap, p, stream);
+    case 432: return launch_t<4, 32>(qmap, pmap, rmap, p, stream);
+    case 464: return launch_t<4, 64>(qmap, pmap, rmap, p, stream);
     default: return cudaErrorInvalidValue;
   }
 }
