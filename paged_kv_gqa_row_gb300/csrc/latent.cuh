@@ -35,6 +35,8 @@ struct LatentParams {
   int head_blocks;                 // tiles a token (heads > tile_rows)
   int teams;                       // groups of head_blocks CTAs that share the stream
   int min_pages;                   // of a share
+  int whole;                       // a team takes one token, all of it: nothing is cut
+  int ahead;                       // pages asked into L2 before they are loaded
   float scale_log2;
 };
 

@@ -40,7 +40,6 @@ namespace {
 
 constexpr int kThreads = 192;
 constexpr float kRaiseLog2 = 32.f;
-constexpr int kAhead = 0;      // pages asked into L2 before they are loaded
 constexpr int kSoftBar = 1;  // named barrier of the softmax warps
 
 template <int NB, int N>
@@ -240,7 +239,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   before -= mine;
   const long long per = max(static_cast<long long>(p.min_pages), (total + p.teams - 1) / p.teams);
   const long long start = team * per;
-  if (start >= before && start < before + mine) {
+  if (p.whole) {
+    // a team a token, whole
+    if (tid == 0 && team < T && unit_starts(p, team)) {
+      share->t = team;
+      share->left_lo = unit_at(p, team).np;
+    }
+  } else if (start >= before && start < before + mine) {
     long long at = before;
     for (int t = ta; t < tb; ++t) {
       if (!unit_starts(p, t)) continue;
@@ -259,14 +264,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = __shfl_sync(0xffffffffu, static_cast<uint32_t>(misc[1]), 0);
+  const uint32_t tmem = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(misc[1]));
   int t = share->t, j0 = share->j;
   long long left = (static_cast<long long>(share->left_hi) << 32) | static_cast<uint32_t>(share->left_lo);
 
   // what the kernel before this one on the stream writes is touched from here on
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (bad && blockIdx.x == 0 && p.status != nullptr) atomicOr(p.status, bad);
-  if (tid == 0 && hb == 0) {
+  if (tid == 0 && hb == 0 && !p.whole) {
     LatentCut cut;
     cut.t0 = t;
     cut.nt = cut.np = 0;
@@ -292,13 +297,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_2d(smem_addr(smem + L::q) + c * (N * 128), &qmap, c * kBoxCols, t * p.heads + hb * N, qfull);
         ++units;
       };
-      // Pages are asked into L2 kAhead pages before they are loaded: shared memory holds two
-      // pages, which alone would not cover HBM's latency.
+      // Pages asked into L2 before there is room for them in shared memory (LatentParams.ahead).
       int at = t, aj = j0, an = 0, ant = 0, afirst = 0, ahead = 0;
       long long aleft = left;
       const int32_t* arow = nullptr;
       auto prefetch = [&]() {
-        if (aleft <= 0 || hb != 0) return;
+        if (aleft <= 0 || hb != 0 || p.ahead == 0) return;
         if (arow == nullptr) {
           const Unit x = unit_at(p, at);
           arow = p.table + static_cast<long long>(max(x.row, 0)) * p.pages_per_row + x.first;
@@ -345,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             ++issued;
           }
-          for (; ahead < g + 1 + kAhead; ++ahead) prefetch();
+          for (; ahead < g + 2 + p.ahead; ++ahead) prefetch();
           if (ok && i == 0 && u > 0) {
             ok = mbar_wait(qempty, (u - 1) & 1, abort_flag);
             if (ok) load_q(t);
@@ -382,21 +386,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t q_lo = static_cast<uint32_t>(qdesc), q_hi = static_cast<uint32_t>(qdesc >> 32);
     const uint32_t v_lo = static_cast<uint32_t>(vdesc), v_hi = static_cast<uint32_t>(vdesc >> 32);
     const uint32_t p_lo = static_cast<uint32_t>(pdesc), p_hi = static_cast<uint32_t>(pdesc >> 32);
-    auto done = [](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test_wait(bar, parity)) != 0; };
+    // (reductions leave their results in uniform registers, which is where loop counters and
+    // conditions must be for the products' operands to be there)
+    auto uniform = [](int x) { return __reduce_max_sync(0xffffffffu, x); };
+    auto done = [](uint32_t bar, uint32_t parity) {
+      return __reduce_and_sync(0xffffffffu, mbar_test_wait(bar, parity) ? 1u : 0u) != 0u;
+    };
     // S^T of page s and the value product of page v <= s are issued in whatever order they
     // become ready: neither waits for the other's data.
     int s = 0, v = 0, u = 0;           // next score page; next value page; unit of page s
     int ut = 0, un = 0, ui = 0;        // tokens and pages (of this share) of unit u, page s in it
     uint32_t first = 0u;               // bit s & 1: page s is its unit's first here
-    bool more = left > 0;              // page s exists
-    if (more) {
+    int more = uniform(left > 0);      // page s exists
+    if (more != 0) {
       const Unit x = unit_at(p, t);
       ut = x.nt;
-      un = static_cast<int>(min(left, static_cast<long long>(x.np - j0)));
+      un = uniform(static_cast<int>(min(left, static_cast<long long>(x.np - j0))));
     }
     uint64_t t0 = 0;
     uint32_t idle = 0;
-    while (more || v < s) {
+    while (more != 0 || v < s) {
       bool did = false;
       if (v < s && done(pfull, v & 1)) {
         tc_fence_after();
@@ -416,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         did = true;
       }
       // (two score buffers: page s - 2 has been read once its value product was issued)
-      if (more && s <= v + 1 && done(full + 8 * (s % kStages), (s / kStages) & 1) && (ui > 0 || done(qfull, u & 1))) {
+      if (more != 0 && s <= v + 1 && done(full + 8 * (s % kStages), (s / kStages) & 1) && (ui > 0 || done(qfull, u & 1))) {
         tc_fence_after();
         const uint32_t sc = tmem + L::kColS + (s & 1) * N;
         uint32_t kd = k_lo + (((s % kStages) * L::kStage) >> 4), qd = q_lo;
@@ -441,11 +450,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           t += ut;
           ui = 0;
           ++u;
-          more = left > 0;
-          if (more) {
+          more = uniform(left > 0);
+          if (more != 0) {
             const Unit x = unit_at(p, t);
             ut = x.nt;
-            un = static_cast<int>(min(left, static_cast<long long>(x.np)));
+            un = uniform(static_cast<int>(min(left, static_cast<long long>(x.np))));
           }
         }
         did = true;
@@ -750,36 +759,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_dealloc(tmem, L::kCols);
 }
 
-// Joins the partial sums of the units that the shares cut.  Every block lists the cut
-// units (one for each share that is the first to start inside one) and takes their rows
-// in turn: a warp a row where no unit has more than kFewParts parts, so that all of a
-// batch's rows are under way at once; else the whole block a row, which splits the parts
-// over groups of threads (a long row's parts are as many as the shares).
+// Joins the partial sums of the units that the shares cut.  The blocks of all shares that
+// start inside one unit (kJoinBlocks each) divide its rows by 128 numbers of a row: a warp
+// takes such an item where the unit has up to kFewParts parts (every part's numbers are
+// asked for before its weight is known), else a whole block, its warps the parts in turn.
+// (What it takes is latency, and cold instruction caches: the end of the first kernel to
+// the end of this one, 64 rows of 32 heads, 13 us with a list of the units and a warp a row.)
 constexpr int kJoinThreads = 256;
-constexpr int kMaxTeams = 256;
-constexpr int kFewParts = 4;
-constexpr int kJoinCtasPerSm = 4;
-
-// Weight 2^(m_k - m) of part k, and 1 / sum, from the parts' references and sums; a warp.
-template <class Slot>
-__device__ __forceinline__ float join_weights(const LatentParams& p, int parts, Slot slot, float* w) {
-  const int lane = threadIdx.x & 31;
-  float m = -INFINITY;
-  for (int k = lane; k < parts; k += 32) m = fmaxf(m, p.ml[slot(k) * 2]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  float l = 0.f;
-  for (int k = lane; k < parts; k += 32) {
-    const float mk = p.ml[slot(k) * 2], lk = p.ml[slot(k) * 2 + 1];
-    const float f = mk == -INFINITY && m == -INFINITY ? 0.f : exp2f(mk - m);
-    w[k] = f;
-    l += f == 0.f && lk == lk ? 0.f : f * lk;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  __syncwarp();
-  return l > 0.f ? 1.f / l : l;
-}
+constexpr int kJoinBlocks = 8;
+constexpr int kFewParts = 8;
 
 __device__ __forceinline__ void add_part(float4& acc, float f, const float4& x) {
   acc.x = fmaf(f, x.x, acc.x);
@@ -788,99 +776,73 @@ __device__ __forceinline__ void add_part(float4& acc, float f, const float4& x) 
   acc.w = fmaf(f, x.w, acc.w);
 }
 
+// A part's weight 2^(its reference - the largest) (none has seen a key: 0)
+__device__ __forceinline__ float part_weight(float mk, float m) { return mk == -INFINITY && m == -INFINITY ? 0.f : ex2_approx(mk - m); }
+
 __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const __grid_constant__ LatentParams p) {
-  __shared__ int s_unit[kMaxTeams], s_end[kMaxTeams];  // share that cuts first; rows up to and with its unit
-  __shared__ int s_rows[kMaxTeams], s_parts[kMaxTeams];
-  __shared__ int s_units, s_most;
-  __shared__ float s_w[kMaxTeams + 8 * kFewParts];
-  __shared__ float s_inv;
   __shared__ float4 s_acc[kJoinThreads];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, C = p.latent_dim;
-  if (tid < p.teams) {
-    const LatentCut cut = p.cuts[tid];
-    const bool first = cut.j0 > 0 && cut.j0 <= cut.per;
-    // parts: shares tid - 1 .. the one that the unit's last page is in
-    s_rows[tid] = first ? cut.nt * p.heads : 0;
-    s_parts[tid] = first ? static_cast<int>((tid * cut.per - cut.j0 + cut.np - 1) / cut.per) - tid + 2 : 0;
-  }
-  __syncthreads();
-  if (warp == 0) {
-    int n = 0, rows = 0, most = 0;
-    for (int base = 0; base < p.teams; base += 32) {
-      const int c = base + lane, r = c < p.teams ? s_rows[c] : 0;
-      int sum = r;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += x;
-      }
-      const unsigned has = __ballot_sync(0xffffffffu, r > 0);
-      if (r > 0) {
-        const int at = n + __popc(has & ((1u << lane) - 1u));
-        s_unit[at] = c;
-        s_end[at] = rows + sum;
-        most = max(most, s_parts[c]);
-      }
-      n += __popc(has);
-      rows += __shfl_sync(0xffffffffu, sum, 31);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
-    if (lane == 0) {
-      s_units = n;
-      s_most = most;
-    }
-  }
-  __syncthreads();
-  if (s_units == 0) return;
-  const int total = s_end[s_units - 1];
-  const bool few = s_most <= kFewParts;
-  const int step = few ? kJoinThreads / 32 : 1;
-  int at = 0;
-  for (int i = blockIdx.x * step + (few ? warp : 0); i < total; i += gridDim.x * step) {
-    while (i >= s_end[at]) ++at;
-    const int c = s_unit[at], r = i - (s_end[at] - s_rows[c]), parts = s_parts[c];
+  const int share = blockIdx.x / kJoinBlocks;
+  const LatentCut cut = p.cuts[share];
+  if (cut.j0 == 0) return;
+  const long long p0 = share * cut.per - cut.j0;                     // the unit's first page in the stream
+  const int c0 = static_cast<int>(p0 / cut.per) + 1;                 // first share that starts inside the unit
+  const int cl = static_cast<int>((p0 + cut.np - 1) / cut.per);      // and the last
+  const int parts = cl - c0 + 2;                                     // shares c0 - 1 .. cl
+  const int nb = C / 128, items = cut.nt * p.heads * nb;
+  const int blocks = (cl - c0 + 1) * kJoinBlocks, block = (share - c0) * kJoinBlocks + blockIdx.x % kJoinBlocks;
+  const bool few = parts <= kFewParts;
+  const int step = few ? blocks * (kJoinThreads / 32) : blocks;
+  for (int i = few ? block * (kJoinThreads / 32) + warp : block; i < items; i += step) {
+    const int r = i / nb, d = i % nb * 128 + lane * 4;
     const int hb = r / p.tile_rows, col = r % p.tile_rows;
     auto slot = [&](int k) {
-      return (static_cast<size_t>(2 * (c - 1 + k) + (k == 0 ? 1 : 0)) * p.head_blocks + hb) * kLatentRows + col;
+      return (static_cast<size_t>(2 * (c0 - 1 + k) + (k == 0 ? 1 : 0)) * p.head_blocks + hb) * kLatentRows + col;
     };
-    uint16_t* out = p.out + (static_cast<size_t>(p.cuts[c].t0) * p.heads + r) * C;
+    float4 x[kFewParts];
     if (few) {
-      float* w = s_w + warp * kFewParts;
-      const float inv = join_weights(p, parts, slot, w);
-      for (int d = lane * 4; d < C; d += 128) {
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int k = 0; k < kFewParts; ++k)
-          if (k < parts) add_part(acc, w[k], *reinterpret_cast<const float4*>(p.o + slot(k) * C + d));
-        *reinterpret_cast<uint2*>(out + d) =
-            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-      }
-      __syncwarp();
+      for (int k = 0; k < kFewParts; ++k)
+        if (k < parts) x[k] = *reinterpret_cast<const float4*>(p.o + slot(k) * C + d);
+    }
+    float m = -INFINITY, l = 0.f;
+    float2 ml = make_float2(-INFINITY, 0.f);
+    for (int k = lane; k < parts; k += 32) {
+      ml = *reinterpret_cast<const float2*>(p.ml + slot(k) * 2);
+      m = fmaxf(m, ml.x);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int k = lane; k < parts; k += 32) {
+      if (!few) ml = *reinterpret_cast<const float2*>(p.ml + slot(k) * 2);
+      const float f = part_weight(ml.x, m);
+      l += f == 0.f && ml.y == ml.y ? 0.f : f * ml.y;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    const float inv = l > 0.f ? 1.f / l : l;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (few) {
+#pragma unroll
+      for (int k = 0; k < kFewParts; ++k)
+        if (k < parts) add_part(acc, part_weight(__shfl_sync(0xffffffffu, ml.x, k), m), x[k]);
     } else {
-      if (warp == 0) {
-        const float inv = join_weights(p, parts, slot, s_w);
-        if (lane == 0) s_inv = inv;
-      }
-      __syncthreads();
-      const int quads = C / 4, groups = kJoinThreads / quads, g = tid / quads, d = tid % quads * 4;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (g < groups) {
-#pragma unroll 8
-        for (int k = g; k < parts; k += groups) add_part(acc, s_w[k], *reinterpret_cast<const float4*>(p.o + slot(k) * C + d));
-      }
+#pragma unroll 4
+      for (int k = warp; k < parts; k += kJoinThreads / 32)
+        add_part(acc, part_weight(p.ml[slot(k) * 2], m), *reinterpret_cast<const float4*>(p.o + slot(k) * C + d));
       s_acc[tid] = acc;
       __syncthreads();
-      if (g == 0) {
-        for (int k = 1; k < groups; ++k) add_part(acc, 1.f, s_acc[tid + k * quads]);
-        const float inv = s_inv;
-        *reinterpret_cast<uint2*>(out + d) =
-            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+      if (warp == 0) {
+#pragma unroll
+        for (int w = 1; w < kJoinThreads / 32; ++w) add_part(acc, 1.f, s_acc[w * 32 + lane]);
       }
       __syncthreads();
     }
+    if (few || warp == 0)
+      *reinterpret_cast<uint2*>(p.out + (static_cast<size_t>(cut.t0) * p.heads + r) * C + d) =
+          make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
   }
 }
 
@@ -901,7 +863,8 @@ cudaError_t launch_t(const CUtensorMap& qmap, const CUtensorMap& pmap, const CUt
   cfg.numAttrs = 1;
   err = cudaLaunchKernelEx(&cfg, latent_kernel<NB, N>, qmap, pmap, rmap, p);
   if (err != cudaSuccess) return err;
-  cfg.gridDim = dim3(static_cast<unsigned>(kJoinCtasPerSm * device_sm_count()));
+  if (p.whole) return cudaSuccess;  // (no unit is cut)
+  cfg.gridDim = dim3(static_cast<unsigned>(kJoinBlocks * p.teams));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, latent_join_kernel, p);
@@ -911,7 +874,6 @@ cudaError_t launch_t(const CUtensorMap& qmap, const CUtensorMap& pmap, const CUt
 
 cudaError_t launch_latent_attn(const CUtensorMap& qmap, const CUtensorMap& pmap, const CUtensorMap& rmap, const LatentParams& p,
                                cudaStream_t stream) {
-  if (p.teams > kMaxTeams) return cudaErrorInvalidValue;
   switch (p.latent_dim / 128 * 100 + p.tile_rows) {
     case 116: return launch_t<1, 16>(qmap, pmap, rmap, p, stream);
     case 132: return launch_t<1, 32>(qmap, pmap, rmap, p, stream);
