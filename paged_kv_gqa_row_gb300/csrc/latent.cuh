@@ -58,6 +58,7 @@ struct LatentAppendParams {
   uint16_t* kv_out;         // or null
   int32_t* status;
   double norm_eps;
+  float inv_dim[2], eps[2];  // 1 / C and the epsilon as float pairs
   long long q_stride, q_out_stride;
   int T, heads, latent_dim, rope_dim, num_pages, num_rows, pages_per_row;
   float inv_freq[32];

@@ -175,6 +175,10 @@ lnk_status lnk_latent_append(const lnk_latent_desc* desc, const lnk_rope_desc* r
   p.kv_out = kv_out;
   p.status = dev_status;
   p.norm_eps = static_cast<double>(norm_eps);
+  const double inv_dim = 1.0 / desc->latent_dim;
+  p.inv_dim[0] = static_cast<float>(inv_dim);
+  p.inv_dim[1] = static_cast<float>(inv_dim - static_cast<double>(p.inv_dim[0]));
+  p.eps[0] = norm_eps;
   p.q_stride = q_stride;
   p.q_out_stride = q_out_stride;
   p.T = T;

@@ -2,10 +2,10 @@
 // and the query heads' last R numbers, and the write of [c, k] into the token's place.
 //
 // A token's heads are split over S CTAs of 128 threads (S = 1 for launches of many
-// tokens); the first also takes the token's row: up to four numbers of c a thread.  The
-// rotation is the float-pair arithmetic of rope_math.cuh; the norm's sum of squares is
-// a float pair too, its factor is computed once a token in double precision, and every
-// stored number is rounded once, to bf16.
+// tokens); the first also takes the token's row: up to four numbers of c a thread.  Every
+// stored number is rounded once, to bf16: in float32 where its error bound leaves no doubt
+// about that rounding, else from the float-pair arithmetic of rope_math.cuh, in which the
+// norm's sum of squares and factor are computed throughout.
 #include <algorithm>
 
 #include "latent.cuh"
@@ -25,19 +25,60 @@ __device__ __forceinline__ DF add_pair(DF a, float hi, float lo) {
   return two_sum(w.hi, __fadd_rn(w.lo, __fadd_rn(a.lo, lo)));
 }
 
-// x w r to the nearest bf16's float (x, w bf16 values; their product is exact).
-__device__ __forceinline__ float normed(float x, float w, DF r) {
-  const float xw = __fmul_rn(x, w);
-  const float v = df_off_tie(mul_df(DF{xw, 0.f}, r));
-  return v == v ? v : __fmul_rn(xw, r.hi);
+// The norm's factor 1 / sqrt(ss / C + eps): a float32 estimate and one Newton step on float
+// pairs, good to 2^-42; sums whose mean square is tiny or huge go through double precision.
+__device__ __forceinline__ DF norm_factor(DF ss, const LatentAppendParams& p) {
+  const DF v = add_pair(df_mul(ss, DF{p.inv_dim[0], p.inv_dim[1]}), p.eps[0], p.eps[1]);
+  if (!(v.hi > 1e-18f && v.hi < 1e18f)) return rms_factor(ss, p.latent_dim, p.norm_eps);
+  const float r0 = rsqrtf(v.hi);
+  const DF vr = df_mul(v, two_prod(r0, r0));              // v r0^2 = 1 + e, |e| about 2^-22
+  const float e = __fadd_rn(__fadd_rn(vr.hi, -1.f), vr.lo);
+  return fast_two_sum(r0, __fmul_rn(__fmul_rn(-0.5f, r0), e));
+}
+
+// Two numbers to bf16 in one rounding where float32 says which way: each is off by at most
+// `el`, `eh`; false where one of them may round either way (or is not finite).
+__device__ __forceinline__ bool sure_bf16x2(float lo, float hi, float el, float eh, uint32_t& bits) {
+  bits = floats_to_bf16x2(__fadd_rn(lo, el), __fadd_rn(hi, eh));
+  return bits == floats_to_bf16x2(__fsub_rn(lo, el), __fsub_rn(hi, eh));
+}
+
+// x w r of two neighbours (x, w bf16 values, whose product is exact).
+__device__ __forceinline__ uint32_t normed(uint32_t x, uint32_t w, DF r) {
+  const float a = __fmul_rn(bf16_lo(x), bf16_lo(w)), b = __fmul_rn(bf16_hi(x), bf16_hi(w));
+  const float ar = __fmul_rn(a, r.hi), br = __fmul_rn(b, r.hi);
+  uint32_t bits;
+  // (the product's rounding and r's low part: 2^-23 together)
+  if (sure_bf16x2(ar, br, __fmul_rn(fabsf(ar), 0x1p-21f), __fmul_rn(fabsf(br), 0x1p-21f), bits)) return bits;
+  const float c = df_off_tie(mul_df(DF{a, 0.f}, r)), d = df_off_tie(mul_df(DF{b, 0.f}, r));
+  return floats_to_bf16x2(c == c ? c : ar, d == d ? d : br);
+}
+
+// rotate_pairs (without a factor), in float32 where that decides the rounding: sine and
+// cosine, the two products and their sum are off by at most 2.5 2^-23 of |x1| + |x2|
+// together, and one element in a thousand is too near a tie.
+// (quick: cosine and sine of elements e and e + 1 in float32)
+__device__ __forceinline__ void rotate(uint32_t xlo, uint32_t xhi, const Coefs* c, float4 quick, int e, uint32_t& lo_bits,
+                                       uint32_t& hi_bits) {
+  float o1[2], o2[2], err[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const float cs = k ? quick.z : quick.x, sn = k ? quick.w : quick.y;
+    const float x1 = k ? bf16_hi(xlo) : bf16_lo(xlo), x2 = k ? bf16_hi(xhi) : bf16_lo(xhi);
+    o1[k] = __fmaf_rn(x1, cs, -__fmul_rn(x2, sn));
+    o2[k] = __fmaf_rn(x2, cs, __fmul_rn(x1, sn));
+    err[k] = __fmul_rn(__fadd_rn(fabsf(x1), fabsf(x2)), 0x1p-21f);
+  }
+  if (sure_bf16x2(o1[0], o1[1], err[0], err[1], lo_bits) & sure_bf16x2(o2[0], o2[1], err[0], err[1], hi_bits)) return;
+  rotate_pairs(xlo, xhi, c, e, false, DF{1.f, 0.f}, lo_bits, hi_bits);
 }
 
 template <int R>
 __global__ void __launch_bounds__(kThreads) latent_append_kernel(const __grid_constant__ LatentAppendParams p, int splits) {
   constexpr int H = R / 2, kLanes = R / 4;  // threads of a head: two numbers of each half
   __shared__ Coefs s_coef[H];
+  __shared__ __align__(16) float2 s_quick[H];
   __shared__ DF s_ss[kThreads / 32];
-  __shared__ DF s_r;
   __shared__ long long s_slot;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
@@ -70,10 +111,10 @@ __global__ void __launch_bounds__(kThreads) latent_append_kernel(const __grid_co
     }
     s_slot = slot;
   }
-  if (tid < H) s_coef[tid] = coefs_of(sn, cs, 1.f, 1.f);
 
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (bad && p.status != nullptr) atomicOr(p.status, bad);
+  // ---- loads ----
   const int C = p.latent_dim, W = C + R;
   const uint16_t* row_in = p.kv + static_cast<size_t>(t) * W;
   uint2 x = make_uint2(0u, 0u), w = make_uint2(0x3F803F80u, 0x3F803F80u);  // (bf16 ones)
@@ -81,6 +122,27 @@ __global__ void __launch_bounds__(kThreads) latent_append_kernel(const __grid_co
   if (has && pos >= 0) {
     x = *reinterpret_cast<const uint2*>(row_in + 4 * tid);
     if (p.norm_w != nullptr) w = *reinterpret_cast<const uint2*>(p.norm_w + 4 * tid);
+  }
+  const int e = 2 * (tid % kLanes);
+  constexpr int kBatch = 2;  // heads whose loads are in flight together
+  const int hstep = splits * (kThreads / kLanes);
+  uint32_t xlo[kBatch], xhi[kBatch];
+  auto load = [&](int h0) {
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int h = h0 + k * hstep;
+      xlo[k] = xhi[k] = 0u;
+      if (h < p.heads && pos >= 0) {
+        const uint16_t* src = p.q + (static_cast<size_t>(t) * p.heads + h) * p.q_stride + e;
+        xlo[k] = *reinterpret_cast<const uint32_t*>(src);
+        xhi[k] = *reinterpret_cast<const uint32_t*>(src + H);
+      }
+    }
+  };
+  load(sp + splits * (tid / kLanes));
+  if (tid < H) {
+    s_coef[tid] = coefs_of(sn, cs, 1.f, 1.f);
+    s_quick[tid] = make_float2(cs.hi, sn.hi);
   }
   if (sp == 0 && p.norm_w != nullptr) {
     const float a0 = bf16_lo(x.x), a1 = bf16_hi(x.x), a2 = bf16_lo(x.y), a3 = bf16_hi(x.y);
@@ -96,36 +158,36 @@ __global__ void __launch_bounds__(kThreads) latent_append_kernel(const __grid_co
   }
   __syncthreads();
   // ---- query heads of this CTA ----
-  const int e = 2 * (tid % kLanes);
-  for (int h = sp + splits * (tid / kLanes); h < p.heads; h += splits * (kThreads / kLanes)) {
-    const uint16_t* src = p.q + (static_cast<size_t>(t) * p.heads + h) * p.q_stride;
-    uint16_t* dst = p.q_out + (static_cast<size_t>(t) * p.heads + h) * p.q_out_stride;
-    uint32_t lo = 0u, hi = 0u;
-    if (pos >= 0)
-      rotate_pairs(*reinterpret_cast<const uint32_t*>(src + e), *reinterpret_cast<const uint32_t*>(src + H + e), s_coef, e,
-                   false, DF{1.f, 0.f}, lo, hi);
-    *reinterpret_cast<uint32_t*>(dst + e) = lo;
-    *reinterpret_cast<uint32_t*>(dst + H + e) = hi;
+  const float4 quick = *reinterpret_cast<const float4*>(&s_quick[e]);
+  for (int h0 = sp + splits * (tid / kLanes); h0 < p.heads;) {
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int h = h0 + k * hstep;
+      if (h >= p.heads) break;
+      uint32_t lo = 0u, hi = 0u;
+      if (pos >= 0) rotate(xlo[k], xhi[k], s_coef, quick, e, lo, hi);
+      uint16_t* dst = p.q_out + (static_cast<size_t>(t) * p.heads + h) * p.q_out_stride + e;
+      *reinterpret_cast<uint32_t*>(dst) = lo;
+      *reinterpret_cast<uint32_t*>(dst + H) = hi;
+    }
+    h0 += kBatch * hstep;
+    if (h0 < p.heads) load(h0);
   }
   if (sp != 0) return;
   // ---- the token's row ----
   DF r{1.f, 0.f};
   if (p.norm_w != nullptr) {
-    if (tid == 0) {
-      DF ss = s_ss[0];
-      for (int k = 1; k < kThreads / 32; ++k) ss = add_pair(ss, s_ss[k].hi, s_ss[k].lo);
-      s_r = rms_factor(ss, C, p.norm_eps);
-    }
-    __syncthreads();
-    r = s_r;
+    DF ss = s_ss[0];
+    for (int k = 1; k < kThreads / 32; ++k) ss = add_pair(ss, s_ss[k].hi, s_ss[k].lo);
+    r = norm_factor(ss, p);
   }
   uint16_t* pool_row = s_slot >= 0 ? p.pool + static_cast<size_t>(s_slot) * W : nullptr;
   uint16_t* kv_row = p.kv_out != nullptr ? p.kv_out + static_cast<size_t>(t) * W : nullptr;
   if (has) {
     uint2 c = x;
     if (p.norm_w != nullptr && pos >= 0) {
-      c.x = floats_to_bf16x2(normed(bf16_lo(x.x), bf16_lo(w.x), r), normed(bf16_hi(x.x), bf16_hi(w.x), r));
-      c.y = floats_to_bf16x2(normed(bf16_lo(x.y), bf16_lo(w.y), r), normed(bf16_hi(x.y), bf16_hi(w.y), r));
+      c.x = normed(x.x, w.x, r);
+      c.y = normed(x.y, w.y, r);
     }
     if (pool_row != nullptr) *reinterpret_cast<uint2*>(pool_row + 4 * tid) = c;
     if (kv_row != nullptr) *reinterpret_cast<uint2*>(kv_row + 4 * tid) = c;
@@ -133,8 +195,8 @@ __global__ void __launch_bounds__(kThreads) latent_append_kernel(const __grid_co
   if (tid < kLanes) {
     uint32_t lo = 0u, hi = 0u;
     if (pos >= 0)
-      rotate_pairs(*reinterpret_cast<const uint32_t*>(row_in + C + e), *reinterpret_cast<const uint32_t*>(row_in + C + H + e),
-                   s_coef, e, false, DF{1.f, 0.f}, lo, hi);
+      rotate(*reinterpret_cast<const uint32_t*>(row_in + C + e), *reinterpret_cast<const uint32_t*>(row_in + C + H + e), s_coef,
+             quick, e, lo, hi);
     if (pool_row != nullptr) {
       *reinterpret_cast<uint32_t*>(pool_row + C + e) = lo;
       *reinterpret_cast<uint32_t*>(pool_row + C + H + e) = hi;
