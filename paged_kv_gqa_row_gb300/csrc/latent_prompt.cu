@@ -15,6 +15,10 @@
 // passes from group to group through shared memory and moves only when it grows by more
 // than 2^8, which is when O is rescaled (the scheme of the paged prompt kernel, chunk.cu).
 //
+// The clusters stay on their SMs and take tiles in turn: the copies of the next tile's
+// queries, keys and values, and its first products, overlap the end of the one before.
+// (With a cluster a tile, four prompts of 1024 to 2047 tokens, 32 heads: 180 us.)
+//
 // Tile ids: prompt n's tiles are base(n) = q_starts[n] / 256 + n onwards, which leaves
 // every prompt room for its tiles without a sum over the prompts before it; ids without
 // queries end at once.
@@ -22,6 +26,8 @@
 // Values that are not finite, at keys that some rows of a tile see and others do not,
 // reach all of them through 0 * NaN: a row whose output is not finite computes it again
 // from its own keys (attend_row).  Key rows past the tile's last key are zeroed.
+#include <algorithm>
+
 #include "latent.cuh"
 #include "ptx.cuh"
 
@@ -29,7 +35,7 @@ namespace lnk {
 namespace {
 
 constexpr int kThreads = 11 * 32;
-constexpr int kStages = 4;
+constexpr int kStages = 3;
 constexpr int kRows = 128;                // query rows per CTA = tensor-memory lanes
 constexpr int kTileRows = 2 * kRows;
 constexpr int kStepKeys = 128;
@@ -47,14 +53,20 @@ struct PromptSmem {
   static constexpr size_t kring = 0;
   static constexpr size_t vring = kring + size_t(kStages) * kKStage;
   static constexpr size_t qsm = vring + size_t(kStages) * kVStage;
-  static constexpr size_t bars = qsm + size_t(kBoxesK) * kQBox;
-  // kfull, kempty, vfull, vempty [stages], sfull[2], sfree[2], pfull[2], pvdone[2], odone, qfull
-  static constexpr int kNumBars = 4 * kStages + 10;
-  static constexpr size_t misc = bars + kNumBars * sizeof(uint64_t);  // [0] tile, [1] abort, [2] tensor memory
-  static constexpr size_t cost = misc + 64;
-  static constexpr size_t xchg = cost + kMaxOrderedTiles * 4;  // hand-off: 10 x 128 words
-  static constexpr size_t end = xchg + 10 * kRows * 4;
+  static constexpr int kQ = kBoxesK * kQBox;                // this CTA's 128 query rows; two tiles' worth
+  static constexpr size_t bars = qsm + 2 * size_t(kQ);
+  // kfull, kempty, vfull, vempty [stages], sfull[2], sfree[2], pfull[2], pvdone[2], odone, ofree,
+  // qfull[2], qempty[2], iempty[2]
+  static constexpr int kNumBars = 4 * kStages + 16;
+  static constexpr size_t misc = bars + kNumBars * sizeof(uint64_t);  // [0] abort, [1] tensor memory, [2] tiles in order
+  static constexpr size_t info = misc + 64;                    // [2] PromptTile: the tiles under way
+  static constexpr size_t order = info + 64;                   // [kMaxOrderedTiles] tile ids, 16 bits each
+  // softmax groups' hand-off: max and ok [2 step parities][128]; at a tile's end max, sum and
+  // ok [2 tile parities][2 groups][128].  (During set-up: the tiles' costs.)
+  static constexpr size_t xchg = order + kMaxOrderedTiles * 2;
+  static constexpr size_t end = xchg + 16 * kRows * 4;
   static constexpr size_t bytes = end + 1024;
+  static_assert(bytes <= 232448, "shared memory");
 };
 
 struct PromptTile {
@@ -62,6 +74,7 @@ struct PromptTile {
   int k0, keys;    // the prompt's first key, keys that the last query sees
   int first;       // keys that the first query sees (may be negative)
   int bad;
+  int h;           // query head
 };
 
 __device__ __forceinline__ PromptTile prompt_tile(const LatentPromptParams& p, int id) {
@@ -73,7 +86,7 @@ __device__ __forceinline__ PromptTile prompt_tile(const LatentPromptParams& p, i
   }
   PromptTile t;
   const int qs = p.q_starts[a], qe = p.q_starts[a + 1], ks = p.k_starts[a], ke = p.k_starts[a + 1];
-  t.q0 = t.n = t.k0 = t.keys = t.first = t.bad = 0;
+  t.q0 = t.n = t.k0 = t.keys = t.first = t.bad = t.h = 0;
   const int k = id - (qs / kTileRows + a);
   if (qs < 0 || qe < qs || qe > p.Tq || ks < 0 || ke < ks || ke > p.Tk) {
     t.bad = k == 0 || a == 0;
@@ -130,46 +143,55 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t sfull = vempty + 8 * kStages;  // [2] Q.K^T into S_b finished
   const uint32_t sfree = sfull + 16;            // [2] the softmax has read S_b (rank 0 only)
   const uint32_t pfull = sfree + 16;            // [2] P_b written (rank 0 only)
-  const uint32_t pvdone = pfull + 16;           // [2] P.V from P_b finished (all but the last)
-  const uint32_t odone = pvdone + 16, qfull = odone + 8;
+  const uint32_t pvdone = pfull + 16;           // [2] P.V from P_b finished
+  const uint32_t odone = pvdone + 16;           // a tile's last P.V
+  const uint32_t ofree = odone + 8;             // both CTAs have read O (rank 0 only)
+  const uint32_t qfull = ofree + 8;             // [2] a tile's queries and its PromptTile are there
+  const uint32_t qempty = qfull + 16;           // [2] its last Q.K^T finished
+  const uint32_t iempty = qempty + 16;          // [2] its PromptTile was read
   int* misc = reinterpret_cast<int*>(smem + L::misc);
-  volatile int* abort_flag = misc + 1;
+  volatile int* abort_flag = misc;
+  volatile PromptTile* info = reinterpret_cast<volatile PromptTile*>(smem + L::info);
+  uint16_t* order = reinterpret_cast<uint16_t*>(smem + L::order);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_cta_rank();
-  const int cid = static_cast<int>(blockIdx.x >> 1);
-  const int h = cid % p.heads;
 
   if (tid == 0) {
     // rank 0's full barriers also count the relay's arrival for rank 1's copy
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(kfull + 8 * s, rank == 0 ? 2 : 1);
-      mbar_init(kempty + 8 * s, 1);
-      mbar_init(vfull + 8 * s, rank == 0 ? 2 : 1);
-      mbar_init(vempty + 8 * s, 1);
+    const uint32_t copies = rank == 0 ? 2 : 1;
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(kfull + 8 * i, copies);
+      mbar_init(kempty + 8 * i, 1);
+      mbar_init(vfull + 8 * i, copies);
+      mbar_init(vempty + 8 * i, 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(sfull + 8 * b, 1);
       mbar_init(sfree + 8 * b, 8);  // one softmax group (four warps) in each CTA
       mbar_init(pfull + 8 * b, 8);
       mbar_init(pvdone + 8 * b, 1);
+      mbar_init(qfull + 8 * b, copies);
+      mbar_init(qempty + 8 * b, 1);
+      mbar_init(iempty + 8 * b, rank == 0 ? 9 : 8);  // the softmax warps, and rank 0's P.V issuer
     }
     mbar_init(odone, 1);
-    mbar_init(qfull, rank == 0 ? 2 : 1);
+    mbar_init(ofree, 16);
     *abort_flag = 0;
+    misc[2] = p.tiles;
     fence_mbarrier_init();
   }
-  if (warp == 1) tmem2_alloc(smem_addr(misc + 2), L::kTmemCols);
+  if (warp == 1) tmem2_alloc(smem_addr(misc + 1), L::kTmemCols);
   // ---- tiles with the most keys first ----
-  int id = p.tiles - 1 - cid / p.heads;
-  if (p.tiles <= kMaxOrderedTiles) {
-    int* cost = reinterpret_cast<int*>(smem + L::cost);
+  const bool ordered = p.tiles <= kMaxOrderedTiles;
+  if (ordered) {
+    int* cost = reinterpret_cast<int*>(smem + L::xchg);
     for (int i = tid; i < p.tiles; i += kThreads) {
       const PromptTile x = prompt_tile(p, i);
       cost[i] = x.n > 0 ? x.keys + 1 : 0;
+      if (x.bad && blockIdx.x == 0 && p.status != nullptr) atomicOr(p.status, LNK_DEV_SEGMENT);
     }
     __syncthreads();
-    const int wanted = cid / p.heads;
     for (int i = tid; i < p.tiles; i += kThreads) {
       const int ci = cost[i];
       int rk = 0;
@@ -177,63 +199,82 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int ck = cost[k];
         rk += (ck > ci) || (ck == ci && k > i);
       }
-      if (rk == wanted) misc[0] = i;
-    }
-    __syncthreads();
-    id = misc[0];
-  }
-  const PromptTile tile = prompt_tile(p, id);
-  if (tile.bad && h == 0 && rank == 0 && tid == 0 && p.status != nullptr) atomicOr(p.status, LNK_DEV_SEGMENT);
-  const int nsteps = tile.n > 0 ? (tile.keys + kStepKeys - 1) / kStepKeys : 0;
-
-  // this CTA's part of step j: its 64 keys, and its value columns of all 128
-  auto load_k = [&](int j) {
-    const uint32_t fb = kfull + 8 * (j % kStages);
-    const uint32_t dst = smem_addr(smem + L::kring) + (j % kStages) * L::kKStage;
-    const int y = tile.k0 + j * kStepKeys + static_cast<int>(rank) * 64;
-    mbar_arrive_expect_tx(fb, L::kKStage);
-#pragma unroll
-    for (int c = 0; c < D / 64; ++c) tma_load_3d(dst + c * kBoxBytes, &kvmap, c * kBoxCols, h, y, fb);
-    tma_load_2d(dst + (D / 64) * kBoxBytes, &rmap, 0, y, fb);
-  };
-  auto load_v = [&](int j) {
-    const uint32_t fb = vfull + 8 * (j % kStages);
-    const uint32_t dst = smem_addr(smem + L::vring) + (j % kStages) * L::kVStage;
-    const int y = tile.k0 + j * kStepKeys, x = D + static_cast<int>(rank) * kBoxCols;
-    mbar_arrive_expect_tx(fb, L::kVStage);
-    tma_load_3d(dst, &kvmap, x, h, y, fb);
-    tma_load_3d(dst + kBoxBytes, &kvmap, x, h, y + 64, fb);
-  };
-  // the first copies need nothing of the other CTA
-  if (tid == 0 && nsteps > 0) {
-    mbar_arrive_expect_tx(qfull, L::kBoxesK * L::kQBox);
-    for (int c = 0; c < L::kBoxesK; ++c)
-      tma_load_3d(smem_addr(smem + L::qsm) + c * L::kQBox, &qmap, c * kBoxCols, h, tile.q0 + static_cast<int>(rank) * kRows,
-                  qfull);
-    for (int j = 0; j < min(nsteps, kStages); ++j) {
-      load_k(j);
-      load_v(j);
+      order[rk] = static_cast<uint16_t>(i);
+      if (ci == 0) atomicMin(misc + 2, rk);  // (from here on: nothing to do)
     }
   }
-  __syncwarp();
   // barriers initialised and tensor memory allocated in both CTAs before any
-  // thread of either uses the other's
+  // thread of either uses them
   tc_fence_before();
   cluster_sync_all();
   tc_fence_after();
-  const uint32_t tmem = static_cast<uint32_t>(misc[2]);
+  const uint32_t tmem = static_cast<uint32_t>(misc[1]);
 
   if (warp == 0) {
     // ============================== producer ==============================
-    if (lane == 0 && nsteps > 0) {
-      int nk = min(nsteps, kStages), nv = nk;  // copies issued
-      for (int j = kStages; j < nsteps; ++j) {
-        if (!mbar_wait(kempty + 8 * (j % kStages), ((j / kStages) - 1) & 1, abort_flag)) break;
-        load_k(j);
-        ++nk;
-        if (!mbar_wait(vempty + 8 * (j % kStages), ((j / kStages) - 1) & 1, abort_flag)) break;
-        load_v(j);
-        ++nv;
+    if (lane == 0) {
+      // The clusters take the items (tile, head) in turn, in the tiles' order, every other
+      // round backwards.
+      const long long items = static_cast<long long>(misc[2]) * p.heads;
+      const int clusters = static_cast<int>(gridDim.x >> 1), cid = static_cast<int>(blockIdx.x >> 1);
+      int it = 0, js = 0, nk = 0, nv = 0;  // tiles, steps; copies issued
+      bool ok = true;
+      for (long long k = 0; ok && k * clusters < items; ++k) {
+        const long long i = k * clusters + (k & 1 ? clusters - 1 - cid : cid);
+        if (i >= items) continue;
+        const int at = static_cast<int>(i / p.heads);
+        PromptTile x = prompt_tile(p, ordered ? order[at] : p.tiles - 1 - at);
+        x.h = static_cast<int>(i % p.heads);
+        if (!ordered && x.bad && x.h == 0 && rank == 0 && p.status != nullptr) atomicOr(p.status, LNK_DEV_SEGMENT);
+        if (x.n <= 0) continue;
+        const int b = it & 1;
+        if (it >= 2) ok = mbar_wait(qempty + 8 * b, ((it >> 1) - 1) & 1, abort_flag) &&
+                          mbar_wait(iempty + 8 * b, ((it >> 1) - 1) & 1, abort_flag);
+        if (!ok) break;
+        info[b].q0 = x.q0;
+        info[b].n = x.n;
+        info[b].k0 = x.k0;
+        info[b].keys = x.keys;
+        info[b].first = x.first;
+        info[b].h = x.h;
+        mbar_arrive_expect_tx(qfull + 8 * b, L::kQ);
+        for (int c = 0; c < L::kBoxesK; ++c)
+          tma_load_3d(smem_addr(smem + L::qsm) + b * L::kQ + c * L::kQBox, &qmap, c * kBoxCols, x.h,
+                      x.q0 + static_cast<int>(rank) * kRows, qfull + 8 * b);
+        ++it;
+        const int nsteps = (x.keys + kStepKeys - 1) / kStepKeys;
+        for (int j = 0; j < nsteps; ++j, ++js) {
+          const int s = js % kStages;
+          if (js >= kStages) ok = mbar_wait(kempty + 8 * s, ((js / kStages) - 1) & 1, abort_flag);
+          if (!ok) break;
+          // this CTA's 64 keys of the step
+          uint32_t dst = smem_addr(smem + L::kring) + s * L::kKStage;
+          const int y = x.k0 + j * kStepKeys, yk = y + static_cast<int>(rank) * 64;
+          mbar_arrive_expect_tx(kfull + 8 * s, L::kKStage);
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c) tma_load_3d(dst + c * kBoxBytes, &kvmap, c * kBoxCols, x.h, yk, kfull + 8 * s);
+          tma_load_2d(dst + (D / 64) * kBoxBytes, &rmap, 0, yk, kfull + 8 * s);
+          ++nk;
+          if (js >= kStages) ok = mbar_wait(vempty + 8 * s, ((js / kStages) - 1) & 1, abort_flag);
+          if (!ok) break;
+          // its value columns of all 128
+          dst = smem_addr(smem + L::vring) + s * L::kVStage;
+          const int xv = D + static_cast<int>(rank) * kBoxCols;
+          mbar_arrive_expect_tx(vfull + 8 * s, L::kVStage);
+          tma_load_3d(dst, &kvmap, xv, x.h, y, vfull + 8 * s);
+          tma_load_3d(dst + kBoxBytes, &kvmap, xv, x.h, y + 64, vfull + 8 * s);
+          ++nv;
+        }
+      }
+      const int tiles = it;
+      if (ok) {  // no more tiles
+        const int b = it & 1;
+        if (it >= 2) ok = mbar_wait(qempty + 8 * b, ((it >> 1) - 1) & 1, abort_flag) &&
+                          mbar_wait(iempty + 8 * b, ((it >> 1) - 1) & 1, abort_flag);
+        if (ok) {
+          info[b].n = -1;
+          mbar_arrive(qfull + 8 * b);
+        }
       }
       // do not leave while a copy may still land in this CTA's memory
       auto drain = [&](uint32_t bar, int parity) {
@@ -241,288 +282,338 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         while (!mbar_try_wait(bar, parity) && global_timer_ns() - t_0 < kWaitLimitNs) {
         }
       };
-      drain(qfull, 0);
+      if (tiles > 0) drain(qfull + 8 * ((tiles - 1) & 1), ((tiles - 1) >> 1) & 1);
       for (int k = max(0, nk - kStages); k < nk; ++k) drain(kfull + 8 * (k % kStages), (k / kStages) & 1);
       for (int k = max(0, nv - kStages); k < nv; ++k) drain(vfull + 8 * (k % kStages), (k / kStages) & 1);
     }
   } else if (warp == 1) {
     if (rank != 0) {
       // ============================ relay (rank 1) ==========================
-      if (lane == 0 && nsteps > 0) {
-        const uint32_t kfull0 = mapa_shared(kfull, 0), vfull0 = mapa_shared(vfull, 0);
-        if (mbar_wait(qfull, 0, abort_flag)) {
-          mbar_arrive_remote(mapa_shared(qfull, 0));
-          for (int j = 0; j < nsteps; ++j) {
-            const int s = j % kStages;
-            if (!mbar_wait(kfull + 8 * s, (j / kStages) & 1, abort_flag)) break;
+      if (lane == 0) {
+        const uint32_t kfull0 = mapa_shared(kfull, 0), vfull0 = mapa_shared(vfull, 0), qfull0 = mapa_shared(qfull, 0);
+        bool ok = true;
+        for (int it = 0, js = 0; ok; ++it) {
+          const int b = it & 1;
+          if (!mbar_wait(qfull + 8 * b, (it >> 1) & 1, abort_flag)) break;
+          const int n = info[b].n, nsteps = (info[b].keys + kStepKeys - 1) / kStepKeys;
+          mbar_arrive_remote(qfull0 + 8 * b);
+          if (n < 0) break;
+          for (int j = 0; ok && j < nsteps; ++j, ++js) {
+            const int s = js % kStages;
+            ok = mbar_wait(kfull + 8 * s, (js / kStages) & 1, abort_flag);
+            if (!ok) break;
             mbar_arrive_remote(kfull0 + 8 * s);
-            if (!mbar_wait(vfull + 8 * s, (j / kStages) & 1, abort_flag)) break;
+            ok = mbar_wait(vfull + 8 * s, (js / kStages) & 1, abort_flag);
+            if (!ok) break;
             mbar_arrive_remote(vfull0 + 8 * s);
           }
         }
       }
-    } else if (lane == 0 && nsteps > 0) {
+    } else if (lane == 0) {
       // ======================= Q.K^T issuer (rank 0) ========================
       constexpr uint32_t kIdS = umma_idesc_bf16(kTileRows, kStepKeys, 0, 0);
       const uint64_t kdesc0 = umma_desc_sw128(smem_addr(smem + L::kring), 0, 1024);
       const uint64_t qdesc0 = umma_desc_sw128(smem_addr(smem + L::qsm), 0, 1024);
       const int rope_steps = p.rope_dim / 16;
-      // S_b of step j, once the softmax has read S_b of step j - 2 and both CTAs' keys are there
-      bool ok = mbar_wait(qfull, 0, abort_flag);
-      for (int j = 0; ok && j < nsteps; ++j) {
-        const int b = j & 1, s = j % kStages;
-        ok = (j < 2 || mbar_wait(sfree + 8 * b, ((j - 2) >> 1) & 1, abort_flag)) &&
-             mbar_wait(kfull + 8 * s, (j / kStages) & 1, abort_flag);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t sc = tmem + L::kColS + static_cast<uint32_t>(b) * kStepKeys;
-        const uint64_t kd = kdesc0 + static_cast<uint64_t>((s * L::kKStage) >> 4);
+      bool ok = true;
+      for (int it = 0, js = 0; ok; ++it) {
+        const int qb = it & 1;
+        if (!mbar_wait(qfull + 8 * qb, (it >> 1) & 1, abort_flag)) break;
+        const int n = info[qb].n, nsteps = (info[qb].keys + kStepKeys - 1) / kStepKeys;
+        if (n < 0) break;
+        const uint64_t qd = qdesc0 + static_cast<uint64_t>((qb * L::kQ) >> 4);
+        // S_b of a step, once the softmax has read S_b of two steps before and both CTAs' keys are there
+        for (int j = 0; j < nsteps; ++j, ++js) {
+          const int b = js & 1, s = js % kStages;
+          ok = (js < 2 || mbar_wait(sfree + 8 * b, ((js - 2) >> 1) & 1, abort_flag)) &&
+               mbar_wait(kfull + 8 * s, (js / kStages) & 1, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t sc = tmem + L::kColS + static_cast<uint32_t>(b) * kStepKeys;
+          const uint64_t kd = kdesc0 + static_cast<uint64_t>((s * L::kKStage) >> 4);
 #pragma unroll
-        for (int kk = 0; kk < D / 16 + 4; ++kk) {
-          if (kk >= D / 16 && kk - D / 16 >= rope_steps) break;
-          const uint32_t koff = ((kk >> 2) * kBoxBytes + (kk & 3) * 32) >> 4;
-          const uint32_t qoff = ((kk >> 2) * L::kQBox + (kk & 3) * 32) >> 4;
-          umma2_ss(sc, qdesc0 + qoff, kd + koff, kIdS, kk > 0);
+          for (int kk = 0; kk < D / 16 + 4; ++kk) {
+            if (kk >= D / 16 && kk - D / 16 >= rope_steps) break;
+            const uint32_t koff = ((kk >> 2) * kBoxBytes + (kk & 3) * 32) >> 4;
+            const uint32_t qoff = ((kk >> 2) * L::kQBox + (kk & 3) * 32) >> 4;
+            umma2_ss(sc, qd + qoff, kd + koff, kIdS, kk > 0);
+          }
+          umma2_commit_both(sfull + 8 * b);
+          umma2_commit_both(kempty + 8 * s);
         }
-        umma2_commit_both(sfull + 8 * b);
-        umma2_commit_both(kempty + 8 * s);
+        umma2_commit_both(qempty + 8 * qb);
       }
     }
   } else if (warp == 10) {
-    if (rank == 0 && lane == 0 && nsteps > 0) {
+    if (rank == 0 && lane == 0) {
       // ========================= P.V issuer (rank 0) ========================
       constexpr uint32_t kIdPV = umma_idesc_bf16(kTileRows, 128, 0, 1);
       const uint64_t vdesc0 = umma_desc_sw128(smem_addr(smem + L::vring), 0, 1024);
       bool ok = true;
-      for (int j = 0; ok && j < nsteps; ++j) {
-        const int b = j & 1, s = j % kStages;
-        ok = mbar_wait(pfull + 8 * b, (j >> 1) & 1, abort_flag) &&
-             mbar_wait(vfull + 8 * s, (j / kStages) & 1, abort_flag);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t pc = tmem + L::kColP + static_cast<uint32_t>(b) * (kStepKeys / 2);
-        const uint64_t vd = vdesc0 + static_cast<uint64_t>((s * L::kVStage) >> 4);
+      for (int it = 0, js = 0, te = 0; ok; ++it) {  // te: tiles with steps
+        const int qb = it & 1;
+        if (!mbar_wait(qfull + 8 * qb, (it >> 1) & 1, abort_flag)) break;
+        const int n = info[qb].n, nsteps = (info[qb].keys + kStepKeys - 1) / kStepKeys;
+        mbar_arrive(iempty + 8 * qb);
+        if (n < 0) break;
+        for (int j = 0; j < nsteps; ++j, ++js) {
+          const int b = js & 1, s = js % kStages;
+          ok = mbar_wait(pfull + 8 * b, (js >> 1) & 1, abort_flag) &&
+               mbar_wait(vfull + 8 * s, (js / kStages) & 1, abort_flag);
+          // (O of the tile before has been read)
+          if (ok && j == 0 && te > 0) ok = mbar_wait(ofree, (te - 1) & 1, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t pc = tmem + L::kColP + static_cast<uint32_t>(b) * (kStepKeys / 2);
+          const uint64_t vd = vdesc0 + static_cast<uint64_t>((s * L::kVStage) >> 4);
 #pragma unroll
-        for (int kk = 0; kk < kStepKeys / 16; ++kk)
-          umma2_ts(tmem + L::kColO, pc + kk * 8, vd + ((kk * 16 * 128) >> 4), kIdPV, (j > 0 || kk > 0));
-        umma2_commit_both(vempty + 8 * s);
-        umma2_commit_both(j + 1 < nsteps ? pvdone + 8 * b : odone);
+          for (int kk = 0; kk < kStepKeys / 16; ++kk)
+            umma2_ts(tmem + L::kColO, pc + kk * 8, vd + ((kk * 16 * 128) >> 4), kIdPV, (j > 0 || kk > 0));
+          umma2_commit_both(vempty + 8 * s);
+          umma2_commit_both(pvdone + 8 * b);
+          if (j + 1 == nsteps) umma2_commit_both(odone);
+        }
+        if (nsteps > 0) ++te;
       }
     }
   } else {
     // ============================== softmax ===============================
-    // Group 0 (warps 2-5) takes the even steps, group 1 (warps 6-9) the odd ones; thread r of
-    // each group owns query row r of this CTA.  The running max passes from the group of step
-    // j to the group of step j + 1 (a named barrier that the publisher arrives on and the
-    // receiver waits on), together with the decision to go on.
+    // Group 0 (warps 2-5) takes the even steps of the CTA, group 1 (warps 6-9) the odd ones;
+    // thread r of each group owns query row r of this CTA.  The running max passes from the
+    // group of a step to the group of the next (a named barrier that the publisher arrives on
+    // and the receiver waits on), together with the decision to go on.
     const int grp = (warp - 2) >> 2;
     const int qt = warp & 3;
     const int rl = qt * 32 + lane;
     const int row = static_cast<int>(rank) * kRows + rl;
-    const bool live = row < tile.n;
-    const int hi = live ? tile.first + row : 0;  // keys that this row sees
     const uint32_t lanes = static_cast<uint32_t>(qt * 32) << 16;
-    const int bar_pub = 1 + qt + 4 * grp, bar_sub = 1 + qt + 4 * (grp ^ 1), bar_fin = 9 + qt;
+    const int bar_pub = 1 + qt + 4 * grp, bar_sub = 1 + qt + 4 * (grp ^ 1), bar_pair = 9 + qt;
     float* hand_m = reinterpret_cast<float*>(smem + L::xchg);           // [2 step parities][128 rows]
     int* hand_ok = reinterpret_cast<int*>(smem + L::xchg) + 2 * kRows;  // [2][128]
-    float* fin_m = reinterpret_cast<float*>(smem + L::xchg) + 4 * kRows;  // [2 groups][128]
-    float* fin_l = fin_m + 2 * kRows;
-    int* fin_ok = reinterpret_cast<int*>(fin_l + 2 * kRows);
-    const uint32_t pfull0 = mapa_shared(pfull, 0), sfree0 = mapa_shared(sfree, 0);
-    float m_ref = -INFINITY;   // the row's running max (log2 units) after this group's last step
-    float m_part = -INFINITY;  // reference of this group's partial sum
-    float l_part = 0.f;
-    bool ok = true, stuck = false;
+    const uint32_t pfull0 = mapa_shared(pfull, 0), sfree0 = mapa_shared(sfree, 0), ofree0 = mapa_shared(ofree, 0);
     const uint32_t sc = tmem + lanes + L::kColS + static_cast<uint32_t>(grp) * kStepKeys;
     const uint32_t pcol = tmem + lanes + L::kColP + static_cast<uint32_t>(grp) * (kStepKeys / 2);
-    for (int j = grp; j < nsteps; j += 2) {
-      const int kb = j * kStepKeys;
-      const int s = j % kStages;
-      bool okw = !stuck && __all_sync(0xffffffffu, mbar_wait(sfull + 8 * grp, (j >> 1) & 1, abort_flag));
-      const bool partial = kb + kStepKeys > tile.keys;
-      if (okw && partial) {
-        // keys past the tile's last may hold anything: zero their value rows
-        okw = __all_sync(0xffffffffu, mbar_wait(vfull + 8 * s, (j / kStages) & 1, abort_flag));
-        if (okw && kb + rl >= tile.keys) {
-          uint8_t* vrow = smem + L::vring + size_t(s) * L::kVStage + (rl >> 6) * kBoxBytes + (rl & 63) * 128;
+    bool ok = true;
+    for (int it = 0, js0 = 0, te = 0; ok; ++it) {
+      const bool there = __all_sync(0xffffffffu, mbar_wait(qfull + 8 * (it & 1), (it >> 1) & 1, abort_flag));
+      if (named_barrier_or(bar_pair, 64, !there)) break;  // (both groups or neither)
+      PromptTile tile;
+      tile.q0 = info[it & 1].q0;
+      tile.n = info[it & 1].n;
+      tile.k0 = info[it & 1].k0;
+      tile.keys = info[it & 1].keys;
+      tile.first = info[it & 1].first;
+      tile.h = info[it & 1].h;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(iempty + 8 * (it & 1));
+      if (tile.n < 0) break;
+      const int nsteps = (tile.keys + kStepKeys - 1) / kStepKeys;
+      const bool live = row < tile.n;
+      const int hi = live ? tile.first + row : 0;  // keys that this row sees
+      float* fin_m = reinterpret_cast<float*>(smem + L::xchg) + (4 + 6 * (it & 1)) * kRows;  // [2 groups][128]
+      float* fin_l = fin_m + 2 * kRows;
+      int* fin_ok = reinterpret_cast<int*>(fin_l + 2 * kRows);
+      float m_ref = -INFINITY;   // the row's running max (log2 units) after this group's last step
+      float m_part = -INFINITY;  // reference of this group's partial sum
+      float l_part = 0.f;
+      bool stuck = false;
+      for (int j = (grp ^ js0) & 1; j < nsteps; j += 2) {
+        const int js = js0 + j;
+        const int kb = j * kStepKeys;
+        const int s = js % kStages;
+        bool okw = !stuck && __all_sync(0xffffffffu, mbar_wait(sfull + 8 * grp, (js >> 1) & 1, abort_flag));
+        const bool partial = kb + kStepKeys > tile.keys;
+        if (okw && partial) {
+          // keys past the tile's last may hold anything: zero their value rows
+          okw = __all_sync(0xffffffffu, mbar_wait(vfull + 8 * s, (js / kStages) & 1, abort_flag));
+          if (okw && kb + rl >= tile.keys) {
+            uint8_t* vrow = smem + L::vring + size_t(s) * L::kVStage + (rl >> 6) * kBoxBytes + (rl & 63) * 128;
 #pragma unroll
-          for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(vrow + c * 16) = make_uint4(0u, 0u, 0u, 0u);
+            for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(vrow + c * 16) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
         }
-        fence_proxy_async_smem();
-      }
-      tc_fence_after();
-      float x[kStepKeys];
-      if (okw) {
-        uint32_t r0[32], r1[32], r2[32], r3[32];
-        tmem_ld32(sc, r0);
-        tmem_ld32(sc + 32, r1);
-        tmem_ld32(sc + 64, r2);
-        tmem_ld32(sc + 96, r3);
-        tmem_ld_wait();
+        tc_fence_after();
+        float x[kStepKeys];
+        if (okw) {
+          uint32_t r0[32], r1[32], r2[32], r3[32];
+          tmem_ld32(sc, r0);
+          tmem_ld32(sc + 32, r1);
+          tmem_ld32(sc + 64, r2);
+          tmem_ld32(sc + 96, r3);
+          tmem_ld_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_remote(sfree0 + 8 * grp);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            x[i] = __uint_as_float(r0[i]);
+            x[32 + i] = __uint_as_float(r1[i]);
+            x[64 + i] = __uint_as_float(r2[i]);
+            x[96 + i] = __uint_as_float(r3[i]);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < kStepKeys; ++i) x[i] = -INFINITY;
+        }
+        const int e0 = live ? hi - kb : kStepKeys;  // visible keys of this step: below e0
+        if (!__all_sync(0xffffffffu, e0 >= kStepKeys)) {
+#pragma unroll
+          for (int i = 0; i < kStepKeys; ++i) x[i] = i < e0 ? x[i] : -INFINITY;
+        }
+        float m8[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          m8[k] = fmax3(x[k], x[8 + k], x[16 + k]);
+#pragma unroll
+          for (int i = 24; i < kStepKeys - 8; i += 16) m8[k] = fmax3(m8[k], x[i + k], x[i + 8 + k]);
+          m8[k] = fmaxf(m8[k], x[kStepKeys - 8 + k]);
+        }
+        const float mraw = fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
+        const float mx = mraw == -INFINITY ? -INFINITY : mraw * p.scale_log2;
+        if (j > 0) {
+          named_barrier_sync(bar_sub, 64);
+          m_ref = hand_m[((js - 1) & 1) * kRows + rl];
+          okw = okw && hand_ok[((js - 1) & 1) * kRows + rl] != 0;
+        }
+        ok = __all_sync(0xffffffffu, okw);
+        float m_new = m_ref, alpha = 1.f;
+        if (mx != -INFINITY) {
+          if (m_ref == -INFINITY) {
+            m_new = mx;
+          } else if (mx > m_ref + kRescaleLog2) {
+            m_new = mx;
+            alpha = exp2f(m_ref - mx);
+          }
+        }
+        if (j + 1 < nsteps) {
+          hand_m[(js & 1) * kRows + rl] = m_new;
+          hand_ok[(js & 1) * kRows + rl] = ok ? 1 : 0;
+          __syncwarp();
+          named_barrier_arrive(bar_pub, 64);
+        }
+        if (!ok) break;
+        m_ref = m_new;
+        if (m_part != m_ref) {
+          if (m_part != -INFINITY) l_part *= exp2f(m_part - m_ref);
+          m_part = m_ref;
+        }
+        const float nbase = m_ref == -INFINITY ? 0.f : -m_ref;
+        const uint64_t c2 = f32x2(p.scale_log2, p.scale_log2), n2 = f32x2(nbase, nbase);
+        // P_grp is free once P.V of two steps before has read it
+        if (js >= 2) stuck = stuck || !__all_sync(0xffffffffu, mbar_wait(pvdone + 8 * grp, ((js - 2) >> 1) & 1, abort_flag));
+        tc_fence_after();
+        uint64_t s2[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+        for (int hh = 0; hh < 4; ++hh) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float a0v, a1v;
+            f32x2_split(fma_f32x2(f32x2(x[hh * 32 + 2 * i], x[hh * 32 + 2 * i + 1]), c2, n2), a0v, a1v);
+            const float e0v = ex2_approx(a0v), e1v = ex2_approx(a1v);
+            s2[i & 3] = add_f32x2(s2[i & 3], f32x2(e0v, e1v));
+            pk[i] = pack_bf16x2(e0v, e1v);
+          }
+          tmem_st16(pcol + hh * 16, pk);
+        }
+        if (__any_sync(0xffffffffu, alpha != 1.f) && j >= 1) {
+          // rescale this row of O between P.V of the step before and of this one (a failed wait
+          // travels with the next hand-off: this one has gone out)
+          stuck = stuck || !__all_sync(0xffffffffu, mbar_wait(pvdone + 8 * ((js - 1) & 1), ((js - 1) >> 1) & 1, abort_flag));
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < (stuck ? 0 : 4); ++c) {
+            uint32_t r[32];
+            tmem_ld32(tmem + lanes + L::kColO + c * 32, r);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
+            tmem_st32(tmem + lanes + L::kColO + c * 32, r);
+          }
+        }
+        tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_remote(sfree0 + 8 * grp);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          x[i] = __uint_as_float(r0[i]);
-          x[32 + i] = __uint_as_float(r1[i]);
-          x[64 + i] = __uint_as_float(r2[i]);
-          x[96 + i] = __uint_as_float(r3[i]);
+        if (lane == 0) {
+          if (partial) mbar_arrive_cluster(pfull0 + 8 * grp);  // publishes the zeroed value rows
+          else mbar_arrive_remote(pfull0 + 8 * grp);
         }
+        {
+          float u0, u1;
+          f32x2_split(add_f32x2(add_f32x2(s2[0], s2[1]), add_f32x2(s2[2], s2[3])), u0, u1);
+          l_part += u0 + u1;
+        }
+      }
+      // ---- normalise and store: group g stores half g of the row ----
+      float mf = -INFINITY;
+      if (nsteps > 0) {
+        const bool okw = ok && !stuck && __all_sync(0xffffffffu, mbar_wait(odone, te & 1, abort_flag));
+        tc_fence_after();
+        fin_m[grp * kRows + rl] = m_part;
+        fin_l[grp * kRows + rl] = l_part;
+        fin_ok[grp * kRows + rl] = okw ? 1 : 0;
+        named_barrier_sync(bar_pair, 64);
+        const float mo = fin_m[(grp ^ 1) * kRows + rl], lo_ = fin_l[(grp ^ 1) * kRows + rl];
+        ok = __all_sync(0xffffffffu, okw && fin_ok[(grp ^ 1) * kRows + rl] != 0);
+        mf = fmaxf(m_part, mo);
+        const float la = m_part == -INFINITY ? 0.f : l_part * exp2f(m_part - mf);
+        const float lb = mo == -INFINITY ? 0.f : lo_ * exp2f(mo - mf);
+        l_part = grp == 0 ? la + lb : lb + la;
+      }
+      const float inv = l_part > 0.f ? 1.f / l_part : l_part;  // (a NaN sum makes the row NaN)
+      uint32_t r[D / 2];
+      if (ok && nsteps > 0) {
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t (&rc)[16] = *reinterpret_cast<uint32_t(*)[16]>(r + c * 16);
+          tmem_ld16(tmem + lanes + L::kColO + grp * (D / 2) + c * 16, rc);
+        }
+        tmem_ld_wait();
+        // O may take the next tile's
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(ofree0);
+        ++te;
       } else {
 #pragma unroll
-        for (int i = 0; i < kStepKeys; ++i) x[i] = -INFINITY;
+        for (int i = 0; i < D / 2; ++i) r[i] = 0u;
       }
-      const int e0 = live ? hi - kb : kStepKeys;  // visible keys of this step: below e0
-      if (!__all_sync(0xffffffffu, e0 >= kStepKeys)) {
+      const size_t orow = (static_cast<size_t>(tile.q0 + row) * p.heads + tile.h) * D;
+      bool again = false;
+      if (live) {
+        uint4* o = reinterpret_cast<uint4*>(p.out + orow + grp * (D / 2));
+        uint32_t odd = 0u;  // bits 15 and 31: an element is not finite
+        const bool none = l_part == 0.f;
 #pragma unroll
-        for (int i = 0; i < kStepKeys; ++i) x[i] = i < e0 ? x[i] : -INFINITY;
-      }
-      float m8[8];
+        for (int i = 0; i < D / 16; ++i) {
+          float v[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        m8[k] = fmax3(x[k], x[8 + k], x[16 + k]);
-#pragma unroll
-        for (int i = 24; i < kStepKeys - 8; i += 16) m8[k] = fmax3(m8[k], x[i + k], x[i + 8 + k]);
-        m8[k] = fmaxf(m8[k], x[kStepKeys - 8 + k]);
-      }
-      const float mraw = fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
-      const float mx = mraw == -INFINITY ? -INFINITY : mraw * p.scale_log2;
-      if (j > 0) {
-        named_barrier_sync(bar_sub, 64);
-        m_ref = hand_m[((j - 1) & 1) * kRows + rl];
-        okw = okw && hand_ok[((j - 1) & 1) * kRows + rl] != 0;
-      }
-      ok = __all_sync(0xffffffffu, okw);
-      float m_new = m_ref, alpha = 1.f;
-      if (mx != -INFINITY) {
-        if (m_ref == -INFINITY) {
-          m_new = mx;
-        } else if (mx > m_ref + kRescaleLog2) {
-          m_new = mx;
-          alpha = exp2f(m_ref - mx);
+          for (int k = 0; k < 8; ++k) v[k] = none ? 0.f : __uint_as_float(r[8 * i + k]) * inv;
+          const uint4 w = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                                     pack_bf16x2(v[6], v[7]));
+          o[i] = w;
+          odd |= ((w.x & 0x7F807F80u) + 0x00800080u) | ((w.y & 0x7F807F80u) + 0x00800080u) |
+                 ((w.z & 0x7F807F80u) + 0x00800080u) | ((w.w & 0x7F807F80u) + 0x00800080u);
         }
+        again = (odd & 0x80008000u) != 0u && l_part == l_part;  // (a NaN sum is the row's own)
       }
-      if (j + 1 < nsteps) {
-        hand_m[(j & 1) * kRows + rl] = m_new;
-        hand_ok[(j & 1) * kRows + rl] = ok ? 1 : 0;
+      unsigned todo = __ballot_sync(0xffffffffu, again);
+      while (todo != 0u) {
+        const int src = __ffs(todo) - 1;
+        todo &= todo - 1;
+        const int rr = row - lane + src;
         __syncwarp();
-        named_barrier_arrive(bar_pub, 64);
+        attend_row<D>(p, p.q + (static_cast<size_t>(tile.q0 + rr) * p.heads + tile.h) * (D + p.rope_dim),
+                      p.kv + (static_cast<size_t>(tile.k0) * p.heads + tile.h) * (2 * D),
+                      p.k_rope + static_cast<long long>(tile.k0) * p.rope_stride, tile.first + rr,
+                      __shfl_sync(0xffffffffu, mf, src), __shfl_sync(0xffffffffu, inv, src),
+                      p.out + (static_cast<size_t>(tile.q0 + rr) * p.heads + tile.h) * D, grp * (D / 2), (grp + 1) * (D / 2));
       }
-      if (!ok) break;
-      m_ref = m_new;
-      if (m_part != m_ref) {
-        if (m_part != -INFINITY) l_part *= exp2f(m_part - m_ref);
-        m_part = m_ref;
-      }
-      const float nbase = m_ref == -INFINITY ? 0.f : -m_ref;
-      const uint64_t c2 = f32x2(p.scale_log2, p.scale_log2), n2 = f32x2(nbase, nbase);
-      // P_grp is free once P.V of step j - 2 has read it
-      if (j >= 2) stuck = stuck || !__all_sync(0xffffffffu, mbar_wait(pvdone + 8 * grp, ((j - 2) >> 1) & 1, abort_flag));
-      tc_fence_after();
-      uint64_t s2[4] = {0ull, 0ull, 0ull, 0ull};
-#pragma unroll
-      for (int hh = 0; hh < 4; ++hh) {
-        uint32_t pk[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float a0v, a1v;
-          f32x2_split(fma_f32x2(f32x2(x[hh * 32 + 2 * i], x[hh * 32 + 2 * i + 1]), c2, n2), a0v, a1v);
-          const float e0v = ex2_approx(a0v), e1v = ex2_approx(a1v);
-          s2[i & 3] = add_f32x2(s2[i & 3], f32x2(e0v, e1v));
-          pk[i] = pack_bf16x2(e0v, e1v);
-        }
-        tmem_st16(pcol + hh * 16, pk);
-      }
-      if (__any_sync(0xffffffffu, alpha != 1.f) && j >= 1) {
-        // rescale this row of O between P.V of step j - 1 and of step j (a failed wait travels
-        // with the next hand-off: this one has gone out)
-        stuck = stuck || !__all_sync(0xffffffffu, mbar_wait(pvdone + 8 * ((j - 1) & 1), ((j - 1) >> 1) & 1, abort_flag));
-        tc_fence_after();
-#pragma unroll 1
-        for (int c = 0; c < (stuck ? 0 : 4); ++c) {
-          uint32_t r[32];
-          tmem_ld32(tmem + lanes + L::kColO + c * 32, r);
-          tmem_ld_wait();
-#pragma unroll
-          for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
-          tmem_st32(tmem + lanes + L::kColO + c * 32, r);
-        }
-      }
-      tmem_st_wait();
-      tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        if (partial) mbar_arrive_cluster(pfull0 + 8 * grp);  // publishes the zeroed value rows
-        else mbar_arrive_remote(pfull0 + 8 * grp);
-      }
-      {
-        float u0, u1;
-        f32x2_split(add_f32x2(add_f32x2(s2[0], s2[1]), add_f32x2(s2[2], s2[3])), u0, u1);
-        l_part += u0 + u1;
-      }
+      js0 += nsteps;
     }
-    // ---- normalise and store: group g stores half g of the row ----
-    float mf = -INFINITY;
-    if (nsteps > 0) {
-      const bool okw = ok && !stuck && __all_sync(0xffffffffu, mbar_wait(odone, 0, abort_flag));
-      tc_fence_after();
-      fin_m[grp * kRows + rl] = m_part;
-      fin_l[grp * kRows + rl] = l_part;
-      fin_ok[grp * kRows + rl] = okw ? 1 : 0;
-      named_barrier_sync(bar_fin, 64);
-      const float mo = fin_m[(grp ^ 1) * kRows + rl], lo_ = fin_l[(grp ^ 1) * kRows + rl];
-      ok = __all_sync(0xffffffffu, okw && fin_ok[(grp ^ 1) * kRows + rl] != 0);
-      mf = fmaxf(m_part, mo);
-      const float la = m_part == -INFINITY ? 0.f : l_part * exp2f(m_part - mf);
-      const float lb = mo == -INFINITY ? 0.f : lo_ * exp2f(mo - mf);
-      l_part = grp == 0 ? la + lb : lb + la;
-    }
-    const float inv = l_part > 0.f ? 1.f / l_part : l_part;  // (a NaN sum makes the row NaN)
-    uint32_t r[D / 2];
-    if (ok && nsteps > 0) {
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t (&rc)[16] = *reinterpret_cast<uint32_t(*)[16]>(r + c * 16);
-        tmem_ld16(tmem + lanes + L::kColO + grp * (D / 2) + c * 16, rc);
-      }
-      tmem_ld_wait();
-    } else {
-#pragma unroll
-      for (int i = 0; i < D / 2; ++i) r[i] = 0u;
-    }
-    const size_t orow = (static_cast<size_t>(tile.q0 + row) * p.heads + h) * D;
-    bool again = false;
-    if (live) {
-      uint4* o = reinterpret_cast<uint4*>(p.out + orow + grp * (D / 2));
-      uint32_t odd = 0u;  // bits 15 and 31: an element is not finite
-      const bool none = l_part == 0.f;
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        float v[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = none ? 0.f : __uint_as_float(r[8 * i + k]) * inv;
-        const uint4 w = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                                   pack_bf16x2(v[6], v[7]));
-        o[i] = w;
-        odd |= ((w.x & 0x7F807F80u) + 0x00800080u) | ((w.y & 0x7F807F80u) + 0x00800080u) |
-               ((w.z & 0x7F807F80u) + 0x00800080u) | ((w.w & 0x7F807F80u) + 0x00800080u);
-      }
-      again = (odd & 0x80008000u) != 0u && l_part == l_part;  // (a NaN sum is the row's own)
-    }
-    unsigned todo = __ballot_sync(0xffffffffu, again);
-    while (todo != 0u) {
-      const int src = __ffs(todo) - 1;
-      todo &= todo - 1;
-      const int rr = row - lane + src;
-      __syncwarp();
-      attend_row<D>(p, p.q + (static_cast<size_t>(tile.q0 + rr) * p.heads + h) * (D + p.rope_dim),
-                    p.kv + (static_cast<size_t>(tile.k0) * p.heads + h) * (2 * D),
-                    p.k_rope + static_cast<long long>(tile.k0) * p.rope_stride, tile.first + rr,
-                    __shfl_sync(0xffffffffu, mf, src), __shfl_sync(0xffffffffu, inv, src),
-                    p.out + (static_cast<size_t>(tile.q0 + rr) * p.heads + h) * D, grp * (D / 2), (grp + 1) * (D / 2));
-    }
-    __syncwarp();
+    if (!ok) *abort_flag = 1;
   }
   __syncwarp();
   if (*abort_flag && lane == 0 && p.status != nullptr) atomicOr(p.status, LNK_DEV_TIMEOUT);
@@ -540,8 +631,9 @@ cudaError_t launch_t(const CUtensorMap& qmap, const CUtensorMap& kvmap, const CU
   const int bytes = static_cast<int>(PromptSmem<D>::bytes);
   const cudaError_t err = set_max_dynamic_smem(reinterpret_cast<const void*>(prompt_kernel<D>), bytes);
   if (err != cudaSuccess) return err;
-  const long long grid = 2ll * p.tiles * p.heads;
-  if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
+  const long long items = static_cast<long long>(p.tiles) * p.heads;
+  const long long grid = 2 * std::min<long long>(items, device_sm_count() / 2);  // a cluster a pair of SMs
+  if (grid <= 0) return cudaErrorInvalidValue;
   prompt_kernel<D><<<static_cast<unsigned>(grid), kThreads, bytes, stream>>>(qmap, kvmap, rmap, p);
   return cudaGetLastError();
 }
