@@ -17,7 +17,8 @@
 //
 // The clusters stay on their SMs and take tiles in turn: the copies of the next tile's
 // queries, keys and values, and its first products, overlap the end of the one before.
-// (With a cluster a tile, four prompts of 1024 to 2047 tokens, 32 heads: 180 us.)
+// (Four prompts of 1024 to 2047 tokens, 32 heads: 180 us with a cluster a tile, 140 us so with
+// one producer for keys and values.)
 //
 // Tile ids: prompt n's tiles are base(n) = q_starts[n] / 256 + n onwards, which leaves
 // every prompt room for its tiles without a sum over the prompts before it; ids without
@@ -34,7 +35,7 @@
 namespace lnk {
 namespace {
 
-constexpr int kThreads = 11 * 32;
+constexpr int kThreads = 12 * 32;
 constexpr int kStages = 3;
 constexpr int kRows = 128;                // query rows per CTA = tensor-memory lanes
 constexpr int kTileRows = 2 * kRows;
@@ -131,6 +132,35 @@ __device__ __noinline__ void attend_row(const LatentPromptParams& p, const uint1
   if (two) out[c0 + 32 + lane] = static_cast<uint16_t>(pack_bf16x2(acc1 * inv, 0.f));
 }
 
+__device__ __forceinline__ void drain(uint32_t bar, int parity) {
+  const uint64_t t_0 = global_timer_ns();
+  while (!mbar_try_wait(bar, parity) && global_timer_ns() - t_0 < kWaitLimitNs) {
+  }
+}
+
+// NC lanes of neighbouring rows hold NC 16-byte pieces of their row each: afterwards lane i
+// holds piece i of each of the rows, so that a store covers whole lines.
+template <int NC>
+__device__ __forceinline__ void transpose_pieces(uint4 (&w)[NC]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int b = 1; b < NC; b <<= 1) {
+    const bool up = (lane & b) != 0;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      if (c & b) continue;
+      const uint4 give = up ? w[c] : w[c | b];
+      uint4 got;
+      got.x = __shfl_xor_sync(0xffffffffu, give.x, b);
+      got.y = __shfl_xor_sync(0xffffffffu, give.y, b);
+      got.z = __shfl_xor_sync(0xffffffffu, give.z, b);
+      got.w = __shfl_xor_sync(0xffffffffu, give.w, b);
+      if (up) w[c] = got;
+      else w[c | b] = got;
+    }
+  }
+}
+
 template <int D>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kvmap,
@@ -154,7 +184,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   volatile PromptTile* info = reinterpret_cast<volatile PromptTile*>(smem + L::info);
   uint16_t* order = reinterpret_cast<uint16_t*>(smem + L::order);
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __reduce_max_sync(0xffffffffu, tid >> 5), lane = tid & 31;
   const uint32_t rank = cluster_cta_rank();
 
   if (tid == 0) {
@@ -173,7 +203,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(pvdone + 8 * b, 1);
       mbar_init(qfull + 8 * b, copies);
       mbar_init(qempty + 8 * b, 1);
-      mbar_init(iempty + 8 * b, rank == 0 ? 9 : 8);  // the softmax warps, and rank 0's P.V issuer
+      mbar_init(iempty + 8 * b, 10);  // the softmax warps, the values' producer, their issuer or relay
     }
     mbar_init(odone, 1);
     mbar_init(ofree, 16);
@@ -208,7 +238,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc_fence_before();
   cluster_sync_all();
   tc_fence_after();
-  const uint32_t tmem = static_cast<uint32_t>(misc[1]);
+  const uint32_t tmem = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(misc[1]));
 
   if (warp == 0) {
     // ============================== producer ==============================
@@ -217,7 +247,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // round backwards.
       const long long items = static_cast<long long>(misc[2]) * p.heads;
       const int clusters = static_cast<int>(gridDim.x >> 1), cid = static_cast<int>(blockIdx.x >> 1);
-      int it = 0, js = 0, nk = 0, nv = 0;  // tiles, steps; copies issued
+      int it = 0, js = 0, nk = 0;  // tiles, steps; copies issued
       bool ok = true;
       for (long long k = 0; ok && k * clusters < items; ++k) {
         const long long i = k * clusters + (k & 1 ? clusters - 1 - cid : cid);
@@ -255,15 +285,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int c = 0; c < D / 64; ++c) tma_load_3d(dst + c * kBoxBytes, &kvmap, c * kBoxCols, x.h, yk, kfull + 8 * s);
           tma_load_2d(dst + (D / 64) * kBoxBytes, &rmap, 0, yk, kfull + 8 * s);
           ++nk;
-          if (js >= kStages) ok = mbar_wait(vempty + 8 * s, ((js / kStages) - 1) & 1, abort_flag);
-          if (!ok) break;
-          // its value columns of all 128
-          dst = smem_addr(smem + L::vring) + s * L::kVStage;
-          const int xv = D + static_cast<int>(rank) * kBoxCols;
-          mbar_arrive_expect_tx(vfull + 8 * s, L::kVStage);
-          tma_load_3d(dst, &kvmap, xv, x.h, y, vfull + 8 * s);
-          tma_load_3d(dst + kBoxBytes, &kvmap, xv, x.h, y + 64, vfull + 8 * s);
-          ++nv;
         }
       }
       const int tiles = it;
@@ -277,20 +298,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
       // do not leave while a copy may still land in this CTA's memory
-      auto drain = [&](uint32_t bar, int parity) {
-        const uint64_t t_0 = global_timer_ns();
-        while (!mbar_try_wait(bar, parity) && global_timer_ns() - t_0 < kWaitLimitNs) {
-        }
-      };
       if (tiles > 0) drain(qfull + 8 * ((tiles - 1) & 1), ((tiles - 1) >> 1) & 1);
       for (int k = max(0, nk - kStages); k < nk; ++k) drain(kfull + 8 * (k % kStages), (k / kStages) & 1);
+    }
+  } else if (warp == 11) {
+    // ========================== the values' producer =======================
+    // (a warp of its own: values are needed, and leave, later than keys)
+    if (lane == 0) {
+      int js = 0, nv = 0;
+      bool ok = true;
+      for (int it = 0; ok; ++it) {
+        const int b = it & 1;
+        if (!mbar_wait(qfull + 8 * b, (it >> 1) & 1, abort_flag)) break;
+        const int n = info[b].n, k0 = info[b].k0, h = info[b].h;
+        const int nsteps = (info[b].keys + kStepKeys - 1) / kStepKeys;
+        mbar_arrive(iempty + 8 * b);
+        if (n < 0) break;
+        for (int j = 0; j < nsteps; ++j, ++js) {
+          const int s = js % kStages;
+          if (js >= kStages) ok = mbar_wait(vempty + 8 * s, ((js / kStages) - 1) & 1, abort_flag);
+          if (!ok) break;
+          // this CTA's value columns of the step's 128 keys
+          const uint32_t dst = smem_addr(smem + L::vring) + s * L::kVStage;
+          const int xv = D + static_cast<int>(rank) * kBoxCols, y = k0 + j * kStepKeys;
+          mbar_arrive_expect_tx(vfull + 8 * s, L::kVStage);
+          tma_load_3d(dst, &kvmap, xv, h, y, vfull + 8 * s);
+          tma_load_3d(dst + kBoxBytes, &kvmap, xv, h, y + 64, vfull + 8 * s);
+          ++nv;
+        }
+      }
       for (int k = max(0, nv - kStages); k < nv; ++k) drain(vfull + 8 * (k % kStages), (k / kStages) & 1);
     }
   } else if (warp == 1) {
     if (rank != 0) {
-      // ============================ relay (rank 1) ==========================
+      // ============= relay of queries and keys (rank 1 to rank 0) ============
       if (lane == 0) {
-        const uint32_t kfull0 = mapa_shared(kfull, 0), vfull0 = mapa_shared(vfull, 0), qfull0 = mapa_shared(qfull, 0);
+        const uint32_t kfull0 = mapa_shared(kfull, 0), qfull0 = mapa_shared(qfull, 0);
         bool ok = true;
         for (int it = 0, js = 0; ok; ++it) {
           const int b = it & 1;
@@ -298,83 +341,114 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const int n = info[b].n, nsteps = (info[b].keys + kStepKeys - 1) / kStepKeys;
           mbar_arrive_remote(qfull0 + 8 * b);
           if (n < 0) break;
-          for (int j = 0; ok && j < nsteps; ++j, ++js) {
-            const int s = js % kStages;
-            ok = mbar_wait(kfull + 8 * s, (js / kStages) & 1, abort_flag);
+          for (int j = 0; j < nsteps; ++j, ++js) {
+            ok = mbar_wait(kfull + 8 * (js % kStages), (js / kStages) & 1, abort_flag);
             if (!ok) break;
-            mbar_arrive_remote(kfull0 + 8 * s);
-            ok = mbar_wait(vfull + 8 * s, (js / kStages) & 1, abort_flag);
-            if (!ok) break;
-            mbar_arrive_remote(vfull0 + 8 * s);
+            mbar_arrive_remote(kfull0 + 8 * (js % kStages));
           }
         }
       }
-    } else if (lane == 0) {
+    } else {
       // ======================= Q.K^T issuer (rank 0) ========================
+      // (The whole warp, on values that reductions make the same in all its threads: from one
+      // thread's branch, between the softmax warps, a product took 110 clocks to issue.)
       constexpr uint32_t kIdS = umma_idesc_bf16(kTileRows, kStepKeys, 0, 0);
-      const uint64_t kdesc0 = umma_desc_sw128(smem_addr(smem + L::kring), 0, 1024);
-      const uint64_t qdesc0 = umma_desc_sw128(smem_addr(smem + L::qsm), 0, 1024);
-      const int rope_steps = p.rope_dim / 16;
+      const uint64_t kdesc = umma_desc_sw128(smem_addr(smem + L::kring), 0, 1024);
+      const uint64_t qdesc = umma_desc_sw128(smem_addr(smem + L::qsm), 0, 1024);
+      const uint32_t k_lo = static_cast<uint32_t>(kdesc), k_hi = static_cast<uint32_t>(kdesc >> 32);
+      const uint32_t q_lo = static_cast<uint32_t>(qdesc), q_hi = static_cast<uint32_t>(qdesc >> 32);
+      auto wait = [&](uint32_t bar, uint32_t parity) {
+        return __reduce_and_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag) ? 1u : 0u) != 0u;
+      };
       bool ok = true;
       for (int it = 0, js = 0; ok; ++it) {
         const int qb = it & 1;
-        if (!mbar_wait(qfull + 8 * qb, (it >> 1) & 1, abort_flag)) break;
-        const int n = info[qb].n, nsteps = (info[qb].keys + kStepKeys - 1) / kStepKeys;
+        if (!wait(qfull + 8 * qb, (it >> 1) & 1)) break;
+        const int n = __reduce_max_sync(0xffffffffu, info[qb].n);
+        const int nsteps = __reduce_max_sync(0xffffffffu, (info[qb].keys + kStepKeys - 1) / kStepKeys);
         if (n < 0) break;
-        const uint64_t qd = qdesc0 + static_cast<uint64_t>((qb * L::kQ) >> 4);
+        const uint32_t qd = q_lo + ((qb * L::kQ) >> 4);
         // S_b of a step, once the softmax has read S_b of two steps before and both CTAs' keys are there
         for (int j = 0; j < nsteps; ++j, ++js) {
           const int b = js & 1, s = js % kStages;
-          ok = (js < 2 || mbar_wait(sfree + 8 * b, ((js - 2) >> 1) & 1, abort_flag)) &&
-               mbar_wait(kfull + 8 * s, (js / kStages) & 1, abort_flag);
+          ok = (js < 2 || wait(sfree + 8 * b, ((js - 2) >> 1) & 1)) && wait(kfull + 8 * s, (js / kStages) & 1);
           if (!ok) break;
           tc_fence_after();
           const uint32_t sc = tmem + L::kColS + static_cast<uint32_t>(b) * kStepKeys;
-          const uint64_t kd = kdesc0 + static_cast<uint64_t>((s * L::kKStage) >> 4);
+          const uint32_t kd = k_lo + ((s * L::kKStage) >> 4);
 #pragma unroll
-          for (int kk = 0; kk < D / 16 + 4; ++kk) {
-            if (kk >= D / 16 && kk - D / 16 >= rope_steps) break;
-            const uint32_t koff = ((kk >> 2) * kBoxBytes + (kk & 3) * 32) >> 4;
-            const uint32_t qoff = ((kk >> 2) * L::kQBox + (kk & 3) * 32) >> 4;
-            umma2_ss(sc, qd + qoff, kd + koff, kIdS, kk > 0);
+          for (int kk = 0; kk < D / 16 + 2; ++kk)
+            umma2_ss_warp(sc, qd + (((kk >> 2) * L::kQBox + (kk & 3) * 32) >> 4), q_hi,
+                          kd + (((kk >> 2) * kBoxBytes + (kk & 3) * 32) >> 4), k_hi, kIdS, kk > 0 ? 1u : 0u);
+          if (p.rope_dim == 64) {
+#pragma unroll
+            for (int kk = D / 16 + 2; kk < D / 16 + 4; ++kk)
+              umma2_ss_warp(sc, qd + (((kk >> 2) * L::kQBox + (kk & 3) * 32) >> 4), q_hi,
+                            kd + (((kk >> 2) * kBoxBytes + (kk & 3) * 32) >> 4), k_hi, kIdS, 1u);
           }
-          umma2_commit_both(sfull + 8 * b);
-          umma2_commit_both(kempty + 8 * s);
+          umma2_commit_both_warp(sfull + 8 * b);
+          umma2_commit_both_warp(kempty + 8 * s);
         }
-        umma2_commit_both(qempty + 8 * qb);
+        umma2_commit_both_warp(qempty + 8 * qb);
       }
+      __syncwarp();
     }
   } else if (warp == 10) {
-    if (rank == 0 && lane == 0) {
+    if (rank != 0) {
+      // ====================== relay of values (rank 1) ======================
+      if (lane == 0) {
+        const uint32_t vfull0 = mapa_shared(vfull, 0);
+        bool ok = true;
+        for (int it = 0, js = 0; ok; ++it) {
+          const int b = it & 1;
+          if (!mbar_wait(qfull + 8 * b, (it >> 1) & 1, abort_flag)) break;
+          const int n = info[b].n, nsteps = (info[b].keys + kStepKeys - 1) / kStepKeys;
+          mbar_arrive(iempty + 8 * b);
+          if (n < 0) break;
+          for (int j = 0; j < nsteps; ++j, ++js) {
+            ok = mbar_wait(vfull + 8 * (js % kStages), (js / kStages) & 1, abort_flag);
+            if (!ok) break;
+            mbar_arrive_remote(vfull0 + 8 * (js % kStages));
+          }
+        }
+      }
+    } else {
       // ========================= P.V issuer (rank 0) ========================
       constexpr uint32_t kIdPV = umma_idesc_bf16(kTileRows, 128, 0, 1);
-      const uint64_t vdesc0 = umma_desc_sw128(smem_addr(smem + L::vring), 0, 1024);
+      const uint64_t vdesc = umma_desc_sw128(smem_addr(smem + L::vring), 0, 1024);
+      const uint32_t v_lo = static_cast<uint32_t>(vdesc), v_hi = static_cast<uint32_t>(vdesc >> 32);
+      auto wait = [&](uint32_t bar, uint32_t parity) {
+        return __reduce_and_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag) ? 1u : 0u) != 0u;
+      };
       bool ok = true;
       for (int it = 0, js = 0, te = 0; ok; ++it) {  // te: tiles with steps
         const int qb = it & 1;
-        if (!mbar_wait(qfull + 8 * qb, (it >> 1) & 1, abort_flag)) break;
-        const int n = info[qb].n, nsteps = (info[qb].keys + kStepKeys - 1) / kStepKeys;
-        mbar_arrive(iempty + 8 * qb);
+        if (!wait(qfull + 8 * qb, (it >> 1) & 1)) break;
+        const int n = __reduce_max_sync(0xffffffffu, info[qb].n);
+        const int nsteps = __reduce_max_sync(0xffffffffu, (info[qb].keys + kStepKeys - 1) / kStepKeys);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(iempty + 8 * qb);
         if (n < 0) break;
         for (int j = 0; j < nsteps; ++j, ++js) {
           const int b = js & 1, s = js % kStages;
-          ok = mbar_wait(pfull + 8 * b, (js >> 1) & 1, abort_flag) &&
-               mbar_wait(vfull + 8 * s, (js / kStages) & 1, abort_flag);
+          ok = wait(pfull + 8 * b, (js >> 1) & 1) && wait(vfull + 8 * s, (js / kStages) & 1);
           // (O of the tile before has been read)
-          if (ok && j == 0 && te > 0) ok = mbar_wait(ofree, (te - 1) & 1, abort_flag);
+          if (ok && j == 0 && te > 0) ok = wait(ofree, (te - 1) & 1);
           if (!ok) break;
           tc_fence_after();
           const uint32_t pc = tmem + L::kColP + static_cast<uint32_t>(b) * (kStepKeys / 2);
-          const uint64_t vd = vdesc0 + static_cast<uint64_t>((s * L::kVStage) >> 4);
+          const uint32_t vd = v_lo + ((s * L::kVStage) >> 4);
 #pragma unroll
           for (int kk = 0; kk < kStepKeys / 16; ++kk)
-            umma2_ts(tmem + L::kColO, pc + kk * 8, vd + ((kk * 16 * 128) >> 4), kIdPV, (j > 0 || kk > 0));
-          umma2_commit_both(vempty + 8 * s);
-          umma2_commit_both(pvdone + 8 * b);
-          if (j + 1 == nsteps) umma2_commit_both(odone);
+            umma2_ts_warp(tmem + L::kColO, pc + kk * 8, vd + ((kk * 16 * 128) >> 4), v_hi, kIdPV,
+                          kk > 0 ? 1u : (j > 0 ? 1u : 0u));
+          umma2_commit_both_warp(vempty + 8 * s);
+          umma2_commit_both_warp(pvdone + 8 * b);
+          if (j + 1 == nsteps) umma2_commit_both_warp(odone);
         }
         if (nsteps > 0) ++te;
       }
+      __syncwarp();
     }
   } else {
     // ============================== softmax ===============================
@@ -579,25 +653,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < D / 2; ++i) r[i] = 0u;
       }
-      const size_t orow = (static_cast<size_t>(tile.q0 + row) * p.heads + tile.h) * D;
-      bool again = false;
-      if (live) {
-        uint4* o = reinterpret_cast<uint4*>(p.out + orow + grp * (D / 2));
-        uint32_t odd = 0u;  // bits 15 and 31: an element is not finite
-        const bool none = l_part == 0.f;
+      constexpr int kPieces = D / 16;  // 16-byte pieces of half a row
+      uint4 w[kPieces];
+      uint32_t odd = 0u;  // bits 15 and 31: an element is not finite
+      const bool none = l_part == 0.f;
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          float v[8];
+      for (int i = 0; i < kPieces; ++i) {
+        float v[8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) v[k] = none ? 0.f : __uint_as_float(r[8 * i + k]) * inv;
-          const uint4 w = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                                     pack_bf16x2(v[6], v[7]));
-          o[i] = w;
-          odd |= ((w.x & 0x7F807F80u) + 0x00800080u) | ((w.y & 0x7F807F80u) + 0x00800080u) |
-                 ((w.z & 0x7F807F80u) + 0x00800080u) | ((w.w & 0x7F807F80u) + 0x00800080u);
-        }
-        again = (odd & 0x80008000u) != 0u && l_part == l_part;  // (a NaN sum is the row's own)
+        for (int k = 0; k < 8; ++k) v[k] = none ? 0.f : __uint_as_float(r[8 * i + k]) * inv;
+        w[i] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                          pack_bf16x2(v[6], v[7]));
+        odd |= ((w[i].x & 0x7F807F80u) + 0x00800080u) | ((w[i].y & 0x7F807F80u) + 0x00800080u) |
+               ((w[i].z & 0x7F807F80u) + 0x00800080u) | ((w[i].w & 0x7F807F80u) + 0x00800080u);
       }
+      // (a NaN sum is the row's own: all of it is NaN)
+      const bool again = live && (odd & 0x80008000u) != 0u && l_part == l_part;
+      transpose_pieces<kPieces>(w);
+      uint16_t* o = p.out + (static_cast<size_t>(tile.q0 + (row & ~(kPieces - 1))) * p.heads + tile.h) * D + grp * (D / 2) +
+                    (lane & (kPieces - 1)) * 8;
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i)
+        if ((row & ~(kPieces - 1)) + i < tile.n)
+          *reinterpret_cast<uint4*>(o + static_cast<size_t>(i) * p.heads * D) = w[i];
       unsigned todo = __ballot_sync(0xffffffffu, again);
       while (todo != 0u) {
         const int src = __ffs(todo) - 1;
