@@ -34,8 +34,7 @@ struct LatentParams {
   int tile_tokens;                 // prompt tokens a tile at most
   int head_blocks;                 // tiles a token (heads > tile_rows)
   int teams;                       // groups of head_blocks CTAs that share the stream
-  int min_pages;                   // of a share
-  int whole;                       // a team takes one token, all of it: nothing is cut
+  int whole;                       // no unit is cut (all have few pages)
   int ahead;                       // pages asked into L2 before they are loaded
   float scale_log2;
 };

@@ -9,7 +9,7 @@ namespace lnk {
 namespace {
 
 constexpr int kMaxLatentHeads = 1024;
-constexpr int kWholePages = 8;  // few short rows: one team each, and no second kernel
+constexpr int kWholePages = 8;  // tokens of so few pages are never cut, and there is no second kernel
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -98,10 +98,9 @@ lnk_status attend(const lnk_latent_desc* desc, const lnk_bf16* q, const int32_t*
   p.head_blocks = (p.heads + p.tile_rows - 1) / p.tile_rows;
   if (p.head_blocks > sms) return LNK_ERANGE;
   p.teams = sms / p.head_blocks;
-  p.min_pages = 2;
   long long most = p.pages_per_row;  // pages of a token
   if (p.window > 0) most = std::min<long long>(most, (p.window - 1) / kPage + 2);
-  p.whole = p.T <= p.teams && most <= kWholePages;
+  p.whole = most <= kWholePages;
   p.ahead = 0;
   p.scale_log2 = latent_scale_log2(desc);
 

@@ -40,6 +40,7 @@ namespace {
 
 constexpr int kThreads = 192;
 constexpr float kRaiseLog2 = 32.f;
+constexpr int kWholePages = 8;
 constexpr int kSoftBar = 1;  // named barrier of the softmax warps
 
 template <int NB, int N>
@@ -75,8 +76,8 @@ struct LatentSmem {
 };
 
 struct Share {
-  int t, j;           // first unit (its first token) and page in it
-  int left_hi, left_lo;
+  int t, j;                 // first unit (its first token) and page in it
+  unsigned long long left;  // pages
 };
 
 struct Unit {
@@ -202,9 +203,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kStages; ++i) mbar_init(full + 8 * i, kGroups);
     mbar_init(pfull, 4);
     *abort_flag = 0;
-    share->t = 0;
+    share->t = 0x7fffffff;
     share->j = 0;
-    share->left_hi = share->left_lo = 0;
+    share->left = 0ull;
     fence_mbarrier_init();
   }
   if (warp == 1) tmem_alloc(smem_addr(misc + 1), L::kCols);
@@ -215,13 +216,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int T = p.T;
   const int span = (T + kThreads - 1) / kThreads;
   const int ta = min(T, tid * span), tb = min(T, ta + span);
-  int bad = 0;
+  int bad = 0, most = 0;
   long long mine = 0;
   for (int t = ta; t < tb; ++t) {
     int row, lo, hi;
     bad |= token_keys(p, t, row, lo, hi);
-    if (unit_starts(p, t)) mine += unit_at(p, t).np;
+    if (unit_starts(p, t)) {
+      const int np = unit_at(p, t).np;
+      mine += np;
+      most = max(most, np);
+    }
   }
+  most = __reduce_max_sync(0xffffffffu, most);
   long long before = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -229,33 +235,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane >= o) before += x;
   }
   if (lane == 31) scan[warp] = before;
+  if (lane == 0) misc[28 + warp] = most;
   __syncthreads();
   long long total = 0;
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) before += scan[w];
     total += scan[w];
+    most = max(most, misc[28 + w]);
   }
   before -= mine;
-  const long long per = max(static_cast<long long>(p.min_pages), (total + p.teams - 1) / p.teams);
+  const long long per = max(1ll, (total + p.teams - 1) / p.teams);
   const long long start = team * per;
-  if (p.whole) {
-    // a team a token, whole
-    if (tid == 0 && team < T && unit_starts(p, team)) {
-      share->t = team;
-      share->left_lo = unit_at(p, team).np;
-    }
-  } else if (start >= before && start < before + mine) {
+  // Units of few pages (or far fewer than a share) stay whole: a team takes those whose first
+  // page lies in its share.
+  const bool whole = p.whole || most <= max(static_cast<long long>(kWholePages), per / 8);
+  if (before < start + per && before + mine > start) {
     long long at = before;
-    for (int t = ta; t < tb; ++t) {
+    for (int t = ta; t < tb && at < start + per; ++t) {
       if (!unit_starts(p, t)) continue;
       const int np = unit_at(p, t).np;
-      if (start < at + np) {
-        const long long left = min(per, total - start);
+      if (whole) {
+        if (at >= start) {
+          atomicMin(&share->t, t);
+          atomicAdd(&share->left, static_cast<unsigned long long>(np));
+        }
+      } else if (at <= start && start < at + np) {
         share->t = t;
         share->j = static_cast<int>(start - at);
-        share->left_hi = static_cast<int>(left >> 32);
-        share->left_lo = static_cast<int>(left);
+        share->left = static_cast<unsigned long long>(min(per, total - start));
         break;
       }
       at += np;
@@ -266,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(misc[1]));
   int t = share->t, j0 = share->j;
-  long long left = (static_cast<long long>(share->left_hi) << 32) | static_cast<uint32_t>(share->left_lo);
+  long long left = static_cast<long long>(share->left);
 
   // what the kernel before this one on the stream writes is touched from here on
   asm volatile("griddepcontrol.wait;" ::: "memory");
