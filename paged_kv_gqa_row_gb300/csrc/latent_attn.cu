@@ -61,9 +61,8 @@ struct LatentSmem {
   static constexpr size_t bars = p + kP;
   // full[S], empty[S][groups], sfull[2], pfull, pvdone, qfull, qempty, fin
   static constexpr int kNumBars = kStages + kStages * kGroups + 7;
-  static constexpr size_t lo = bars + 8 * kNumBars;
-  static constexpr size_t hi = lo + 4 * kLatentRows;
-  static constexpr size_t alpha = hi + 4 * kLatentRows;      // factors of a raise; at the end 1 / sum
+  static constexpr size_t keys = (bars + 8 * kNumBars + 15) & ~size_t(15);  // int2 a row
+  static constexpr size_t alpha = keys + 8 * kLatentRows;      // factors of a raise; at the end 1 / sum
   static constexpr size_t ref = alpha + 4 * kLatentRows;
   static constexpr size_t misc = ref + 4 * kLatentRows;      // abort, tensor memory, share
   static constexpr size_t end = misc + 256;
@@ -183,8 +182,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t empty = full + 8 * kStages;                 // [stage][group]
   const uint32_t sfull = empty + 8 * kStages * kGroups;      // [2]
   const uint32_t pfull = sfull + 16, pvdone = pfull + 8, qfull = pvdone + 8, qempty = qfull + 8, fin = qempty + 8;
-  int* row_lo = reinterpret_cast<int*>(smem + L::lo);
-  int* row_hi = reinterpret_cast<int*>(smem + L::hi);
+  int2* row_keys = reinterpret_cast<int2*>(smem + L::keys);  // keys that a row sees: [x, y)
   float* s_alpha = reinterpret_cast<float*>(smem + L::alpha);
   float* s_ref = reinterpret_cast<float*>(smem + L::ref);
   int* misc = reinterpret_cast<int*>(smem + L::misc);
@@ -504,8 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (sid < N) {
         int lo = 0, hi = 0x7fffffff, row;
         if (sid < nrows) token_keys(p, t + (hb * N + sid) / p.heads, row, lo, hi);
-        row_lo[sid] = lo;
-        row_hi[sid] = hi;
+        row_keys[sid] = make_int2(lo, hi);
         s_ref[sid] = -INFINITY;  // the score of the row's first key, once it is known
       }
       named_barrier_sync(kSoftBar, 128);
@@ -516,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < N / 4; ++i) {
         nref[i] = l[i] = 0.f;
         const int col = 8 * (i >> 1) + ca + (i & 1);
-        if (col < nrows && row_hi[col] > row_lo[col]) unset |= 1u << i;
+        if (col < nrows && row_keys[col].y > row_keys[col].x) unset |= 1u << i;
       }
       bool force = true;            // some row has no reference yet (the same in every thread)
       for (int i = 0; i < n; ++i, ++g) {
@@ -530,24 +527,56 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld_16x256b(tmem + lanes + L::kColS + (g & 1) * N, r);
           tmem_ld_wait();
         }
+        // (The paths off the usual page are kept short: their instructions are cold when they
+        // are met, a line of them a few hundred clocks.)
         if (!(held && kb >= un.in_lo && kb + kPage <= un.in_hi)) {
+          if (un.nt == 1 || !held) {  // one row of the table's keys for all columns
+            const bool see0 = held && kb + ka >= un.kmin && kb + ka < un.kmax;
+            const bool see8 = held && kb + ka + 8 >= un.kmin && kb + ka + 8 < un.kmax;
 #pragma unroll
-          for (int x = 0; x < NX; ++x) {
-            const int col = 8 * (x >> 2) + ca + (x & 1), key = kb + ka + (x & 2 ? 8 : 0);
-            if (!(held && key >= row_lo[col] && key < row_hi[col])) r[x] = 0xFF800000u;
+            for (int x = 0; x < NX; ++x)
+              if (!(x & 2 ? see8 : see0)) r[x] = 0xFF800000u;
+          } else {
+#pragma unroll
+            for (int x = 0; x < NX; x += 4) {
+              const int4 k = *reinterpret_cast<const int4*>(row_keys + 2 * x + ca);  // of columns 2 x + ca, + 1
+              const int key = kb + ka;
+              if (key < k.x || key >= k.y) r[x] = 0xFF800000u;
+              if (key < k.z || key >= k.w) r[x + 1] = 0xFF800000u;
+              if (key + 8 < k.x || key + 8 >= k.y) r[x + 2] = 0xFF800000u;
+              if (key + 8 < k.z || key + 8 >= k.w) r[x + 3] = 0xFF800000u;
+            }
           }
         }
         if (force) {
+          if (un.nt == 1 || p.window == 0) {  // the same first key for all rows
+            const int first = max(un.kmin, kb) - kb;
+            if (ka == first || ka + 8 == first) {
 #pragma unroll
-          for (int x = 0; x < NX; ++x) {
-            const int col = 8 * (x >> 2) + ca + (x & 1), key = kb + ka + (x & 2 ? 8 : 0);
-            if (key == max(row_lo[col], kb)) s_ref[col] = fmaxf(s_ref[col], __uint_as_float(r[x]));
+              for (int x = 0; x < N / 4; ++x) {
+                const int at = (x >> 1) * 4 + (x & 1);
+                s_ref[8 * (x >> 1) + ca + (x & 1)] = __uint_as_float(ka == first ? r[at] : r[at + 2]);
+              }
+            }
+          } else {
+#pragma unroll 1
+            for (int col = 0; col < N; ++col) {
+              // (the thread that holds the column's first key of this page)
+              const int first = max(row_keys[col].x, kb) - kb - ka;
+              if ((first == 0 || first == 8) && (col & 6) == ca) {
+                float f = -INFINITY;
+#pragma unroll
+                for (int x = 0; x < NX; ++x)
+                  if (8 * (x >> 2) + ca + (x & 1) == col && (x & 2 ? 8 : 0) == first) f = __uint_as_float(r[x]);
+                s_ref[col] = f;
+              }
+            }
           }
           named_barrier_sync(kSoftBar, 128);
 #pragma unroll
           for (int x = 0; x < N / 4; ++x) {
             const float f = s_ref[8 * (x >> 1) + ca + (x & 1)];
-            if ((unset >> x & 1) && f != -INFINITY) {
+            if ((unset >> x & 1) && f > -INFINITY) {  // (a NaN score: the maximum of the others, below)
               nref[x] = -f * p.scale_log2;
               unset &= ~(1u << x);
             }
@@ -568,9 +597,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         exponents();
         if (force) {
           // a column without a reference that sees a score all the same (its first one is -inf)
+          if (unset != 0u) {
 #pragma unroll
-          for (int x = 0; x < NX; ++x)
-            if ((unset >> ((x >> 2) * 2 + (x & 1)) & 1) && a[x] > -INFINITY) mx = INFINITY;
+            for (int x = 0; x < NX; ++x)
+              if ((unset >> ((x >> 2) * 2 + (x & 1)) & 1) && a[x] > -INFINITY) mx = INFINITY;
+          }
           force = __any_sync(0xffffffffu, unset != 0u);
         }
         if (named_barrier_or(kSoftBar, 128, mx > kRaiseLog2 || !ok)) {
@@ -644,13 +675,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---- value rows that no token of the unit sees may hold anything: zero ----
         if (!(held && kb >= un.kmin && kb + kPage <= un.kmax)) {
           uint8_t* v = smem + L::stage + (g % kStages) * L::kStage;
-          const int key = sid & 63;
-          if (!held || kb + key < un.kmin || kb + key >= un.kmax)
-            for (int c = sid >> 6; c < 2 * NB; c += 2)
+          // rows [0, below) and [above, 64), 16 bytes of a row a thread (eight threads a line)
+          const int below = held ? min(kPage, max(0, un.kmin - kb)) : kPage;
+          const int above = held ? max(below, min(kPage, un.kmax - kb)) : kPage;
+          const int out = below + kPage - above;
+#pragma unroll 1
+          for (int k = sid >> 3; k < out; k += 16) {
+            const int key = k < below ? k : k - below + above;
+            uint8_t* to = v + (key >> 3) * L::kRg + (key & 7) * 128 + (sid & 7) * 16;
 #pragma unroll
-              for (int k = 0; k < 8; ++k)
-                *reinterpret_cast<uint4*>(v + (key >> 3) * L::kRg + c * 1024 + (key & 7) * 128 + k * 16) =
-                    make_uint4(0u, 0u, 0u, 0u);
+            for (int c = 0; c < 2 * NB; ++c) *reinterpret_cast<uint4*>(to + c * 1024) = make_uint4(0u, 0u, 0u, 0u);
+          }
         }
         fence_proxy_async_smem();
         tc_fence_before();
@@ -683,34 +718,58 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       named_barrier_sync(kSoftBar, 128);
-      // a lane holds one number of every row: 64 bytes (or 128) of a row a store
       uint32_t odd = 0u;  // bits 15 and 31: an element is not finite
+      if (direct) {
+        // Numbers lane / 4 (+ 8, 16, 24) of two rows a thread, packed and transposed in blocks of
+        // eight rows and eight numbers; then four lanes trade their pieces, so that each stores
+        // 16 bytes of a row: 64 bytes of eight rows a store.
 #pragma unroll 1
-      for (int c = 0; c < NB * N; c += kEnd) {
-        const int mb = c / N, c0 = c % N, dim = mb * 128 + qt * 32 + lane;
-        if (c0 >= nrows) continue;
-        uint32_t v[kEnd];
-        if constexpr (kEnd == 32) tmem_ld32(tmem + lanes + c, v);
-        else tmem_ld16(tmem + lanes + c, v);
-        tmem_ld_wait();
-        const bool whole = c0 + kEnd <= nrows;
-        if (direct) {
-          uint16_t* o = p.out + static_cast<size_t>(rowbase + c0) * C + dim;
+        for (int mb = 0; mb < NB; ++mb) {
+#pragma unroll 1
+          for (int c0 = 0; c0 < N && c0 < nrows; c0 += 8) {
+            uint32_t v[4], w[4], m[4];
+            tmem_ld_16x256b(tmem + lanes + mb * N + c0, v);
+            tmem_ld_16x256b(tmem + lanes + (16u << 16) + mb * N + c0, w);
+            tmem_ld_wait();
+            const float f0 = s_alpha[c0 + ca], f1 = s_alpha[c0 + ca + 1];
+            auto piece = [&](uint32_t x, uint32_t y) {
+              return movmatrix_trans(pack_bf16x2(f0 == 0.f ? 0.f : __uint_as_float(x) * f0, f1 == 0.f ? 0.f : __uint_as_float(y) * f1));
+            };
+            m[0] = piece(v[0], v[1]);
+            m[1] = piece(v[2], v[3]);
+            m[2] = piece(w[0], w[1]);
+            m[3] = piece(w[2], w[3]);
 #pragma unroll
-          for (int k = 0; k < kEnd; k += 2) {
-            const float f0 = s_alpha[c0 + k], f1 = s_alpha[c0 + k + 1];
-            const uint32_t w = pack_bf16x2(f0 == 0.f ? 0.f : __uint_as_float(v[k]) * f0,
-                                           f1 == 0.f ? 0.f : __uint_as_float(v[k + 1]) * f1);
-            if (whole || c0 + k < nrows) {
-              o[k * C] = static_cast<uint16_t>(w);
-              odd |= (w & 0x7F80u) + 0x0080u;
+            for (int k = 0; k < 4; ++k) odd |= (m[k] & 0x7F807F80u) + 0x00800080u;
+            // lane l of four: piece l of each lane's four
+#pragma unroll
+            for (int s = 1; s < 4; s <<= 1) {
+              const bool up = (lane & s) != 0;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                if (k & s) continue;
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? m[k] : m[k | s], s);
+                if (up) m[k] = got;
+                else m[k | s] = got;
+              }
             }
-            if (whole || c0 + k + 1 < nrows) {
-              o[(k + 1) * C] = static_cast<uint16_t>(w >> 16);
-              odd |= (w & 0x7F800000u) + 0x00800000u;
-            }
+            const int rr = c0 + (lane >> 2);
+            if (rr < nrows)
+              *reinterpret_cast<uint4*>(p.out + static_cast<size_t>(rowbase + rr) * C + mb * 128 + qt * 32 + (lane & 3) * 8) =
+                  make_uint4(m[0], m[1], m[2], m[3]);
           }
-        } else {
+        }
+      } else {
+        // a lane holds one number of every row: 128 bytes of a row a store
+#pragma unroll 1
+        for (int c = 0; c < NB * N; c += kEnd) {
+          const int mb = c / N, c0 = c % N, dim = mb * 128 + qt * 32 + lane;
+          if (c0 >= nrows) continue;
+          uint32_t v[kEnd];
+          if constexpr (kEnd == 32) tmem_ld32(tmem + lanes + c, v);
+          else tmem_ld16(tmem + lanes + c, v);
+          tmem_ld_wait();
+          const bool whole = c0 + kEnd <= nrows;
           float* o = p.o + (slot + c0) * C + dim;
 #pragma unroll
           for (int k = 0; k < kEnd; ++k) {
@@ -739,8 +798,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (!__any_sync(0xffffffffu, bad)) continue;
           float acc[NB];
-          attend_column<NB>(p, p.q + static_cast<size_t>(rowbase + rr) * w, trow, max(row_lo[rr], seg_lo),
-                            min(row_hi[rr], seg_hi), s_ref[rr], qt * 32 + lane, acc);
+          attend_column<NB>(p, p.q + static_cast<size_t>(rowbase + rr) * w, trow, max(row_keys[rr].x, seg_lo),
+                            min(row_keys[rr].y, seg_hi), s_ref[rr], qt * 32 + lane, acc);
 #pragma unroll
           for (int mb = 0; mb < NB; ++mb) {
             const int dim = mb * 128 + qt * 32 + lane;
