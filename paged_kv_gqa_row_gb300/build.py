@@ -21,8 +21,8 @@ NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr
 
 LIBS = {
     "lnk": {
-        "sources": [os.path.join(CSRC, f) for f in ("api.cu", "append_rope.cu", "append4.cu", "decode.cu", "decode4.cu", "chunk.cu", "chunk4.cu", "decode_static.cu", "pages.cu", "read_tokens.cu", "latent_api.cu", "latent_append.cu", "latent_attn.cu", "latent_prompt.cu", "selftest.cu", "pager.cpp")],
-        "headers": [os.path.join(CSRC, f) for f in ("common.cuh", "decode_plan.cuh", "latent.cuh", "ptx.cuh", "rope_math.cuh")] + [os.path.join(INCLUDE, "lnk.h")],
+        "sources": [os.path.join(CSRC, f) for f in ("api.cu", "append_rope.cu", "append4.cu", "decode.cu", "decode4.cu", "chunk.cu", "chunk4.cu", "decode_static.cu", "pages.cu", "read_tokens.cu", "latent_api.cu", "latent_append.cu", "latent_attn.cu", "latent_join.cu", "latent_pair.cu", "latent_prompt.cu", "selftest.cu", "pager.cpp")],
+        "headers": [os.path.join(CSRC, f) for f in ("common.cuh", "decode_plan.cuh", "latent.cuh", "latent_units.cuh", "ptx.cuh", "rope_math.cuh")] + [os.path.join(INCLUDE, "lnk.h")],
         "out": os.path.join(PKG, "liblnk.so"),
     },
     "synth": {

@@ -27,15 +27,15 @@ struct LatentParams {
   uint16_t* out;                   // [T][H][C]
   int32_t* status;
   LatentCut* cuts;                 // [teams]
-  float* ml;                       // [2 * CTAs][kLatentRows][2]: reference (log2 units), sum
-  float* o;                        // [2 * CTAs][kLatentRows][C]: unnormalised partial outputs
+  float* ml;                       // [2 * teams * head blocks][slot rows][2]: reference (log2 units), sum
+  float* o;                        // [2 * teams * head blocks][slot rows][C]: unnormalised partial outputs
   int P, T, heads, latent_dim, rope_dim, num_pages, num_rows, pages_per_row, window;
-  int tile_rows;                   // query rows a tile (64, 32 or 16)
+  int tile_rows;                   // query rows a tile (128: on pairs of SMs; 64, 32 or 16)
+  int slot_rows;                   // rows of a partial sum in the workspace
   int tile_tokens;                 // prompt tokens a tile at most
   int head_blocks;                 // tiles a token (heads > tile_rows)
-  int teams;                       // groups of head_blocks CTAs that share the stream
+  int teams;                       // groups of head_blocks CTAs (or pairs) that share the stream
   int whole;                       // no unit is cut (all have few pages)
-  int ahead;                       // pages asked into L2 before they are loaded
   float scale_log2;
 };
 
@@ -43,6 +43,15 @@ struct LatentParams {
 // keys, or of 8 and without the rotated part where that has 32 numbers; rmap: that part.
 cudaError_t launch_latent_attn(const CUtensorMap& qmap, const CUtensorMap& pmap, const CUtensorMap& rmap,
                                const LatentParams& p, cudaStream_t stream);
+
+// The same with tiles of 128 rows on pairs of SMs.  qmap: boxes of 64 rows; kmap: the pool as
+// [8 keys][64 numbers] blocks, boxes of 32 keys (with a rotated part of 32: of 8 keys, without
+// it, and rmap that part); vmap: boxes of 64 keys and half of a latent.
+cudaError_t launch_latent_pair(const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                               const CUtensorMap& rmap, const LatentParams& p, cudaStream_t stream);
+
+// Joins the partial sums that either of them left.
+cudaError_t launch_latent_join(const LatentParams& p, cudaStream_t stream);
 
 struct LatentAppendParams {
   const uint16_t* q;        // [T][H] rotated parts, q_stride elements from head to head

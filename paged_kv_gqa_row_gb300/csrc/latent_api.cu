@@ -92,35 +92,41 @@ lnk_status attend(const lnk_latent_desc* desc, const lnk_bf16* q, const int32_t*
   p.num_rows = desc->num_rows;
   p.pages_per_row = desc->pages_per_row;
   p.window = desc->window;
-  // decode rows alone never share a tile: no more rows than heads need; prompt tokens fill it
-  p.tile_rows = P > 0 || p.heads > 32 ? 64 : (p.heads > 16 ? 32 : 16);
+  // Tiles of 128 rows on pairs of SMs for more heads than 64, and where prompt tokens fill two
+  // such tiles a pair; else of 64 (decode rows alone never share a tile: no more rows than
+  // heads need).
+  const bool pairs = p.heads > kLatentRows || static_cast<long long>(P) * p.heads >= 2ll * sms * kLatentRows;
+  p.tile_rows = pairs ? 2 * kLatentRows : (P > 0 || p.heads > 32 ? 64 : (p.heads > 16 ? 32 : 16));
+  p.slot_rows = std::max(kLatentRows, p.tile_rows);
   p.tile_tokens = std::max(1, p.tile_rows / p.heads);
   p.head_blocks = (p.heads + p.tile_rows - 1) / p.tile_rows;
-  if (p.head_blocks > sms) return LNK_ERANGE;
-  p.teams = sms / p.head_blocks;
+  p.teams = (pairs ? sms / 2 : sms) / p.head_blocks;
+  if (p.teams <= 0) return LNK_ERANGE;
   long long most = p.pages_per_row;  // pages of a token
   if (p.window > 0) most = std::min<long long>(most, (p.window - 1) / kPage + 2);
   p.whole = most <= kWholePages;
-  p.ahead = 0;
   p.scale_log2 = latent_scale_log2(desc);
 
   const long long width = desc->latent_dim + desc->rope_dim;
   const long long qdims[2] = {width, static_cast<long long>(p.T) * p.heads};
-  const long long pdims[4] = {kBoxCols, 8, width / kBoxCols, static_cast<long long>(p.num_pages) * kPage / 8};
+  const long long keys8 = static_cast<long long>(p.num_pages) * kPage / 8;
+  const long long pdims[4] = {kBoxCols, 8, width / kBoxCols, keys8};
   const long long rdims[2] = {width, static_cast<long long>(p.num_pages) * kPage};
   const long long strides[2] = {1, width}, pstrides[4] = {1, width, kBoxCols, 8 * width};
-  const int qbox[2] = {kBoxCols, p.tile_rows}, rbox[2] = {kBoxCols, 8};
-  const int pbox[4] = {kBoxCols, 8, static_cast<int>(width / kBoxCols), p.rope_dim == 64 ? 2 : 1};
-  CUtensorMap qmap, pmap, rmap;
+  // with a rotated part of 32 numbers a row is no multiple of 64: that part has copies of its own
+  const bool r64 = p.rope_dim == 64;
+  const int qbox[2] = {kBoxCols, std::min(p.tile_rows, kLatentRows)}, rbox[2] = {kBoxCols, 8};
+  const int pbox[4] = {kBoxCols, 8, static_cast<int>(width / kBoxCols), r64 ? (pairs ? 4 : 2) : 1};
+  const int vbox[4] = {kBoxCols, 8, p.latent_dim / 2 / kBoxCols, 8};
+  CUtensorMap qmap, pmap, vmap, rmap;
   if (!bf16_tensor_map(&qmap, q, 2, qdims, strides, qbox) || !bf16_tensor_map(&pmap, pool, 4, pdims, pstrides, pbox))
     return LNK_ECUDA;
-  if (p.rope_dim == 32) {
-    if (!bf16_tensor_map(&rmap, pool, 2, rdims, strides, rbox)) return LNK_ECUDA;
-  } else {
-    rmap = pmap;  // (not used)
-  }
-  return launch_latent_attn(qmap, pmap, rmap, p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? LNK_OK
-                                                                                                       : LNK_ECUDA;
+  if (r64) rmap = pmap;  // (not used)
+  else if (!bf16_tensor_map(&rmap, pool, 2, rdims, strides, rbox)) return LNK_ECUDA;
+  if (pairs && !bf16_tensor_map(&vmap, pool, 4, pdims, pstrides, vbox)) return LNK_ECUDA;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t err = pairs ? launch_latent_pair(qmap, pmap, vmap, rmap, p, s) : launch_latent_attn(qmap, pmap, rmap, p, s);
+  return err == cudaSuccess ? LNK_OK : LNK_ECUDA;
 }
 
 }  // namespace

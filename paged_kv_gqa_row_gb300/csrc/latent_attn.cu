@@ -14,10 +14,10 @@
 // A page therefore lies in shared memory once, as keys and as values: [8 keys][64 numbers]
 // of 1 KB each, so that what a copy of 16 keys reads is contiguous in the pool.
 //
-// One persistent CTA an SM.  The pages of all tiles, laid end to end, are one stream
-// that the CTAs cut into equal shares (heads beyond 64: teams of CTAs, one for 64 heads
-// each, take the same share, so that the pages come from HBM once); a tile that is cut
-// leaves unnormalised sums in the workspace, which a second kernel joins.
+// One persistent CTA an SM, each with a share of the stream of pages (latent_units.cuh); a
+// tile that is cut leaves unnormalised sums in the workspace, which a second kernel joins.
+// More than 64 rows of one token, and large launches of prompt tokens, take tiles of 128
+// rows on pairs of SMs (latent_pair.cu).
 //
 // Softmax: P = 2^(s scale log2(e) - ref).  P is rounded to bf16 and summed in float32,
 // whose relative precision does not depend on the reference, so that need not be the
@@ -32,7 +32,7 @@
 // would reach all of them through 0 * NaN.  Key rows that no token of the tile sees are
 // zeroed before they are values; a row whose output is not finite while its sum is
 // computes again from its own keys (attend_column).
-#include "latent.cuh"
+#include "latent_units.cuh"
 #include "ptx.cuh"
 
 namespace lnk {
@@ -40,7 +40,6 @@ namespace {
 
 constexpr int kThreads = 192;
 constexpr float kRaiseLog2 = 32.f;
-constexpr int kWholePages = 8;
 constexpr int kSoftBar = 1;  // named barrier of the softmax warps
 
 template <int NB, int N>
@@ -73,74 +72,6 @@ struct LatentSmem {
   static constexpr uint32_t kCols = NB * N + 2 * N <= 64 ? 64 : NB * N + 2 * N <= 128 ? 128
                                   : NB * N + 2 * N <= 256 ? 256 : 512;
 };
-
-struct Share {
-  int t, j;                 // first unit (its first token) and page in it
-  unsigned long long left;  // pages
-};
-
-struct Unit {
-  int nt, row;        // tokens; table row (-1: nothing to see)
-  int kmin, kmax;     // keys that some token sees
-  int in_lo, in_hi;   // keys that every token sees
-  int first, np;      // first page; pages (one at least)
-};
-
-__device__ __forceinline__ int token_keys(const LatentParams& p, int t, int& row, int& lo, int& hi) {
-  int pos;
-  if (t < p.P) {
-    row = p.rows[t];
-    pos = p.positions[t];
-  } else {
-    row = t - p.P;
-    pos = p.step_positions[t - p.P];
-  }
-  lo = hi = 0;
-  if (pos < 0) return 0;
-  if (row < 0 || row >= p.num_rows) return LNK_DEV_BAD_ROW;
-  if (pos >= p.pages_per_row * kPage) return LNK_DEV_BAD_POSITION;
-  lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
-  hi = pos + 1;
-  return 0;
-}
-
-__device__ __forceinline__ bool unit_starts(const LatentParams& p, int t) {
-  return t >= p.P || p.tile_tokens == 1 || t % p.tile_tokens == 0 || p.rows[t] != p.rows[t - 1];
-}
-
-__device__ __forceinline__ Unit unit_at(const LatentParams& p, int t) {
-  Unit u;
-  u.nt = 0;
-  u.row = -1;
-  u.kmin = 0x7fffffff;
-  u.kmax = 0;
-  u.in_lo = 0;
-  u.in_hi = 0x7fffffff;
-  const int end = t < p.P ? min(p.P, (t / p.tile_tokens + 1) * p.tile_tokens) : t + 1;
-  int row0 = 0;
-  for (int s = t; s < end; ++s) {
-    int row, lo, hi;
-    token_keys(p, s, row, lo, hi);
-    if (s == t) row0 = row;
-    else if (row != row0) break;
-    ++u.nt;
-    u.in_lo = max(u.in_lo, lo);
-    u.in_hi = min(u.in_hi, hi);
-    if (hi > lo) {
-      u.row = row;
-      u.kmin = min(u.kmin, lo);
-      u.kmax = max(u.kmax, hi);
-    }
-  }
-  if (u.row < 0) u.kmin = 0;
-  u.first = u.kmin / kPage;
-  u.np = u.row < 0 ? 1 : (u.kmax - 1) / kPage - u.first + 1;
-  return u;
-}
-
-__device__ __forceinline__ float bf16_at(const uint16_t* x) {
-  return __uint_as_float(static_cast<uint32_t>(*x) << 16);
-}
 
 // One row's sums over its own visible keys [lo, hi), relative to the reference that the
 // tile's softmax used, key by key: element 128 mb + d of the row in acc[mb].  The whole warp.
@@ -187,111 +118,36 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* s_ref = reinterpret_cast<float*>(smem + L::ref);
   int* misc = reinterpret_cast<int*>(smem + L::misc);
   volatile int* abort_flag = misc;
-  long long* scan = reinterpret_cast<long long*>(misc + 4);  // [7]: sums of the warps before, and the total
-  Share* share = reinterpret_cast<Share*>(misc + 20);
 
   // the joining kernel may start: it waits for this grid's end
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-  const int team = blockIdx.x / p.head_blocks, hb = blockIdx.x % p.head_blocks;
+  const int team = blockIdx.x;
 
   if (tid == 0) {
     for (int i = 0; i < L::kNumBars; ++i) mbar_init(full + 8 * i, 1);
     for (int i = 0; i < kStages; ++i) mbar_init(full + 8 * i, kGroups);
     mbar_init(pfull, 4);
     *abort_flag = 0;
-    share->t = 0x7fffffff;
-    share->j = 0;
-    share->left = 0ull;
     fence_mbarrier_init();
   }
   if (warp == 1) tmem_alloc(smem_addr(misc + 1), L::kCols);
 
-  // ---- this team's share of the stream: the units' pages counted by all threads, each
-  // thread a range of tokens (positions, rows and the table are read before the wait
-  // for the kernel before this one) ----
-  const int T = p.T;
-  const int span = (T + kThreads - 1) / kThreads;
-  const int ta = min(T, tid * span), tb = min(T, ta + span);
-  int bad = 0, most = 0;
-  long long mine = 0;
-  for (int t = ta; t < tb; ++t) {
-    int row, lo, hi;
-    bad |= token_keys(p, t, row, lo, hi);
-    if (unit_starts(p, t)) {
-      const int np = unit_at(p, t).np;
-      mine += np;
-      most = max(most, np);
-    }
-  }
-  most = __reduce_max_sync(0xffffffffu, most);
-  long long before = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, before, o);
-    if (lane >= o) before += x;
-  }
-  if (lane == 31) scan[warp] = before;
-  if (lane == 0) misc[28 + warp] = most;
-  __syncthreads();
-  long long total = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) before += scan[w];
-    total += scan[w];
-    most = max(most, misc[28 + w]);
-  }
-  before -= mine;
-  const long long per = max(1ll, (total + p.teams - 1) / p.teams);
-  const long long start = team * per;
-  // Units of few pages (or far fewer than a share) stay whole: a team takes those whose first
-  // page lies in its share.
-  const bool whole = p.whole || most <= max(static_cast<long long>(kWholePages), per / 8);
-  if (before < start + per && before + mine > start) {
-    long long at = before;
-    for (int t = ta; t < tb && at < start + per; ++t) {
-      if (!unit_starts(p, t)) continue;
-      const int np = unit_at(p, t).np;
-      if (whole) {
-        if (at >= start) {
-          atomicMin(&share->t, t);
-          atomicAdd(&share->left, static_cast<unsigned long long>(np));
-        }
-      } else if (at <= start && start < at + np) {
-        share->t = t;
-        share->j = static_cast<int>(start - at);
-        share->left = static_cast<unsigned long long>(min(per, total - start));
-        break;
-      }
-      at += np;
-    }
-  }
+  // positions, rows and the table are read before the wait for the kernel before this one
+  const Shares shares = count_shares<kThreads>(p, team, misc + 4);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(misc[1]));
+  const Share* share = share_of(misc + 4);
   int t = share->t, j0 = share->j;
   long long left = static_cast<long long>(share->left);
 
   // what the kernel before this one on the stream writes is touched from here on
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (bad && blockIdx.x == 0 && p.status != nullptr) atomicOr(p.status, bad);
-  if (tid == 0 && hb == 0 && !p.whole) {
-    LatentCut cut;
-    cut.t0 = t;
-    cut.nt = cut.np = 0;
-    cut.j0 = left > 0 ? j0 : 0;
-    cut.per = per;
-    cut.pad = 0;
-    if (cut.j0 > 0) {
-      const Unit u = unit_at(p, t);
-      cut.nt = u.nt;
-      cut.np = u.np;
-    }
-    p.cuts[team] = cut;
-  }
-  // the tile's query rows: from row `t * heads + hb * N` of q on, as many as the unit has
+  if (shares.bad && blockIdx.x == 0 && p.status != nullptr) atomicOr(p.status, shares.bad);
+  if (tid == 0 && !p.whole) write_cut(p, team, t, left > 0 ? j0 : 0, shares.per);
   if (warp == 0) {
     // ============================== producer ==============================
     if (lane == 0) {
@@ -300,32 +156,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto load_q = [&](int t) {
         mbar_arrive_expect_tx(qfull, L::kQ);
         for (int c = 0; c < L::kChunks; ++c)
-          tma_load_2d(smem_addr(smem + L::q) + c * (N * 128), &qmap, c * kBoxCols, t * p.heads + hb * N, qfull);
+          tma_load_2d(smem_addr(smem + L::q) + c * (N * 128), &qmap, c * kBoxCols, t * p.heads, qfull);
         ++units;
-      };
-      // Pages asked into L2 before there is room for them in shared memory (LatentParams.ahead).
-      int at = t, aj = j0, an = 0, ant = 0, afirst = 0, ahead = 0;
-      long long aleft = left;
-      const int32_t* arow = nullptr;
-      auto prefetch = [&]() {
-        if (aleft <= 0 || hb != 0 || p.ahead == 0) return;
-        if (arow == nullptr) {
-          const Unit x = unit_at(p, at);
-          arow = p.table + static_cast<long long>(max(x.row, 0)) * p.pages_per_row + x.first;
-          an = x.row >= 0 ? x.np : 0;
-          ant = x.nt;
-          afirst = x.np;
-        }
-        const int page = aj < an ? arow[aj] : -1;
-        if (page >= 0 && page < p.num_pages)
-          bulk_prefetch_l2(p.pool + static_cast<size_t>(page) * kPage * (p.latent_dim + p.rope_dim),
-                           kPage * (p.latent_dim + p.rope_dim) * 2);
-        --aleft;
-        if (++aj >= afirst) {
-          at += ant;
-          aj = 0;
-          arow = nullptr;
-        }
       };
       if (left > 0) load_q(t);
       for (int u = 0; ok && left > 0; ++u) {
@@ -335,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; ok && i < n; ++i, ++g) {
           int page = un.row >= 0 ? trow[i] : 0;
           if (page < 0 || page >= p.num_pages) {
-            if (hb == 0 && p.status != nullptr) atomicOr(p.status, LNK_DEV_BAD_PAGE);
+            if (p.status != nullptr) atomicOr(p.status, LNK_DEV_BAD_PAGE);
             page = 0;  // (its keys are masked and its values zeroed)
           }
           const int st = g % kStages;
@@ -355,7 +187,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             ++issued;
           }
-          for (; ahead < g + 2 + p.ahead; ++ahead) prefetch();
           if (ok && i == 0 && u > 0) {
             ok = mbar_wait(qempty, (u - 1) & 1, abort_flag);
             if (ok) load_q(t);
@@ -494,14 +325,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (ok && left > 0) {
       const Unit un = unit_at(p, t);
       const int n = static_cast<int>(min(left, static_cast<long long>(un.np - j0)));
-      const int nrows = min(N, un.nt * p.heads - hb * N);
-      const int rowbase = t * p.heads + hb * N;
+      const int nrows = un.nt * p.heads;  // at most N
+      const int rowbase = t * p.heads;
       const bool direct = j0 == 0 && n == un.np;
       named_barrier_sync(kSoftBar, 128);  // (the unit before is done with the rows' data)
       // keys that each row sees (rows past the unit's: everything, nobody reads them)
       if (sid < N) {
         int lo = 0, hi = 0x7fffffff, row;
-        if (sid < nrows) token_keys(p, t + (hb * N + sid) / p.heads, row, lo, hi);
+        if (sid < nrows) token_keys(p, t + sid / p.heads, row, lo, hi);
         row_keys[sid] = make_int2(lo, hi);
         s_ref[sid] = -INFINITY;  // the score of the row's first key, once it is known
       }
@@ -708,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (sid < 4) s_ref[8 * (x >> 1) + ca + (x & 1)] = nref[x];
       }
       named_barrier_sync(kSoftBar, 128);
-      const size_t slot = direct ? 0 : (static_cast<size_t>(2 * team + (j0 == 0 ? 1 : 0)) * p.head_blocks + hb) * kLatentRows;
+      const size_t slot = direct ? 0 : static_cast<size_t>(2 * team + (j0 == 0 ? 1 : 0)) * p.slot_rows;
       if (sid < N) {
         const float s = (scratch[sid] + scratch[N + sid]) + (scratch[2 * N + sid] + scratch[3 * N + sid]);
         s_alpha[sid] = direct ? (s > 0.f ? 1.f / s : s) : (s == s ? 1.f : s);
@@ -826,100 +657,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_dealloc(tmem, L::kCols);
 }
 
-// Joins the partial sums of the units that the shares cut.  The blocks of all shares that
-// start inside one unit (kJoinBlocks each) divide its rows by 128 numbers of a row: a warp
-// takes such an item where the unit has up to kFewParts parts (every part's numbers are
-// asked for before its weight is known), else a whole block, its warps the parts in turn.
-// (What it takes is latency, and cold instruction caches: the end of the first kernel to
-// the end of this one, 64 rows of 32 heads, 13 us with a list of the units and a warp a row.)
-constexpr int kJoinThreads = 256;
-constexpr int kJoinBlocks = 8;
-constexpr int kFewParts = 8;
-
-__device__ __forceinline__ void add_part(float4& acc, float f, const float4& x) {
-  acc.x = fmaf(f, x.x, acc.x);
-  acc.y = fmaf(f, x.y, acc.y);
-  acc.z = fmaf(f, x.z, acc.z);
-  acc.w = fmaf(f, x.w, acc.w);
-}
-
-// A part's weight 2^(its reference - the largest) (none has seen a key: 0)
-__device__ __forceinline__ float part_weight(float mk, float m) { return mk == -INFINITY && m == -INFINITY ? 0.f : ex2_approx(mk - m); }
-
-__global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const __grid_constant__ LatentParams p) {
-  __shared__ float4 s_acc[kJoinThreads];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, C = p.latent_dim;
-  const int share = blockIdx.x / kJoinBlocks;
-  const LatentCut cut = p.cuts[share];
-  if (cut.j0 == 0) return;
-  const long long p0 = share * cut.per - cut.j0;                     // the unit's first page in the stream
-  const int c0 = static_cast<int>(p0 / cut.per) + 1;                 // first share that starts inside the unit
-  const int cl = static_cast<int>((p0 + cut.np - 1) / cut.per);      // and the last
-  const int parts = cl - c0 + 2;                                     // shares c0 - 1 .. cl
-  const int nb = C / 128, items = cut.nt * p.heads * nb;
-  const int blocks = (cl - c0 + 1) * kJoinBlocks, block = (share - c0) * kJoinBlocks + blockIdx.x % kJoinBlocks;
-  const bool few = parts <= kFewParts;
-  const int step = few ? blocks * (kJoinThreads / 32) : blocks;
-  for (int i = few ? block * (kJoinThreads / 32) + warp : block; i < items; i += step) {
-    const int r = i / nb, d = i % nb * 128 + lane * 4;
-    const int hb = r / p.tile_rows, col = r % p.tile_rows;
-    auto slot = [&](int k) {
-      return (static_cast<size_t>(2 * (c0 - 1 + k) + (k == 0 ? 1 : 0)) * p.head_blocks + hb) * kLatentRows + col;
-    };
-    float4 x[kFewParts];
-    if (few) {
-#pragma unroll
-      for (int k = 0; k < kFewParts; ++k)
-        if (k < parts) x[k] = *reinterpret_cast<const float4*>(p.o + slot(k) * C + d);
-    }
-    float m = -INFINITY, l = 0.f;
-    float2 ml = make_float2(-INFINITY, 0.f);
-    for (int k = lane; k < parts; k += 32) {
-      ml = *reinterpret_cast<const float2*>(p.ml + slot(k) * 2);
-      m = fmaxf(m, ml.x);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    for (int k = lane; k < parts; k += 32) {
-      if (!few) ml = *reinterpret_cast<const float2*>(p.ml + slot(k) * 2);
-      const float f = part_weight(ml.x, m);
-      l += f == 0.f && ml.y == ml.y ? 0.f : f * ml.y;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    const float inv = l > 0.f ? 1.f / l : l;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (few) {
-#pragma unroll
-      for (int k = 0; k < kFewParts; ++k)
-        if (k < parts) add_part(acc, part_weight(__shfl_sync(0xffffffffu, ml.x, k), m), x[k]);
-    } else {
-#pragma unroll 4
-      for (int k = warp; k < parts; k += kJoinThreads / 32)
-        add_part(acc, part_weight(p.ml[slot(k) * 2], m), *reinterpret_cast<const float4*>(p.o + slot(k) * C + d));
-      s_acc[tid] = acc;
-      __syncthreads();
-      if (warp == 0) {
-#pragma unroll
-        for (int w = 1; w < kJoinThreads / 32; ++w) add_part(acc, 1.f, s_acc[w * 32 + lane]);
-      }
-      __syncthreads();
-    }
-    if (few || warp == 0)
-      *reinterpret_cast<uint2*>(p.out + (static_cast<size_t>(cut.t0) * p.heads + r) * C + d) =
-          make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-  }
-}
-
 template <int NB, int N>
 cudaError_t launch_t(const CUtensorMap& qmap, const CUtensorMap& pmap, const CUtensorMap& rmap, const LatentParams& p, cudaStream_t stream) {
   const int bytes = static_cast<int>(LatentSmem<NB, N>::bytes);
   cudaError_t err = set_max_dynamic_smem(reinterpret_cast<const void*>(latent_kernel<NB, N>), bytes);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.teams * p.head_blocks));
+  cfg.gridDim = dim3(static_cast<unsigned>(p.teams));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = stream;
@@ -930,11 +674,7 @@ cudaError_t launch_t(const CUtensorMap& qmap, const CUtensorMap& pmap, const CUt
   cfg.numAttrs = 1;
   err = cudaLaunchKernelEx(&cfg, latent_kernel<NB, N>, qmap, pmap, rmap, p);
   if (err != cudaSuccess) return err;
-  if (p.whole) return cudaSuccess;  // (no unit is cut)
-  cfg.gridDim = dim3(static_cast<unsigned>(kJoinBlocks * p.teams));
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, latent_join_kernel, p);
+  return launch_latent_join(p, stream);
 }
 
 }  // namespace

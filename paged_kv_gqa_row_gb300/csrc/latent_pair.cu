@@ -1,0 +1,655 @@
+// Attention over a paged latent cache in tiles of 128 query rows, for tokens of more than 64
+// heads and for launches of many prompt tokens (what it computes and how the pages are
+// shared out: latent_attn.cu).
+//
+// A pair of SMs takes a tile as 2-SM products of M = 128 rows: CTA r of the pair holds rows
+// 64 r .. 64 r + 63 in its tensor memory, where 128 lanes are the 64 rows twice, the second
+// time for the second half of the columns.  Per page of 64 keys
+//   S[128 x 64]  = Q K^T   K: CTA r holds keys 32 r .. + 31, all numbers, K-major;
+//   O[128 x C]  += P V     V: CTA r holds all 64 keys, half r of the latent, MN-major;
+// so a page is copied 1.9 times into the pair's shared memory, and a row's 512 values take
+// 256 columns (with all rows on one SM they would fill tensor memory).  Keys and values have
+// rings of their own: keys leave after Q.K^T, values after P.V a softmax later.
+// (The one-SM kernel reads a page and multiplies it for 64 rows in 2550 clocks at best, on
+// each of two SMs for 128 rows; these products take 1610 for the pair: operands of a 2-SM
+// product are read from both shared memories at once.)
+//
+// Warps: 0 loads keys and query rows, 2 values (each CTA its own); 1 issues the products in
+// rank 0 and tells rank 0 of rank 1's keys and queries in rank 1, where warp 3 does so for
+// values; 4-7 softmax: thread L owns row L % 64 of its CTA and keys 32 (L / 64) .. + 31 of a page,
+// and that row's half L / 64 of O.
+#include "latent_units.cuh"
+#include "ptx.cuh"
+
+namespace lnk {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kRows = 64;          // rows of a CTA
+constexpr float kRaiseLog2 = 32.f;
+constexpr int kSoftBar = 1;
+
+template <int NB>
+struct PairSmem {
+  static constexpr int kChunks = 2 * NB + 1;              // 64 numbers of a row each; the last: the rotated ones
+  static constexpr int kRg = kChunks * 1024;              // eight keys
+  static constexpr int kK = 4 * kRg;                      // a page's keys of this CTA
+  static constexpr int kVRg = NB * 1024;                  // eight keys' values, this CTA's half
+  static constexpr int kV = 8 * kVRg;
+  static constexpr int kQ = kChunks * kRows * 128;
+  static constexpr int kP = kRows * 128;
+  static constexpr int kMisc = 2048;
+  static constexpr int kBudget = 232448 - 1024 - kMisc - kQ - kP;
+  static constexpr int kStages = kBudget / (kK + kV) < 4 ? kBudget / (kK + kV) : 4;
+  static constexpr size_t k = 0;
+  static constexpr size_t v = k + size_t(kStages) * kK;
+  static constexpr size_t q = v + size_t(kStages) * kV;
+  static constexpr size_t p = q + kQ;
+  static constexpr size_t bars = p + kP;
+  // kfull, kempty, vfull, vempty [stages], sfull[2], pfull, pvdone, qfull, qempty, fin
+  static constexpr int kNumBars = 4 * kStages + 7;
+  static constexpr size_t ref = bars + 8 * kNumBars;      // [64] a row's first score; in a raise the maxima
+  static constexpr size_t pair = ref + 4 * kRows;         // [2][64] what a row's two threads tell each other
+  static constexpr size_t misc = pair + 8 * kRows;        // abort, tensor memory, share
+  static constexpr size_t end = misc + 256;
+  static_assert(end - bars <= kMisc, "barriers and row data");
+  static_assert(kStages >= 2, "stages");
+  static constexpr size_t bytes = bars + kMisc + 1024;
+  static constexpr uint32_t kColS = NB * 64;              // after O
+  static constexpr uint32_t kCols = NB * 64 + 64 <= 128 ? 128 : NB * 64 + 64 <= 256 ? 256 : 512;
+};
+
+__device__ __forceinline__ void drain(uint32_t bar, int parity) {
+  const uint64_t t_0 = global_timer_ns();
+  while (!mbar_try_wait(bar, parity) && global_timer_ns() - t_0 < kWaitLimitNs) {
+  }
+}
+
+// Eight lanes of neighbouring rows hold eight 16-byte pieces of their row each: afterwards
+// lane i holds piece i of each of the rows, so that a store covers whole lines.
+__device__ __forceinline__ void transpose_pieces(uint4 (&w)[8]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int b = 1; b < 8; b <<= 1) {
+    const bool up = (lane & b) != 0;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      if (c & b) continue;
+      const uint4 give = up ? w[c] : w[c | b];
+      uint4 got;
+      got.x = __shfl_xor_sync(0xffffffffu, give.x, b);
+      got.y = __shfl_xor_sync(0xffffffffu, give.y, b);
+      got.z = __shfl_xor_sync(0xffffffffu, give.z, b);
+      got.w = __shfl_xor_sync(0xffffffffu, give.w, b);
+      if (up) w[c] = got;
+      else w[c | b] = got;
+    }
+  }
+}
+
+// One row's sums over its own visible keys [lo, hi), relative to the reference that its softmax
+// used: numbers d0 + lane + 32 i of the latent in acc[i].  The whole warp.
+template <int NB>
+__device__ __noinline__ void attend_half(const LatentParams& p, const uint16_t* q, const int32_t* trow, int lo, int hi,
+                                         float nref, int d0, float (&acc)[2 * NB]) {
+  const int w = p.latent_dim + p.rope_dim, lane = threadIdx.x & 31;
+#pragma unroll
+  for (int i = 0; i < 2 * NB; ++i) acc[i] = 0.f;
+#pragma unroll 1
+  for (int key = lo; key < hi; ++key) {
+    const int page = trow[key / kPage];
+    if (page < 0 || page >= p.num_pages) continue;
+    const uint16_t* k = p.pool + (static_cast<size_t>(page) * kPage + key % kPage) * w;
+    float s = 0.f;
+#pragma unroll 1
+    for (int e = lane; e < w; e += 32) s = fmaf(bf16_at(q + e), bf16_at(k + e), s);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    const float e = exp2f(fmaf(s, p.scale_log2, nref));
+#pragma unroll
+    for (int i = 0; i < 2 * NB; ++i) acc[i] = fmaf(e, bf16_at(k + d0 + lane + 32 * i), acc[i]);
+  }
+}
+
+template <int NB>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    pair_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap rmap,
+                const __grid_constant__ LatentParams p) {
+  using L = PairSmem<NB>;
+  constexpr int kStages = L::kStages;
+  constexpr int C = NB * 128;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t kfull = smem_addr(smem + L::bars);
+  const uint32_t kempty = kfull + 8 * kStages, vfull = kempty + 8 * kStages, vempty = vfull + 8 * kStages;
+  const uint32_t sfull = vempty + 8 * kStages;  // [2] scores of a page
+  const uint32_t pfull = sfull + 16;            // probabilities of a page (rank 0 only)
+  const uint32_t pvdone = pfull + 8, qfull = pvdone + 8, qempty = qfull + 8, fin = qempty + 8;
+  float* s_ref = reinterpret_cast<float*>(smem + L::ref);
+  float* s_pair = reinterpret_cast<float*>(smem + L::pair);
+  int* misc = reinterpret_cast<int*>(smem + L::misc);
+  volatile int* abort_flag = misc;
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  const int tid = threadIdx.x, warp = __reduce_max_sync(0xffffffffu, tid >> 5), lane = tid & 31;
+  const int rank = static_cast<int>(cluster_cta_rank());
+  const int team = static_cast<int>(blockIdx.x >> 1) / p.head_blocks, hb = static_cast<int>(blockIdx.x >> 1) % p.head_blocks;
+
+  if (tid == 0) {
+    // rank 0's full barriers also count the relay's arrival for rank 1's copy
+    const uint32_t copies = rank == 0 ? 2 : 1;
+    for (int i = 0; i < L::kNumBars; ++i) mbar_init(kfull + 8 * i, 1);
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(kfull + 8 * i, copies);
+      mbar_init(vfull + 8 * i, copies);
+    }
+    mbar_init(qfull, copies);
+    mbar_init(pfull, 8);  // the softmax warps of both CTAs
+    *abort_flag = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == 1) tmem2_alloc(smem_addr(misc + 1), L::kCols);
+  // positions, rows and the table are read before the wait for the kernel before this one
+  const Shares shares = count_shares<kThreads>(p, team, misc + 4);
+  // barriers initialised and tensor memory allocated in both CTAs before any
+  // thread of either uses them
+  tc_fence_before();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(misc[1]));
+  const Share* share = share_of(misc + 4);
+  int t = share->t, j0 = share->j;
+  long long left = static_cast<long long>(share->left);
+
+  // what the kernel before this one on the stream writes is touched from here on
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (shares.bad && blockIdx.x == 0 && p.status != nullptr) atomicOr(p.status, shares.bad);
+  if (tid == 0 && rank == 0 && hb == 0 && !p.whole) write_cut(p, team, t, left > 0 ? j0 : 0, shares.per);
+
+  // Walks the share: f(unit, its pages here, unit's number) for each of its units in turn.
+  auto units = [&](auto&& f) {
+    for (int u = 0; left > 0; ++u) {
+      const Unit un = unit_at(p, t);
+      const int n = static_cast<int>(min(left, static_cast<long long>(un.np - j0)));
+      if (!f(un, n, u)) break;
+      left -= n;
+      t += un.nt;
+      j0 = 0;
+    }
+  };
+  // The page of table entry `i` of a unit here, or page 0 for one that is not there (its keys are
+  // masked and its values zeroed).
+  auto page_of = [&](const Unit& un, int i, bool report) {
+    int page = un.row >= 0 ? p.table[static_cast<long long>(un.row) * p.pages_per_row + un.first + j0 + i] : 0;
+    if (page < 0 || page >= p.num_pages) {
+      if (report && hb == 0 && rank == 0 && p.status != nullptr) atomicOr(p.status, LNK_DEV_BAD_PAGE);
+      page = 0;
+    }
+    return page;
+  };
+
+  if (warp == 0) {
+    // ===================== producer of keys and queries =====================
+    if (lane == 0) {
+      int g = 0, asked = 0;  // pages; query tiles asked for
+      auto load_q = [&](int t) {
+        mbar_arrive_expect_tx(qfull, L::kQ);
+        for (int c = 0; c < L::kChunks; ++c)
+          tma_load_2d(smem_addr(smem + L::q) + c * (kRows * 128), &qmap, c * kBoxCols, t * p.heads + hb * 2 * kRows + rank * kRows,
+                      qfull);
+        ++asked;
+      };
+      if (left > 0) load_q(t);
+      units([&](const Unit& un, int n, int u) {
+        for (int i = 0; i < n; ++i, ++g) {
+          const int page = page_of(un, i, true);
+          const int st = g % kStages;
+          if (g >= kStages && !mbar_wait(kempty + 8 * st, ((g / kStages) - 1) & 1, abort_flag)) return false;
+          const uint32_t dst = smem_addr(smem + L::k) + st * L::kK, fb = kfull + 8 * st;
+          mbar_arrive_expect_tx(fb, L::kK);
+          if (p.rope_dim == 64) {
+            tma_load_4d(dst, &kmap, 0, 0, 0, page * 8 + rank * 4, fb);
+          } else {
+            for (int k = 0; k < 4; ++k) {
+              tma_load_4d(dst + k * L::kRg, &kmap, 0, 0, 0, page * 8 + rank * 4 + k, fb);
+              tma_load_2d(dst + k * L::kRg + 2 * NB * 1024, &rmap, C, page * kPage + (rank * 4 + k) * 8, fb);
+            }
+          }
+          if (i == 0 && u > 0) {
+            if (!mbar_wait(qempty, (u - 1) & 1, abort_flag)) {
+              ++g;  // (this page was asked for)
+              return false;
+            }
+            load_q(t);
+          }
+        }
+        return true;
+      });
+      // do not leave while a copy may still land in this CTA's memory
+      for (int k = max(0, g - kStages); k < g; ++k) drain(kfull + 8 * (k % kStages), (k / kStages) & 1);
+      if (asked > 0) drain(qfull, (asked - 1) & 1);
+    }
+  } else if (warp == 2) {
+    // ========================== producer of values ==========================
+    if (lane == 0) {
+      int g = 0;
+      units([&](const Unit& un, int n, int) {
+        for (int i = 0; i < n; ++i, ++g) {
+          const int page = page_of(un, i, false);
+          const int st = g % kStages;
+          if (g >= kStages && !mbar_wait(vempty + 8 * st, ((g / kStages) - 1) & 1, abort_flag)) return false;
+          mbar_arrive_expect_tx(vfull + 8 * st, L::kV);
+          tma_load_4d(smem_addr(smem + L::v) + st * L::kV, &vmap, 0, 0, rank * NB, page * 8, vfull + 8 * st);
+        }
+        return true;
+      });
+      for (int k = max(0, g - kStages); k < g; ++k) drain(vfull + 8 * (k % kStages), (k / kStages) & 1);
+    }
+  } else if (warp == 3 || (warp == 1 && rank != 0)) {
+    // ====================== relays of rank 1 to rank 0 ======================
+    if (rank != 0 && lane == 0) {
+      const bool keys = warp == 1;
+      const uint32_t mine = keys ? kfull : vfull, theirs = mapa_shared(mine, 0), qfull0 = mapa_shared(qfull, 0);
+      int g = 0;
+      units([&](const Unit&, int n, int u) {
+        if (keys) {
+          if (!mbar_wait(qfull, u & 1, abort_flag)) return false;
+          mbar_arrive_remote(qfull0);
+        }
+        for (int i = 0; i < n; ++i, ++g) {
+          if (!mbar_wait(mine + 8 * (g % kStages), (g / kStages) & 1, abort_flag)) return false;
+          mbar_arrive_remote(theirs + 8 * (g % kStages));
+        }
+        return true;
+      });
+    }
+  } else if (warp == 1) {
+    // ======================= products' issuer (rank 0) ======================
+    // The whole warp runs this, on values that are the same in all its threads (latent_attn.cu).
+    constexpr uint32_t kIdS = umma_idesc_bf16(2 * kRows, kPage, 0, 0);
+    constexpr uint32_t kIdPV = umma_idesc_bf16(2 * kRows, 256, 0, 1);
+    constexpr uint32_t kIdPV1 = umma_idesc_bf16(2 * kRows, 128, 0, 1);  // (the odd 64 numbers of a half)
+    const uint64_t kdesc = umma_desc_sw128(smem_addr(smem + L::k), 0, L::kRg);
+    const uint64_t qdesc = umma_desc_sw128(smem_addr(smem + L::q), 0, 1024);
+    const uint64_t vdesc = umma_desc_sw128(smem_addr(smem + L::v), 1024, L::kVRg);
+    const uint64_t pdesc = umma_desc_sw128(smem_addr(smem + L::p), 0, 1024);
+    const uint32_t k_lo = static_cast<uint32_t>(kdesc), k_hi = static_cast<uint32_t>(kdesc >> 32);
+    const uint32_t q_lo = static_cast<uint32_t>(qdesc), q_hi = static_cast<uint32_t>(qdesc >> 32);
+    const uint32_t v_lo = static_cast<uint32_t>(vdesc), v_hi = static_cast<uint32_t>(vdesc >> 32);
+    const uint32_t p_lo = static_cast<uint32_t>(pdesc), p_hi = static_cast<uint32_t>(pdesc >> 32);
+    auto uniform = [](int x) { return __reduce_max_sync(0xffffffffu, x); };
+    auto done = [](uint32_t bar, uint32_t parity) {
+      return __reduce_and_sync(0xffffffffu, mbar_test_wait_cluster(bar, parity) ? 1u : 0u) != 0u;
+    };
+    // scores of page s and the value product of page v <= s, in whatever order they become ready
+    int s = 0, v = 0, u = 0;
+    int ut = 0, un = 0, ui = 0;  // tokens and pages (of this share) of unit u, page s in it
+    uint32_t first = 0u;         // bit s & 1: page s is its unit's first here
+    int more = uniform(left > 0);
+    if (more != 0) {
+      const Unit x = unit_at(p, t);
+      ut = x.nt;
+      un = uniform(static_cast<int>(min(left, static_cast<long long>(x.np - j0))));
+    }
+    uint64_t t0 = 0;
+    uint32_t idle = 0;
+    while (more != 0 || v < s) {
+      bool did = false;
+      if (v < s && done(pfull, v & 1) && done(vfull + 8 * (v % kStages), (v / kStages) & 1)) {
+        tc_fence_after();
+        const uint32_t vd = v_lo + (((v % kStages) * L::kV) >> 4);
+        const uint32_t keep = first >> (v & 1) & 1u ? 0u : 1u;
+#pragma unroll 1
+        for (int kk = 0; kk < kPage / 16; ++kk) {
+          const uint32_t sum = kk > 0 ? 1u : keep;
+#pragma unroll
+          for (int b = 0; b < NB / 2; ++b)
+            umma2_ss_warp(tmem + b * 128, p_lo + ((kk * 32) >> 4), p_hi, vd + ((kk * 2 * L::kVRg + b * 2048) >> 4), v_hi, kIdPV,
+                          sum);
+          if constexpr (NB % 2 == 1)
+            umma2_ss_warp(tmem + (NB / 2) * 128, p_lo + ((kk * 32) >> 4), p_hi,
+                          vd + ((kk * 2 * L::kVRg + (NB / 2) * 2048) >> 4), v_hi, kIdPV1, sum);
+        }
+        umma2_commit_both_warp(vempty + 8 * (v % kStages));
+        umma2_commit_both_warp(pvdone);
+        ++v;
+        did = true;
+      }
+      // (two score buffers: page s - 2 has been read once its value product was issued)
+      if (more != 0 && s <= v + 1 && done(kfull + 8 * (s % kStages), (s / kStages) & 1) && (ui > 0 || done(qfull, u & 1))) {
+        tc_fence_after();
+        const uint32_t sc = tmem + L::kColS + (s & 1) * 32;
+        uint32_t kd = k_lo + (((s % kStages) * L::kK) >> 4), qd = q_lo;
+#pragma unroll 1
+        for (int c = 0; c < 2 * NB; ++c, kd += 1024 >> 4, qd += (kRows * 128) >> 4) {
+          umma2_ss_warp(sc, qd, q_hi, kd, k_hi, kIdS, c > 0 ? 1u : 0u);
+#pragma unroll
+          for (int kk = 1; kk < 4; ++kk) umma2_ss_warp(sc, qd + ((kk * 32) >> 4), q_hi, kd + ((kk * 32) >> 4), k_hi, kIdS, 1u);
+        }
+        umma2_ss_warp(sc, qd, q_hi, kd, k_hi, kIdS, 1u);
+        umma2_ss_warp(sc, qd + (32 >> 4), q_hi, kd + (32 >> 4), k_hi, kIdS, 1u);
+        if (p.rope_dim == 64) {
+          umma2_ss_warp(sc, qd + (64 >> 4), q_hi, kd + (64 >> 4), k_hi, kIdS, 1u);
+          umma2_ss_warp(sc, qd + (96 >> 4), q_hi, kd + (96 >> 4), k_hi, kIdS, 1u);
+        }
+        umma2_commit_both_warp(sfull + 8 * (s & 1));
+        umma2_commit_both_warp(kempty + 8 * (s % kStages));
+        first = (first & ~(1u << (s & 1))) | (ui == 0 ? 1u << (s & 1) : 0u);
+        ++s;
+        if (++ui == un) {  // the unit's last scores: its query rows may go
+          umma2_commit_both_warp(qempty);
+          left -= un;
+          t += ut;
+          ui = 0;
+          ++u;
+          more = uniform(left > 0);
+          if (more != 0) {
+            const Unit x = unit_at(p, t);
+            ut = x.nt;
+            un = uniform(static_cast<int>(min(left, static_cast<long long>(x.np))));
+          }
+        }
+        did = true;
+      }
+      if (did) {
+        idle = 0;
+      } else if ((++idle & 255u) == 0) {
+        if (idle == 256u) t0 = global_timer_ns();
+        const bool late = global_timer_ns() - t0 > kWaitLimitNs || idle >= kWaitLimitIters;
+        if (__any_sync(0xffffffffu, late || *abort_flag != 0)) {
+          *abort_flag = 1;
+          break;
+        }
+      }
+    }
+    // no product is in flight when the tensor memory goes
+    umma2_commit_both_warp(fin);
+    mbar_wait(fin, 0, abort_flag);
+    __syncwarp();
+  } else {
+    // ============================== softmax ===============================
+    const int qt = warp & 3;
+    const int row = (qt & 1) * 32 + lane, half = qt >> 1;
+    const int rr = rank * kRows + row;               // row of the tile
+    const uint32_t lanes = static_cast<uint32_t>(qt * 32) << 16;
+    const uint32_t pfull0 = mapa_shared(pfull, 0);
+    const uint64_t scale2 = f32x2(p.scale_log2, p.scale_log2);
+    uint8_t* prow = smem + L::p + row * 128;
+    bool ok = true;
+    int g = 0;
+    units([&](const Unit& un, int n, int) {
+      const int nrows = min(2 * kRows, un.nt * p.heads - hb * 2 * kRows);
+      const int rowbase = t * p.heads + hb * 2 * kRows;
+      const bool direct = j0 == 0 && n == un.np;
+      // keys that this row sees (rows past the unit's: everything, nobody reads them)
+      int lo = 0, hi = 0x7fffffff;
+      if (rr < nrows) {
+        int r0;
+        token_keys(p, t + (hb * 2 * kRows + rr) / p.heads, r0, lo, hi);
+      }
+      const int32_t* trow = p.table + static_cast<long long>(max(un.row, 0)) * p.pages_per_row;
+      float nref = 0.f, l = 0.f;           // minus the reference (0 while there is none), this thread's part of the sum
+      bool unset = rr < nrows && hi > lo;  // no reference yet, and keys to see
+      bool force = true;                   // some row of the CTA has none
+      if (half == 0) s_ref[row] = -INFINITY;
+      named_barrier_sync(kSoftBar, 128);
+      for (int i = 0; i < n; ++i, ++g) {
+        const int lp = un.first + j0 + i, kb = lp * kPage, k0 = kb + half * 32;
+        const int page = un.row >= 0 ? trow[lp] : -1;
+        const bool held = page >= 0 && page < p.num_pages;
+        ok = __all_sync(0xffffffffu, mbar_wait(sfull + 8 * (g & 1), (g >> 1) & 1, abort_flag));
+        tc_fence_after();
+        uint32_t r[32];
+        if (ok) {
+          tmem_ld32(tmem + lanes + L::kColS + (g & 1) * 32, r);
+          tmem_ld_wait();
+        }
+        if (!(held && kb >= un.in_lo && kb + kPage <= un.in_hi)) {
+          const int a = held ? lo - k0 : 32, e = hi - k0;
+#pragma unroll
+          for (int x = 0; x < 32; ++x)
+            if (x < a || x >= e) r[x] = 0xFF800000u;
+        }
+        if (force) {
+          const int f = max(lo, kb) - k0;  // the row's first key of this page
+          if (f >= 0 && f < 32) {
+            float x0 = __uint_as_float(r[0]);
+            if (f > 0) {
+#pragma unroll
+              for (int x = 1; x < 32; ++x)
+                if (x == f) x0 = __uint_as_float(r[x]);
+            }
+            s_ref[row] = x0;
+          }
+          named_barrier_sync(kSoftBar, 128);
+          const float f0 = s_ref[row];
+          if (unset && f0 > -INFINITY) {  // (a NaN score: the maximum of the others, below)
+            nref = -f0 * p.scale_log2;
+            unset = false;
+          }
+        }
+        float a[32];
+        float mx = -INFINITY;
+        auto exponents = [&]() {
+          const uint64_t n2 = f32x2(nref, nref);
+#pragma unroll
+          for (int x = 0; x < 32; x += 2) {
+            f32x2_split(fma_f32x2(f32x2(__uint_as_float(r[x]), __uint_as_float(r[x + 1])), scale2, n2), a[x], a[x + 1]);
+            mx = fmax3(mx, a[x], a[x + 1]);
+          }
+        };
+        exponents();
+        // (a row without a reference that sees a score all the same: its first one is -inf or NaN)
+        const bool raise = unset ? mx > -INFINITY : mx > kRaiseLog2;
+        if (named_barrier_or(kSoftBar, 128, raise || !ok)) {
+          // ---- references raised (or set) to the page's maximum ----
+          if (g > 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait(pvdone, (g - 1) & 1, abort_flag));
+          if (named_barrier_or(kSoftBar, 128, !ok)) {
+            ok = false;
+            return false;
+          }
+          tc_fence_after();
+          float m = -INFINITY;
+#pragma unroll
+          for (int x = 0; x < 32; ++x) m = fmaxf(m, __uint_as_float(r[x]));
+          s_pair[half * kRows + row] = m;
+          named_barrier_sync(kSoftBar, 128);
+          m = fmaxf(m, s_pair[(half ^ 1) * kRows + row]);
+          float f = 1.f;
+          if (m != -INFINITY) {
+            m *= p.scale_log2;
+            if (unset) {
+              nref = -m;
+              unset = false;
+            } else if (m + nref > kRaiseLog2) {
+              f = ex2_approx(-nref - m);
+              l *= f;
+              nref = -m;
+            }
+          }
+          if (__any_sync(0xffffffffu, f != 1.f) && i > 0) {
+#pragma unroll 1
+            for (int c = 0; c < NB * 64; c += 16) {
+              uint32_t v[16];
+              tmem_ld16(tmem + lanes + c, v);
+              tmem_ld_wait();
+#pragma unroll
+              for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * f);
+              tmem_st16(tmem + lanes + c, v);
+            }
+            tmem_st_wait();
+          }
+          exponents();
+        }
+        if (force) force = named_barrier_or(kSoftBar, 128, unset);
+        // ---- P into shared memory, once the product before has read the last one ----
+        if (g > 0) ok = __all_sync(0xffffffffu, mbar_wait(pvdone, (g - 1) & 1, abort_flag));
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t w[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float e0 = ex2_approx(a[8 * c + 2 * k]), e1 = ex2_approx(a[8 * c + 2 * k + 1]);
+            l += e0 + e1;
+            w[k] = pack_bf16x2(e0, e1);
+          }
+          *reinterpret_cast<uint4*>(prow + (((half * 4 + c) ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        // ---- value rows that no token of the unit sees may hold anything: zero ----
+        if (!(held && kb >= un.kmin && kb + kPage <= un.kmax)) {
+          ok = ok && __all_sync(0xffffffffu, mbar_wait(vfull + 8 * (g % kStages), (g / kStages) & 1, abort_flag));
+          uint8_t* v = smem + L::v + (g % kStages) * L::kV;
+          // rows [0, below) and [above, 64), 16 bytes of a row a thread (eight threads a line)
+          const int below = held ? min(kPage, max(0, un.kmin - kb)) : kPage;
+          const int above = held ? max(below, min(kPage, un.kmax - kb)) : kPage;
+          const int out = ok ? below + kPage - above : 0, sid = tid - 128;
+#pragma unroll 1
+          for (int k = sid >> 3; k < out; k += 16) {
+            const int key = k < below ? k : k - below + above;
+            uint8_t* to = v + (key >> 3) * L::kVRg + (key & 7) * 128 + (sid & 7) * 16;
+#pragma unroll
+            for (int c = 0; c < NB; ++c) *reinterpret_cast<uint4*>(to + c * 1024) = make_uint4(0u, 0u, 0u, 0u);
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(pfull0);  // (publishes P, and zeroed values, to the pair's products)
+      }
+      // ---- the unit's end: sums joined, outputs or partial sums stored ----
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(pvdone, (g - 1) & 1, abort_flag));
+      if (named_barrier_or(kSoftBar, 128, !ok)) {
+        ok = false;
+        return false;
+      }
+      tc_fence_after();
+      s_pair[half * kRows + row] = l;
+      named_barrier_sync(kSoftBar, 128);
+      const float sum = s_pair[row] + s_pair[kRows + row];
+      const float inv = sum > 0.f ? 1.f / sum : sum;  // (a NaN sum makes the row NaN)
+      const size_t slot = direct ? 0 : (static_cast<size_t>(2 * team + (j0 == 0 ? 1 : 0)) * p.head_blocks + hb) * p.slot_rows;
+      if (!direct && half == 0) {
+        p.ml[(slot + rr) * 2] = sum == 0.f ? -INFINITY : -nref;
+        p.ml[(slot + rr) * 2 + 1] = sum;
+      }
+      uint32_t odd = 0u;  // bits 15 and 31: an element is not finite
+      const int r8 = rank * kRows + (row & ~7);
+      if (direct) {
+#pragma unroll 1
+        for (int c = 0; c < NB; ++c) {  // 64 numbers a step
+          uint4 w[8];
+#pragma unroll
+          for (int h2 = 0; h2 < 2; ++h2) {
+            uint32_t v[32];
+            tmem_ld32(tmem + lanes + c * 64 + h2 * 32, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t x[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float y0 = __uint_as_float(v[8 * k + 2 * e]) * inv, y1 = __uint_as_float(v[8 * k + 2 * e + 1]) * inv;
+                x[e] = sum == 0.f ? 0u : pack_bf16x2(y0, y1);
+                odd |= (x[e] & 0x7F807F80u) + 0x00800080u;
+              }
+              w[4 * h2 + k] = make_uint4(x[0], x[1], x[2], x[3]);
+            }
+          }
+          transpose_pieces(w);
+          uint16_t* o = p.out + static_cast<size_t>(rowbase + r8) * C + half * (C / 2) + c * 64 + (lane & 7) * 8;
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (r8 + k < nrows) *reinterpret_cast<uint4*>(o + k * C) = w[k];
+        }
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < 2 * NB; ++c) {  // 32 numbers a step
+          uint32_t v[32];
+          tmem_ld32(tmem + lanes + c * 32, v);
+          tmem_ld_wait();
+          uint4 w[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            w[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) odd |= ((v[4 * k + e] >> 16 & 0x7F80u) + 0x0080u) & 0x8000u;
+          }
+          transpose_pieces(w);
+          float* o = p.o + (slot + r8) * C + half * (C / 2) + c * 32 + (lane & 7) * 4;
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (r8 + k < nrows) *reinterpret_cast<uint4*>(o + k * C) = w[k];
+        }
+      }
+      unsigned todo = __ballot_sync(0xffffffffu, rr < nrows && (odd & 0x80008000u) != 0u && sum == sum);
+      while (todo != 0u) {
+        const int src = __ffs(todo) - 1;
+        todo &= todo - 1;
+        const int ro = rr - lane + src, w = p.latent_dim + p.rope_dim;
+        __syncwarp();
+        float acc[2 * NB];
+        attend_half<NB>(p, p.q + static_cast<size_t>(rowbase + ro) * w, trow,
+                        max(__shfl_sync(0xffffffffu, lo, src), (un.first + j0) * kPage),
+                        min(__shfl_sync(0xffffffffu, hi, src), (un.first + j0 + n) * kPage),
+                        __shfl_sync(0xffffffffu, nref, src), half * (C / 2), acc);
+        const float f = __shfl_sync(0xffffffffu, inv, src);
+#pragma unroll
+        for (int k = 0; k < 2 * NB; ++k) {
+          const int d = half * (C / 2) + lane + 32 * k;
+          if (direct) p.out[static_cast<size_t>(rowbase + ro) * C + d] = static_cast<uint16_t>(pack_bf16x2(acc[k] * f, 0.f));
+          else p.o[(slot + ro) * C + d] = acc[k];
+        }
+      }
+      tc_fence_before();
+      named_barrier_sync(kSoftBar, 128);  // (the rows' data may be written again)
+      return true;
+    });
+    if (!ok) *abort_flag = 1;
+  }
+  __syncwarp();
+  if (*abort_flag && lane == 0 && p.status != nullptr) atomicOr(p.status, LNK_DEV_TIMEOUT);
+  // neither CTA frees its tensor memory or leaves while the pair's products,
+  // copies or remote arrivals may still touch it
+  tc_fence_before();
+  cluster_sync_all();
+  tc_fence_after();
+  if (warp == 1) tmem2_dealloc(tmem, L::kCols);
+}
+
+template <int NB>
+cudaError_t launch_t(const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap, const CUtensorMap& rmap,
+                     const LatentParams& p, cudaStream_t stream) {
+  const int bytes = static_cast<int>(PairSmem<NB>::bytes);
+  cudaError_t err = set_max_dynamic_smem(reinterpret_cast<const void*>(pair_kernel<NB>), bytes);
+  if (err != cudaSuccess) return err;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * p.teams * p.head_blocks));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  err = cudaLaunchKernelEx(&cfg, pair_kernel<NB>, qmap, kmap, vmap, rmap, p);
+  if (err != cudaSuccess) return err;
+  return launch_latent_join(p, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_latent_pair(const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                               const CUtensorMap& rmap, const LatentParams& p, cudaStream_t stream) {
+  switch (p.latent_dim / 128) {
+    case 1: return launch_t<1>(qmap, kmap, vmap, rmap, p, stream);
+    case 2: return launch_t<2>(qmap, kmap, vmap, rmap, p, stream);
+    case 3: return launch_t<3>(qmap, kmap, vmap, rmap, p, stream);
+    case 4: return launch_t<4>(qmap, kmap, vmap, rmap, p, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace lnk

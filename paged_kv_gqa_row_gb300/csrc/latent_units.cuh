@@ -1,0 +1,182 @@
+// How a latent attention launch's work is laid out: tiles of query rows that see one table
+// row (units), their pages laid end to end in one stream, and the teams' equal shares of it.
+// A unit is one decode row's token, or a run of prompt tokens of one table row that fit a
+// tile together; with more heads than a tile has rows, each of the team's CTAs (or pairs)
+// takes a block of heads over the same pages.
+#pragma once
+
+#include "latent.cuh"
+
+namespace lnk {
+namespace {
+
+constexpr int kWholePages = 8;  // tokens of so few pages are never cut
+
+struct Share {
+  unsigned long long left;  // pages of this team's share
+  int t, j;                 // its first unit (that one's first token) and first page in it
+};
+
+struct Shares {
+  long long per;  // pages of a share
+  int bad;        // device status bits of this thread's tokens
+};
+
+struct Unit {
+  int nt, row;        // tokens; table row (-1: nothing to see)
+  int kmin, kmax;     // keys that some token sees
+  int in_lo, in_hi;   // keys that every token sees
+  int first, np;      // first page; pages (one at least)
+};
+
+__device__ __forceinline__ int token_keys(const LatentParams& p, int t, int& row, int& lo, int& hi) {
+  int pos;
+  if (t < p.P) {
+    row = p.rows[t];
+    pos = p.positions[t];
+  } else {
+    row = t - p.P;
+    pos = p.step_positions[t - p.P];
+  }
+  lo = hi = 0;
+  if (pos < 0) return 0;
+  if (row < 0 || row >= p.num_rows) return LNK_DEV_BAD_ROW;
+  if (pos >= p.pages_per_row * kPage) return LNK_DEV_BAD_POSITION;
+  lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
+  hi = pos + 1;
+  return 0;
+}
+
+__device__ __forceinline__ bool unit_starts(const LatentParams& p, int t) {
+  return t >= p.P || p.tile_tokens == 1 || t % p.tile_tokens == 0 || p.rows[t] != p.rows[t - 1];
+}
+
+__device__ __forceinline__ Unit unit_at(const LatentParams& p, int t) {
+  Unit u;
+  u.nt = 0;
+  u.row = -1;
+  u.kmin = 0x7fffffff;
+  u.kmax = 0;
+  u.in_lo = 0;
+  u.in_hi = 0x7fffffff;
+  const int end = t < p.P ? min(p.P, (t / p.tile_tokens + 1) * p.tile_tokens) : t + 1;
+  int row0 = 0;
+  for (int s = t; s < end; ++s) {
+    int row, lo, hi;
+    token_keys(p, s, row, lo, hi);
+    if (s == t) row0 = row;
+    else if (row != row0) break;
+    ++u.nt;
+    u.in_lo = max(u.in_lo, lo);
+    u.in_hi = min(u.in_hi, hi);
+    if (hi > lo) {
+      u.row = row;
+      u.kmin = min(u.kmin, lo);
+      u.kmax = max(u.kmax, hi);
+    }
+  }
+  if (u.row < 0) u.kmin = 0;
+  u.first = u.kmin / kPage;
+  u.np = u.row < 0 ? 1 : (u.kmax - 1) / kPage - u.first + 1;
+  return u;
+}
+
+__device__ __forceinline__ float bf16_at(const uint16_t* x) {
+  return __uint_as_float(static_cast<uint32_t>(*x) << 16);
+}
+
+
+// Counts the units' pages and finds this team's share: all threads of the CTA, each with a
+// range of tokens.  mem: 32 ints of shared memory, 8-byte aligned; share_of(mem) is the
+// result, after a barrier of the CTA.
+__device__ __forceinline__ const Share* share_of(const int* mem) { return reinterpret_cast<const Share*>(mem + 16); }
+
+template <int kThreads>
+__device__ __forceinline__ Shares count_shares(const LatentParams& p, int team, int* mem) {
+  constexpr int kWarps = kThreads / 32;
+  static_assert(kWarps <= 8, "shared memory of the count");
+  long long* scan = reinterpret_cast<long long*>(mem);   // [kWarps]
+  Share* share = reinterpret_cast<Share*>(mem + 16);
+  int* longest = mem + 20;                               // [kWarps]
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    share->t = 0x7fffffff;
+    share->j = 0;
+    share->left = 0ull;
+  }
+  const int span = (p.T + kThreads - 1) / kThreads;
+  const int ta = min(p.T, tid * span), tb = min(p.T, ta + span);
+  int bad = 0, most = 0;
+  long long mine = 0;
+  for (int t = ta; t < tb; ++t) {
+    int row, lo, hi;
+    bad |= token_keys(p, t, row, lo, hi);
+    if (unit_starts(p, t)) {
+      const int np = unit_at(p, t).np;
+      mine += np;
+      most = max(most, np);
+    }
+  }
+  most = __reduce_max_sync(0xffffffffu, most);
+  long long before = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += x;
+  }
+  if (lane == 31) scan[warp] = before;
+  if (lane == 0) longest[warp] = most;
+  __syncthreads();
+  long long total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += scan[w];
+    total += scan[w];
+    most = max(most, longest[w]);
+  }
+  before -= mine;
+  const long long per = max(1ll, (total + p.teams - 1) / p.teams);
+  const long long start = team * per;
+  // Units of few pages (or far fewer than a share) stay whole: a team takes those whose first
+  // page lies in its share.
+  const bool whole = p.whole || most <= max(static_cast<long long>(kWholePages), per / 8);
+  if (before < start + per && before + mine > start) {
+    long long at = before;
+    for (int t = ta; t < tb && at < start + per; ++t) {
+      if (!unit_starts(p, t)) continue;
+      const int np = unit_at(p, t).np;
+      if (whole) {
+        if (at >= start) {
+          atomicMin(&share->t, t);
+          atomicAdd(&share->left, static_cast<unsigned long long>(np));
+        }
+      } else if (at <= start && start < at + np) {
+        share->t = t;
+        share->j = static_cast<int>(start - at);
+        share->left = static_cast<unsigned long long>(min(per, total - start));
+        break;
+      }
+      at += np;
+    }
+  }
+  return {per, bad};
+}
+
+// What the joining kernel needs to know of the unit in which a share starts (j0 pages into it).
+__device__ __forceinline__ void write_cut(const LatentParams& p, int team, int t, int j0, long long per) {
+  LatentCut cut;
+  cut.t0 = t;
+  cut.nt = cut.np = 0;
+  cut.j0 = j0;
+  cut.per = per;
+  cut.pad = 0;
+  if (j0 > 0) {
+    const Unit u = unit_at(p, t);
+    cut.nt = u.nt;
+    cut.np = u.np;
+  }
+  p.cuts[team] = cut;
+}
+
+}  // namespace
+}  // namespace lnk

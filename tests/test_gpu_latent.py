@@ -45,12 +45,20 @@ STEPS = [
     ("many-heads", 128, 512, 64, [(5, 300), (3, 64)], [200], 0),
     ("window", 16, 512, 64, [(70, 200), (33, 0)], [500, 3], 65),
     ("window-1", 8, 128, 64, [(70, 100)], [70], 1),
+    # enough rows for tiles of 128 on pairs of SMs
+    ("pairs", 20, 128, 64, [(700, 30), (330, 5)], [70], 0),
+    ("pairs-c256", 48, 256, 32, [(300, 0), (113, 64)], [], 0),
+    ("pairs-c384", 30, 384, 64, [(651, 3)], [300, 1], 0),
+    ("pairs-window", 64, 512, 64, [(310, 90)], [500], 65),
+    ("pairs-one-head", 1, 128, 32, [(19500, 0)], [], 40),
 ]
 
 
 @pytest.mark.parametrize("name,heads,c,r,pieces,dec,window", STEPS, ids=[x[0] for x in STEPS])
 def test_step(name, heads, c, r, pieces, dec, window):
-    Step(100 + len(name), heads, c, r, pieces, dec, window).upload().run().verify()
+    s = Step(100 + len(name), heads, c, r, pieces, dec, window).upload().run()
+    # (of many tokens: the ends, and every 37th)
+    s.verify(None if s.P < 200 else {*range(0, s.P, 37), *range(s.P - 3, s.P + s.B), *range(5)})
 
 
 def _ulp1(got, want, what):
@@ -185,13 +193,12 @@ def test_bad_rows_positions_and_pages():
             check(out[t], want, spread, size, p + 1, s.c + s.r, f"token {t}")
 
 
-def test_raises_of_the_reference():
-    """Scores that grow by far more than 2^16 from page to page, and sums that must follow."""
-    for heads, c, r in ((24, 512, 64), (64, 256, 32)):
-        s = Step(6, heads, c, r, pieces=[(9, 300)], dec=[1000, 333], scale=0.3)
+@pytest.mark.parametrize("scale", [0.3, 2.0])
+def test_raises_of_the_reference(scale):
+    """Scores that grow by far more than 2^32 from page to page, and sums that must follow."""
+    for heads, c, r in ((24, 512, 64), (64, 256, 32), (100, 512, 64), (16, 128, 64)):
+        s = Step(6, heads, c, r, pieces=[(9, 300)], dec=[1000, 333], scale=scale)
         grow = np.linspace(0.05, 3.0, s.pages * PAGE)
-        order = np.argsort(np.concatenate([s.table[row][s.table[row] >= 0] for row in range(s.table.shape[0])]), kind="stable")
-        del order
         for row in range(s.table.shape[0]):
             pages = s.table[row][s.table[row] >= 0]
             slots = (pages[:, None] * PAGE + np.arange(PAGE)).reshape(-1)
@@ -207,15 +214,16 @@ def _numbers_where(out, finite_tokens, nan_tokens):
         assert np.isnan(f[t]).all(), f"token {t}"
 
 
+@pytest.mark.parametrize("heads,count", [(12, 12), (40, 500)], ids=["one-sm", "pairs"])
 @pytest.mark.parametrize("bad", [0x7FC0, 0x7F80, 0xFF80], ids=["nan", "inf", "-inf"])
-def test_values_that_are_not_finite_reach_only_those_who_see_them(bad):
-    # a piece of 12 tokens, five or so a tile, whose 7th token's key is not finite
-    s = Step(7, 12, 256, 64, pieces=[(12, 100)], dec=[500, 70])
+def test_values_that_are_not_finite_reach_only_those_who_see_them(bad, heads, count):
+    # a piece of tokens, a few a tile, whose 7th token's key is not finite
+    s = Step(7, heads, 256, 64, pieces=[(count, 100)], dec=[500, 70])
     slot = s.table[2, 106 // PAGE] * PAGE + 106 % PAGE
     clean = s.pool.copy()
     s.pool[slot] = bad
     # what lies behind each row's last key may be anything as well
-    for row, p in ((0, 500), (1, 70), (2, 112)):
+    for row, p in ((0, 500), (1, 70), (2, 100 + count)):
         if p % PAGE:
             first = s.table[row, p // PAGE] * PAGE
             s.pool[first + p % PAGE:first + PAGE] = 0x7FC0
@@ -233,9 +241,10 @@ def test_values_that_are_not_finite_reach_only_those_who_see_them(bad):
         check(out[t], want, spread, size, p + 1, s.c + s.r, f"token {t}")
 
 
-def test_a_long_row_with_a_key_that_is_not_finite_in_a_cut_share():
+@pytest.mark.parametrize("heads", [16, 128], ids=["one-sm", "pairs"])
+def test_a_long_row_with_a_key_that_is_not_finite_in_a_cut_share(heads):
     """The keys that a piece's first tokens do not see lie in a part whose sums are joined later."""
-    s = Step(8, 16, 512, 64, pieces=[(4, 9000)])
+    s = Step(8, heads, 512, 64, pieces=[(4, 9000)])
     clean = s.pool.copy()
     s.pool[s.table[0, 9002 // PAGE] * PAGE + 9002 % PAGE, :5] = 0x7FC0
     s.upload().run()
@@ -250,7 +259,7 @@ def test_a_long_row_with_a_key_that_is_not_finite_in_a_cut_share():
 def test_graph_replays_on_another_stream_and_two_workspaces():
     """A captured step replayed on new inputs, with another step's calls beside it on another stream."""
     a = Step(9, 40, 512, 64, pieces=[(7, 200)], dec=[900, 300]).upload()
-    b = Step(10, 64, 256, 32, dec=[1500, 20, 64]).upload()
+    b = Step(10, 100, 256, 32, dec=[1500, 20, 64]).upload()
     a.run().verify()
     b.run().verify()
     want_a, want_b = bits(a.out).copy(), bits(b.out).copy()
