@@ -17,7 +17,11 @@
 // Warps: 0 loads keys and query rows, 2 values (each CTA its own); 1 issues the products in
 // rank 0 and tells rank 0 of rank 1's keys and queries in rank 1, where warp 3 does so for
 // values; 4-7 softmax: thread L owns row L % 64 of its CTA and keys 32 (L / 64) .. + 31 of a page,
-// and that row's half L / 64 of O.
+// and that row's half L / 64 of O.  Scores and probabilities have two buffers each.
+// (Rank 0's products read rank 1's probabilities from rank 1's shared memory.  The softmax warps
+// order their stores before the async proxy and then arrive at rank 0's barrier; arriving
+// with a release to the cluster instead took a memory barrier of 1500 to 3500 clocks, in these
+// warps or in a relay's: 32 rows of 128 heads 89 us.)
 #include "latent_units.cuh"
 #include "ptx.cuh"
 
@@ -39,15 +43,15 @@ struct PairSmem {
   static constexpr int kQ = kChunks * kRows * 128;
   static constexpr int kP = kRows * 128;
   static constexpr int kMisc = 2048;
-  static constexpr int kBudget = 232448 - 1024 - kMisc - kQ - kP;
+  static constexpr int kBudget = 232448 - 1024 - kMisc - kQ - 2 * kP;
   static constexpr int kStages = kBudget / (kK + kV) < 4 ? kBudget / (kK + kV) : 4;
   static constexpr size_t k = 0;
   static constexpr size_t v = k + size_t(kStages) * kK;
   static constexpr size_t q = v + size_t(kStages) * kV;
   static constexpr size_t p = q + kQ;
-  static constexpr size_t bars = p + kP;
-  // kfull, kempty, vfull, vempty [stages], sfull[2], pfull, pvdone, qfull, qempty, fin
-  static constexpr int kNumBars = 4 * kStages + 7;
+  static constexpr size_t bars = p + 2 * kP;
+  // kfull, kempty, vfull, vempty [stages], sfull[2], pfull[2], pvdone[2], qfull, qempty, fin
+  static constexpr int kNumBars = 4 * kStages + 9;
   static constexpr size_t ref = bars + 8 * kNumBars;      // [64] a row's first score; in a raise the maxima
   static constexpr size_t pair = ref + 4 * kRows;         // [2][64] what a row's two threads tell each other
   static constexpr size_t misc = pair + 8 * kRows;        // abort, tensor memory, share
@@ -124,8 +128,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t kfull = smem_addr(smem + L::bars);
   const uint32_t kempty = kfull + 8 * kStages, vfull = kempty + 8 * kStages, vempty = vfull + 8 * kStages;
   const uint32_t sfull = vempty + 8 * kStages;  // [2] scores of a page
-  const uint32_t pfull = sfull + 16;            // probabilities of a page (rank 0 only)
-  const uint32_t pvdone = pfull + 8, qfull = pvdone + 8, qempty = qfull + 8, fin = qempty + 8;
+  const uint32_t pfull = sfull + 16;            // [2] probabilities of a page (rank 0 only)
+  const uint32_t pvdone = pfull + 16;           // [2] the value product of a page
+  const uint32_t qfull = pvdone + 16, qempty = qfull + 8, fin = qempty + 8;
   float* s_ref = reinterpret_cast<float*>(smem + L::ref);
   float* s_pair = reinterpret_cast<float*>(smem + L::pair);
   int* misc = reinterpret_cast<int*>(smem + L::misc);
@@ -146,7 +151,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(vfull + 8 * i, copies);
     }
     mbar_init(qfull, copies);
-    mbar_init(pfull, 8);  // the softmax warps of both CTAs
+    for (int i = 0; i < 2; ++i) mbar_init(pfull + 8 * i, 8);  // the softmax warps of both CTAs
     *abort_flag = 0;
     fence_mbarrier_init();
   }
@@ -250,11 +255,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (warp == 3 || (warp == 1 && rank != 0)) {
     // ====================== relays of rank 1 to rank 0 ======================
     if (rank != 0 && lane == 0) {
-      const bool keys = warp == 1;
-      const uint32_t mine = keys ? kfull : vfull, theirs = mapa_shared(mine, 0), qfull0 = mapa_shared(qfull, 0);
+      const uint32_t mine = warp == 1 ? kfull : vfull, theirs = mapa_shared(mine, 0);
+      const uint32_t qfull0 = mapa_shared(qfull, 0);
       int g = 0;
       units([&](const Unit&, int n, int u) {
-        if (keys) {
+        if (warp == 1) {
           if (!mbar_wait(qfull, u & 1, abort_flag)) return false;
           mbar_arrive_remote(qfull0);
         }
@@ -297,23 +302,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint32_t idle = 0;
     while (more != 0 || v < s) {
       bool did = false;
-      if (v < s && done(pfull, v & 1) && done(vfull + 8 * (v % kStages), (v / kStages) & 1)) {
+      if (v < s && done(pfull + 8 * (v & 1), (v >> 1) & 1) && done(vfull + 8 * (v % kStages), (v / kStages) & 1)) {
         tc_fence_after();
-        const uint32_t vd = v_lo + (((v % kStages) * L::kV) >> 4);
+        const uint32_t vd = v_lo + (((v % kStages) * L::kV) >> 4), pd = p_lo + (((v & 1) * L::kP) >> 4);
         const uint32_t keep = first >> (v & 1) & 1u ? 0u : 1u;
 #pragma unroll 1
         for (int kk = 0; kk < kPage / 16; ++kk) {
           const uint32_t sum = kk > 0 ? 1u : keep;
 #pragma unroll
           for (int b = 0; b < NB / 2; ++b)
-            umma2_ss_warp(tmem + b * 128, p_lo + ((kk * 32) >> 4), p_hi, vd + ((kk * 2 * L::kVRg + b * 2048) >> 4), v_hi, kIdPV,
+            umma2_ss_warp(tmem + b * 128, pd + ((kk * 32) >> 4), p_hi, vd + ((kk * 2 * L::kVRg + b * 2048) >> 4), v_hi, kIdPV,
                           sum);
           if constexpr (NB % 2 == 1)
-            umma2_ss_warp(tmem + (NB / 2) * 128, p_lo + ((kk * 32) >> 4), p_hi,
+            umma2_ss_warp(tmem + (NB / 2) * 128, pd + ((kk * 32) >> 4), p_hi,
                           vd + ((kk * 2 * L::kVRg + (NB / 2) * 2048) >> 4), v_hi, kIdPV1, sum);
         }
         umma2_commit_both_warp(vempty + 8 * (v % kStages));
-        umma2_commit_both_warp(pvdone);
+        umma2_commit_both_warp(pvdone + 8 * (v & 1));
         ++v;
         did = true;
       }
@@ -445,7 +450,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const bool raise = unset ? mx > -INFINITY : mx > kRaiseLog2;
         if (named_barrier_or(kSoftBar, 128, raise || !ok)) {
           // ---- references raised (or set) to the page's maximum ----
-          if (g > 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait(pvdone, (g - 1) & 1, abort_flag));
+          if (g > 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait(pvdone + 8 * ((g - 1) & 1), ((g - 1) >> 1) & 1, abort_flag));
           if (named_barrier_or(kSoftBar, 128, !ok)) {
             ok = false;
             return false;
@@ -484,8 +489,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           exponents();
         }
         if (force) force = named_barrier_or(kSoftBar, 128, unset);
-        // ---- P into shared memory, once the product before has read the last one ----
-        if (g > 0) ok = __all_sync(0xffffffffu, mbar_wait(pvdone, (g - 1) & 1, abort_flag));
+        // ---- P into shared memory, once the product of two pages before has read what is there ----
+        if (g > 1) ok = __all_sync(0xffffffffu, mbar_wait(pvdone + 8 * (g & 1), ((g - 2) >> 1) & 1, abort_flag));
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t w[4];
@@ -495,7 +500,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             l += e0 + e1;
             w[k] = pack_bf16x2(e0, e1);
           }
-          *reinterpret_cast<uint4*>(prow + (((half * 4 + c) ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+          *reinterpret_cast<uint4*>(prow + (g & 1) * L::kP + (((half * 4 + c) ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
         // ---- value rows that no token of the unit sees may hold anything: zero ----
         if (!(held && kb >= un.kmin && kb + kPage <= un.kmax)) {
@@ -516,10 +521,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(pfull0);  // (publishes P, and zeroed values, to the pair's products)
+        if (lane == 0) mbar_arrive_remote(pfull0 + 8 * (g & 1));
       }
       // ---- the unit's end: sums joined, outputs or partial sums stored ----
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(pvdone, (g - 1) & 1, abort_flag));
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(pvdone + 8 * ((g - 1) & 1), ((g - 1) >> 1) & 1, abort_flag));
       if (named_barrier_or(kSoftBar, 128, !ok)) {
         ok = false;
         return false;

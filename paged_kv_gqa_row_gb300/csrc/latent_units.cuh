@@ -87,17 +87,17 @@ __device__ __forceinline__ float bf16_at(const uint16_t* x) {
 
 
 // Counts the units' pages and finds this team's share: all threads of the CTA, each with a
-// range of tokens.  mem: 32 ints of shared memory, 8-byte aligned; share_of(mem) is the
+// range of tokens.  mem: 40 ints of shared memory, 8-byte aligned; share_of(mem) is the
 // result, after a barrier of the CTA.
-__device__ __forceinline__ const Share* share_of(const int* mem) { return reinterpret_cast<const Share*>(mem + 16); }
+__device__ __forceinline__ const Share* share_of(const int* mem) { return reinterpret_cast<const Share*>(mem + 20); }
 
 template <int kThreads>
 __device__ __forceinline__ Shares count_shares(const LatentParams& p, int team, int* mem) {
   constexpr int kWarps = kThreads / 32;
-  static_assert(kWarps <= 8, "shared memory of the count");
+  static_assert(kWarps <= 10, "shared memory of the count");
   long long* scan = reinterpret_cast<long long*>(mem);   // [kWarps]
-  Share* share = reinterpret_cast<Share*>(mem + 16);
-  int* longest = mem + 20;                               // [kWarps]
+  Share* share = reinterpret_cast<Share*>(mem + 20);
+  int* longest = mem + 24;                               // [kWarps]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     share->t = 0x7fffffff;
