@@ -92,10 +92,10 @@ lnk_status attend(const lnk_latent_desc* desc, const lnk_bf16* q, const int32_t*
   p.num_rows = desc->num_rows;
   p.pages_per_row = desc->pages_per_row;
   p.window = desc->window;
-  // Tiles of 128 rows on pairs of SMs for more heads than 64, and where prompt tokens fill two
-  // such tiles a pair; else of 64 (decode rows alone never share a tile: no more rows than
-  // heads need).
-  const bool pairs = p.heads > kLatentRows || static_cast<long long>(P) * p.heads >= 2ll * sms * kLatentRows;
+  // Tiles of 128 rows on pairs of SMs for more heads than 64, and where prompt tokens fill one
+  // for every pair (a step of 272 tokens of 64 heads and 32 decode rows: 148 us so, 197 us in
+  // tiles of 64); else of 64 (decode rows alone never share a tile: no more rows than heads need).
+  const bool pairs = p.heads > kLatentRows || static_cast<long long>(P) * p.heads >= static_cast<long long>(sms) * kLatentRows;
   p.tile_rows = pairs ? 2 * kLatentRows : (P > 0 || p.heads > 32 ? 64 : (p.heads > 16 ? 32 : 16));
   p.slot_rows = std::max(kLatentRows, p.tile_rows);
   p.tile_tokens = std::max(1, p.tile_rows / p.heads);

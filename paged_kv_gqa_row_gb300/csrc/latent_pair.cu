@@ -69,28 +69,6 @@ __device__ __forceinline__ void drain(uint32_t bar, int parity) {
   }
 }
 
-// Eight lanes of neighbouring rows hold eight 16-byte pieces of their row each: afterwards
-// lane i holds piece i of each of the rows, so that a store covers whole lines.
-__device__ __forceinline__ void transpose_pieces(uint4 (&w)[8]) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int b = 1; b < 8; b <<= 1) {
-    const bool up = (lane & b) != 0;
-#pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      if (c & b) continue;
-      const uint4 give = up ? w[c] : w[c | b];
-      uint4 got;
-      got.x = __shfl_xor_sync(0xffffffffu, give.x, b);
-      got.y = __shfl_xor_sync(0xffffffffu, give.y, b);
-      got.z = __shfl_xor_sync(0xffffffffu, give.z, b);
-      got.w = __shfl_xor_sync(0xffffffffu, give.w, b);
-      if (up) w[c] = got;
-      else w[c | b] = got;
-    }
-  }
-}
-
 // One row's sums over its own visible keys [lo, hi), relative to the reference that its softmax
 // used: numbers d0 + lane + 32 i of the latent in acc[i].  The whole warp.
 template <int NB>
@@ -539,72 +517,102 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         p.ml[(slot + rr) * 2] = sum == 0.f ? -INFINITY : -nref;
         p.ml[(slot + rr) * 2 + 1] = sum;
       }
-      uint32_t odd = 0u;  // bits 15 and 31: an element is not finite
-      const int r8 = rank * kRows + (row & ~7);
-      if (direct) {
+      if (half == 0) s_ref[row] = inv;
+      named_barrier_sync(kSoftBar, 128);
+      // 16 rows and 64 numbers a step: a thread gets numbers 8 i + 2 (lane % 4), + 1 of rows lane / 4
+      // and lane / 4 + 8.  (A loop of few instructions: they are cold when a unit ends.)
+      unsigned odd[4];  // of rows 8 k .. + 7 of the warp's, four bits each: not all is finite
+      const int wrow = (qt & 1) * 32 + (lane >> 2), ca = 2 * (lane & 3);
 #pragma unroll 1
-        for (int c = 0; c < NB; ++c) {  // 64 numbers a step
-          uint4 w[8];
+      for (int h16 = 0; h16 < 2; ++h16) {
+        float bad0 = 0.f, bad1 = 0.f;  // 0 times every number: NaN once one is not finite
+        const int ra = wrow + h16 * 16, rb = ra + 8;
+        const bool see_a = rank * kRows + ra < nrows, see_b = rank * kRows + rb < nrows;
+        const float fa = direct ? s_ref[ra] : 1.f, fb = direct ? s_ref[rb] : 1.f;
+#pragma unroll 1
+        for (int c = 0; c < NB; ++c) {
+          uint32_t v[32];
+          tmem_ld_16x256b(tmem + lanes + (static_cast<uint32_t>(h16 * 16) << 16) + c * 64, v);
+          tmem_ld_wait();
+          const int d = half * (C / 2) + c * 64;
+          if (direct) {
+            uint32_t wa[8], wb[8];
 #pragma unroll
-          for (int h2 = 0; h2 < 2; ++h2) {
-            uint32_t v[32];
-            tmem_ld32(tmem + lanes + c * 64 + h2 * 32, v);
-            tmem_ld_wait();
+            for (int i = 0; i < 8; ++i) {
+              const float a0 = __uint_as_float(v[4 * i]) * fa, a1 = __uint_as_float(v[4 * i + 1]) * fa;
+              const float b0 = __uint_as_float(v[4 * i + 2]) * fb, b1 = __uint_as_float(v[4 * i + 3]) * fb;
+              bad0 = fmaf(a0, 0.f, fmaf(a1, 0.f, bad0));
+              bad1 = fmaf(b0, 0.f, fmaf(b1, 0.f, bad1));
+              wa[i] = fa == 0.f ? 0u : pack_bf16x2(a0, a1);
+              wb[i] = fb == 0.f ? 0u : pack_bf16x2(b0, b1);
+            }
+            // four lanes trade: lane l gets eight numbers of groups l and 4 + l
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint32_t x[4];
+            for (int b = 1; b < 4; b <<= 1) {
+              const bool up = (lane & b) != 0;
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float y0 = __uint_as_float(v[8 * k + 2 * e]) * inv, y1 = __uint_as_float(v[8 * k + 2 * e + 1]) * inv;
-                x[e] = sum == 0.f ? 0u : pack_bf16x2(y0, y1);
-                odd |= (x[e] & 0x7F807F80u) + 0x00800080u;
+              for (int k = 0; k < 8; ++k) {
+                if (k & b) continue;
+                const uint32_t ga = __shfl_xor_sync(0xffffffffu, up ? wa[k] : wa[k | b], b);
+                const uint32_t gb = __shfl_xor_sync(0xffffffffu, up ? wb[k] : wb[k | b], b);
+                if (up) {
+                  wa[k] = ga;
+                  wb[k] = gb;
+                } else {
+                  wa[k | b] = ga;
+                  wb[k | b] = gb;
+                }
               }
-              w[4 * h2 + k] = make_uint4(x[0], x[1], x[2], x[3]);
+            }
+            uint16_t* o = p.out + static_cast<size_t>(rowbase + rank * kRows + ra) * C + d + (lane & 3) * 8;
+            if (see_a) {
+              *reinterpret_cast<uint4*>(o) = make_uint4(wa[0], wa[1], wa[2], wa[3]);
+              *reinterpret_cast<uint4*>(o + 32) = make_uint4(wa[4], wa[5], wa[6], wa[7]);
+            }
+            if (see_b) {
+              *reinterpret_cast<uint4*>(o + 8 * C) = make_uint4(wb[0], wb[1], wb[2], wb[3]);
+              *reinterpret_cast<uint4*>(o + 8 * C + 32) = make_uint4(wb[4], wb[5], wb[6], wb[7]);
+            }
+          } else {
+            float* o = p.o + (slot + rank * kRows + ra) * C + d + ca;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              bad0 = fmaf(__uint_as_float(v[4 * i]), 0.f, fmaf(__uint_as_float(v[4 * i + 1]), 0.f, bad0));
+              bad1 = fmaf(__uint_as_float(v[4 * i + 2]), 0.f, fmaf(__uint_as_float(v[4 * i + 3]), 0.f, bad1));
+              if (see_a) *reinterpret_cast<uint2*>(o + 8 * i) = make_uint2(v[4 * i], v[4 * i + 1]);
+              if (see_b) *reinterpret_cast<uint2*>(o + 8 * C + 8 * i) = make_uint2(v[4 * i + 2], v[4 * i + 3]);
             }
           }
-          transpose_pieces(w);
-          uint16_t* o = p.out + static_cast<size_t>(rowbase + r8) * C + half * (C / 2) + c * 64 + (lane & 7) * 8;
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (r8 + k < nrows) *reinterpret_cast<uint4*>(o + k * C) = w[k];
         }
-      } else {
-#pragma unroll 1
-        for (int c = 0; c < 2 * NB; ++c) {  // 32 numbers a step
-          uint32_t v[32];
-          tmem_ld32(tmem + lanes + c * 32, v);
-          tmem_ld_wait();
-          uint4 w[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            w[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) odd |= ((v[4 * k + e] >> 16 & 0x7F80u) + 0x0080u) & 0x8000u;
-          }
-          transpose_pieces(w);
-          float* o = p.o + (slot + r8) * C + half * (C / 2) + c * 32 + (lane & 7) * 4;
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (r8 + k < nrows) *reinterpret_cast<uint4*>(o + k * C) = w[k];
+        const unsigned ba = __ballot_sync(0xffffffffu, see_a && bad0 != bad0), bb = __ballot_sync(0xffffffffu, see_b && bad1 != bad1);
+        if (h16 == 0) {
+          odd[0] = ba;
+          odd[1] = bb;
+        } else {
+          odd[2] = ba;
+          odd[3] = bb;
         }
       }
-      unsigned todo = __ballot_sync(0xffffffffu, rr < nrows && (odd & 0x80008000u) != 0u && sum == sum);
-      while (todo != 0u) {
-        const int src = __ffs(todo) - 1;
-        todo &= todo - 1;
-        const int ro = rr - lane + src, w = p.latent_dim + p.rope_dim;
-        __syncwarp();
-        float acc[2 * NB];
-        attend_half<NB>(p, p.q + static_cast<size_t>(rowbase + ro) * w, trow,
-                        max(__shfl_sync(0xffffffffu, lo, src), (un.first + j0) * kPage),
-                        min(__shfl_sync(0xffffffffu, hi, src), (un.first + j0 + n) * kPage),
-                        __shfl_sync(0xffffffffu, nref, src), half * (C / 2), acc);
-        const float f = __shfl_sync(0xffffffffu, inv, src);
+      if ((odd[0] | odd[1] | odd[2] | odd[3]) != 0u) {
+#pragma unroll 1
+        for (int k = 0; k < 32; ++k) {
+          const unsigned m = k < 16 ? (k < 8 ? odd[0] : odd[1]) : (k < 24 ? odd[2] : odd[3]);
+          const float total = __shfl_sync(0xffffffffu, sum, k);
+          if ((m >> (4 * (k & 7)) & 15u) == 0u || total != total) continue;  // (a NaN sum is the row's own)
+          const int ro = rank * kRows + (qt & 1) * 32 + k, w = p.latent_dim + p.rope_dim;
+          __syncwarp();
+          float acc[2 * NB];
+          attend_half<NB>(p, p.q + static_cast<size_t>(rowbase + ro) * w, trow,
+                          max(__shfl_sync(0xffffffffu, lo, k), (un.first + j0) * kPage),
+                          min(__shfl_sync(0xffffffffu, hi, k), (un.first + j0 + n) * kPage),
+                          __shfl_sync(0xffffffffu, nref, k), half * (C / 2), acc);
+          const float f = __shfl_sync(0xffffffffu, inv, k);
 #pragma unroll
-        for (int k = 0; k < 2 * NB; ++k) {
-          const int d = half * (C / 2) + lane + 32 * k;
-          if (direct) p.out[static_cast<size_t>(rowbase + ro) * C + d] = static_cast<uint16_t>(pack_bf16x2(acc[k] * f, 0.f));
-          else p.o[(slot + ro) * C + d] = acc[k];
+          for (int i = 0; i < 2 * NB; ++i) {
+            const int d = half * (C / 2) + lane + 32 * i;
+            if (direct) p.out[static_cast<size_t>(rowbase + ro) * C + d] = static_cast<uint16_t>(pack_bf16x2(acc[i] * f, 0.f));
+            else p.o[(slot + ro) * C + d] = acc[i];
+          }
         }
       }
       tc_fence_before();
