@@ -16,6 +16,10 @@
  *   lnk_paged_read_tokens   the stored k/v of given tokens, as bf16 (the
  *                           append's inverse).
  *
+ * The same step where a token keeps one latent row that all query heads share
+ * ("Latent cache" below): lnk_latent_append, lnk_latent_decode_attn,
+ * lnk_latent_step_attn, lnk_latent_prompt_attn, lnk_latent_copy_pages.
+ *
  * Sources: the model pages "Mistral 7B Instruct v0.3", "Qwen3-4B" and
  * "Llama 3.1 8B Instruct", Entries table (prefill_paged, decode_paged,
  * step_paged); "Phi-3 Mini 4K Instruct -- files", src/attention.linnet
@@ -587,7 +591,8 @@ size_t lnk_latent_workspace_size(const lnk_latent_desc* desc);
  *            stride rotates in place; otherwise the two must not overlap.
  *   kv_out   device [T][C + R] or NULL: what the pool receives, packed (zero for
  *            inactive tokens): the input of the expanded form's products
- *   T        tokens (0 is allowed and enqueues nothing)
+ *   T        tokens (0 is allowed and enqueues nothing).  No two active ones may have
+ *            the same place in the pool (it would hold numbers of both)
  *
  * Element i of a rotated part turns with element i + R / 2.  Numerics, the order of
  * reads before the kernel before this one has ended, and what infinities and NaN do:

@@ -5,7 +5,31 @@
 
 namespace lnk {
 
-constexpr int kLatentRows = 64;  // query rows of an attention tile at most
+constexpr int kLatentRows = 64;  // query rows of a one-SM attention tile at most
+constexpr int kWholePages = 8;   // tokens of so few pages are never cut
+
+__device__ __forceinline__ float bf16_at(const uint16_t* x) {
+  return __uint_as_float(static_cast<uint32_t>(*x) << 16);
+}
+
+// Bits 15 and 31: a bf16 number among eight is not finite.
+__device__ __forceinline__ uint32_t odd_halves(const uint4& x) {
+  auto odd = [](uint32_t w) { return (w & 0x7F807F80u) + 0x00800080u; };
+  return (odd(x.x) | odd(x.y) | odd(x.z) | odd(x.w)) & 0x80008000u;
+}
+
+// s + the products of eight pairs of bf16 numbers
+__device__ __forceinline__ float dot8(const uint4& a, const uint4& b, float s) {
+  auto two = [&s](uint32_t x, uint32_t y) {
+    s = fmaf(__uint_as_float(x << 16), __uint_as_float(y << 16), s);
+    s = fmaf(__uint_as_float(x & 0xFFFF0000u), __uint_as_float(y & 0xFFFF0000u), s);
+  };
+  two(a.x, b.x);
+  two(a.y, b.y);
+  two(a.z, b.z);
+  two(a.w, b.w);
+  return s;
+}
 
 // A row of a tile (a unit of the stream of pages) that the teams' shares cut: what
 // the joining kernel needs to know, written by the team whose share starts inside it.

@@ -9,7 +9,6 @@ namespace lnk {
 namespace {
 
 constexpr int kMaxLatentHeads = 1024;
-constexpr int kWholePages = 8;  // tokens of so few pages are never cut, and there is no second kernel
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 

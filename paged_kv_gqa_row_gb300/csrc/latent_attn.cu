@@ -31,7 +31,7 @@
 // A value that is not finite, at a key that some rows of a tile see and others do not,
 // would reach all of them through 0 * NaN.  Key rows that no token of the tile sees are
 // zeroed before they are values; a row whose output is not finite while its sum is
-// computes again from its own keys (attend_column).
+// computes again from its own keys (attend_again).
 #include "latent_units.cuh"
 #include "ptx.cuh"
 
@@ -72,30 +72,6 @@ struct LatentSmem {
   static constexpr uint32_t kCols = NB * N + 2 * N <= 64 ? 64 : NB * N + 2 * N <= 128 ? 128
                                   : NB * N + 2 * N <= 256 ? 256 : 512;
 };
-
-// One row's sums over its own visible keys [lo, hi), relative to the reference that the
-// tile's softmax used, key by key: element 128 mb + d of the row in acc[mb].  The whole warp.
-template <int NB>
-__device__ __noinline__ void attend_column(const LatentParams& p, const uint16_t* q, const int32_t* trow, int lo, int hi,
-                                           float nref, int d, float (&acc)[NB]) {
-  const int w = p.latent_dim + p.rope_dim, lane = threadIdx.x & 31;
-#pragma unroll
-  for (int mb = 0; mb < NB; ++mb) acc[mb] = 0.f;
-#pragma unroll 1
-  for (int key = lo; key < hi; ++key) {
-    const int page = trow[key / kPage];
-    if (page < 0 || page >= p.num_pages) continue;
-    const uint16_t* k = p.pool + (static_cast<size_t>(page) * kPage + key % kPage) * w;
-    float s = 0.f;
-#pragma unroll 1
-    for (int e = lane; e < w; e += 32) s = fmaf(bf16_at(q + e), bf16_at(k + e), s);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    const float e = exp2f(fmaf(s, p.scale_log2, nref));
-#pragma unroll
-    for (int mb = 0; mb < NB; ++mb) acc[mb] = fmaf(e, bf16_at(k + mb * 128 + d), acc[mb]);
-  }
-}
 
 template <int NB, int N>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -613,10 +589,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (__any_sync(0xffffffffu, (odd & 0x80008000u) != 0u)) {
         const int w = p.latent_dim + p.rope_dim;
-        const int seg_lo = (un.first + j0) * kPage, seg_hi = (un.first + j0 + n) * kPage;
+        const int seg_lo = max(un.kmin, (un.first + j0) * kPage), seg_hi = min(un.kmax, (un.first + j0 + n) * kPage);
+        int in_lo = 0, in_hi = 0x7fffffff;  // keys that every row with keys sees
+        for (int rr = lane; rr < nrows; rr += 32) {
+          if (row_keys[rr].y <= row_keys[rr].x) continue;
+          in_lo = max(in_lo, row_keys[rr].x);
+          in_hi = min(in_hi, row_keys[rr].y);
+        }
+        const int2 bad_keys = odd_keys(p, trow, seg_lo, seg_hi, __reduce_max_sync(0xffffffffu, in_lo),
+                                       __reduce_min_sync(0xffffffffu, in_hi));
 #pragma unroll 1
         for (int rr = 0; rr < nrows; ++rr) {
           if (s_alpha[rr] != s_alpha[rr]) continue;  // (a sum that is NaN is the row's own: all of it is)
+          if (row_keys[rr].x <= bad_keys.x && row_keys[rr].y > bad_keys.y) continue;  // (so is what is not finite)
           bool bad = false;
 #pragma unroll 1
           for (int mb = 0; mb < NB; ++mb) {
@@ -629,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (!__any_sync(0xffffffffu, bad)) continue;
           float acc[NB];
-          attend_column<NB>(p, p.q + static_cast<size_t>(rowbase + rr) * w, trow, max(row_keys[rr].x, seg_lo),
+          attend_again<NB, 128>(p, p.q + static_cast<size_t>(rowbase + rr) * w, trow, max(row_keys[rr].x, seg_lo),
                             min(row_keys[rr].y, seg_hi), s_ref[rr], qt * 32 + lane, acc);
 #pragma unroll
           for (int mb = 0; mb < NB; ++mb) {

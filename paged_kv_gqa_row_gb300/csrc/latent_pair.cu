@@ -69,30 +69,6 @@ __device__ __forceinline__ void drain(uint32_t bar, int parity) {
   }
 }
 
-// One row's sums over its own visible keys [lo, hi), relative to the reference that its softmax
-// used: numbers d0 + lane + 32 i of the latent in acc[i].  The whole warp.
-template <int NB>
-__device__ __noinline__ void attend_half(const LatentParams& p, const uint16_t* q, const int32_t* trow, int lo, int hi,
-                                         float nref, int d0, float (&acc)[2 * NB]) {
-  const int w = p.latent_dim + p.rope_dim, lane = threadIdx.x & 31;
-#pragma unroll
-  for (int i = 0; i < 2 * NB; ++i) acc[i] = 0.f;
-#pragma unroll 1
-  for (int key = lo; key < hi; ++key) {
-    const int page = trow[key / kPage];
-    if (page < 0 || page >= p.num_pages) continue;
-    const uint16_t* k = p.pool + (static_cast<size_t>(page) * kPage + key % kPage) * w;
-    float s = 0.f;
-#pragma unroll 1
-    for (int e = lane; e < w; e += 32) s = fmaf(bf16_at(q + e), bf16_at(k + e), s);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    const float e = exp2f(fmaf(s, p.scale_log2, nref));
-#pragma unroll
-    for (int i = 0; i < 2 * NB; ++i) acc[i] = fmaf(e, bf16_at(k + d0 + lane + 32 * i), acc[i]);
-  }
-}
-
 template <int NB>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     pair_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
@@ -594,18 +570,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
       if ((odd[0] | odd[1] | odd[2] | odd[3]) != 0u) {
+        const int seg_lo = max(un.kmin, (un.first + j0) * kPage), seg_hi = min(un.kmax, (un.first + j0 + n) * kPage);
+        const int2 bad_keys = odd_keys(p, trow, seg_lo, seg_hi, __reduce_max_sync(0xffffffffu, hi > lo ? lo : 0),
+                                       __reduce_min_sync(0xffffffffu, hi > lo ? hi : 0x7fffffff));
 #pragma unroll 1
         for (int k = 0; k < 32; ++k) {
           const unsigned m = k < 16 ? (k < 8 ? odd[0] : odd[1]) : (k < 24 ? odd[2] : odd[3]);
           const float total = __shfl_sync(0xffffffffu, sum, k);
           if ((m >> (4 * (k & 7)) & 15u) == 0u || total != total) continue;  // (a NaN sum is the row's own)
+          const int lo_k = __shfl_sync(0xffffffffu, lo, k), hi_k = __shfl_sync(0xffffffffu, hi, k);
+          if (lo_k <= bad_keys.x && hi_k > bad_keys.y) continue;  // (so is what is not finite)
           const int ro = rank * kRows + (qt & 1) * 32 + k, w = p.latent_dim + p.rope_dim;
           __syncwarp();
           float acc[2 * NB];
-          attend_half<NB>(p, p.q + static_cast<size_t>(rowbase + ro) * w, trow,
-                          max(__shfl_sync(0xffffffffu, lo, k), (un.first + j0) * kPage),
-                          min(__shfl_sync(0xffffffffu, hi, k), (un.first + j0 + n) * kPage),
-                          __shfl_sync(0xffffffffu, nref, k), half * (C / 2), acc);
+          attend_again<2 * NB, 32>(p, p.q + static_cast<size_t>(rowbase + ro) * w, trow, max(lo_k, seg_lo), min(hi_k, seg_hi),
+                                   __shfl_sync(0xffffffffu, nref, k), half * (C / 2) + lane, acc);
           const float f = __shfl_sync(0xffffffffu, inv, k);
 #pragma unroll
           for (int i = 0; i < 2 * NB; ++i) {

@@ -102,34 +102,57 @@ __device__ __forceinline__ PromptTile prompt_tile(const LatentPromptParams& p, i
   return t;
 }
 
-__device__ __forceinline__ float bf16_at(const uint16_t* x) {
-  return __uint_as_float(static_cast<uint32_t>(*x) << 16);
+// The last key of [a, b) of a prompt and head (kv: its first key's row) that has a number in
+// columns c0 .. c0 + D / 2 - 1 of its values that is not finite, or -1.  The whole warp.
+template <int D>
+__device__ __noinline__ int last_odd_key(const LatentPromptParams& p, const uint16_t* kv, int a, int b, int c0) {
+  constexpr int kLanes = D / 16, kKeys = 32 / kLanes;  // lanes a key, keys at once
+  const int lane = threadIdx.x & 31, piece = lane % kLanes;
+#pragma unroll 1
+  for (int k0 = b - 1; k0 >= a; k0 -= kKeys) {
+    const int key = k0 - lane / kLanes;
+    const uint16_t* v = kv + static_cast<size_t>(max(key, a)) * p.heads * (2 * D) + D + c0 + piece * 8;
+    const unsigned odd = __ballot_sync(0xffffffffu, key >= a && odd_halves(*reinterpret_cast<const uint4*>(v)) != 0u);
+    if (odd != 0u) return k0 - (__ffs(odd) - 1) / kLanes;
+  }
+  return -1;
 }
 
 // One row's value sums over its own keys, relative to the maximum and sum of its softmax:
-// columns c0 + lane and c0 + 32 + lane (below c1), the whole warp.
+// columns c0 .. c0 + D / 2 - 1, the whole warp: a key a lane for the scores, the columns over
+// the lanes for the sums.
 template <int D>
 __device__ __noinline__ void attend_row(const LatentPromptParams& p, const uint16_t* q, const uint16_t* kv,
-                                        const uint16_t* k_rope, int keys, float m, float inv, uint16_t* out, int c0, int c1) {
+                                        const uint16_t* k_rope, int keys, float m, float inv, uint16_t* out, int c0) {
+  constexpr int NV = D / 64;
   const int lane = threadIdx.x & 31;
-  float acc0 = 0.f, acc1 = 0.f;
-  const size_t stride = static_cast<size_t>(p.heads) * 2 * D;
-  const bool two = c0 + 32 + lane < c1;
-#pragma unroll 1
-  for (int key = 0; key < keys; ++key, kv += stride, k_rope += p.rope_stride) {
-    float s = 0.f;
-#pragma unroll 1
-    for (int e = lane; e < D; e += 32) s = fmaf(bf16_at(q + e), bf16_at(kv + e), s);
-#pragma unroll 1
-    for (int e = lane; e < p.rope_dim; e += 32) s = fmaf(bf16_at(q + D + e), bf16_at(k_rope + e), s);
+  float acc[NV];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    const float w = exp2f(fmaf(s, p.scale_log2, -m));
-    acc0 = fmaf(w, bf16_at(kv + D + c0 + lane), acc0);
-    if (two) acc1 = fmaf(w, bf16_at(kv + D + c0 + 32 + lane), acc1);
+  for (int i = 0; i < NV; ++i) acc[i] = 0.f;
+  const size_t stride = static_cast<size_t>(p.heads) * 2 * D;
+#pragma unroll 1
+  for (int key0 = 0; key0 < keys; key0 += 32) {
+    const int key = min(key0 + lane, keys - 1);
+    const uint16_t* k = kv + key * stride;
+    const uint16_t* r = k_rope + key * p.rope_stride;
+    float s = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < D; i += 8) s = dot8(*reinterpret_cast<const uint4*>(q + i), *reinterpret_cast<const uint4*>(k + i), s);
+#pragma unroll 4
+    for (int i = 0; i < p.rope_dim; i += 8)
+      s = dot8(*reinterpret_cast<const uint4*>(q + D + i), *reinterpret_cast<const uint4*>(r + i), s);
+    const float e = exp2f(fmaf(s, p.scale_log2, -m));
+    const int n = min(32, keys - key0);
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float f = __shfl_sync(0xffffffffu, e, i);
+      const uint16_t* v = kv + (key0 + i) * stride + D + c0 + lane;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) acc[j] = fmaf(f, bf16_at(v + 32 * j), acc[j]);
+    }
   }
-  out[c0 + lane] = static_cast<uint16_t>(pack_bf16x2(acc0 * inv, 0.f));
-  if (two) out[c0 + 32 + lane] = static_cast<uint16_t>(pack_bf16x2(acc1 * inv, 0.f));
+#pragma unroll
+  for (int j = 0; j < NV; ++j) out[c0 + lane + 32 * j] = static_cast<uint16_t>(pack_bf16x2(acc[j] * inv, 0.f));
 }
 
 __device__ __forceinline__ void drain(uint32_t bar, int parity) {
@@ -677,16 +700,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if ((row & ~(kPieces - 1)) + i < tile.n)
           *reinterpret_cast<uint4*>(o + static_cast<size_t>(i) * p.heads * D) = w[i];
       unsigned todo = __ballot_sync(0xffffffffu, again);
-      while (todo != 0u) {
-        const int src = __ffs(todo) - 1;
-        todo &= todo - 1;
-        const int rr = row - lane + src;
-        __syncwarp();
-        attend_row<D>(p, p.q + (static_cast<size_t>(tile.q0 + rr) * p.heads + tile.h) * (D + p.rope_dim),
-                      p.kv + (static_cast<size_t>(tile.k0) * p.heads + tile.h) * (2 * D),
-                      p.k_rope + static_cast<long long>(tile.k0) * p.rope_stride, tile.first + rr,
-                      __shfl_sync(0xffffffffu, mf, src), __shfl_sync(0xffffffffu, inv, src),
-                      p.out + (static_cast<size_t>(tile.q0 + rr) * p.heads + tile.h) * D, grp * (D / 2), (grp + 1) * (D / 2));
+      if (todo != 0u) {
+        const uint16_t* kv = p.kv + (static_cast<size_t>(tile.k0) * p.heads + tile.h) * (2 * D);
+        const int bad_key = last_odd_key<D>(p, kv, max(0, tile.first + row - lane), tile.keys, grp * (D / 2));
+        while (todo != 0u) {
+          const int src = __ffs(todo) - 1;
+          todo &= todo - 1;
+          const int rr = row - lane + src;
+          if (tile.first + rr > bad_key) break;  // (it sees them all: what is not finite is its own; so do those after it)
+          __syncwarp();
+          attend_row<D>(p, p.q + (static_cast<size_t>(tile.q0 + rr) * p.heads + tile.h) * (D + p.rope_dim), kv,
+                        p.k_rope + static_cast<long long>(tile.k0) * p.rope_stride, tile.first + rr,
+                        __shfl_sync(0xffffffffu, mf, src), __shfl_sync(0xffffffffu, inv, src),
+                        p.out + (static_cast<size_t>(tile.q0 + rr) * p.heads + tile.h) * D, grp * (D / 2));
+        }
       }
       __syncwarp();
       js0 += nsteps;

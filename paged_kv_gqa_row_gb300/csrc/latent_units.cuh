@@ -10,8 +10,6 @@
 namespace lnk {
 namespace {
 
-constexpr int kWholePages = 8;  // tokens of so few pages are never cut
-
 struct Share {
   unsigned long long left;  // pages of this team's share
   int t, j;                 // its first unit (that one's first token) and first page in it
@@ -81,10 +79,65 @@ __device__ __forceinline__ Unit unit_at(const LatentParams& p, int t) {
   return u;
 }
 
-__device__ __forceinline__ float bf16_at(const uint16_t* x) {
-  return __uint_as_float(static_cast<uint32_t>(*x) << 16);
+// The first key from `from` on (to `to`, exclusive, in steps of +1 or -1) whose latent has a
+// number that is not finite, or -1.  The whole warp.
+__device__ __noinline__ int odd_key(const LatentParams& p, const int32_t* trow, int from, int to, int step) {
+  const int w = p.latent_dim + p.rope_dim, lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int key = from; key != to; key += step) {
+    const int page = trow[key / kPage];
+    if (page < 0 || page >= p.num_pages) continue;
+    const uint16_t* c = p.pool + (static_cast<size_t>(page) * kPage + key % kPage) * w;
+    uint32_t odd = 0u;
+#pragma unroll 1
+    for (int e = lane * 8; e < p.latent_dim; e += 256) odd |= odd_halves(*reinterpret_cast<const uint4*>(c + e));
+    if (__any_sync(0xffffffffu, odd != 0u)) return key;
+  }
+  return -1;
 }
 
+// The keys of [lo, hi) that rows which all see [in_lo, in_hi) may not see and that hold numbers
+// which are not finite: a row that starts behind x or ends at or before y has some of them.
+__device__ __forceinline__ int2 odd_keys(const LatentParams& p, const int32_t* trow, int lo, int hi, int in_lo, int in_hi) {
+  const int a = min(in_lo, hi), b = max(in_hi, lo);
+  const int x = lo < a ? odd_key(p, trow, lo, a, 1) : -1;
+  return make_int2(x < 0 ? 0x7fffffff : x, b < hi ? odd_key(p, trow, hi - 1, b - 1, -1) : -1);
+}
+
+// One row's sums over its own visible keys [lo, hi), relative to the reference that its softmax
+// used: number d + STEP i of the latent in acc[i].  The whole warp: a key a lane for the
+// scores, the numbers of a key over the lanes for the sums.
+template <int NV, int STEP>
+__device__ __noinline__ void attend_again(const LatentParams& p, const uint16_t* q, const int32_t* trow, int lo, int hi,
+                                          float nref, int d, float (&acc)[NV]) {
+  const int w = p.latent_dim + p.rope_dim, lane = threadIdx.x & 31;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) acc[i] = 0.f;
+#pragma unroll 1
+  for (int key0 = lo; key0 < hi; key0 += 32) {
+    const int key = key0 + lane;
+    const int page = key < hi ? trow[key / kPage] : -1;
+    const bool here = page >= 0 && page < p.num_pages;
+    const uint16_t* k = p.pool + (here ? (static_cast<size_t>(page) * kPage + key % kPage) * w : 0);
+    float e = 0.f;
+    if (here) {
+      float s = 0.f;
+#pragma unroll 4
+      for (int i = 0; i < w; i += 8) s = dot8(*reinterpret_cast<const uint4*>(q + i), *reinterpret_cast<const uint4*>(k + i), s);
+      e = exp2f(fmaf(s, p.scale_log2, nref));
+    }
+    unsigned todo = __ballot_sync(0xffffffffu, here);
+#pragma unroll 2
+    while (todo != 0u) {
+      const int src = __ffs(todo) - 1;
+      todo &= todo - 1;
+      const float f = __shfl_sync(0xffffffffu, e, src);
+      const uint16_t* v = reinterpret_cast<const uint16_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(k), src)) + d;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) acc[i] = fmaf(f, bf16_at(v + STEP * i), acc[i]);
+    }
+  }
+}
 
 // Counts the units' pages and finds this team's share: all threads of the CTA, each with a
 // range of tokens.  mem: 40 ints of shared memory, 8-byte aligned; share_of(mem) is the

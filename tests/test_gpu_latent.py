@@ -256,6 +256,27 @@ def test_a_long_row_with_a_key_that_is_not_finite_in_a_cut_share(heads):
         check(out[t], want, spread, size, 9001, s.c + s.r, f"token {t}")
 
 
+@pytest.mark.parametrize("heads", [16, 128], ids=["one-sm", "pairs"])
+def test_keys_that_are_not_finite_cost_no_wait(heads):
+    """Behind a long context, and in the context of all of a piece's tokens: no wait of the kernel runs out."""
+    s = Step(12, heads, 256, 32, pieces=[(6, 60000), (40, 8000)], dec=[9000])
+    clean = s.pool.copy()
+    s.pool[s.table[1, 60004 // PAGE] * PAGE + 60004 % PAGE] = 0x7FC0
+    s.pool[s.table[2, 0] * PAGE + 5, :7] = 0x7F80
+    s.pool[s.table[0, 0] * PAGE + 5, :7] = 0x7FC0
+    s.upload().run()
+    torch.cuda.synchronize()
+    assert int(s.status.item()) == 0
+    out = bits(s.out)
+    f = bf16.to_f64(out)
+    assert np.isnan(f[4:6]).all()
+    assert np.isnan(f[s.P]).all()  # (NaN among a key's numbers: its score, and all of the row)
+    assert not np.isfinite(f[6:46, :, :7]).any()
+    for t in (0, 3):
+        want, spread, size = latent.attention_at(s.q[t][:2], 1, 60000 + t, s.table, clean, s.c, s.scale)
+        check(out[t][:2], want, spread, size, 60001 + t, s.c + s.r, f"token {t}")
+
+
 def test_graph_replays_on_another_stream_and_two_workspaces():
     """A captured step replayed on new inputs, with another step's calls beside it on another stream."""
     a = Step(9, 40, 512, 64, pieces=[(7, 200)], dec=[900, 300]).upload()

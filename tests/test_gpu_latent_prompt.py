@@ -103,6 +103,26 @@ def test_values_that_are_not_finite_reach_only_those_who_see_them(bad):
         assert not np.isfinite(f[i, 0]).any() and np.isfinite(f[i, 1]).all()
 
 
+def test_values_that_are_not_finite_cost_no_wait():
+    """At the start and near the end of a long prompt: those that see them, and no wait of the kernel runs out."""
+    s = Prompts(7, 2, 128, 64, [(600, 30000)])
+    clean = s.kv.copy()
+    s.kv[5, 0, 128 + 70] = 0x7FC0
+    s.kv[30550, 1, 128 + 9] = 0x7FC0
+    s.upload().run()
+    torch.cuda.synchronize()
+    assert int(s.status.item()) == 0
+    out = bits(s.out)
+    f = bf16.to_f64(out)
+    own = np.delete(np.arange(128), 70)  # (number 70 of head 0 is NaN for all: the 6th key's is)
+    for i in range(49, 550, 100):
+        want, spread, size = latent.expanded_at(s.q[i], clean, s.kr, 128, 30000 + i, s.scale)
+        check(out[i, 0, own], want[0, own], spread[0, own], size[0], 30001 + i, 192, f"query {i}, head 0")
+        check(out[i, 1], want[1], spread[1], size[1], 30001 + i, 192, f"query {i}, head 1")
+    assert np.isnan(f[:, 0, 70]).all() and np.isfinite(np.delete(f[:, 0], 70, axis=1)).all()
+    assert np.isnan(f[550:, 1, 9]).all() and np.isfinite(f[:550, 1]).all() and np.isfinite(np.delete(f[:, 1], 9, axis=1)).all()
+
+
 def test_starts_that_do_not_ascend_or_lie_outside():
     s = Prompts(4, 2, 64, 64, [(30, 0), (40, 0), (50, 0)]).upload()
     want = bits(s.run().out).copy()
