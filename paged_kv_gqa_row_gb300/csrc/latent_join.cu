@@ -7,17 +7,20 @@ namespace lnk {
 namespace {
 
 // Joins the partial sums of the units that the shares cut.  The blocks of all shares that
-// start inside one unit divide its rows: a warp takes a row where the unit has up to kFewParts
-// parts, else a block 128 numbers of a row, its warps the parts in turn (a long row's parts are as
-// many as the shares).  What a launch takes is latency and cold instruction caches, so the
+// start inside one unit divide its rows: a warp takes a row, part after part, or a block 128
+// numbers of a row, its warps the parts in turn (a long row's parts are as many as the
+// shares), whichever ends first: 8 rows of 100 to 1500 keys and 64 heads, whose units have few
+// blocks, 43 us with blocks from nine parts on, 21 us so.
+// What a launch takes is latency and cold instruction caches, so the
 // first numbers are asked for before their weights are known, and the blocks are so few and
 // small that all are on the SMs when the first kernel ends.  Both kernels, decode of 32
 // rows of 128 heads, 64 rows of 32, 2 long rows of 40: eight small blocks a share, a warp
 // for 128 numbers of a row, 63.6, 71.2 and 62.9 us; 4 blocks an SM 59.6, 75.0 and 69.7; these 2
-// an SM 56.8, 68.6 and 64.2; one 63.6, 71.0 and 65.7; 16 parts of a warp at once 64.4, 72.9, 68.7.
+// an SM 56.8, 68.6 and 64.2; one 63.6, 71.0 and 65.7; 16 parts of a warp at once 64.4, 72.9, 68.7;
+// a third form, a warp for 128 numbers, beside these two 57.4, 74.9 and 80.
 constexpr int kJoinThreads = 256;
 constexpr int kJoinCtasPerSm = 2;
-constexpr int kFewParts = 8;
+constexpr int kBlockItem = 4;  // what a block's 128 numbers take, in parts of a warp's row
 constexpr int kAtOnce = 12;  // parts a warp of a block has under way
 
 __device__ __forceinline__ void add_part(float4& acc, float f, const float4& x) {
@@ -45,7 +48,7 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm)
   const int parts = cl - c0 + 2;                                     // shares c0 - 1 .. cl
   const int nb = C / 128, rows = cut.nt * p.heads;
   const int blocks = (cl - c0 + 1) * per_share, block = (share - c0) * per_share + static_cast<int>(blockIdx.x) % per_share;
-  const bool few = parts <= kFewParts;
+  const bool few = parts <= 32 && (rows + 8 * blocks - 1) / (8 * blocks) * parts <= (rows * nb + blocks - 1) / blocks * kBlockItem;
   const int items = few ? rows : rows * nb, step = few ? blocks * (kJoinThreads / 32) : blocks;
   for (int i = few ? block * (kJoinThreads / 32) + warp : block; i < items; i += step) {
     const int r = few ? i : i / nb, d = (few ? 0 : i % nb * 128) + lane * 4;
