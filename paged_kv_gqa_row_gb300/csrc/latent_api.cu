@@ -91,10 +91,14 @@ lnk_status attend(const lnk_latent_desc* desc, const lnk_bf16* q, const int32_t*
   p.num_rows = desc->num_rows;
   p.pages_per_row = desc->pages_per_row;
   p.window = desc->window;
-  // Tiles of 128 rows on pairs of SMs for more heads than 64, and where prompt tokens fill one
-  // for every pair (a step of 272 tokens of 64 heads and 32 decode rows: 148 us so, 197 us in
-  // tiles of 64); else of 64 (decode rows alone never share a tile: no more rows than heads need).
-  const bool pairs = p.heads > kLatentRows || static_cast<long long>(P) * p.heads >= static_cast<long long>(sms) * kLatentRows;
+  // Tiles of 128 rows on pairs of SMs for more heads than 64 (64 decode rows of 128 heads: 85.6
+  // us so, 111 in two tiles of 64), and for launches of so many prompt tokens that their
+  // products weigh more than the pages' way to the SMs (with 32 decode rows of 2000 to 4000 keys,
+  // 4 pieces of 32 tokens of 64 heads: 88 us so, 110 in tiles of 64; of 16 tokens 66 and 70; of 4
+  // 49 and 49; of 16 tokens of 16 heads 49 and 47).  Else tiles of 64, or of 32 or 16 for decode
+  // rows of fewer heads, which never share a tile (64 rows of 16 heads, 3000 to 5000 keys: 59.8
+  // us in 16, 61.4 in 32, 66.4 in 64, 74.1 on pairs).
+  const bool pairs = p.heads > kLatentRows || static_cast<long long>(P) * p.heads >= static_cast<long long>(sms) * 16;
   p.tile_rows = pairs ? 2 * kLatentRows : (P > 0 || p.heads > 32 ? 64 : (p.heads > 16 ? 32 : 16));
   p.slot_rows = std::max(kLatentRows, p.tile_rows);
   p.tile_tokens = std::max(1, p.tile_rows / p.heads);
@@ -103,7 +107,7 @@ lnk_status attend(const lnk_latent_desc* desc, const lnk_bf16* q, const int32_t*
   if (p.teams <= 0) return LNK_ERANGE;
   long long most = p.pages_per_row;  // pages of a token
   if (p.window > 0) most = std::min<long long>(most, (p.window - 1) / kPage + 2);
-  p.whole = most <= kWholePages;
+  p.whole = most <= kWholePages;  // (and there is no second kernel: 64 rows of 100 to 500 keys 17.4 us so, 19.6 with it)
   p.scale_log2 = latent_scale_log2(desc);
 
   const long long width = desc->latent_dim + desc->rope_dim;
