@@ -6,6 +6,10 @@
 // stored number is rounded once, to bf16: in float32 where its error bound leaves no doubt
 // about that rounding, else from the float-pair arithmetic of rope_math.cuh, in which the
 // norm's sum of squares and factor are computed throughout.
+//
+// Bound: one chain of dependent reads for few tokens (64 tokens of 64 heads: 2.9 us), the issue
+// of instructions for many (2000 tokens of 40 heads, 27 MB: 11.0 us, 1100 a warp; 4.05 at the
+// copy rate).
 #include <algorithm>
 
 #include "latent.cuh"

@@ -30,8 +30,12 @@
 //
 // A value that is not finite, at a key that some rows of a tile see and others do not,
 // would reach all of them through 0 * NaN.  Key rows that no token of the tile sees are
-// zeroed before they are values; a row whose output is not finite while its sum is
-// computes again from its own keys (attend_again).
+// zeroed before they are values; a row whose output is not finite while its sum is, and
+// which does not see such a key of the tile, computes again from its own (attend_again).
+//
+// Bound: HBM while all CTAs stream (64 rows of 32 heads, 512 to 8192 keys: 322 MB in 45 us, the
+// copy rate), then the starts, the tiles' ends and the join: 68.6 us, 4.8 TB/s, where one wave
+// of prefetches into L2 ahead of the copies took 5 us more.
 #include "latent_units.cuh"
 #include "ptx.cuh"
 
