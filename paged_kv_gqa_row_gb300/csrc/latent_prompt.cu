@@ -6,20 +6,18 @@
 // A tile is 256 consecutive queries of one prompt and one head, taken by a cluster of two
 // CTAs as one 2-SM unit (CTA rank r owns rows 128 r .. + 127 in its tensor-memory lanes);
 // the prompt's keys are streamed 128 a step:
-//   S_b[256 x 128] = Q K_j^T   K_j: rank r holds keys 64 r .. + 63 of the step, D + R
-//                              numbers each, K-major;
-//   O[256 x 128]  += P_b V_j   P_b from tensor memory, V_j MN-major: rank r holds value
-//                              columns 64 r .. + 63 of all 128 keys.
-// S and P are double-buffered; two groups of softmax warps take the steps in turn, so
-// that one's loads and maxima overlap the other's exponentials.  The row's running maximum
-// passes from group to group through shared memory and moves only when it grows by more
-// than 2^8, which is when O is rescaled (the scheme of the paged prompt kernel, chunk.cu).
-//
-// The clusters stay on their SMs and take tiles in turn: the copies of the next tile's
-// queries, keys and values, and its first products, overlap the end of the one before.
-// (Four prompts of 1024 to 2047 tokens, 32 heads: 180 us with a cluster a tile, 140 us so with
-// one producer for keys and values, 132 with two: 0.78 Pflop/s.  Bound: the chain of a step,
-// product, softmax and product; the tensor pipe is active 46% of the time.)
+//   S[256 x 128]  = Q K_j^T   K_j: rank r holds keys 64 r .. + 63 of the step, D + R
+//                             numbers each, K-major;
+//   O[256 x 128] += P V_j     P from tensor memory, written over the scores that it is made
+//                             from; V_j MN-major: rank r holds value columns 64 r .. + 63 of
+//                             all 128 keys.
+// A step is a chain: product, softmax, product.  So a cluster has two tiles under way, each with
+// its own half of tensor memory (scores and output), its own query rows, rings of keys and
+// values, producer, issuer and softmax warps: two workers that share nothing but the pipes, one's
+// products running while the other's softmax does, ends of tiles included.  A row belongs to one
+// thread from its first key to its stored output.  Its running maximum moves only when it
+// grows by more than 2^8, which is when O is rescaled (the scheme of the paged prompt
+// kernel, chunk.cu).
 //
 // Tile ids: prompt n's tiles are base(n) = q_starts[n] / 256 + n onwards, which leaves
 // every prompt room for its tiles without a sum over the prompts before it; ids without
@@ -37,7 +35,8 @@ namespace lnk {
 namespace {
 
 constexpr int kThreads = 12 * 32;
-constexpr int kStages = 3;
+constexpr int kWorkers = 2;               // tiles that a cluster has under way
+constexpr int kStages = 2;                // steps of keys in a worker's ring (of values: one)
 constexpr int kRows = 128;                // query rows per CTA = tensor-memory lanes
 constexpr int kTileRows = 2 * kRows;
 constexpr int kStepKeys = 128;
@@ -50,23 +49,22 @@ struct PromptSmem {
   static constexpr int kKStage = kBoxesK * kBoxBytes;       // this CTA's 64 keys
   static constexpr int kVStage = 2 * kBoxBytes;             // 128 keys, 64 columns
   static constexpr int kQBox = kRows * 128;
+  static constexpr int kQ = kBoxesK * kQBox;                // this CTA's 128 query rows
   static constexpr uint32_t kTmemCols = 512;
-  static constexpr uint32_t kColS = 0, kColP = 256, kColO = 384;
-  static constexpr size_t kring = 0;
-  static constexpr size_t vring = kring + size_t(kStages) * kKStage;
-  static constexpr size_t qsm = vring + size_t(kStages) * kVStage;
-  static constexpr int kQ = kBoxesK * kQBox;                // this CTA's 128 query rows; two tiles' worth
-  static constexpr size_t bars = qsm + 2 * size_t(kQ);
-  // kfull, kempty, vfull, vempty [stages], sfull[2], sfree[2], pfull[2], pvdone[2], odone, ofree,
-  // qfull[2], qempty[2], iempty[2]
-  static constexpr int kNumBars = 4 * kStages + 16;
-  static constexpr size_t misc = bars + kNumBars * sizeof(uint64_t);  // [0] abort, [1] tensor memory, [2] tiles in order
-  static constexpr size_t info = misc + 64;                    // [2] PromptTile: the tiles under way
-  static constexpr size_t order = info + 64;                   // [kMaxOrderedTiles] tile ids, 16 bits each
-  // softmax groups' hand-off: max and ok [2 step parities][128]; at a tile's end max, sum and
-  // ok [2 tile parities][2 groups][128].  (During set-up: the tiles' costs.)
-  static constexpr size_t xchg = order + kMaxOrderedTiles * 2;
-  static constexpr size_t end = xchg + 16 * kRows * 4;
+  static constexpr uint32_t kColS = 0, kColO = 256;         // [worker] 128 columns each; P in the first 64 of S
+  // a worker's query rows, keys and values
+  static constexpr size_t q = 0;
+  static constexpr size_t k = q + kQ;
+  static constexpr size_t v = k + size_t(kStages) * kKStage;
+  static constexpr size_t worker = v + kVStage;
+  // [worker] kfull, kempty [stages], qfull[2], iempty[2], qempty, vfull, vempty, sfull, pfull, pvdone
+  static constexpr size_t bars = kWorkers * worker;
+  static constexpr int kNumBars = 2 * kStages + 10;
+  static constexpr size_t misc = bars + kWorkers * kNumBars * sizeof(uint64_t);  // [0] abort, [1] tensor memory, [2] tiles in order
+  static constexpr size_t info = misc + 64;                    // [worker][2] PromptTile: the tiles under way
+  static constexpr size_t order = info + 128;                  // [kMaxOrderedTiles] tile ids, 16 bits each
+  static constexpr size_t end = order + kMaxOrderedTiles * 2;
+  static_assert(kMaxOrderedTiles * 4 <= worker, "the tiles' costs lie in a ring during set-up");
   static constexpr size_t bytes = end + 1024;
   static_assert(bytes <= 232448, "shared memory");
 };
@@ -78,6 +76,7 @@ struct PromptTile {
   int bad;
   int h;           // query head
 };
+static_assert(sizeof(PromptTile) * 4 <= 128, "room for the tiles under way");
 
 __device__ __forceinline__ PromptTile prompt_tile(const LatentPromptParams& p, int id) {
   int a = 0, b = p.prompts - 1;  // the last prompt whose base is at most id
@@ -192,54 +191,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   using L = PromptSmem<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const uint32_t kfull = smem_addr(smem + L::bars);
-  const uint32_t kempty = kfull + 8 * kStages, vfull = kempty + 8 * kStages, vempty = vfull + 8 * kStages;
-  const uint32_t sfull = vempty + 8 * kStages;  // [2] Q.K^T into S_b finished
-  const uint32_t sfree = sfull + 16;            // [2] the softmax has read S_b (rank 0 only)
-  const uint32_t pfull = sfree + 16;            // [2] P_b written (rank 0 only)
-  const uint32_t pvdone = pfull + 16;           // [2] P.V from P_b finished
-  const uint32_t odone = pvdone + 16;           // a tile's last P.V
-  const uint32_t ofree = odone + 8;             // both CTAs have read O (rank 0 only)
-  const uint32_t qfull = ofree + 8;             // [2] a tile's queries and its PromptTile are there
-  const uint32_t qempty = qfull + 16;           // [2] its last Q.K^T finished
-  const uint32_t iempty = qempty + 16;          // [2] its PromptTile was read
-  int* misc = reinterpret_cast<int*>(smem + L::misc);
-  volatile int* abort_flag = misc;
-  volatile PromptTile* info = reinterpret_cast<volatile PromptTile*>(smem + L::info);
-  uint16_t* order = reinterpret_cast<uint16_t*>(smem + L::order);
-
   const int tid = threadIdx.x, warp = __reduce_max_sync(0xffffffffu, tid >> 5), lane = tid & 31;
   const uint32_t rank = cluster_cta_rank();
+  // worker 0: producer 0, issuer or relay 1, softmax 2-5; worker 1: softmax 6-9, 10, 11
+  const int g = warp >= 6 ? 1 : 0;
+  const uint32_t kfull = smem_addr(smem + L::bars) + g * (L::kNumBars * 8);
+  const uint32_t kempty = kfull + 8 * kStages;
+  const uint32_t qfull = kempty + 8 * kStages;  // [2] a tile's queries and its PromptTile are there
+  const uint32_t iempty = qfull + 16;           // [2] its PromptTile was read
+  const uint32_t qempty = iempty + 16;          // its last Q.K^T finished
+  const uint32_t vfull = qempty + 8, vempty = vfull + 8;
+  const uint32_t sfull = vempty + 8;            // Q.K^T finished (and the P.V before it)
+  const uint32_t pfull = sfull + 8;             // P written (rank 0 only)
+  const uint32_t pvdone = pfull + 8;            // P.V finished
+  const uint32_t smem_w = smem_addr(smem) + g * static_cast<uint32_t>(L::worker);
+  int* misc = reinterpret_cast<int*>(smem + L::misc);
+  volatile int* abort_flag = misc;
+  volatile PromptTile* info = reinterpret_cast<volatile PromptTile*>(smem + L::info) + 2 * g;
+  uint16_t* order = reinterpret_cast<uint16_t*>(smem + L::order);
 
-  if (tid == 0) {
+  if (lane == 0 && (warp == 0 || warp == 11)) {
     // rank 0's full barriers also count the relay's arrival for rank 1's copy
     const uint32_t copies = rank == 0 ? 2 : 1;
     for (int i = 0; i < kStages; ++i) {
       mbar_init(kfull + 8 * i, copies);
       mbar_init(kempty + 8 * i, 1);
-      mbar_init(vfull + 8 * i, copies);
-      mbar_init(vempty + 8 * i, 1);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(sfull + 8 * b, 1);
-      mbar_init(sfree + 8 * b, 8);  // one softmax group (four warps) in each CTA
-      mbar_init(pfull + 8 * b, 8);
-      mbar_init(pvdone + 8 * b, 1);
       mbar_init(qfull + 8 * b, copies);
-      mbar_init(qempty + 8 * b, 1);
-      mbar_init(iempty + 8 * b, 10);  // the softmax warps, the values' producer, their issuer or relay
+      mbar_init(iempty + 8 * b, 5);  // the softmax warps, the issuer or relay
     }
-    mbar_init(odone, 1);
-    mbar_init(ofree, 16);
+    mbar_init(qempty, 1);
+    mbar_init(vfull, copies);
+    mbar_init(vempty, 1);
+    mbar_init(sfull, 1);
+    mbar_init(pfull, 8);  // four softmax warps in each CTA
+    mbar_init(pvdone, 1);
+    fence_mbarrier_init();
+  }
+  if (tid == 0) {
     *abort_flag = 0;
     misc[2] = p.tiles;
-    fence_mbarrier_init();
   }
   if (warp == 1) tmem2_alloc(smem_addr(misc + 1), L::kTmemCols);
   // ---- tiles with the most keys first ----
   const bool ordered = p.tiles <= kMaxOrderedTiles;
   if (ordered) {
-    int* cost = reinterpret_cast<int*>(smem + L::xchg);
+    int* cost = reinterpret_cast<int*>(smem);
     for (int i = tid; i < p.tiles; i += kThreads) {
       const PromptTile x = prompt_tile(p, i);
       cost[i] = x.n > 0 ? x.keys + 1 : 0;
@@ -256,6 +254,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       order[rk] = static_cast<uint16_t>(i);
       if (ci == 0) atomicMin(misc + 2, rk);  // (from here on: nothing to do)
     }
+    fence_proxy_async_smem();  // (copies will write where the costs were)
   }
   // barriers initialised and tensor memory allocated in both CTAs before any
   // thread of either uses them
@@ -264,17 +263,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(misc[1]));
 
-  if (warp == 0) {
+  if (warp == 0 || warp == 11) {
     // ============================== producer ==============================
     if (lane == 0) {
-      // The clusters take the items (tile, head) in turn, in the tiles' order, every other
+      // The workers take the items (tile, head) in turn, in the tiles' order, every other
       // round backwards.
       const long long items = static_cast<long long>(misc[2]) * p.heads;
-      const int clusters = static_cast<int>(gridDim.x >> 1), cid = static_cast<int>(blockIdx.x >> 1);
-      int it = 0, js = 0, nk = 0;  // tiles, steps; copies issued
+      const int clusters = static_cast<int>(gridDim.x >> 1), workers = clusters * kWorkers;
+      const int wid = static_cast<int>(blockIdx.x >> 1) + g * clusters;
+      int it = 0, nk = 0, nv = 0;  // tiles; copies issued
       bool ok = true;
-      for (long long k = 0; ok && k * clusters < items; ++k) {
-        const long long i = k * clusters + (k & 1 ? clusters - 1 - cid : cid);
+      for (long long k = 0; ok && k * workers < items; ++k) {
+        const long long i = k * workers + (k & 1 ? workers - 1 - wid : wid);
         if (i >= items) continue;
         const int at = static_cast<int>(i / p.heads);
         PromptTile x = prompt_tile(p, ordered ? order[at] : p.tiles - 1 - at);
@@ -282,8 +282,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (!ordered && x.bad && x.h == 0 && rank == 0 && p.status != nullptr) atomicOr(p.status, LNK_DEV_SEGMENT);
         if (x.n <= 0) continue;
         const int b = it & 1;
-        if (it >= 2) ok = mbar_wait(qempty + 8 * b, ((it >> 1) - 1) & 1, abort_flag) &&
-                          mbar_wait(iempty + 8 * b, ((it >> 1) - 1) & 1, abort_flag);
+        if (it >= 1) ok = mbar_wait(qempty, (it - 1) & 1, abort_flag);
+        if (ok && it >= 2) ok = mbar_wait(iempty + 8 * b, ((it >> 1) - 1) & 1, abort_flag);
         if (!ok) break;
         info[b].q0 = x.q0;
         info[b].n = x.n;
@@ -293,29 +293,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         info[b].h = x.h;
         mbar_arrive_expect_tx(qfull + 8 * b, L::kQ);
         for (int c = 0; c < L::kBoxesK; ++c)
-          tma_load_3d(smem_addr(smem + L::qsm) + b * L::kQ + c * L::kQBox, &qmap, c * kBoxCols, x.h,
+          tma_load_3d(smem_w + static_cast<uint32_t>(L::q) + c * L::kQBox, &qmap, c * kBoxCols, x.h,
                       x.q0 + static_cast<int>(rank) * kRows, qfull + 8 * b);
         ++it;
         const int nsteps = (x.keys + kStepKeys - 1) / kStepKeys;
-        for (int j = 0; j < nsteps; ++j, ++js) {
-          const int s = js % kStages;
-          if (js >= kStages) ok = mbar_wait(kempty + 8 * s, ((js / kStages) - 1) & 1, abort_flag);
-          if (!ok) break;
-          // this CTA's 64 keys of the step
-          uint32_t dst = smem_addr(smem + L::kring) + s * L::kKStage;
-          const int y = x.k0 + j * kStepKeys, yk = y + static_cast<int>(rank) * 64;
-          mbar_arrive_expect_tx(kfull + 8 * s, L::kKStage);
+        // keys a step ahead of the values, in the order in which the products free them
+        for (int j = 0; j <= nsteps; ++j) {
+          if (j < nsteps) {
+            const int s = nk % kStages;
+            if (nk >= kStages) ok = mbar_wait(kempty + 8 * s, ((nk / kStages) - 1) & 1, abort_flag);
+            if (!ok) break;
+            // this CTA's 64 keys of the step
+            const uint32_t dst = smem_w + static_cast<uint32_t>(L::k) + s * L::kKStage;
+            const int y = x.k0 + j * kStepKeys + static_cast<int>(rank) * 64;
+            mbar_arrive_expect_tx(kfull + 8 * s, L::kKStage);
 #pragma unroll
-          for (int c = 0; c < D / 64; ++c) tma_load_3d(dst + c * kBoxBytes, &kvmap, c * kBoxCols, x.h, yk, kfull + 8 * s);
-          tma_load_2d(dst + (D / 64) * kBoxBytes, &rmap, 0, yk, kfull + 8 * s);
-          ++nk;
+            for (int c = 0; c < D / 64; ++c) tma_load_3d(dst + c * kBoxBytes, &kvmap, c * kBoxCols, x.h, y, kfull + 8 * s);
+            tma_load_2d(dst + (D / 64) * kBoxBytes, &rmap, 0, y, kfull + 8 * s);
+            ++nk;
+          }
+          if (j > 0) {
+            if (nv >= 1) ok = mbar_wait(vempty, (nv - 1) & 1, abort_flag);
+            if (!ok) break;
+            // this CTA's value columns of the step's 128 keys
+            const uint32_t dst = smem_w + static_cast<uint32_t>(L::v);
+            const int xv = D + static_cast<int>(rank) * kBoxCols, y = x.k0 + (j - 1) * kStepKeys;
+            mbar_arrive_expect_tx(vfull, L::kVStage);
+            tma_load_3d(dst, &kvmap, xv, x.h, y, vfull);
+            tma_load_3d(dst + kBoxBytes, &kvmap, xv, x.h, y + 64, vfull);
+            ++nv;
+          }
         }
       }
       const int tiles = it;
       if (ok) {  // no more tiles
         const int b = it & 1;
-        if (it >= 2) ok = mbar_wait(qempty + 8 * b, ((it >> 1) - 1) & 1, abort_flag) &&
-                          mbar_wait(iempty + 8 * b, ((it >> 1) - 1) & 1, abort_flag);
+        if (it >= 2) ok = mbar_wait(iempty + 8 * b, ((it >> 1) - 1) & 1, abort_flag);
         if (ok) {
           info[b].n = -1;
           mbar_arrive(qfull + 8 * b);
@@ -324,63 +337,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // do not leave while a copy may still land in this CTA's memory
       if (tiles > 0) drain(qfull + 8 * ((tiles - 1) & 1), ((tiles - 1) >> 1) & 1);
       for (int k = max(0, nk - kStages); k < nk; ++k) drain(kfull + 8 * (k % kStages), (k / kStages) & 1);
+      if (nv > 0) drain(vfull, (nv - 1) & 1);
     }
-  } else if (warp == 11) {
-    // ========================== the values' producer =======================
-    // (a warp of its own: values are needed, and leave, later than keys)
-    if (lane == 0) {
-      int js = 0, nv = 0;
-      bool ok = true;
-      for (int it = 0; ok; ++it) {
-        const int b = it & 1;
-        if (!mbar_wait(qfull + 8 * b, (it >> 1) & 1, abort_flag)) break;
-        const int n = info[b].n, k0 = info[b].k0, h = info[b].h;
-        const int nsteps = (info[b].keys + kStepKeys - 1) / kStepKeys;
-        mbar_arrive(iempty + 8 * b);
-        if (n < 0) break;
-        for (int j = 0; j < nsteps; ++j, ++js) {
-          const int s = js % kStages;
-          if (js >= kStages) ok = mbar_wait(vempty + 8 * s, ((js / kStages) - 1) & 1, abort_flag);
-          if (!ok) break;
-          // this CTA's value columns of the step's 128 keys
-          const uint32_t dst = smem_addr(smem + L::vring) + s * L::kVStage;
-          const int xv = D + static_cast<int>(rank) * kBoxCols, y = k0 + j * kStepKeys;
-          mbar_arrive_expect_tx(vfull + 8 * s, L::kVStage);
-          tma_load_3d(dst, &kvmap, xv, h, y, vfull + 8 * s);
-          tma_load_3d(dst + kBoxBytes, &kvmap, xv, h, y + 64, vfull + 8 * s);
-          ++nv;
-        }
-      }
-      for (int k = max(0, nv - kStages); k < nv; ++k) drain(vfull + 8 * (k % kStages), (k / kStages) & 1);
-    }
-  } else if (warp == 1) {
+  } else if (warp == 1 || warp == 10) {
     if (rank != 0) {
-      // ============= relay of queries and keys (rank 1 to rank 0) ============
+      // ========= relay of queries, keys and values (rank 1 to rank 0) ========
       if (lane == 0) {
-        const uint32_t kfull0 = mapa_shared(kfull, 0), qfull0 = mapa_shared(qfull, 0);
+        const uint32_t kfull0 = mapa_shared(kfull, 0), qfull0 = mapa_shared(qfull, 0), vfull0 = mapa_shared(vfull, 0);
         bool ok = true;
-        for (int it = 0, js = 0; ok; ++it) {
+        for (int it = 0, nk = 0, nv = 0; ok; ++it) {
           const int b = it & 1;
           if (!mbar_wait(qfull + 8 * b, (it >> 1) & 1, abort_flag)) break;
           const int n = info[b].n, nsteps = (info[b].keys + kStepKeys - 1) / kStepKeys;
+          mbar_arrive(iempty + 8 * b);
           mbar_arrive_remote(qfull0 + 8 * b);
           if (n < 0) break;
-          for (int j = 0; j < nsteps; ++j, ++js) {
-            ok = mbar_wait(kfull + 8 * (js % kStages), (js / kStages) & 1, abort_flag);
-            if (!ok) break;
-            mbar_arrive_remote(kfull0 + 8 * (js % kStages));
+          for (int j = 0; j <= nsteps; ++j) {
+            if (j < nsteps) {
+              ok = mbar_wait(kfull + 8 * (nk % kStages), (nk / kStages) & 1, abort_flag);
+              if (!ok) break;
+              mbar_arrive_remote(kfull0 + 8 * (nk % kStages));
+              ++nk;
+            }
+            if (j > 0) {
+              ok = mbar_wait(vfull, nv & 1, abort_flag);
+              if (!ok) break;
+              mbar_arrive_remote(vfull0);
+              ++nv;
+            }
           }
         }
       }
     } else {
-      // ======================= Q.K^T issuer (rank 0) ========================
+      // ============================ issuer (rank 0) =========================
       // (The whole warp, on values that reductions make the same in all its threads: from one
       // thread's branch, between the softmax warps, a product took 110 clocks to issue.)
       constexpr uint32_t kIdS = umma_idesc_bf16(kTileRows, kStepKeys, 0, 0);
-      const uint64_t kdesc = umma_desc_sw128(smem_addr(smem + L::kring), 0, 1024);
-      const uint64_t qdesc = umma_desc_sw128(smem_addr(smem + L::qsm), 0, 1024);
+      constexpr uint32_t kIdPV = umma_idesc_bf16(kTileRows, 128, 0, 1);
+      const uint64_t qdesc = umma_desc_sw128(smem_w + static_cast<uint32_t>(L::q), 0, 1024);
+      const uint64_t kdesc = umma_desc_sw128(smem_w + static_cast<uint32_t>(L::k), 0, 1024);
+      const uint64_t vdesc = umma_desc_sw128(smem_w + static_cast<uint32_t>(L::v), 0, 1024);
       const uint32_t k_lo = static_cast<uint32_t>(kdesc), k_hi = static_cast<uint32_t>(kdesc >> 32);
       const uint32_t q_lo = static_cast<uint32_t>(qdesc), q_hi = static_cast<uint32_t>(qdesc >> 32);
+      const uint32_t v_lo = static_cast<uint32_t>(vdesc), v_hi = static_cast<uint32_t>(vdesc >> 32);
+      const uint32_t sc = tmem + L::kColS + g * 128u, oc = tmem + L::kColO + g * 128u;
       auto wait = [&](uint32_t bar, uint32_t parity) {
         return __reduce_and_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag) ? 1u : 0u) != 0u;
       };
@@ -390,111 +390,57 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (!wait(qfull + 8 * qb, (it >> 1) & 1)) break;
         const int n = __reduce_max_sync(0xffffffffu, info[qb].n);
         const int nsteps = __reduce_max_sync(0xffffffffu, (info[qb].keys + kStepKeys - 1) / kStepKeys);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(iempty + 8 * qb);
         if (n < 0) break;
-        const uint32_t qd = q_lo + ((qb * L::kQ) >> 4);
-        // S_b of a step, once the softmax has read S_b of two steps before and both CTAs' keys are there
+#pragma unroll 1
         for (int j = 0; j < nsteps; ++j, ++js) {
-          const int b = js & 1, s = js % kStages;
-          ok = (js < 2 || wait(sfree + 8 * b, ((js - 2) >> 1) & 1)) && wait(kfull + 8 * s, (js / kStages) & 1);
+          const int s = js % kStages;
+          // S, over the P that the P.V before reads
+          ok = (js < 1 || wait(pvdone, (js - 1) & 1)) && wait(kfull + 8 * s, (js / kStages) & 1);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t sc = tmem + L::kColS + static_cast<uint32_t>(b) * kStepKeys;
           const uint32_t kd = k_lo + ((s * L::kKStage) >> 4);
 #pragma unroll
           for (int kk = 0; kk < D / 16 + 2; ++kk)
-            umma2_ss_warp(sc, qd + (((kk >> 2) * L::kQBox + (kk & 3) * 32) >> 4), q_hi,
+            umma2_ss_warp(sc, q_lo + (((kk >> 2) * L::kQBox + (kk & 3) * 32) >> 4), q_hi,
                           kd + (((kk >> 2) * kBoxBytes + (kk & 3) * 32) >> 4), k_hi, kIdS, kk > 0 ? 1u : 0u);
           if (p.rope_dim == 64) {
 #pragma unroll
             for (int kk = D / 16 + 2; kk < D / 16 + 4; ++kk)
-              umma2_ss_warp(sc, qd + (((kk >> 2) * L::kQBox + (kk & 3) * 32) >> 4), q_hi,
+              umma2_ss_warp(sc, q_lo + (((kk >> 2) * L::kQBox + (kk & 3) * 32) >> 4), q_hi,
                             kd + (((kk >> 2) * kBoxBytes + (kk & 3) * 32) >> 4), k_hi, kIdS, 1u);
           }
-          umma2_commit_both_warp(sfull + 8 * b);
+          umma2_commit_both_warp(sfull);
           umma2_commit_both_warp(kempty + 8 * s);
-        }
-        umma2_commit_both_warp(qempty + 8 * qb);
-      }
-      __syncwarp();
-    }
-  } else if (warp == 10) {
-    if (rank != 0) {
-      // ====================== relay of values (rank 1) ======================
-      if (lane == 0) {
-        const uint32_t vfull0 = mapa_shared(vfull, 0);
-        bool ok = true;
-        for (int it = 0, js = 0; ok; ++it) {
-          const int b = it & 1;
-          if (!mbar_wait(qfull + 8 * b, (it >> 1) & 1, abort_flag)) break;
-          const int n = info[b].n, nsteps = (info[b].keys + kStepKeys - 1) / kStepKeys;
-          mbar_arrive(iempty + 8 * b);
-          if (n < 0) break;
-          for (int j = 0; j < nsteps; ++j, ++js) {
-            ok = mbar_wait(vfull + 8 * (js % kStages), (js / kStages) & 1, abort_flag);
-            if (!ok) break;
-            mbar_arrive_remote(vfull0 + 8 * (js % kStages));
-          }
-        }
-      }
-    } else {
-      // ========================= P.V issuer (rank 0) ========================
-      constexpr uint32_t kIdPV = umma_idesc_bf16(kTileRows, 128, 0, 1);
-      const uint64_t vdesc = umma_desc_sw128(smem_addr(smem + L::vring), 0, 1024);
-      const uint32_t v_lo = static_cast<uint32_t>(vdesc), v_hi = static_cast<uint32_t>(vdesc >> 32);
-      auto wait = [&](uint32_t bar, uint32_t parity) {
-        return __reduce_and_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag) ? 1u : 0u) != 0u;
-      };
-      bool ok = true;
-      for (int it = 0, js = 0, te = 0; ok; ++it) {  // te: tiles with steps
-        const int qb = it & 1;
-        if (!wait(qfull + 8 * qb, (it >> 1) & 1)) break;
-        const int n = __reduce_max_sync(0xffffffffu, info[qb].n);
-        const int nsteps = __reduce_max_sync(0xffffffffu, (info[qb].keys + kStepKeys - 1) / kStepKeys);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(iempty + 8 * qb);
-        if (n < 0) break;
-        for (int j = 0; j < nsteps; ++j, ++js) {
-          const int b = js & 1, s = js % kStages;
-          ok = wait(pfull + 8 * b, (js >> 1) & 1) && wait(vfull + 8 * s, (js / kStages) & 1);
-          // (O of the tile before has been read)
-          if (ok && j == 0 && te > 0) ok = wait(ofree, (te - 1) & 1);
+          if (j + 1 == nsteps) umma2_commit_both_warp(qempty);
+          // (that all rows' P is there says too that the tile before's O has been read)
+          ok = wait(pfull, js & 1) && wait(vfull, js & 1);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t pc = tmem + L::kColP + static_cast<uint32_t>(b) * (kStepKeys / 2);
-          const uint32_t vd = v_lo + ((s * L::kVStage) >> 4);
 #pragma unroll
           for (int kk = 0; kk < kStepKeys / 16; ++kk)
-            umma2_ts_warp(tmem + L::kColO, pc + kk * 8, vd + ((kk * 16 * 128) >> 4), v_hi, kIdPV,
-                          kk > 0 ? 1u : (j > 0 ? 1u : 0u));
-          umma2_commit_both_warp(vempty + 8 * s);
-          umma2_commit_both_warp(pvdone + 8 * b);
-          if (j + 1 == nsteps) umma2_commit_both_warp(odone);
+            umma2_ts_warp(oc, sc + kk * 8, v_lo + ((kk * 16 * 128) >> 4), v_hi, kIdPV, kk > 0 || j > 0 ? 1u : 0u);
+          umma2_commit_both_warp(pvdone);
+          umma2_commit_both_warp(vempty);
         }
-        if (nsteps > 0) ++te;
+        if (nsteps == 0) umma2_commit_both_warp(qempty);
       }
       __syncwarp();
     }
   } else {
     // ============================== softmax ===============================
-    // Group 0 (warps 2-5) takes the even steps of the CTA, group 1 (warps 6-9) the odd ones;
-    // thread r of each group owns query row r of this CTA.  The running max passes from the
-    // group of a step to the group of the next (a named barrier that the publisher arrives on
-    // and the receiver waits on), together with the decision to go on.
-    const int grp = (warp - 2) >> 2;
+    // thread r of a worker's four warps owns query row r of this CTA
     const int qt = warp & 3;
     const int rl = qt * 32 + lane;
     const int row = static_cast<int>(rank) * kRows + rl;
     const uint32_t lanes = static_cast<uint32_t>(qt * 32) << 16;
-    const int bar_pub = 1 + qt + 4 * grp, bar_sub = 1 + qt + 4 * (grp ^ 1), bar_pair = 9 + qt;
-    float* hand_m = reinterpret_cast<float*>(smem + L::xchg);           // [2 step parities][128 rows]
-    int* hand_ok = reinterpret_cast<int*>(smem + L::xchg) + 2 * kRows;  // [2][128]
-    const uint32_t pfull0 = mapa_shared(pfull, 0), sfree0 = mapa_shared(sfree, 0), ofree0 = mapa_shared(ofree, 0);
-    const uint32_t sc = tmem + lanes + L::kColS + static_cast<uint32_t>(grp) * kStepKeys;
-    const uint32_t pcol = tmem + lanes + L::kColP + static_cast<uint32_t>(grp) * (kStepKeys / 2);
+    const uint32_t pfull0 = mapa_shared(pfull, 0);
+    const uint32_t sc = tmem + lanes + L::kColS + g * 128u, oc = tmem + lanes + L::kColO + g * 128u;
     bool ok = true;
-    for (int it = 0, js0 = 0, te = 0; ok; ++it) {
-      const bool there = __all_sync(0xffffffffu, mbar_wait(qfull + 8 * (it & 1), (it >> 1) & 1, abort_flag));
-      if (named_barrier_or(bar_pair, 64, !there)) break;  // (both groups or neither)
+    for (int it = 0, js = 0; ok; ++it) {
+      ok = __all_sync(0xffffffffu, mbar_wait(qfull + 8 * (it & 1), (it >> 1) & 1, abort_flag));
+      if (!ok) break;
       PromptTile tile;
       tile.q0 = info[it & 1].q0;
       tile.n = info[it & 1].n;
@@ -508,41 +454,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int nsteps = (tile.keys + kStepKeys - 1) / kStepKeys;
       const bool live = row < tile.n;
       const int hi = live ? tile.first + row : 0;  // keys that this row sees
-      float* fin_m = reinterpret_cast<float*>(smem + L::xchg) + (4 + 6 * (it & 1)) * kRows;  // [2 groups][128]
-      float* fin_l = fin_m + 2 * kRows;
-      int* fin_ok = reinterpret_cast<int*>(fin_l + 2 * kRows);
-      float m_ref = -INFINITY;   // the row's running max (log2 units) after this group's last step
-      float m_part = -INFINITY;  // reference of this group's partial sum
-      float l_part = 0.f;
-      bool stuck = false;
-      for (int j = (grp ^ js0) & 1; j < nsteps; j += 2) {
-        const int js = js0 + j;
+      float m_ref = -INFINITY;  // the row's running max (log2 units), and its sum's reference
+      float l = 0.f;
+      for (int j = 0; j < nsteps; ++j, ++js) {
         const int kb = j * kStepKeys;
-        const int s = js % kStages;
-        bool okw = !stuck && __all_sync(0xffffffffu, mbar_wait(sfull + 8 * grp, (js >> 1) & 1, abort_flag));
+        ok = __all_sync(0xffffffffu, mbar_wait(sfull, js & 1, abort_flag));
         const bool partial = kb + kStepKeys > tile.keys;
-        if (okw && partial) {
+        if (ok && partial) {
           // keys past the tile's last may hold anything: zero their value rows
-          okw = __all_sync(0xffffffffu, mbar_wait(vfull + 8 * s, (js / kStages) & 1, abort_flag));
-          if (okw && kb + rl >= tile.keys) {
-            uint8_t* vrow = smem + L::vring + size_t(s) * L::kVStage + (rl >> 6) * kBoxBytes + (rl & 63) * 128;
+          ok = __all_sync(0xffffffffu, mbar_wait(vfull, js & 1, abort_flag));
+          if (ok && kb + rl >= tile.keys) {
+            uint8_t* vrow = smem + g * L::worker + L::v + (rl >> 6) * kBoxBytes + (rl & 63) * 128;
 #pragma unroll
             for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(vrow + c * 16) = make_uint4(0u, 0u, 0u, 0u);
           }
           fence_proxy_async_smem();
         }
+        if (!ok) break;
         tc_fence_after();
         float x[kStepKeys];
-        if (okw) {
+        {
           uint32_t r0[32], r1[32], r2[32], r3[32];
           tmem_ld32(sc, r0);
           tmem_ld32(sc + 32, r1);
           tmem_ld32(sc + 64, r2);
           tmem_ld32(sc + 96, r3);
           tmem_ld_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_remote(sfree0 + 8 * grp);
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             x[i] = __uint_as_float(r0[i]);
@@ -550,9 +487,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             x[64 + i] = __uint_as_float(r2[i]);
             x[96 + i] = __uint_as_float(r3[i]);
           }
-        } else {
-#pragma unroll
-          for (int i = 0; i < kStepKeys; ++i) x[i] = -INFINITY;
         }
         const int e0 = live ? hi - kb : kStepKeys;  // visible keys of this step: below e0
         if (!__all_sync(0xffffffffu, e0 >= kStepKeys)) {
@@ -569,38 +503,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         const float mraw = fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
         const float mx = mraw == -INFINITY ? -INFINITY : mraw * p.scale_log2;
-        if (j > 0) {
-          named_barrier_sync(bar_sub, 64);
-          m_ref = hand_m[((js - 1) & 1) * kRows + rl];
-          okw = okw && hand_ok[((js - 1) & 1) * kRows + rl] != 0;
-        }
-        ok = __all_sync(0xffffffffu, okw);
-        float m_new = m_ref, alpha = 1.f;
+        float alpha = 1.f;
         if (mx != -INFINITY) {
           if (m_ref == -INFINITY) {
-            m_new = mx;
+            m_ref = mx;
           } else if (mx > m_ref + kRescaleLog2) {
-            m_new = mx;
             alpha = exp2f(m_ref - mx);
+            m_ref = mx;
+            l *= alpha;
           }
-        }
-        if (j + 1 < nsteps) {
-          hand_m[(js & 1) * kRows + rl] = m_new;
-          hand_ok[(js & 1) * kRows + rl] = ok ? 1 : 0;
-          __syncwarp();
-          named_barrier_arrive(bar_pub, 64);
-        }
-        if (!ok) break;
-        m_ref = m_new;
-        if (m_part != m_ref) {
-          if (m_part != -INFINITY) l_part *= exp2f(m_part - m_ref);
-          m_part = m_ref;
         }
         const float nbase = m_ref == -INFINITY ? 0.f : -m_ref;
         const uint64_t c2 = f32x2(p.scale_log2, p.scale_log2), n2 = f32x2(nbase, nbase);
-        // P_grp is free once P.V of two steps before has read it
-        if (js >= 2) stuck = stuck || !__all_sync(0xffffffffu, mbar_wait(pvdone + 8 * grp, ((js - 2) >> 1) & 1, abort_flag));
-        tc_fence_after();
         uint64_t s2[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
         for (int hh = 0; hh < 4; ++hh) {
@@ -613,111 +527,90 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             s2[i & 3] = add_f32x2(s2[i & 3], f32x2(e0v, e1v));
             pk[i] = pack_bf16x2(e0v, e1v);
           }
-          tmem_st16(pcol + hh * 16, pk);
+          tmem_st16(sc + hh * 16, pk);
         }
         if (__any_sync(0xffffffffu, alpha != 1.f) && j >= 1) {
-          // rescale this row of O between P.V of the step before and of this one (a failed wait
-          // travels with the next hand-off: this one has gone out)
-          stuck = stuck || !__all_sync(0xffffffffu, mbar_wait(pvdone + 8 * ((js - 1) & 1), ((js - 1) >> 1) & 1, abort_flag));
-          tc_fence_after();
+          // rescale this row of O (the P.V of the step before ended before this step's scores came)
 #pragma unroll 1
-          for (int c = 0; c < (stuck ? 0 : 4); ++c) {
+          for (int c = 0; c < 4; ++c) {
             uint32_t r[32];
-            tmem_ld32(tmem + lanes + L::kColO + c * 32, r);
+            tmem_ld32(oc + c * 32, r);
             tmem_ld_wait();
 #pragma unroll
             for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
-            tmem_st32(tmem + lanes + L::kColO + c * 32, r);
+            tmem_st32(oc + c * 32, r);
           }
         }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          if (partial) mbar_arrive_cluster(pfull0 + 8 * grp);  // publishes the zeroed value rows
-          else mbar_arrive_remote(pfull0 + 8 * grp);
+          if (partial) mbar_arrive_cluster(pfull0);  // publishes the zeroed value rows
+          else mbar_arrive_remote(pfull0);
         }
-        {
-          float u0, u1;
-          f32x2_split(add_f32x2(add_f32x2(s2[0], s2[1]), add_f32x2(s2[2], s2[3])), u0, u1);
-          l_part += u0 + u1;
-        }
+        float u0, u1;
+        f32x2_split(add_f32x2(add_f32x2(s2[0], s2[1]), add_f32x2(s2[2], s2[3])), u0, u1);
+        l += u0 + u1;
       }
-      // ---- normalise and store: group g stores half g of the row ----
-      float mf = -INFINITY;
-      if (nsteps > 0) {
-        const bool okw = ok && !stuck && __all_sync(0xffffffffu, mbar_wait(odone, te & 1, abort_flag));
-        tc_fence_after();
-        fin_m[grp * kRows + rl] = m_part;
-        fin_l[grp * kRows + rl] = l_part;
-        fin_ok[grp * kRows + rl] = okw ? 1 : 0;
-        named_barrier_sync(bar_pair, 64);
-        const float mo = fin_m[(grp ^ 1) * kRows + rl], lo_ = fin_l[(grp ^ 1) * kRows + rl];
-        ok = __all_sync(0xffffffffu, okw && fin_ok[(grp ^ 1) * kRows + rl] != 0);
-        mf = fmaxf(m_part, mo);
-        const float la = m_part == -INFINITY ? 0.f : l_part * exp2f(m_part - mf);
-        const float lb = mo == -INFINITY ? 0.f : lo_ * exp2f(mo - mf);
-        l_part = grp == 0 ? la + lb : lb + la;
-      }
-      const float inv = l_part > 0.f ? 1.f / l_part : l_part;  // (a NaN sum makes the row NaN)
-      uint32_t r[D / 2];
-      if (ok && nsteps > 0) {
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t (&rc)[16] = *reinterpret_cast<uint32_t(*)[16]>(r + c * 16);
-          tmem_ld16(tmem + lanes + L::kColO + grp * (D / 2) + c * 16, rc);
-        }
-        tmem_ld_wait();
-        // O may take the next tile's
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_remote(ofree0);
-        ++te;
-      } else {
-#pragma unroll
-        for (int i = 0; i < D / 2; ++i) r[i] = 0u;
-      }
+      // ---- normalise and store, half a row at a time ----
+      if (ok && nsteps > 0) ok = __all_sync(0xffffffffu, mbar_wait(pvdone, (js - 1) & 1, abort_flag));
+      if (!ok) break;
+      tc_fence_after();
+      const float inv = l > 0.f ? 1.f / l : l;  // (a NaN sum makes the row NaN)
+      const bool none = l == 0.f;
       constexpr int kPieces = D / 16;  // 16-byte pieces of half a row
-      uint4 w[kPieces];
-      uint32_t odd = 0u;  // bits 15 and 31: an element is not finite
-      const bool none = l_part == 0.f;
+#pragma unroll 1
+      for (int hf = 0; hf < 2; ++hf) {
+        uint32_t r[D / 2];
+        if (nsteps > 0) {
 #pragma unroll
-      for (int i = 0; i < kPieces; ++i) {
-        float v[8];
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t (&rc)[16] = *reinterpret_cast<uint32_t(*)[16]>(r + c * 16);
+            tmem_ld16(oc + hf * (D / 2) + c * 16, rc);
+          }
+          tmem_ld_wait();
+        } else {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = none ? 0.f : __uint_as_float(r[8 * i + k]) * inv;
-        w[i] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                          pack_bf16x2(v[6], v[7]));
-        odd |= ((w[i].x & 0x7F807F80u) + 0x00800080u) | ((w[i].y & 0x7F807F80u) + 0x00800080u) |
-               ((w[i].z & 0x7F807F80u) + 0x00800080u) | ((w[i].w & 0x7F807F80u) + 0x00800080u);
-      }
-      // (a NaN sum is the row's own: all of it is NaN)
-      const bool again = live && (odd & 0x80008000u) != 0u && l_part == l_part;
-      transpose_pieces<kPieces>(w);
-      uint16_t* o = p.out + (static_cast<size_t>(tile.q0 + (row & ~(kPieces - 1))) * p.heads + tile.h) * D + grp * (D / 2) +
-                    (lane & (kPieces - 1)) * 8;
-#pragma unroll
-      for (int i = 0; i < kPieces; ++i)
-        if ((row & ~(kPieces - 1)) + i < tile.n)
-          *reinterpret_cast<uint4*>(o + static_cast<size_t>(i) * p.heads * D) = w[i];
-      unsigned todo = __ballot_sync(0xffffffffu, again);
-      if (todo != 0u) {
-        const uint16_t* kv = p.kv + (static_cast<size_t>(tile.k0) * p.heads + tile.h) * (2 * D);
-        const int bad_key = last_odd_key<D>(p, kv, max(0, tile.first + row - lane), tile.keys, grp * (D / 2));
-        while (todo != 0u) {
-          const int src = __ffs(todo) - 1;
-          todo &= todo - 1;
-          const int rr = row - lane + src;
-          if (tile.first + rr > bad_key) break;  // (it sees them all: what is not finite is its own; so do those after it)
-          __syncwarp();
-          attend_row<D>(p, p.q + (static_cast<size_t>(tile.q0 + rr) * p.heads + tile.h) * (D + p.rope_dim), kv,
-                        p.k_rope + static_cast<long long>(tile.k0) * p.rope_stride, tile.first + rr,
-                        __shfl_sync(0xffffffffu, mf, src), __shfl_sync(0xffffffffu, inv, src),
-                        p.out + (static_cast<size_t>(tile.q0 + rr) * p.heads + tile.h) * D, grp * (D / 2));
+          for (int i = 0; i < D / 2; ++i) r[i] = 0u;
         }
+        uint4 w[kPieces];
+        uint32_t odd = 0u;  // bits 15 and 31: an element is not finite
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+          float v[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[k] = none ? 0.f : __uint_as_float(r[8 * i + k]) * inv;
+          w[i] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                            pack_bf16x2(v[6], v[7]));
+          odd |= odd_halves(w[i]);
+        }
+        // (a NaN sum is the row's own: all of it is NaN)
+        const bool again = live && odd != 0u && l == l;
+        transpose_pieces<kPieces>(w);
+        uint16_t* o = p.out + (static_cast<size_t>(tile.q0 + (row & ~(kPieces - 1))) * p.heads + tile.h) * D + hf * (D / 2) +
+                      (lane & (kPieces - 1)) * 8;
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i)
+          if ((row & ~(kPieces - 1)) + i < tile.n)
+            *reinterpret_cast<uint4*>(o + static_cast<size_t>(i) * p.heads * D) = w[i];
+        unsigned todo = __ballot_sync(0xffffffffu, again);
+        if (todo != 0u) {
+          const uint16_t* kv = p.kv + (static_cast<size_t>(tile.k0) * p.heads + tile.h) * (2 * D);
+          const int bad_key = last_odd_key<D>(p, kv, max(0, tile.first + row - lane), tile.keys, hf * (D / 2));
+          while (todo != 0u) {
+            const int src = __ffs(todo) - 1;
+            todo &= todo - 1;
+            const int rr = row - lane + src;
+            if (tile.first + rr > bad_key) break;  // (it sees them all: what is not finite is its own; so do those after it)
+            __syncwarp();
+            attend_row<D>(p, p.q + (static_cast<size_t>(tile.q0 + rr) * p.heads + tile.h) * (D + p.rope_dim), kv,
+                          p.k_rope + static_cast<long long>(tile.k0) * p.rope_stride, tile.first + rr,
+                          __shfl_sync(0xffffffffu, m_ref, src), __shfl_sync(0xffffffffu, inv, src),
+                          p.out + (static_cast<size_t>(tile.q0 + rr) * p.heads + tile.h) * D, hf * (D / 2));
+          }
+        }
+        __syncwarp();
       }
-      __syncwarp();
-      js0 += nsteps;
     }
     if (!ok) *abort_flag = 1;
   }
