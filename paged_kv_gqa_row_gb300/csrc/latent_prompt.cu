@@ -57,9 +57,9 @@ struct PromptSmem {
   static constexpr size_t k = q + kQ;
   static constexpr size_t v = k + size_t(kStages) * kKStage;
   static constexpr size_t worker = v + kVStage;
-  // [worker] kfull, kempty [stages], qfull[2], iempty[2], qempty, vfull, vempty, sfull, pfull, pvdone
+  // [worker] kfull, kempty [stages], qfull[2], iempty[2], qempty, vfull, vempty, sfull, pfull[2], pvdone
   static constexpr size_t bars = kWorkers * worker;
-  static constexpr int kNumBars = 2 * kStages + 10;
+  static constexpr int kNumBars = 2 * kStages + 11;
   static constexpr size_t misc = bars + kWorkers * kNumBars * sizeof(uint64_t);  // [0] abort, [1] tensor memory, [2] tiles in order
   static constexpr size_t info = misc + 64;                    // [worker][2] PromptTile: the tiles under way
   static constexpr size_t order = info + 128;                  // [kMaxOrderedTiles] tile ids, 16 bits each
@@ -202,8 +202,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t qempty = iempty + 16;          // its last Q.K^T finished
   const uint32_t vfull = qempty + 8, vempty = vfull + 8;
   const uint32_t sfull = vempty + 8;            // Q.K^T finished (and the P.V before it)
-  const uint32_t pfull = sfull + 8;             // P written (rank 0 only)
-  const uint32_t pvdone = pfull + 8;            // P.V finished
+  const uint32_t pfull = sfull + 8;             // [2] half of P written (rank 0 only)
+  const uint32_t pvdone = pfull + 16;           // P.V finished
   const uint32_t smem_w = smem_addr(smem) + g * static_cast<uint32_t>(L::worker);
   int* misc = reinterpret_cast<int*>(smem + L::misc);
   volatile int* abort_flag = misc;
@@ -225,7 +225,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(vfull, copies);
     mbar_init(vempty, 1);
     mbar_init(sfull, 1);
-    mbar_init(pfull, 8);  // four softmax warps in each CTA
+    for (int i = 0; i < 2; ++i) mbar_init(pfull + 8 * i, 8);  // four softmax warps in each CTA
     mbar_init(pvdone, 1);
     fence_mbarrier_init();
   }
@@ -397,7 +397,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int j = 0; j < nsteps; ++j, ++js) {
           const int s = js % kStages;
           // S, over the P that the P.V before reads
-          ok = (js < 1 || wait(pvdone, (js - 1) & 1)) && wait(kfull + 8 * s, (js / kStages) & 1);
+          ok = wait(kfull + 8 * s, (js / kStages) & 1) && (js < 1 || wait(pvdone, (js - 1) & 1));
           if (!ok) break;
           tc_fence_after();
           const uint32_t kd = k_lo + ((s * L::kKStage) >> 4);
@@ -415,12 +415,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           umma2_commit_both_warp(kempty + 8 * s);
           if (j + 1 == nsteps) umma2_commit_both_warp(qempty);
           // (that all rows' P is there says too that the tile before's O has been read)
-          ok = wait(pfull, js & 1) && wait(vfull, js & 1);
+          ok = wait(vfull, js & 1) && wait(pfull, js & 1);
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
-          for (int kk = 0; kk < kStepKeys / 16; ++kk)
+          for (int kk = 0; kk < kStepKeys / 32; ++kk)
             umma2_ts_warp(oc, sc + kk * 8, v_lo + ((kk * 16 * 128) >> 4), v_hi, kIdPV, kk > 0 || j > 0 ? 1u : 0u);
+          ok = wait(pfull + 8, js & 1);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = kStepKeys / 32; kk < kStepKeys / 16; ++kk)
+            umma2_ts_warp(oc, sc + kk * 8, v_lo + ((kk * 16 * 128) >> 4), v_hi, kIdPV, 1u);
           umma2_commit_both_warp(pvdone);
           umma2_commit_both_warp(vempty);
         }
@@ -515,6 +521,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         const float nbase = m_ref == -INFINITY ? 0.f : -m_ref;
         const uint64_t c2 = f32x2(p.scale_log2, p.scale_log2), n2 = f32x2(nbase, nbase);
+        if (__any_sync(0xffffffffu, alpha != 1.f) && j >= 1) {
+          // rescale this row of O (the P.V of the step before ended before this step's scores came)
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            uint32_t r[16];
+            tmem_ld16(oc + c * 16, r);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
+            tmem_st16(oc + c * 16, r);
+          }
+        }
         uint64_t s2[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
         for (int hh = 0; hh < 4; ++hh) {
@@ -528,25 +546,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             pk[i] = pack_bf16x2(e0v, e1v);
           }
           tmem_st16(sc + hh * 16, pk);
-        }
-        if (__any_sync(0xffffffffu, alpha != 1.f) && j >= 1) {
-          // rescale this row of O (the P.V of the step before ended before this step's scores came)
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t r[32];
-            tmem_ld32(oc + c * 32, r);
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
-            tmem_st32(oc + c * 32, r);
+          if (hh & 1) {  // the products of half of P may begin
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              if (partial) mbar_arrive_cluster(pfull0 + 8 * (hh >> 1));  // publishes the zeroed value rows
+              else mbar_arrive_remote(pfull0 + 8 * (hh >> 1));
+            }
           }
-        }
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if (partial) mbar_arrive_cluster(pfull0);  // publishes the zeroed value rows
-          else mbar_arrive_remote(pfull0);
         }
         float u0, u1;
         f32x2_split(add_f32x2(add_f32x2(s2[0], s2[1]), add_f32x2(s2[2], s2[3])), u0, u1);
