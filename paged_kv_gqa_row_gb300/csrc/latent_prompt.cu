@@ -57,9 +57,9 @@ struct PromptSmem {
   static constexpr size_t k = q + kQ;
   static constexpr size_t v = k + size_t(kStages) * kKStage;
   static constexpr size_t worker = v + kVStage;
-  // [worker] kfull, kempty [stages], qfull[2], iempty[2], qempty, vfull, vempty, sfull, pfull[2], pvdone
+  // [worker] kfull, kempty [stages], qfull[2], iempty[2], qempty, vfull, vempty, sfull, pfull[2], pvdone, efree
   static constexpr size_t bars = kWorkers * worker;
-  static constexpr int kNumBars = 2 * kStages + 11;
+  static constexpr int kNumBars = 2 * kStages + 12;
   static constexpr size_t misc = bars + kWorkers * kNumBars * sizeof(uint64_t);  // [0] abort, [1] tensor memory, [2] tiles in order
   static constexpr size_t info = misc + 64;                    // [worker][2] PromptTile: the tiles under way
   static constexpr size_t order = info + 128;                  // [kMaxOrderedTiles] tile ids, 16 bits each
@@ -161,29 +161,6 @@ __device__ __forceinline__ void drain(uint32_t bar, int parity) {
   }
 }
 
-// NC lanes of neighbouring rows hold NC 16-byte pieces of their row each: afterwards lane i
-// holds piece i of each of the rows, so that a store covers whole lines.
-template <int NC>
-__device__ __forceinline__ void transpose_pieces(uint4 (&w)[NC]) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int b = 1; b < NC; b <<= 1) {
-    const bool up = (lane & b) != 0;
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      if (c & b) continue;
-      const uint4 give = up ? w[c] : w[c | b];
-      uint4 got;
-      got.x = __shfl_xor_sync(0xffffffffu, give.x, b);
-      got.y = __shfl_xor_sync(0xffffffffu, give.y, b);
-      got.z = __shfl_xor_sync(0xffffffffu, give.z, b);
-      got.w = __shfl_xor_sync(0xffffffffu, give.w, b);
-      if (up) w[c] = got;
-      else w[c | b] = got;
-    }
-  }
-}
-
 template <int D>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kvmap,
@@ -193,8 +170,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = __reduce_max_sync(0xffffffffu, tid >> 5), lane = tid & 31;
   const uint32_t rank = cluster_cta_rank();
-  // worker 0: producer 0, issuer or relay 1, softmax 2-5; worker 1: softmax 6-9, 10, 11
-  const int g = warp >= 6 ? 1 : 0;
+  // producers 0 and 2, issuers or relays 1 and 3, softmax 4-7 and 8-11
+  const int g = warp < 4 ? warp >> 1 : (warp - 4) >> 2;
   const uint32_t kfull = smem_addr(smem + L::bars) + g * (L::kNumBars * 8);
   const uint32_t kempty = kfull + 8 * kStages;
   const uint32_t qfull = kempty + 8 * kStages;  // [2] a tile's queries and its PromptTile are there
@@ -204,13 +181,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t sfull = vempty + 8;            // Q.K^T finished (and the P.V before it)
   const uint32_t pfull = sfull + 8;             // [2] half of P written (rank 0 only)
   const uint32_t pvdone = pfull + 16;           // P.V finished
+  const uint32_t efree = pvdone + 8;            // the tile's outputs have left the values' place
   const uint32_t smem_w = smem_addr(smem) + g * static_cast<uint32_t>(L::worker);
   int* misc = reinterpret_cast<int*>(smem + L::misc);
   volatile int* abort_flag = misc;
   volatile PromptTile* info = reinterpret_cast<volatile PromptTile*>(smem + L::info) + 2 * g;
   uint16_t* order = reinterpret_cast<uint16_t*>(smem + L::order);
 
-  if (lane == 0 && (warp == 0 || warp == 11)) {
+  if (lane == 0 && (warp == 0 || warp == 2)) {
     // rank 0's full barriers also count the relay's arrival for rank 1's copy
     const uint32_t copies = rank == 0 ? 2 : 1;
     for (int i = 0; i < kStages; ++i) {
@@ -227,6 +205,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(sfull, 1);
     for (int i = 0; i < 2; ++i) mbar_init(pfull + 8 * i, 8);  // four softmax warps in each CTA
     mbar_init(pvdone, 1);
+    mbar_init(efree, 4);
     fence_mbarrier_init();
   }
   if (tid == 0) {
@@ -263,8 +242,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(misc[1]));
 
-  if (warp == 0 || warp == 11) {
+  if (warp == 0 || warp == 2) {
     // ============================== producer ==============================
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     if (lane == 0) {
       // The workers take the items (tile, head) in turn, in the tiles' order, every other
       // round backwards.
@@ -314,6 +294,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           if (j > 0) {
             if (nv >= 1) ok = mbar_wait(vempty, (nv - 1) & 1, abort_flag);
+            if (j == 1 && it >= 2) ok = ok && mbar_wait(efree, (it - 2) & 1, abort_flag);  // (it counts this tile)
             if (!ok) break;
             // this CTA's value columns of the step's 128 keys
             const uint32_t dst = smem_w + static_cast<uint32_t>(L::v);
@@ -339,7 +320,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int k = max(0, nk - kStages); k < nk; ++k) drain(kfull + 8 * (k % kStages), (k / kStages) & 1);
       if (nv > 0) drain(vfull, (nv - 1) & 1);
     }
-  } else if (warp == 1 || warp == 10) {
+  } else if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     if (rank != 0) {
       // ========= relay of queries, keys and values (rank 1 to rank 0) ========
       if (lane == 0) {
@@ -436,6 +418,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else {
     // ============================== softmax ===============================
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // thread r of a worker's four warps owns query row r of this CTA
     const int qt = warp & 3;
     const int rl = qt * 32 + lane;
@@ -472,9 +455,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (ok && kb + rl >= tile.keys) {
             uint8_t* vrow = smem + g * L::worker + L::v + (rl >> 6) * kBoxBytes + (rl & 63) * 128;
 #pragma unroll
-            for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(vrow + c * 16) = make_uint4(0u, 0u, 0u, 0u);
+            for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(vrow + ((c ^ rl) & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
           }
-          fence_proxy_async_smem();
+          fence_proxy_async_smem();  // (and no release to the cluster, which takes thousands of clocks: latent_pair.cu)
         }
         if (!ok) break;
         tc_fence_after();
@@ -497,7 +480,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int e0 = live ? hi - kb : kStepKeys;  // visible keys of this step: below e0
         if (!__all_sync(0xffffffffu, e0 >= kStepKeys)) {
 #pragma unroll
-          for (int i = 0; i < kStepKeys; ++i) x[i] = i < e0 ? x[i] : -INFINITY;
+          for (int b = 0; b < kStepKeys; b += 32) {
+            const uint32_t see = e0 >= b + 32 ? 0xffffffffu : e0 <= b ? 0u : (1u << (e0 - b)) - 1u;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[b + i] = see >> i & 1u ? x[b + i] : -INFINITY;
+          }
         }
         float m8[8];
 #pragma unroll
@@ -533,31 +520,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tmem_st16(oc + c * 16, r);
           }
         }
-        uint64_t s2[4] = {0ull, 0ull, 0ull, 0ull};
+        float s1[4] = {0.f,0.f,0.f,0.f};
 #pragma unroll
-        for (int hh = 0; hh < 4; ++hh) {
-          uint32_t pk[16];
+        for (int hh = 0; hh < 2; ++hh) {
+          uint32_t pk[32];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
+          for (int i = 0; i < 32; ++i) {
             float a0v, a1v;
-            f32x2_split(fma_f32x2(f32x2(x[hh * 32 + 2 * i], x[hh * 32 + 2 * i + 1]), c2, n2), a0v, a1v);
+            f32x2_split(fma_f32x2(f32x2(x[hh * 64 + 2 * i], x[hh * 64 + 2 * i + 1]), c2, n2), a0v, a1v);
             const float e0v = ex2_approx(a0v), e1v = ex2_approx(a1v);
-            s2[i & 3] = add_f32x2(s2[i & 3], f32x2(e0v, e1v));
+            s1[i & 3] += e0v; s1[(i + 2) & 3] += e1v;
             pk[i] = pack_bf16x2(e0v, e1v);
           }
-          tmem_st16(sc + hh * 16, pk);
-          if (hh & 1) {  // the products of half of P may begin
+          tmem_st32(sc + hh * 32, pk);
+          {  // the products of half of P may begin
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) {
-              if (partial) mbar_arrive_cluster(pfull0 + 8 * (hh >> 1));  // publishes the zeroed value rows
-              else mbar_arrive_remote(pfull0 + 8 * (hh >> 1));
-            }
+            if (lane == 0) mbar_arrive_remote(pfull0 + 8 * hh);
           }
         }
         float u0, u1;
-        f32x2_split(add_f32x2(add_f32x2(s2[0], s2[1]), add_f32x2(s2[2], s2[3])), u0, u1);
+        u0 = s1[0] + s1[1]; u1 = s1[2] + s1[3];
         l += u0 + u1;
       }
       // ---- normalise and store, half a row at a time ----
@@ -594,7 +578,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         // (a NaN sum is the row's own: all of it is NaN)
         const bool again = live && odd != 0u && l == l;
-        transpose_pieces<kPieces>(w);
+        // through shared memory (where the values were, whose products have ended), so that a store
+        // covers whole lines
+        uint8_t* mine = smem + g * L::worker + L::v + qt * (32 * 16 * kPieces);
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i)
+          *reinterpret_cast<uint4*>(mine + (lane * kPieces + (i ^ (lane & (kPieces - 1)))) * 16) = w[i];
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+          const int rr = (lane & ~(kPieces - 1)) + i;
+          w[i] = *reinterpret_cast<const uint4*>(mine + (rr * kPieces + ((lane & (kPieces - 1)) ^ (rr & (kPieces - 1)))) * 16);
+        }
         uint16_t* o = p.out + (static_cast<size_t>(tile.q0 + (row & ~(kPieces - 1))) * p.heads + tile.h) * D + hf * (D / 2) +
                       (lane & (kPieces - 1)) * 8;
 #pragma unroll
@@ -619,6 +614,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
       }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(efree);
     }
     if (!ok) *abort_flag = 1;
   }
