@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // conditions must be for the products' operands to be there)
     auto uniform = [](int x) { return __reduce_max_sync(0xffffffffu, x); };
     auto done = [](uint32_t bar, uint32_t parity) {
-      return __reduce_and_sync(0xffffffffu, mbar_test_wait(bar, parity) ? 1u : 0u) != 0u;
+      return __all_sync(0xffffffffu, mbar_test_wait(bar, parity)) != 0;
     };
     // S^T of page s and the value product of page v <= s are issued in whatever order they
     // become ready: neither waits for the other's data.

@@ -244,7 +244,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t p_lo = static_cast<uint32_t>(pdesc), p_hi = static_cast<uint32_t>(pdesc >> 32);
     auto uniform = [](int x) { return __reduce_max_sync(0xffffffffu, x); };
     auto done = [](uint32_t bar, uint32_t parity) {
-      return __reduce_and_sync(0xffffffffu, mbar_test_wait_cluster(bar, parity) ? 1u : 0u) != 0u;
+      return __all_sync(0xffffffffu, mbar_test_wait_cluster(bar, parity)) != 0;
     };
     // scores of page s and the value product of page v <= s, in whatever order they become ready
     int s = 0, v = 0, u = 0;

@@ -364,7 +364,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t v_lo = static_cast<uint32_t>(vdesc), v_hi = static_cast<uint32_t>(vdesc >> 32);
       const uint32_t sc = tmem + L::kColS + g * 128u, oc = tmem + L::kColO + g * 128u;
       auto wait = [&](uint32_t bar, uint32_t parity) {
-        return __reduce_and_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag) ? 1u : 0u) != 0u;
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag)) != 0;
+      };
+      auto wait2 = [&](uint32_t b1, uint32_t p1, uint32_t b2, uint32_t p2) {
+        return __all_sync(0xffffffffu, mbar_wait(b1, p1, abort_flag) && mbar_wait(b2, p2, abort_flag)) != 0;
       };
       bool ok = true;
       for (int it = 0, js = 0; ok; ++it) {
@@ -379,7 +382,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int j = 0; j < nsteps; ++j, ++js) {
           const int s = js % kStages;
           // S, over the P that the P.V before reads
-          ok = wait(kfull + 8 * s, (js / kStages) & 1) && (js < 1 || wait(pvdone, (js - 1) & 1));
+          ok = js < 1 ? wait(kfull + 8 * s, (js / kStages) & 1) : wait2(kfull + 8 * s, (js / kStages) & 1, pvdone, (js - 1) & 1);
           if (!ok) break;
           tc_fence_after();
           const uint32_t kd = k_lo + ((s * L::kKStage) >> 4);
@@ -397,7 +400,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           umma2_commit_both_warp(kempty + 8 * s);
           if (j + 1 == nsteps) umma2_commit_both_warp(qempty);
           // (that all rows' P is there says too that the tile before's O has been read)
-          ok = wait(vfull, js & 1) && wait(pfull, js & 1);
+          ok = wait2(vfull, js & 1, pfull, js & 1);
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
