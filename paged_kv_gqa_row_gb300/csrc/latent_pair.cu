@@ -554,13 +554,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               *reinterpret_cast<uint4*>(o + 8 * C + 32) = make_uint4(wb[4], wb[5], wb[6], wb[7]);
             }
           } else {
-            float* o = p.o + (slot + rank * kRows + ra) * C + d + ca;
+            // two lanes trade: the even one gets four numbers of group 2 i, the odd one of 2 i + 1
+            const bool up = (lane & 1) != 0;
+            float* o = p.o + (slot + rank * kRows + ra) * C + d + (up ? ca + 6 : ca);
+            auto trade = [&](uint32_t x0, uint32_t x1, uint32_t y0, uint32_t y1) {
+              const uint32_t g0 = __shfl_xor_sync(0xffffffffu, up ? x0 : y0, 1), g1 = __shfl_xor_sync(0xffffffffu, up ? x1 : y1, 1);
+              return up ? make_uint4(g0, g1, y0, y1) : make_uint4(x0, x1, g0, g1);
+            };
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              bad0 = fmaf(__uint_as_float(v[4 * i]), 0.f, fmaf(__uint_as_float(v[4 * i + 1]), 0.f, bad0));
-              bad1 = fmaf(__uint_as_float(v[4 * i + 2]), 0.f, fmaf(__uint_as_float(v[4 * i + 3]), 0.f, bad1));
-              if (see_a) *reinterpret_cast<uint2*>(o + 8 * i) = make_uint2(v[4 * i], v[4 * i + 1]);
-              if (see_b) *reinterpret_cast<uint2*>(o + 8 * C + 8 * i) = make_uint2(v[4 * i + 2], v[4 * i + 3]);
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t* x = v + 8 * i;  // groups 2 i and 2 i + 1
+              const uint4 wa = trade(x[0], x[1], x[4], x[5]), wb = trade(x[2], x[3], x[6], x[7]);
+#pragma unroll
+              for (int k = 0; k < 8; k += 4) {
+                bad0 = fmaf(__uint_as_float(x[k]), 0.f, fmaf(__uint_as_float(x[k + 1]), 0.f, bad0));
+                bad1 = fmaf(__uint_as_float(x[k + 2]), 0.f, fmaf(__uint_as_float(x[k + 3]), 0.f, bad1));
+              }
+              if (see_a) *reinterpret_cast<uint4*>(o + 16 * i) = wa;
+              if (see_b) *reinterpret_cast<uint4*>(o + 8 * C + 16 * i) = wb;
             }
           }
         }
