@@ -21,11 +21,11 @@
 // (Rank 0's products read rank 1's probabilities from rank 1's shared memory.  The softmax warps
 // order their stores before the async proxy and then arrive at rank 0's barrier; arriving
 // with a release to the cluster instead took a memory barrier of 1500 to 3500 clocks, in these
-// warps or in a relay's: 32 rows of 128 heads 89 us, with the join, and 57 now.)
+// warps or in a relay's: 32 rows of 128 heads 89 us, with the join, and 55 now.)
 //
 // Bound: the products' operands (the pipe with its reads is active 73% of a step of 272 prompt
-// tokens of 64 heads and 32 decode rows, 0.12 Tflop in 129 us), and the tiles' ends, which the one accumulator
-// waits for.
+// tokens of 64 heads and 32 decode rows, 0.12 Tflop in 125 us), and the tiles' ends, which the
+// one accumulator waits for.
 #include "latent_units.cuh"
 #include "ptx.cuh"
 

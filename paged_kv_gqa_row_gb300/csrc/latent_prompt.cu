@@ -19,13 +19,24 @@
 // grows by more than 2^8, which is when O is rescaled (the scheme of the paged prompt
 // kernel, chunk.cu).
 //
+// Bound: the chain of a step, 3600 cycles of which the two workers' products take 2720.  Four
+// prompts of 1024 to 2047 tokens, 32 heads, 0.10 Tflop: 132 us with one tile under way, two score
+// buffers and two groups of softmax warps that handed the maximum on; 124 with two workers;
+// 112 with the products of P's first half begun before the second is there (its first quarter
+// 107.5 to 105 at that stage, three quarters 112, each quarter on its own 114); 105 with sums
+// in scalars (pairs of float32 cost the registers' order: 113 to 107) and the registers of the
+// loading warps given to the softmax; 103 with votes where reductions ended the waits:
+// 1.0 Pflop/s.  Scores in halves of 64 keys, the second of the next step before this one's P.V: 5
+// us more.
+//
 // Tile ids: prompt n's tiles are base(n) = q_starts[n] / 256 + n onwards, which leaves
 // every prompt room for its tiles without a sum over the prompts before it; ids without
 // queries end at once.
 //
 // Values that are not finite, at keys that some rows of a tile see and others do not,
 // reach all of them through 0 * NaN: a row whose output is not finite computes it again
-// from its own keys (attend_row), if there is such a value among the tile's keys behind it.  Key rows past the tile's last key are zeroed.
+// from its own keys (attend_row), if there is such a value among the tile's keys behind it.
+// Key rows past the tile's last key are zeroed.
 #include <algorithm>
 
 #include "latent.cuh"
@@ -244,6 +255,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (warp == 0 || warp == 2) {
     // ============================== producer ==============================
+    // (the launch's registers, 384 x 168, hold 128 x 80 and 256 x 208)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     if (lane == 0) {
       // The workers take the items (tile, head) in turn, in the tiles' order, every other
@@ -523,7 +535,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tmem_st16(oc + c * 16, r);
           }
         }
-        float s1[4] = {0.f,0.f,0.f,0.f};
+        float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
           uint32_t pk[32];
@@ -532,20 +544,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             float a0v, a1v;
             f32x2_split(fma_f32x2(f32x2(x[hh * 64 + 2 * i], x[hh * 64 + 2 * i + 1]), c2, n2), a0v, a1v);
             const float e0v = ex2_approx(a0v), e1v = ex2_approx(a1v);
-            s1[i & 3] += e0v; s1[(i + 2) & 3] += e1v;
+            s[i & 3] += e0v;
+            s[(i + 2) & 3] += e1v;
             pk[i] = pack_bf16x2(e0v, e1v);
           }
           tmem_st32(sc + hh * 32, pk);
-          {  // the products of half of P may begin
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_remote(pfull0 + 8 * hh);
-          }
+          // the products of half of P may begin
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_remote(pfull0 + 8 * hh);
         }
-        float u0, u1;
-        u0 = s1[0] + s1[1]; u1 = s1[2] + s1[3];
-        l += u0 + u1;
+        l += (s[0] + s[1]) + (s[2] + s[3]);
       }
       // ---- normalise and store, half a row at a time ----
       if (ok && nsteps > 0) ok = __all_sync(0xffffffffu, mbar_wait(pvdone, (js - 1) & 1, abort_flag));

@@ -79,6 +79,22 @@ def test_prompts(name, heads, d, r, pieces):
     Prompts(len(name), heads, d, r, pieces, gap=3).upload().run().verify()
 
 
+def test_more_tiles_than_are_ordered_by_cost():
+    Prompts(8, 1, 64, 32, [(1 + i % 5, i % 7 - 2) for i in range(700)]).upload().run().verify()
+
+
+@pytest.mark.parametrize("d,r", [(128, 64), (64, 32)])
+def test_many_tiles_a_worker(d, r):
+    s = Prompts(9, 48, d, r, [(900, 0), (513, 130), (257, 3), (1300, 0)]).upload().run()
+    s.verify(skip=lambda n, i: i % 97 and i not in (127, 128, 255, 256, 511, 512))
+    want = bits(s.out).copy()
+    for _ in range(20):  # (whatever the two workers of a cluster meet: the same numbers)
+        s.out.fill_(0x7FC1)
+        s.run()
+        torch.cuda.synchronize()
+        assert int(s.status.item()) == 0 and (bits(s.out) == want).all()
+
+
 def test_rotated_keys_inside_wider_rows():
     Prompts(1, 3, 128, 64, [(70, 0), (40, 30)], rope_stride=576).upload().run().verify()
 
