@@ -289,8 +289,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                       x.q0 + static_cast<int>(rank) * kRows, qfull + 8 * b);
         ++it;
         const int nsteps = (x.keys + kStepKeys - 1) / kStepKeys;
+        // (efree is waited for once a tile: with a phase left out, the wait for the next one would
+        // take the one before the missing one for it)
+        if (nsteps == 0 && it >= 2) ok = mbar_wait(efree, (it - 2) & 1, abort_flag);
         // keys a step ahead of the values, in the order in which the products free them
-        for (int j = 0; j <= nsteps; ++j) {
+        for (int j = 0; ok && j <= nsteps; ++j) {
           if (j < nsteps) {
             const int s = nk % kStages;
             if (nk >= kStages) ok = mbar_wait(kempty + 8 * s, ((nk / kStages) - 1) & 1, abort_flag);

@@ -83,6 +83,20 @@ def test_more_tiles_than_are_ordered_by_cost():
     Prompts(8, 1, 64, 32, [(1 + i % 5, i % 7 - 2) for i in range(700)]).upload().run().verify()
 
 
+def test_tiles_without_keys_between_others():
+    """A tile's outputs leave through the place of the values: the next tile's may come only then, whatever
+    lies between the two."""
+    pieces = [(3, -3) if i % 2 else (200 + i % 57, i % 5) for i in range(600)]
+    s = Prompts(10, 4, 128, 64, pieces).upload().run()
+    s.verify(skip=lambda n, i: (n + i) % 61 != 0)
+    want = bits(s.out).copy()
+    for _ in range(30):
+        s.out.fill_(0x7FC1)
+        s.run()
+        torch.cuda.synchronize()
+        assert int(s.status.item()) == 0 and (bits(s.out) == want).all()
+
+
 @pytest.mark.parametrize("d,r", [(128, 64), (64, 32)])
 def test_many_tiles_a_worker(d, r):
     s = Prompts(9, 48, d, r, [(900, 0), (513, 130), (257, 3), (1300, 0)]).upload().run()
