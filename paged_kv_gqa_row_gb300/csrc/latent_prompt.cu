@@ -289,11 +289,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                       x.q0 + static_cast<int>(rank) * kRows, qfull + 8 * b);
         ++it;
         const int nsteps = (x.keys + kStepKeys - 1) / kStepKeys;
-        // (efree is waited for once a tile: with a phase left out, the wait for the next one would
-        // take the one before the missing one for it)
-        if (nsteps == 0 && it >= 2) ok = mbar_wait(efree, (it - 2) & 1, abort_flag);
         // keys a step ahead of the values, in the order in which the products free them
-        for (int j = 0; ok && j <= nsteps; ++j) {
+        for (int j = 0; j <= nsteps; ++j) {
           if (j < nsteps) {
             const int s = nk % kStages;
             if (nk >= kStages) ok = mbar_wait(kempty + 8 * s, ((nk / kStages) - 1) & 1, abort_flag);
@@ -307,9 +304,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tma_load_2d(dst + (D / 64) * kBoxBytes, &rmap, 0, y, kfull + 8 * s);
             ++nk;
           }
+          // the tile before's outputs leave through the values' place.  (Waited for once a tile, of no
+          // keys too: with a phase left out, the wait for the next would take an older one for it.  it
+          // counts this tile.)
+          if (j == (nsteps > 0 ? 1 : 0) && it >= 2) ok = mbar_wait(efree, (it - 2) & 1, abort_flag);
+          if (!ok) break;
           if (j > 0) {
             if (nv >= 1) ok = mbar_wait(vempty, (nv - 1) & 1, abort_flag);
-            if (j == 1 && it >= 2) ok = ok && mbar_wait(efree, (it - 2) & 1, abort_flag);  // (it counts this tile)
             if (!ok) break;
             // this CTA's value columns of the step's 128 keys
             const uint32_t dst = smem_w + static_cast<uint32_t>(L::v);
