@@ -112,8 +112,9 @@ extern "C" lnk_status lnk_paged_copy_pages_layers(const lnk_attn_desc* desc, lnk
   return lnk::copy_pages(desc, k_pools, v_pools, layers, src_pages, dst_pages, n, dev_status, stream);
 }
 
-// A latent page is split into parts, a CTA each, so that a copy of few pages spreads
-// over the SMs.
+// A latent page is split into four parts, a CTA each, so that a copy of few pages spreads
+// over the SMs (3 pages of 72 KB in 32 layers: 3.6 us, whole pages 5.6, halves 4.3; 160 pages in
+// them, 755 MB: 112 us, whole pages 113.5).
 extern "C" lnk_status lnk_latent_copy_pages(const lnk_latent_desc* desc, lnk_bf16* const* pools, int32_t layers,
                                             const int32_t* src_pages, const int32_t* dst_pages, int32_t n,
                                             int32_t* dev_status, lnk_stream stream) {
