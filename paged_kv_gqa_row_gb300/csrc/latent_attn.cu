@@ -605,7 +605,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int rr = 0; rr < nrows; ++rr) {
           if (s_alpha[rr] != s_alpha[rr]) continue;  // (a sum that is NaN is the row's own: all of it is)
-          if (row_keys[rr].x <= bad_keys.x && row_keys[rr].y > bad_keys.y) continue;  // (so is what is not finite)
+          // (so is what is not finite of a row that sees all such keys; one that sees nothing gets its zeros)
+          if (row_keys[rr].y > row_keys[rr].x && row_keys[rr].x <= bad_keys.x && row_keys[rr].y > bad_keys.y) continue;
           bool bad = false;
 #pragma unroll 1
           for (int mb = 0; mb < NB; ++mb) {

@@ -594,7 +594,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const float total = __shfl_sync(0xffffffffu, sum, k);
           if ((m >> (4 * (k & 7)) & 15u) == 0u || total != total) continue;  // (a NaN sum is the row's own)
           const int lo_k = __shfl_sync(0xffffffffu, lo, k), hi_k = __shfl_sync(0xffffffffu, hi, k);
-          if (lo_k <= bad_keys.x && hi_k > bad_keys.y) continue;  // (so is what is not finite)
+          // (so is what is not finite of a row that sees all such keys; one that sees nothing gets its zeros)
+          if (hi_k > lo_k && lo_k <= bad_keys.x && hi_k > bad_keys.y) continue;
           const int ro = rank * kRows + (qt & 1) * 32 + k, w = p.latent_dim + p.rope_dim;
           __syncwarp();
           float acc[2 * NB];
