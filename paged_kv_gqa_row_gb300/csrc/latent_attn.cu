@@ -618,6 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (k == (rr & 15)) bad |= (__float_as_uint(__uint_as_float(v[k]) * s_alpha[rr]) & 0x7F800000u) == 0x7F800000u;
           }
           if (!__any_sync(0xffffffffu, bad)) continue;
+          __syncwarp();  // (other lanes stored what is stored again)
           float acc[NB];
           attend_again<NB, 128>(p, p.q + static_cast<size_t>(rowbase + rr) * w, trow, max(row_keys[rr].x, seg_lo),
                             min(row_keys[rr].y, seg_hi), s_ref[rr], qt * 32 + lane, acc);
