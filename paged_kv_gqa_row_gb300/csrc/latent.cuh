@@ -8,6 +8,11 @@ namespace lnk {
 constexpr int kLatentRows = 64;  // query rows of a one-SM attention tile at most
 constexpr int kWholePages = 8;   // tokens of so few pages are never cut
 
+// A softmax reference (log2 units) is set this far above a score, and raised when another score
+// exceeds it by the second.
+constexpr float kAheadLog2 = 24.f;
+constexpr float kRaiseLog2 = 8.f;
+
 __device__ __forceinline__ float bf16_at(const uint16_t* x) {
   return __uint_as_float(static_cast<uint32_t>(*x) << 16);
 }

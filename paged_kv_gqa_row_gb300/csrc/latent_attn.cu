@@ -21,9 +21,10 @@
 //
 // Softmax: P = 2^(s scale log2(e) - ref).  P is rounded to bf16 and summed in float32,
 // whose relative precision does not depend on the reference, so that need not be the
-// maximum: it is the score of the row's first key, and is raised (to a page's maximum)
-// only when a score exceeds it by 2^32.  The usual page needs no maximum across threads,
-// only a vote.
+// maximum: it is 2^24 above the score of the row's first key, and is raised (to 2^24 above a
+// page's maximum) only when a score exceeds it by 2^8, so that sums leave float32's range for
+// latents beyond 2^119 / keys alone (from the score itself, with 2^32 above it: 2^95 / keys).
+// The usual page needs no maximum across threads, only a vote.
 //
 // Warps: 0 loads (TMA), 1 issues the products, 2-5 do the softmax: warp w holds keys
 // 16 (w % 4) .. + 15 of S^T and 32 lanes of each 128 numbers of O^T.
@@ -43,7 +44,6 @@ namespace lnk {
 namespace {
 
 constexpr int kThreads = 192;
-constexpr float kRaiseLog2 = 32.f;
 constexpr int kSoftBar = 1;  // named barrier of the softmax warps
 
 template <int NB, int N>
@@ -322,8 +322,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t unset = 0u;          // columns (bit) without a reference that see keys
 #pragma unroll
       for (int i = 0; i < N / 4; ++i) {
-        nref[i] = l[i] = 0.f;
         const int col = 8 * (i >> 1) + ca + (i & 1);
+        nref[i] = col < nrows ? 0.f : -INFINITY;  // (rows past the unit's have no weights, and nothing to raise)
+        l[i] = 0.f;
         if (col < nrows && row_keys[col].y > row_keys[col].x) unset |= 1u << i;
       }
       bool force = true;            // some row has no reference yet (the same in every thread)
@@ -388,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int x = 0; x < N / 4; ++x) {
             const float f = s_ref[8 * (x >> 1) + ca + (x & 1)];
             if ((unset >> x & 1) && f > -INFINITY) {  // (a NaN score: the maximum of the others, below)
-              nref[x] = -f * p.scale_log2;
+              nref[x] = fmaf(-f, p.scale_log2, -kAheadLog2);
               unset &= ~(1u << x);
             }
           }
@@ -416,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           force = __any_sync(0xffffffffu, unset != 0u);
         }
         if (named_barrier_or(kSoftBar, 128, mx > kRaiseLog2 || !ok)) {
-          // ---- references raised (or set) to the page's maximum ----
+          // ---- references raised (or set) with the page's maximum ----
           if (g > 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait(pvdone, (g - 1) & 1, abort_flag));
           if (named_barrier_or(kSoftBar, 128, !ok)) {
             ok = false;
@@ -441,12 +442,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (m != -INFINITY) {
               m *= p.scale_log2;
               if (unset >> x & 1) {
-                nref[x] = -m;
+                nref[x] = -m - kAheadLog2;
                 unset &= ~(1u << x);
               } else if (m + nref[x] > kRaiseLog2) {
-                f = ex2_approx(-nref[x] - m);
+                f = ex2_approx((-m - kAheadLog2) - nref[x]);
                 l[x] *= f;
-                nref[x] = -m;
+                nref[x] = -m - kAheadLog2;
                 moved = true;
               }
             }

@@ -34,7 +34,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kRows = 64;          // rows of a CTA
-constexpr float kRaiseLog2 = 32.f;
 constexpr int kSoftBar = 1;
 
 template <int NB>
@@ -353,7 +352,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         token_keys(p, t + (hb * 2 * kRows + rr) / p.heads, r0, lo, hi);
       }
       const int32_t* trow = p.table + static_cast<long long>(max(un.row, 0)) * p.pages_per_row;
-      float nref = 0.f, l = 0.f;           // minus the reference (0 while there is none), this thread's part of the sum
+      // minus the reference (0 while there is none; rows past the unit's have no weights, and nothing to
+      // raise), this thread's part of the sum
+      float nref = rr < nrows ? 0.f : -INFINITY, l = 0.f;
       bool unset = rr < nrows && hi > lo;  // no reference yet, and keys to see
       bool force = true;                   // some row of the CTA has none
       if (half == 0) s_ref[row] = -INFINITY;
@@ -389,7 +390,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           named_barrier_sync(kSoftBar, 128);
           const float f0 = s_ref[row];
           if (unset && f0 > -INFINITY) {  // (a NaN score: the maximum of the others, below)
-            nref = -f0 * p.scale_log2;
+            nref = fmaf(-f0, p.scale_log2, -kAheadLog2);
             unset = false;
           }
         }
@@ -407,7 +408,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // (a row without a reference that sees a score all the same: its first one is -inf or NaN)
         const bool raise = unset ? mx > -INFINITY : mx > kRaiseLog2;
         if (named_barrier_or(kSoftBar, 128, raise || !ok)) {
-          // ---- references raised (or set) to the page's maximum ----
+          // ---- references raised (or set) with the page's maximum ----
           if (g > 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait(pvdone + 8 * ((g - 1) & 1), ((g - 1) >> 1) & 1, abort_flag));
           if (named_barrier_or(kSoftBar, 128, !ok)) {
             ok = false;
@@ -424,12 +425,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (m != -INFINITY) {
             m *= p.scale_log2;
             if (unset) {
-              nref = -m;
+              nref = -m - kAheadLog2;
               unset = false;
             } else if (m + nref > kRaiseLog2) {
-              f = ex2_approx(-nref - m);
+              f = ex2_approx((-m - kAheadLog2) - nref);
               l *= f;
-              nref = -m;
+              nref = -m - kAheadLog2;
             }
           }
           if (__any_sync(0xffffffffu, f != 1.f) && i > 0) {

@@ -97,3 +97,19 @@ def test_keys_that_leave_the_window_inside_a_tile(kind, before, window):
             assert np.isnan(bf16.to_f64(out[t])).all(), f"token {t}"
         elif row == 0 or t <= last + 2 * per_tile:
             compare(s, out, t, row, p, clean)
+
+
+@pytest.mark.parametrize("heads,pieces,dec", [(16, [(5, 100)], [700]), (16, [], [5000, 64]), (40, [(90, 100)], [700]),
+                                              (128, [(2, 70)], [3000])], ids=["one-sm", "cut", "pairs", "cut-pairs"])
+def test_large_latents_behind_a_first_key_of_low_score(heads, pieces, dec):
+    """Sums stay in float32's range where the softmax of the same numbers does: weights relative to the
+    first key's score, 2^26 to 2^30 for the others here, and latents of 2^100."""
+    s = Step(35, heads, 256, 64, pieces=pieces, dec=dec, scale=1.0)
+    rng = np.random.default_rng(36)
+    s.q[:, :, :s.c] = 0
+    s.q[:, :, s.c:] = bf16.from_f64(np.ones((1,)))[0]
+    s.pool[:, :s.c] = bf16.from_f64(bf16.to_f64(s.pool[:, :s.c]) * 2.0 ** 100)
+    s.pool[:, s.c:] = bf16.from_f64(rng.choice([-1, 1], (len(s.pool), s.r)) * rng.uniform(0.02, 0.06, (len(s.pool), s.r)))
+    for row in range(s.table.shape[0]):
+        s.pool[slot(s, row, 0), s.c:] = bf16.from_f64(np.full(s.r, -0.3))
+    s.upload().run().verify()
