@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; ok && i < n; ++i, ++g) {
           int page = un.row >= 0 ? trow[i] : 0;
           if (page < 0 || page >= p.num_pages) {
-            if (p.status != nullptr) atomicOr(p.status, LNK_DEV_BAD_PAGE);
+            if (p.status != nullptr && page_seen(p, t, un.nt, un.first + j0 + i)) atomicOr(p.status, LNK_DEV_BAD_PAGE);
             page = 0;  // (its keys are masked and its values zeroed)
           }
           const int st = g % kStages;

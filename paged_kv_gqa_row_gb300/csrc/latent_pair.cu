@@ -146,7 +146,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   auto page_of = [&](const Unit& un, int i, bool report) {
     int page = un.row >= 0 ? p.table[static_cast<long long>(un.row) * p.pages_per_row + un.first + j0 + i] : 0;
     if (page < 0 || page >= p.num_pages) {
-      if (report && hb == 0 && rank == 0 && p.status != nullptr) atomicOr(p.status, LNK_DEV_BAD_PAGE);
+      if (report && hb == 0 && rank == 0 && p.status != nullptr && page_seen(p, t, un.nt, un.first + j0 + i))
+        atomicOr(p.status, LNK_DEV_BAD_PAGE);
       page = 0;
     }
     return page;

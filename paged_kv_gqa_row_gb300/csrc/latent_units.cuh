@@ -79,6 +79,18 @@ __device__ __forceinline__ Unit unit_at(const LatentParams& p, int t) {
   return u;
 }
 
+// Whether a token of the unit that starts at t sees a key of the row's page lp: only then must the
+// table name one (between the windows of tokens far apart lie pages that nobody needs).
+__device__ __noinline__ bool page_seen(const LatentParams& p, int t, int nt, int lp) {
+#pragma unroll 1
+  for (int s = t; s < t + nt; ++s) {
+    int row, lo, hi;
+    token_keys(p, s, row, lo, hi);
+    if (hi > lo && lo / kPage <= lp && lp <= (hi - 1) / kPage) return true;
+  }
+  return false;
+}
+
 // The first key from `from` on (to `to`, exclusive, in steps of +1 or -1) whose latent has a
 // number that is not finite, or -1.  The whole warp.
 __device__ __noinline__ int odd_key(const LatentParams& p, const int32_t* trow, int from, int to, int step) {

@@ -99,6 +99,16 @@ def test_keys_that_leave_the_window_inside_a_tile(kind, before, window):
             compare(s, out, t, row, p, clean)
 
 
+@pytest.mark.parametrize("kind", KINDS)
+def test_pages_between_two_windows_need_not_be_there(kind):
+    """Two tokens of one tile far apart in their row: the pages that neither's window reaches."""
+    s, per_tile = piece(kind, 500, 34, window=65)
+    s.positions[:] = -1
+    s.positions[:2] = 70, 500
+    s.table[1, 2:6] = (-1, s.pages, -1, -1)
+    s.upload().run().verify()
+
+
 @pytest.mark.parametrize("heads,pieces,dec", [(16, [(5, 100)], [700]), (16, [], [5000, 64]), (40, [(90, 100)], [700]),
                                               (128, [(2, 70)], [3000])], ids=["one-sm", "cut", "pairs", "cut-pairs"])
 def test_large_latents_behind_a_first_key_of_low_score(heads, pieces, dec):
