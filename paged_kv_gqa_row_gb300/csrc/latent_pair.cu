@@ -19,9 +19,9 @@
 // values; 4-7 softmax: thread L owns row L % 64 of its CTA and keys 32 (L / 64) .. + 31 of a page,
 // and that row's half L / 64 of O.  Scores and probabilities have two buffers each.
 // (Rank 0's products read rank 1's probabilities from rank 1's shared memory.  The softmax warps
-// order their stores before the async proxy and then arrive at rank 0's barrier; arriving
-// with a release to the cluster instead took a memory barrier of 1500 to 3500 clocks, in these
-// warps or in a relay's: 32 rows of 128 heads 89 us, with the join, and 55 now.)
+// order their stores before the async proxy and arrive at rank 0's barrier with a release of
+// shared memory alone to the cluster; a release of all memory took a barrier of 1500 to 3500
+// clocks, in these warps or in a relay's: 32 rows of 128 heads 89 us, with the join, and 56 now.)
 //
 // Bound: the products' operands (the pipe with its reads is active 73% of a step of 272 prompt
 // tokens of 64 heads and 32 decode rows, 0.12 Tflop in 125 us), and the tiles' ends, which the
@@ -481,7 +481,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_remote(pfull0 + 8 * (g & 1));
+        if (lane == 0) mbar_arrive_remote_shared(pfull0 + 8 * (g & 1));
       }
       // ---- the unit's end: sums joined, outputs or partial sums stored ----
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait(pvdone + 8 * ((g - 1) & 1), ((g - 1) >> 1) & 1, abort_flag));

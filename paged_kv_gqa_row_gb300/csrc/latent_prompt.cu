@@ -382,8 +382,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       auto wait = [&](uint32_t bar, uint32_t parity) {
         return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag)) != 0;
       };
-      auto wait2 = [&](uint32_t b1, uint32_t p1, uint32_t b2, uint32_t p2) {
-        return __all_sync(0xffffffffu, mbar_wait(b1, p1, abort_flag) && mbar_wait(b2, p2, abort_flag)) != 0;
+      auto wait2 = [&](uint32_t b1, uint32_t p1, uint32_t b2, uint32_t p2) {  // (the second as ptx.cuh asks for)
+        return __all_sync(0xffffffffu, mbar_wait(b1, p1, abort_flag) && mbar_wait_cluster(b2, p2, abort_flag)) != 0;
       };
       bool ok = true;
       for (int it = 0, js = 0; ok; ++it) {
@@ -476,7 +476,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(vrow + ((c ^ rl) & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
           }
-          fence_proxy_async_smem();  // (and no release to the cluster, which takes thousands of clocks: latent_pair.cu)
+          fence_proxy_async_smem();  // (the arrival for the first half of P publishes them to the cluster)
         }
         if (!ok) break;
         tc_fence_after();
@@ -557,7 +557,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_remote(pfull0 + 8 * hh);
+          if (lane == 0) {
+            if (hh == 0 && partial) mbar_arrive_remote_shared(pfull0);
+            else mbar_arrive_remote(pfull0 + 8 * hh);
+          }
         }
         l += (s[0] + s[1]) + (s[2] + s[3]);
       }

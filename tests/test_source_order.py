@@ -21,3 +21,33 @@ def test_rows_that_are_stored_again_wait_for_the_lanes_that_stored_them_first(na
     assert calls
     for at in calls:
         assert "__syncwarp();" in src[at - 160:at], src[at - 160:at]
+
+
+def between(src, start, end):
+    at = src.index(start)
+    return src[at:src.index(end, at)]
+
+
+def test_shared_memory_that_the_peers_products_read_is_released_to_the_cluster_and_acquired_from_it():
+    """Ordinary stores of one CTA that a product of both reads: a proxy fence of the storing threads, an arrival
+    with a release to the cluster, a wait with an acquire from it."""
+    ptx = source("ptx.cuh")
+    body = between(ptx, "void mbar_arrive_remote_shared(", "\n}")
+    assert body.index("fence.release.sync_restrict::shared::cta.cluster;") < body.index("mbarrier.arrive.relaxed.cluster.")
+    for name in ("bool mbar_try_wait_cluster(", "bool mbar_test_wait_cluster("):
+        assert ".acquire.cluster." in between(ptx, name, "\n}")
+    # pairs: probabilities and zeroed values of every page
+    src = source("latent_pair.cu")
+    stores = src[src.index("// ---- P into shared memory"):]
+    fence, arrive = stores.index("fence_proxy_async_smem();"), stores.index("mbar_arrive_remote_shared(pfull0")
+    assert stores.index("= make_uint4(0u, 0u, 0u, 0u);") < fence < arrive
+    assert re.findall(r"mbar_arrive\w*\(pfull0", src) == ["mbar_arrive_remote_shared(pfull0"]
+    issuer = between(src, "// ======================= products' issuer", "// ============================== softmax")
+    assert "mbar_test_wait_cluster(bar, parity)" in between(issuer, "auto done =", "};") and "done(pfull" in issuer
+    # prompts: zeroed values of a tile's last step (probabilities are in tensor memory)
+    src = source("latent_prompt.cu")
+    step = src[src.index("if (ok && partial) {"):]
+    assert step.index("= make_uint4(0u, 0u, 0u, 0u);") < step.index("fence_proxy_async_smem();") < step.index("mbar_arrive_remote_shared(pfull0)")
+    assert "if (hh == 0 && partial) mbar_arrive_remote_shared(pfull0);" in step
+    issuer = between(src, "issuer (rank 0)", "// ============================== softmax")
+    assert "mbar_wait_cluster(b2, p2" in between(issuer, "auto wait2 =", "};") and "wait2(vfull, js & 1, pfull, js & 1)" in issuer
