@@ -538,7 +538,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int j = 0; ok && j < nsteps; ++j) {
         const int b = j & 1, sv = j % kStagesV;
-        ok = mbar_wait(smem_addr(pfull + b), (j >> 1) & 1, abort_flag) &&
+        ok = mbar_wait_cluster(smem_addr(pfull + b), (j >> 1) & 1, abort_flag) &&
              mbar_wait(smem_addr(vfull + sv), (j / kStagesV) & 1, abort_flag);
         if (!ok) break;
         tc_fence_after();

@@ -34,8 +34,10 @@ def test_shared_memory_that_the_peers_products_read_is_released_to_the_cluster_a
     ptx = source("ptx.cuh")
     body = between(ptx, "void mbar_arrive_remote_shared(", "\n}")
     assert body.index("fence.release.sync_restrict::shared::cta.cluster;") < body.index("mbarrier.arrive.relaxed.cluster.")
-    for name in ("bool mbar_try_wait_cluster(", "bool mbar_test_wait_cluster("):
-        assert ".acquire.cluster." in between(ptx, name, "\n}")
+    assert "fence.acquire.sync_restrict::shared::cluster.cluster;" in between(ptx, "void fence_acquire_shared_cluster(", "\n}")
+    for name in ("bool mbar_wait_cluster(", "bool mbar_test_wait_cluster("):
+        body = between(ptx, name, "\n}")
+        assert body.rindex("fence_acquire_shared_cluster();") > max(body.rfind("mbar_try_wait_relaxed("), body.rfind(".relaxed.cluster."))
     # pairs: probabilities and zeroed values of every page
     src = source("latent_pair.cu")
     stores = src[src.index("// ---- P into shared memory"):]
@@ -51,3 +53,10 @@ def test_shared_memory_that_the_peers_products_read_is_released_to_the_cluster_a
     assert "if (hh == 0 && partial) mbar_arrive_remote_shared(pfull0);" in step
     issuer = between(src, "issuer (rank 0)", "// ============================== softmax")
     assert "mbar_wait_cluster(b2, p2" in between(issuer, "auto wait2 =", "};") and "wait2(vfull, js & 1, pfull, js & 1)" in issuer
+
+
+def test_the_paged_prompt_kernel_acquires_zeroed_values_from_the_cluster():
+    src = source("chunk.cu")
+    assert "if (partial) mbar_arrive_cluster(pfull0" in src
+    issuer = between(src, "// ========================= P.V issuer (rank 0)", "// ============================== softmax")
+    assert "mbar_wait_cluster(smem_addr(pfull + b)" in issuer
