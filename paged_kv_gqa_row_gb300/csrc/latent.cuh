@@ -2,6 +2,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "ptx.cuh"
 
 namespace lnk {
 
@@ -12,6 +13,22 @@ constexpr int kWholePages = 8;   // tokens of so few pages are never cut
 // exceeds it by the second.
 constexpr float kAheadLog2 = 24.f;
 constexpr float kRaiseLog2 = 8.f;
+
+// Rows that attend_again computes again can take longer than a wait may: their
+// warps keep writing the time into the beat, a word of each CTA of the cluster from which the
+// other roles' limits count.  It lies kBeat words behind the abort flag.
+constexpr int kBeat = 3;
+template <bool kPair>
+__device__ __forceinline__ void beat(volatile int* abort) {
+  if ((threadIdx.x & 31) != 0) return;
+  const int now = static_cast<int>(beat_now());
+  abort[kBeat] = now;
+  if (kPair) st_shared_remote(mapa_shared(smem_addr(const_cast<int*>(abort) + kBeat), cluster_cta_rank() ^ 1u), now);
+}
+
+__device__ __forceinline__ bool wait_with_beat(uint32_t bar, uint32_t parity, volatile int* abort) {
+  return mbar_wait(bar, parity, abort, kWaitLimitNs, abort + kBeat);
+}
 
 __device__ __forceinline__ float bf16_at(const uint16_t* x) {
   return __uint_as_float(static_cast<uint32_t>(*x) << 16);

@@ -32,7 +32,8 @@
 // A value that is not finite, at a key that some rows of a tile see and others do not,
 // would reach all of them through 0 * NaN.  Key rows that no token of the tile sees are
 // zeroed before they are values; a row whose output is not finite while its sum is, and
-// which does not see such a key of the tile, computes again from its own (attend_again).
+// which does not see such a key of the tile, computes again from its own (attend_again; the
+// other roles' waits allow for the time, latent.cuh).
 //
 // Bound: HBM while all CTAs stream (64 rows of 32 heads, 512 to 8192 keys: 322 MB in 45 us, the
 // copy rate), then the starts, the tiles' ends and the join: 68.1 us, 4.8 TB/s.  (Prefetches
@@ -67,7 +68,7 @@ struct LatentSmem {
   static constexpr size_t keys = (bars + 8 * kNumBars + 15) & ~size_t(15);  // int2 a row
   static constexpr size_t alpha = keys + 8 * kLatentRows;      // factors of a raise; at the end 1 / sum
   static constexpr size_t ref = alpha + 4 * kLatentRows;
-  static constexpr size_t misc = ref + 4 * kLatentRows;      // abort, tensor memory, share
+  static constexpr size_t misc = ref + 4 * kLatentRows;      // abort, tensor memory, beat, share
   static constexpr size_t end = misc + 256;
   static_assert(end - bars <= kMisc, "barriers and row data");
   static_assert(kStages >= 2, "stages");
@@ -109,7 +110,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < L::kNumBars; ++i) mbar_init(full + 8 * i, 1);
     for (int i = 0; i < kStages; ++i) mbar_init(full + 8 * i, kGroups);
     mbar_init(pfull, 4);
-    *abort_flag = 0;
+    abort_flag[0] = abort_flag[kBeat] = 0;
     fence_mbarrier_init();
   }
   if (warp == 1) tmem_alloc(smem_addr(misc + 1), L::kCols);
@@ -154,7 +155,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t dst = smem_addr(smem + L::stage) + st * L::kStage;
           for (int gr = 0; ok && gr < kGroups; ++gr) {
             const uint32_t fb = full + 8 * st;
-            if (g >= kStages) ok = mbar_wait(empty + 8 * (st * kGroups + gr), ((g / kStages) - 1) & 1, abort_flag);
+            if (g >= kStages) ok = wait_with_beat(empty + 8 * (st * kGroups + gr), ((g / kStages) - 1) & 1, abort_flag);
             if (!ok) break;
             mbar_arrive_expect_tx(fb, L::kGroup);
             if (p.rope_dim == 64) {
@@ -168,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++issued;
           }
           if (ok && i == 0 && u > 0) {
-            ok = mbar_wait(qempty, (u - 1) & 1, abort_flag);
+            ok = wait_with_beat(qempty, (u - 1) & 1, abort_flag);
             if (ok) load_q(t);
           }
         }
@@ -280,7 +281,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         idle = 0;
       } else if ((++idle & 255u) == 0) {
         if (idle == 256u) t0 = global_timer_ns();
-        const bool late = global_timer_ns() - t0 > kWaitLimitNs || idle >= kWaitLimitIters;
+        const bool late = (global_timer_ns() - t0 > kWaitLimitNs && !beat_is_recent(abort_flag + kBeat)) ||
+                          idle >= kWaitLimitIters;
         if (__any_sync(0xffffffffu, late || *abort_flag != 0)) {
           *abort_flag = 1;
           break;
@@ -289,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // no product is in flight when the tensor memory goes
     umma_commit_warp(fin);
-    mbar_wait(fin, 0, abort_flag);
+    wait_with_beat(fin, 0, abort_flag);
     __syncwarp();
   } else {
     // ============================== softmax ===============================
@@ -332,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int lp = un.first + j0 + i, kb = lp * kPage;
         const int page = un.row >= 0 ? trow[lp] : -1;
         const bool held = page >= 0 && page < p.num_pages;
-        ok = __all_sync(0xffffffffu, mbar_wait(sfull + 8 * (g & 1), (g >> 1) & 1, abort_flag));
+        ok = __all_sync(0xffffffffu, wait_with_beat(sfull + 8 * (g & 1), (g >> 1) & 1, abort_flag));
         tc_fence_after();
         uint32_t r[NX];
         if (ok) {
@@ -418,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (named_barrier_or(kSoftBar, 128, mx > kRaiseLog2 || !ok)) {
           // ---- references raised (or set) with the page's maximum ----
-          if (g > 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait(pvdone, (g - 1) & 1, abort_flag));
+          if (g > 0 && ok) ok = __all_sync(0xffffffffu, wait_with_beat(pvdone, (g - 1) & 1, abort_flag));
           if (named_barrier_or(kSoftBar, 128, !ok)) {
             ok = false;
             break;
@@ -471,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           exponents();
         }
         // ---- P^T into shared memory, once the product before has read the last one ----
-        if (g > 0) ok = __all_sync(0xffffffffu, mbar_wait(pvdone, (g - 1) & 1, abort_flag));
+        if (g > 0) ok = __all_sync(0xffffffffu, wait_with_beat(pvdone, (g - 1) & 1, abort_flag));
         uint8_t* prow = smem + L::p + ka * 128 + (lane & 3) * 4;
 #pragma unroll
         for (int x = 0; x < NX; x += 4) {
@@ -505,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(pfull);
       }
       // ---- the unit's end: sums joined, outputs or partial sums stored ----
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(pvdone, (g - 1) & 1, abort_flag));
+      if (ok) ok = __all_sync(0xffffffffu, wait_with_beat(pvdone, (g - 1) & 1, abort_flag));
       if (named_barrier_or(kSoftBar, 128, !ok)) {
         ok = false;
         break;
@@ -601,8 +603,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           in_lo = max(in_lo, row_keys[rr].x);
           in_hi = min(in_hi, row_keys[rr].y);
         }
-        const int2 bad_keys = odd_keys(p, trow, seg_lo, seg_hi, __reduce_max_sync(0xffffffffu, in_lo),
-                                       __reduce_min_sync(0xffffffffu, in_hi));
+        const int2 bad_keys = odd_keys<false>(p, trow, seg_lo, seg_hi, __reduce_max_sync(0xffffffffu, in_lo),
+                                       __reduce_min_sync(0xffffffffu, in_hi), abort_flag);
 #pragma unroll 1
         for (int rr = 0; rr < nrows; ++rr) {
           if (s_alpha[rr] != s_alpha[rr]) continue;  // (a sum that is NaN is the row's own: all of it is)
@@ -621,8 +623,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!__any_sync(0xffffffffu, bad)) continue;
           __syncwarp();  // (other lanes stored what is stored again)
           float acc[NB];
-          attend_again<NB, 128>(p, p.q + static_cast<size_t>(rowbase + rr) * w, trow, max(row_keys[rr].x, seg_lo),
-                            min(row_keys[rr].y, seg_hi), s_ref[rr], qt * 32 + lane, acc);
+          attend_again<NB, 128, false>(p, p.q + static_cast<size_t>(rowbase + rr) * w, trow, max(row_keys[rr].x, seg_lo),
+                            min(row_keys[rr].y, seg_hi), s_ref[rr], qt * 32 + lane, acc, abort_flag);
 #pragma unroll
           for (int mb = 0; mb < NB; ++mb) {
             const int dim = mb * 128 + qt * 32 + lane;

@@ -57,7 +57,7 @@ struct PairSmem {
   static constexpr int kNumBars = 4 * kStages + 9;
   static constexpr size_t ref = bars + 8 * kNumBars;      // [64] a row's first score; in a raise the maxima
   static constexpr size_t pair = ref + 4 * kRows;         // [2][64] what a row's two threads tell each other
-  static constexpr size_t misc = pair + 8 * kRows;        // abort, tensor memory, share
+  static constexpr size_t misc = pair + 8 * kRows;        // abort, tensor memory, beat, share
   static constexpr size_t end = misc + 256;
   static_assert(end - bars <= kMisc, "barriers and row data");
   static_assert(kStages >= 2, "stages");
@@ -109,7 +109,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     mbar_init(qfull, copies);
     for (int i = 0; i < 2; ++i) mbar_init(pfull + 8 * i, 8);  // the softmax warps of both CTAs
-    *abort_flag = 0;
+    abort_flag[0] = abort_flag[kBeat] = 0;
     fence_mbarrier_init();
   }
   if (warp == 1) tmem2_alloc(smem_addr(misc + 1), L::kCols);
@@ -169,7 +169,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int i = 0; i < n; ++i, ++g) {
           const int page = page_of(un, i, true);
           const int st = g % kStages;
-          if (g >= kStages && !mbar_wait(kempty + 8 * st, ((g / kStages) - 1) & 1, abort_flag)) return false;
+          if (g >= kStages && !wait_with_beat(kempty + 8 * st, ((g / kStages) - 1) & 1, abort_flag)) return false;
           const uint32_t dst = smem_addr(smem + L::k) + st * L::kK, fb = kfull + 8 * st;
           mbar_arrive_expect_tx(fb, L::kK);
           if (p.rope_dim == 64) {
@@ -181,7 +181,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
           }
           if (i == 0 && u > 0) {
-            if (!mbar_wait(qempty, (u - 1) & 1, abort_flag)) {
+            if (!wait_with_beat(qempty, (u - 1) & 1, abort_flag)) {
               ++g;  // (this page was asked for)
               return false;
             }
@@ -202,7 +202,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int i = 0; i < n; ++i, ++g) {
           const int page = page_of(un, i, false);
           const int st = g % kStages;
-          if (g >= kStages && !mbar_wait(vempty + 8 * st, ((g / kStages) - 1) & 1, abort_flag)) return false;
+          if (g >= kStages && !wait_with_beat(vempty + 8 * st, ((g / kStages) - 1) & 1, abort_flag)) return false;
           mbar_arrive_expect_tx(vfull + 8 * st, L::kV);
           tma_load_4d(smem_addr(smem + L::v) + st * L::kV, &vmap, 0, 0, rank * NB, page * 8, vfull + 8 * st);
         }
@@ -218,11 +218,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int g = 0;
       units([&](const Unit&, int n, int u) {
         if (warp == 1) {
-          if (!mbar_wait(qfull, u & 1, abort_flag)) return false;
+          if (!wait_with_beat(qfull, u & 1, abort_flag)) return false;
           mbar_arrive_remote(qfull0);
         }
         for (int i = 0; i < n; ++i, ++g) {
-          if (!mbar_wait(mine + 8 * (g % kStages), (g / kStages) & 1, abort_flag)) return false;
+          if (!wait_with_beat(mine + 8 * (g % kStages), (g / kStages) & 1, abort_flag)) return false;
           mbar_arrive_remote(theirs + 8 * (g % kStages));
         }
         return true;
@@ -320,7 +320,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         idle = 0;
       } else if ((++idle & 255u) == 0) {
         if (idle == 256u) t0 = global_timer_ns();
-        const bool late = global_timer_ns() - t0 > kWaitLimitNs || idle >= kWaitLimitIters;
+        const bool late = (global_timer_ns() - t0 > kWaitLimitNs && !beat_is_recent(abort_flag + kBeat)) ||
+                          idle >= kWaitLimitIters;
         if (__any_sync(0xffffffffu, late || *abort_flag != 0)) {
           *abort_flag = 1;
           break;
@@ -329,7 +330,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     // no product is in flight when the tensor memory goes
     umma2_commit_both_warp(fin);
-    mbar_wait(fin, 0, abort_flag);
+    wait_with_beat(fin, 0, abort_flag);
     __syncwarp();
   } else {
     // ============================== softmax ===============================
@@ -364,7 +365,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int lp = un.first + j0 + i, kb = lp * kPage, k0 = kb + half * 32;
         const int page = un.row >= 0 ? trow[lp] : -1;
         const bool held = page >= 0 && page < p.num_pages;
-        ok = __all_sync(0xffffffffu, mbar_wait(sfull + 8 * (g & 1), (g >> 1) & 1, abort_flag));
+        ok = __all_sync(0xffffffffu, wait_with_beat(sfull + 8 * (g & 1), (g >> 1) & 1, abort_flag));
         tc_fence_after();
         uint32_t r[32];
         if (ok) {
@@ -410,7 +411,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const bool raise = unset ? mx > -INFINITY : mx > kRaiseLog2;
         if (named_barrier_or(kSoftBar, 128, raise || !ok)) {
           // ---- references raised (or set) with the page's maximum ----
-          if (g > 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait(pvdone + 8 * ((g - 1) & 1), ((g - 1) >> 1) & 1, abort_flag));
+          if (g > 0 && ok) ok = __all_sync(0xffffffffu, wait_with_beat(pvdone + 8 * ((g - 1) & 1), ((g - 1) >> 1) & 1, abort_flag));
           if (named_barrier_or(kSoftBar, 128, !ok)) {
             ok = false;
             return false;
@@ -450,7 +451,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         if (force) force = named_barrier_or(kSoftBar, 128, unset);
         // ---- P into shared memory, once the product of two pages before has read what is there ----
-        if (g > 1) ok = __all_sync(0xffffffffu, mbar_wait(pvdone + 8 * (g & 1), ((g - 2) >> 1) & 1, abort_flag));
+        if (g > 1) ok = __all_sync(0xffffffffu, wait_with_beat(pvdone + 8 * (g & 1), ((g - 2) >> 1) & 1, abort_flag));
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t w[4];
@@ -464,7 +465,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         // ---- value rows that no token of the unit sees may hold anything: zero ----
         if (!(held && kb >= un.kmin && kb + kPage <= un.kmax)) {
-          ok = ok && __all_sync(0xffffffffu, mbar_wait(vfull + 8 * (g % kStages), (g / kStages) & 1, abort_flag));
+          ok = ok && __all_sync(0xffffffffu, wait_with_beat(vfull + 8 * (g % kStages), (g / kStages) & 1, abort_flag));
           uint8_t* v = smem + L::v + (g % kStages) * L::kV;
           // rows [0, below) and [above, 64), 16 bytes of a row a thread (eight threads a line)
           const int below = held ? min(kPage, max(0, un.kmin - kb)) : kPage;
@@ -484,7 +485,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive_remote_shared(pfull0 + 8 * (g & 1));
       }
       // ---- the unit's end: sums joined, outputs or partial sums stored ----
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(pvdone + 8 * ((g - 1) & 1), ((g - 1) >> 1) & 1, abort_flag));
+      if (ok) ok = __all_sync(0xffffffffu, wait_with_beat(pvdone + 8 * ((g - 1) & 1), ((g - 1) >> 1) & 1, abort_flag));
       if (named_barrier_or(kSoftBar, 128, !ok)) {
         ok = false;
         return false;
@@ -588,8 +589,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       if ((odd[0] | odd[1] | odd[2] | odd[3]) != 0u) {
         const int seg_lo = max(un.kmin, (un.first + j0) * kPage), seg_hi = min(un.kmax, (un.first + j0 + n) * kPage);
-        const int2 bad_keys = odd_keys(p, trow, seg_lo, seg_hi, __reduce_max_sync(0xffffffffu, hi > lo ? lo : 0),
-                                       __reduce_min_sync(0xffffffffu, hi > lo ? hi : 0x7fffffff));
+        const int2 bad_keys = odd_keys<true>(p, trow, seg_lo, seg_hi, __reduce_max_sync(0xffffffffu, hi > lo ? lo : 0),
+                                       __reduce_min_sync(0xffffffffu, hi > lo ? hi : 0x7fffffff), abort_flag);
 #pragma unroll 1
         for (int k = 0; k < 32; ++k) {
           const unsigned m = k < 16 ? (k < 8 ? odd[0] : odd[1]) : (k < 24 ? odd[2] : odd[3]);
@@ -601,8 +602,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const int ro = rank * kRows + (qt & 1) * 32 + k, w = p.latent_dim + p.rope_dim;
           __syncwarp();
           float acc[2 * NB];
-          attend_again<2 * NB, 32>(p, p.q + static_cast<size_t>(rowbase + ro) * w, trow, max(lo_k, seg_lo), min(hi_k, seg_hi),
-                                   __shfl_sync(0xffffffffu, nref, k), half * (C / 2) + lane, acc);
+          attend_again<2 * NB, 32, true>(p, p.q + static_cast<size_t>(rowbase + ro) * w, trow, max(lo_k, seg_lo), min(hi_k, seg_hi),
+                                   __shfl_sync(0xffffffffu, nref, k), half * (C / 2) + lane, acc, abort_flag);
           const float f = __shfl_sync(0xffffffffu, inv, k);
 #pragma unroll
           for (int i = 0; i < 2 * NB; ++i) {

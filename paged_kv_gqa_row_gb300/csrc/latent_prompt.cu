@@ -35,8 +35,10 @@
 //
 // Values that are not finite, at keys that some rows of a tile see and others do not,
 // reach all of them through 0 * NaN: a row whose output is not finite computes it again
-// from its own keys (attend_row), if there is such a value among the tile's keys behind it.
-// Key rows past the tile's last key are zeroed.
+// from its own keys, if there is such a value among the tile's keys behind it.  That takes
+// long behind long prefixes (a warp's 32 rows behind 60 000 keys 0.34 s), so it is done when
+// all the worker's tiles are stored and no role waits for another (repair_rows).  Key rows
+// past the tile's last key are zeroed.
 #include <algorithm>
 
 #include "latent.cuh"
@@ -71,7 +73,7 @@ struct PromptSmem {
   // [worker] kfull, kempty [stages], qfull[2], iempty[2], qempty, vfull, vempty, sfull, pfull[2], pvdone, efree
   static constexpr size_t bars = kWorkers * worker;
   static constexpr int kNumBars = 2 * kStages + 12;
-  static constexpr size_t misc = bars + kWorkers * kNumBars * sizeof(uint64_t);  // [0] abort, [1] tensor memory, [2] tiles in order
+  static constexpr size_t misc = bars + kWorkers * kNumBars * sizeof(uint64_t);  // [0] abort, [1] tensor memory, [2] tiles in order, [3] [4] repair
   static constexpr size_t info = misc + 64;                    // [worker][2] PromptTile: the tiles under way
   static constexpr size_t order = info + 128;                  // [kMaxOrderedTiles] tile ids, 16 bits each
   static constexpr size_t end = order + kMaxOrderedTiles * 2;
@@ -113,37 +115,36 @@ __device__ __forceinline__ PromptTile prompt_tile(const LatentPromptParams& p, i
   return t;
 }
 
-// The last key of [a, b) of a prompt and head (kv: its first key's row) that has a number in
-// columns c0 .. c0 + D / 2 - 1 of its values that is not finite, or -1.  The whole warp.
+// The last key of [a, b) of a prompt and head (kv: its first key's row) that has a number among
+// its values that is not finite, or -1.  The whole warp.
 template <int D>
-__device__ __noinline__ int last_odd_key(const LatentPromptParams& p, const uint16_t* kv, int a, int b, int c0) {
-  constexpr int kLanes = D / 16, kKeys = 32 / kLanes;  // lanes a key, keys at once
+__device__ __noinline__ int last_odd_key(const LatentPromptParams& p, const uint16_t* kv, int a, int b) {
+  constexpr int kLanes = D / 8, kKeys = 32 / kLanes;  // lanes a key, keys at once
   const int lane = threadIdx.x & 31, piece = lane % kLanes;
 #pragma unroll 1
   for (int k0 = b - 1; k0 >= a; k0 -= kKeys) {
     const int key = k0 - lane / kLanes;
-    const uint16_t* v = kv + static_cast<size_t>(max(key, a)) * p.heads * (2 * D) + D + c0 + piece * 8;
+    const uint16_t* v = kv + static_cast<size_t>(max(key, a)) * p.heads * (2 * D) + D + piece * 8;
     const unsigned odd = __ballot_sync(0xffffffffu, key >= a && odd_halves(*reinterpret_cast<const uint4*>(v)) != 0u);
     if (odd != 0u) return k0 - (__ffs(odd) - 1) / kLanes;
   }
   return -1;
 }
 
-// One row's value sums over its own keys, relative to the maximum and sum of its softmax:
-// columns c0 .. c0 + D / 2 - 1, the whole warp: a key a lane for the scores, the columns over
-// the lanes for the sums.
+// One row's output from its own keys: the whole warp, a key a lane for the scores, the columns
+// over the lanes for the sums, relative to the maximum so far.
 template <int D>
 __device__ __noinline__ void attend_row(const LatentPromptParams& p, const uint16_t* q, const uint16_t* kv,
-                                        const uint16_t* k_rope, int keys, float m, float inv, uint16_t* out, int c0) {
-  constexpr int NV = D / 64;
+                                        const uint16_t* k_rope, int keys, uint16_t* out) {
+  constexpr int NV = D / 32;
   const int lane = threadIdx.x & 31;
-  float acc[NV];
+  float m = -INFINITY, l = 0.f, acc[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) acc[i] = 0.f;
   const size_t stride = static_cast<size_t>(p.heads) * 2 * D;
 #pragma unroll 1
   for (int key0 = 0; key0 < keys; key0 += 32) {
-    const int key = min(key0 + lane, keys - 1);
+    const int key = min(key0 + lane, keys - 1), n = min(32, keys - key0);
     const uint16_t* k = kv + key * stride;
     const uint16_t* r = k_rope + key * p.rope_stride;
     float s = 0.f;
@@ -152,18 +153,79 @@ __device__ __noinline__ void attend_row(const LatentPromptParams& p, const uint1
 #pragma unroll 4
     for (int i = 0; i < p.rope_dim; i += 8)
       s = dot8(*reinterpret_cast<const uint4*>(q + D + i), *reinterpret_cast<const uint4*>(r + i), s);
-    const float e = exp2f(fmaf(s, p.scale_log2, -m));
-    const int n = min(32, keys - key0);
+    s *= p.scale_log2;
+    float top = m;  // (the last lanes' keys repeat the last one; of NaN scores the sum tells)
+    top = fmaxf(top, s);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (top > m) {
+      const float f = exp2f(m - top);
+      l *= f;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) acc[j] *= f;
+      m = top;
+    }
+    const float e = lane < n ? exp2f(s - (m == -INFINITY ? 0.f : m)) : 0.f;
+    l += e;
 #pragma unroll 4
     for (int i = 0; i < n; ++i) {
       const float f = __shfl_sync(0xffffffffu, e, i);
-      const uint16_t* v = kv + (key0 + i) * stride + D + c0 + lane;
+      const uint16_t* v = kv + (key0 + i) * stride + D + lane;
 #pragma unroll
       for (int j = 0; j < NV; ++j) acc[j] = fmaf(f, bf16_at(v + 32 * j), acc[j]);
     }
   }
 #pragma unroll
-  for (int j = 0; j < NV; ++j) out[c0 + lane + 32 * j] = static_cast<uint16_t>(pack_bf16x2(acc[j] * inv, 0.f));
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  const float inv = l > 0.f ? 1.f / l : l;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) out[lane + 32 * j] = static_cast<uint16_t>(pack_bf16x2(l == 0.f ? 0.f : acc[j] * inv, 0.f));
+}
+
+// A worker's item (tile, head) in its turn `k`: they are taken in the tiles' order, every other
+// round backwards.  False: there is none left; n == 0: nothing to do.
+__device__ __forceinline__ bool worker_item(const LatentPromptParams& p, const uint16_t* order, int tiles, int wid, int workers,
+                                            long long k, PromptTile& x) {
+  const long long items = static_cast<long long>(tiles) * p.heads;
+  if (k * workers >= items) return false;
+  const long long i = k * workers + (k & 1 ? workers - 1 - wid : wid);
+  x.n = 0;
+  if (i >= items) return true;
+  const int at = static_cast<int>(i / p.heads);
+  x = prompt_tile(p, order != nullptr ? order[at] : p.tiles - 1 - at);
+  x.h = static_cast<int>(i % p.heads);
+  return true;
+}
+
+// The rows of a softmax warp (rows row0 .. + 31 of its worker's tiles, all stored) whose output is not
+// finite, again, where a value behind what they see is not: at the end, when nothing waits for them.
+template <int D>
+__device__ __noinline__ void repair_rows(const LatentPromptParams& p, const uint16_t* order, int tiles, int wid, int workers,
+                                         int row0) {
+  const int lane = threadIdx.x & 31;
+  PromptTile x;
+#pragma unroll 1
+  for (long long k = 0; worker_item(p, order, tiles, wid, workers, k, x); ++k) {
+    if (row0 >= x.n) continue;
+    uint16_t* out = p.out + (static_cast<size_t>(x.q0 + row0) * p.heads + x.h) * D;
+    uint32_t odd = 0u;
+    if (row0 + lane < x.n) {
+#pragma unroll 1
+      for (int i = 0; i < D; i += 8) odd |= odd_halves(*reinterpret_cast<const uint4*>(out + static_cast<size_t>(lane) * p.heads * D + i));
+    }
+    unsigned todo = __ballot_sync(0xffffffffu, odd != 0u);
+    if (todo == 0u) continue;
+    const uint16_t* kv = p.kv + (static_cast<size_t>(x.k0) * p.heads + x.h) * (2 * D);
+    const int bad_key = last_odd_key<D>(p, kv, max(0, x.first + row0), x.keys);
+    while (todo != 0u) {
+      const int rr = __ffs(todo) - 1, sees = x.first + row0 + rr;
+      todo &= todo - 1;
+      if (sees > bad_key) break;  // (it sees them all: what is not finite is its own; so do those after it)
+      __syncwarp();
+      attend_row<D>(p, p.q + (static_cast<size_t>(x.q0 + row0 + rr) * p.heads + x.h) * (D + p.rope_dim), kv,
+                    p.k_rope + static_cast<long long>(x.k0) * p.rope_stride, sees, out + static_cast<size_t>(rr) * p.heads * D);
+    }
+  }
 }
 
 __device__ __forceinline__ void drain(uint32_t bar, int parity) {
@@ -196,8 +258,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t smem_w = smem_addr(smem) + g * static_cast<uint32_t>(L::worker);
   int* misc = reinterpret_cast<int*>(smem + L::misc);
   volatile int* abort_flag = misc;
+  volatile int* repair = misc + 3;  // [worker] a row's output is not finite, its sum is
   volatile PromptTile* info = reinterpret_cast<volatile PromptTile*>(smem + L::info) + 2 * g;
   uint16_t* order = reinterpret_cast<uint16_t*>(smem + L::order);
+  const int workers = static_cast<int>(gridDim.x >> 1) * kWorkers;
+  const int wid = static_cast<int>(blockIdx.x >> 1) + g * static_cast<int>(gridDim.x >> 1);
 
   if (lane == 0 && (warp == 0 || warp == 2)) {
     // rank 0's full barriers also count the relay's arrival for rank 1's copy
@@ -221,6 +286,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
   if (tid == 0) {
     *abort_flag = 0;
+    repair[0] = repair[1] = 0;
     misc[2] = p.tiles;
   }
   if (warp == 1) tmem2_alloc(smem_addr(misc + 1), L::kTmemCols);
@@ -258,19 +324,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // (the launch's registers, 384 x 168, hold 128 x 80 and 256 x 208)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     if (lane == 0) {
-      // The workers take the items (tile, head) in turn, in the tiles' order, every other
-      // round backwards.
-      const long long items = static_cast<long long>(misc[2]) * p.heads;
-      const int clusters = static_cast<int>(gridDim.x >> 1), workers = clusters * kWorkers;
-      const int wid = static_cast<int>(blockIdx.x >> 1) + g * clusters;
       int it = 0, nk = 0, nv = 0;  // tiles; copies issued
       bool ok = true;
-      for (long long k = 0; ok && k * workers < items; ++k) {
-        const long long i = k * workers + (k & 1 ? workers - 1 - wid : wid);
-        if (i >= items) continue;
-        const int at = static_cast<int>(i / p.heads);
-        PromptTile x = prompt_tile(p, ordered ? order[at] : p.tiles - 1 - at);
-        x.h = static_cast<int>(i % p.heads);
+      PromptTile x;
+      x.bad = 0;
+      for (long long k = 0; ok && worker_item(p, ordered ? order : nullptr, misc[2], wid, workers, k, x); ++k) {
         if (!ordered && x.bad && x.h == 0 && rank == 0 && p.status != nullptr) atomicOr(p.status, LNK_DEV_SEGMENT);
         if (x.n <= 0) continue;
         const int b = it & 1;
@@ -597,7 +655,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           odd |= odd_halves(w[i]);
         }
         // (a NaN sum is the row's own: all of it is NaN)
-        const bool again = live && odd != 0u && l == l;
+        if (live && odd != 0u && l == l) repair[g] = 1;
         // through shared memory (where the values were, whose products have ended), so that a store
         // covers whole lines
         uint8_t* mine = smem + g * L::worker + L::v + qt * (32 * 16 * kPieces);
@@ -616,22 +674,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int i = 0; i < kPieces; ++i)
           if ((row & ~(kPieces - 1)) + i < tile.n)
             *reinterpret_cast<uint4*>(o + static_cast<size_t>(i) * p.heads * D) = w[i];
-        unsigned todo = __ballot_sync(0xffffffffu, again);
-        if (todo != 0u) {
-          const uint16_t* kv = p.kv + (static_cast<size_t>(tile.k0) * p.heads + tile.h) * (2 * D);
-          const int bad_key = last_odd_key<D>(p, kv, max(0, tile.first + row - lane), tile.keys, hf * (D / 2));
-          while (todo != 0u) {
-            const int src = __ffs(todo) - 1;
-            todo &= todo - 1;
-            const int rr = row - lane + src;
-            if (tile.first + rr > bad_key) break;  // (it sees them all: what is not finite is its own; so do those after it)
-            __syncwarp();
-            attend_row<D>(p, p.q + (static_cast<size_t>(tile.q0 + rr) * p.heads + tile.h) * (D + p.rope_dim), kv,
-                          p.k_rope + static_cast<long long>(tile.k0) * p.rope_stride, tile.first + rr,
-                          __shfl_sync(0xffffffffu, m_ref, src), __shfl_sync(0xffffffffu, inv, src),
-                          p.out + (static_cast<size_t>(tile.q0 + rr) * p.heads + tile.h) * D, hf * (D / 2));
-          }
-        }
         __syncwarp();
       }
       fence_proxy_async_smem();
@@ -639,6 +681,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(efree);
     }
     if (!ok) *abort_flag = 1;
+    else if (__any_sync(0xffffffffu, repair[g] != 0))
+      repair_rows<D>(p, ordered ? order : nullptr, misc[2], wid, workers, static_cast<int>(rank) * kRows + qt * 32);
   }
   __syncwarp();
   if (*abort_flag && lane == 0 && p.status != nullptr) atomicOr(p.status, LNK_DEV_TIMEOUT);

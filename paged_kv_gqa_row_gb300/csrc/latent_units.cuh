@@ -93,10 +93,12 @@ __device__ __noinline__ bool page_seen(const LatentParams& p, int t, int nt, int
 
 // The first key from `from` on (to `to`, exclusive, in steps of +1 or -1) whose latent has a
 // number that is not finite, or -1.  The whole warp.
-__device__ __noinline__ int odd_key(const LatentParams& p, const int32_t* trow, int from, int to, int step) {
+template <bool kPair>
+__device__ __noinline__ int odd_key(const LatentParams& p, const int32_t* trow, int from, int to, int step, volatile int* abort) {
   const int w = p.latent_dim + p.rope_dim, lane = threadIdx.x & 31;
 #pragma unroll 1
   for (int key = from; key != to; key += step) {
+    if (key % kPage == 0) beat<kPair>(abort);
     const int page = trow[key / kPage];
     if (page < 0 || page >= p.num_pages) continue;
     const uint16_t* c = p.pool + (static_cast<size_t>(page) * kPage + key % kPage) * w;
@@ -110,23 +112,26 @@ __device__ __noinline__ int odd_key(const LatentParams& p, const int32_t* trow, 
 
 // The keys of [lo, hi) that rows which all see [in_lo, in_hi) may not see and that hold numbers
 // which are not finite: a row that starts behind x or ends at or before y has some of them.
-__device__ __forceinline__ int2 odd_keys(const LatentParams& p, const int32_t* trow, int lo, int hi, int in_lo, int in_hi) {
+template <bool kPair>
+__device__ __forceinline__ int2 odd_keys(const LatentParams& p, const int32_t* trow, int lo, int hi, int in_lo, int in_hi,
+                                         volatile int* abort) {
   const int a = min(in_lo, hi), b = max(in_hi, lo);
-  const int x = lo < a ? odd_key(p, trow, lo, a, 1) : -1;
-  return make_int2(x < 0 ? 0x7fffffff : x, b < hi ? odd_key(p, trow, hi - 1, b - 1, -1) : -1);
+  const int x = lo < a ? odd_key<kPair>(p, trow, lo, a, 1, abort) : -1;
+  return make_int2(x < 0 ? 0x7fffffff : x, b < hi ? odd_key<kPair>(p, trow, hi - 1, b - 1, -1, abort) : -1);
 }
 
 // One row's sums over its own visible keys [lo, hi), relative to the reference that its softmax
 // used: number d + STEP i of the latent in acc[i].  The whole warp: a key a lane for the
 // scores, the numbers of a key over the lanes for the sums.
-template <int NV, int STEP>
+template <int NV, int STEP, bool kPair>
 __device__ __noinline__ void attend_again(const LatentParams& p, const uint16_t* q, const int32_t* trow, int lo, int hi,
-                                          float nref, int d, float (&acc)[NV]) {
+                                          float nref, int d, float (&acc)[NV], volatile int* abort) {
   const int w = p.latent_dim + p.rope_dim, lane = threadIdx.x & 31;
 #pragma unroll
   for (int i = 0; i < NV; ++i) acc[i] = 0.f;
 #pragma unroll 1
   for (int key0 = lo; key0 < hi; key0 += 32) {
+    beat<kPair>(abort);
     const int key = key0 + lane;
     const int page = key < hi ? trow[key / kPage] : -1;
     const bool here = page >= 0 && page < p.num_pages;

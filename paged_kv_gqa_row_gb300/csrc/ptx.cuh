@@ -106,19 +106,26 @@ __device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
 // false) when *abort becomes non-zero or after `limit_ns` (about two seconds
 // unless a self-test asks for less), in which case it sets *abort so that
 // the other roles of the CTA stop too.  The iteration count is capped as
-// well, so the loop ends even if the timer does not advance.
+// well, so the loop ends even if the timer does not advance.  `beat`, if
+// there is one, is a word into which a role at long work outside the pipeline
+// writes the time now and then (beat_now): the limit counts from there.
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr uint32_t kWaitLimitIters = 1u << 30;
 
+__device__ __forceinline__ uint32_t beat_now() { return static_cast<uint32_t>(global_timer_ns() >> 10); }
+__device__ __forceinline__ bool beat_is_recent(const volatile int* beat, uint64_t limit_ns = kWaitLimitNs) {
+  return beat_now() - static_cast<uint32_t>(*beat) <= static_cast<uint32_t>(limit_ns >> 10);
+}
+
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort,
-                                          uint64_t limit_ns = kWaitLimitNs) {
+                                          uint64_t limit_ns = kWaitLimitNs, const volatile int* beat = nullptr) {
   if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = global_timer_ns();
   for (uint32_t it = 1; it < kWaitLimitIters; ++it) {
     if (mbar_try_wait(bar, parity)) return true;
     if ((it & 255u) == 0) {
       if (*abort) return false;
-      if (global_timer_ns() - t0 > limit_ns) break;
+      if (global_timer_ns() - t0 > limit_ns && !(beat != nullptr && beat_is_recent(beat, limit_ns))) break;
     }
   }
   *abort = 1;
@@ -461,6 +468,11 @@ __device__ __forceinline__ uint32_t mapa_shared(uint32_t addr, uint32_t rank) {
   uint32_t r;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
+}
+
+// A word of a CTA of the cluster, by its shared::cluster address.
+__device__ __forceinline__ void st_shared_remote(uint32_t cluster_addr, int v) {
+  asm volatile("st.relaxed.cluster.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
 }
 
 // Arrive on an mbarrier named by its shared::cluster address (in this CTA or
