@@ -594,9 +594,12 @@ size_t lnk_latent_workspace_size(const lnk_latent_desc* desc);
  *   T        tokens (0 is allowed and enqueues nothing).  No two active ones may have
  *            the same place in the pool (it would hold numbers of both)
  *
- * Element i of a rotated part turns with element i + R / 2.  Numerics, the order of
- * reads before the kernel before this one has ended, and what infinities and NaN do:
- * as in lnk_paged_append_rope, the norm being that of its QK-norm over C numbers.
+ * Element i of a rotated part turns with element i + R / 2 (a model whose rotation pairs
+ * neighbours needs its projections' rows in that order).  The frequencies are those of
+ * lnk_rope_desc, a base and its rescale by wavelength, and no others: rescalings that blend by
+ * dimension (YaRN) cannot be expressed, and no table of frequencies is taken.  Numerics, the
+ * order of reads before the kernel before this one has ended, and what infinities and NaN
+ * do: as in lnk_paged_append_rope, the norm being that of its QK-norm over C numbers.
  */
 lnk_status lnk_latent_append(const lnk_latent_desc* desc, const lnk_rope_desc* rope, const lnk_bf16* q,
                              int64_t q_stride, const lnk_bf16* kv, const int32_t* positions,

@@ -35,9 +35,9 @@
 // which does not see such a key of the tile, computes again from its own (attend_again; the
 // other roles' waits allow for the time, latent.cuh).
 //
-// Bound: HBM while all CTAs stream (64 rows of 32 heads, 512 to 8192 keys: 322 MB in 45 us, the
-// copy rate), then the starts, the tiles' ends and the join: 68.1 us, 4.8 TB/s.  (Prefetches
-// into L2 ahead of the copies: 5 us more.)
+// Bound: HBM while all CTAs stream (64 rows of 32 heads, 512 to 8192 keys: 322 MB in 47 us, about
+// the copy rate), then the start (9 us to the first value product), the tiles' ends and the
+// join: 68.6 us, 4.7 TB/s.  (Prefetches into L2 ahead of the copies: 5 us more.)
 #include "latent_units.cuh"
 #include "ptx.cuh"
 

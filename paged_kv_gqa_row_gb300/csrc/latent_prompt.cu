@@ -25,9 +25,9 @@
 // 112 with the products of P's first half begun before the second is there (its first quarter
 // 107.5 to 105 at that stage, three quarters 112, each quarter on its own 114); 105 with sums
 // in scalars (pairs of float32 cost the registers' order: 113 to 107) and the registers of the
-// loading warps given to the softmax; 103 with votes where reductions ended the waits:
-// 1.0 Pflop/s.  Scores in halves of 64 keys, the second of the next step before this one's P.V: 5
-// us more.
+// loading warps given to the softmax; 103 with votes where reductions ended the waits, 105 now that
+// rows are repaired at the end: 0.98 Pflop/s.  Scores in halves of 64 keys, the second of the next
+// step before this one's P.V: 5 us more.
 //
 // Tile ids: prompt n's tiles are base(n) = q_starts[n] / 256 + n onwards, which leaves
 // every prompt room for its tiles without a sum over the prompts before it; ids without
