@@ -321,9 +321,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         idle = 0;
       } else if ((++idle & 255u) == 0) {
         if (idle == 256u) t0 = global_timer_ns();
-        const bool late = (global_timer_ns() - t0 > kWaitLimitNs && !beat_is_recent(abort_flag + kBeat)) ||
-                          idle >= kWaitLimitIters;
-        if (__any_sync(0xffffffffu, late || *abort_flag != 0)) {
+        const bool late = global_timer_ns() - t0 > kWaitLimitNs || idle >= kWaitLimitIters;
+        if (__any_sync(0xffffffffu, (late && !beat_is_recent(abort_flag + kBeat)) || *abort_flag != 0)) {
           *abort_flag = 1;
           break;
         }
